@@ -23,6 +23,8 @@ __all__ = [
     "qk_state_init", "qk_dequantize", "qk_gemv_nf4", "qk_gemv_nf4_grouped", "qk_gemm_nf4_workspace_size", "qk_gemm_nf4", "qk_gemm_nf4_noalloc",
     "qk_gemm_nf4_grouped_workspace_size", "qk_gemm_nf4_grouped", "GemmTask", "qk_dequantize_grouped", "DequantTask", "qk_last_error", "qk_version",
     "qk_backend_info", "quantize",
+    "Int4State", "Int4Weight", "qk_int4_state_init", "qk_gemv_int4", "qk_gemv_int4_grouped", "qk_moe_workspace_size",
+    "qk_moe_int4", "qk_moe_nf4",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -37,6 +39,8 @@ NF4, FP4, CUSTOM = 0, 1, 2
 QK_STATE_MAGIC = 0x314B5451
 QK_STATE_VERSION = 1
 QK_DQ_BLOCK = 256
+QK_INT4_MAGIC = 0x34494B51
+QK_INT4_VERSION = 1
 
 _DTYPE_CODE = {torch.float32: QK_F32, torch.bfloat16: QK_BF16, torch.float16: QK_F16}
 
@@ -71,6 +75,24 @@ class QuantState(ctypes.Structure):
     ]
 
 
+class Int4State(ctypes.Structure):
+    """Mirror of qk_int4_state (include/qk.h)."""
+    _fields_ = [
+        ("magic", ctypes.c_uint32),
+        ("version", ctypes.c_uint32),
+        ("struct_bytes", ctypes.c_uint32),
+        ("group", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("code_stride", ctypes.c_int64),
+        ("scale_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("zeros", ctypes.c_void_p),
+    ]
+
+
 class QuantTask(ctypes.Structure):
     """qk_quant_task."""
     _fields_ = [("x", ctypes.c_void_p), ("n", ctypes.c_int64), ("codes", ctypes.c_void_p),
@@ -86,6 +108,11 @@ class DqTask(ctypes.Structure):
 class GemvTask(ctypes.Structure):
     """Mirror of qk_gemv_task (include/qk.h)."""
     _fields_ = [("x", ctypes.c_void_p), ("st", ctypes.POINTER(QuantState)), ("y", ctypes.c_void_p)]
+
+
+class GemvInt4Task(ctypes.Structure):
+    """Mirror of qk_gemv_int4_task (include/qk.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("st", ctypes.POINTER(Int4State)), ("y", ctypes.c_void_p)]
 
 
 class DequantTask(ctypes.Structure):
@@ -122,6 +149,7 @@ def lib():
         raise QKError(QK_ERR_NO_DEVICE, _load_error) from e
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     st_p = ctypes.POINTER(QuantState)
+    i4_p = ctypes.POINTER(Int4State)
     sigs = {
         "qk_make_codebook": [i32, ctypes.POINTER(ctypes.c_float)],
         "qk_quantize_blockwise": [vp, i32, i64, i32, ctypes.POINTER(ctypes.c_float), vp, vp, vp],
@@ -149,6 +177,12 @@ def lib():
         "qk_int8_matmul": [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, vp],
         "qk_quantize_blockwise_8bit": [vp, i32, i64, i32, ctypes.POINTER(ctypes.c_float), vp, vp, vp],
         "qk_dequantize_blockwise_8bit": [vp, vp, i64, i32, ctypes.POINTER(ctypes.c_float), vp, i32, vp],
+        "qk_int4_state_init": [i4_p, i64, i64, i32, vp, i64, vp, i32, vp],
+        "qk_gemv_int4": [vp, i32, i32, i4_p, vp, vp],
+        "qk_gemv_int4_grouped": [ctypes.POINTER(GemvInt4Task), i32, i32, i32, vp],
+        "qk_moe_workspace_size": [i32, i32, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "qk_moe_int4": [vp, i32, i32, vp, i32, i32, i32, i32, i4_p, i4_p, vp, vp, ctypes.c_size_t, vp],
+        "qk_moe_nf4": [vp, i32, vp, i32, i32, i32, i32, st_p, st_p, vp, vp, ctypes.c_size_t, vp],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -772,6 +806,164 @@ def qk_qlora_backward(dY: torch.Tensor, state: QuantState, X=None, A=None, B=Non
                                        float(lora_scale), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(workspace),
                                        0 if workspace is None else workspace.numel(), ctypes.c_void_p(_stream(dY))))
     return dX, dA, dB
+
+
+def qk_int4_state_init(rows: int, cols: int, group: int, codes: torch.Tensor, scales: torch.Tensor,
+                       zeros=None) -> Int4State:
+    """Descriptor of an int4 weight [rows, cols] with one scale (fp16 or bf16) and one zero point
+    (uint8; None: 8) per group of `group` inputs of a row (0: per row).  codes: uint8 [rows, stride],
+    two codes per byte, the first in the high nibble, stride a multiple of 16; scales, zeros:
+    [rows, ceil(cols / group)]."""
+    ngroups = -(-cols // group) if group > 0 else 1
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[0] != rows:
+        raise ValueError(f"codes must be uint8 [{rows}, stride], got {codes.dtype} {tuple(codes.shape)}")
+    if scales.dtype not in (torch.float16, torch.bfloat16) or scales.numel() != rows * ngroups:
+        raise ValueError(f"scales must be fp16 or bf16 [{rows}, {ngroups}], got {scales.dtype} {tuple(scales.shape)}")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.numel() != rows * ngroups):
+        raise ValueError(f"zeros must be uint8 [{rows}, {ngroups}], got {zeros.dtype} {tuple(zeros.shape)}")
+    _require_cuda(codes, scales, zeros)
+    _same_device(codes, scales, zeros)
+    st = Int4State()
+    _check(lib().qk_int4_state_init(ctypes.byref(st), int(rows), int(cols), int(group), _ptr(codes), codes.shape[1],
+                                    _ptr(scales), _DTYPE_CODE[scales.dtype], _ptr(zeros)))
+    # keep the device buffers alive as long as the descriptor
+    st._keep = (codes, scales, zeros)
+    return st
+
+
+def _same_device(*ts):
+    devs = {t.device for t in ts if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors of one call must be on one device, got {sorted(map(str, devs))}")
+
+
+def _int4_acts(x: torch.Tensor, state: Int4State, y, name: str):
+    """(x as [M, K], y allocated or checked) of a product with an int4 weight."""
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be bf16 or fp16, got {x.dtype}")
+    x2 = _rows_of(x, state.cols, name)
+    M = x2.shape[0]
+    if y is None:
+        y = torch.empty((M, state.rows), dtype=x.dtype, device=x.device)
+    else:
+        _check_out(y, (M, state.rows), x.dtype, "y" if name == "x" else name[:-1] + "y")
+    _require_cuda(x, y)
+    _same_device(x, y, state._keep[0])
+    return x2, y
+
+
+def qk_gemv_int4(x: torch.Tensor, state: Int4State, y=None) -> torch.Tensor:
+    """y [M, N] = x W^T for x [M, K] (bf16 or fp16, M <= 16) and an int4 weight, in x's dtype."""
+    x2, y = _int4_acts(x, state, y, "x")
+    with _on(x.device):
+        _check(lib().qk_gemv_int4(_ptr(x2), _DTYPE_CODE[x.dtype], x2.shape[0], ctypes.byref(state), _ptr(y),
+                                  ctypes.c_void_p(_stream(x))))
+    return y
+
+
+def qk_gemv_int4_grouped(tasks, ys=None):
+    """y_i = x_i W_i^T for a list of (x_i, state_i) with one dtype and the same M, in as few launches
+    as the weights' groups allow.  Returns the list of y_i."""
+    tasks = list(tasks)
+    if not tasks:
+        raise ValueError("qk_gemv_int4_grouped needs at least one (x, state)")
+    if ys is not None and len(ys) != len(tasks):
+        raise ValueError(f"{len(tasks)} tasks but {len(ys)} outputs")
+    arr = (GemvInt4Task * len(tasks))()
+    keep, outs = [], []
+    for i, (x, state) in enumerate(tasks):
+        x2, y = _int4_acts(x, state, None if ys is None else ys[i], f"task {i}: x")
+        if i and (x2.shape[0] != keep[0].shape[0] or x2.dtype != keep[0].dtype):
+            raise ValueError(f"task {i}: every x needs the rows and the dtype of the first ({keep[0].shape[0]}, "
+                             f"{keep[0].dtype}), got {x2.shape[0]}, {x2.dtype}")
+        if i:
+            _same_device(keep[0], x2)
+        arr[i].x = x2.data_ptr()
+        arr[i].st = ctypes.pointer(state)
+        arr[i].y = y.data_ptr()
+        keep.append(x2)
+        outs.append(y)
+    with _on(keep[0].device):
+        _check(lib().qk_gemv_int4_grouped(arr, len(tasks), _DTYPE_CODE[keep[0].dtype], keep[0].shape[0],
+                                          ctypes.c_void_p(_stream(keep[0]))))
+    return outs
+
+
+def qk_moe_workspace_size(T: int, top_k: int, inner: int) -> int:
+    """Workspace bytes of qk_moe_nf4 / qk_moe_int4 for T tokens, top_k experts each, `inner` features."""
+    out = ctypes.c_size_t(0)
+    _check(lib().qk_moe_workspace_size(int(T), int(top_k), int(inner), ctypes.byref(out)))
+    return int(out.value)
+
+
+def _moe_args(x, logits, top_k, gate_up, down, y, workspace, dtypes):
+    if x.dtype not in dtypes:
+        raise ValueError(f"x must be one of {dtypes}, got {x.dtype}")
+    if logits.dtype not in _DTYPE_CODE:
+        raise ValueError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
+    x2 = _rows_of(x, gate_up.cols, "x")
+    T = x2.shape[0]
+    if logits.dim() < 1 or logits.numel() != T * logits.shape[-1]:
+        raise ValueError(f"logits {tuple(logits.shape)} do not hold one row per token ({T})")
+    if y is None:
+        y = torch.empty((T, down.rows // max(1, logits.shape[-1])), dtype=x.dtype, device=x.device)
+    else:
+        _check_out(y, (T, gate_up.cols), x.dtype, "y")
+    if workspace is None:
+        workspace = torch.empty(qk_moe_workspace_size(T, top_k, down.cols), dtype=torch.uint8, device=x.device)
+    _require_cuda(x, logits, y, workspace)
+    _same_device(x, logits, y, workspace, gate_up._keep[0], down._keep[0])
+    return x2, T, logits.shape[-1], y, workspace
+
+
+def qk_moe_int4(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate_up: Int4State, down: Int4State,
+                renormalize: bool = True, y=None, workspace=None) -> torch.Tensor:
+    """Mixture-of-experts layer of x [T, H] (bf16 or fp16, T <= 16) with the router's logits [T, E] over
+    int4 experts: gate_up [E * 2 * I, H] (gate rows, then up rows, of each expert), down [E * H, I]."""
+    x2, T, E, y, workspace = _moe_args(x, logits, top_k, gate_up, down, y, workspace, (torch.bfloat16, torch.float16))
+    with _on(x.device):
+        _check(lib().qk_moe_int4(_ptr(x2), _DTYPE_CODE[x.dtype], T, _ptr(logits), _DTYPE_CODE[logits.dtype], E,
+                                 int(top_k), int(bool(renormalize)), ctypes.byref(gate_up), ctypes.byref(down), _ptr(y),
+                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                 ctypes.c_void_p(_stream(x))))
+    return y
+
+
+def qk_moe_nf4(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate_up: QuantState, down: QuantState,
+               renormalize: bool = True, y=None, workspace=None) -> torch.Tensor:
+    """qk_moe_int4 over experts quantized by this library (NF4, FP4 or custom levels, plain or
+    double-quantized), x in bf16: quantize the stacked weights [E * 2 * I, H] and [E * H, I]."""
+    x2, T, E, y, workspace = _moe_args(x, logits, top_k, gate_up, down, y, workspace, (torch.bfloat16,))
+    with _on(x.device):
+        _check(lib().qk_moe_nf4(_ptr(x2), T, _ptr(logits), _DTYPE_CODE[logits.dtype], E, int(top_k),
+                                int(bool(renormalize)), ctypes.byref(gate_up), ctypes.byref(down), _ptr(y),
+                                _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                ctypes.c_void_p(_stream(x))))
+    return y
+
+
+class Int4Weight:
+    """A weight W[N, K] = scales * (codes - zeros) in int4 groups, packed on the device from unpacked
+    integer codes [N, K] (0..15), scales [N, G] (fp16 or bf16) and zero points [N, G] (None: 8)."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros=None, group: int = 128):
+        if codes.dim() != 2 or codes.dtype.is_floating_point:
+            raise ValueError(f"codes must be integers [N, K], got {codes.dtype} {tuple(codes.shape)}")
+        rows, cols = codes.shape
+        stride = (-(-cols // 2) + 15) // 16 * 16
+        q = torch.zeros((rows, 2 * stride), dtype=torch.uint8, device=codes.device)
+        q[:, :cols] = codes
+        self.codes = (q[:, 0::2] << 4) | (q[:, 1::2] & 15)
+        self.scales = scales.contiguous()
+        self.zeros = None if zeros is None else zeros.to(torch.uint8).contiguous()
+        self.state = qk_int4_state_init(rows, cols, group, self.codes, self.scales, self.zeros)
+
+    @property
+    def shape(self):
+        return (self.state.rows, self.state.cols)
+
+    def gemv(self, x, y=None):
+        return qk_gemv_int4(x, self.state, y)
 
 
 class QuantizedWeight:

@@ -31,7 +31,8 @@ PROBE_LIB = os.path.join(PKG, "libqk_probe.so")
 PROBE_SOURCE = "hbm_probe.hip"
 
 SOURCES = ["api.cpp", "codebook.cpp", "quantize.hip", "double_quant.hip", "dequantize.hip", "gemv.hip", "gemm.hip",
-           "merge.hip", "backward.hip", "quantize8.hip", "int8mm.hip"]
+           "merge.hip", "backward.hip", "quantize8.hip", "int8mm.hip",
+           "int4_gemv.hip", "moe.hip"]
 
 COMMON_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

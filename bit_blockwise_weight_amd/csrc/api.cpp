@@ -115,6 +115,71 @@ qk::DeqArgs deq_args(const qk_quant_state* st) {
     return a;
 }
 
+qk_status check_int4_fields(const qk_int4_state* st, qk_status bad, const char* who) {
+    if (st->rows < 1 || st->rows > ((int64_t)1 << 28) || st->cols < 1 || st->cols > ((int64_t)1 << 24))
+        return fail(bad, "%s: rows must be in 1..2^28 and cols in 1..2^24 (got %lld, %lld)", who, (long long)st->rows,
+                    (long long)st->cols);
+    if (st->group != 0 && st->group != 32 && st->group != 64 && st->group != 128 && st->group != 256)
+        return fail(bad, "%s: group %d (expected 32, 64, 128, 256, or 0 for one per row)", who, st->group);
+    if (st->scale_dtype != QK_F16 && st->scale_dtype != QK_BF16)
+        return fail(bad, "%s: scale dtype %d (expected QK_F16 or QK_BF16)", who, st->scale_dtype);
+    if (st->code_stride % 16 != 0 || st->code_stride < cdiv(st->cols, 2) || st->code_stride > ((int64_t)1 << 24))
+        return fail(bad, "%s: code_stride %lld (a multiple of 16, at least %lld and at most 2^24)", who,
+                    (long long)st->code_stride, (long long)cdiv(st->cols, 2));
+    if (!st->codes || !st->scales) return fail(bad, "%s: codes or scales pointer is NULL", who);
+    if (!aligned(st->codes, 16) || !aligned(st->scales, 2))
+        return fail(bad, "%s: codes must be 16-byte aligned and scales 2-byte aligned", who);
+    return QK_OK;
+}
+
+qk_status validate_int4(const qk_int4_state* st) {
+    if (!st) return fail(QK_ERR_INVALID_ARG, "int4 state pointer is NULL");
+    if (st->magic != QK_INT4_MAGIC)
+        return fail(QK_ERR_BAD_STATE, "int4 state: bad magic 0x%08x (not a qk_int4_state or corrupted)", st->magic);
+    if (st->version != QK_INT4_VERSION)
+        return fail(QK_ERR_BAD_STATE, "int4 state: unknown version %u (this library reads %u)", st->version,
+                    QK_INT4_VERSION);
+    if (st->struct_bytes != sizeof(qk_int4_state))
+        return fail(QK_ERR_BAD_STATE, "int4 state: struct_bytes %u != %zu", st->struct_bytes, sizeof(qk_int4_state));
+    if (st->reserved != 0) return fail(QK_ERR_BAD_STATE, "int4 state: reserved field is not 0");
+    return check_int4_fields(st, QK_ERR_BAD_STATE, "int4 state");
+}
+
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + bn && b0 < a0 + an;
+}
+
+// The checks that both mixture-of-experts calls share, for stacked weights [up_rows, H] and [down_rows, I].
+qk_status check_moe(const char* who, const qk::MoeItem& m, int64_t up_rows, int64_t down_rows, void* workspace,
+                    size_t workspace_bytes) {
+    if (!m.x || !m.logits || !m.y) return fail(QK_ERR_INVALID_ARG, "%s: NULL x, logits or y", who);
+    if (m.T < 1 || m.T > 16) return fail(QK_ERR_INVALID_ARG, "%s: T must be in 1..16 (got %d)", who, m.T);
+    if (m.E < 1 || m.E > 256) return fail(QK_ERR_INVALID_ARG, "%s: E must be in 1..256 (got %d)", who, m.E);
+    if (m.top_k < 1 || m.top_k > 16 || m.top_k > m.E)
+        return fail(QK_ERR_INVALID_ARG, "%s: top_k must be in 1..min(E, 16) (got %d of %d experts)", who, m.top_k, m.E);
+    if (m.logits_dtype != QK_F32 && m.logits_dtype != QK_BF16 && m.logits_dtype != QK_F16)
+        return fail(QK_ERR_INVALID_ARG, "%s: unknown logits dtype %d", who, m.logits_dtype);
+    if (!aligned(m.x, 2) || !aligned(m.y, 2) || !aligned(m.logits, m.logits_dtype == QK_F32 ? 4 : 2))
+        return fail(QK_ERR_INVALID_ARG, "%s: x, y and logits must be aligned to their elements", who);
+    if (up_rows != 2 * (int64_t)m.E * m.I || down_rows != (int64_t)m.E * m.H)
+        return fail(QK_ERR_INVALID_ARG,
+                    "%s: gate_up [%lld, %lld] and down [%lld, %lld] are not the stacks [E*2*I, H], [E*H, I] of %d experts",
+                    who, (long long)up_rows, (long long)m.H, (long long)down_rows, (long long)m.I, m.E);
+    const size_t need = qk::moe_workspace_bytes(m.T, m.top_k, m.I);
+    if (!workspace || workspace_bytes < need)
+        return fail(QK_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who, need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (!aligned(workspace, 16)) return fail(QK_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", who);
+    const size_t xb = (size_t)m.T * (size_t)m.H * 2;
+    const size_t lb = (size_t)m.T * (size_t)m.E * (m.logits_dtype == QK_F32 ? 4 : 2);
+    if (overlap(workspace, need, m.x, xb) || overlap(workspace, need, m.y, xb) || overlap(workspace, need, m.logits, lb))
+        return fail(QK_ERR_INVALID_ARG, "%s: the workspace overlaps x, logits or y", who);
+    if (overlap(m.y, xb, m.x, xb) && m.y != m.x)
+        return fail(QK_ERR_INVALID_ARG, "%s: y overlaps x without being x", who);
+    return QK_OK;
+}
+
 thread_local const char* g_gemv_variant = "none";
 thread_local const char* g_gemm_variant = "none";
 
@@ -732,6 +797,127 @@ qk_status qk_gemm_nf4_noalloc(const void* X, int64_t M, const qk_quant_state* st
     return launched(qk::launch_gemm(X, M, w, A, B, A ? r : 0, lora_scale, Y, scratch,
                                     reinterpret_cast<hipStream_t>(stream), &g_gemm_variant),
                     "qk_gemm_nf4_noalloc");
+}
+
+qk_status qk_int4_state_init(qk_int4_state* st, int64_t rows, int64_t cols, int32_t group, const uint8_t* codes,
+                             int64_t code_stride, const void* scales, int32_t scale_dtype, const uint8_t* zeros) {
+    if (!st) return fail(QK_ERR_INVALID_ARG, "qk_int4_state_init: NULL state");
+    qk_int4_state s;
+    std::memset(&s, 0, sizeof(s));
+    s.magic = QK_INT4_MAGIC;
+    s.version = QK_INT4_VERSION;
+    s.struct_bytes = sizeof(qk_int4_state);
+    s.group = group;
+    s.rows = rows;
+    s.cols = cols;
+    s.code_stride = code_stride;
+    s.scale_dtype = scale_dtype;
+    s.codes = codes;
+    s.scales = scales;
+    s.zeros = zeros;
+    const qk_status v = check_int4_fields(&s, QK_ERR_INVALID_ARG, "qk_int4_state_init");
+    if (v != QK_OK) return v;
+    *st = s;
+    return ok();
+}
+
+namespace {
+
+qk_status gemv_int4(const char* who, const qk_gemv_int4_task* tasks, int32_t ntasks, int32_t dtype, int32_t M,
+                    void* stream) {
+    if (dtype != QK_BF16 && dtype != QK_F16)
+        return fail(QK_ERR_INVALID_ARG, "%s: dtype %d (expected QK_BF16 or QK_F16)", who, dtype);
+    if (M < 1 || M > 16) return fail(QK_ERR_INVALID_ARG, "%s: M must be in 1..16 (got %d)", who, M);
+    qk::Int4Item items[256];
+    for (int32_t i = 0; i < ntasks; ++i) {
+        const qk_gemv_int4_task& t = tasks[i];
+        const qk_status v = validate_int4(t.st);
+        if (v != QK_OK) return v;
+        if (!t.x || !t.y) return fail(QK_ERR_INVALID_ARG, "%s: task %d: NULL x or y", who, i);
+        if (!aligned(t.x, 2) || !aligned(t.y, 2))
+            return fail(QK_ERR_INVALID_ARG, "%s: task %d: x and y must be 2-byte aligned", who, i);
+        items[i] = qk::Int4Item{t.x, t.y, t.st};
+    }
+    // every y must be disjoint from the other ys and from every x
+    for (int32_t i = 0; i < ntasks; ++i) {
+        const size_t yb = (size_t)M * (size_t)tasks[i].st->rows * 2;
+        for (int32_t j = 0; j < ntasks; ++j) {
+            if (overlap(tasks[i].y, yb, tasks[j].x, (size_t)M * (size_t)tasks[j].st->cols * 2))
+                return fail(QK_ERR_INVALID_ARG, "%s: y of task %d overlaps x of task %d", who, i, j);
+            if (j != i && overlap(tasks[i].y, yb, tasks[j].y, (size_t)M * (size_t)tasks[j].st->rows * 2))
+                return fail(QK_ERR_INVALID_ARG, "%s: y of task %d overlaps y of task %d", who, i, j);
+        }
+    }
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_int4_gemv_group(items, ntasks, M, dtype == QK_F16, reinterpret_cast<hipStream_t>(stream)),
+                    who);
+}
+
+}  // namespace
+
+qk_status qk_gemv_int4(const void* x, int32_t dtype, int32_t M, const qk_int4_state* st, void* y, void* stream) {
+    const qk_gemv_int4_task t = {x, st, y};
+    return gemv_int4("qk_gemv_int4", &t, 1, dtype, M, stream);
+}
+
+qk_status qk_gemv_int4_grouped(const qk_gemv_int4_task* tasks, int32_t ntasks, int32_t dtype, int32_t M, void* stream) {
+    if (!tasks) return fail(QK_ERR_INVALID_ARG, "qk_gemv_int4_grouped: tasks is NULL");
+    if (ntasks < 1 || ntasks > 256)
+        return fail(QK_ERR_INVALID_ARG, "qk_gemv_int4_grouped: ntasks must be in 1..256 (got %d)", ntasks);
+    return gemv_int4("qk_gemv_int4_grouped", tasks, ntasks, dtype, M, stream);
+}
+
+qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t I, size_t* bytes) {
+    if (!bytes) return fail(QK_ERR_INVALID_ARG, "qk_moe_workspace_size: bytes is NULL");
+    if (T < 1 || T > 16 || top_k < 1 || top_k > 16 || I < 1 || I > ((int64_t)1 << 24))
+        return fail(QK_ERR_INVALID_ARG, "qk_moe_workspace_size: T and top_k must be in 1..16 and I in 1..2^24 (got %d, %d, %lld)",
+                    T, top_k, (long long)I);
+    *bytes = qk::moe_workspace_bytes(T, top_k, I);
+    return ok();
+}
+
+qk_status qk_moe_int4(const void* x, int32_t dtype, int32_t T, const void* logits, int32_t logits_dtype, int32_t E,
+                      int32_t top_k, int32_t renormalize, const qk_int4_state* gate_up, const qk_int4_state* down,
+                      void* y, void* workspace, size_t workspace_bytes, void* stream) {
+    qk_status v = validate_int4(gate_up);
+    if (v == QK_OK) v = validate_int4(down);
+    if (v != QK_OK) return v;
+    if (dtype != QK_BF16 && dtype != QK_F16)
+        return fail(QK_ERR_INVALID_ARG, "qk_moe_int4: dtype %d (expected QK_BF16 or QK_F16)", dtype);
+    const qk::MoeItem m{x, logits, y, gate_up->cols, down->cols, logits_dtype, T, E, top_k, renormalize != 0,
+                        dtype == QK_F16};
+    v = check_moe("qk_moe_int4", m, gate_up->rows, down->rows, workspace, workspace_bytes);
+    if (v != QK_OK) return v;
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_moe_int4(m, gate_up, down, workspace, reinterpret_cast<hipStream_t>(stream)),
+                    "qk_moe_int4");
+}
+
+qk_status qk_moe_nf4(const void* x, int32_t T, const void* logits, int32_t logits_dtype, int32_t E, int32_t top_k,
+                     int32_t renormalize, const qk_quant_state* gate_up, const qk_quant_state* down, void* y,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    qk_status v = validate_state(gate_up);
+    if (v == QK_OK) v = validate_state(down);
+    if (v != QK_OK) return v;
+    if (gate_up->cols > ((int64_t)1 << 24) || down->cols > ((int64_t)1 << 24))
+        return fail(QK_ERR_INVALID_ARG, "qk_moe_nf4: H and I must be at most 2^24 (got %lld, %lld)",
+                    (long long)gate_up->cols, (long long)down->cols);
+    const qk::MoeItem m{x, logits, y, gate_up->cols, down->cols, logits_dtype, T, E, top_k, renormalize != 0, 0};
+    v = check_moe("qk_moe_nf4", m, gate_up->rows, down->rows, workspace, workspace_bytes);
+    if (v != QK_OK) return v;
+    if (m.H % 64 != 0 || m.I % 64 != 0)
+        return fail(QK_ERR_UNSUPPORTED, "qk_moe_nf4: H and I must be multiples of 64 (got %lld, %lld)", (long long)m.H,
+                    (long long)m.I);
+    if (!aligned(gate_up->codes, 16) || !aligned(down->codes, 16))
+        return fail(QK_ERR_INVALID_ARG, "qk_moe_nf4: codes must be 16-byte aligned");
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_moe_levels(m, qk::MatArgs{deq_args(gate_up), gate_up->rows, gate_up->cols},
+                                          qk::MatArgs{deq_args(down), down->rows, down->cols}, workspace,
+                                          reinterpret_cast<hipStream_t>(stream)),
+                    "qk_moe_nf4");
 }
 
 const char* qk_last_error(void) { return g_last_error.c_str(); }

@@ -191,4 +191,37 @@ hipError_t launch_qlora_backward(const void* dY, int64_t M, const MatArgs& w, co
 hipError_t launch_lora_merge(const MatArgs& w, const void* A, const void* B, int32_t r, float scale, void* out,
                              hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// int4 weights with group scales, and the mixture-of-experts layer
+// ---------------------------------------------------------------------------
+namespace w4 {
+struct Int4View;
+}
+w4::Int4View int4_view(const qk_int4_state* st);
+// Scale groups that a run of 128 k spans, as far as the kernels tell them apart: 4, 2 or 1.
+int int4_groups_per_chunk(int32_t group);
+struct Int4Item {
+    const void* x;
+    void* y;
+    const qk_int4_state* st;
+};
+hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t M, bool f16, hipStream_t s);
+
+struct MoeItem {
+    const void* x;        // [T, H]
+    const void* logits;   // [T, E]
+    void* y;              // [T, H]
+    int64_t H;
+    int64_t I;
+    int32_t logits_dtype;
+    int32_t T, E, top_k;
+    int32_t renorm;       // weights relative to the chosen experts
+    int32_t f16;          // x and y are fp16 (int4 experts), otherwise bf16
+};
+size_t moe_workspace_bytes(int32_t T, int32_t top_k, int64_t I);
+hipError_t launch_moe_int4(const MoeItem& m, const qk_int4_state* gate_up, const qk_int4_state* down, void* workspace,
+                           hipStream_t s);
+hipError_t launch_moe_levels(const MoeItem& m, const MatArgs& gate_up, const MatArgs& down, void* workspace,
+                             hipStream_t s);
+
 }  // namespace qk

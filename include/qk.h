@@ -577,6 +577,123 @@ qk_status qk_int8_matmul(const int8_t* Xq, const float* SX, const int8_t* CB, co
                          int64_t K, const void* X, const int32_t* outlier_idx, const int32_t* outlier_count, void* Y,
                          void* stream);
 
+/*
+ * Descriptor of an int4 weight W [rows, cols] with group scales: integer codes and,
+ * per group of `group` consecutive inputs of a row (the last may be partial), a
+ * 16-bit scale and an integer zero point,
+ *     W[n, k] = s[n, k / group] * (q[n, k] - z[n, k / group]).
+ * This is the form in which group-quantized 4-bit checkpoints come; unlike
+ * qk_quant_state its groups never cross rows and its rows are padded.  Plain data,
+ * the pointers are device pointers owned by the caller.  Build it with
+ * qk_int4_state_init(); a descriptor whose magic, version, size or fields do not fit
+ * is rejected with QK_ERR_BAD_STATE by every call that takes one.
+ */
+#define QK_INT4_MAGIC 0x34494B51u    /* "QKI4" little-endian */
+#define QK_INT4_VERSION 1u
+
+typedef struct qk_int4_state {
+    uint32_t magic;          /* QK_INT4_MAGIC */
+    uint32_t version;        /* QK_INT4_VERSION */
+    uint32_t struct_bytes;   /* sizeof(qk_int4_state) */
+    int32_t group;           /* 32, 64, 128 or 256; 0: one group per row */
+    int64_t rows;            /* N, 1..2^28 */
+    int64_t cols;            /* K, 1..2^24 */
+    int64_t code_stride;     /* bytes from a row of codes to the next: a multiple of 16,
+                                >= ceil(cols / 2) */
+    int32_t scale_dtype;     /* QK_F16 or QK_BF16 */
+    int32_t reserved;        /* 0 */
+    const uint8_t* codes;    /* device, [rows, code_stride], 16-byte aligned: code 2t of a row in
+                                the high nibble of its byte t, code 2t+1 in the low nibble; what
+                                lies past the row's last code is ignored */
+    const void* scales;      /* device, [rows, G] of scale_dtype, G = ceil(cols / group) (1 for
+                                group 0), 2-byte aligned; finite */
+    const uint8_t* zeros;    /* device, [rows, G], values 0..255, or NULL: 8 for every group */
+} qk_int4_state;
+
+/*
+ * qk_int4_state_init — host.  Fills a descriptor.
+ *   Errors: QK_ERR_INVALID_ARG (null state / codes / scales, sizes out of range, unknown
+ *   group or scale dtype, a code_stride that is too small or not a multiple of 16,
+ *   misaligned buffers).
+ */
+qk_status qk_int4_state_init(qk_int4_state* st, int64_t rows, int64_t cols, int32_t group, const uint8_t* codes,
+                             int64_t code_stride, const void* scales, int32_t scale_dtype, const uint8_t* zeros);
+
+/*
+ * qk_gemv_int4 — device.  Decode-time product with an int4 weight,
+ *     y[m, :] = x[m, :] · W^T,  m < M.
+ *   The codes, less a constant, enter the products exactly; sums, scales and zero points
+ *   are fp32, and y is rounded once.  The same inputs give the same bits on every call.
+ *   x:  device, [M, K] of dtype (QK_BF16 or QK_F16) row-major, 2-byte aligned (16-byte
+ *       alignment and K % 8 == 0 load fastest).
+ *   M:  1..16.
+ *   st: host pointer to a valid descriptor of W [N, K].
+ *   y:  device, [M, N] of dtype, written; must not overlap x.
+ *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_HIP.
+ */
+qk_status qk_gemv_int4(const void* x, int32_t dtype, int32_t M, const qk_int4_state* st, void* y, void* stream);
+
+/*
+ * qk_gemv_int4_grouped — device.  qk_gemv_int4 of several weights, each with its own x and
+ * y and the same M and dtype, in one launch per run of up to 16 weights of one scale
+ * granularity (groups of 32, of 64, or of 128 and more).  Each y is bit-for-bit what
+ * qk_gemv_int4 of that weight alone writes.
+ *   tasks: host array of ntasks entries; x, st, y as for qk_gemv_int4.
+ *   ntasks: 1..256.   M: 1..16.
+ *   No y may overlap another task's y or any task's x (else QK_ERR_INVALID_ARG).
+ *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_HIP.
+ */
+typedef struct qk_gemv_int4_task {
+    const void* x;
+    const qk_int4_state* st;
+    void* y;
+} qk_gemv_int4_task;
+
+qk_status qk_gemv_int4_grouped(const qk_gemv_int4_task* tasks, int32_t ntasks, int32_t dtype, int32_t M, void* stream);
+
+/*
+ * qk_moe_workspace_size — host.  Bytes of device workspace that qk_moe_nf4 and
+ * qk_moe_int4 need for T tokens, top_k experts per token and experts of I inner features.
+ */
+qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t I, size_t* bytes);
+
+/*
+ * qk_moe_int4, qk_moe_nf4 — device.  A whole mixture-of-experts layer with SwiGLU experts
+ * for a few tokens, from the router's logits on, the experts' weights staying in 4 bits:
+ *     S_t     = the top_k largest of logits[t, :], equal ones by the lower index
+ *     w[t, e] = exp(logits[t, e] - max) / sum, the sum over S_t (renormalize != 0) or over
+ *               all experts (renormalize == 0)
+ *     h[t, e] = silu(x_t · Wg_e^T) * (x_t · Wu_e^T)
+ *     y_t     = sum over e in S_t of w[t, e] · h[t, e] · Wd_e^T
+ *   A logit of -inf masks an expert for a token (a NaN counts as -inf): it is never chosen,
+ *   and a token with nothing left to choose gets y_t = 0.  The weights are the int4 values,
+ *   or, for qk_moe_nf4, the bf16 copies of the 16 levels times the fp32 block scale, as in
+ *   qk_gemv_nf4.  Sums are fp32, h is kept to 16 bits of mantissa, y is rounded once.  Only
+ *   the weights of chosen experts are read.  The same inputs give the same bits on every
+ *   call, and a token's result does not depend on the other tokens' logits or values.
+ *   x: device, [T, H] of dtype, 2-byte aligned (qk_moe_int4: QK_BF16 or QK_F16; qk_moe_nf4:
+ *     bf16).   T: 1..16.
+ *   logits: device, [T, E] of logits_dtype (QK_F32, QK_BF16 or QK_F16), naturally aligned;
+ *     +inf is not supported (its tokens get NaN).   E: 1..256.   top_k: 1..min(E, 16).
+ *   gate_up: host pointer to the descriptor of the stacked [E * 2 * I, H] weights: expert e's
+ *     gate in rows [2 e I, 2 e I + I), its up projection in the next I rows.
+ *   down: descriptor of the stacked [E * H, I] weights: expert e in rows [e H, e H + H).
+ *   H and I follow from the descriptors.  qk_moe_nf4 needs H and I to be multiples of 64
+ *     (else QK_ERR_UNSUPPORTED) and 16-byte aligned codes.
+ *   y: device, [T, H] of dtype, written.  May be x itself.
+ *   workspace: device, >= qk_moe_workspace_size(T, top_k, I) bytes, 16-byte aligned;
+ *     contents on entry ignored; no overlap with the other buffers.  Calls that may run at
+ *     the same time need workspaces of their own.
+ *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_UNSUPPORTED, QK_ERR_WORKSPACE,
+ *   QK_ERR_HIP.
+ */
+qk_status qk_moe_int4(const void* x, int32_t dtype, int32_t T, const void* logits, int32_t logits_dtype, int32_t E,
+                      int32_t top_k, int32_t renormalize, const qk_int4_state* gate_up, const qk_int4_state* down,
+                      void* y, void* workspace, size_t workspace_bytes, void* stream);
+qk_status qk_moe_nf4(const void* x, int32_t T, const void* logits, int32_t logits_dtype, int32_t E, int32_t top_k,
+                     int32_t renormalize, const qk_quant_state* gate_up, const qk_quant_state* down, void* y,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Message for the calling thread's last failed call ("" if none).  The
  * string stays valid until the thread's next qk_* call. */
 const char* qk_last_error(void);
