@@ -180,7 +180,7 @@ def lib():
         "qk_int4_state_init": [i4_p, i64, i64, i32, vp, i64, vp, i32, vp],
         "qk_gemv_int4": [vp, i32, i32, i4_p, vp, vp],
         "qk_gemv_int4_grouped": [ctypes.POINTER(GemvInt4Task), i32, i32, i32, vp],
-        "qk_moe_workspace_size": [i32, i32, i64, ctypes.POINTER(ctypes.c_size_t)],
+        "qk_moe_workspace_size": [i32, i32, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
         "qk_moe_int4": [vp, i32, i32, vp, i32, i32, i32, i32, i4_p, i4_p, vp, vp, ctypes.c_size_t, vp],
         "qk_moe_nf4": [vp, i32, vp, i32, i32, i32, i32, st_p, st_p, vp, vp, ctypes.c_size_t, vp],
     }
@@ -889,10 +889,11 @@ def qk_gemv_int4_grouped(tasks, ys=None):
     return outs
 
 
-def qk_moe_workspace_size(T: int, top_k: int, inner: int) -> int:
-    """Workspace bytes of qk_moe_nf4 / qk_moe_int4 for T tokens, top_k experts each, `inner` features."""
+def qk_moe_workspace_size(T: int, top_k: int, hidden: int, inner: int) -> int:
+    """Workspace bytes of qk_moe_nf4 / qk_moe_int4 for T tokens of `hidden` features, top_k experts each of
+    `inner` features."""
     out = ctypes.c_size_t(0)
-    _check(lib().qk_moe_workspace_size(int(T), int(top_k), int(inner), ctypes.byref(out)))
+    _check(lib().qk_moe_workspace_size(int(T), int(top_k), int(hidden), int(inner), ctypes.byref(out)))
     return int(out.value)
 
 
@@ -910,7 +911,7 @@ def _moe_args(x, logits, top_k, gate_up, down, y, workspace, dtypes):
     else:
         _check_out(y, (T, gate_up.cols), x.dtype, "y")
     if workspace is None:
-        workspace = torch.empty(qk_moe_workspace_size(T, top_k, down.cols), dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(qk_moe_workspace_size(T, top_k, gate_up.cols, down.cols), dtype=torch.uint8, device=x.device)
     _require_cuda(x, logits, y, workspace)
     _same_device(x, logits, y, workspace, gate_up._keep[0], down._keep[0])
     return x2, T, logits.shape[-1], y, workspace

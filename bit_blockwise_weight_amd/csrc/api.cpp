@@ -150,6 +150,9 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
     return a0 < b0 + bn && b0 < a0 + an;
 }
 
+// Largest H and I of a mixture-of-experts layer (byte offsets into its activations stay in 32 bits).
+constexpr int64_t kMaxMoeDim = (int64_t)1 << 20;
+
 // The checks that both mixture-of-experts calls share, for stacked weights [up_rows, H] and [down_rows, I].
 qk_status check_moe(const char* who, const qk::MoeItem& m, int64_t up_rows, int64_t down_rows, void* workspace,
                     size_t workspace_bytes) {
@@ -162,11 +165,14 @@ qk_status check_moe(const char* who, const qk::MoeItem& m, int64_t up_rows, int6
         return fail(QK_ERR_INVALID_ARG, "%s: unknown logits dtype %d", who, m.logits_dtype);
     if (!aligned(m.x, 2) || !aligned(m.y, 2) || !aligned(m.logits, m.logits_dtype == QK_F32 ? 4 : 2))
         return fail(QK_ERR_INVALID_ARG, "%s: x, y and logits must be aligned to their elements", who);
+    if (m.H > kMaxMoeDim || m.I > kMaxMoeDim)
+        return fail(QK_ERR_INVALID_ARG, "%s: H and I must be at most 2^20 (got %lld, %lld)", who, (long long)m.H,
+                    (long long)m.I);
     if (up_rows != 2 * (int64_t)m.E * m.I || down_rows != (int64_t)m.E * m.H)
         return fail(QK_ERR_INVALID_ARG,
                     "%s: gate_up [%lld, %lld] and down [%lld, %lld] are not the stacks [E*2*I, H], [E*H, I] of %d experts",
                     who, (long long)up_rows, (long long)m.H, (long long)down_rows, (long long)m.I, m.E);
-    const size_t need = qk::moe_workspace_bytes(m.T, m.top_k, m.I);
+    const size_t need = qk::moe_workspace_bytes(m.T, m.top_k, m.H, m.I);
     if (!workspace || workspace_bytes < need)
         return fail(QK_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who, need,
                     workspace ? workspace_bytes : (size_t)0);
@@ -868,12 +874,14 @@ qk_status qk_gemv_int4_grouped(const qk_gemv_int4_task* tasks, int32_t ntasks, i
     return gemv_int4("qk_gemv_int4_grouped", tasks, ntasks, dtype, M, stream);
 }
 
-qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t I, size_t* bytes) {
+qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t H, int64_t I, size_t* bytes) {
     if (!bytes) return fail(QK_ERR_INVALID_ARG, "qk_moe_workspace_size: bytes is NULL");
-    if (T < 1 || T > 16 || top_k < 1 || top_k > 16 || I < 1 || I > ((int64_t)1 << 24))
-        return fail(QK_ERR_INVALID_ARG, "qk_moe_workspace_size: T and top_k must be in 1..16 and I in 1..2^24 (got %d, %d, %lld)",
-                    T, top_k, (long long)I);
-    *bytes = qk::moe_workspace_bytes(T, top_k, I);
+    if (T < 1 || T > 16 || top_k < 1 || top_k > 16)
+        return fail(QK_ERR_INVALID_ARG, "qk_moe_workspace_size: T and top_k must be in 1..16 (got %d, %d)", T, top_k);
+    if (H < 1 || H > kMaxMoeDim || I < 1 || I > kMaxMoeDim)
+        return fail(QK_ERR_INVALID_ARG, "qk_moe_workspace_size: H and I must be in 1..2^20 (got %lld, %lld)", (long long)H,
+                    (long long)I);
+    *bytes = qk::moe_workspace_bytes(T, top_k, H, I);
     return ok();
 }
 
@@ -901,9 +909,6 @@ qk_status qk_moe_nf4(const void* x, int32_t T, const void* logits, int32_t logit
     qk_status v = validate_state(gate_up);
     if (v == QK_OK) v = validate_state(down);
     if (v != QK_OK) return v;
-    if (gate_up->cols > ((int64_t)1 << 24) || down->cols > ((int64_t)1 << 24))
-        return fail(QK_ERR_INVALID_ARG, "qk_moe_nf4: H and I must be at most 2^24 (got %lld, %lld)",
-                    (long long)gate_up->cols, (long long)down->cols);
     const qk::MoeItem m{x, logits, y, gate_up->cols, down->cols, logits_dtype, T, E, top_k, renormalize != 0, 0};
     v = check_moe("qk_moe_nf4", m, gate_up->rows, down->rows, workspace, workspace_bytes);
     if (v != QK_OK) return v;

@@ -2,11 +2,9 @@
 //     y[m, n] = sum_k x[m, k] s[n, k / g] (q[n, k] - z[n, k / g]),   m < M <= 16
 // for one weight or for up to 16 of a grouped call in one launch.
 //
-// A workgroup of 8 waves owns 16 RT consecutive rows of one weight; its waves take the row's
-// 128-k chunks in turn (chunk w, w + 8, ...) and their partial outputs are added through LDS
-// in wave order, so the result does not depend on timing.  The activations of a window of 8 U
-// chunks are staged in LDS once for the 8 waves (in the order the decoded codes have, zero past
-// K), while the codes of the next window are already being loaded.
+// The rows of all weights of a launch are cut into items of 16 RT rows, and the items, in order,
+// into equal shares of work, one per workgroup of 8 waves; a workgroup walks its items with
+// RowTiles (w4_tile.h), the next item's codes being loaded while one is multiplied.
 // Bound by the bytes of the codes at every M (64 flops a byte at M = 16).
 #include <algorithm>
 
@@ -19,8 +17,7 @@ namespace {
 
 using namespace w4;
 
-constexpr int kWaves = 8;
-constexpr int kThreads = kWaves * 64;
+constexpr int kThreads = 512;
 
 struct Int4Task {
     const uint16_t* x;       // [M, K]
@@ -28,157 +25,114 @@ struct Int4Task {
     Int4View w;
     int64_t N;
     int64_t K;
-    int64_t item0;           // first workgroup of the task
     int32_t x_aligned;       // rows of x start at 16-byte boundaries
-    int32_t pad;
+    int32_t kwl;             // log2 of the waves that split a row
 };
 
 struct Int4Group {
     Int4Task t[kMaxGemvTasks];
+    int64_t cost0[kMaxGemvTasks + 1];    // work before the task's first item, in chunks of an item
+    int32_t chunks[kMaxGemvTasks];       // work of one item
     int32_t ntasks;
     int32_t M;
+    int32_t x_bufs;
+    int32_t pad;
 };
 
-// bytes of a staged activation row: the window and 16 more, so that the rows of a fragment
-// read fall in different banks
-template <int U>
-constexpr int kPitch = kWaves * U * kChunk * 2 + 16;
-
-template <int F, int NG, int RT, int U>
-__global__ __launch_bounds__(kThreads) void int4_gemv_kernel(Int4Group g) {
+template <int F, int NG, int RT, int NS, int MI, bool kResident>
+__global__ __launch_bounds__(kThreads, 2) void int4_gemv_kernel(Int4Group g) {
     extern __shared__ __align__(16) uint8_t lds[];
-    constexpr int kWin = kWaves * U * kChunk;          // k per window
-    constexpr int kWinUnits = kWin / 8;                // 16-byte units of a row in a window
-    constexpr int kGroupChunks = 4 / NG;               // MFMAs per scale
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = lane & 15, h = lane >> 4;
-    int ti = 0;
-    while (ti + 1 < g.ntasks && (int64_t)blockIdx.x >= g.t[ti + 1].item0) ++ti;
-    const Int4Task& t = g.t[ti];
-    const int M = g.M;
-    const int64_t row0 = ((int64_t)blockIdx.x - t.item0) * (16 * RT);
-    const int64_t K = t.K, N = t.N;
-    int64_t row[RT];
-    const uint8_t* codes[RT];
+    typedef RowTiles<F, NG, RT, NS, MI, kResident, false> Tiles;
+    // this workgroup's share: the items that start in [lo, hi) of the work
+    const int64_t all = g.cost0[g.ntasks];
+    const int64_t lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
+    for (int ti = 0; ti < g.ntasks; ++ti) {
+        const int64_t c0 = g.cost0[ti], c1 = g.cost0[ti + 1];
+        if (c1 <= lo || c0 >= hi) continue;
+        const int64_t ch = g.chunks[ti];
+        const int64_t i0 = lo > c0 ? (lo - c0 + ch - 1) / ch : 0;
+        const int64_t i1 = ((hi < c1 ? hi : c1) - c0 + ch - 1) / ch;
+        if (i0 >= i1) continue;
+        const Int4Task& t = g.t[ti];
+        Rows<RT> p;
+        p.kwl = t.kwl;
+        p.group_step = 16 * RT;
+        p.step = (16 * RT * 8) >> t.kwl;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        row[r] = row0 + 16 * r + n < N ? row0 + 16 * r + n : N - 1;
-        codes[r] = t.w.codes + row[r] * t.w.stride;
-    }
-    const int nchunk = (int)((K + kChunk - 1) / kChunk);
-    const int nwin = (nchunk + kWaves * U - 1) / (kWaves * U);
-
-    floatx4_t y[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) y[r] = (floatx4_t){0, 0, 0, 0};
-    u32x4_t cw[2][U][RT];
-    GroupScales<NG> sc[2][U][RT];
-
-    auto fetch = [&](int buf, int win) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            int c = (win * U + u) * kWaves + wave;
-            c = c < nchunk ? c : nchunk - 1;
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                cw[buf][u][r] = load_codes(codes[r], t.w.stride, c, h);
-                sc[buf][u][r].load(t.w, row[r], c);
+        for (int r = 0; r < RT; ++r) {
+            p.base[r] = 0;
+            p.off[r] = 16 * r;
+        }
+        p.count = t.N;
+        p.x = t.x;
+        p.xrow = nullptr;
+        p.K = t.K;
+        p.x_pitch = t.K;
+        p.x_rows = g.M;
+        p.x_aligned = t.x_aligned;
+        p.M = g.M;
+        p.x_bufs = g.x_bufs;
+        Tiles::run(t.w, p, i0, i1, nullptr, lds, [&](int64_t item, const float* put) {
+            for (int o = threadIdx.x; o < (RT * 64 * MI * 8) >> t.kwl; o += kThreads) {
+                const int q = o / (RT * 64 * MI), r = o / (64 * MI) % RT, e = o % (64 * MI), m = Tiles::act_of(e);
+                const int64_t n = item * p.step + q * (16 * RT) + 16 * r + (e & 15);
+                const float v = Tiles::sum(put, t.kwl, q, r, e);
+                if (m < g.M && n < t.N) t.y[m * t.N + n] = float_to_bits16(v, F == kInt4F16);
             }
-        }
-    };
-    auto stage = [&](int win) {
-        for (int i = tid; i < M * kWinUnits; i += kThreads) {
-            const int m = i / kWinUnits, u = i % kWinUnits;
-            const u32x4_t v = load_x8(t.x + m * K, (int64_t)win * kWin + 8 * u, K, t.x_aligned);
-            *reinterpret_cast<u32x4_t*>(lds + m * kPitch<U> + 16 * u) = int4_order(v);
-        }
-    };
-    const uint8_t* arow = lds + (n < M ? n : M - 1) * kPitch<U> + 16 * h;
-    auto compute = [&](int buf, int win) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if ((win * U + u) * kWaves + wave >= nchunk) break;
-            u32x4_t w[RT];
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                w[r] = cw[buf][u][r];
-                transpose_groups(w[r]);
-            }
-#pragma unroll
-            for (int q = 0; q < NG; ++q) {
-                floatx4_t acc[RT], xs = {0, 0, 0, 0};
-#pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r] = (floatx4_t){0, 0, 0, 0};
-#pragma unroll
-                for (int j = q * kGroupChunks; j < (q + 1) * kGroupChunks; ++j) {
-                    const u32x4_t a =
-                        *reinterpret_cast<const u32x4_t*>(arow + (u * kWaves + wave) * (kChunk * 2) + 64 * j);
-                    xs = mfma<F>(a, ones<F>(), xs);
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) acc[r] = mfma<F>(a, decode8<F>(w[r][j]), acc[r]);
-                }
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const float s = sc[buf][u][r].scale(t.w, q);
-                    const float zb = (float)sc[buf][u][r].z[q] + kCodeBias<F>;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[r][i] = fmaf(s, fmaf(-zb, xs[i], acc[r][i]), y[r][i]);
-                }
-            }
-        }
-    };
-
-    fetch(0, 0);
-    for (int win = 0; win < nwin; win += 2) {
-        stage(win);
-        if (win + 1 < nwin) fetch(1, win + 1);
-        __syncthreads();
-        compute(0, win);
-        __syncthreads();
-        if (win + 1 < nwin) {
-            stage(win + 1);
-            if (win + 2 < nwin) fetch(0, win + 2);
-            __syncthreads();
-            compute(1, win + 1);
-            __syncthreads();
-        }
-    }
-
-    // the 8 partial sums of every output, in wave order
-    floatx4_t* red = reinterpret_cast<floatx4_t*>(lds);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) red[(wave * RT + r) * 64 + lane] = y[r];
-    __syncthreads();
-    const float* redf = reinterpret_cast<const float*>(lds);
-    for (int o = tid; o < RT * 256; o += kThreads) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += redf[w * RT * 256 + o];
-        const int r = o >> 8, l = (o >> 2) & 63, m = 4 * (l >> 4) + (o & 3);
-        const int64_t nn = row0 + 16 * r + (l & 15);
-        if (m < M && nn < N) t.y[m * N + nn] = float_to_bits16(v, F == kInt4F16);
+        });
     }
 }
 
-template <int F, int NG, int RT, int U>
-hipError_t launch_one(const Int4Group& g, int64_t items, hipStream_t s) {
-    const size_t lds = std::max<size_t>((size_t)g.M * kPitch<U>, (size_t)kWaves * RT * 64 * 16);
-    int4_gemv_kernel<F, NG, RT, U><<<dim3((unsigned)items), dim3(kThreads), lds, s>>>(g);
+// How a weight of K inputs is cut for M activation rows: tiles per item and row group, lines per wave and
+// window, waves that split a row, and whether the activations of a whole row stay in LDS.
+struct Shape {
+    int rt;
+    int ns;
+    int kwl;
+    bool resident;
+};
+
+constexpr size_t kMaxResident = 72 * 1024;
+
+Shape shape_for(int M, int64_t K) {
+    if (w4_x_bytes(8, 2, M, K, true, 1) <= kMaxResident) return {2, 2, w4_kwl(2, K), true};
+    return {4, 1, 2, false};
+}
+
+template <int F, int NG, int RT, int NS, int MI, bool kResident>
+hipError_t launch_one(Int4Group& g, int64_t items, int64_t kmax, hipStream_t s) {
+    typedef RowTiles<F, NG, RT, NS, MI, kResident, false> Tiles;
+    g.x_bufs = 2;
+    const size_t lds = Tiles::kFixedBytes + w4_x_bytes(4, NS, g.M, kmax, kResident, 2);
+    if (lds > 65536) {
+        const hipError_t e =
+            hipFuncSetAttribute(reinterpret_cast<const void*>(&int4_gemv_kernel<F, NG, RT, NS, MI, kResident>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t grid = std::min<int64_t>(items, device_cu_count());
+    int4_gemv_kernel<F, NG, RT, NS, MI, kResident><<<dim3((unsigned)grid), dim3(kThreads), lds, s>>>(g);
     return hipGetLastError();
 }
 
+template <int F, int NG, int MI>
+hipError_t launch_shape(Int4Group& g, int64_t items, bool resident, int64_t kmax, hipStream_t s) {
+    if (resident) return launch_one<F, NG, 2, 2, MI, true>(g, items, kmax, s);
+    return launch_one<F, NG, 4, 1, MI, false>(g, items, kmax, s);
+}
+
 template <int F, int NG>
-hipError_t launch_m(const Int4Group& g, int64_t items, int rt, hipStream_t s) {
-    if (g.M <= 4) return launch_one<F, NG, 1, 2>(g, items, s);
-    (void)rt;
-    return launch_one<F, NG, 1, 1>(g, items, s);
+hipError_t launch_mi(Int4Group& g, int64_t items, bool resident, int64_t kmax, hipStream_t s) {
+    if (g.M <= 4) return launch_shape<F, NG, 1>(g, items, resident, kmax, s);
+    if (g.M <= 8) return launch_shape<F, NG, 2>(g, items, resident, kmax, s);
+    return launch_shape<F, NG, 4>(g, items, resident, kmax, s);
 }
 
 template <int F>
-hipError_t launch_ng(const Int4Group& g, int64_t items, int ng, int rt, hipStream_t s) {
-    if (ng == 4) return launch_m<F, 4>(g, items, rt, s);
-    if (ng == 2) return launch_m<F, 2>(g, items, rt, s);
-    return launch_m<F, 1>(g, items, rt, s);
+hipError_t launch_ng(Int4Group& g, int64_t items, int ng, bool resident, int64_t kmax, hipStream_t s) {
+    if (ng == 4) return launch_mi<F, 4>(g, items, resident, kmax, s);
+    if (ng == 2) return launch_mi<F, 2>(g, items, resident, kmax, s);
+    return launch_mi<F, 1>(g, items, resident, kmax, s);
 }
 
 }  // namespace
@@ -205,28 +159,36 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
     for (int32_t first = 0; first < count; ++first) {
         if (done[first]) continue;
         const int ng = int4_groups_per_chunk(items[first].st->group);
+        // the weights of the launch: one scale granularity, activations that all fit, or all do not
+        const bool resident = shape_for(M, items[first].st->cols).resident;
         Int4Group g;
         g.ntasks = 0;
         g.M = M;
-        int64_t item0 = 0;
+        g.cost0[0] = 0;
+        int64_t total = 0, kmax = 0;
         for (int32_t i = first; i < count && g.ntasks < kMaxGemvTasks; ++i) {
-            if (done[i] || int4_groups_per_chunk(items[i].st->group) != ng) continue;
             const qk_int4_state* st = items[i].st;
-            const int64_t tiles = (st->rows + 15) / 16;
-            if (g.ntasks > 0 && item0 + tiles > (1 << 24)) break;
+            const Shape sh = shape_for(M, st->cols);
+            if (done[i] || int4_groups_per_chunk(st->group) != ng || sh.resident != resident) continue;
             done[i] = true;
-            Int4Task& t = g.t[g.ntasks++];
+            const int64_t rows = (16 * sh.rt * 8) >> sh.kwl;
+            const int64_t tiles = (st->rows + rows - 1) / rows;
+            Int4Task& t = g.t[g.ntasks];
             t.x = static_cast<const uint16_t*>(items[i].x);
             t.y = static_cast<uint16_t*>(items[i].y);
             t.w = int4_view(st);
             t.N = st->rows;
             t.K = st->cols;
-            t.item0 = item0;
             t.x_aligned = st->cols % 8 == 0 && reinterpret_cast<uintptr_t>(items[i].x) % 16 == 0;
-            t.pad = 0;
-            item0 += tiles;
+            t.kwl = sh.kwl;
+            g.chunks[g.ntasks] = (int32_t)((st->cols + kChunk - 1) / kChunk * (8 >> sh.kwl));
+            total += tiles;
+            kmax = std::max(kmax, st->cols);
+            g.cost0[g.ntasks + 1] = g.cost0[g.ntasks] + tiles * g.chunks[g.ntasks];
+            ++g.ntasks;
         }
-        const hipError_t e = f16 ? launch_ng<kInt4F16>(g, item0, ng, 1, s) : launch_ng<kInt4Bf16>(g, item0, ng, 1, s);
+        const hipError_t e = f16 ? launch_ng<kInt4F16>(g, total, ng, resident, kmax, s)
+                                 : launch_ng<kInt4Bf16>(g, total, ng, resident, kmax, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -6,18 +6,16 @@
 // with the weights of all experts stacked in two quantized tensors, gate and up rows of an
 // expert one after the other in the first.
 //
-//   moe_route_kernel  one workgroup: each wave selects one token's experts, then the
-//                     experts with a token are listed in increasing order, each with its
-//                     tokens (for the up kernel) and with a weight and a row of h per
-//                     token (for the down kernel).
-//   moe_up_kernel     a workgroup per (listed expert, 16 rows of gate and the 16 of up):
-//                     only the expert's own tokens are staged in LDS; each wave takes
-//                     128-k chunks of the rows, the partial sums are added in wave order.
-//                     h is kept as two bf16 values (hi + lo, 16 bits of mantissa): the
-//                     down product then loses nothing against the bf16 or fp16 output.
-//   moe_down_kernel   a workgroup per 16 outputs; its waves take the (expert, chunk) steps in
-//                     turn and keep one accumulator per token, the token's weight being
-//                     applied with the row scale: no partial sums in memory, no atomics.
+//   moe_route_kernel    one workgroup: each wave selects one token's experts, then the
+//                       experts that have a token are listed in increasing order, each with
+//                       its tokens, their weights and their pairs (token, position).
+//   moe_up_kernel       items of 16 rows of gate and the same 16 of up of a listed expert
+//                       (RowTiles, w4_tile.h), dealt in equal shares; only the expert's own
+//                       tokens are staged.  h is written in fp32.
+//   moe_down_kernel     items of rows of Wd of a listed expert times its tokens' h, which enters
+//                       the matrix cores as two bf16 values (hi + lo, 16 bits of mantissa), so the
+//                       product loses nothing against the 16-bit output; w h Wd^T goes to memory in fp32.
+//   moe_combine_kernel  adds each token's parts in the order of its choices: no atomics.
 // Every weight of a listed expert is read once per layer; that is the bound.
 #include <algorithm>
 
@@ -33,17 +31,18 @@ using namespace w4;
 constexpr int kMaxT = 16;
 constexpr int kMaxE = 256;
 constexpr int kMaxK = 16;
+constexpr int kThreads = 512;
 
 // Routing result, in the workspace.
 struct Routes {
     int32_t nactive;
     int32_t pad[3];
+    int32_t chosen[kMaxT];            // experts of each token (its positions 0, 1, ... are taken)
     int32_t expert[kMaxE];            // listed experts, increasing
     int32_t count[kMaxE];             // tokens of each
     uint8_t tok[kMaxE][kMaxT];        // those tokens, increasing
-    int16_t row[kMaxE][kMaxT];        // row of h of each: t * top_k + position
-    float w[kMaxE][kMaxT];            // weight per token, 0 for the others
-    int16_t hrow[kMaxE][kMaxT];       // row of h per token, -1 for the others
+    uint8_t pair[kMaxE][kMaxT];       // their pairs: t * top_k + position
+    float w[kMaxE][kMaxT];            // their weights
 };
 
 struct RouteArgs {
@@ -88,8 +87,8 @@ __global__ __launch_bounds__(kMaxT * 64) void moe_route_kernel(RouteArgs a, Rout
             for (int d = 32; d > 0; d >>= 1) den += __shfl_xor(den, d);
         }
         float mine = 0.0f;                               // lane k: weight of the k-th choice
-        int id = -1;
-        for (int k = 0; k < a.top_k; ++k) {
+        int id = -1, k = 0;
+        for (; k < a.top_k; ++k) {
             float best = v[0];
             int e = lane;
 #pragma unroll
@@ -115,6 +114,7 @@ __global__ __launch_bounds__(kMaxT * 64) void moe_route_kernel(RouteArgs a, Rout
                 id = c;
             }
         }
+        if (lane == 0) out->chosen[t] = k;
         if (lane < a.top_k) {
             ids[t][lane] = id;
             wt[t][lane] = id >= 0 ? mine / den : 0.0f;
@@ -138,25 +138,18 @@ __global__ __launch_bounds__(kMaxT * 64) void moe_route_kernel(RouteArgs a, Rout
     out->expert[rank] = tid;
     out->count[rank] = __popc(mk);
     int pos = 0;
-    for (int tt = 0; tt < kMaxT; ++tt) {
-        float w = 0.0f;
-        int r = -1;
-        if ((mk >> tt) & 1u) {
-            for (int k = 0; k < a.top_k; ++k)
-                if (ids[tt][k] == tid) {
-                    w = wt[tt][k];
-                    r = tt * a.top_k + k;
-                }
-            out->tok[rank][pos] = (uint8_t)tt;
-            out->row[rank][pos] = (int16_t)r;
-            ++pos;
-        }
-        out->w[rank][tt] = w;
-        out->hrow[rank][tt] = (int16_t)r;
+    for (uint32_t left = mk; left; left &= left - 1, ++pos) {
+        const int tt = __ffs((int)left) - 1;
+        for (int k = 0; k < a.top_k; ++k)
+            if (ids[tt][k] == tid) {
+                out->tok[rank][pos] = (uint8_t)tt;
+                out->pair[rank][pos] = (uint8_t)(tt * a.top_k + k);
+                out->w[rank][pos] = wt[tt][k];
+            }
     }
 }
 
-// A weight view of either form, with the calls the kernels make of it.
+// A weight view of either form.
 template <int F>
 struct View {
     typedef Int4View type;
@@ -166,300 +159,202 @@ struct View<kLevels> {
     typedef LevelsView type;
 };
 
-template <int F, int NG>
-struct Scales {
-    typedef GroupScales<NG> type;
-};
-template <int NG>
-struct Scales<kLevels, NG> {
-    typedef LevelScales type;
-};
-
 template <int F>
-struct UpArgs {
-    const uint16_t* x;       // [T, H]
+struct ExpertArgs {
+    const void* x;           // up: x [T, H], 16-bit; down: h [T * top_k, Ipad], fp32
     typename View<F>::type w;
     const Routes* routes;
-    uint16_t* h;             // [T * top_k, 2 * Ipad]: per 8 values, 8 hi then 8 lo
+    float* out;              // up: h; down: the parts [T * top_k, H]
     int64_t H;
     int64_t I;
-    int64_t Ipad;            // I rounded up to a chunk
-    int32_t T;
+    int64_t Ipad;            // I rounded up to 8 values
+    int32_t x_rows;
     int32_t x_aligned;
+    int32_t kwl;
+    int32_t x_bufs;
 };
 
-template <int F>
-constexpr int kUpWaves = F == kLevels ? 16 : 8;
-template <int F>
-constexpr int kUpPitch = kUpWaves<F> * kChunk * 2 + 16;
+// Activations of a whole row stay in LDS up to this size.
+template <int F, int MI>
+constexpr size_t kMaxRows = F != kLevels ? 72 * 1024 : MI == 1 ? 36 * 1024 : 28 * 1024;
 
-template <int F, int NG>
-__global__ __launch_bounds__(kUpWaves<F> * 64) void moe_up_kernel(UpArgs<F> p) {
+template <int F, int NG, int MI, bool kResident>
+__global__ __launch_bounds__(kThreads, 2) void moe_up_kernel(ExpertArgs<F> p) {
     extern __shared__ __align__(16) uint8_t lds[];
-    constexpr int W = kUpWaves<F>, kThreads = W * 64;
-    constexpr int kWinUnits = W * kChunk / 8;
-    constexpr int kPitch = kUpPitch<F>;
-    constexpr int kGroupMfmas = 4 / NG;
-    const int a = blockIdx.y;
-    if (a >= p.routes->nactive) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = lane & 15, hq = lane >> 4;
-    const int M = p.routes->count[a];
-    const int64_t e = p.routes->expert[a];
-    const int64_t i0 = (int64_t)blockIdx.x * 16;
-    uint8_t* xlds = lds + (F == kLevels ? kTabBytes : 0);
-    // rows of gate and of up (past the last one of the expert: its last row, never stored)
-    const int64_t in = i0 + n < p.I ? i0 + n : p.I - 1;
-    const int64_t row[2] = {e * 2 * p.I + in, e * 2 * p.I + p.I + in};
-    const uint8_t* codes[2] = {p.w.codes + row[0] * p.w.stride, p.w.codes + row[1] * p.w.stride};
-    const int nchunk = (int)((p.H + kChunk - 1) / kChunk);
-    const int nwin = (nchunk + W - 1) / W;
-    float mean = 0.0f;
-    if constexpr (F == kLevels) {
-        build_table(lds, p.w.levels, tid, kThreads);
-        if (p.w.nested) mean = *p.w.dq_mean;
-    }
-
-    floatx4_t y[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    u32x4_t cw[2][2];
-    typename Scales<F, NG>::type sc[2][2];
-    auto fetch = [&](int buf, int win) {
-        int c = win * W + wave;
-        c = c < nchunk ? c : nchunk - 1;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            cw[buf][r] = load_codes(codes[r], p.w.stride, c, hq);
-            sc[buf][r].load(p.w, row[r], c);
-        }
-    };
-    auto stage = [&](int win) {
-        for (int i = tid; i < M * kWinUnits; i += kThreads) {
-            const int m = i / kWinUnits, u = i % kWinUnits;
-            u32x4_t v = load_x8(p.x + (int64_t)p.routes->tok[a][m] * p.H, (int64_t)win * (W * kChunk) + 8 * u, p.H,
-                                p.x_aligned);
-            if constexpr (F != kLevels) v = int4_order(v);
-            *reinterpret_cast<u32x4_t*>(xlds + m * kPitch + 16 * u) = v;
-        }
-    };
-    const uint8_t* arow = xlds + (n < M ? n : M - 1) * kPitch + wave * (kChunk * 2) + 16 * hq;
-    auto compute = [&](int buf, int win) {
-        if (win * W + wave >= nchunk) return;
-        u32x4_t w[2] = {cw[buf][0], cw[buf][1]};
-        transpose_groups(w[0]);
-        transpose_groups(w[1]);
-#pragma unroll
-        for (int q = 0; q < NG; ++q) {
-            floatx4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, xs = {0, 0, 0, 0};
-#pragma unroll
-            for (int j = q * kGroupMfmas; j < (q + 1) * kGroupMfmas; ++j) {
-                const u32x4_t av = *reinterpret_cast<const u32x4_t*>(arow + 64 * j);
-                if constexpr (F == kLevels) {
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) acc[r] = mfma<F>(av, decode8_table(lds, w[r][j], 4 * lane), acc[r]);
-                } else {
-                    xs = mfma<F>(av, ones<F>(), xs);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) acc[r] = mfma<F>(av, decode8<F>(w[r][j]), acc[r]);
+    typedef RowTiles<F, NG, 2, kResident ? 2 : 1, MI, kResident, false> Tiles;
+    uint8_t* work = lds + (F == kLevels ? kTabBytes : 0);
+    if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads);
+    // an item: per row group 16 rows of gate and the same of up of one listed expert; equal shares of the items
+    const int step = 128 >> p.kwl;
+    const int64_t tiles = (p.Ipad + step - 1) / step, all = tiles * p.routes->nactive;
+    int64_t lo = all * blockIdx.x / gridDim.x;
+    const int64_t hi = all * (blockIdx.x + 1) / gridDim.x;
+    while (lo < hi) {
+        const int a = (int)(lo / tiles);
+        const int64_t i0 = lo - a * tiles, i1 = hi - a * tiles < tiles ? hi - a * tiles : tiles;
+        lo += i1 - i0;
+        const int count = p.routes->count[a];
+        const int64_t e = p.routes->expert[a];
+        Rows<2> r;
+        r.base[0] = e * 2 * p.I;
+        r.base[1] = r.base[0] + p.I;
+        r.off[0] = r.off[1] = 0;
+        r.step = step;
+        r.group_step = 16;
+        r.count = p.I;
+        r.x = p.x;
+        r.K = r.x_pitch = p.H;
+        r.x_rows = p.x_rows;
+        r.x_aligned = p.x_aligned;
+        r.kwl = p.kwl;
+        r.x_bufs = p.x_bufs;
+        // 4 MI tokens at a time (an expert rarely has more)
+        for (int m0 = 0; m0 < count; m0 += 4 * MI) {
+            const int M = count - m0 < 4 * MI ? count - m0 : 4 * MI;
+            r.xrow = p.routes->tok[a] + m0;
+            r.M = M;
+            Tiles::run(p.w, r, i0, i1, lds, work, [&](int64_t item, const float* put) {
+                for (int o = threadIdx.x; o < (64 * MI * 8) >> p.kwl; o += kThreads) {
+                    const int q = o / (64 * MI), s = o % (64 * MI), m = Tiles::act_of(s);
+                    const int64_t i = item * step + 16 * q + (s & 15);
+                    if (m < M && i < p.Ipad) {
+                        const float gate = Tiles::sum(put, p.kwl, q, 0, s), up = Tiles::sum(put, p.kwl, q, 1, s);
+                        const float v = gate / (1.0f + expf(-gate)) * up;
+                        p.out[p.routes->pair[a][m0 + m] * p.Ipad + i] = i < p.I ? v : 0.0f;
+                    }
                 }
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if constexpr (F == kLevels) {
-                    const float s = sc[buf][r].scale(p.w, mean, q);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[r][i] = fmaf(s, acc[r][i], y[r][i]);
-                } else {
-                    const float s = sc[buf][r].scale(p.w, q);
-                    const float zb = (float)sc[buf][r].z[q] + kCodeBias<F>;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[r][i] = fmaf(s, fmaf(-zb, xs[i], acc[r][i]), y[r][i]);
-                }
-            }
-        }
-    };
-
-    fetch(0, 0);
-    for (int win = 0; win < nwin; win += 2) {
-        stage(win);
-        if (win + 1 < nwin) fetch(1, win + 1);
-        __syncthreads();
-        compute(0, win);
-        __syncthreads();
-        if (win + 1 < nwin) {
-            stage(win + 1);
-            if (win + 2 < nwin) fetch(0, win + 2);
-            __syncthreads();
-            compute(1, win + 1);
-            __syncthreads();
-        }
-    }
-
-    floatx4_t* red = reinterpret_cast<floatx4_t*>(lds);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) red[(wave * 2 + r) * 64 + lane] = y[r];
-    __syncthreads();
-    const float* redf = reinterpret_cast<const float*>(lds);
-    if (tid < 256) {
-        float gate = 0.0f, up = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            gate += redf[w * 512 + tid];
-            up += redf[w * 512 + 256 + tid];
-        }
-        const int l = tid >> 2, m = 4 * (l >> 4) + (tid & 3), i = (int)i0 + (l & 15);
-        if (m < M) {
-            float v = gate / (1.0f + expf(-gate)) * up;
-            if (i >= p.I) v = 0.0f;                      // the padding of h takes part in the down product
-            const uint16_t hi = float_to_bits16(v, false);
-            const uint16_t lo = float_to_bits16(v - bf16_bits_to_float(hi), false);
-            uint16_t* dst = p.h + (int64_t)p.routes->row[a][m] * (2 * p.Ipad) + (i >> 3) * 16 +
-                            (F == kLevels ? (i & 7) : int4_slot(i));
-            dst[0] = hi;
-            dst[8] = lo;
+            });
         }
     }
 }
 
-template <int F>
-struct DownArgs {
-    const uint16_t* h;
-    typename View<F>::type w;
-    const Routes* routes;
-    uint16_t* y;             // [T, H]
-    int64_t H;
-    int64_t Ipad;
-    int32_t nchunk;
-    int32_t T;
-    int32_t y_f16;
-    int32_t pad;
-};
-
-constexpr int kDownWaves = 16;
-
-// Two: more than 8 tokens, hi and lo of h in products of their own; otherwise rows 0..7 of the
-// activation operand are the tokens' hi parts and rows 8..15 their lo parts.
-template <int F, int NG, bool Two>
-__global__ __launch_bounds__(kDownWaves * 64) void moe_down_kernel(DownArgs<F> p) {
+template <int F, int NG, int RT, int MI, bool kResident>
+__global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(ExpertArgs<F> p) {
     extern __shared__ __align__(16) uint8_t lds[];
-    constexpr int W = kDownWaves, kThreads = W * 64;
-    constexpr int kGroupMfmas = 4 / NG;
-    constexpr int kParts = Two ? 2 : 1;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = lane & 15, hq = lane >> 4;
-    const int nact = p.routes->nactive;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int64_t nn = n0 + n < p.H ? n0 + n : p.H - 1;
-    float mean = 0.0f;
-    if constexpr (F == kLevels) {
-        build_table(lds, p.w.levels, tid, kThreads);
-        if (p.w.nested) mean = *p.w.dq_mean;
-        __syncthreads();
-    }
-    const int tok = Two ? n : (n & 7);                   // token of the lane's activation row
-    const int wt0 = Two ? 4 * hq : (4 * hq) & 7;         // token of the lane's first accumulator
-
-    floatx4_t y = {0, 0, 0, 0};
-    struct Job {
-        u32x4_t code;
-        u32x4_t a[kParts][4];
-        typename Scales<F, NG>::type sc;
-        floatx4_t wt;
-    };
-    Job job[2];
-    const int njobs = nact * p.nchunk;
-    auto fetch = [&](Job& jb, int q) {
-        const int a = q / p.nchunk, c = q % p.nchunk;
-        const int64_t row = (int64_t)p.routes->expert[a] * p.H + nn;
-        jb.code = load_codes(p.w.codes + row * p.w.stride, p.w.stride, c, hq);
-        jb.sc.load(p.w, row, c);
-        jb.wt = *reinterpret_cast<const floatx4_t*>(&p.routes->w[a][wt0]);
-        const int r = p.routes->hrow[a][tok];
-        const uint16_t* src = p.h + (int64_t)r * (2 * p.Ipad) + (c * kChunk + 8 * hq) * 2 + (Two ? 0 : 8 * (n >> 3));
+    typedef RowTiles<F, NG, RT, kResident ? 2 : 1, MI, kResident, true> Tiles;
+    uint8_t* work = lds + (F == kLevels ? kTabBytes : 0);
+    if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads);
+    const int step = (16 * RT * 8) >> p.kwl;
+    const int64_t tiles = (p.H + step - 1) / step, all = tiles * p.routes->nactive;
+    int64_t lo = all * blockIdx.x / gridDim.x;
+    const int64_t hi = all * (blockIdx.x + 1) / gridDim.x;
+    while (lo < hi) {
+        const int a = (int)(lo / tiles);
+        const int64_t i0 = lo - a * tiles, i1 = hi - a * tiles < tiles ? hi - a * tiles : tiles;
+        lo += i1 - i0;
+        const int count = p.routes->count[a];
+        Rows<RT> r;
 #pragma unroll
-        for (int s = 0; s < kParts; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                jb.a[s][j] = (u32x4_t){0, 0, 0, 0};
-                if (r >= 0) jb.a[s][j] = *reinterpret_cast<const u32x4_t*>(src + 64 * j + 8 * s);
-            }
-    };
-    auto compute = [&](Job& jb) {
-        u32x4_t w = jb.code;
-        transpose_groups(w);
-#pragma unroll
-        for (int q = 0; q < NG; ++q) {
-            floatx4_t acc = {0, 0, 0, 0}, xs = {0, 0, 0, 0};
-#pragma unroll
-            for (int j = q * kGroupMfmas; j < (q + 1) * kGroupMfmas; ++j) {
-                u32x4_t b;
-                if constexpr (F == kLevels) b = decode8_table(lds, w[j], 4 * lane);
-                else b = decode8<F>(w[j]);
-#pragma unroll
-                for (int s = 0; s < kParts; ++s) {
-                    acc = mfma<F>(jb.a[s][j], b, acc);
-                    if constexpr (F != kLevels) xs = mfma<F>(jb.a[s][j], ones<F>(), xs);
+        for (int t = 0; t < RT; ++t) {
+            r.base[t] = p.routes->expert[a] * p.H;
+            r.off[t] = 16 * t;
+        }
+        r.step = step;
+        r.group_step = 16 * RT;
+        r.count = p.H;
+        r.x = p.x;
+        r.K = p.I;
+        r.x_pitch = p.Ipad;
+        r.x_rows = p.x_rows;
+        r.x_aligned = 1;
+        r.kwl = p.kwl;
+        r.x_bufs = p.x_bufs;
+        // two activation rows a token
+        for (int m0 = 0; m0 < count; m0 += 2 * MI) {
+            const int M = count - m0 < 2 * MI ? count - m0 : 2 * MI;
+            r.xrow = p.routes->pair[a] + m0;
+            r.M = M;
+            Tiles::run(p.w, r, i0, i1, lds, work, [&](int64_t item, const float* put) {
+                for (int o = threadIdx.x; o < M * step; o += kThreads) {
+                    const int m = o / step, row = o % step, q = row / (16 * RT), t = row / 16 % RT;
+                    const int64_t n = item * step + row;
+                    const float v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m)) +
+                                    Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m + 1));
+                    if (n < p.H) p.out[p.routes->pair[a][m0 + m] * p.H + n] = v * p.routes->w[a][m0 + m];
                 }
-            }
-            float s;
-            if constexpr (F == kLevels) s = jb.sc.scale(p.w, mean, q);
-            else s = jb.sc.scale(p.w, q);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v = acc[i];
-                if constexpr (F != kLevels) v = fmaf(-((float)jb.sc.z[q] + kCodeBias<F>), xs[i], v);
-                y[i] = fmaf(s * jb.wt[i], v, y[i]);
-            }
+            });
         }
-    };
-
-    if (wave < njobs) fetch(job[0], wave);
-    for (int q = wave; q < njobs; q += 2 * W) {
-        if (q + W < njobs) fetch(job[1], q + W);
-        compute(job[0]);
-        if (q + W < njobs) {
-            if (q + 2 * W < njobs) fetch(job[0], q + 2 * W);
-            compute(job[1]);
-        }
-    }
-
-    __syncthreads();                                     // the last table reads
-    floatx4_t* red = reinterpret_cast<floatx4_t*>(lds);
-    red[wave * 64 + lane] = y;
-    __syncthreads();
-    if (tid < 256) {
-        const int l = tid >> 2, m = 4 * (l >> 4) + (tid & 3);
-        const float* redf = reinterpret_cast<const float*>(lds);
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            float u = redf[w * 256 + tid];
-            if (!Two && tid < 128) u += redf[w * 256 + tid + 128];     // the lo part: lane + 32
-            v += u;
-        }
-        const int64_t o = n0 + (l & 15);
-        if (m < p.T && o < p.H) p.y[m * p.H + o] = float_to_bits16(v, p.y_f16);
     }
 }
 
-template <int F, int NG>
-hipError_t launch_up(const UpArgs<F>& p, int32_t amax, hipStream_t s) {
-    constexpr int W = kUpWaves<F>;
-    const size_t lds = std::max<size_t>((F == kLevels ? kTabBytes : 0) + (size_t)p.T * kUpPitch<F>,
-                                        (size_t)W * 2 * 64 * 16);
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_up_kernel<F, NG>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+__global__ __launch_bounds__(256) void moe_combine_kernel(const float* parts, const Routes* routes, uint16_t* y,
+                                                          int64_t H, int32_t top_k, int32_t f16) {
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int t = blockIdx.y;
+    if (n >= H) return;
+    const int chosen = routes->chosen[t];
+    const float* src = parts + (int64_t)t * top_k * H + n;
+    float v = 0.0f;
+    for (int k = 0; k < chosen; ++k) v += src[k * H];
+    y[t * H + n] = float_to_bits16(v, f16);
+}
+
+template <class K>
+hipError_t allow_lds(K kernel, size_t lds) {
+    if (lds <= 65536) return hipSuccess;
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+}
+
+// rows: activation rows that a pass stages at most
+template <int F, int NG, int MI, bool kResident>
+hipError_t launch_up_one(ExpertArgs<F> p, int rows, int32_t listed, hipStream_t s) {
+    constexpr int NS = kResident ? 2 : 1;
+    typedef RowTiles<F, NG, 2, NS, MI, kResident, false> Tiles;
+    p.kwl = kResident ? w4_kwl(NS, p.H) : 2;
+    p.x_bufs = 2;
+    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, NS, rows, p.H, kResident, 2);
+    const hipError_t e = allow_lds(&moe_up_kernel<F, NG, MI, kResident>, lds);
     if (e != hipSuccess) return e;
-    moe_up_kernel<F, NG><<<dim3((unsigned)(p.Ipad / 16), (unsigned)amax), dim3(W * 64), lds, s>>>(p);
+    const int64_t items = (p.Ipad + (128 >> p.kwl) - 1) / (128 >> p.kwl) * listed;
+    moe_up_kernel<F, NG, MI, kResident>
+        <<<dim3((unsigned)std::min<int64_t>(items, device_cu_count())), dim3(kThreads), lds, s>>>(p);
     return hipGetLastError();
 }
 
+template <int F, int NG, int MI>
+hipError_t launch_up_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hipStream_t s) {
+    const int rows = std::min(T, 4 * MI);
+    if (w4_x_bytes(8, 2, rows, p.H, true, 1) <= kMaxRows<F, MI>) return launch_up_one<F, NG, MI, true>(p, rows, listed, s);
+    return launch_up_one<F, NG, MI, false>(p, rows, listed, s);
+}
+
+// Tokens that a pass over an expert's rows takes (4 MI): by the number that it has on average.
 template <int F, int NG>
-hipError_t launch_down(const DownArgs<F>& p, hipStream_t s) {
-    const size_t lds = F == kLevels ? kTabBytes : kDownWaves * 64 * 16;
-    const dim3 grid((unsigned)((p.H + 15) / 16));
-    if (p.T > 8) moe_down_kernel<F, NG, true><<<grid, dim3(kDownWaves * 64), lds, s>>>(p);
-    else moe_down_kernel<F, NG, false><<<grid, dim3(kDownWaves * 64), lds, s>>>(p);
+hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, hipStream_t s) {
+    const int pairs = m.T * m.top_k;
+    if (m.T <= 4 || pairs <= 2 * m.E) return launch_up_mi<F, NG, 1>(p, m.T, listed, s);
+    if (F == kLevels || m.T <= 8 || pairs <= 5 * m.E) return launch_up_mi<F, NG, 2>(p, m.T, listed, s);
+    return launch_up_mi<F, NG, F == kLevels ? 2 : 4>(p, m.T, listed, s);
+}
+
+template <int F, int NG, int RT, int MI, bool kResident>
+hipError_t launch_down_one(ExpertArgs<F> p, int rows, int32_t listed, hipStream_t s) {
+    constexpr int NS = kResident ? 2 : 1;
+    typedef RowTiles<F, NG, RT, NS, MI, kResident, true> Tiles;
+    p.kwl = kResident ? w4_kwl(NS, p.I) : 2;
+    p.x_bufs = 2;
+    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, NS, rows, p.I, kResident, 2);
+    const hipError_t e = allow_lds(&moe_down_kernel<F, NG, RT, MI, kResident>, lds);
+    if (e != hipSuccess) return e;
+    const int64_t step = (16 * RT * 8) >> p.kwl, items = (p.H + step - 1) / step * listed;
+    moe_down_kernel<F, NG, RT, MI, kResident>
+        <<<dim3((unsigned)std::min<int64_t>(items, device_cu_count())), dim3(kThreads), lds, s>>>(p);
     return hipGetLastError();
+}
+
+template <int F, int NG, int MI>
+hipError_t launch_down_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hipStream_t s) {
+    const int rows = std::min(2 * T, 4 * MI);
+    if (w4_x_bytes(8, 2, rows, p.I, true, 1) > kMaxRows<F, MI>) return launch_down_one<F, NG, 2, MI, false>(p, rows, listed, s);
+    return launch_down_one<F, NG, 2, MI, true>(p, rows, listed, s);
+}
+
+template <int F, int NG>
+hipError_t launch_down(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, hipStream_t s) {
+    const int pairs = m.T * m.top_k;
+    if (m.T <= 2 || pairs <= m.E) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
+    if (F == kLevels || m.T <= 4 || 2 * pairs <= 5 * m.E) return launch_down_mi<F, NG, 2>(p, m.T, listed, s);
+    return launch_down_mi<F, NG, F == kLevels ? 2 : 4>(p, m.T, listed, s);
 }
 
 LevelsView levels_view(const MatArgs& w) {
@@ -470,61 +365,52 @@ LevelsView levels_view(const MatArgs& w) {
     v.dq_scale = w.w.dq_scale;
     v.dq_mean = w.w.dq_mean;
     v.stride = w.K / 2;
-    v.last_block = (w.w.n + w.w.blocksize - 1) / w.w.blocksize - 1;
     v.bshift = w.w.blocksize_log2;
     v.nested = w.w.nested;
     for (int i = 0; i < 16; ++i) v.levels[i] = w.w.levels[i];
     return v;
 }
 
+// The workspace: routes, h, parts.
 constexpr size_t kRoutesBytes = (sizeof(Routes) + 255) / 256 * 256;
+size_t h_bytes(int32_t T, int32_t top_k, int64_t I) {
+    return ((size_t)T * (size_t)top_k * (size_t)((I + 7) / 8 * 8) * 4 + 255) / 256 * 256;
+}
 
 struct Buffers {
     Routes* routes;
-    uint16_t* h;
+    float* h;
+    float* parts;
 };
-Buffers buffers(void* workspace) {
+Buffers buffers(const MoeItem& m, void* workspace) {
     uint8_t* b = static_cast<uint8_t*>(workspace);
-    return {reinterpret_cast<Routes*>(b), reinterpret_cast<uint16_t*>(b + kRoutesBytes)};
+    return {reinterpret_cast<Routes*>(b), reinterpret_cast<float*>(b + kRoutesBytes),
+            reinterpret_cast<float*>(b + kRoutesBytes + h_bytes(m.T, m.top_k, m.I))};
 }
 
 template <int F>
-UpArgs<F> up_args(const MoeItem& m, const Buffers& b) {
-    UpArgs<F> p;
-    p.x = static_cast<const uint16_t*>(m.x);
+ExpertArgs<F> expert_args(const MoeItem& m, const Buffers& b, bool up) {
+    ExpertArgs<F> p;
+    p.x = up ? m.x : b.h;
     p.routes = b.routes;
-    p.h = b.h;
+    p.out = up ? b.h : b.parts;
     p.H = m.H;
     p.I = m.I;
-    p.Ipad = (m.I + kChunk - 1) / kChunk * kChunk;
-    p.T = m.T;
-    p.x_aligned = m.H % 8 == 0 && reinterpret_cast<uintptr_t>(m.x) % 16 == 0;
+    p.Ipad = (m.I + 7) / 8 * 8;
+    p.x_rows = up ? m.T : m.T * m.top_k;
+    p.x_aligned = !up || (m.H % 8 == 0 && reinterpret_cast<uintptr_t>(m.x) % 16 == 0);
+    p.kwl = p.x_bufs = 0;
     return p;
 }
 
 template <int F>
-DownArgs<F> down_args(const MoeItem& m, const Buffers& b) {
-    DownArgs<F> p;
-    p.h = b.h;
-    p.routes = b.routes;
-    p.y = static_cast<uint16_t*>(m.y);
-    p.H = m.H;
-    p.Ipad = (m.I + kChunk - 1) / kChunk * kChunk;
-    p.nchunk = (int32_t)(p.Ipad / kChunk);
-    p.T = m.T;
-    p.y_f16 = m.f16;
-    p.pad = 0;
-    return p;
-}
-
-template <int F>
-hipError_t launch_up_int4(const MoeItem& m, const Buffers& b, const qk_int4_state* w, int32_t amax, hipStream_t s) {
-    UpArgs<F> p = up_args<F>(m, b);
+hipError_t launch_up_int4(const MoeItem& m, const Buffers& b, const qk_int4_state* w, int32_t listed, hipStream_t s) {
+    ExpertArgs<F> p = expert_args<F>(m, b, true);
     p.w = int4_view(w);
     const int ng = int4_groups_per_chunk(w->group);
-    if (ng == 4) return launch_up<F, 4>(p, amax, s);
-    if (ng == 2) return launch_up<F, 2>(p, amax, s);
-    return launch_up<F, 1>(p, amax, s);
+    if (ng == 4) return launch_up<F, 4>(p, m, listed, s);
+    if (ng == 2) return launch_up<F, 2>(p, m, listed, s);
+    return launch_up<F, 1>(p, m, listed, s);
 }
 
 hipError_t launch_route(const MoeItem& m, const Buffers& b, hipStream_t s) {
@@ -533,42 +419,50 @@ hipError_t launch_route(const MoeItem& m, const Buffers& b, hipStream_t s) {
     return hipGetLastError();
 }
 
+hipError_t launch_combine(const MoeItem& m, const Buffers& b, hipStream_t s) {
+    moe_combine_kernel<<<dim3((unsigned)((m.H + 255) / 256), (unsigned)m.T), dim3(256), 0, s>>>(
+        b.parts, b.routes, static_cast<uint16_t*>(m.y), m.H, m.top_k, m.f16);
+    return hipGetLastError();
+}
+
 }  // namespace
 
-size_t moe_workspace_bytes(int32_t T, int32_t top_k, int64_t I) {
-    const size_t ipad = ((size_t)I + kChunk - 1) / kChunk * kChunk;
-    return kRoutesBytes + (size_t)T * (size_t)top_k * ipad * 4;
+size_t moe_workspace_bytes(int32_t T, int32_t top_k, int64_t H, int64_t I) {
+    return kRoutesBytes + h_bytes(T, top_k, I) + (size_t)T * (size_t)top_k * (size_t)H * 4;
 }
 
 hipError_t launch_moe_int4(const MoeItem& m, const qk_int4_state* gate_up, const qk_int4_state* down, void* workspace,
                            hipStream_t s) {
-    const Buffers b = buffers(workspace);
-    const int32_t amax = std::min(m.E, m.T * m.top_k);
+    const Buffers b = buffers(m, workspace);
+    const int32_t listed = std::min(m.E, m.T * m.top_k);
     hipError_t e = launch_route(m, b, s);
     if (e != hipSuccess) return e;
-    e = m.f16 ? launch_up_int4<kInt4F16>(m, b, gate_up, amax, s) : launch_up_int4<kInt4Bf16>(m, b, gate_up, amax, s);
+    e = m.f16 ? launch_up_int4<kInt4F16>(m, b, gate_up, listed, s) : launch_up_int4<kInt4Bf16>(m, b, gate_up, listed, s);
     if (e != hipSuccess) return e;
-    DownArgs<kInt4Bf16> p = down_args<kInt4Bf16>(m, b);
+    ExpertArgs<kInt4Bf16> p = expert_args<kInt4Bf16>(m, b, false);
     p.w = int4_view(down);
     const int ng = int4_groups_per_chunk(down->group);
-    if (ng == 4) return launch_down<kInt4Bf16, 4>(p, s);
-    if (ng == 2) return launch_down<kInt4Bf16, 2>(p, s);
-    return launch_down<kInt4Bf16, 1>(p, s);
+    e = ng == 4 ? launch_down<kInt4Bf16, 4>(p, m, listed, s)
+        : ng == 2 ? launch_down<kInt4Bf16, 2>(p, m, listed, s) : launch_down<kInt4Bf16, 1>(p, m, listed, s);
+    if (e != hipSuccess) return e;
+    return launch_combine(m, b, s);
 }
 
 hipError_t launch_moe_levels(const MoeItem& m, const MatArgs& gate_up, const MatArgs& down, void* workspace,
                              hipStream_t s) {
-    const Buffers b = buffers(workspace);
-    const int32_t amax = std::min(m.E, m.T * m.top_k);
+    const Buffers b = buffers(m, workspace);
+    const int32_t listed = std::min(m.E, m.T * m.top_k);
     hipError_t e = launch_route(m, b, s);
     if (e != hipSuccess) return e;
-    UpArgs<kLevels> u = up_args<kLevels>(m, b);
+    ExpertArgs<kLevels> u = expert_args<kLevels>(m, b, true);
     u.w = levels_view(gate_up);
-    e = launch_up<kLevels, 2>(u, amax, s);
+    e = launch_up<kLevels, 2>(u, m, listed, s);
     if (e != hipSuccess) return e;
-    DownArgs<kLevels> d = down_args<kLevels>(m, b);
+    ExpertArgs<kLevels> d = expert_args<kLevels>(m, b, false);
     d.w = levels_view(down);
-    return launch_down<kLevels, 2>(d, s);
+    e = launch_down<kLevels, 2>(d, m, listed, s);
+    if (e != hipSuccess) return e;
+    return launch_combine(m, b, s);
 }
 
 }  // namespace qk

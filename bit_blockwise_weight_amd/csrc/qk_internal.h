@@ -218,7 +218,7 @@ struct MoeItem {
     int32_t renorm;       // weights relative to the chosen experts
     int32_t f16;          // x and y are fp16 (int4 experts), otherwise bf16
 };
-size_t moe_workspace_bytes(int32_t T, int32_t top_k, int64_t I);
+size_t moe_workspace_bytes(int32_t T, int32_t top_k, int64_t H, int64_t I);
 hipError_t launch_moe_int4(const MoeItem& m, const qk_int4_state* gate_up, const qk_int4_state* down, void* workspace,
                            hipStream_t s);
 hipError_t launch_moe_levels(const MoeItem& m, const MatArgs& gate_up, const MatArgs& down, void* workspace,

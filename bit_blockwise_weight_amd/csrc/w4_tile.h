@@ -2,12 +2,15 @@
 // weights straight from memory (int4 with group scales; NF4 and other 16-level tables
 // in the mixture-of-experts layer), for gfx950.
 //
-// One step of a wave is a "chunk": 16 weight rows x 128 k.  Lane l holds row n = l % 16
-// and, with h = l / 16, the 16 bytes of k = 128 c + 32 h + [0, 32): one 16-byte load, 64
-// contiguous bytes of a row per instruction.  The four dwords of a lane are transposed
-// over the four lane groups in registers (four lane swaps), after which dword j holds
-// k = 128 c + 32 j + 8 h + [0, 8): MFMA j (16x16x32) then covers the 32 consecutive k of
-// [128 c + 32 j, +32), so a scale group of 32 or more never splits an MFMA.
+// One step of a wave is a "chunk": 16 weight rows x 128 k.  For its MFMAs (16x16x32) lane l
+// holds row n = l % 16 and, with h = l / 16, the 16 bytes of k = 128 c + 32 h + [0, 32).  Where
+// a scale group covers the whole chunk its four MFMAs take the four dwords as they are, in any k
+// order; for groups of 64 two lane swaps, for groups of 32 four, exchange dwords between the
+// lane groups, so that a pair of MFMAs, or every one, stays inside a group.
+//
+// From memory the codes come in whole 128-byte lines, 8 rows x 128 bytes per load instruction,
+// and change to the layout above through a wave's own piece of LDS.  Loading them in that
+// layout directly (16 rows x 64 bytes an instruction) streams 105 MB in 23 us against 18 us.
 //
 //   A = activations (row m = l % 16, k = 8 (l / 16) + i), B = W^T (column n = l % 16, the
 //   same k), D: column n = l % 16, rows m = 4 (l / 16) + r.  A scale of row n is then one
@@ -55,10 +58,20 @@ __device__ __forceinline__ uint16_t float_to_bits16(float v, bool f16) {
     return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// d[j] of lane group h  ->  d[h] of lane group j (see the top of the file)
-__device__ __forceinline__ void transpose_groups(u32x4_t& d) {
+// Brings the four dwords of the lane groups into the order in which no MFMA crosses a scale
+// group, for NG groups in the chunk (see the top of the file).
+template <int NG>
+__device__ __forceinline__ void order_chunk(u32x4_t& d) {
+    if constexpr (NG == 1) return;
     auto a = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
     auto b = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+    if constexpr (NG == 2) {
+        d[0] = a[0];
+        d[1] = b[0];
+        d[2] = a[1];
+        d[3] = b[1];
+        return;
+    }
     auto lo = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
     auto hi = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
     d[0] = lo[0];
@@ -66,19 +79,44 @@ __device__ __forceinline__ void transpose_groups(u32x4_t& d) {
     d[2] = hi[0];
     d[3] = hi[1];
 }
+// First k, inside the chunk, of the eight that MFMA j takes from lane group h after order_chunk.
+template <int NG>
+__device__ __forceinline__ constexpr int chunk_k(int j, int h) {
+    if (NG == 1) return 32 * h + 8 * j;
+    if (NG == 2) return 64 * (j >> 1) + 32 * (h & 1) + 16 * (h >> 1) + 8 * (j & 1);
+    return 32 * j + 8 * h;
+}
 
-// Eight codes of a dword as an MFMA fragment (int4 forms).
+// Constants that the compiler must keep in registers (as literals it cannot use v_and_or_b32,
+// which may read one scalar register and no literal).
+struct Magic {
+    uint32_t m0, m4, e;          // masks of the low nibbles, of the next ones; exponent
+    __device__ __forceinline__ explicit Magic(bool f16) : m0(0x000F000Fu), m4(0x00F000F0u), e(f16 ? 0x64006400u : 0x43004300u) {
+        asm("" : "+s"(m0));
+        asm("" : "+s"(m4));
+        asm("" : "+v"(e));
+    }
+};
+
+// Eight codes of a dword as an MFMA fragment (int4 forms): 7 instructions in bf16, 9 in fp16.
 template <int F>
-__device__ __forceinline__ u32x4_t decode8(uint32_t w) {
+__device__ __forceinline__ u32x4_t decode8(uint32_t w, const Magic& k) {
     static_assert(F == kInt4Bf16 || F == kInt4F16, "levels are decoded through their table");
-    constexpr uint32_t kMagic = F == kInt4Bf16 ? 0x43004300u : 0x64006400u;
     u32x4_t f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | kMagic;
-        if constexpr (F == kInt4F16)
-            v = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, v) - (f16x2_t){1032, 1032});
-        f[i] = v;
+    if constexpr (F == kInt4Bf16) {
+        f[0] = (w & k.m0) | k.e;
+        f[1] = ((w >> 4) & k.m0) | k.e;
+        f[2] = ((w >> 8) & k.m0) | k.e;
+        f[3] = ((w >> 12) & k.m0) | k.e;
+    } else {
+        // 1024 + q less 1032, or (1024 + 16 q) / 16 less 72: q - 8 either way, exact
+        const uint32_t v = w >> 8;
+        const f16x2_t c1 = {-1032, -1032}, sc = {0.0625f, 0.0625f}, c2 = {-72, -72};
+        const uint32_t a0 = (w & k.m0) | k.e, a1 = (w & k.m4) | k.e, a2 = (v & k.m0) | k.e, a3 = (v & k.m4) | k.e;
+        f[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a0) + c1);
+        f[1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, a1), sc, c2));
+        f[2] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a2) + c1);
+        f[3] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, a3), sc, c2));
     }
     return f;
 }
@@ -130,48 +168,6 @@ struct Int4View {
     int32_t pad;
 };
 
-// Codes of one chunk of a row: bytes past the row's end are never read (what is read in
-// their place meets activations that are zero).
-__device__ __forceinline__ u32x4_t load_codes(const uint8_t* row, int64_t stride, int c, int h) {
-    int64_t off = (int64_t)c * (kChunk / 2) + 16 * h;
-    off = off < stride - 16 ? off : stride - 16;
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(row + off));
-}
-
-// Scales and zero points of one row in one chunk: NG groups of 128 / NG k.  Groups past the
-// row's end (they only meet zero activations) repeat the last one.
-template <int NG>
-struct GroupScales {
-    uint16_t s[NG];
-    uint8_t z[NG];
-    __device__ __forceinline__ void load(const Int4View& w, int64_t row, int c) {
-        const int64_t base = row * w.G;
-        const int g0 = (c * kChunk) >> w.gshift;
-#pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            const int g = g0 + i < w.G ? g0 + i : w.G - 1;
-            s[i] = w.scales[base + g];
-            z[i] = w.zeros ? w.zeros[base + g] : (uint8_t)8;
-        }
-    }
-    __device__ __forceinline__ float scale(const Int4View& w, int i) const {
-        return w.scale_f16 ? f16_bits_to_float(s[i]) : bf16_bits_to_float(s[i]);
-    }
-};
-
-// Eight consecutive activations of a row from k on, zero past the row's end (cols).
-__device__ __forceinline__ u32x4_t load_x8(const uint16_t* row, int64_t k, int64_t cols, bool aligned16) {
-    if (aligned16 && k + 8 <= cols) return *reinterpret_cast<const u32x4_t*>(row + k);
-    u32x4_t v = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = k + 2 * i < cols ? row[k + 2 * i] : 0u;
-        const uint32_t hi = k + 2 * i + 1 < cols ? row[k + 2 * i + 1] : 0u;
-        v[i] = lo | (hi << 16);
-    }
-    return v;
-}
-
 // A 16-level weight (NF4 and the like) as the kernels see it: rows of K elements, K a multiple
 // of 64, so that every run of 64 k of a row lies in one quantization block.
 struct LevelsView {
@@ -181,35 +177,9 @@ struct LevelsView {
     const float* dq_scale;
     const float* dq_mean;
     int64_t stride;           // K / 2
-    int64_t last_block;       // number of blocks - 1
     int32_t bshift;           // log2(block size)
     int32_t nested;
     float levels[16];
-};
-
-// Block scales of one row in one chunk (two runs of 64 k; a run past the row's end meets zero
-// activations, its index is only kept in range).
-struct LevelScales {
-    float a[2];
-    int8_t q[2];
-    __device__ __forceinline__ void load(const LevelsView& w, int64_t row, int c) {
-        const int64_t e = row * (2 * w.stride) + (int64_t)c * kChunk;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            int64_t b = (e + 64 * i) >> w.bshift;
-            b = b < w.last_block ? b : w.last_block;
-            if (w.nested) {
-                q[i] = w.q8[b];
-                a[i] = w.dq_scale[b / QK_DQ_BLOCK];
-            } else {
-                q[i] = 0;
-                a[i] = w.absmax[b];
-            }
-        }
-    }
-    __device__ __forceinline__ float scale(const LevelsView& w, float mean, int i) const {
-        return w.nested ? __fadd_rn(__fmul_rn((float)q[i], a[i]), mean) : a[i];
-    }
 };
 
 // Table of the 256 code bytes as (bf16 level of the high nibble, bf16 level of the low nibble),
@@ -233,6 +203,385 @@ __device__ __forceinline__ u32x4_t decode8_table(const uint8_t* tab, uint32_t w,
     }
     return f;
 }
+
+// ---------------------------------------------------------------------------
+// Items of RT tiles of 16 weight rows (per row group) times M activation rows, one after the
+// other by one workgroup of W waves: run() takes a run of items that share their activations.
+//
+// kw of the waves split k, W / kw groups of them take different rows.  A row is cut into windows
+// of kw * 256 NS k; a wave takes NS lines (of 128 bytes, 256 k) of each row per window, and the
+// partial outputs of the kw waves meet in LDS once per item and are added in their order (no
+// atomics, the same bits every time).  While a wave works on one window the codes and scales of
+// the next one (of the same item or the next) are already on their way into registers: one
+// workgroup per CU keeps W * NS * RT * 2 KB of codes in flight throughout.
+//
+// Activations (in the order of decoded int4, zero past K) live in LDS, 16 bytes more than a row
+// apart, so that a fragment read of 16 rows falls in different banks: all of K for the whole run
+// (kResident), or the current window, loaded one window ahead.  With kSplit they are fp32 and
+// become two bf16 rows, hi and lo (activation m: rows 2 m and 2 m + 1; 16 bits of mantissa).
+// Scales go to LDS as well, per row and group the pair (scale, scale * (zero point + bias)); a
+// wave writes and reads only its own, an odd number of pairs apart.
+//
+// Codes are read by buffer loads whose range check returns 0 without a memory access: rows past
+// the last one and lines past K cost no traffic and no branch.
+// ---------------------------------------------------------------------------
+typedef __attribute__((ext_vector_type(2))) float floatx2_t;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
+    const int32_t n = (int32_t)(bytes < 0x7FFF0000 ? bytes : 0x7FFF0000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, n, 0x00020000);
+}
+constexpr int32_t kOutside = 0x7FFF0000;  // an offset that no range reaches
+constexpr int kNontemporal = 2;           // cache policy: each code byte is read once
+
+// What a run of items reads.  Tile r of row group q in item i holds the rows base[r] + j,
+// j = i * step + q * group_step + off[r] + [0, 16), as far as j < count.
+template <int RT>
+struct Rows {
+    int64_t base[RT];
+    int32_t off[RT];
+    int32_t step, group_step;
+    int64_t count;
+    const void* x;           // 16-bit values, or fp32 (kSplit)
+    const uint8_t* xrow;     // activation m is row xrow[m] of x; NULL: row m
+    int64_t K;
+    int64_t x_pitch;         // values from a row of x to the next
+    int32_t x_rows;          // rows of x
+    int32_t x_aligned;       // 16-byte loads of x are possible
+    int32_t M;               // activations
+    int32_t kwl;             // log2(kw)
+    int32_t x_bufs;          // buffers for windows of x (not resident): 1 or 2
+};
+
+// The product's row 4 h + i lands in register i of lane group h.  With few activation rows only the
+// first MI registers of a group carry any: row m sits at 4 (m / MI) + m % MI.
+template <int MI>
+__device__ __forceinline__ constexpr int act_of_row(int row) { return MI * (row >> 2) + (row & (MI - 1)); }
+
+constexpr int kLineK = 256;               // k of a 128-byte line of codes
+
+// bytes of LDS that the activations take (rows: twice their number with kSplit)
+inline size_t w4_x_bytes(int kw, int NS, int rows, int64_t K, bool resident, int bufs) {
+    const size_t k = (size_t)((K + kLineK * NS - 1) / (kLineK * NS)) * (kLineK * NS);
+    return resident ? (size_t)rows * (k * 2 + 16) : (size_t)bufs * rows * ((size_t)kw * NS * kLineK * 2 + 16);
+}
+// log2 of the waves (of 8) that split a row of K: as many as it has windows' worth of lines
+inline int w4_kwl(int NS, int64_t K) {
+    const int64_t n = (K + kLineK * NS - 1) / (kLineK * NS);
+    return n > 4 ? 3 : n > 2 ? 2 : n > 1 ? 1 : 0;
+}
+
+template <int F, int NG, int RT, int NS, int MI, bool kResident, bool kSplit>
+struct RowTiles {
+    static constexpr int W = 8;
+    static constexpr int kThreads = W * 64;
+    static constexpr int U = 2 * NS;                            // chunks of a wave in a window
+    static constexpr int kMfmas = 4 / NG;                       // MFMAs per scale group
+    static constexpr int kEntries = U * NG;                     // scale groups of a wave's chunks in a window
+    static constexpr int kSPitch = kEntries | 1;
+    static constexpr int kSBatch = (kEntries + 3) / 4;          // of them per lane
+    static constexpr int kScaleBytes = W * RT * 16 * kSPitch * 8;
+    static constexpr int kCodeBytes = W * 16 * 128 * NS;        // a tile's codes changing layout
+    static constexpr int kPutBytes = W * RT * 64 * MI * 4;
+    static constexpr int kPuts = kPutBytes <= 8192 ? 2 : 1;
+    // units of x per thread and batch; a window's fit one batch (kw <= 4)
+    static constexpr int kXUnits = kResident ? 2 : kSplit ? (MI * NS + 1) / 2 : MI * NS;
+    static constexpr int kFixedBytes = kScaleBytes + kCodeBytes + kPuts * kPutBytes;
+
+    struct Fetched {
+        u32x4_t c[RT][U];
+        float s[RT][kSBatch];
+        uint32_t z[RT][kSBatch];
+    };
+
+    // tab: the level table (kLevels); lds: kFixedBytes + w4_x_bytes(), 16-byte aligned.
+    // out(item, put) stores an item's outputs from the partial sums.
+    template <class V, class Out>
+    static __device__ __forceinline__ void run(const V& w, const Rows<RT>& p, int64_t item0, int64_t item1,
+                                               const uint8_t* tab, uint8_t* lds, Out&& out) {
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int n = lane & 15, h = lane >> 4;
+        const int kw = 1 << p.kwl, wk = wave & (kw - 1), wr = wave >> p.kwl;
+        floatx2_t* slds = reinterpret_cast<floatx2_t*>(lds) + wave * (RT * 16 * kSPitch);
+        uint8_t* clds = lds + kScaleBytes + wave * (16 * 128 * NS);
+        float* put = reinterpret_cast<float*>(lds + kScaleBytes + kCodeBytes);
+        uint8_t* xlds = lds + kFixedBytes;
+        const int nchunk = (int)((p.K + kChunk - 1) / kChunk);
+        const int wchunks = kw * U;
+        const int win_pitch = wchunks * (kChunk * 2) + 16;
+        const int xpitch = kResident ? (nchunk + U - 1) / U * (U * kChunk * 2) + 16 : win_pitch;
+        const int xrows = kSplit ? 2 * p.M : p.M;
+        const Magic magic(F == kInt4F16);
+        float mean = 0.0f, zbias = 0.0f;
+        if constexpr (F == kLevels) mean = w.nested ? *w.dq_mean : 0.0f;
+        else zbias = kCodeBias<F> + (w.zeros ? 0.0f : 8.0f);
+        const __amdgpu_buffer_rsrc_t xbuf = buffer(p.x, (int64_t)p.x_rows * p.x_pitch * (kSplit ? 4 : 2));
+
+        // Staging of activations, thread by thread, rows as if they had 2^ush units of 8 values.  Rows that
+        // cannot be read 16 bytes at a time are read element by element when they are stored.
+        const int units = (kResident ? nchunk : wchunks) * (kChunk / 8);
+        const int ush = 32 - __builtin_clz(units - 1);
+        const int total = p.M << ush;
+        u32x4_t xr[kXUnits][kSplit ? 2 : 1];
+        auto x_load = [&](int base, int k0) {
+#pragma unroll
+            for (int b = 0; b < kXUnits; ++b) {
+                const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
+                const bool in = i < total && u < units && k < p.K && p.x_aligned;
+                const int row = in && p.xrow ? p.xrow[m] : m;
+                const int32_t off = in ? (row * (int32_t)p.x_pitch + k) * (kSplit ? 4 : 2) : kOutside;
+                xr[b][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 0, 0);
+                if constexpr (kSplit) xr[b][1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 16, 0);
+            }
+        };
+        // Every thread stores (what lies outside, to the 16 bytes behind row 0, which nobody reads): under a
+        // condition the compiler would move the loads down to it, behind those of the codes.
+        auto x_store = [&](uint8_t* dst, int base, int k0) {
+#pragma unroll
+            for (int b = 0; b < kXUnits; ++b) {
+                const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1);
+                const bool in = i < total && u < units;
+                if constexpr (kSplit) {
+                    u32x4_t hi, lo;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w0 = xr[b][j >> 1][2 * (j & 1)], w1 = xr[b][j >> 1][2 * (j & 1) + 1];
+                        const float a = as_float(w0), c = as_float(w1);
+                        const uint32_t pk = pack_bf16x2(a, c);
+                        hi[j] = pk;
+                        lo[j] = pack_bf16x2(a - bf16_lo(pk), c - bf16_hi(pk));
+                    }
+                    if constexpr (F != kLevels) {
+                        hi = int4_order(hi);
+                        lo = int4_order(lo);
+                    }
+                    const int at = in ? 2 * m * xpitch + 16 * u : xpitch - 16;
+                    *reinterpret_cast<u32x4_t*>(dst + at) = hi;
+                    *reinterpret_cast<u32x4_t*>(dst + (in ? at + xpitch : at)) = lo;
+                } else {
+                    const int at = in ? m * xpitch + 16 * u : xpitch - 16;
+                    *reinterpret_cast<u32x4_t*>(dst + at) = F == kLevels ? xr[b][0] : int4_order(xr[b][0]);
+                }
+            }
+            if constexpr (!kSplit) {
+                if (p.x_aligned) return;
+#pragma unroll 1
+                for (int b = 0; b < kXUnits; ++b) {
+                    const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
+                    if (i >= total || u >= units) continue;
+                    const uint16_t* src = static_cast<const uint16_t*>(p.x) + (p.xrow ? p.xrow[m] : m) * p.x_pitch + k;
+                    u32x4_t v;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo = k + 2 * j < p.K ? src[2 * j] : 0u;
+                        const uint32_t hi = k + 2 * j + 1 < p.K ? src[2 * j + 1] : 0u;
+                        v[j] = lo | (hi << 16);
+                    }
+                    *reinterpret_cast<u32x4_t*>(dst + m * xpitch + 16 * u) = F == kLevels ? v : int4_order(v);
+                }
+            }
+        };
+
+        // codes and scales of the wave's lines in the window that starts at chunk c0
+        const int32_t voff = (int32_t)((lane >> 3) * w.stride) + 16 * (lane & 7);
+        const int32_t stride8 = (int32_t)(8 * w.stride);
+        auto fetch = [&](Fetched& f, int64_t item, int c0, bool any) {
+            const int c = c0 + wk * U;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const int64_t j = item * p.step + wr * p.group_step + p.off[r], left = any ? p.count - j : 0;
+                const int valid = left > 16 ? 16 : left > 0 ? (int)left : 0;
+                const int64_t first = p.base[r] + j;
+                if constexpr (F == kLevels) {
+#pragma unroll
+                    for (int b = 0; b < kSBatch; ++b) {
+                        const int64_t k = (int64_t)c * kChunk + (h + 4 * b) * 64;
+                        f.s[r][b] = 0.0f;
+                        f.z[r][b] = 0;
+                        if (n < valid && k < p.K) {
+                            const int64_t blk = ((first + n) * p.K + k) >> w.bshift;
+                            if (w.nested) {
+                                f.z[r][b] = (uint8_t)w.q8[blk];
+                                f.s[r][b] = w.dq_scale[blk / QK_DQ_BLOCK];
+                            } else {
+                                f.s[r][b] = w.absmax[blk];
+                            }
+                        }
+                    }
+                } else {
+                    const __amdgpu_buffer_rsrc_t sbuf = buffer(w.scales + first * w.G, (int64_t)valid * w.G * 2);
+                    const __amdgpu_buffer_rsrc_t zbuf =
+                        buffer(w.zeros ? w.zeros + first * w.G : nullptr, w.zeros ? (int64_t)valid * w.G : 0);
+#pragma unroll
+                    for (int b = 0; b < kSBatch; ++b) {
+                        const int e = h + 4 * b;
+                        const int g = n * w.G + (NG > 1 ? c * NG + e : ((c + e) * kChunk) >> w.gshift);
+                        f.s[r][b] = as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sbuf, 2 * g, 0, 0));
+                        f.z[r][b] = (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zbuf, g, 0, 0);
+                    }
+                }
+                const __amdgpu_buffer_rsrc_t cbuf = buffer(w.codes + first * w.stride, (int64_t)valid * w.stride);
+#pragma unroll
+                for (int q = 0; q < U; ++q) {                    // rows 8 (q % 2) + lane / 8 of line q / 2
+                    const int cq = c + (q & ~1);
+                    f.c[r][q] = __builtin_amdgcn_raw_buffer_load_b128(
+                        cbuf, voff, cq < nchunk ? (q & 1) * stride8 + cq * (kChunk / 2) : kOutside, kNontemporal);
+                }
+            }
+        };
+
+        const int am = act_of_row<MI>(n);
+        const int arow = (am < xrows ? am : xrows - 1) * xpitch;
+        float y[RT][MI];
+        // one window's products
+        auto compute = [&](Fetched& f, int c0, const uint8_t* xwin) {
+            const int cw = c0 + wk * U;
+            if (cw >= nchunk) return;
+            // from lines to fragments: 16-byte unit u of row r sits in unit u ^ r of its row
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+#pragma unroll
+                for (int q = 0; q < U; ++q) {
+                    const int row = 8 * (q & 1) + (lane >> 3), unit = 8 * (q >> 1) + (lane & 7);
+                    *reinterpret_cast<u32x4_t*>(clds + row * (128 * NS) + 16 * (unit ^ (row & (8 * NS - 1)))) = f.c[r][q];
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    f.c[r][u] = *reinterpret_cast<const u32x4_t*>(clds + n * (128 * NS) +
+                                                                  16 * ((4 * u + h) ^ (n & (8 * NS - 1))));
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int b = 0; b < kSBatch; ++b) {
+                    floatx2_t v;
+                    if constexpr (F == kLevels) {
+                        v[0] = w.nested ? __fadd_rn(__fmul_rn((float)(int8_t)f.z[r][b], f.s[r][b]), mean) : f.s[r][b];
+                        v[1] = 0.0f;
+                    } else {
+                        const uint16_t bits = (uint16_t)as_uint(f.s[r][b]);
+                        v[0] = w.scale_f16 ? f16_bits_to_float(bits) : bf16_bits_to_float(bits);
+                        v[1] = v[0] * ((float)f.z[r][b] + zbias);
+                    }
+                    if (h + 4 * b < kEntries) slds[(16 * r + n) * kSPitch + h + 4 * b] = v;
+                }
+            const uint8_t* ax = xwin + arow + 2 * (kResident ? cw * kChunk : wk * (U * kChunk));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (cw + u >= nchunk) break;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) order_chunk<NG>(f.c[r][u]);
+#pragma unroll
+                for (int q = 0; q < NG; ++q) {
+                    floatx4_t acc[RT], xs = {0, 0, 0, 0};
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) acc[r] = (floatx4_t){0, 0, 0, 0};
+#pragma unroll
+                    for (int j = q * kMfmas; j < (q + 1) * kMfmas; ++j) {
+                        const u32x4_t a = *reinterpret_cast<const u32x4_t*>(ax + 2 * (u * kChunk + chunk_k<NG>(j, h)));
+                        if constexpr (F == kLevels) {
+#pragma unroll
+                            for (int r = 0; r < RT; ++r)
+                                acc[r] = mfma<F>(a, decode8_table(tab, f.c[r][u][j], 4 * lane), acc[r]);
+                        } else {
+                            xs = mfma<F>(a, ones<F>(), xs);
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) acc[r] = mfma<F>(a, decode8<F>(f.c[r][u][j], magic), acc[r]);
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const floatx2_t s = slds[(16 * r + n) * kSPitch + u * NG + q];
+#pragma unroll
+                        for (int i = 0; i < MI; ++i) {
+                            if constexpr (F != kLevels) y[r][i] = fmaf(-s[1], xs[i], y[r][i]);
+                            y[r][i] = fmaf(s[0], acc[r][i], y[r][i]);
+                        }
+                    }
+                }
+            }
+        };
+
+        Fetched f[2];
+        x_load(0, 0);
+        fetch(f[0], item0, 0, true);
+        if constexpr (kResident) {
+            x_store(xlds, 0, 0);
+            for (int base = kXUnits * kThreads; base < total; base += kXUnits * kThreads) {
+                x_load(base, 0);
+                x_store(xlds, base, 0);
+            }
+            __syncthreads();
+        }
+        int64_t item = item0;
+        int c0 = 0, xsel = 0, putsel = 0;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) y[r][i] = 0.0f;
+        // One window.  The loop below always makes two steps; a step past the last item reads nothing
+        // (its ranges are empty) and computes nothing.  Its loads are issued without a condition: a branch
+        // around them would make the wait for this window's codes cover the next one's too.
+        auto step = [&](Fetched& cur, Fetched& nxt) {
+            uint8_t* xwin = xlds + (kResident ? 0 : xsel * (xrows * win_pitch));
+            if constexpr (!kResident) {
+                if (p.x_bufs == 1) __syncthreads();              // the last window's reads
+                x_store(xwin, 0, c0 * kChunk);
+            }
+            int64_t ni = item;
+            int nc = c0 + wchunks;
+            const bool last = nc >= nchunk;                      // last window of the item
+            if (last) {
+                nc = 0;
+                ++ni;
+            }
+            if constexpr (!kResident) x_load(0, nc * kChunk);
+            fetch(nxt, ni, nc, ni < item1);
+            if constexpr (!kResident) {
+                __syncthreads();
+                xsel ^= p.x_bufs - 1;
+            }
+            if (item < item1) {
+                compute(cur, c0, xwin);
+                if (last) {
+                    float* pp = put + putsel * (kPutBytes / 4);
+                    if constexpr (kPuts == 2) putsel ^= 1;
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int i = 0; i < MI; ++i) {
+                            pp[(wave * RT + r) * (64 * MI) + 64 * i + lane] = y[r][i];
+                            y[r][i] = 0.0f;
+                        }
+                    __syncthreads();
+                    out(item, pp);
+                    if constexpr (kPuts == 1) __syncthreads();
+                }
+            }
+            item = ni;
+            c0 = nc;
+        };
+        do {
+            step(f[0], f[1]);
+            step(f[1], f[0]);
+        } while (item < item1);
+        __syncthreads();
+    }
+
+    // From the partial sums: output o (o < 64 MI) of tile r of row group q, the waves added in their
+    // order.  Its row in the tile is o % 16, its activation row act_of(o).
+    static __device__ __forceinline__ float sum(const float* put, int kwl, int q, int r, int o) {
+        float v = 0.0f;
+        const float* first = put + ((q << kwl) * RT + r) * (64 * MI) + o;
+        for (int w = 0; w < (1 << kwl); ++w) v += first[w * (RT * 64 * MI)];
+        return v;
+    }
+    static __device__ __forceinline__ int act_of(int o) { return MI * ((o & 63) >> 4) + (o >> 6); }
+    // Where that output of activation row m sits.
+    static __device__ __forceinline__ int place_of(int row, int m) {
+        return 64 * (m & (MI - 1)) + 16 * (m / MI) + row;
+    }
+};
 
 }  // namespace w4
 }  // namespace qk

@@ -653,9 +653,10 @@ qk_status qk_gemv_int4_grouped(const qk_gemv_int4_task* tasks, int32_t ntasks, i
 
 /*
  * qk_moe_workspace_size — host.  Bytes of device workspace that qk_moe_nf4 and
- * qk_moe_int4 need for T tokens, top_k experts per token and experts of I inner features.
+ * qk_moe_int4 need for T tokens of H features, top_k experts per token and experts of I inner features
+ * (T and top_k 1..16, H and I 1..2^20).
  */
-qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t I, size_t* bytes);
+qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t H, int64_t I, size_t* bytes);
 
 /*
  * qk_moe_int4, qk_moe_nf4 — device.  A whole mixture-of-experts layer with SwiGLU experts
@@ -678,10 +679,10 @@ qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t I, size_t* byt
  *   gate_up: host pointer to the descriptor of the stacked [E * 2 * I, H] weights: expert e's
  *     gate in rows [2 e I, 2 e I + I), its up projection in the next I rows.
  *   down: descriptor of the stacked [E * H, I] weights: expert e in rows [e H, e H + H).
- *   H and I follow from the descriptors.  qk_moe_nf4 needs H and I to be multiples of 64
+ *   H and I follow from the descriptors (each at most 2^20).  qk_moe_nf4 needs H and I to be multiples of 64
  *     (else QK_ERR_UNSUPPORTED) and 16-byte aligned codes.
  *   y: device, [T, H] of dtype, written.  May be x itself.
- *   workspace: device, >= qk_moe_workspace_size(T, top_k, I) bytes, 16-byte aligned;
+ *   workspace: device, >= qk_moe_workspace_size(T, top_k, H, I) bytes, 16-byte aligned;
  *     contents on entry ignored; no overlap with the other buffers.  Calls that may run at
  *     the same time need workspaces of their own.
  *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_UNSUPPORTED, QK_ERR_WORKSPACE,

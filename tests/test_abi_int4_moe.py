@@ -116,12 +116,15 @@ def _moe_nf4(L, up, down, T=2, E=4, top_k=2, x=X, y=Y, ws=WS, bytes_=1 << 19):
 
 
 def test_workspace_size(L):
-    assert qk.qk_moe_workspace_size(16, 8, 11008) >= 16 * 8 * 11008 * 4
-    assert qk.qk_moe_workspace_size(1, 1, 1) <= qk.qk_moe_workspace_size(1, 1, 129) <= qk.qk_moe_workspace_size(2, 1, 129)
+    assert qk.qk_moe_workspace_size(16, 8, 4096, 11008) >= 16 * 8 * (4096 + 11008) * 4
+    w = qk.qk_moe_workspace_size
+    assert w(1, 1, 1, 1) <= w(1, 1, 1, 129) <= w(2, 1, 1, 129) <= w(2, 1, 200, 129)
     out = ctypes.c_size_t()
-    for a in ((0, 1, 1), (17, 1, 1), (1, 0, 1), (1, 17, 1), (1, 1, 0), (1, 1, (1 << 24) + 1)):
+    big = (1 << 20) + 1
+    for a in ((0, 1, 1, 1), (17, 1, 1, 1), (1, 0, 1, 1), (1, 17, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0), (1, 1, 1, big),
+              (1, 1, big, 1)):
         assert L.qk_moe_workspace_size(*a, ctypes.byref(out)) == qk.QK_ERR_INVALID_ARG
-    assert L.qk_moe_workspace_size(1, 1, 1, None) == qk.QK_ERR_INVALID_ARG
+    assert L.qk_moe_workspace_size(1, 1, 1, 1, None) == qk.QK_ERR_INVALID_ARG
 
 
 def test_moe_refusals(L):
@@ -131,7 +134,7 @@ def test_moe_refusals(L):
                 dict(y=Y + 1), dict(logits=LG + 2), dict(ws=WS + 8), dict(ws=X - 64), dict(y=WS + 64),
                 dict(logits=WS + 4096), dict(y=X + 256)):
         assert _moe(L, up, down, **bad) == qk.QK_ERR_INVALID_ARG, bad
-    need = qk.qk_moe_workspace_size(2, 2, 64)
+    need = qk.qk_moe_workspace_size(2, 2, 128, 64)
     assert _moe(L, up, down, bytes_=need - 1) == qk.QK_ERR_WORKSPACE
     assert _moe(L, up, down, ws=None) == qk.QK_ERR_WORKSPACE
     assert _moe(L, None, down) == qk.QK_ERR_INVALID_ARG and _moe(L, up, None) == qk.QK_ERR_INVALID_ARG

@@ -182,7 +182,7 @@ def test_all_tokens_empty_and_poisoned_workspace():
     x = torch.randn((16, 160), generator=gen, device="cuda").to(torch.bfloat16)
     lg = torch.randn((16, 6), generator=gen, device="cuda")
     want = qk.qk_moe_int4(x, lg, 2, up.state, down.state)
-    n = qk.qk_moe_workspace_size(16, 2, 96)
+    n = qk.qk_moe_workspace_size(16, 2, 160, 96)
     for fill in (0xFF, 0x7F, 0x00):
         ws = torch.full((n + 64,), fill, dtype=torch.uint8, device="cuda")
         assert torch.equal(qk.qk_moe_int4(x, lg, 2, up.state, down.state, workspace=ws[:n]), want)
