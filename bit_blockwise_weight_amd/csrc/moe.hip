@@ -165,33 +165,41 @@ struct ExpertArgs {
     typename View<F>::type w;
     const Routes* routes;
     float* out;              // up: h; down: the parts [T * top_k, H]
-    int64_t H;
-    int64_t I;
-    int64_t Ipad;            // I rounded up to 8 values
+    int32_t H;
+    int32_t I;
+    int32_t Ipad;            // I rounded up to 8 values
+    uint32_t grid;           // workgroups
     int32_t x_rows;
     int32_t x_aligned;
     int32_t kwl;
     int32_t x_bufs;
 };
 
-// Activations of a whole row stay in LDS up to this size.
-template <int F, int MI>
-constexpr size_t kMaxRows = F != kLevels ? 72 * 1024 : MI == 1 ? 36 * 1024 : 28 * 1024;
+// Workgroups per CU: the level table takes 64 KB of its LDS.
+template <int F>
+constexpr int kPerCu = F == kLevels ? 1 : 2;
+// The activations of a whole row stay in LDS where all of them fit.
+template <int F, int NG, int RT, int MI>
+bool fits(int rows, int64_t K) {
+    return (F == kLevels ? kTabBytes : 0) + w4_fixed_bytes(NG, RT, MI) + w4_x_bytes(8, rows, K, true, 1) <=
+           kLdsBytes / kPerCu<F>;
+}
 
 template <int F, int NG, int MI, bool kResident>
-__global__ __launch_bounds__(kThreads, 2) void moe_up_kernel(ExpertArgs<F> p) {
+__global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertArgs<F> p) {
     extern __shared__ __align__(16) uint8_t lds[];
-    typedef RowTiles<F, NG, 2, kResident ? 2 : 1, MI, kResident, false> Tiles;
+    typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
     uint8_t* work = lds + (F == kLevels ? kTabBytes : 0);
     if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads);
     // an item: per row group 16 rows of gate and the same of up of one listed expert; equal shares of the items
     const int step = 128 >> p.kwl;
-    const int64_t tiles = (p.Ipad + step - 1) / step, all = tiles * p.routes->nactive;
-    int64_t lo = all * blockIdx.x / gridDim.x;
-    const int64_t hi = all * (blockIdx.x + 1) / gridDim.x;
+    const uint32_t tiles = (uint32_t)(p.Ipad + step - 1) / step, all = tiles * p.routes->nactive;
+    const uint32_t share = all / p.grid, more = all % p.grid, b = blockIdx.x;
+    uint32_t lo = b * share + (b < more ? b : more);
+    const uint32_t hi = lo + share + (b < more);
     while (lo < hi) {
         const int a = (int)(lo / tiles);
-        const int64_t i0 = lo - a * tiles, i1 = hi - a * tiles < tiles ? hi - a * tiles : tiles;
+        const int i0 = (int)(lo - a * tiles), i1 = (int)(hi - a * tiles < tiles ? hi - a * tiles : tiles);
         lo += i1 - i0;
         const int count = p.routes->count[a];
         const int64_t e = p.routes->expert[a];
@@ -213,14 +221,14 @@ __global__ __launch_bounds__(kThreads, 2) void moe_up_kernel(ExpertArgs<F> p) {
             const int M = count - m0 < 4 * MI ? count - m0 : 4 * MI;
             r.xrow = p.routes->tok[a] + m0;
             r.M = M;
-            Tiles::run(p.w, r, i0, i1, lds, work, [&](int64_t item, const float* put) {
+            Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, const float* put) {
                 for (int o = threadIdx.x; o < (64 * MI * 8) >> p.kwl; o += kThreads) {
                     const int q = o / (64 * MI), s = o % (64 * MI), m = Tiles::act_of(s);
-                    const int64_t i = item * step + 16 * q + (s & 15);
+                    const int i = item * step + 16 * q + (s & 15);
                     if (m < M && i < p.Ipad) {
                         const float gate = Tiles::sum(put, p.kwl, q, 0, s), up = Tiles::sum(put, p.kwl, q, 1, s);
                         const float v = gate / (1.0f + expf(-gate)) * up;
-                        p.out[p.routes->pair[a][m0 + m] * p.Ipad + i] = i < p.I ? v : 0.0f;
+                        p.out[(int64_t)p.routes->pair[a][m0 + m] * p.Ipad + i] = i < p.I ? v : 0.0f;
                     }
                 }
             });
@@ -229,24 +237,25 @@ __global__ __launch_bounds__(kThreads, 2) void moe_up_kernel(ExpertArgs<F> p) {
 }
 
 template <int F, int NG, int RT, int MI, bool kResident>
-__global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(ExpertArgs<F> p) {
+__global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(ExpertArgs<F> p) {
     extern __shared__ __align__(16) uint8_t lds[];
-    typedef RowTiles<F, NG, RT, kResident ? 2 : 1, MI, kResident, true> Tiles;
+    typedef RowTiles<F, NG, RT, MI, kResident, true> Tiles;
     uint8_t* work = lds + (F == kLevels ? kTabBytes : 0);
     if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads);
     const int step = (16 * RT * 8) >> p.kwl;
-    const int64_t tiles = (p.H + step - 1) / step, all = tiles * p.routes->nactive;
-    int64_t lo = all * blockIdx.x / gridDim.x;
-    const int64_t hi = all * (blockIdx.x + 1) / gridDim.x;
+    const uint32_t tiles = (uint32_t)(p.H + step - 1) / step, all = tiles * p.routes->nactive;
+    const uint32_t share = all / p.grid, more = all % p.grid, b = blockIdx.x;
+    uint32_t lo = b * share + (b < more ? b : more);
+    const uint32_t hi = lo + share + (b < more);
     while (lo < hi) {
         const int a = (int)(lo / tiles);
-        const int64_t i0 = lo - a * tiles, i1 = hi - a * tiles < tiles ? hi - a * tiles : tiles;
+        const int i0 = (int)(lo - a * tiles), i1 = (int)(hi - a * tiles < tiles ? hi - a * tiles : tiles);
         lo += i1 - i0;
         const int count = p.routes->count[a];
         Rows<RT> r;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            r.base[t] = p.routes->expert[a] * p.H;
+            r.base[t] = (int64_t)p.routes->expert[a] * p.H;
             r.off[t] = 16 * t;
         }
         r.step = step;
@@ -264,13 +273,13 @@ __global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(ExpertArgs<F> p) 
             const int M = count - m0 < 2 * MI ? count - m0 : 2 * MI;
             r.xrow = p.routes->pair[a] + m0;
             r.M = M;
-            Tiles::run(p.w, r, i0, i1, lds, work, [&](int64_t item, const float* put) {
+            Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, const float* put) {
                 for (int o = threadIdx.x; o < M * step; o += kThreads) {
                     const int m = o / step, row = o % step, q = row / (16 * RT), t = row / 16 % RT;
-                    const int64_t n = item * step + row;
+                    const int n = item * step + row;
                     const float v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m)) +
                                     Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m + 1));
-                    if (n < p.H) p.out[p.routes->pair[a][m0 + m] * p.H + n] = v * p.routes->w[a][m0 + m];
+                    if (n < p.H) p.out[(int64_t)p.routes->pair[a][m0 + m] * p.H + n] = v * p.routes->w[a][m0 + m];
                 }
             });
         }
@@ -298,23 +307,22 @@ hipError_t allow_lds(K kernel, size_t lds) {
 // rows: activation rows that a pass stages at most
 template <int F, int NG, int MI, bool kResident>
 hipError_t launch_up_one(ExpertArgs<F> p, int rows, int32_t listed, hipStream_t s) {
-    constexpr int NS = kResident ? 2 : 1;
-    typedef RowTiles<F, NG, 2, NS, MI, kResident, false> Tiles;
-    p.kwl = kResident ? w4_kwl(NS, p.H) : 2;
+    typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
+    p.kwl = kResident ? w4_kwl(p.H) : 2;
     p.x_bufs = 2;
-    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, NS, rows, p.H, kResident, 2);
+    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, rows, p.H, kResident, 2);
     const hipError_t e = allow_lds(&moe_up_kernel<F, NG, MI, kResident>, lds);
     if (e != hipSuccess) return e;
-    const int64_t items = (p.Ipad + (128 >> p.kwl) - 1) / (128 >> p.kwl) * listed;
-    moe_up_kernel<F, NG, MI, kResident>
-        <<<dim3((unsigned)std::min<int64_t>(items, device_cu_count())), dim3(kThreads), lds, s>>>(p);
+    const int64_t items = (int64_t)(p.Ipad + (128 >> p.kwl) - 1) / (128 >> p.kwl) * listed;
+    p.grid = (uint32_t)std::min<int64_t>(items, kPerCu<F> * device_cu_count());
+    moe_up_kernel<F, NG, MI, kResident><<<dim3(p.grid), dim3(kThreads), lds, s>>>(p);
     return hipGetLastError();
 }
 
 template <int F, int NG, int MI>
 hipError_t launch_up_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hipStream_t s) {
     const int rows = std::min(T, 4 * MI);
-    if (w4_x_bytes(8, 2, rows, p.H, true, 1) <= kMaxRows<F, MI>) return launch_up_one<F, NG, MI, true>(p, rows, listed, s);
+    if (fits<F, NG, 2, MI>(rows, p.H)) return launch_up_one<F, NG, MI, true>(p, rows, listed, s);
     return launch_up_one<F, NG, MI, false>(p, rows, listed, s);
 }
 
@@ -329,23 +337,22 @@ hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, h
 
 template <int F, int NG, int RT, int MI, bool kResident>
 hipError_t launch_down_one(ExpertArgs<F> p, int rows, int32_t listed, hipStream_t s) {
-    constexpr int NS = kResident ? 2 : 1;
-    typedef RowTiles<F, NG, RT, NS, MI, kResident, true> Tiles;
-    p.kwl = kResident ? w4_kwl(NS, p.I) : 2;
+    typedef RowTiles<F, NG, RT, MI, kResident, true> Tiles;
+    p.kwl = kResident ? w4_kwl(p.I) : 2;
     p.x_bufs = 2;
-    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, NS, rows, p.I, kResident, 2);
+    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, rows, p.I, kResident, 2);
     const hipError_t e = allow_lds(&moe_down_kernel<F, NG, RT, MI, kResident>, lds);
     if (e != hipSuccess) return e;
     const int64_t step = (16 * RT * 8) >> p.kwl, items = (p.H + step - 1) / step * listed;
-    moe_down_kernel<F, NG, RT, MI, kResident>
-        <<<dim3((unsigned)std::min<int64_t>(items, device_cu_count())), dim3(kThreads), lds, s>>>(p);
+    p.grid = (uint32_t)std::min<int64_t>(items, kPerCu<F> * device_cu_count());
+    moe_down_kernel<F, NG, RT, MI, kResident><<<dim3(p.grid), dim3(kThreads), lds, s>>>(p);
     return hipGetLastError();
 }
 
 template <int F, int NG, int MI>
 hipError_t launch_down_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hipStream_t s) {
     const int rows = std::min(2 * T, 4 * MI);
-    if (w4_x_bytes(8, 2, rows, p.I, true, 1) > kMaxRows<F, MI>) return launch_down_one<F, NG, 2, MI, false>(p, rows, listed, s);
+    if (!fits<F, NG, 2, MI>(rows, p.I)) return launch_down_one<F, NG, 2, MI, false>(p, rows, listed, s);
     return launch_down_one<F, NG, 2, MI, true>(p, rows, listed, s);
 }
 
@@ -394,9 +401,10 @@ ExpertArgs<F> expert_args(const MoeItem& m, const Buffers& b, bool up) {
     p.x = up ? m.x : b.h;
     p.routes = b.routes;
     p.out = up ? b.h : b.parts;
-    p.H = m.H;
-    p.I = m.I;
-    p.Ipad = (m.I + 7) / 8 * 8;
+    p.H = (int32_t)m.H;
+    p.I = (int32_t)m.I;
+    p.Ipad = (int32_t)((m.I + 7) / 8 * 8);
+    p.grid = 0;
     p.x_rows = up ? m.T : m.T * m.top_k;
     p.x_aligned = !up || (m.H % 8 == 0 && reinterpret_cast<uintptr_t>(m.x) % 16 == 0);
     p.kwl = p.x_bufs = 0;

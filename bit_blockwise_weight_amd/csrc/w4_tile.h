@@ -209,11 +209,10 @@ __device__ __forceinline__ u32x4_t decode8_table(const uint8_t* tab, uint32_t w,
 // other by one workgroup of W waves: run() takes a run of items that share their activations.
 //
 // kw of the waves split k, W / kw groups of them take different rows.  A row is cut into windows
-// of kw * 256 NS k; a wave takes NS lines (of 128 bytes, 256 k) of each row per window, and the
+// of kw * 256 k; a wave takes one line (128 bytes, 256 k) of each row per window, and the
 // partial outputs of the kw waves meet in LDS once per item and are added in their order (no
 // atomics, the same bits every time).  While a wave works on one window the codes and scales of
-// the next one (of the same item or the next) are already on their way into registers: one
-// workgroup per CU keeps W * NS * RT * 2 KB of codes in flight throughout.
+// the next one (of the same item or the next) are already on their way into registers.
 //
 // Activations (in the order of decoded int4, zero past K) live in LDS, 16 bytes more than a row
 // apart, so that a fragment read of 16 rows falls in different banks: all of K for the whole run
@@ -241,11 +240,11 @@ struct Rows {
     int64_t base[RT];
     int32_t off[RT];
     int32_t step, group_step;
-    int64_t count;
+    int32_t count;
     const void* x;           // 16-bit values, or fp32 (kSplit)
     const uint8_t* xrow;     // activation m is row xrow[m] of x; NULL: row m
-    int64_t K;
-    int64_t x_pitch;         // values from a row of x to the next
+    int32_t K;
+    int32_t x_pitch;         // values from a row of x to the next
     int32_t x_rows;          // rows of x
     int32_t x_aligned;       // 16-byte loads of x are possible
     int32_t M;               // activations
@@ -260,36 +259,45 @@ __device__ __forceinline__ constexpr int act_of_row(int row) { return MI * (row 
 
 constexpr int kLineK = 256;               // k of a 128-byte line of codes
 
-// bytes of LDS that the activations take (rows: twice their number with kSplit)
-inline size_t w4_x_bytes(int kw, int NS, int rows, int64_t K, bool resident, int bufs) {
-    const size_t k = (size_t)((K + kLineK * NS - 1) / (kLineK * NS)) * (kLineK * NS);
-    return resident ? (size_t)rows * (k * 2 + 16) : (size_t)bufs * rows * ((size_t)kw * NS * kLineK * 2 + 16);
+// bytes of LDS beside the activations: scales, codes, partial sums (two buffers where they are small)
+constexpr int w4_put_bytes(int RT, int MI) { return 8 * RT * 64 * MI * 4; }
+constexpr int w4_fixed_bytes(int NG, int RT, int MI) {
+    return 8 * RT * 16 * ((2 * NG) | 1) * 8 + 8 * RT * 16 * 128 +
+           (w4_put_bytes(RT, MI) <= 8192 ? 2 : 1) * w4_put_bytes(RT, MI);
 }
-// log2 of the waves (of 8) that split a row of K: as many as it has windows' worth of lines
-inline int w4_kwl(int NS, int64_t K) {
-    const int64_t n = (K + kLineK * NS - 1) / (kLineK * NS);
+constexpr size_t kLdsBytes = 160 * 1024;  // of a CU
+
+// bytes of LDS that the activations take (rows: twice their number with kSplit)
+inline size_t w4_x_bytes(int kw, int rows, int64_t K, bool resident, int bufs) {
+    const size_t k = (size_t)((K + kLineK - 1) / kLineK) * kLineK;
+    return resident ? (size_t)rows * (k * 2 + 16) : (size_t)bufs * rows * ((size_t)kw * kLineK * 2 + 16);
+}
+// log2 of the waves (of 8) that split a row of K: as many as it has lines
+inline int w4_kwl(int64_t K) {
+    const int64_t n = (K + kLineK - 1) / kLineK;
     return n > 4 ? 3 : n > 2 ? 2 : n > 1 ? 1 : 0;
 }
 
-template <int F, int NG, int RT, int NS, int MI, bool kResident, bool kSplit>
+template <int F, int NG, int RT, int MI, bool kResident, bool kSplit>
 struct RowTiles {
     static constexpr int W = 8;
     static constexpr int kThreads = W * 64;
-    static constexpr int U = 2 * NS;                            // chunks of a wave in a window
+    static constexpr int U = 2;                                 // chunks of a wave in a window
     static constexpr int kMfmas = 4 / NG;                       // MFMAs per scale group
     static constexpr int kEntries = U * NG;                     // scale groups of a wave's chunks in a window
     static constexpr int kSPitch = kEntries | 1;
     static constexpr int kSBatch = (kEntries + 3) / 4;          // of them per lane
     static constexpr int kScaleBytes = W * RT * 16 * kSPitch * 8;
-    static constexpr int kCodeBytes = W * 16 * 128 * NS;        // a tile's codes changing layout
-    static constexpr int kPutBytes = W * RT * 64 * MI * 4;
+    static constexpr int kCodeBytes = W * RT * 16 * 128;        // a window's codes changing layout
+    static constexpr int kPutBytes = w4_put_bytes(RT, MI);
     static constexpr int kPuts = kPutBytes <= 8192 ? 2 : 1;
     // units of x per thread and batch; a window's fit one batch (kw <= 4)
-    static constexpr int kXUnits = kResident ? 2 : kSplit ? (MI * NS + 1) / 2 : MI * NS;
-    static constexpr int kFixedBytes = kScaleBytes + kCodeBytes + kPuts * kPutBytes;
+    static constexpr int kXUnits = kResident ? 2 : kSplit ? (MI + 1) / 2 : MI;
+    static constexpr int kFixedBytes = w4_fixed_bytes(NG, RT, MI);
+    static_assert(kFixedBytes == kScaleBytes + kCodeBytes + kPuts * kPutBytes);
 
     struct Fetched {
-        u32x4_t c[RT][U];
+        u32x4_t c[RT][2];
         float s[RT][kSBatch];
         uint32_t z[RT][kSBatch];
     };
@@ -297,16 +305,16 @@ struct RowTiles {
     // tab: the level table (kLevels); lds: kFixedBytes + w4_x_bytes(), 16-byte aligned.
     // out(item, put) stores an item's outputs from the partial sums.
     template <class V, class Out>
-    static __device__ __forceinline__ void run(const V& w, const Rows<RT>& p, int64_t item0, int64_t item1,
+    static __device__ __forceinline__ void run(const V& w, const Rows<RT>& p, int item0, int item1,
                                                const uint8_t* tab, uint8_t* lds, Out&& out) {
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int n = lane & 15, h = lane >> 4;
         const int kw = 1 << p.kwl, wk = wave & (kw - 1), wr = wave >> p.kwl;
         floatx2_t* slds = reinterpret_cast<floatx2_t*>(lds) + wave * (RT * 16 * kSPitch);
-        uint8_t* clds = lds + kScaleBytes + wave * (16 * 128 * NS);
+        uint8_t* clds = lds + kScaleBytes + wave * (RT * 16 * 128);
         float* put = reinterpret_cast<float*>(lds + kScaleBytes + kCodeBytes);
         uint8_t* xlds = lds + kFixedBytes;
-        const int nchunk = (int)((p.K + kChunk - 1) / kChunk);
+        const int nchunk = (p.K + kChunk - 1) / kChunk;
         const int wchunks = kw * U;
         const int win_pitch = wchunks * (kChunk * 2) + 16;
         const int xpitch = kResident ? (nchunk + U - 1) / U * (U * kChunk * 2) + 16 : win_pitch;
@@ -319,7 +327,7 @@ struct RowTiles {
 
         // Staging of activations, thread by thread, rows as if they had 2^ush units of 8 values.  Rows that
         // cannot be read 16 bytes at a time are read element by element when they are stored.
-        const int units = (kResident ? nchunk : wchunks) * (kChunk / 8);
+        const int units = (kResident ? (nchunk + U - 1) / U * U : wchunks) * (kChunk / 8);
         const int ush = 32 - __builtin_clz(units - 1);
         const int total = p.M << ush;
         u32x4_t xr[kXUnits][kSplit ? 2 : 1];
@@ -329,7 +337,7 @@ struct RowTiles {
                 const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
                 const bool in = i < total && u < units && k < p.K && p.x_aligned;
                 const int row = in && p.xrow ? p.xrow[m] : m;
-                const int32_t off = in ? (row * (int32_t)p.x_pitch + k) * (kSplit ? 4 : 2) : kOutside;
+                const int32_t off = in ? (row * p.x_pitch + k) * (kSplit ? 4 : 2) : kOutside;
                 xr[b][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 0, 0);
                 if constexpr (kSplit) xr[b][1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 16, 0);
             }
@@ -369,7 +377,7 @@ struct RowTiles {
                 for (int b = 0; b < kXUnits; ++b) {
                     const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
                     if (i >= total || u >= units) continue;
-                    const uint16_t* src = static_cast<const uint16_t*>(p.x) + (p.xrow ? p.xrow[m] : m) * p.x_pitch + k;
+                    const uint16_t* src = static_cast<const uint16_t*>(p.x) + (int64_t)(p.xrow ? p.xrow[m] : m) * p.x_pitch + k;
                     u32x4_t v;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -385,17 +393,17 @@ struct RowTiles {
         // codes and scales of the wave's lines in the window that starts at chunk c0
         const int32_t voff = (int32_t)((lane >> 3) * w.stride) + 16 * (lane & 7);
         const int32_t stride8 = (int32_t)(8 * w.stride);
-        auto fetch = [&](Fetched& f, int64_t item, int c0, bool any) {
+        auto fetch = [&](Fetched& f, int item, int c0, bool any) {
             const int c = c0 + wk * U;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const int64_t j = item * p.step + wr * p.group_step + p.off[r], left = any ? p.count - j : 0;
-                const int valid = left > 16 ? 16 : left > 0 ? (int)left : 0;
+                const int j = item * p.step + wr * p.group_step + p.off[r], left = any ? p.count - j : 0;
+                const int valid = left > 16 ? 16 : left > 0 ? left : 0;
                 const int64_t first = p.base[r] + j;
                 if constexpr (F == kLevels) {
 #pragma unroll
                     for (int b = 0; b < kSBatch; ++b) {
-                        const int64_t k = (int64_t)c * kChunk + (h + 4 * b) * 64;
+                        const int k = c * kChunk + (h + 4 * b) * 64;
                         f.s[r][b] = 0.0f;
                         f.z[r][b] = 0;
                         if (n < valid && k < p.K) {
@@ -422,36 +430,21 @@ struct RowTiles {
                 }
                 const __amdgpu_buffer_rsrc_t cbuf = buffer(w.codes + first * w.stride, (int64_t)valid * w.stride);
 #pragma unroll
-                for (int q = 0; q < U; ++q) {                    // rows 8 (q % 2) + lane / 8 of line q / 2
-                    const int cq = c + (q & ~1);
+                for (int q = 0; q < 2; ++q)                      // rows 8 q + lane / 8
                     f.c[r][q] = __builtin_amdgcn_raw_buffer_load_b128(
-                        cbuf, voff, cq < nchunk ? (q & 1) * stride8 + cq * (kChunk / 2) : kOutside, kNontemporal);
-                }
+                        cbuf, voff, c < nchunk ? q * stride8 + c * (kChunk / 2) : kOutside, kNontemporal);
             }
         };
 
-        const int am = act_of_row<MI>(n);
-        const int arow = (am < xrows ? am : xrows - 1) * xpitch;
-        float y[RT][MI];
-        // one window's products
-        auto compute = [&](Fetched& f, int c0, const uint8_t* xwin) {
-            const int cw = c0 + wk * U;
-            if (cw >= nchunk) return;
-            // from lines to fragments: 16-byte unit u of row r sits in unit u ^ r of its row
+        // What was fetched goes to the wave's own LDS: codes from lines to fragments (16-byte unit u of row r
+        // sits in unit u ^ (r % 8) of its row), scales converted.
+        auto land = [&](const Fetched& f) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
 #pragma unroll
-                for (int q = 0; q < U; ++q) {
-                    const int row = 8 * (q & 1) + (lane >> 3), unit = 8 * (q >> 1) + (lane & 7);
-                    *reinterpret_cast<u32x4_t*>(clds + row * (128 * NS) + 16 * (unit ^ (row & (8 * NS - 1)))) = f.c[r][q];
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    f.c[r][u] = *reinterpret_cast<const u32x4_t*>(clds + n * (128 * NS) +
-                                                                  16 * ((4 * u + h) ^ (n & (8 * NS - 1))));
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
+                for (int q = 0; q < 2; ++q)
+                    *reinterpret_cast<u32x4_t*>(clds + (16 * r + 8 * q + (lane >> 3)) * 128 +
+                                                16 * ((lane & 7) ^ (lane >> 3))) = f.c[r][q];
 #pragma unroll
                 for (int b = 0; b < kSBatch; ++b) {
                     floatx2_t v;
@@ -465,12 +458,29 @@ struct RowTiles {
                     }
                     if (h + 4 * b < kEntries) slds[(16 * r + n) * kSPitch + h + 4 * b] = v;
                 }
+            }
+        };
+        const int am = act_of_row<MI>(n);
+        const int arow = (am < xrows ? am : xrows - 1) * xpitch;
+        float y[RT][MI];
+        // The products of one window.  Rolled: a workgroup runs this code a few times at most, and fetching an
+        // instruction for the first time costs more than looping.
+        auto compute = [&](int c0, const uint8_t* xwin) {
+            const int cw = c0 + wk * U;
             const uint8_t* ax = xwin + arow + 2 * (kResident ? cw * kChunk : wk * (U * kChunk));
-#pragma unroll
+            const floatx2_t* sp = slds + n * kSPitch;
+#pragma unroll 1
             for (int u = 0; u < U; ++u) {
-                if (cw + u >= nchunk) break;
+                u32x4_t c[RT];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) order_chunk<NG>(f.c[r][u]);
+                for (int r = 0; r < RT; ++r)
+                    c[r] = *reinterpret_cast<const u32x4_t*>(clds + (16 * r + n) * 128 + 16 * ((4 * u + h) ^ (n & 7)));
+                u32x4_t a[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    a[j] = *reinterpret_cast<const u32x4_t*>(ax + 2 * (u * kChunk + chunk_k<NG>(j, h)));
+#pragma unroll
+                for (int r = 0; r < RT; ++r) order_chunk<NG>(c[r]);
 #pragma unroll
                 for (int q = 0; q < NG; ++q) {
                     floatx4_t acc[RT], xs = {0, 0, 0, 0};
@@ -478,20 +488,19 @@ struct RowTiles {
                     for (int r = 0; r < RT; ++r) acc[r] = (floatx4_t){0, 0, 0, 0};
 #pragma unroll
                     for (int j = q * kMfmas; j < (q + 1) * kMfmas; ++j) {
-                        const u32x4_t a = *reinterpret_cast<const u32x4_t*>(ax + 2 * (u * kChunk + chunk_k<NG>(j, h)));
                         if constexpr (F == kLevels) {
 #pragma unroll
                             for (int r = 0; r < RT; ++r)
-                                acc[r] = mfma<F>(a, decode8_table(tab, f.c[r][u][j], 4 * lane), acc[r]);
+                                acc[r] = mfma<F>(a[j], decode8_table(tab, c[r][j], 4 * lane), acc[r]);
                         } else {
-                            xs = mfma<F>(a, ones<F>(), xs);
+                            xs = mfma<F>(a[j], ones<F>(), xs);
 #pragma unroll
-                            for (int r = 0; r < RT; ++r) acc[r] = mfma<F>(a, decode8<F>(f.c[r][u][j], magic), acc[r]);
+                            for (int r = 0; r < RT; ++r) acc[r] = mfma<F>(a[j], decode8<F>(c[r][j], magic), acc[r]);
                         }
                     }
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const floatx2_t s = slds[(16 * r + n) * kSPitch + u * NG + q];
+                        const floatx2_t s = sp[16 * r * kSPitch + u * NG + q];
 #pragma unroll
                         for (int i = 0; i < MI; ++i) {
                             if constexpr (F != kLevels) y[r][i] = fmaf(-s[1], xs[i], y[r][i]);
@@ -502,78 +511,77 @@ struct RowTiles {
             }
         };
 
-        Fetched f[2];
+        Fetched f;
         x_load(0, 0);
-        fetch(f[0], item0, 0, true);
+        fetch(f, item0, 0, true);
         if constexpr (kResident) {
             x_store(xlds, 0, 0);
+#pragma unroll 1
             for (int base = kXUnits * kThreads; base < total; base += kXUnits * kThreads) {
                 x_load(base, 0);
                 x_store(xlds, base, 0);
             }
             __syncthreads();
         }
-        int64_t item = item0;
+        int item = item0;
         int c0 = 0, xsel = 0, putsel = 0;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int i = 0; i < MI; ++i) y[r][i] = 0.0f;
-        // One window.  The loop below always makes two steps; a step past the last item reads nothing
-        // (its ranges are empty) and computes nothing.  Its loads are issued without a condition: a branch
-        // around them would make the wait for this window's codes cover the next one's too.
-        auto step = [&](Fetched& cur, Fetched& nxt) {
+        while (true) {
             uint8_t* xwin = xlds + (kResident ? 0 : xsel * (xrows * win_pitch));
             if constexpr (!kResident) {
                 if (p.x_bufs == 1) __syncthreads();              // the last window's reads
                 x_store(xwin, 0, c0 * kChunk);
             }
-            int64_t ni = item;
+            land(f);
+            int ni = item;
             int nc = c0 + wchunks;
             const bool last = nc >= nchunk;                      // last window of the item
             if (last) {
                 nc = 0;
                 ++ni;
             }
+            // Unconditional (past the last item the ranges are empty and nothing is read): a branch around
+            // them would make later waits cover these loads.
             if constexpr (!kResident) x_load(0, nc * kChunk);
-            fetch(nxt, ni, nc, ni < item1);
+            fetch(f, ni, nc, ni < item1);
             if constexpr (!kResident) {
                 __syncthreads();
                 xsel ^= p.x_bufs - 1;
             }
-            if (item < item1) {
-                compute(cur, c0, xwin);
-                if (last) {
-                    float* pp = put + putsel * (kPutBytes / 4);
-                    if constexpr (kPuts == 2) putsel ^= 1;
+            if (c0 + wk * U < nchunk) compute(c0, xwin);
+            if (last) {
+                float* pp = put + putsel * (kPutBytes / 4);
+                if constexpr (kPuts == 2) putsel ^= 1;
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
+                for (int r = 0; r < RT; ++r)
 #pragma unroll
-                        for (int i = 0; i < MI; ++i) {
-                            pp[(wave * RT + r) * (64 * MI) + 64 * i + lane] = y[r][i];
-                            y[r][i] = 0.0f;
-                        }
-                    __syncthreads();
-                    out(item, pp);
-                    if constexpr (kPuts == 1) __syncthreads();
-                }
+                    for (int i = 0; i < MI; ++i) {
+                        pp[(wave * RT + r) * (64 * MI) + 64 * i + lane] = y[r][i];
+                        y[r][i] = 0.0f;
+                    }
+                __syncthreads();
+                out(item, pp);
+                if constexpr (kPuts == 1) __syncthreads();
+                if (ni >= item1) break;
             }
             item = ni;
             c0 = nc;
-        };
-        do {
-            step(f[0], f[1]);
-            step(f[1], f[0]);
-        } while (item < item1);
+        }
         __syncthreads();
     }
 
     // From the partial sums: output o (o < 64 MI) of tile r of row group q, the waves added in their
     // order.  Its row in the tile is o % 16, its activation row act_of(o).
     static __device__ __forceinline__ float sum(const float* put, int kwl, int q, int r, int o) {
-        float v = 0.0f;
         const float* first = put + ((q << kwl) * RT + r) * (64 * MI) + o;
-        for (int w = 0; w < (1 << kwl); ++w) v += first[w * (RT * 64 * MI)];
+        float p[W], v = 0.0f;                                    // all reads first, then the sum
+#pragma unroll
+        for (int w = 0; w < W; ++w) p[w] = first[(w < (1 << kwl) ? w : 0) * (RT * 64 * MI)];
+#pragma unroll
+        for (int w = 0; w < W; ++w) v += w < (1 << kwl) ? p[w] : 0.0f;
         return v;
     }
     static __device__ __forceinline__ int act_of(int o) { return MI * ((o & 63) >> 4) + (o >> 6); }
