@@ -30,20 +30,23 @@ struct Int4Task {
     int32_t share, more;     // tiles of 16 rows per workgroup; the first `more` workgroups take one tile more
 };
 
+// A launch of one weight has arguments of its own: finding a task in the longer list costs two
+// dependent reads of the arguments, about a microsecond.
+template <int kTasks>
 struct Int4Group {
-    int32_t wg0[kMaxGemvTasks];          // first workgroup of each task (past the last one: never reached)
+    int32_t wg0[kTasks];     // first workgroup of each task (past the last one: never reached)
     int32_t M;
     int32_t x_bufs;
-    Int4Task t[kMaxGemvTasks];
+    Int4Task t[kTasks];
 };
 
-template <int F, int NG, int RT, int MI, bool kResident>
-__global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group g) {
+template <int F, int NG, int RT, int MI, bool kResident, int kTasks>
+__global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks> g) {
     extern __shared__ __align__(16) uint8_t lds[];
     typedef RowTiles<F, NG, RT, MI, kResident, false> Tiles;
     int ti = 0;
 #pragma unroll
-    for (int i = 1; i < kMaxGemvTasks; ++i) ti += (int)blockIdx.x >= g.wg0[i];
+    for (int i = 1; i < kTasks; ++i) ti += (int)blockIdx.x >= g.wg0[i];
     const Int4Task& t = g.t[ti];
     // this workgroup's rows
     const int b = (int)blockIdx.x - g.wg0[ti];
@@ -68,13 +71,16 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group g) {
     p.M = g.M;
     p.x_bufs = g.x_bufs;
     const int steps = 7 - t.kwl + (RT == 2);             // log2(step)
-    Tiles::run(t.w, p, 0, (p.count + p.step - 1) >> steps, nullptr, lds, [&](int item, const float* put) {
-        for (int o = threadIdx.x; o < (RT * 64 * MI * 8) >> t.kwl; o += kThreads) {
-            const int q = o / (RT * 64 * MI), r = o / (64 * MI) % RT, e = o % (64 * MI), m = Tiles::act_of(e);
-            const int j = item * p.step + q * (16 * RT) + 16 * r + (e & 15);
-            const float v = Tiles::sum(put, t.kwl, q, r, e);
-            if (m < g.M && j < p.count) t.y[m * t.N + row0 + j] = float_to_bits16(v, F == kInt4F16);
-        }
+    Tiles::run(t.w, p, 0, (p.count + p.step - 1) >> steps, nullptr, lds, [&](int item, int q, const float* put) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int o = 64 * i + (threadIdx.x & 63), m = Tiles::act_of(o);
+                const int j = item * p.step + q * (16 * RT) + 16 * r + (o & 15);
+                const float v = Tiles::sum(put, t.kwl, q, r, o);
+                if (m < g.M && j < p.count) t.y[m * t.N + row0 + j] = float_to_bits16(v, F == kInt4F16);
+            }
     });
 }
 
@@ -86,35 +92,51 @@ bool resident_for(int M, int ng, int64_t K) {
     return w4_fixed_bytes(ng, kRt, mi_for(M)) + w4_x_bytes(8, M, K, true, 1) <= kLdsBytes / 2;
 }
 
-template <int F, int NG, int MI, bool kResident>
-hipError_t launch_one(Int4Group& g, int64_t grid, int64_t kmax, hipStream_t s) {
-    typedef RowTiles<F, NG, kRt, MI, kResident, false> Tiles;
-    g.x_bufs = 2;
-    const size_t lds = Tiles::kFixedBytes + w4_x_bytes(4, g.M, kmax, kResident, 2);
+constexpr int32_t kNever = 0x7FFFFFFF;
+
+template <int F, int NG, int MI, bool kResident, int kTasks>
+hipError_t launch_tasks(const Int4Group<kTasks>& g, int64_t grid, size_t lds, hipStream_t s) {
+    const auto kernel = &int4_gemv_kernel<F, NG, kRt, MI, kResident, kTasks>;
     if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&int4_gemv_kernel<F, NG, kRt, MI, kResident>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
-    int4_gemv_kernel<F, NG, kRt, MI, kResident><<<dim3((unsigned)grid), dim3(kThreads), lds, s>>>(g);
+    kernel<<<dim3((unsigned)grid), dim3(kThreads), lds, s>>>(g);
     return hipGetLastError();
 }
 
+template <int F, int NG, int MI, bool kResident>
+hipError_t launch_one(Int4Group<kMaxGemvTasks>& g, int64_t grid, int64_t kmax, hipStream_t s) {
+    typedef RowTiles<F, NG, kRt, MI, kResident, false> Tiles;
+    g.x_bufs = 2;
+    const size_t lds = Tiles::kFixedBytes + w4_x_bytes(4, g.M, kmax, kResident, 2);
+    if (g.wg0[1] == kNever) {
+        Int4Group<1> one;
+        one.wg0[0] = 0;
+        one.M = g.M;
+        one.x_bufs = g.x_bufs;
+        one.t[0] = g.t[0];
+        return launch_tasks<F, NG, MI, kResident, 1>(one, grid, lds, s);
+    }
+    return launch_tasks<F, NG, MI, kResident, kMaxGemvTasks>(g, grid, lds, s);
+}
+
 template <int F, int NG, int MI>
-hipError_t launch_shape(Int4Group& g, int64_t grid, bool resident, int64_t kmax, hipStream_t s) {
+hipError_t launch_shape(Int4Group<kMaxGemvTasks>& g, int64_t grid, bool resident, int64_t kmax, hipStream_t s) {
     if (resident) return launch_one<F, NG, MI, true>(g, grid, kmax, s);
     return launch_one<F, NG, MI, false>(g, grid, kmax, s);
 }
 
 template <int F, int NG>
-hipError_t launch_mi(Int4Group& g, int64_t grid, bool resident, int64_t kmax, hipStream_t s) {
+hipError_t launch_mi(Int4Group<kMaxGemvTasks>& g, int64_t grid, bool resident, int64_t kmax, hipStream_t s) {
     if (mi_for(g.M) == 1) return launch_shape<F, NG, 1>(g, grid, resident, kmax, s);
     if (mi_for(g.M) == 2) return launch_shape<F, NG, 2>(g, grid, resident, kmax, s);
     return launch_shape<F, NG, 4>(g, grid, resident, kmax, s);
 }
 
 template <int F>
-hipError_t launch_ng(Int4Group& g, int64_t grid, int ng, bool resident, int64_t kmax, hipStream_t s) {
+hipError_t launch_ng(Int4Group<kMaxGemvTasks>& g, int64_t grid, int ng, bool resident, int64_t kmax, hipStream_t s) {
     if (ng == 4) return launch_mi<F, 4>(g, grid, resident, kmax, s);
     if (ng == 2) return launch_mi<F, 2>(g, grid, resident, kmax, s);
     return launch_mi<F, 1>(g, grid, resident, kmax, s);
@@ -146,7 +168,7 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
         const int ng = int4_groups_per_chunk(items[first].st->group);
         // the weights of the launch: one scale granularity, activations that all fit, or all do not
         const bool resident = resident_for(M, ng, items[first].st->cols);
-        Int4Group g;
+        Int4Group<kMaxGemvTasks> g;
         int32_t n = 0;
         int64_t tiles[kMaxGemvTasks], items_of[kMaxGemvTasks], kmax = 0;
         double work = 0;
@@ -173,13 +195,15 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
         for (int32_t i = 0; i < n; ++i) {
             Int4Task& t = g.t[i];
             const double part = 2.0 * device_cu_count() * ((double)tiles[i] * (double)t.K / work);
-            const int64_t wgs = std::max<int64_t>(1, std::min<int64_t>(items_of[i], (int64_t)(part + 0.5)));
+            int64_t wgs = std::max<int64_t>(1, std::min<int64_t>(items_of[i], (int64_t)(part + 0.5)));
+            // a workgroup's rows stay under 2 GB of codes (and of scales: at most two bytes for 16 of codes)
+            wgs = std::max(wgs, (int64_t)((double)(tiles[i] + 1) * 16 * (double)t.w.stride / (1 << 30)) + 1);
             t.share = (int32_t)(tiles[i] / wgs);
             t.more = (int32_t)(tiles[i] % wgs);
             g.wg0[i] = (int32_t)grid;
             grid += wgs;
         }
-        for (int32_t i = n; i < kMaxGemvTasks; ++i) g.wg0[i] = 0x7FFFFFFF;
+        for (int32_t i = n; i < kMaxGemvTasks; ++i) g.wg0[i] = kNever;
         g.M = M;
         const hipError_t e = f16 ? launch_ng<kInt4F16>(g, grid, ng, resident, kmax, s)
                                  : launch_ng<kInt4Bf16>(g, grid, ng, resident, kmax, s);

@@ -221,9 +221,10 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertA
             const int M = count - m0 < 4 * MI ? count - m0 : 4 * MI;
             r.xrow = p.routes->tok[a] + m0;
             r.M = M;
-            Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, const float* put) {
-                for (int o = threadIdx.x; o < (64 * MI * 8) >> p.kwl; o += kThreads) {
-                    const int q = o / (64 * MI), s = o % (64 * MI), m = Tiles::act_of(s);
+            Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, int q, const float* put) {
+#pragma unroll
+                for (int s = threadIdx.x & 63; s < 64 * MI; s += 64) {
+                    const int m = Tiles::act_of(s);
                     const int i = item * step + 16 * q + (s & 15);
                     if (m < M && i < p.Ipad) {
                         const float gate = Tiles::sum(put, p.kwl, q, 0, s), up = Tiles::sum(put, p.kwl, q, 1, s);
@@ -273,10 +274,10 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(Exper
             const int M = count - m0 < 2 * MI ? count - m0 : 2 * MI;
             r.xrow = p.routes->pair[a] + m0;
             r.M = M;
-            Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, const float* put) {
-                for (int o = threadIdx.x; o < M * step; o += kThreads) {
-                    const int m = o / step, row = o % step, q = row / (16 * RT), t = row / 16 % RT;
-                    const int n = item * step + row;
+            Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, int q, const float* put) {
+                for (int o = threadIdx.x & 63; o < M * (16 * RT); o += 64) {
+                    const int m = o / (16 * RT), row = o % (16 * RT), t = row / 16;
+                    const int n = item * step + q * (16 * RT) + row;
                     const float v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m)) +
                                     Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m + 1));
                     if (n < p.H) p.out[(int64_t)p.routes->pair[a][m0 + m] * p.H + n] = v * p.routes->w[a][m0 + m];

@@ -210,8 +210,9 @@ __device__ __forceinline__ u32x4_t decode8_table(const uint8_t* tab, uint32_t w,
 //
 // kw of the waves split k, W / kw groups of them take different rows.  A row is cut into windows
 // of kw * 256 k; a wave takes one line (128 bytes, 256 k) of each row per window, and the
-// partial outputs of the kw waves meet in LDS once per item and are added in their order (no
-// atomics, the same bits every time).  While a wave works on one window the codes and scales of
+// partial outputs of the kw waves meet in LDS once per item, where the last wave to arrive adds
+// them in wave order (the same bits every time).  No wave waits for another except every
+// kSlots items, and per window where the activations do not stay.  While a wave works on one window the codes and scales of
 // the next one (of the same item or the next) are already on their way into registers.
 //
 // Activations (in the order of decoded int4, zero past K) live in LDS, 16 bytes more than a row
@@ -259,11 +260,11 @@ __device__ __forceinline__ constexpr int act_of_row(int row) { return MI * (row 
 
 constexpr int kLineK = 256;               // k of a 128-byte line of codes
 
-// bytes of LDS beside the activations: scales, codes, partial sums (two buffers where they are small)
+// bytes of LDS beside the activations: scales, codes, partial sums of a few items and their counters
 constexpr int w4_put_bytes(int RT, int MI) { return 8 * RT * 64 * MI * 4; }
+constexpr int w4_slots(int MI) { return MI == 1 ? 4 : 2; }
 constexpr int w4_fixed_bytes(int NG, int RT, int MI) {
-    return 8 * RT * 16 * ((2 * NG) | 1) * 8 + 8 * RT * 16 * 128 +
-           (w4_put_bytes(RT, MI) <= 8192 ? 2 : 1) * w4_put_bytes(RT, MI);
+    return 8 * RT * 16 * ((2 * NG) | 1) * 8 + 8 * RT * 16 * 128 + w4_slots(MI) * (w4_put_bytes(RT, MI) + 32);
 }
 constexpr size_t kLdsBytes = 160 * 1024;  // of a CU
 
@@ -290,11 +291,11 @@ struct RowTiles {
     static constexpr int kScaleBytes = W * RT * 16 * kSPitch * 8;
     static constexpr int kCodeBytes = W * RT * 16 * 128;        // a window's codes changing layout
     static constexpr int kPutBytes = w4_put_bytes(RT, MI);
-    static constexpr int kPuts = kPutBytes <= 8192 ? 2 : 1;
+    static constexpr int kSlots = w4_slots(MI);
     // units of x per thread and batch; a window's fit one batch (kw <= 4)
     static constexpr int kXUnits = kResident ? 2 : kSplit ? (MI + 1) / 2 : MI;
     static constexpr int kFixedBytes = w4_fixed_bytes(NG, RT, MI);
-    static_assert(kFixedBytes == kScaleBytes + kCodeBytes + kPuts * kPutBytes);
+    static_assert(kFixedBytes == kScaleBytes + kCodeBytes + kSlots * (kPutBytes + 32));
 
     struct Fetched {
         u32x4_t c[RT][2];
@@ -303,7 +304,7 @@ struct RowTiles {
     };
 
     // tab: the level table (kLevels); lds: kFixedBytes + w4_x_bytes(), 16-byte aligned.
-    // out(item, put) stores an item's outputs from the partial sums.
+    // out(item, q, put), called by one wave, stores the outputs of row group q of an item from the partial sums.
     template <class V, class Out>
     static __device__ __forceinline__ void run(const V& w, const Rows<RT>& p, int item0, int item1,
                                                const uint8_t* tab, uint8_t* lds, Out&& out) {
@@ -313,6 +314,7 @@ struct RowTiles {
         floatx2_t* slds = reinterpret_cast<floatx2_t*>(lds) + wave * (RT * 16 * kSPitch);
         uint8_t* clds = lds + kScaleBytes + wave * (RT * 16 * 128);
         float* put = reinterpret_cast<float*>(lds + kScaleBytes + kCodeBytes);
+        int* arrived = reinterpret_cast<int*>(lds + kScaleBytes + kCodeBytes + kSlots * kPutBytes);
         uint8_t* xlds = lds + kFixedBytes;
         const int nchunk = (p.K + kChunk - 1) / kChunk;
         const int wchunks = kw * U;
@@ -390,24 +392,38 @@ struct RowTiles {
             }
         };
 
-        // codes and scales of the wave's lines in the window that starts at chunk c0
-        const int32_t voff = (int32_t)((lane >> 3) * w.stride) + 16 * (lane & 7);
-        const int32_t stride8 = (int32_t)(8 * w.stride);
-        auto fetch = [&](Fetched& f, int item, int c0, bool any) {
+        // Codes and scales of the wave's lines in the window that starts at chunk c0 of the item whose tile 0
+        // of this wave's row group starts at row j.  One descriptor per tile covers the whole run of rows (under
+        // 2 GB, see the callers), so a window costs a few scalar instructions; j < 0: nothing.
+        __amdgpu_buffer_rsrc_t cbuf[RT], sbuf[RT], zbuf[RT];
+        int32_t shift[RT];                                       // tile r's rows start at shift[r] + j of its range
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            shift[r] = p.off[r];
+            cbuf[r] = buffer(w.codes + p.base[r] * w.stride, (int64_t)p.count * w.stride);
+            if constexpr (F != kLevels) {
+                sbuf[r] = buffer(w.scales + p.base[r] * w.G, (int64_t)p.count * w.G * 2);
+                zbuf[r] = buffer(w.zeros ? w.zeros + p.base[r] * w.G : nullptr, w.zeros ? (int64_t)p.count * w.G : 0);
+            }
+        }
+        const int32_t stride = (int32_t)w.stride;
+        const int32_t voff = (lane >> 3) * stride + 16 * (lane & 7);
+        int32_t ng = 0;
+        if constexpr (F != kLevels) ng = n * w.G;
+        auto fetch = [&](Fetched& f, int j, int c0) {
             const int c = c0 + wk * U;
+            const bool in = j >= 0 && c < nchunk;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const int j = item * p.step + wr * p.group_step + p.off[r], left = any ? p.count - j : 0;
-                const int valid = left > 16 ? 16 : left > 0 ? left : 0;
-                const int64_t first = p.base[r] + j;
+                const int row = j + shift[r];
                 if constexpr (F == kLevels) {
 #pragma unroll
                     for (int b = 0; b < kSBatch; ++b) {
                         const int k = c * kChunk + (h + 4 * b) * 64;
                         f.s[r][b] = 0.0f;
                         f.z[r][b] = 0;
-                        if (n < valid && k < p.K) {
-                            const int64_t blk = ((first + n) * p.K + k) >> w.bshift;
+                        if (in && row + n < p.count && k < p.K) {
+                            const int64_t blk = ((p.base[r] + row + n) * p.K + k) >> w.bshift;
                             if (w.nested) {
                                 f.z[r][b] = (uint8_t)w.q8[blk];
                                 f.s[r][b] = w.dq_scale[blk / QK_DQ_BLOCK];
@@ -417,22 +433,20 @@ struct RowTiles {
                         }
                     }
                 } else {
-                    const __amdgpu_buffer_rsrc_t sbuf = buffer(w.scales + first * w.G, (int64_t)valid * w.G * 2);
-                    const __amdgpu_buffer_rsrc_t zbuf =
-                        buffer(w.zeros ? w.zeros + first * w.G : nullptr, w.zeros ? (int64_t)valid * w.G : 0);
+                    const int32_t soff = in ? row * w.G : kOutside / 2;
 #pragma unroll
                     for (int b = 0; b < kSBatch; ++b) {
                         const int e = h + 4 * b;
-                        const int g = n * w.G + (NG > 1 ? c * NG + e : ((c + e) * kChunk) >> w.gshift);
-                        f.s[r][b] = as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sbuf, 2 * g, 0, 0));
-                        f.z[r][b] = (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zbuf, g, 0, 0);
+                        const int g = ng + (NG > 1 ? c * NG + e : ((c + e) * kChunk) >> w.gshift);
+                        f.s[r][b] = as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sbuf[r], 2 * g, 2 * soff, 0));
+                        f.z[r][b] = (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zbuf[r], g, soff, 0);
                     }
                 }
-                const __amdgpu_buffer_rsrc_t cbuf = buffer(w.codes + first * w.stride, (int64_t)valid * w.stride);
+                const int32_t coff = row * stride + c * (kChunk / 2);
 #pragma unroll
                 for (int q = 0; q < 2; ++q)                      // rows 8 q + lane / 8
-                    f.c[r][q] = __builtin_amdgcn_raw_buffer_load_b128(
-                        cbuf, voff, c < nchunk ? q * stride8 + c * (kChunk / 2) : kOutside, kNontemporal);
+                    f.c[r][q] = __builtin_amdgcn_raw_buffer_load_b128(cbuf[r], voff, in ? coff + 8 * q * stride : kOutside,
+                                                                      kNontemporal);
             }
         };
 
@@ -513,7 +527,9 @@ struct RowTiles {
 
         Fetched f;
         x_load(0, 0);
-        fetch(f, item0, 0, true);
+        int j = item0 * p.step + wr * p.group_step;               // row of the next window to fetch
+        fetch(f, j, 0);
+        if (tid < kSlots * W) arrived[tid] = 0;
         if constexpr (kResident) {
             x_store(xlds, 0, 0);
 #pragma unroll 1
@@ -524,7 +540,7 @@ struct RowTiles {
             __syncthreads();
         }
         int item = item0;
-        int c0 = 0, xsel = 0, putsel = 0;
+        int c0 = 0, xsel = 0, slot = 0;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -536,25 +552,24 @@ struct RowTiles {
                 x_store(xwin, 0, c0 * kChunk);
             }
             land(f);
-            int ni = item;
             int nc = c0 + wchunks;
             const bool last = nc >= nchunk;                      // last window of the item
+            const bool end = last && item + 1 >= item1;
             if (last) {
                 nc = 0;
-                ++ni;
+                j += p.step;
             }
-            // Unconditional (past the last item the ranges are empty and nothing is read): a branch around
+            // Unconditional (past the last item every offset is outside and nothing is read): a branch around
             // them would make later waits cover these loads.
             if constexpr (!kResident) x_load(0, nc * kChunk);
-            fetch(f, ni, nc, ni < item1);
+            fetch(f, end ? -1 : j, nc);
             if constexpr (!kResident) {
                 __syncthreads();
                 xsel ^= p.x_bufs - 1;
             }
             if (c0 + wk * U < nchunk) compute(c0, xwin);
             if (last) {
-                float* pp = put + putsel * (kPutBytes / 4);
-                if constexpr (kPuts == 2) putsel ^= 1;
+                float* pp = put + slot * (kPutBytes / 4);
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -562,12 +577,20 @@ struct RowTiles {
                         pp[(wave * RT + r) * (64 * MI) + 64 * i + lane] = y[r][i];
                         y[r][i] = 0.0f;
                     }
-                __syncthreads();
-                out(item, pp);
-                if constexpr (kPuts == 1) __syncthreads();
-                if (ni >= item1) break;
+                int before = 0;
+                if (lane == 0)
+                    before = __hip_atomic_fetch_add(&arrived[slot * W + wr], 1, __ATOMIC_ACQ_REL,
+                                                    __HIP_MEMORY_SCOPE_WORKGROUP);
+                if (__builtin_amdgcn_readfirstlane(before) == kw - 1) out(item, wr, pp);
+                if (end) break;
+                ++item;
+                if (++slot == kSlots) {
+                    slot = 0;
+                    __syncthreads();
+                    if (tid < kSlots * W) arrived[tid] = 0;
+                    __syncthreads();
+                }
             }
-            item = ni;
             c0 = nc;
         }
         __syncthreads();
