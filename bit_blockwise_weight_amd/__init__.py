@@ -111,8 +111,8 @@ class GemvTask(ctypes.Structure):
 
 
 class GemvInt4Task(ctypes.Structure):
-    """Mirror of qk_gemv_int4_task (include/qk.h)."""
-    _fields_ = [("x", ctypes.c_void_p), ("st", ctypes.POINTER(Int4State)), ("y", ctypes.c_void_p)]
+    """Mirror of qk_gemv_int4_task (include/qk.h); st is the descriptor's address."""
+    _fields_ = [("x", ctypes.c_void_p), ("st", ctypes.c_void_p), ("y", ctypes.c_void_p)]
 
 
 class DequantTask(ctypes.Structure):
@@ -821,43 +821,64 @@ def qk_int4_state_init(rows: int, cols: int, group: int, codes: torch.Tensor, sc
         raise ValueError(f"scales must be fp16 or bf16 [{rows}, {ngroups}], got {scales.dtype} {tuple(scales.shape)}")
     if zeros is not None and (zeros.dtype != torch.uint8 or zeros.numel() != rows * ngroups):
         raise ValueError(f"zeros must be uint8 [{rows}, {ngroups}], got {zeros.dtype} {tuple(zeros.shape)}")
-    _require_cuda(codes, scales, zeros)
-    _same_device(codes, scales, zeros)
+    dev = codes.device
     st = Int4State()
-    _check(lib().qk_int4_state_init(ctypes.byref(st), int(rows), int(cols), int(group), _ptr(codes), codes.shape[1],
-                                    _ptr(scales), _DTYPE_CODE[scales.dtype], _ptr(zeros)))
+    _check(lib().qk_int4_state_init(ctypes.byref(st), int(rows), int(cols), int(group), _ready(codes, dev, "codes"),
+                                    codes.shape[1], _ready(scales, dev, "scales"), _DTYPE_CODE[scales.dtype],
+                                    None if zeros is None else _ready(zeros, dev, "zeros")))
     # keep the device buffers alive as long as the descriptor
     st._keep = (codes, scales, zeros)
+    st._device, st._shape, st._address = dev, (int(rows), int(cols)), ctypes.addressof(st)
     return st
 
 
-def _same_device(*ts):
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors of one call must be on one device, got {sorted(map(str, devs))}")
+# The decode calls below take a few microseconds on the GPU, so their wrappers do no more than they must: one
+# pass over the arguments, addresses as plain integers, no context managers on the common path.
+
+def _ready(t: torch.Tensor, dev: torch.device, name: str) -> int:
+    """The address of a contiguous tensor on device dev."""
+    if t.device != dev or not t.is_cuda:
+        if not t.is_cuda:
+            raise ValueError("tensors passed to libqk must be on a HIP device")
+        raise ValueError(f"tensors of one call must be on one device: {name} is on {t.device}, not on {dev}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libqk must be contiguous")
+    return t.data_ptr()
 
 
-def _int4_acts(x: torch.Tensor, state: Int4State, y, name: str):
-    """(x as [M, K], y allocated or checked) of a product with an int4 weight."""
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"{name} must be bf16 or fp16, got {x.dtype}")
-    x2 = _rows_of(x, state.cols, name)
-    M = x2.shape[0]
-    if y is None:
-        y = torch.empty((M, state.rows), dtype=x.dtype, device=x.device)
+def _call(dev: torch.device, fn, *args):
+    """fn(*args, current stream of dev) with dev current."""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
-        _check_out(y, (M, state.rows), x.dtype, "y" if name == "x" else name[:-1] + "y")
-    _require_cuda(x, y)
-    _same_device(x, y, state._keep[0])
-    return x2, y
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != QK_OK:
+        _check(status)
+
+
+def _int4_acts(x: torch.Tensor, state: Int4State, y, dev, name: str):
+    """(address of x, M, y allocated or checked, address of y) of a product with an int4 weight."""
+    cols, rows = state._shape[1], state._shape[0]
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float16:
+        raise ValueError(f"{name}x must be bf16 or fp16, got {x.dtype}")
+    if x.dim() == 0 or x.shape[-1] != cols:
+        raise ValueError(f"{name}x {tuple(x.shape)} does not end in the weight's {cols} columns")
+    M = x.shape[0] if x.dim() == 2 else x.numel() // cols
+    xp = _ready(x, dev, f"{name}x")
+    if y is None:
+        y = torch.empty((M, rows), dtype=x.dtype, device=dev)
+        return xp, M, y, y.data_ptr()
+    _check_out(y, (M, rows), x.dtype, f"{name}y")
+    return xp, M, y, _ready(y, dev, f"{name}y")
 
 
 def qk_gemv_int4(x: torch.Tensor, state: Int4State, y=None) -> torch.Tensor:
     """y [M, N] = x W^T for x [M, K] (bf16 or fp16, M <= 16) and an int4 weight, in x's dtype."""
-    x2, y = _int4_acts(x, state, y, "x")
-    with _on(x.device):
-        _check(lib().qk_gemv_int4(_ptr(x2), _DTYPE_CODE[x.dtype], x2.shape[0], ctypes.byref(state), _ptr(y),
-                                  ctypes.c_void_p(_stream(x))))
+    dev = state._device
+    xp, M, y, yp = _int4_acts(x, state, y, dev, "")
+    _call(dev, lib().qk_gemv_int4, xp, _DTYPE_CODE[x.dtype], M, state, yp)
     return y
 
 
@@ -869,23 +890,20 @@ def qk_gemv_int4_grouped(tasks, ys=None):
         raise ValueError("qk_gemv_int4_grouped needs at least one (x, state)")
     if ys is not None and len(ys) != len(tasks):
         raise ValueError(f"{len(tasks)} tasks but {len(ys)} outputs")
-    arr = (GemvInt4Task * len(tasks))()
-    keep, outs = [], []
+    flat, outs = [], []
+    dev, dtype, rows = tasks[0][1]._device, tasks[0][0].dtype, None
     for i, (x, state) in enumerate(tasks):
-        x2, y = _int4_acts(x, state, None if ys is None else ys[i], f"task {i}: x")
-        if i and (x2.shape[0] != keep[0].shape[0] or x2.dtype != keep[0].dtype):
-            raise ValueError(f"task {i}: every x needs the rows and the dtype of the first ({keep[0].shape[0]}, "
-                             f"{keep[0].dtype}), got {x2.shape[0]}, {x2.dtype}")
-        if i:
-            _same_device(keep[0], x2)
-        arr[i].x = x2.data_ptr()
-        arr[i].st = ctypes.pointer(state)
-        arr[i].y = y.data_ptr()
-        keep.append(x2)
+        if state._device != dev:
+            raise ValueError(f"task {i}: every weight must be on the device of the first ({dev}), got {state._device}")
+        xp, M, y, yp = _int4_acts(x, state, None if ys is None else ys[i], dev, f"task {i}: ")
+        if rows is None:
+            rows = M
+        if M != rows or x.dtype is not dtype:
+            raise ValueError(f"task {i}: every x needs the rows and the dtype of the first ({rows}, {dtype}), got "
+                             f"{M}, {x.dtype}")
+        flat.append((xp, state._address, yp))
         outs.append(y)
-    with _on(keep[0].device):
-        _check(lib().qk_gemv_int4_grouped(arr, len(tasks), _DTYPE_CODE[keep[0].dtype], keep[0].shape[0],
-                                          ctypes.c_void_p(_stream(keep[0]))))
+    _call(dev, lib().qk_gemv_int4_grouped, (GemvInt4Task * len(flat))(*flat), len(flat), _DTYPE_CODE[dtype], rows)
     return outs
 
 
@@ -897,50 +915,51 @@ def qk_moe_workspace_size(T: int, top_k: int, hidden: int, inner: int) -> int:
     return int(out.value)
 
 
-def _moe_args(x, logits, top_k, gate_up, down, y, workspace, dtypes):
-    if x.dtype not in dtypes:
-        raise ValueError(f"x must be one of {dtypes}, got {x.dtype}")
+def _moe(fn, dtype_arg, x, logits, top_k, gate_up, down, renormalize, y, workspace, dev):
+    hidden, inner = gate_up.cols, down.cols
     if logits.dtype not in _DTYPE_CODE:
         raise ValueError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
-    x2 = _rows_of(x, gate_up.cols, "x")
-    T = x2.shape[0]
-    if logits.dim() < 1 or logits.numel() != T * logits.shape[-1]:
+    if x.dim() == 0 or x.shape[-1] != hidden:
+        raise ValueError(f"x {tuple(x.shape)} does not end in the experts' {hidden} features")
+    T = x.numel() // hidden
+    E = logits.shape[-1] if logits.dim() else 0
+    if logits.numel() != T * E:
         raise ValueError(f"logits {tuple(logits.shape)} do not hold one row per token ({T})")
+    xp, lp = _ready(x, dev, "x"), _ready(logits, dev, "logits")
     if y is None:
-        y = torch.empty((T, down.rows // max(1, logits.shape[-1])), dtype=x.dtype, device=x.device)
+        y = torch.empty((T, hidden), dtype=x.dtype, device=dev)
     else:
-        _check_out(y, (T, gate_up.cols), x.dtype, "y")
+        _check_out(y, (T, hidden), x.dtype, "y")
     if workspace is None:
-        workspace = torch.empty(qk_moe_workspace_size(T, top_k, gate_up.cols, down.cols), dtype=torch.uint8, device=x.device)
-    _require_cuda(x, logits, y, workspace)
-    _same_device(x, logits, y, workspace, gate_up._keep[0], down._keep[0])
-    return x2, T, logits.shape[-1], y, workspace
+        workspace = torch.empty(qk_moe_workspace_size(T, top_k, hidden, inner), dtype=torch.uint8, device=dev)
+    _call(dev, fn, xp, *dtype_arg, T, lp, _DTYPE_CODE[logits.dtype], E, int(top_k), 1 if renormalize else 0, gate_up,
+          down, _ready(y, dev, "y"), _ready(workspace, dev, "workspace"), workspace.nbytes)
+    return y
 
 
 def qk_moe_int4(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate_up: Int4State, down: Int4State,
                 renormalize: bool = True, y=None, workspace=None) -> torch.Tensor:
     """Mixture-of-experts layer of x [T, H] (bf16 or fp16, T <= 16) with the router's logits [T, E] over
     int4 experts: gate_up [E * 2 * I, H] (gate rows, then up rows, of each expert), down [E * H, I]."""
-    x2, T, E, y, workspace = _moe_args(x, logits, top_k, gate_up, down, y, workspace, (torch.bfloat16, torch.float16))
-    with _on(x.device):
-        _check(lib().qk_moe_int4(_ptr(x2), _DTYPE_CODE[x.dtype], T, _ptr(logits), _DTYPE_CODE[logits.dtype], E,
-                                 int(top_k), int(bool(renormalize)), ctypes.byref(gate_up), ctypes.byref(down), _ptr(y),
-                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 ctypes.c_void_p(_stream(x))))
-    return y
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float16:
+        raise ValueError(f"x must be bf16 or fp16, got {x.dtype}")
+    dev = gate_up._device
+    if down._device != dev:
+        raise ValueError(f"gate_up is on {dev}, down on {down._device}")
+    return _moe(lib().qk_moe_int4, (_DTYPE_CODE[x.dtype],), x, logits, top_k, gate_up, down, renormalize, y, workspace,
+                dev)
 
 
 def qk_moe_nf4(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate_up: QuantState, down: QuantState,
                renormalize: bool = True, y=None, workspace=None) -> torch.Tensor:
     """qk_moe_int4 over experts quantized by this library (NF4, FP4 or custom levels, plain or
     double-quantized), x in bf16: quantize the stacked weights [E * 2 * I, H] and [E * H, I]."""
-    x2, T, E, y, workspace = _moe_args(x, logits, top_k, gate_up, down, y, workspace, (torch.bfloat16,))
-    with _on(x.device):
-        _check(lib().qk_moe_nf4(_ptr(x2), T, _ptr(logits), _DTYPE_CODE[logits.dtype], E, int(top_k),
-                                int(bool(renormalize)), ctypes.byref(gate_up), ctypes.byref(down), _ptr(y),
-                                _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                ctypes.c_void_p(_stream(x))))
-    return y
+    if x.dtype is not torch.bfloat16:
+        raise ValueError(f"x must be bf16, got {x.dtype}")
+    dev = gate_up._keep[0].device
+    if down._keep[0].device != dev:
+        raise ValueError(f"gate_up is on {dev}, down on {down._keep[0].device}")
+    return _moe(lib().qk_moe_nf4, (), x, logits, top_k, gate_up, down, renormalize, y, workspace, dev)
 
 
 class Int4Weight:

@@ -87,21 +87,17 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
 constexpr int kRt = 2;                                   // tiles of 16 rows per item and row group
 constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
-// The activations of a whole row stay in LDS where two workgroups of a CU can hold them.
-bool resident_for(int M, int ng, int64_t K) {
-    return w4_fixed_bytes(ng, kRt, mi_for(M)) + w4_x_bytes(8, M, K, true, 1) <= kLdsBytes / 2;
-}
+// The activations of a whole row stay in LDS where they fit.
+size_t resident_lds(int M, int ng, int64_t K) { return w4_fixed_bytes(ng, kRt, mi_for(M)) + w4_x_bytes(8, M, K, true, 1); }
+bool resident_for(int M, int ng, int64_t K) { return resident_lds(M, ng, K) <= kLdsBytes; }
 
 constexpr int32_t kNever = 0x7FFFFFFF;
 
 template <int F, int NG, int MI, bool kResident, int kTasks>
 hipError_t launch_tasks(const Int4Group<kTasks>& g, int64_t grid, size_t lds, hipStream_t s) {
-    const auto kernel = &int4_gemv_kernel<F, NG, kRt, MI, kResident, kTasks>;
-    if (lds > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-        if (e != hipSuccess) return e;
-    }
+    constexpr auto kernel = &int4_gemv_kernel<F, NG, kRt, MI, kResident, kTasks>;
+    const hipError_t e = allow_lds<kernel>(lds);
+    if (e != hipSuccess) return e;
     kernel<<<dim3((unsigned)grid), dim3(kThreads), lds, s>>>(g);
     return hipGetLastError();
 }
@@ -190,11 +186,12 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             kmax = std::max(kmax, st->cols);
             ++n;
         }
-        // two workgroups per CU, dealt to the tasks by their work, at most one per item
+        const int per_cu = resident && resident_lds(M, ng, kmax) > kLdsBytes / 2 ? 1 : 2;
+        // the workgroups that the CUs hold at a time, dealt to the tasks by their work, at most one per item
         int64_t grid = 0;
         for (int32_t i = 0; i < n; ++i) {
             Int4Task& t = g.t[i];
-            const double part = 2.0 * device_cu_count() * ((double)tiles[i] * (double)t.K / work);
+            const double part = (double)per_cu * device_cu_count() * ((double)tiles[i] * (double)t.K / work);
             int64_t wgs = std::max<int64_t>(1, std::min<int64_t>(items_of[i], (int64_t)(part + 0.5)));
             // a workgroup's rows stay under 2 GB of codes (and of scales: at most two bytes for 16 of codes)
             wgs = std::max(wgs, (int64_t)((double)(tiles[i] + 1) * 16 * (double)t.w.stride / (1 << 30)) + 1);

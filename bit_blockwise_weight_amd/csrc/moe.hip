@@ -6,10 +6,9 @@
 // with the weights of all experts stacked in two quantized tensors, gate and up rows of an
 // expert one after the other in the first.
 //
-//   moe_route_kernel    one workgroup: each wave selects one token's experts, then the
-//                       experts that have a token are listed in increasing order, each with
-//                       its tokens, their weights and their pairs (token, position).
-//   moe_up_kernel       items of 16 rows of gate and the same 16 of up of a listed expert
+//   moe_up_kernel       routes first: selects each token's experts and lists the experts
+//                       that have a token in increasing order, each with its tokens, their
+//                       weights and their pairs (token, position).  Then items of 16 rows of gate and the same 16 of up of a listed expert
 //                       (RowTiles, w4_tile.h), dealt in equal shares; only the expert's own
 //                       tokens are staged.  h is written in fp32.
 //   moe_down_kernel     items of rows of Wd of a listed expert times its tokens' h, which enters
@@ -31,19 +30,22 @@ using namespace w4;
 constexpr int kMaxT = 16;
 constexpr int kMaxE = 256;
 constexpr int kMaxK = 16;
+constexpr int kMaxPairs = kMaxT * kMaxK;
 constexpr int kThreads = 512;
 
-// Routing result, in the workspace.
+// Routing result: the experts that have a token, in increasing order, and their tokens, in increasing
+// order, one after the other.
 struct Routes {
     int32_t nactive;
     int32_t pad[3];
-    int32_t chosen[kMaxT];            // experts of each token (its positions 0, 1, ... are taken)
-    int32_t expert[kMaxE];            // listed experts, increasing
-    int32_t count[kMaxE];             // tokens of each
-    uint8_t tok[kMaxE][kMaxT];        // those tokens, increasing
-    uint8_t pair[kMaxE][kMaxT];       // their pairs: t * top_k + position
-    float w[kMaxE][kMaxT];            // their weights
+    int32_t chosen[kMaxT];                // experts of each token (its positions 0, 1, ... are taken)
+    int32_t expert[kMaxE];
+    int32_t start[kMaxE + 4];             // first entry of each listed expert below; one more ends the last
+    float w[kMaxPairs];                   // weight of the entry
+    uint8_t tok[kMaxPairs];               // its token
+    uint8_t pair[kMaxPairs];              // its row of h: t * top_k + position
 };
+static_assert(sizeof(Routes) % 16 == 0);
 
 struct RouteArgs {
     const void* logits;
@@ -51,7 +53,7 @@ struct RouteArgs {
     int32_t T, E, top_k, renorm;
 };
 
-__device__ __forceinline__ float load_logit(const void* p, int32_t dtype, int64_t i) {
+__device__ __forceinline__ float load_logit(const void* p, int32_t dtype, int i) {
     float v;
     if (dtype == QK_F32) v = static_cast<const float*>(p)[i];
     else if (dtype == QK_F16) v = f16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
@@ -59,94 +61,111 @@ __device__ __forceinline__ float load_logit(const void* p, int32_t dtype, int64_
     return v == v ? v : -INFINITY;                       // a NaN logit is never chosen
 }
 
-__global__ __launch_bounds__(kMaxT * 64) void moe_route_kernel(RouteArgs a, Routes* out) {
-    __shared__ int ids[kMaxT][kMaxK];
-    __shared__ float wt[kMaxT][kMaxK];
-    __shared__ uint32_t mask[kMaxE];
-    __shared__ int wcount[4];
-    const int tid = threadIdx.x, lane = tid & 63, t = tid >> 6;
-    if (tid < kMaxE) mask[tid] = 0;
+// Scratch of route(), in LDS.
+struct RouteScratch {
+    float logit[kMaxT][kMaxE + 16];
+    float best[kMaxT][kMaxK];             // the chosen logits by position, -inf behind the last
+    uint8_t who[kMaxT][kMaxK];            // and their experts
+    float den[kMaxT];
+    uint32_t mask[kMaxE];                 // tokens of each expert
+    int32_t slot[kMaxE];                  // its place in the list
+    int32_t waves[8][2];
+};
+
+// Fills r (LDS) from the logits, by one workgroup of kThreads.  Every logit's rank among its token's is counted
+// at once (how many are larger, or equal with a lower index): the rank is the position, so the choice takes no
+// rounds that wait for each other.  The loops stay rolled: the code runs once, and fetching it is most of its time.
+__device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Routes& r) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int padded = (a.E + 15) & ~15;
+#pragma unroll 1
+    for (int t = wave; t < a.T; t += 8)
+#pragma unroll 1
+        for (int e = lane; e < padded; e += 64) s.logit[t][e] = e < a.E ? load_logit(a.logits, a.dtype, t * a.E + e) : -INFINITY;
+    if (tid < kMaxE) s.mask[tid] = 0;
+    if (tid < kMaxT * kMaxK) s.best[tid / kMaxK][tid % kMaxK] = -INFINITY;
     __syncthreads();
-    if (t < a.T) {
-        float v[4];
-        float top = -INFINITY;
+#pragma unroll 1
+    for (int i = tid; i < a.T * a.E; i += kThreads) {
+        const int t = i / a.E, e = i - t * a.E;
+        const float v = s.logit[t][e];
+        int rank = 0;
+#pragma unroll 1
+        for (int j = 0; j < padded; j += 16) {
+            float o[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = lane + 64 * i;
-            v[i] = e < a.E ? load_logit(a.logits, a.dtype, (int64_t)t * a.E + e) : -INFINITY;
-            top = fmaxf(top, v[i]);
+            for (int q = 0; q < 16; ++q) o[q] = s.logit[t][j + q];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) rank += (o[q] > v) | ((o[q] == v) & (j + q < e));
         }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+        if (rank < a.top_k && v != -INFINITY) {
+            s.best[t][rank] = v;
+            s.who[t][rank] = (uint8_t)e;
+            atomicOr(&s.mask[e], 1u << t);
+        }
+    }
+    __syncthreads();
+    // the denominators: a wave per token
+#pragma unroll 1
+    for (int t = wave; t < a.T; t += 8) {
+        const float top = s.best[t][0];
+        const float* from = a.renorm ? s.best[t] : s.logit[t];
+        const int n = a.renorm ? a.top_k : a.E;
         float den = 0.0f;
-        if (!a.renorm) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (v[i] != -INFINITY) den += expf(v[i] - top);
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) den += __shfl_xor(den, d);
-        }
-        float mine = 0.0f;                               // lane k: weight of the k-th choice
-        int id = -1, k = 0;
-        for (; k < a.top_k; ++k) {
-            float best = v[0];
-            int e = lane;
-#pragma unroll
-            for (int i = 1; i < 4; ++i)
-                if (v[i] > best) {
-                    best = v[i];
-                    e = lane + 64 * i;
-                }
-            float m = best;
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-            if (m == -INFINITY) break;                   // nothing left that may be chosen
-            int c = best == m ? e : kMaxE;
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) c = min(c, __shfl_xor(c, d));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (c == lane + 64 * i) v[i] = -INFINITY;
-            const float p = expf(m - top);
-            if (a.renorm) den += p;
-            if (lane == k) {
-                mine = p;
-                id = c;
-            }
-        }
-        if (lane == 0) out->chosen[t] = k;
-        if (lane < a.top_k) {
-            ids[t][lane] = id;
-            wt[t][lane] = id >= 0 ? mine / den : 0.0f;
-            if (id >= 0) atomicOr(&mask[id], 1u << t);
-        }
+#pragma unroll 1
+        for (int i = lane; i < n; i += 64) den += from[i] == -INFINITY ? 0.0f : expf(from[i] - top);
+#pragma unroll 1
+        for (int d = 32; d > 0; d >>= 1) den += __shfl_xor(den, d);
+        if (lane == 0) s.den[t] = den;
     }
-    __syncthreads();
-    const uint32_t mk = tid < kMaxE ? mask[tid] : 0u;
+    // the list: thread e, an exclusive scan over the experts
+    const uint32_t mk = tid < kMaxE ? s.mask[tid] : 0u;
     const unsigned long long bal = __ballot(mk != 0);
-    if (tid < kMaxE && lane == 0) wcount[t] = __popcll(bal);
+    int sum = __popc(mk);
+#pragma unroll 1
+    for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(sum, d);
+        if (lane >= d) sum += up;
+    }
+    if (lane == 63) {
+        s.waves[wave][0] = __popcll(bal);
+        s.waves[wave][1] = sum;
+    }
     __syncthreads();
-    if (tid >= kMaxE) return;
-    int rank = __popcll(bal & ((1ull << lane) - 1));
-    int total = 0;
-    for (int w = 0; w < 4; ++w) {
-        if (w < t) rank += wcount[w];
-        total += wcount[w];
+    int slot = __popcll(bal & ((1ull << lane) - 1)), first = sum - __popc(mk), total = 0, entries = 0;
+#pragma unroll 1
+    for (int w = 0; w < kMaxE / 64; ++w) {
+        if (w < wave) {
+            slot += s.waves[w][0];
+            first += s.waves[w][1];
+        }
+        total += s.waves[w][0];
+        entries += s.waves[w][1];
     }
-    if (tid == 0) out->nactive = total;
-    if (!mk) return;
-    out->expert[rank] = tid;
-    out->count[rank] = __popc(mk);
-    int pos = 0;
-    for (uint32_t left = mk; left; left &= left - 1, ++pos) {
-        const int tt = __ffs((int)left) - 1;
-        for (int k = 0; k < a.top_k; ++k)
-            if (ids[tt][k] == tid) {
-                out->tok[rank][pos] = (uint8_t)tt;
-                out->pair[rank][pos] = (uint8_t)(tt * a.top_k + k);
-                out->w[rank][pos] = wt[tt][k];
-            }
+    if (tid == 0) {
+        r.nactive = total;
+        r.start[total] = entries;
     }
+    if (mk) {
+        r.expert[slot] = tid;
+        r.start[slot] = first;
+        s.slot[tid] = first;
+    }
+    if (tid < a.T) {
+        int n = 0;
+#pragma unroll 1
+        while (n < a.top_k && s.best[tid][n] != -INFINITY) ++n;
+        r.chosen[tid] = n;
+    }
+    __syncthreads();
+    const int t = tid / kMaxK, k = tid % kMaxK;
+    if (t < a.T && k < a.top_k && s.best[t][k] != -INFINITY) {
+        const int e = s.who[t][k], at = s.slot[e] + __popc(s.mask[e] & ((1u << t) - 1));
+        r.tok[at] = (uint8_t)t;
+        r.pair[at] = (uint8_t)(t * a.top_k + k);
+        r.w[at] = expf(s.best[t][k] - s.best[t][0]) / s.den[t];
+    }
+    __syncthreads();
 }
 
 // A weight view of either form.
@@ -175,25 +194,36 @@ struct ExpertArgs {
     int32_t x_bufs;
 };
 
-// Workgroups per CU: the level table takes 64 KB of its LDS.
+// Workgroups per CU, at most: the level table takes 64 KB of its LDS.
 template <int F>
 constexpr int kPerCu = F == kLevels ? 1 : 2;
+template <int F>
+int64_t workgroups(int64_t items, size_t lds) {
+    return std::min<int64_t>(items, (lds > kLdsBytes / 2 ? 1 : kPerCu<F>) * device_cu_count());
+}
 // The activations of a whole row stay in LDS where all of them fit.
 template <int F, int NG, int RT, int MI>
 bool fits(int rows, int64_t K) {
-    return (F == kLevels ? kTabBytes : 0) + w4_fixed_bytes(NG, RT, MI) + w4_x_bytes(8, rows, K, true, 1) <=
-           kLdsBytes / kPerCu<F>;
+    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes(NG, RT, MI) +
+               w4_x_bytes(8, rows, K, true, 1) <= kLdsBytes;
 }
 
 template <int F, int NG, int MI, bool kResident>
-__global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertArgs<F> p) {
+__global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertArgs<F> p, RouteArgs ra, Routes* keep) {
     extern __shared__ __align__(16) uint8_t lds[];
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
-    uint8_t* work = lds + (F == kLevels ? kTabBytes : 0);
+    uint8_t* work = lds + (F == kLevels ? kTabBytes : 0) + sizeof(Routes);
+    static_assert(sizeof(RouteScratch) <= Tiles::kFixedBytes);
+    // Every workgroup routes for itself (a launch of its own would cost more); the first one keeps the result.
+    Routes& routes = *reinterpret_cast<Routes*>(lds + (F == kLevels ? kTabBytes : 0));
+    route(ra, *reinterpret_cast<RouteScratch*>(work), routes);
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < (int)(sizeof(Routes) / 4); i += kThreads)
+            reinterpret_cast<uint32_t*>(keep)[i] = reinterpret_cast<const uint32_t*>(&routes)[i];
     if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads);
     // an item: per row group 16 rows of gate and the same of up of one listed expert; equal shares of the items
     const int step = 128 >> p.kwl;
-    const uint32_t tiles = (uint32_t)(p.Ipad + step - 1) / step, all = tiles * p.routes->nactive;
+    const uint32_t tiles = (uint32_t)(p.Ipad + step - 1) / step, all = tiles * (uint32_t)routes.nactive;
     const uint32_t share = all / p.grid, more = all % p.grid, b = blockIdx.x;
     uint32_t lo = b * share + (b < more ? b : more);
     const uint32_t hi = lo + share + (b < more);
@@ -201,8 +231,8 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertA
         const int a = (int)(lo / tiles);
         const int i0 = (int)(lo - a * tiles), i1 = (int)(hi - a * tiles < tiles ? hi - a * tiles : tiles);
         lo += i1 - i0;
-        const int count = p.routes->count[a];
-        const int64_t e = p.routes->expert[a];
+        const int first = routes.start[a], count = routes.start[a + 1] - first;
+        const int64_t e = routes.expert[a];
         Rows<2> r;
         r.base[0] = e * 2 * p.I;
         r.base[1] = r.base[0] + p.I;
@@ -219,7 +249,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertA
         // 4 MI tokens at a time (an expert rarely has more)
         for (int m0 = 0; m0 < count; m0 += 4 * MI) {
             const int M = count - m0 < 4 * MI ? count - m0 : 4 * MI;
-            r.xrow = p.routes->tok[a] + m0;
+            r.xrow = routes.tok + first + m0;
             r.M = M;
             Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, int q, const float* put) {
 #pragma unroll
@@ -229,7 +259,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertA
                     if (m < M && i < p.Ipad) {
                         const float gate = Tiles::sum(put, p.kwl, q, 0, s), up = Tiles::sum(put, p.kwl, q, 1, s);
                         const float v = gate / (1.0f + expf(-gate)) * up;
-                        p.out[(int64_t)p.routes->pair[a][m0 + m] * p.Ipad + i] = i < p.I ? v : 0.0f;
+                        p.out[(int64_t)routes.pair[first + m0 + m] * p.Ipad + i] = i < p.I ? v : 0.0f;
                     }
                 }
             });
@@ -244,7 +274,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(Exper
     uint8_t* work = lds + (F == kLevels ? kTabBytes : 0);
     if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads);
     const int step = (16 * RT * 8) >> p.kwl;
-    const uint32_t tiles = (uint32_t)(p.H + step - 1) / step, all = tiles * p.routes->nactive;
+    const uint32_t tiles = (uint32_t)(p.H + step - 1) / step, all = tiles * (uint32_t)p.routes->nactive;
     const uint32_t share = all / p.grid, more = all % p.grid, b = blockIdx.x;
     uint32_t lo = b * share + (b < more ? b : more);
     const uint32_t hi = lo + share + (b < more);
@@ -252,7 +282,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(Exper
         const int a = (int)(lo / tiles);
         const int i0 = (int)(lo - a * tiles), i1 = (int)(hi - a * tiles < tiles ? hi - a * tiles : tiles);
         lo += i1 - i0;
-        const int count = p.routes->count[a];
+        const int first = p.routes->start[a], count = p.routes->start[a + 1] - first;
         Rows<RT> r;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
@@ -272,7 +302,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(Exper
         // two activation rows a token
         for (int m0 = 0; m0 < count; m0 += 2 * MI) {
             const int M = count - m0 < 2 * MI ? count - m0 : 2 * MI;
-            r.xrow = p.routes->pair[a] + m0;
+            r.xrow = p.routes->pair + first + m0;
             r.M = M;
             Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, int q, const float* put) {
                 for (int o = threadIdx.x & 63; o < M * (16 * RT); o += 64) {
@@ -280,7 +310,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(Exper
                     const int n = item * step + q * (16 * RT) + row;
                     const float v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m)) +
                                     Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m + 1));
-                    if (n < p.H) p.out[(int64_t)p.routes->pair[a][m0 + m] * p.H + n] = v * p.routes->w[a][m0 + m];
+                    if (n < p.H) p.out[(int64_t)p.routes->pair[first + m0 + m] * p.H + n] = v * p.routes->w[first + m0 + m];
                 }
             });
         }
@@ -299,41 +329,38 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* parts, co
     y[t * H + n] = float_to_bits16(v, f16);
 }
 
-template <class K>
-hipError_t allow_lds(K kernel, size_t lds) {
-    if (lds <= 65536) return hipSuccess;
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-}
 
 // rows: activation rows that a pass stages at most
 template <int F, int NG, int MI, bool kResident>
-hipError_t launch_up_one(ExpertArgs<F> p, int rows, int32_t listed, hipStream_t s) {
+hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int rows, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
     p.kwl = kResident ? w4_kwl(p.H) : 2;
     p.x_bufs = 2;
-    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, rows, p.H, kResident, 2);
-    const hipError_t e = allow_lds(&moe_up_kernel<F, NG, MI, kResident>, lds);
+    const size_t lds = (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + Tiles::kFixedBytes +
+                       w4_x_bytes(1 << p.kwl, rows, p.H, kResident, 2);
+    const hipError_t e = allow_lds<&moe_up_kernel<F, NG, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
     const int64_t items = (int64_t)(p.Ipad + (128 >> p.kwl) - 1) / (128 >> p.kwl) * listed;
-    p.grid = (uint32_t)std::min<int64_t>(items, kPerCu<F> * device_cu_count());
-    moe_up_kernel<F, NG, MI, kResident><<<dim3(p.grid), dim3(kThreads), lds, s>>>(p);
+    p.grid = (uint32_t)workgroups<F>(items, lds);
+    moe_up_kernel<F, NG, MI, kResident><<<dim3(p.grid), dim3(kThreads), lds, s>>>(p, ra, keep);
     return hipGetLastError();
 }
 
 template <int F, int NG, int MI>
-hipError_t launch_up_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hipStream_t s) {
-    const int rows = std::min(T, 4 * MI);
-    if (fits<F, NG, 2, MI>(rows, p.H)) return launch_up_one<F, NG, MI, true>(p, rows, listed, s);
-    return launch_up_one<F, NG, MI, false>(p, rows, listed, s);
+hipError_t launch_up_mi(const ExpertArgs<F>& p, const RouteArgs& ra, Routes* keep, int32_t listed, hipStream_t s) {
+    const int rows = std::min(ra.T, 4 * MI);
+    if (fits<F, NG, 2, MI>(rows, p.H)) return launch_up_one<F, NG, MI, true>(p, ra, keep, rows, listed, s);
+    return launch_up_one<F, NG, MI, false>(p, ra, keep, rows, listed, s);
 }
 
 // Tokens that a pass over an expert's rows takes (4 MI): by the number that it has on average.
 template <int F, int NG>
-hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, hipStream_t s) {
+hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int32_t listed, hipStream_t s) {
+    const RouteArgs ra{m.logits, m.logits_dtype, m.T, m.E, m.top_k, m.renorm};
     const int pairs = m.T * m.top_k;
-    if (m.T <= 4 || pairs <= 2 * m.E) return launch_up_mi<F, NG, 1>(p, m.T, listed, s);
-    if (F == kLevels || m.T <= 8 || pairs <= 5 * m.E) return launch_up_mi<F, NG, 2>(p, m.T, listed, s);
-    return launch_up_mi<F, NG, F == kLevels ? 2 : 4>(p, m.T, listed, s);
+    if (m.T <= 4 || pairs <= 2 * m.E) return launch_up_mi<F, NG, 1>(p, ra, keep, listed, s);
+    if (F == kLevels || m.T <= 8 || pairs <= 5 * m.E) return launch_up_mi<F, NG, 2>(p, ra, keep, listed, s);
+    return launch_up_mi<F, NG, F == kLevels ? 2 : 4>(p, ra, keep, listed, s);
 }
 
 template <int F, int NG, int RT, int MI, bool kResident>
@@ -342,10 +369,10 @@ hipError_t launch_down_one(ExpertArgs<F> p, int rows, int32_t listed, hipStream_
     p.kwl = kResident ? w4_kwl(p.I) : 2;
     p.x_bufs = 2;
     const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, rows, p.I, kResident, 2);
-    const hipError_t e = allow_lds(&moe_down_kernel<F, NG, RT, MI, kResident>, lds);
+    const hipError_t e = allow_lds<&moe_down_kernel<F, NG, RT, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
     const int64_t step = (16 * RT * 8) >> p.kwl, items = (p.H + step - 1) / step * listed;
-    p.grid = (uint32_t)std::min<int64_t>(items, kPerCu<F> * device_cu_count());
+    p.grid = (uint32_t)workgroups<F>(items, lds);
     moe_down_kernel<F, NG, RT, MI, kResident><<<dim3(p.grid), dim3(kThreads), lds, s>>>(p);
     return hipGetLastError();
 }
@@ -417,15 +444,9 @@ hipError_t launch_up_int4(const MoeItem& m, const Buffers& b, const qk_int4_stat
     ExpertArgs<F> p = expert_args<F>(m, b, true);
     p.w = int4_view(w);
     const int ng = int4_groups_per_chunk(w->group);
-    if (ng == 4) return launch_up<F, 4>(p, m, listed, s);
-    if (ng == 2) return launch_up<F, 2>(p, m, listed, s);
-    return launch_up<F, 1>(p, m, listed, s);
-}
-
-hipError_t launch_route(const MoeItem& m, const Buffers& b, hipStream_t s) {
-    RouteArgs r{m.logits, m.logits_dtype, m.T, m.E, m.top_k, m.renorm};
-    moe_route_kernel<<<dim3(1), dim3(kMaxT * 64), 0, s>>>(r, b.routes);
-    return hipGetLastError();
+    if (ng == 4) return launch_up<F, 4>(p, m, b.routes, listed, s);
+    if (ng == 2) return launch_up<F, 2>(p, m, b.routes, listed, s);
+    return launch_up<F, 1>(p, m, b.routes, listed, s);
 }
 
 hipError_t launch_combine(const MoeItem& m, const Buffers& b, hipStream_t s) {
@@ -444,9 +465,7 @@ hipError_t launch_moe_int4(const MoeItem& m, const qk_int4_state* gate_up, const
                            hipStream_t s) {
     const Buffers b = buffers(m, workspace);
     const int32_t listed = std::min(m.E, m.T * m.top_k);
-    hipError_t e = launch_route(m, b, s);
-    if (e != hipSuccess) return e;
-    e = m.f16 ? launch_up_int4<kInt4F16>(m, b, gate_up, listed, s) : launch_up_int4<kInt4Bf16>(m, b, gate_up, listed, s);
+    hipError_t e = m.f16 ? launch_up_int4<kInt4F16>(m, b, gate_up, listed, s) : launch_up_int4<kInt4Bf16>(m, b, gate_up, listed, s);
     if (e != hipSuccess) return e;
     ExpertArgs<kInt4Bf16> p = expert_args<kInt4Bf16>(m, b, false);
     p.w = int4_view(down);
@@ -461,11 +480,9 @@ hipError_t launch_moe_levels(const MoeItem& m, const MatArgs& gate_up, const Mat
                              hipStream_t s) {
     const Buffers b = buffers(m, workspace);
     const int32_t listed = std::min(m.E, m.T * m.top_k);
-    hipError_t e = launch_route(m, b, s);
-    if (e != hipSuccess) return e;
     ExpertArgs<kLevels> u = expert_args<kLevels>(m, b, true);
     u.w = levels_view(gate_up);
-    e = launch_up<kLevels, 2>(u, m, listed, s);
+    hipError_t e = launch_up<kLevels, 2>(u, m, b.routes, listed, s);
     if (e != hipSuccess) return e;
     ExpertArgs<kLevels> d = expert_args<kLevels>(m, b, false);
     d.w = levels_view(down);

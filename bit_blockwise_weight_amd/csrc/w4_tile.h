@@ -32,6 +32,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qk_device.h"
 #include "qk_internal.h"
 
@@ -267,6 +269,22 @@ constexpr int w4_fixed_bytes(int NG, int RT, int MI) {
     return 8 * RT * 16 * ((2 * NG) | 1) * 8 + 8 * RT * 16 * 128 + w4_slots(MI) * (w4_put_bytes(RT, MI) + 32);
 }
 constexpr size_t kLdsBytes = 160 * 1024;  // of a CU
+
+// Lets a kernel use more than 64 KB of LDS: once per device.
+template <auto kKernel>
+hipError_t allow_lds(size_t lds) {
+    if (lds <= 65536) return hipSuccess;
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            (int)kLdsBytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // bytes of LDS that the activations take (rows: twice their number with kSplit)
 inline size_t w4_x_bytes(int kw, int rows, int64_t K, bool resident, int bufs) {

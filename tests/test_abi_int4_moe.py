@@ -79,7 +79,7 @@ def test_grouped_gemv_refusals(L):
         arr = (qk.GemvInt4Task * 2)()
         for i in range(2):
             arr[i].x, arr[i].y = xs[i], ys[i]
-            arr[i].st = ctypes.pointer(states[i]) if states[i] is not None else None
+            arr[i].st = ctypes.addressof(states[i]) if states[i] is not None else None
         return L.qk_gemv_int4_grouped(arr, n, qk.QK_F16, M, None)
 
     for bad in (dict(n=0), dict(n=257), dict(n=2, M=17), dict(n=2, ys=(Y, Y)), dict(n=2, ys=(Y, Y + 128)),
@@ -171,7 +171,12 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(L):
     with pytest.raises(ValueError):
         qk.qk_gemv_int4_grouped([])
     _, st = _init(L)
+    st._device, st._shape, st._address = torch.device("cuda", 0), (64, 128), ctypes.addressof(st)
     with pytest.raises(ValueError, match="bf16 or fp16"):
         qk.qk_gemv_int4(z((1, 128)), st)
     with pytest.raises(ValueError, match="128 columns"):
         qk.qk_gemv_int4(z((1, 64), dtype=torch.float16), st)
+    with pytest.raises(ValueError, match="HIP device"):
+        qk.qk_gemv_int4(z((1, 128), dtype=torch.float16), st)
+    with pytest.raises(ValueError, match="2 outputs"):
+        qk.qk_gemv_int4_grouped([(z((1, 128)), st)], [None, None])
