@@ -88,7 +88,10 @@ constexpr int kRt = 2;                                   // tiles of 16 rows per
 constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
 // The activations of a whole row stay in LDS where they fit.
-size_t resident_lds(int M, int ng, int64_t K) { return w4_fixed_bytes(ng, kRt, mi_for(M)) + w4_x_bytes(8, M, K, true, 1); }
+size_t x_lds(int M, int ng, int64_t K, bool resident) {
+    return mi_for(M) == 1 ? w4_fix_bytes(4, M, ng, K, resident, 2) : w4_x_bytes(4, M, K, resident, 2);
+}
+size_t resident_lds(int M, int ng, int64_t K) { return w4_fixed_bytes(ng, kRt, mi_for(M)) + x_lds(M, ng, K, true); }
 bool resident_for(int M, int ng, int64_t K) { return resident_lds(M, ng, K) <= kLdsBytes; }
 
 constexpr int32_t kNever = 0x7FFFFFFF;
@@ -106,7 +109,7 @@ template <int F, int NG, int MI, bool kResident>
 hipError_t launch_one(Int4Group<kMaxGemvTasks>& g, int64_t grid, int64_t kmax, hipStream_t s) {
     typedef RowTiles<F, NG, kRt, MI, kResident, false> Tiles;
     g.x_bufs = 2;
-    const size_t lds = Tiles::kFixedBytes + w4_x_bytes(4, g.M, kmax, kResident, 2);
+    const size_t lds = Tiles::kFixedBytes + x_lds(g.M, NG, kmax, kResident);
     if (g.wg0[1] == kNever) {
         Int4Group<1> one;
         one.wg0[0] = 0;

@@ -201,12 +201,21 @@ template <int F>
 int64_t workgroups(int64_t items, size_t lds) {
     return std::min<int64_t>(items, (lds > kLdsBytes / 2 ? 1 : kPerCu<F>) * device_cu_count());
 }
-// The activations of a whole row stay in LDS where all of them fit.
-template <int F, int NG, int RT, int MI>
-bool fits(int rows, int64_t K) {
-    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes(NG, RT, MI) +
-               w4_x_bytes(8, rows, K, true, 1) <= kLdsBytes;
+// LDS of the activations; those of a whole row stay there where all of them fit.
+template <int F, int NG, int MI>
+size_t x_lds(int tokens, bool split, int64_t K, bool resident) {
+    return F != kLevels && MI == 1 ? w4_fix_bytes(4, tokens, NG, K, resident, 2)
+                                   : w4_x_bytes(4, split ? 2 * tokens : tokens, K, resident, 2);
 }
+template <int F, int NG, int RT, int MI>
+bool fits(int tokens, bool split, int64_t K) {
+    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes(NG, RT, MI) + x_lds<F, NG, MI>(tokens, split, K, true) <=
+           kLdsBytes;
+}
+// Tokens that a pass over an expert's rows takes; the down product needs two operand rows for one, but not in fixed
+// point.
+template <int F, int MI, bool kSplit>
+constexpr int kTokens = kSplit && (F == kLevels || MI > 1) ? 2 * MI : 4 * MI;
 
 template <int F, int NG, int MI, bool kResident>
 __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertArgs<F> p, RouteArgs ra, Routes* keep) {
@@ -299,17 +308,21 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(Exper
         r.x_aligned = 1;
         r.kwl = p.kwl;
         r.x_bufs = p.x_bufs;
-        // two activation rows a token
-        for (int m0 = 0; m0 < count; m0 += 2 * MI) {
-            const int M = count - m0 < 2 * MI ? count - m0 : 2 * MI;
+        constexpr int kTok = kTokens<F, MI, true>;
+        for (int m0 = 0; m0 < count; m0 += kTok) {
+            const int M = count - m0 < kTok ? count - m0 : kTok;
             r.xrow = p.routes->pair + first + m0;
             r.M = M;
             Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, int q, const float* put) {
                 for (int o = threadIdx.x & 63; o < M * (16 * RT); o += 64) {
                     const int m = o / (16 * RT), row = o % (16 * RT), t = row / 16;
                     const int n = item * step + q * (16 * RT) + row;
-                    const float v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m)) +
-                                    Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m + 1));
+                    float v;
+                    if constexpr (Tiles::kFix)
+                        v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, m));
+                    else                                 // two operand rows a token
+                        v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m)) +
+                            Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m + 1));
                     if (n < p.H) p.out[(int64_t)p.routes->pair[first + m0 + m] * p.H + n] = v * p.routes->w[first + m0 + m];
                 }
             });
@@ -332,12 +345,12 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* parts, co
 
 // rows: activation rows that a pass stages at most
 template <int F, int NG, int MI, bool kResident>
-hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int rows, int32_t listed, hipStream_t s) {
+hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
     p.kwl = kResident ? w4_kwl(p.H) : 2;
     p.x_bufs = 2;
     const size_t lds = (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + Tiles::kFixedBytes +
-                       w4_x_bytes(1 << p.kwl, rows, p.H, kResident, 2);
+                       x_lds<F, NG, MI>(tokens, false, p.H, kResident);
     const hipError_t e = allow_lds<&moe_up_kernel<F, NG, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
     const int64_t items = (int64_t)(p.Ipad + (128 >> p.kwl) - 1) / (128 >> p.kwl) * listed;
@@ -348,9 +361,9 @@ hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int
 
 template <int F, int NG, int MI>
 hipError_t launch_up_mi(const ExpertArgs<F>& p, const RouteArgs& ra, Routes* keep, int32_t listed, hipStream_t s) {
-    const int rows = std::min(ra.T, 4 * MI);
-    if (fits<F, NG, 2, MI>(rows, p.H)) return launch_up_one<F, NG, MI, true>(p, ra, keep, rows, listed, s);
-    return launch_up_one<F, NG, MI, false>(p, ra, keep, rows, listed, s);
+    const int tokens = std::min(ra.T, kTokens<F, MI, false>);
+    if (fits<F, NG, 2, MI>(tokens, false, p.H)) return launch_up_one<F, NG, MI, true>(p, ra, keep, tokens, listed, s);
+    return launch_up_one<F, NG, MI, false>(p, ra, keep, tokens, listed, s);
 }
 
 // Tokens that a pass over an expert's rows takes (4 MI): by the number that it has on average.
@@ -364,11 +377,11 @@ hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int
 }
 
 template <int F, int NG, int RT, int MI, bool kResident>
-hipError_t launch_down_one(ExpertArgs<F> p, int rows, int32_t listed, hipStream_t s) {
+hipError_t launch_down_one(ExpertArgs<F> p, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, RT, MI, kResident, true> Tiles;
     p.kwl = kResident ? w4_kwl(p.I) : 2;
     p.x_bufs = 2;
-    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + w4_x_bytes(1 << p.kwl, rows, p.I, kResident, 2);
+    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + x_lds<F, NG, MI>(tokens, true, p.I, kResident);
     const hipError_t e = allow_lds<&moe_down_kernel<F, NG, RT, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
     const int64_t step = (16 * RT * 8) >> p.kwl, items = (p.H + step - 1) / step * listed;
@@ -379,17 +392,21 @@ hipError_t launch_down_one(ExpertArgs<F> p, int rows, int32_t listed, hipStream_
 
 template <int F, int NG, int MI>
 hipError_t launch_down_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hipStream_t s) {
-    const int rows = std::min(2 * T, 4 * MI);
-    if (!fits<F, NG, 2, MI>(rows, p.I)) return launch_down_one<F, NG, 2, MI, false>(p, rows, listed, s);
-    return launch_down_one<F, NG, 2, MI, true>(p, rows, listed, s);
+    const int tokens = std::min(T, kTokens<F, MI, true>);
+    if (!fits<F, NG, 2, MI>(tokens, true, p.I)) return launch_down_one<F, NG, 2, MI, false>(p, tokens, listed, s);
+    return launch_down_one<F, NG, 2, MI, true>(p, tokens, listed, s);
 }
 
 template <int F, int NG>
 hipError_t launch_down(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, hipStream_t s) {
     const int pairs = m.T * m.top_k;
-    if (m.T <= 2 || pairs <= m.E) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
-    if (F == kLevels || m.T <= 4 || 2 * pairs <= 5 * m.E) return launch_down_mi<F, NG, 2>(p, m.T, listed, s);
-    return launch_down_mi<F, NG, F == kLevels ? 2 : 4>(p, m.T, listed, s);
+    if constexpr (F == kLevels) {
+        if (m.T <= 2 || pairs <= m.E) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
+        return launch_down_mi<F, NG, 2>(p, m.T, listed, s);
+    } else {
+        if (m.T <= 4 || pairs <= 2 * m.E) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
+        return launch_down_mi<F, NG, 4>(p, m.T, listed, s);
+    }
 }
 
 LevelsView levels_view(const MatArgs& w) {

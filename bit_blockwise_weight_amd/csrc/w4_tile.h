@@ -44,6 +44,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
+typedef int32_t intx4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
@@ -146,6 +147,19 @@ __device__ __forceinline__ floatx4_t mfma(u32x4_t a, u32x4_t b, floatx4_t c) {
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                        __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Integer products of four dwords' 8 codes each, as bytes: 3 instructions a dword (the odd codes, then the even
+// ones; the activations' bytes are stored in that order).
+__device__ __forceinline__ intx4_t mfma_i8_64(u32x4_t a, uint32_t w0, uint32_t w1, intx4_t c) {
+    const u32x4_t b = {w0 & 0x0F0F0F0Fu, (w0 >> 4) & 0x0F0F0F0Fu, w1 & 0x0F0F0F0Fu, (w1 >> 4) & 0x0F0F0F0Fu};
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(intx4_t, a), __builtin_bit_cast(intx4_t, b), c, 0, 0,
+                                                 0);
+}
+__device__ __forceinline__ intx4_t mfma_i8_32(uint32_t a0, uint32_t a1, uint32_t w, intx4_t c) {
+    const uint64_t a = a0 | ((uint64_t)a1 << 32);
+    const uint64_t b = (w & 0x0F0F0F0Fu) | ((uint64_t)((w >> 4) & 0x0F0F0F0Fu) << 32);
+    return __builtin_amdgcn_mfma_i32_16x16x32_i8((long)a, (long)b, c, 0, 0, 0);
 }
 
 // A fragment of ones, and what the stored codes exceed q by.
@@ -264,7 +278,7 @@ constexpr int kLineK = 256;               // k of a 128-byte line of codes
 
 // bytes of LDS beside the activations: scales, codes, partial sums of a few items and their counters
 constexpr int w4_put_bytes(int RT, int MI) { return 8 * RT * 64 * MI * 4; }
-constexpr int w4_slots(int MI) { return MI == 1 ? 4 : 2; }
+constexpr int w4_slots(int) { return 2; }
 constexpr int w4_fixed_bytes(int NG, int RT, int MI) {
     return 8 * RT * 16 * ((2 * NG) | 1) * 8 + 8 * RT * 16 * 128 + w4_slots(MI) * (w4_put_bytes(RT, MI) + 32);
 }
@@ -286,10 +300,15 @@ hipError_t allow_lds(size_t lds) {
     return e;
 }
 
-// bytes of LDS that the activations take (rows: twice their number with kSplit)
+// bytes of LDS that the activations take: rows of 16-bit values (two an activation with kSplit), or M
+// activations in fixed point, three bytes a value and a pair per scale group (NG of them in a chunk)
 inline size_t w4_x_bytes(int kw, int rows, int64_t K, bool resident, int bufs) {
     const size_t k = (size_t)((K + kLineK - 1) / kLineK) * kLineK;
     return resident ? (size_t)rows * (k * 2 + 16) : (size_t)bufs * rows * ((size_t)kw * kLineK * 2 + 16);
+}
+inline size_t w4_fix_bytes(int kw, int M, int NG, int64_t K, bool resident, int bufs) {
+    const size_t k = resident ? (size_t)((K + kLineK - 1) / kLineK) * kLineK : (size_t)kw * kLineK;
+    return (resident ? 1 : bufs) * (size_t)M * (3 * (k + 16) + k / kChunk * NG * 8);
 }
 // log2 of the waves (of 8) that split a row of K: as many as it has lines
 inline int w4_kwl(int64_t K) {
@@ -301,6 +320,7 @@ template <int F, int NG, int RT, int MI, bool kResident, bool kSplit>
 struct RowTiles {
     static constexpr int W = 8;
     static constexpr int kThreads = W * 64;
+    static constexpr bool kFix = F != kLevels && MI == 1;       // up to four activations, in fixed point
     static constexpr int U = 2;                                 // chunks of a wave in a window
     static constexpr int kMfmas = 4 / NG;                       // MFMAs per scale group
     static constexpr int kEntries = U * NG;                     // scale groups of a wave's chunks in a window
@@ -311,7 +331,7 @@ struct RowTiles {
     static constexpr int kPutBytes = w4_put_bytes(RT, MI);
     static constexpr int kSlots = w4_slots(MI);
     // units of x per thread and batch; a window's fit one batch (kw <= 4)
-    static constexpr int kXUnits = kResident ? 2 : kSplit ? (MI + 1) / 2 : MI;
+    static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : kSplit ? (MI + 1) / 2 : MI;
     static constexpr int kFixedBytes = w4_fixed_bytes(NG, RT, MI);
     static_assert(kFixedBytes == kScaleBytes + kCodeBytes + kSlots * (kPutBytes + 32));
 
@@ -336,18 +356,19 @@ struct RowTiles {
         uint8_t* xlds = lds + kFixedBytes;
         const int nchunk = (p.K + kChunk - 1) / kChunk;
         const int wchunks = kw * U;
-        const int win_pitch = wchunks * (kChunk * 2) + 16;
-        const int xpitch = kResident ? (nchunk + U - 1) / U * (U * kChunk * 2) + 16 : win_pitch;
-        const int xrows = kSplit ? 2 * p.M : p.M;
+        const int xchunks = kResident ? (nchunk + U - 1) / U * U : wchunks;   // chunks of x that LDS holds
+        const int xpitch = xchunks * (kFix ? kChunk : 2 * kChunk) + 16;
+        const int xrows = kFix ? 3 * p.M : kSplit ? 2 * p.M : p.M;
+        const int xbytes = xrows * xpitch + (kFix ? p.M * xchunks * (NG * 8) : 0);
         const Magic magic(F == kInt4F16);
         float mean = 0.0f, zbias = 0.0f;
         if constexpr (F == kLevels) mean = w.nested ? *w.dq_mean : 0.0f;
-        else zbias = kCodeBias<F> + (w.zeros ? 0.0f : 8.0f);
+        else zbias = (kFix ? 0.0f : kCodeBias<F>) + (w.zeros ? 0.0f : 8.0f);
         const __amdgpu_buffer_rsrc_t xbuf = buffer(p.x, (int64_t)p.x_rows * p.x_pitch * (kSplit ? 4 : 2));
 
         // Staging of activations, thread by thread, rows as if they had 2^ush units of 8 values.  Rows that
         // cannot be read 16 bytes at a time are read element by element when they are stored.
-        const int units = (kResident ? (nchunk + U - 1) / U * U : wchunks) * (kChunk / 8);
+        const int units = xchunks * (kChunk / 8);
         const int ush = 32 - __builtin_clz(units - 1);
         const int total = p.M << ush;
         u32x4_t xr[kXUnits][kSplit ? 2 : 1];
@@ -364,7 +385,88 @@ struct RowTiles {
         };
         // Every thread stores (what lies outside, to the 16 bytes behind row 0, which nobody reads): under a
         // condition the compiler would move the loads down to it, behind those of the codes.
+        // Fixed point: with e the exponent of the largest |x| of a chunk (16 lanes hold it), X = RN(x 2^(21 - e)) is
+        // an integer of 23 bits, kept as three signed bytes, X = b0 2^16 + b1 2^8 + b2; products with the codes
+        // are then exact int32 sums.  The rounding, at most 2^-22 of the chunk's largest value, is the size of
+        // the rounding of an fp32 sum that holds that value.
+        auto x_store_fix = [&](uint8_t* dst, int base, int k0) {
+#pragma unroll 1
+            for (int b = 0; b < kXUnits; ++b) {
+                const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
+                const bool in = i < total && u < units;
+                float v[8];
+                if constexpr (kSplit) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = as_float(xr[b][q >> 2][q & 3]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t d = xr[b][0][q];
+                        if (!p.x_aligned) {
+                            const uint16_t* src =
+                                static_cast<const uint16_t*>(p.x) + (int64_t)(in && p.xrow ? p.xrow[m] : m) * p.x_pitch + k;
+                            const uint32_t lo = in && k + 2 * q < p.K ? src[2 * q] : 0u;
+                            const uint32_t hi = in && k + 2 * q + 1 < p.K ? src[2 * q + 1] : 0u;
+                            d = lo | (hi << 16);
+                        }
+                        if constexpr (F == kInt4F16) {
+                            v[2 * q] = f16_bits_to_float((uint16_t)d);
+                            v[2 * q + 1] = f16_bits_to_float((uint16_t)(d >> 16));
+                        } else {
+                            v[2 * q] = bf16_lo(d);
+                            v[2 * q + 1] = bf16_hi(d);
+                        }
+                    }
+                }
+                uint32_t big = 0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) big = max(big, as_uint(v[q]) & 0x7FFFFFFFu);
+                const uint32_t e = max(group_max_u32<16>(big) >> 23, 27u);      // below 2^-100: lost against 2^-121
+                const float up = as_float((148u + 127u - e) << 23);             // 2^(21 - (e - 127))
+                int32_t X[8], sum = 0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    X[q] = (int32_t)rintf(v[q] * up);
+                    sum += X[q];
+                }
+                // sums over a scale group (or a chunk): 4, 8 or 16 lanes
+#pragma unroll
+                for (int d = 1; d < 16 / NG; d <<= 1) sum += __shfl_xor(sum, d);
+                u32x2_t d0, d1, d2;
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {                    // the odd values, then the even ones
+                    const int32_t* q = X;
+                    uint32_t c[3][4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int32_t x2 = q[2 * t + 1 - o], x1 = (x2 + 128) >> 8, x0 = (x1 + 128) >> 8;
+                        c[0][t] = (uint32_t)x0;
+                        c[1][t] = (uint32_t)x1;
+                        c[2][t] = (uint32_t)x2;
+                    }
+#pragma unroll
+                    for (int pl = 0; pl < 3; ++pl) {
+                        const uint32_t ab = __builtin_amdgcn_perm(c[pl][1], c[pl][0], 0x0C0C0400u);
+                        const uint32_t cd = __builtin_amdgcn_perm(c[pl][3], c[pl][2], 0x04000C0Cu);
+                        (pl == 0 ? d0 : pl == 1 ? d1 : d2)[o] = ab | cd;
+                    }
+                }
+                const int at = in ? 3 * m * xpitch + 8 * u : xpitch - 16, row = in ? xpitch : 0;
+                *reinterpret_cast<u32x2_t*>(dst + at) = d0;
+                *reinterpret_cast<u32x2_t*>(dst + at + row) = d1;
+                *reinterpret_cast<u32x2_t*>(dst + at + 2 * row) = d2;
+                if (in && (lane & (16 / NG - 1)) == 0) {         // (2^(e - 21), sum); an infinity or a NaN makes its row NaN
+                    const float down = e == 255 ? __builtin_nanf("") : as_float((e + 127u - 148u) << 23);
+                    reinterpret_cast<floatx2_t*>(dst + 3 * p.M * xpitch)[m * (xchunks * NG) + (u * NG >> 4)] =
+                        (floatx2_t){down, (float)sum};
+                }
+            }
+        };
         auto x_store = [&](uint8_t* dst, int base, int k0) {
+            if constexpr (kFix) {
+                x_store_fix(dst, base, k0);
+                return;
+            }
 #pragma unroll
             for (int b = 0; b < kXUnits; ++b) {
                 const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1);
@@ -486,18 +588,76 @@ struct RowTiles {
                     } else {
                         const uint16_t bits = (uint16_t)as_uint(f.s[r][b]);
                         v[0] = w.scale_f16 ? f16_bits_to_float(bits) : bf16_bits_to_float(bits);
-                        v[1] = v[0] * ((float)f.z[r][b] + zbias);
+                        v[1] = (float)f.z[r][b] + zbias;
+                        if constexpr (!kFix) v[1] *= v[0];
                     }
                     if (h + 4 * b < kEntries) slds[(16 * r + n) * kSPitch + h + 4 * b] = v;
                 }
             }
         };
-        const int am = act_of_row<MI>(n);
-        const int arow = (am < xrows ? am : xrows - 1) * xpitch;
+        int arow;                                                // the lane's row of the activation operand
+        if constexpr (kFix) {                                    // row 4 m + i: byte i of activation m
+            const int m = (n >> 2) < p.M ? n >> 2 : p.M - 1, i = (n & 3) < 3 ? n & 3 : 2;
+            arow = (3 * m + i) * xpitch;
+        } else {
+            const int am = act_of_row<MI>(n);
+            arow = (am < xrows ? am : xrows - 1) * xpitch;
+        }
+        const int xpair = 3 * p.M * xpitch + (h < p.M ? h : p.M - 1) * (xchunks * NG * 8);
         float y[RT][MI];
         // The products of one window.  Rolled: a workgroup runs this code a few times at most, and fetching an
         // instruction for the first time costs more than looping.
+        auto compute_fix = [&](int c0, const uint8_t* xwin) {
+            const int first = kResident ? c0 + wk * U : wk * U;  // the wave's first chunk in LDS
+            const uint8_t* ax = xwin + arow + first * kChunk;
+            const floatx2_t* xt = reinterpret_cast<const floatx2_t*>(xwin + xpair) + first * NG;
+            const floatx2_t* sp = slds + n * kSPitch;
+#pragma unroll 1
+            for (int u = 0; u < U; ++u) {
+                u32x4_t c[RT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    c[r] = *reinterpret_cast<const u32x4_t*>(clds + (16 * r + n) * 128 + 16 * ((4 * u + h) ^ (n & 7)));
+                u32x4_t a[2];
+                if constexpr (NG == 4) {                         // four products of 32 k, eight bytes a lane each
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const u32x2_t t = *reinterpret_cast<const u32x2_t*>(ax + u * kChunk + 32 * j + 8 * h);
+                        a[j >> 1][2 * (j & 1)] = t[0];
+                        a[j >> 1][2 * (j & 1) + 1] = t[1];
+                    }
+                } else {                                         // two of 64 k, sixteen bytes
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        a[j] = *reinterpret_cast<const u32x4_t*>(ax + u * kChunk + chunk_k<NG>(2 * j, h));
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) order_chunk<NG>(c[r]);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const floatx2_t x = xt[u * NG + g];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        intx4_t acc = {0, 0, 0, 0};
+                        if constexpr (NG == 4) {
+                            acc = mfma_i8_32(a[g >> 1][2 * (g & 1)], a[g >> 1][2 * (g & 1) + 1], c[r][g], acc);
+                        } else {
+#pragma unroll
+                            for (int j = 2 * g / NG; j < 2 * (g + 1) / NG; ++j)
+                                acc = mfma_i8_64(a[j], c[r][2 * j], c[r][2 * j + 1], acc);
+                        }
+                        const floatx2_t s = sp[16 * r * kSPitch + u * NG + g];
+                        const float v = fmaf((float)acc[0], 65536.0f, fmaf((float)acc[1], 256.0f, (float)acc[2]));
+                        y[r][0] = fmaf(s[0] * x[0], fmaf(-s[1], x[1], v), y[r][0]);
+                    }
+                }
+            }
+        };
         auto compute = [&](int c0, const uint8_t* xwin) {
+            if constexpr (kFix) {
+                compute_fix(c0, xwin);
+                return;
+            }
             const int cw = c0 + wk * U;
             const uint8_t* ax = xwin + arow + 2 * (kResident ? cw * kChunk : wk * (U * kChunk));
             const floatx2_t* sp = slds + n * kSPitch;
@@ -564,7 +724,7 @@ struct RowTiles {
 #pragma unroll
             for (int i = 0; i < MI; ++i) y[r][i] = 0.0f;
         while (true) {
-            uint8_t* xwin = xlds + (kResident ? 0 : xsel * (xrows * win_pitch));
+            uint8_t* xwin = xlds + (kResident ? 0 : xsel * xbytes);
             if constexpr (!kResident) {
                 if (p.x_bufs == 1) __syncthreads();              // the last window's reads
                 x_store(xwin, 0, c0 * kChunk);
