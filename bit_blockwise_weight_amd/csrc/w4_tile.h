@@ -46,6 +46,7 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
 typedef int32_t intx4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x3_t __attribute__((ext_vector_type(3)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // Weight forms of the kernels: int4 times bf16 or fp16 activations, 16 levels times bf16.
@@ -325,7 +326,6 @@ struct RowTiles {
     static constexpr int kMfmas = 4 / NG;                       // MFMAs per scale group
     static constexpr int kEntries = U * NG;                     // scale groups of a wave's chunks in a window
     static constexpr int kSPitch = kEntries | 1;
-    static constexpr int kSBatch = (kEntries + 3) / 4;          // of them per lane
     static constexpr int kScaleBytes = W * RT * 16 * kSPitch * 8;
     static constexpr int kCodeBytes = W * RT * 16 * 128;        // a window's codes changing layout
     static constexpr int kPutBytes = w4_put_bytes(RT, MI);
@@ -335,10 +335,16 @@ struct RowTiles {
     static constexpr int kFixedBytes = w4_fixed_bytes(NG, RT, MI);
     static_assert(kFixedBytes == kScaleBytes + kCodeBytes + kSlots * (kPutBytes + 32));
 
+    static_assert(RT == 2);
+    // The scales of a window come by one load per kind, in lane 16 r + n for row n of tile r (a load instruction that
+    // touches many lines costs as much as one that brings a kilobyte of codes): as dwords from an address rounded
+    // down to 4 bytes, put right when they land.
     struct Fetched {
         u32x4_t c[RT][2];
-        float s[RT][kSBatch];
-        uint32_t z[RT][kSBatch];
+        u32x4_t s;           // int4: 2 NG scales; levels: four block scales of a plain weight
+        uint32_t s4;         // int4 with NG = 4: the fifth dword
+        u32x3_t z;           // int4: 2 NG zero points; levels: q8 of four blocks
+        u32x2_t d;           // levels: double-quantization scales of the first block and of the next 256
     };
 
     // tab: the level table (kLevels); lds: kFixedBytes + w4_x_bytes(), 16-byte aligned.
@@ -512,57 +518,83 @@ struct RowTiles {
             }
         };
 
-        // Codes and scales of the wave's lines in the window that starts at chunk c0 of the item whose tile 0
+        // Codes and scales of the wave's line in the window that starts at chunk c0 of the item whose tile 0
         // of this wave's row group starts at row j.  One descriptor per tile covers the whole run of rows (under
         // 2 GB, see the callers), so a window costs a few scalar instructions; j < 0: nothing.
-        __amdgpu_buffer_rsrc_t cbuf[RT], sbuf[RT], zbuf[RT];
-        int32_t shift[RT];                                       // tile r's rows start at shift[r] + j of its range
+        __amdgpu_buffer_rsrc_t cbuf[RT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            shift[r] = p.off[r];
-            cbuf[r] = buffer(w.codes + p.base[r] * w.stride, (int64_t)p.count * w.stride);
-            if constexpr (F != kLevels) {
-                sbuf[r] = buffer(w.scales + p.base[r] * w.G, (int64_t)p.count * w.G * 2);
-                zbuf[r] = buffer(w.zeros ? w.zeros + p.base[r] * w.G : nullptr, w.zeros ? (int64_t)p.count * w.G : 0);
-            }
-        }
+        for (int r = 0; r < RT; ++r) cbuf[r] = buffer(w.codes + p.base[r] * w.stride, (int64_t)p.count * w.stride);
         const int32_t stride = (int32_t)w.stride;
         const int32_t voff = (lane >> 3) * stride + 16 * (lane & 7);
-        int32_t ng = 0;
-        if constexpr (F != kLevels) ng = n * w.G;
+        // scales: row of the lane relative to base[0]; lanes 32..63 and what is past the end read nothing
+        const int32_t apart = (int32_t)(p.base[1] - p.base[0]) + p.off[1];
+        const int32_t srow = n + (lane & 16 ? apart : p.off[0]);
+        const int64_t srows = p.base[1] - p.base[0] + p.count;
+        __amdgpu_buffer_rsrc_t sbuf, zbuf, dbuf;
+        uint32_t sfirst = 0, zfirst = 0, dfirst = 0;             // of base[0], from the rounded-down address, in its unit
+        if constexpr (F == kLevels) {
+            const int64_t e0 = p.base[0] * p.K, b0 = e0 >> w.bshift;
+            const int64_t blocks = ((srows * p.K + (e0 - (b0 << w.bshift)) - 1) >> w.bshift) + 1;
+            sbuf = buffer(w.absmax + b0, w.nested ? 0 : blocks * 4);
+            const uint64_t qa = reinterpret_cast<uint64_t>(w.q8 + b0);
+            zbuf = buffer(reinterpret_cast<const void*>(qa & ~3ull), w.nested ? (blocks + (int64_t)(qa & 3) + 3) / 4 * 4 : 0);
+            const int64_t dlast = (b0 + blocks - 1) / QK_DQ_BLOCK, d0 = b0 / QK_DQ_BLOCK;
+            dbuf = buffer(w.dq_scale + d0, w.nested ? (dlast - d0 + 1) * 4 : 0);
+            sfirst = (uint32_t)(e0 - (b0 << w.bshift));          // elements of the first block before base[0]
+            zfirst = (uint32_t)(qa & 3);
+            dfirst = (uint32_t)(b0 % QK_DQ_BLOCK);
+        } else {
+            const uint64_t sa = reinterpret_cast<uint64_t>(w.scales + p.base[0] * w.G);
+            sbuf = buffer(reinterpret_cast<const void*>(sa & ~3ull), (srows * w.G * 2 + (int64_t)(sa & 3) + 3) / 4 * 4);
+            const uint64_t za = reinterpret_cast<uint64_t>(w.zeros + p.base[0] * w.G);
+            zbuf = buffer(reinterpret_cast<const void*>(za & ~3ull), w.zeros ? (srows * w.G + (int64_t)(za & 3) + 3) / 4 * 4 : 0);
+            sfirst = (uint32_t)(sa & 3);
+            zfirst = (uint32_t)(za & 3);
+        }
+        // Where the lane's scales of a window start: int4, the index of the first group from base[0]; levels, the
+        // block of the first 64 values, from the first block (and in `run` which 64 values of it).
+        auto scale_at = [&](int j, int c) -> uint32_t {
+            if constexpr (F == kLevels) return (uint32_t)(j + srow) * (uint32_t)p.K + (uint32_t)c * kChunk + sfirst;
+            else return (uint32_t)(j + srow) * (uint32_t)w.G + (uint32_t)((c * kChunk) >> w.gshift);
+        };
+        uint32_t at = 0;                                         // of the window in flight
         auto fetch = [&](Fetched& f, int j, int c0) {
             const int c = c0 + wk * U;
-            const bool in = j >= 0 && c < nchunk;
+            const bool in = j >= 0 && c < nchunk, lane_in = in && lane < 32;
+            at = scale_at(j, c);
+            if constexpr (F == kLevels) {
+                const uint32_t blk = at >> w.bshift;
+                f.s = __builtin_amdgcn_raw_buffer_load_b128(sbuf, lane_in ? 4 * blk : kOutside, 0, 0);
+                const u32x2_t t = __builtin_amdgcn_raw_buffer_load_b64(zbuf, lane_in ? (blk + zfirst) & ~3u : kOutside, 0, 0);
+                f.z[0] = t[0];
+                f.z[1] = t[1];
+                f.d = __builtin_amdgcn_raw_buffer_load_b64(dbuf, lane_in ? (blk + dfirst) / QK_DQ_BLOCK * 4 : kOutside, 0, 0);
+            } else {
+                const uint32_t so = lane_in ? (2 * at + sfirst) & ~3u : kOutside;
+                const uint32_t zo = lane_in ? (at + zfirst) & ~3u : kOutside;
+                if constexpr (NG == 4) {
+                    f.s = __builtin_amdgcn_raw_buffer_load_b128(sbuf, so, 0, 0);
+                    f.s4 = __builtin_amdgcn_raw_buffer_load_b32(sbuf, so, 16, 0);
+                    f.z = __builtin_amdgcn_raw_buffer_load_b96(zbuf, zo, 0, 0);
+                } else {
+                    if constexpr (NG == 2) {
+                        const u32x3_t t = __builtin_amdgcn_raw_buffer_load_b96(sbuf, so, 0, 0);
+                        f.s[0] = t[0];
+                        f.s[1] = t[1];
+                        f.s[2] = t[2];
+                    } else {
+                        const u32x2_t t = __builtin_amdgcn_raw_buffer_load_b64(sbuf, so, 0, 0);
+                        f.s[0] = t[0];
+                        f.s[1] = t[1];
+                    }
+                    const u32x2_t t = __builtin_amdgcn_raw_buffer_load_b64(zbuf, zo, 0, 0);
+                    f.z[0] = t[0];
+                    f.z[1] = t[1];
+                }
+            }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const int row = j + shift[r];
-                if constexpr (F == kLevels) {
-#pragma unroll
-                    for (int b = 0; b < kSBatch; ++b) {
-                        const int k = c * kChunk + (h + 4 * b) * 64;
-                        f.s[r][b] = 0.0f;
-                        f.z[r][b] = 0;
-                        if (in && row + n < p.count && k < p.K) {
-                            const int64_t blk = ((p.base[r] + row + n) * p.K + k) >> w.bshift;
-                            if (w.nested) {
-                                f.z[r][b] = (uint8_t)w.q8[blk];
-                                f.s[r][b] = w.dq_scale[blk / QK_DQ_BLOCK];
-                            } else {
-                                f.s[r][b] = w.absmax[blk];
-                            }
-                        }
-                    }
-                } else {
-                    const int32_t soff = in ? row * w.G : kOutside / 2;
-#pragma unroll
-                    for (int b = 0; b < kSBatch; ++b) {
-                        const int e = h + 4 * b;
-                        const int g = ng + (NG > 1 ? c * NG + e : ((c + e) * kChunk) >> w.gshift);
-                        f.s[r][b] = as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sbuf[r], 2 * g, 2 * soff, 0));
-                        f.z[r][b] = (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(zbuf[r], g, soff, 0);
-                    }
-                }
-                const int32_t coff = row * stride + c * (kChunk / 2);
+                const int32_t coff = (j + p.off[r]) * stride + c * (kChunk / 2);
 #pragma unroll
                 for (int q = 0; q < 2; ++q)                      // rows 8 q + lane / 8
                     f.c[r][q] = __builtin_amdgcn_raw_buffer_load_b128(cbuf[r], voff, in ? coff + 8 * q * stride : kOutside,
@@ -579,19 +611,49 @@ struct RowTiles {
                 for (int q = 0; q < 2; ++q)
                     *reinterpret_cast<u32x4_t*>(clds + (16 * r + 8 * q + (lane >> 3)) * 128 +
                                                 16 * ((lane & 7) ^ (lane >> 3))) = f.c[r][q];
+            }
+            if (lane >= 32) return;
+            if constexpr (F == kLevels) {
+                // the four runs of 64: their blocks follow the first one's
+                const uint32_t blk = at >> w.bshift, run = at >> 6, shift = w.bshift - 6;
+                const uint32_t q = __builtin_amdgcn_alignbyte(f.z[1], f.z[0], blk + zfirst);
 #pragma unroll
-                for (int b = 0; b < kSBatch; ++b) {
-                    floatx2_t v;
-                    if constexpr (F == kLevels) {
-                        v[0] = w.nested ? __fadd_rn(__fmul_rn((float)(int8_t)f.z[r][b], f.s[r][b]), mean) : f.s[r][b];
-                        v[1] = 0.0f;
+                for (int e = 0; e < kEntries; ++e) {
+                    const uint32_t o = ((run + e) >> shift) - blk;
+                    float v;
+                    if (w.nested) {
+                        const uint32_t dq = (blk + o + dfirst) / QK_DQ_BLOCK - (blk + dfirst) / QK_DQ_BLOCK;
+                        v = __fadd_rn(__fmul_rn((float)(int8_t)(q >> (8 * o)), as_float(dq ? f.d[1] : f.d[0])), mean);
                     } else {
-                        const uint16_t bits = (uint16_t)as_uint(f.s[r][b]);
-                        v[0] = w.scale_f16 ? f16_bits_to_float(bits) : bf16_bits_to_float(bits);
-                        v[1] = (float)f.z[r][b] + zbias;
-                        if constexpr (!kFix) v[1] *= v[0];
+                        v = as_float(o == 0 ? f.s[0] : o == 1 ? f.s[1] : o == 2 ? f.s[2] : f.s[3]);
                     }
-                    if (h + 4 * b < kEntries) slds[(16 * r + n) * kSPitch + h + 4 * b] = v;
+                    slds[lane * kSPitch + e] = (floatx2_t){v, 0.0f};
+                }
+            } else {
+                const uint32_t sh = 8 * ((2 * at + sfirst) & 2);
+                uint32_t sv[NG], zv[NG == 4 ? 2 : 1];
+                sv[0] = __builtin_amdgcn_alignbit(f.s[1], f.s[0], sh);
+                if constexpr (NG >= 2) sv[1] = __builtin_amdgcn_alignbit(f.s[2], f.s[1], sh);
+                if constexpr (NG == 4) {
+                    sv[2] = __builtin_amdgcn_alignbit(f.s[3], f.s[2], sh);
+                    sv[3] = __builtin_amdgcn_alignbit(f.s4, f.s[3], sh);
+                }
+                zv[0] = __builtin_amdgcn_alignbyte(f.z[1], f.z[0], at + zfirst);
+                if constexpr (NG == 4) zv[1] = __builtin_amdgcn_alignbyte(f.z[2], f.z[1], at + zfirst);
+                if constexpr (NG == 1) {                         // groups of 256 and more: both chunks in one
+                    if (w.gshift > 7) {
+                        sv[0] = (sv[0] & 0xFFFFu) | (sv[0] << 16);
+                        zv[0] = (zv[0] & 0xFFu) | (zv[0] << 8);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kEntries; ++e) {
+                    const uint16_t bits = (uint16_t)(sv[e >> 1] >> (16 * (e & 1)));
+                    floatx2_t v;
+                    v[0] = w.scale_f16 ? f16_bits_to_float(bits) : bf16_bits_to_float(bits);
+                    v[1] = (float)((zv[e >> 2] >> (8 * (e & 3))) & 255u) + zbias;
+                    if constexpr (!kFix) v[1] *= v[0];
+                    slds[lane * kSPitch + e] = v;
                 }
             }
         };
