@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
     p.M = g.M;
     p.x_bufs = g.x_bufs;
     const int steps = 7 - t.kwl + (RT == 2);             // log2(step)
-    Tiles::run(t.w, p, 0, (p.count + p.step - 1) >> steps, nullptr, lds, [&](int item, int q, const float* put) {
+    Tiles::run(t.w, p, 0, (p.count + p.step - 1) >> steps, lds, [&](int item, int q, const float* put) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll

@@ -260,7 +260,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertA
             const int M = count - m0 < 4 * MI ? count - m0 : 4 * MI;
             r.xrow = routes.tok + first + m0;
             r.M = M;
-            Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, int q, const float* put) {
+            Tiles::run(p.w, r, i0, i1, work, [&](int item, int q, const float* put) {
 #pragma unroll
                 for (int s = threadIdx.x & 63; s < 64 * MI; s += 64) {
                     const int m = Tiles::act_of(s);
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(Exper
             const int M = count - m0 < kTok ? count - m0 : kTok;
             r.xrow = p.routes->pair + first + m0;
             r.M = M;
-            Tiles::run(p.w, r, i0, i1, lds, work, [&](int item, int q, const float* put) {
+            Tiles::run(p.w, r, i0, i1, work, [&](int item, int q, const float* put) {
                 for (int o = threadIdx.x & 63; o < M * (16 * RT); o += 64) {
                     const int m = o / (16 * RT), row = o % (16 * RT), t = row / 16;
                     const int n = item * step + q * (16 * RT) + row;

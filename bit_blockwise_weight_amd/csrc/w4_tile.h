@@ -200,7 +200,8 @@ struct LevelsView {
 };
 
 // Table of the 256 code bytes as (bf16 level of the high nibble, bf16 level of the low nibble),
-// 64 copies so that a lane reads its own bank: entry b of copy l at b * 256 + 4 l.
+// 64 copies so that a lane reads its own bank: entry b of copy l at b * 256 + 4 l of LDS itself (the
+// kernels have no other LDS than the dynamic part, which starts at 0), so that a v_perm makes the address.
 constexpr int kTabBytes = 256 * 64 * 4;
 
 __device__ __forceinline__ void build_table(uint8_t* tab, const float* levels, int tid, int threads) {
@@ -211,12 +212,14 @@ __device__ __forceinline__ void build_table(uint8_t* tab, const float* levels, i
     }
 }
 
-__device__ __forceinline__ u32x4_t decode8_table(const uint8_t* tab, uint32_t w, uint32_t lane4) {
+typedef const __attribute__((address_space(3))) uint32_t* lds_u32_t;
+
+__device__ __forceinline__ u32x4_t decode8_table(uint32_t w, uint32_t lane4) {
     u32x4_t f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t off = __builtin_amdgcn_perm(w, lane4, 0x0C0C0000u | ((4u + i) << 8));
-        f[i] = *reinterpret_cast<const uint32_t*>(tab + off);
+        f[i] = *reinterpret_cast<lds_u32_t>(off);
     }
     return f;
 }
@@ -347,11 +350,11 @@ struct RowTiles {
         u32x2_t d;           // levels: double-quantization scales of the first block and of the next 256
     };
 
-    // tab: the level table (kLevels); lds: kFixedBytes + w4_x_bytes(), 16-byte aligned.
+    // lds (behind the level table, for kLevels): kFixedBytes + w4_x_bytes(), 16-byte aligned.
     // out(item, q, put), called by one wave, stores the outputs of row group q of an item from the partial sums.
     template <class V, class Out>
     static __device__ __forceinline__ void run(const V& w, const Rows<RT>& p, int item0, int item1,
-                                               const uint8_t* tab, uint8_t* lds, Out&& out) {
+                                               uint8_t* lds, Out&& out) {
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int n = lane & 15, h = lane >> 4;
         const int kw = 1 << p.kwl, wk = wave & (kw - 1), wr = wave >> p.kwl;
@@ -745,7 +748,7 @@ struct RowTiles {
                         if constexpr (F == kLevels) {
 #pragma unroll
                             for (int r = 0; r < RT; ++r)
-                                acc[r] = mfma<F>(a[j], decode8_table(tab, c[r][j], 4 * lane), acc[r]);
+                                acc[r] = mfma<F>(a[j], decode8_table(c[r][j], 4 * lane), acc[r]);
                         } else {
                             xs = mfma<F>(a[j], ones<F>(), xs);
 #pragma unroll
