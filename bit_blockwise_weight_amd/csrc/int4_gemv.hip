@@ -36,7 +36,7 @@ template <int kTasks>
 struct Int4Group {
     int32_t wg0[kTasks];     // first workgroup of each task (past the last one: never reached)
     int32_t M;
-    int32_t x_bufs;
+    int32_t pad;
     Int4Task t[kTasks];
 };
 
@@ -69,7 +69,6 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
     p.x_rows = g.M;
     p.x_aligned = t.x_aligned;
     p.M = g.M;
-    p.x_bufs = g.x_bufs;
     const int steps = 7 - t.kwl + (RT == 2);             // log2(step)
     Tiles::run(t.w, p, 0, (p.count + p.step - 1) >> steps, lds, [&](int item, int q, const float* put) {
 #pragma unroll
@@ -89,9 +88,9 @@ constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
 // The activations of a whole row stay in LDS where they fit.
 size_t x_lds(int M, int ng, int64_t K, bool resident) {
-    return mi_for(M) == 1 ? w4_fix_bytes(4, M, ng, K, resident, 2) : w4_x_bytes(4, M, K, resident, 2);
+    return mi_for(M) == 1 ? w4_fix_bytes(4, M, ng, K, resident) : w4_x_bytes(4, M, K, resident);
 }
-size_t resident_lds(int M, int ng, int64_t K) { return w4_fixed_bytes(ng, kRt, mi_for(M)) + x_lds(M, ng, K, true); }
+size_t resident_lds(int M, int ng, int64_t K) { return w4_fixed_bytes(ng, kRt, mi_for(M), true) + x_lds(M, ng, K, true); }
 bool resident_for(int M, int ng, int64_t K) { return resident_lds(M, ng, K) <= kLdsBytes; }
 
 constexpr int32_t kNever = 0x7FFFFFFF;
@@ -108,13 +107,13 @@ hipError_t launch_tasks(const Int4Group<kTasks>& g, int64_t grid, size_t lds, hi
 template <int F, int NG, int MI, bool kResident>
 hipError_t launch_one(Int4Group<kMaxGemvTasks>& g, int64_t grid, int64_t kmax, hipStream_t s) {
     typedef RowTiles<F, NG, kRt, MI, kResident, false> Tiles;
-    g.x_bufs = 2;
+    g.pad = 0;
     const size_t lds = Tiles::kFixedBytes + x_lds(g.M, NG, kmax, kResident);
     if (g.wg0[1] == kNever) {
         Int4Group<1> one;
         one.wg0[0] = 0;
         one.M = g.M;
-        one.x_bufs = g.x_bufs;
+        one.pad = 0;
         one.t[0] = g.t[0];
         return launch_tasks<F, NG, MI, kResident, 1>(one, grid, lds, s);
     }
@@ -189,7 +188,9 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             kmax = std::max(kmax, st->cols);
             ++n;
         }
-        const int per_cu = resident && resident_lds(M, ng, kmax) > kLdsBytes / 2 ? 1 : 2;
+        const size_t lds = resident ? resident_lds(M, ng, kmax)
+                                    : w4_fixed_bytes(ng, kRt, mi_for(M), false) + x_lds(M, ng, kmax, false);
+        const int per_cu = lds > kLdsBytes / 2 ? 1 : 2;
         // the workgroups that the CUs hold at a time, dealt to the tasks by their work, at most one per item
         int64_t grid = 0;
         for (int32_t i = 0; i < n; ++i) {

@@ -191,7 +191,6 @@ struct ExpertArgs {
     int32_t x_rows;
     int32_t x_aligned;
     int32_t kwl;
-    int32_t x_bufs;
 };
 
 // Workgroups per CU, at most: the level table takes 64 KB of its LDS.
@@ -204,12 +203,12 @@ int64_t workgroups(int64_t items, size_t lds) {
 // LDS of the activations; those of a whole row stay there where all of them fit.
 template <int F, int NG, int MI>
 size_t x_lds(int tokens, bool split, int64_t K, bool resident) {
-    return F != kLevels && MI == 1 ? w4_fix_bytes(4, tokens, NG, K, resident, 2)
-                                   : w4_x_bytes(4, split ? 2 * tokens : tokens, K, resident, 2);
+    return F != kLevels && MI == 1 ? w4_fix_bytes(4, tokens, NG, K, resident)
+                                   : w4_x_bytes(4, split ? 2 * tokens : tokens, K, resident);
 }
 template <int F, int NG, int RT, int MI>
 bool fits(int tokens, bool split, int64_t K) {
-    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes(NG, RT, MI) + x_lds<F, NG, MI>(tokens, split, K, true) <=
+    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes(NG, RT, MI, true) + x_lds<F, NG, MI>(tokens, split, K, true) <=
            kLdsBytes;
 }
 // Tokens that a pass over an expert's rows takes; the down product needs two operand rows for one, but not in fixed
@@ -254,7 +253,6 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertA
         r.x_rows = p.x_rows;
         r.x_aligned = p.x_aligned;
         r.kwl = p.kwl;
-        r.x_bufs = p.x_bufs;
         // 4 MI tokens at a time (an expert rarely has more)
         for (int m0 = 0; m0 < count; m0 += 4 * MI) {
             const int M = count - m0 < 4 * MI ? count - m0 : 4 * MI;
@@ -307,7 +305,6 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(Exper
         r.x_rows = p.x_rows;
         r.x_aligned = 1;
         r.kwl = p.kwl;
-        r.x_bufs = p.x_bufs;
         constexpr int kTok = kTokens<F, MI, true>;
         for (int m0 = 0; m0 < count; m0 += kTok) {
             const int M = count - m0 < kTok ? count - m0 : kTok;
@@ -348,7 +345,6 @@ template <int F, int NG, int MI, bool kResident>
 hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
     p.kwl = kResident ? w4_kwl(p.H) : 2;
-    p.x_bufs = 2;
     const size_t lds = (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + Tiles::kFixedBytes +
                        x_lds<F, NG, MI>(tokens, false, p.H, kResident);
     const hipError_t e = allow_lds<&moe_up_kernel<F, NG, MI, kResident>>(lds);
@@ -380,7 +376,6 @@ template <int F, int NG, int RT, int MI, bool kResident>
 hipError_t launch_down_one(ExpertArgs<F> p, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, RT, MI, kResident, true> Tiles;
     p.kwl = kResident ? w4_kwl(p.I) : 2;
-    p.x_bufs = 2;
     const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + x_lds<F, NG, MI>(tokens, true, p.I, kResident);
     const hipError_t e = allow_lds<&moe_down_kernel<F, NG, RT, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
@@ -452,7 +447,7 @@ ExpertArgs<F> expert_args(const MoeItem& m, const Buffers& b, bool up) {
     p.grid = 0;
     p.x_rows = up ? m.T : m.T * m.top_k;
     p.x_aligned = !up || (m.H % 8 == 0 && reinterpret_cast<uintptr_t>(m.x) % 16 == 0);
-    p.kwl = p.x_bufs = 0;
+    p.kwl = 0;
     return p;
 }
 

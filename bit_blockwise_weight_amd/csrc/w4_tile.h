@@ -232,12 +232,12 @@ __device__ __forceinline__ u32x4_t decode8_table(uint32_t w, uint32_t lane4) {
 // of kw * 256 k; a wave takes one line (128 bytes, 256 k) of each row per window, and the
 // partial outputs of the kw waves meet in LDS once per item, where the last wave to arrive adds
 // them in wave order (the same bits every time).  No wave waits for another except every
-// kSlots items, and per window where the activations do not stay.  While a wave works on one window the codes and scales of
+// kSlots items, and per window of these where the activations do not stay.  While a wave works on one window the codes and scales of
 // the next one (of the same item or the next) are already on their way into registers.
 //
 // Activations (in the order of decoded int4, zero past K) live in LDS, 16 bytes more than a row
 // apart, so that a fragment read of 16 rows falls in different banks: all of K for the whole run
-// (kResident), or the current window, loaded one window ahead.  With kSplit they are fp32 and
+// (kResident), or the current window, loaded one window ahead and used for kSlots items.  With kSplit they are fp32 and
 // become two bf16 rows, hi and lo (activation m: rows 2 m and 2 m + 1; 16 bits of mantissa).
 // Scales go to LDS as well, per row and group the pair (scale, scale * (zero point + bias)); a
 // wave writes and reads only its own, an odd number of pairs apart.
@@ -269,8 +269,7 @@ struct Rows {
     int32_t x_rows;          // rows of x
     int32_t x_aligned;       // 16-byte loads of x are possible
     int32_t M;               // activations
-    int32_t kwl;             // log2(kw)
-    int32_t x_bufs;          // buffers for windows of x (not resident): 1 or 2
+    int32_t kwl;             // log2(kw); at most 2 where x is not resident
 };
 
 // The product's row 4 h + i lands in register i of lane group h.  With few activation rows only the
@@ -282,9 +281,9 @@ constexpr int kLineK = 256;               // k of a 128-byte line of codes
 
 // bytes of LDS beside the activations: scales, codes, partial sums of a few items and their counters
 constexpr int w4_put_bytes(int RT, int MI) { return 8 * RT * 64 * MI * 4; }
-constexpr int w4_slots(int) { return 2; }
-constexpr int w4_fixed_bytes(int NG, int RT, int MI) {
-    return 8 * RT * 16 * ((2 * NG) | 1) * 8 + 8 * RT * 16 * 128 + w4_slots(MI) * (w4_put_bytes(RT, MI) + 32);
+constexpr int w4_slots(bool resident) { return resident ? 2 : 3; }
+constexpr int w4_fixed_bytes(int NG, int RT, int MI, bool resident) {
+    return 8 * RT * 16 * ((2 * NG) | 1) * 8 + 8 * RT * 16 * 128 + w4_slots(resident) * (w4_put_bytes(RT, MI) + 32);
 }
 constexpr size_t kLdsBytes = 160 * 1024;  // of a CU
 
@@ -306,13 +305,13 @@ hipError_t allow_lds(size_t lds) {
 
 // bytes of LDS that the activations take: rows of 16-bit values (two an activation with kSplit), or M
 // activations in fixed point, three bytes a value and a pair per scale group (NG of them in a chunk)
-inline size_t w4_x_bytes(int kw, int rows, int64_t K, bool resident, int bufs) {
-    const size_t k = (size_t)((K + kLineK - 1) / kLineK) * kLineK;
-    return resident ? (size_t)rows * (k * 2 + 16) : (size_t)bufs * rows * ((size_t)kw * kLineK * 2 + 16);
-}
-inline size_t w4_fix_bytes(int kw, int M, int NG, int64_t K, bool resident, int bufs) {
+inline size_t w4_x_bytes(int kw, int rows, int64_t K, bool resident) {
     const size_t k = resident ? (size_t)((K + kLineK - 1) / kLineK) * kLineK : (size_t)kw * kLineK;
-    return (resident ? 1 : bufs) * (size_t)M * (3 * (k + 16) + k / kChunk * NG * 8);
+    return (size_t)rows * (k * 2 + 16);
+}
+inline size_t w4_fix_bytes(int kw, int M, int NG, int64_t K, bool resident) {
+    const size_t k = resident ? (size_t)((K + kLineK - 1) / kLineK) * kLineK : (size_t)kw * kLineK;
+    return (size_t)M * (3 * (k + 16) + k / kChunk * NG * 8);
 }
 // log2 of the waves (of 8) that split a row of K: as many as it has lines
 inline int w4_kwl(int64_t K) {
@@ -332,10 +331,10 @@ struct RowTiles {
     static constexpr int kScaleBytes = W * RT * 16 * kSPitch * 8;
     static constexpr int kCodeBytes = W * RT * 16 * 128;        // a window's codes changing layout
     static constexpr int kPutBytes = w4_put_bytes(RT, MI);
-    static constexpr int kSlots = w4_slots(MI);
+    static constexpr int kSlots = w4_slots(kResident);
     // units of x per thread and batch; a window's fit one batch (kw <= 4)
     static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : kSplit ? (MI + 1) / 2 : MI;
-    static constexpr int kFixedBytes = w4_fixed_bytes(NG, RT, MI);
+    static constexpr int kFixedBytes = w4_fixed_bytes(NG, RT, MI, kResident);
     static_assert(kFixedBytes == kScaleBytes + kCodeBytes + kSlots * (kPutBytes + 32));
 
     static_assert(RT == 2);
@@ -368,7 +367,6 @@ struct RowTiles {
         const int xchunks = kResident ? (nchunk + U - 1) / U * U : wchunks;   // chunks of x that LDS holds
         const int xpitch = xchunks * (kFix ? kChunk : 2 * kChunk) + 16;
         const int xrows = kFix ? 3 * p.M : kSplit ? 2 * p.M : p.M;
-        const int xbytes = xrows * xpitch + (kFix ? p.M * xchunks * (NG * 8) : 0);
         const Magic magic(F == kInt4F16);
         float mean = 0.0f, zbias = 0.0f;
         if constexpr (F == kLevels) mean = w.nested ? *w.dq_mean : 0.0f;
@@ -769,11 +767,42 @@ struct RowTiles {
         };
 
         Fetched f;
+        float* mine = put + wave * (RT * 64 * MI) + lane;        // this wave's sums of an item, slot by slot
+        auto save = [&](int slot) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < MI; ++i) mine[slot * (kPutBytes / 4) + (r * MI + i) * 64] = y[r][i];
+        };
+        auto clear = [&] {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < MI; ++i) y[r][i] = 0.0f;
+        };
+        // The wave's sums of an item are saved: the last wave of the row group to say so adds them up.
+        auto finish = [&](int item, int slot) {
+            int before = 0;
+            if (lane == 0)
+                before = __hip_atomic_fetch_add(&arrived[slot * W + wr], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_WORKGROUP);
+            if (__builtin_amdgcn_readfirstlane(before) == kw - 1) out(item, wr, put + slot * (kPutBytes / 4));
+        };
+        // after the last item of the slots: no sum may be overwritten before it is added
+        auto recycle = [&] {
+            __syncthreads();
+            if (tid < kSlots * W) arrived[tid] = 0;
+            __syncthreads();
+        };
+        int j = item0 * p.step + wr * p.group_step;              // row of the next window to fetch
         x_load(0, 0);
-        int j = item0 * p.step + wr * p.group_step;               // row of the next window to fetch
         fetch(f, j, 0);
         if (tid < kSlots * W) arrived[tid] = 0;
+        clear();
+        // Every step: what was fetched goes to LDS, the next window's loads are issued (without a condition: a
+        // branch around them would make later waits cover them; past the end every offset is outside and nothing is
+        // read), the products are made.
         if constexpr (kResident) {
+            // item by item, window by window
             x_store(xlds, 0, 0);
 #pragma unroll 1
             for (int base = kXUnits * kThreads; base < total; base += kXUnits * kThreads) {
@@ -781,60 +810,62 @@ struct RowTiles {
                 x_store(xlds, base, 0);
             }
             __syncthreads();
-        }
-        int item = item0;
-        int c0 = 0, xsel = 0, slot = 0;
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int i = 0; i < MI; ++i) y[r][i] = 0.0f;
-        while (true) {
-            uint8_t* xwin = xlds + (kResident ? 0 : xsel * xbytes);
-            if constexpr (!kResident) {
-                if (p.x_bufs == 1) __syncthreads();              // the last window's reads
-                x_store(xwin, 0, c0 * kChunk);
-            }
-            land(f);
-            int nc = c0 + wchunks;
-            const bool last = nc >= nchunk;                      // last window of the item
-            const bool end = last && item + 1 >= item1;
-            if (last) {
-                nc = 0;
-                j += p.step;
-            }
-            // Unconditional (past the last item every offset is outside and nothing is read): a branch around
-            // them would make later waits cover these loads.
-            if constexpr (!kResident) x_load(0, nc * kChunk);
-            fetch(f, end ? -1 : j, nc);
-            if constexpr (!kResident) {
-                __syncthreads();
-                xsel ^= p.x_bufs - 1;
-            }
-            if (c0 + wk * U < nchunk) compute(c0, xwin);
-            if (last) {
-                float* pp = put + slot * (kPutBytes / 4);
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int i = 0; i < MI; ++i) {
-                        pp[(wave * RT + r) * (64 * MI) + 64 * i + lane] = y[r][i];
-                        y[r][i] = 0.0f;
-                    }
-                int before = 0;
-                if (lane == 0)
-                    before = __hip_atomic_fetch_add(&arrived[slot * W + wr], 1, __ATOMIC_ACQ_REL,
-                                                    __HIP_MEMORY_SCOPE_WORKGROUP);
-                if (__builtin_amdgcn_readfirstlane(before) == kw - 1) out(item, wr, pp);
+            int item = item0, c0 = 0, slot = 0;
+            while (true) {
+                land(f);
+                const bool last = c0 + wchunks >= nchunk;        // last window of the item
+                const bool end = last && item + 1 >= item1;
+                const int nc = last ? 0 : c0 + wchunks;
+                if (last) j += p.step;
+                fetch(f, end ? -1 : j, nc);
+                if (c0 + wk * U < nchunk) compute(c0, xlds);
+                c0 = nc;
+                if (!last) continue;
+                save(slot);
+                clear();
+                finish(item, slot);
                 if (end) break;
                 ++item;
                 if (++slot == kSlots) {
                     slot = 0;
-                    __syncthreads();
-                    if (tid < kSlots * W) arrived[tid] = 0;
-                    __syncthreads();
+                    recycle();
                 }
             }
-            c0 = nc;
+        } else {
+            // kSlots items at a time, so that a window of activations serves all of them; their sums stay in LDS
+            // from window to window
+            for (int first = item0; first < item1; first += kSlots) {
+                const int items = item1 - first < kSlots ? item1 - first : kSlots;
+                const int j0 = j;
+#pragma unroll 1
+                for (int c0 = 0; c0 < nchunk; c0 += wchunks) {
+                    const bool last = c0 + wchunks >= nchunk;
+                    const int nc = last ? 0 : c0 + wchunks;
+                    __syncthreads();                             // the last window's reads
+                    x_store(xlds, 0, c0 * kChunk);
+                    x_load(0, nc * kChunk);
+                    __syncthreads();
+#pragma unroll 1
+                    for (int slot = 0; slot < items; ++slot) {
+                        land(f);
+                        const bool turn = slot + 1 == items;     // on to the next window, or to the next items
+                        const bool end = turn && last && first + items >= item1;
+                        j = turn && !last ? j0 : j + p.step;
+                        fetch(f, end ? -1 : j, turn ? nc : c0);
+                        if (c0 > 0)
+#pragma unroll
+                            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                                for (int i = 0; i < MI; ++i) y[r][i] = mine[slot * (kPutBytes / 4) + (r * MI + i) * 64];
+                        else
+                            clear();
+                        if (c0 + wk * U < nchunk) compute(c0, xlds);
+                        save(slot);
+                        if (last) finish(first + slot, slot);
+                    }
+                }
+                if (first + items < item1) recycle();
+            }
         }
         __syncthreads();
     }
