@@ -446,7 +446,7 @@ ExpertArgs<F> expert_args(const MoeItem& m, const Buffers& b, bool up) {
     p.Ipad = (int32_t)((m.I + 7) / 8 * 8);
     p.grid = 0;
     p.x_rows = up ? m.T : m.T * m.top_k;
-    p.x_aligned = !up || (m.H % 8 == 0 && reinterpret_cast<uintptr_t>(m.x) % 16 == 0);
+    p.x_aligned = !up || (m.H % 8 == 0 && reinterpret_cast<uintptr_t>(m.x) % 4 == 0);
     p.kwl = 0;
     return p;
 }

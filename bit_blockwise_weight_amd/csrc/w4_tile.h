@@ -267,7 +267,7 @@ struct Rows {
     int32_t K;
     int32_t x_pitch;         // values from a row of x to the next
     int32_t x_rows;          // rows of x
-    int32_t x_aligned;       // 16-byte loads of x are possible
+    int32_t x_aligned;       // rows of x start at multiples of 4 bytes and K % 8 == 0
     int32_t M;               // activations
     int32_t kwl;             // log2(kw); at most 2 where x is not resident
 };
@@ -371,24 +371,48 @@ struct RowTiles {
         float mean = 0.0f, zbias = 0.0f;
         if constexpr (F == kLevels) mean = w.nested ? *w.dq_mean : 0.0f;
         else zbias = (kFix ? 0.0f : kCodeBias<F>) + (w.zeros ? 0.0f : 8.0f);
-        const __amdgpu_buffer_rsrc_t xbuf = buffer(p.x, (int64_t)p.x_rows * p.x_pitch * (kSplit ? 4 : 2));
-
-        // Staging of activations, thread by thread, rows as if they had 2^ush units of 8 values.  Rows that
-        // cannot be read 16 bytes at a time are read element by element when they are stored.
+        // Staging of activations, thread by thread, rows as if they had 2^ush units of 8 values.  A unit is read
+        // as four dwords from an address rounded down to 4 bytes, and one dword more where rows may start
+        // between dwords, and put right (and zero past K) when it is stored.
+        const uint64_t xa = reinterpret_cast<uint64_t>(p.x);
+        const uint32_t xodd = (uint32_t)(xa & 2);
+        const __amdgpu_buffer_rsrc_t xbuf = buffer(reinterpret_cast<const void*>(xa & ~3ull),
+                                                   ((int64_t)p.x_rows * p.x_pitch * (kSplit ? 4 : 2) + xodd + 3) / 4 * 4);
         const int units = xchunks * (kChunk / 8);
         const int ush = 32 - __builtin_clz(units - 1);
         const int total = p.M << ush;
         u32x4_t xr[kXUnits][kSplit ? 2 : 1];
+        uint32_t xe[kXUnits];
         auto x_load = [&](int base, int k0) {
 #pragma unroll
             for (int b = 0; b < kXUnits; ++b) {
                 const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
-                const bool in = i < total && u < units && k < p.K && p.x_aligned;
+                const bool in = i < total && u < units && k < p.K;
                 const int row = in && p.xrow ? p.xrow[m] : m;
-                const int32_t off = in ? (row * p.x_pitch + k) * (kSplit ? 4 : 2) : kOutside;
-                xr[b][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 0, 0);
-                if constexpr (kSplit) xr[b][1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 16, 0);
+                if constexpr (kSplit) {
+                    const int32_t off = in ? (row * p.x_pitch + k) * 4 : kOutside;
+                    xr[b][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 0, 0);
+                    xr[b][1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 16, 0);
+                } else {
+                    const int32_t off = in ? ((row * p.x_pitch + k) * 2 + xodd) & ~3 : kOutside;
+                    xr[b][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, off, 0, 0);
+                    xe[b] = __builtin_amdgcn_raw_buffer_load_b32(xbuf, off, p.x_aligned ? kOutside : 16, 0);
+                }
             }
+        };
+        // Unit b of a batch as 8 16-bit values: from the dwords it was read in, zero past K.
+        auto x_unit = [&](int b, int m, int k) -> u32x4_t {
+            u32x4_t v = xr[b][0];
+            if (!p.x_aligned) {
+                const int row = p.xrow ? p.xrow[m < p.M ? m : 0] : m;
+                const uint32_t sh = 8 * (((row * p.x_pitch + k) * 2 + xodd) & 2);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t d = __builtin_amdgcn_alignbit(q < 3 ? xr[b][0][q + 1] : xe[b], xr[b][0][q], sh);
+                    v[q] = k + 2 * q + 1 < p.K ? d : k + 2 * q < p.K ? d & 0xFFFFu : 0u;
+                }
+            }
+            return v;
         };
         // Every thread stores (what lies outside, to the 16 bytes behind row 0, which nobody reads): under a
         // condition the compiler would move the loads down to it, behind those of the codes.
@@ -406,16 +430,10 @@ struct RowTiles {
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[q] = as_float(xr[b][q >> 2][q & 3]);
                 } else {
+                    const u32x4_t x8 = x_unit(b, m, k);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint32_t d = xr[b][0][q];
-                        if (!p.x_aligned) {
-                            const uint16_t* src =
-                                static_cast<const uint16_t*>(p.x) + (int64_t)(in && p.xrow ? p.xrow[m] : m) * p.x_pitch + k;
-                            const uint32_t lo = in && k + 2 * q < p.K ? src[2 * q] : 0u;
-                            const uint32_t hi = in && k + 2 * q + 1 < p.K ? src[2 * q + 1] : 0u;
-                            d = lo | (hi << 16);
-                        }
+                        const uint32_t d = x8[q];
                         if constexpr (F == kInt4F16) {
                             v[2 * q] = f16_bits_to_float((uint16_t)d);
                             v[2 * q + 1] = f16_bits_to_float((uint16_t)(d >> 16));
@@ -497,24 +515,8 @@ struct RowTiles {
                     *reinterpret_cast<u32x4_t*>(dst + (in ? at + xpitch : at)) = lo;
                 } else {
                     const int at = in ? m * xpitch + 16 * u : xpitch - 16;
-                    *reinterpret_cast<u32x4_t*>(dst + at) = F == kLevels ? xr[b][0] : int4_order(xr[b][0]);
-                }
-            }
-            if constexpr (!kSplit) {
-                if (p.x_aligned) return;
-#pragma unroll 1
-                for (int b = 0; b < kXUnits; ++b) {
-                    const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
-                    if (i >= total || u >= units) continue;
-                    const uint16_t* src = static_cast<const uint16_t*>(p.x) + (int64_t)(p.xrow ? p.xrow[m] : m) * p.x_pitch + k;
-                    u32x4_t v;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t lo = k + 2 * j < p.K ? src[2 * j] : 0u;
-                        const uint32_t hi = k + 2 * j + 1 < p.K ? src[2 * j + 1] : 0u;
-                        v[j] = lo | (hi << 16);
-                    }
-                    *reinterpret_cast<u32x4_t*>(dst + m * xpitch + 16 * u) = F == kLevels ? v : int4_order(v);
+                    const u32x4_t v = x_unit(b, m, k0 + 8 * u);
+                    *reinterpret_cast<u32x4_t*>(dst + at) = F == kLevels ? v : int4_order(v);
                 }
             }
         };
