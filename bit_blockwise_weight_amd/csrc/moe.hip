@@ -63,18 +63,43 @@ __device__ __forceinline__ float load_logit(const void* p, int32_t dtype, int i)
 
 // Scratch of route(), in LDS.
 struct RouteScratch {
-    float logit[kMaxT][kMaxE + 16];
+    float logit[kMaxT][kMaxE];
     float best[kMaxT][kMaxK];             // the chosen logits by position, -inf behind the last
-    uint8_t who[kMaxT][kMaxK];            // and their experts
+    int32_t who[kMaxT][kMaxK];            // and their experts
     float den[kMaxT];
     uint32_t mask[kMaxE];                 // tokens of each expert
-    int32_t slot[kMaxE];                  // its place in the list
-    int32_t waves[8][2];
+    int32_t first[kMaxE];                 // its first entry
+    uint32_t any[kMaxE / 32];             // experts with a token
+    int32_t total[4];
 };
+
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp_from(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, kCtrl, kRows, 0xF, false);
+}
+// Inclusive prefix sum over the wave: shifts inside the rows of 16 lanes, then the last lane of row 0 and 2 added to
+// rows 1 and 3, and lane 31 to the upper half.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp_from<0x111, 0xF>(v);
+    v += dpp_from<0x112, 0xF>(v);
+    v += dpp_from<0x114, 0xF>(v);
+    v += dpp_from<0x118, 0xF>(v);
+    v += dpp_from<0x142, 0xA>(v);
+    v += dpp_from<0x143, 0xC>(v);
+    return v;
+}
+// Sum over 16 lanes, in every one of them.
+__device__ __forceinline__ float row_sum(float v) {
+    v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0xB1, 0xF, 0xF, false));    // xor 1
+    v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0x4E, 0xF, 0xF, false));    // xor 2
+    v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0x141, 0xF, 0xF, false));   // half mirror
+    v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0x140, 0xF, 0xF, false));   // mirror
+    return v;
+}
 
 // Fills r (LDS) from the logits, by one workgroup of kThreads.  Every logit's rank among its token's is counted
 // at once (how many are larger, or equal with a lower index): the rank is the position, so the choice takes no
-// rounds that wait for each other.  The loops stay rolled: the code runs once, and fetching it is most of its time.
+// rounds that wait for each other.  The loops stay rolled: the code runs once, and fetching it is much of its time.
 __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Routes& r) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int padded = (a.E + 15) & ~15;
@@ -82,8 +107,11 @@ __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Route
     for (int t = wave; t < a.T; t += 8)
 #pragma unroll 1
         for (int e = lane; e < padded; e += 64) s.logit[t][e] = e < a.E ? load_logit(a.logits, a.dtype, t * a.E + e) : -INFINITY;
-    if (tid < kMaxE) s.mask[tid] = 0;
-    if (tid < kMaxT * kMaxK) s.best[tid / kMaxK][tid % kMaxK] = -INFINITY;
+    if (tid < kMaxE) {
+        s.mask[tid] = 0;
+        s.best[tid / kMaxK][tid % kMaxK] = -INFINITY;
+    }
+    if (tid < kMaxE / 32) s.any[tid] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int i = tid; i < a.T * a.E; i += kThreads) {
@@ -92,78 +120,83 @@ __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Route
         int rank = 0;
 #pragma unroll 1
         for (int j = 0; j < padded; j += 16) {
-            float o[16];
+            floatx4_t o[4];
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = s.logit[t][j + q];
+            for (int q = 0; q < 4; ++q) o[q] = *reinterpret_cast<const floatx4_t*>(&s.logit[t][j + 4 * q]);
 #pragma unroll
-            for (int q = 0; q < 16; ++q) rank += (o[q] > v) | ((o[q] == v) & (j + q < e));
+            for (int q = 0; q < 16; ++q) rank += (o[q >> 2][q & 3] > v) | ((o[q >> 2][q & 3] == v) & (j + q < e));
         }
         if (rank < a.top_k && v != -INFINITY) {
             s.best[t][rank] = v;
-            s.who[t][rank] = (uint8_t)e;
+            s.who[t][rank] = e;
             atomicOr(&s.mask[e], 1u << t);
+            atomicOr(&s.any[e >> 5], 1u << (e & 31));
         }
     }
     __syncthreads();
-    // the denominators: a wave per token
-#pragma unroll 1
-    for (int t = wave; t < a.T; t += 8) {
-        const float top = s.best[t][0];
-        const float* from = a.renorm ? s.best[t] : s.logit[t];
-        const int n = a.renorm ? a.top_k : a.E;
-        float den = 0.0f;
-#pragma unroll 1
-        for (int i = lane; i < n; i += 64) den += from[i] == -INFINITY ? 0.0f : expf(from[i] - top);
-#pragma unroll 1
-        for (int d = 32; d > 0; d >>= 1) den += __shfl_xor(den, d);
-        if (lane == 0) s.den[t] = den;
-    }
-    // the list: thread e, an exclusive scan over the experts
-    const uint32_t mk = tid < kMaxE ? s.mask[tid] : 0u;
-    const unsigned long long bal = __ballot(mk != 0);
-    int sum = __popc(mk);
-#pragma unroll 1
-    for (int d = 1; d < 64; d <<= 1) {
-        const int up = __shfl_up(sum, d);
-        if (lane >= d) sum += up;
-    }
-    if (lane == 63) {
-        s.waves[wave][0] = __popcll(bal);
-        s.waves[wave][1] = sum;
-    }
-    __syncthreads();
-    int slot = __popcll(bal & ((1ull << lane) - 1)), first = sum - __popc(mk), total = 0, entries = 0;
-#pragma unroll 1
-    for (int w = 0; w < kMaxE / 64; ++w) {
-        if (w < wave) {
-            slot += s.waves[w][0];
-            first += s.waves[w][1];
-        }
-        total += s.waves[w][0];
-        entries += s.waves[w][1];
-    }
-    if (tid == 0) {
-        r.nactive = total;
-        r.start[total] = entries;
-    }
-    if (mk) {
-        r.expert[slot] = tid;
-        r.start[slot] = first;
-        s.slot[tid] = first;
-    }
-    if (tid < a.T) {
-        int n = 0;
-#pragma unroll 1
-        while (n < a.top_k && s.best[tid][n] != -INFINITY) ++n;
-        r.chosen[tid] = n;
-    }
-    __syncthreads();
+    // thread 16 t + k: choice k of token t; thread e: expert e
     const int t = tid / kMaxK, k = tid % kMaxK;
-    if (t < a.T && k < a.top_k && s.best[t][k] != -INFINITY) {
-        const int e = s.who[t][k], at = s.slot[e] + __popc(s.mask[e] & ((1u << t) - 1));
+    float p = 0.0f, den = 1.0f;
+    bool mine = false;
+    uint32_t mk = 0;
+    int scan = 0;
+    if (tid < kMaxE) {
+        const float v = s.best[t][k], top = s.best[t][0];
+        mine = t < a.T && k < a.top_k && v != -INFINITY;
+        if (mine) p = expf(v - top);
+        den = row_sum(p);
+        const int chosen = __popc((uint32_t)(__ballot(mine) >> (lane & 48)) & 0xFFFFu);
+        if (k == 0 && t < a.T) r.chosen[t] = chosen;
+        mk = s.mask[tid];
+        scan = wave_scan(__popc(mk));
+        if (lane == 63) s.total[wave] = scan;
+    }
+    if (!a.renorm) {                                     // the sum over every expert instead: a wave per token
+#pragma unroll 1
+        for (int tt = wave; tt < a.T; tt += 8) {
+            const float top = s.best[tt][0];
+            float sum = 0.0f;
+#pragma unroll 1
+            for (int i = lane; i < a.E; i += 64) {
+                const float v = s.logit[tt][i];
+                if (v != -INFINITY) sum += expf(v - top);
+            }
+            sum = row_sum(sum);
+            sum = (as_float(__builtin_amdgcn_readlane(as_uint(sum), 0)) + as_float(__builtin_amdgcn_readlane(as_uint(sum), 16))) +
+                  (as_float(__builtin_amdgcn_readlane(as_uint(sum), 32)) + as_float(__builtin_amdgcn_readlane(as_uint(sum), 48)));
+            if (lane == 0) s.den[tt] = sum;
+        }
+    }
+    __syncthreads();
+    if (tid < kMaxE) {
+        int first = scan - __popc(mk), entries = 0, slot = 0, listed = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w < wave) first += s.total[w];
+            entries += s.total[w];
+        }
+#pragma unroll
+        for (int w = 0; w < kMaxE / 32; ++w) {
+            const uint32_t bits = s.any[w];
+            listed += __popc(bits);
+            slot += __popc(w < tid >> 5 ? bits : w == tid >> 5 ? bits & ((1u << (tid & 31)) - 1) : 0u);
+        }
+        s.first[tid] = first;
+        if (mk) {
+            r.expert[slot] = tid;
+            r.start[slot] = first;
+        }
+        if (tid == 0) {
+            r.nactive = listed;
+            r.start[listed] = entries;
+        }
+    }
+    __syncthreads();
+    if (mine) {
+        const int e = s.who[t][k], at = s.first[e] + __popc(s.mask[e] & ((1u << t) - 1));
         r.tok[at] = (uint8_t)t;
         r.pair[at] = (uint8_t)(t * a.top_k + k);
-        r.w[at] = expf(s.best[t][k] - s.best[t][0]) / s.den[t];
+        r.w[at] = p / (a.renorm ? den : s.den[t]);
     }
     __syncthreads();
 }
