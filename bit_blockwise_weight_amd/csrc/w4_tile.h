@@ -134,12 +134,6 @@ __device__ __forceinline__ u32x4_t int4_order(u32x4_t v) {
     r[3] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100);   // (2, 6)
     return r;
 }
-// Position inside its eight that element k of a row takes in that order.
-__device__ __forceinline__ int int4_slot(int k) {
-    const int e = k & 7;                                    // 1 5 0 4 3 7 2 6
-    return 4 * ((e >> 1) & 1) + 2 * (1 - (e & 1)) + (e >> 2);
-}
-
 template <int F>
 __device__ __forceinline__ floatx4_t mfma(u32x4_t a, u32x4_t b, floatx4_t c) {
     if constexpr (F == kInt4F16)
@@ -561,10 +555,13 @@ struct RowTiles {
             else return (uint32_t)(j + srow) * (uint32_t)w.G + (uint32_t)((c * kChunk) >> w.gshift);
         };
         uint32_t at = 0;                                         // of the window in flight
+        int left = 0;                                            // and the scale groups (runs of 64) from there to the row's end
         auto fetch = [&](Fetched& f, int j, int c0) {
             const int c = c0 + wk * U;
             const bool in = j >= 0 && c < nchunk, lane_in = in && lane < 32;
             at = scale_at(j, c);
+            if constexpr (F == kLevels) left = (p.K >> 6) - 2 * c;
+            else left = w.G - ((c * kChunk) >> w.gshift);
             if constexpr (F == kLevels) {
                 const uint32_t blk = at >> w.bshift;
                 f.s = __builtin_amdgcn_raw_buffer_load_b128(sbuf, lane_in ? 4 * blk : kOutside, 0, 0);
@@ -630,7 +627,7 @@ struct RowTiles {
                     } else {
                         v = as_float(o == 0 ? f.s[0] : o == 1 ? f.s[1] : o == 2 ? f.s[2] : f.s[3]);
                     }
-                    slds[lane * kSPitch + e] = (floatx2_t){v, 0.0f};
+                    slds[lane * kSPitch + e] = (floatx2_t){e < left ? v : 0.0f, 0.0f};
                 }
             } else {
                 const uint32_t sh = 8 * ((2 * at + sfirst) & 2);
@@ -643,6 +640,10 @@ struct RowTiles {
                 }
                 zv[0] = __builtin_amdgcn_alignbyte(f.z[1], f.z[0], at + zfirst);
                 if constexpr (NG == 4) zv[1] = __builtin_amdgcn_alignbyte(f.z[2], f.z[1], at + zfirst);
+                // What lies behind the row's last group (the next row's, or memory of somebody else) meets activations
+                // of 0, but may be an infinity or a NaN: a scale of 0 instead.
+#pragma unroll
+                for (int i = 0; i < NG; ++i) sv[i] &= left >= 2 * i + 2 ? 0xFFFFFFFFu : left == 2 * i + 1 ? 0xFFFFu : 0u;
                 if constexpr (NG == 1) {                         // groups of 256 and more: both chunks in one
                     if (w.gshift > 7) {
                         sv[0] = (sv[0] & 0xFFFFu) | (sv[0] << 16);

@@ -142,3 +142,34 @@ def test_graph_replays_and_streams():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, eager)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 16])
+def test_memory_behind_the_scales_is_not_used(group, M):
+    """Scales and zero points that end inside a dword, and at a row that ends inside a chunk, with NaN behind them."""
+    for N, K in ((1, 1), (1, 32), (3, 33), (5, 160), (7, 300)):
+        say(f"case: gemv_int4 NaN behind the scales M={M} N={N} K={K} group={group}")
+        w, x, ref, tol = _case(11, M, N, K, group, True, torch.bfloat16, torch.float16)
+        n = w.scales.numel()
+        sb = torch.full((n + 64,), float("nan"), dtype=torch.float16, device="cuda")
+        zb = torch.full((n + 64,), 255, dtype=torch.uint8, device="cuda")
+        sb[:n] = w.scales.reshape(-1)
+        zb[:n] = w.zeros.reshape(-1)
+        st = qk.qk_int4_state_init(N, K, group, w.codes, sb[:n].view(N, -1), zb[:n].view(N, -1))
+        _check(qk.qk_gemv_int4(x, st), ref, tol, f"N={N} K={K} group={group}")
+
+
+@pytest.mark.parametrize("M", [1, 8])
+def test_a_row_of_infinite_scales_stays_in_its_outputs(M):
+    """The scales behind a row's last group are the next row's."""
+    say(f"case: gemv_int4 infinite scales in one row M={M}")
+    for group, K in ((32, 160), (64, 192), (128, 384)):
+        w, x, ref, tol = _case(12, M, 40, K, group, True, torch.bfloat16, torch.float16)
+        s = w.scales.clone()
+        s[17] = float("inf")
+        st = qk.qk_int4_state_init(40, K, group, w.codes, s, w.zeros)
+        y = qk.qk_gemv_int4(x, st)
+        keep = torch.arange(40, device="cuda") != 17
+        assert torch.equal(y[:, keep], w.gemv(x)[:, keep])
+        assert not bool(torch.isfinite(y[:, 17]).any())

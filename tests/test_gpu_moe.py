@@ -260,3 +260,22 @@ def test_decode_layer_of_both_operators():
     y2 = qk.qk_moe_nf4(hidden, lg, 2, un.state, dn.state)
     ref, bound = moe_f64(hidden, routes, lambda e: (un.f64(e)[:I], un.f64(e)[I:]), dn.f64)
     _check(y2, ref, _tolerance(hidden, routes, un, dn, I, H, torch.bfloat16, ref, bound), "NF4 layer")
+
+
+def test_a_row_of_infinite_block_scales_stays_in_its_outputs():
+    """K = 64 * odd: the chunk that holds a row's end reaches into the next row's blocks."""
+    say("case: moe_nf4 infinite block scales: of an expert that nobody chooses, of one row of a chosen one")
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    E, H, I, block = 3, 192, 64, 64
+    up, down = (Nf4Experts(gen, E, 2 * I, H, block, qk.NF4, False), Nf4Experts(gen, E, H, I, block, qk.NF4, False))
+    x = torch.randn((2, H), generator=gen, device="cuda").to(torch.bfloat16)
+    lg = torch.tensor([[1.0, float("-inf"), 0.0]] * 2, device="cuda")         # expert 1 lies between the chosen ones
+    want = qk.qk_moe_nf4(x, lg, 2, up.state, down.state)
+    assert bool(torch.isfinite(want).all())
+    for e, n in ((up, 2 * I * H), (down, H * I)):
+        e.qw.absmax[n // block:2 * n // block] = float("inf")                 # the blocks of expert 1 alone
+    assert torch.equal(qk.qk_moe_nf4(x, lg, 2, up.state, down.state), want)
+    down.qw.absmax[2 * H + 17] = float("inf")                                 # row 17 of expert 2: output 17
+    y = qk.qk_moe_nf4(x, lg, 2, up.state, down.state)
+    keep = torch.arange(H, device="cuda") != 17
+    assert torch.equal(y[:, keep], want[:, keep]) and not bool(torch.isfinite(y[:, 17]).any())
