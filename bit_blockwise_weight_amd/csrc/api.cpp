@@ -153,6 +153,15 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 // Largest H and I of a mixture-of-experts layer (byte offsets into its activations stay in 32 bits).
 constexpr int64_t kMaxMoeDim = (int64_t)1 << 20;
 
+// Offsets into one expert's weights stay in 32 bits: so many bytes from the first of its rows to the last one that the
+// kernels form an offset of (behind the matrix nothing is read, but they walk in steps of 16 rows and more).
+qk_status check_expert(const char* who, const char* which, int64_t rows, int64_t row_bytes) {
+    if (rows * row_bytes >= ((int64_t)1 << 31) - (1 << 16))
+        return fail(QK_ERR_UNSUPPORTED, "%s: %s: an expert's matrix passes 32-bit offsets (%lld rows of %lld bytes)", who,
+                    which, (long long)rows, (long long)row_bytes);
+    return QK_OK;
+}
+
 // The checks that both mixture-of-experts calls share, for stacked weights [up_rows, H] and [down_rows, I].
 qk_status check_moe(const char* who, const qk::MoeItem& m, int64_t up_rows, int64_t down_rows, void* workspace,
                     size_t workspace_bytes) {
@@ -896,6 +905,8 @@ qk_status qk_moe_int4(const void* x, int32_t dtype, int32_t T, const void* logit
     const qk::MoeItem m{x, logits, y, gate_up->cols, down->cols, logits_dtype, T, E, top_k, renormalize != 0,
                         dtype == QK_F16};
     v = check_moe("qk_moe_int4", m, gate_up->rows, down->rows, workspace, workspace_bytes);
+    if (v == QK_OK) v = check_expert("qk_moe_int4", "gate_up", m.I + 16, gate_up->code_stride);
+    if (v == QK_OK) v = check_expert("qk_moe_int4", "down", m.H + 16, down->code_stride);
     if (v != QK_OK) return v;
     const qk_status dev = ensure_device();
     if (dev != QK_OK) return dev;
@@ -911,6 +922,10 @@ qk_status qk_moe_nf4(const void* x, int32_t T, const void* logits, int32_t logit
     if (v != QK_OK) return v;
     const qk::MoeItem m{x, logits, y, gate_up->cols, down->cols, logits_dtype, T, E, top_k, renormalize != 0, 0};
     v = check_moe("qk_moe_nf4", m, gate_up->rows, down->rows, workspace, workspace_bytes);
+    // An element's block is found from its index, unsigned, in gate and up together or in down: 2^32 of them are 2^31
+    // bytes.  The last item of a run may start 256 rows behind the end.
+    if (v == QK_OK) v = check_expert("qk_moe_nf4", "gate_up", 2 * m.I + 512, m.H / 2);
+    if (v == QK_OK) v = check_expert("qk_moe_nf4", "down", m.H + 512, m.I / 2);
     if (v != QK_OK) return v;
     if (m.H % 64 != 0 || m.I % 64 != 0)
         return fail(QK_ERR_UNSUPPORTED, "qk_moe_nf4: H and I must be multiples of 64 (got %lld, %lld)", (long long)m.H,

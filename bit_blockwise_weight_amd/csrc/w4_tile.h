@@ -255,7 +255,7 @@ struct Rows {
     int64_t base[RT];
     int32_t off[RT];
     int32_t step, group_step;
-    int32_t count;
+    int32_t count;           // (count + 16) rows of codes stay under 2^31 - 2^16 bytes
     const void* x;           // 16-bit values, or fp32 (kSplit)
     const uint8_t* xrow;     // activation m is row xrow[m] of x; NULL: row m
     int32_t K;
@@ -594,10 +594,12 @@ struct RowTiles {
             }
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const int32_t coff = (j + p.off[r]) * stride + c * (kChunk / 2);
+                // tiles behind the last row, too, are outside: no offset of theirs is formed
+                const bool in_tile = in && j + p.off[r] < p.count;
+                const int32_t coff = in_tile ? (j + p.off[r]) * stride + c * (kChunk / 2) : kOutside;
 #pragma unroll
                 for (int q = 0; q < 2; ++q)                      // rows 8 q + lane / 8
-                    f.c[r][q] = __builtin_amdgcn_raw_buffer_load_b128(cbuf[r], voff, in ? coff + 8 * q * stride : kOutside,
+                    f.c[r][q] = __builtin_amdgcn_raw_buffer_load_b128(cbuf[r], voff, in_tile ? coff + 8 * q * stride : kOutside,
                                                                       kNontemporal);
             }
         };

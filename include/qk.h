@@ -679,8 +679,10 @@ qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t H, int64_t I, 
  *   gate_up: host pointer to the descriptor of the stacked [E * 2 * I, H] weights: expert e's
  *     gate in rows [2 e I, 2 e I + I), its up projection in the next I rows.
  *   down: descriptor of the stacked [E * H, I] weights: expert e in rows [e H, e H + H).
- *   H and I follow from the descriptors (each at most 2^20).  qk_moe_nf4 needs H and I to be multiples of 64
- *     (else QK_ERR_UNSUPPORTED) and 16-byte aligned codes.
+ *   H and I follow from the descriptors (each at most 2^20).  One expert's gate, up or down matrix (qk_moe_nf4:
+ *     gate and up together) must stay under about 2 GiB of codes (else QK_ERR_UNSUPPORTED); the stack may be as
+ *     large as memory.  qk_moe_nf4 needs H and I to be multiples of 64 (else QK_ERR_UNSUPPORTED) and 16-byte
+ *     aligned codes.
  *   y: device, [T, H] of dtype, written.  May be x itself.
  *   workspace: device, >= qk_moe_workspace_size(T, top_k, H, I) bytes, 16-byte aligned;
  *     contents on entry ignored; no overlap with the other buffers.  Calls that may run at

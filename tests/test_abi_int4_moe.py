@@ -156,6 +156,32 @@ def test_moe_nf4_refusals(L):
     assert _moe_nf4(L, bad, down) == qk.QK_ERR_BAD_STATE and _moe_nf4(L, up, bad) == qk.QK_ERR_BAD_STATE
 
 
+def test_moe_refuses_experts_that_pass_32_bit_offsets(L):
+    """(I + 16) rows of gate_up codes, (H + 16) of down: under 2^31 - 2^16 bytes, whatever a row's padding."""
+    ws = dict(E=1, top_k=1, T=1, bytes_=1 << 30, ws=1 << 40)
+    top = (1 << 31) - (1 << 16)
+    for I, stride, good in ((48, 1 << 24, True), (112, 1 << 24, False), (241, (top // 257 // 16) * 16, True),
+                            (241, (top // 257 // 16 + 1) * 16, False)):
+        up, down = _init(L, rows=2 * I, cols=128, stride=stride)[1], _init(L, rows=128, cols=I, stride=128)[1]
+        if good:
+            if not torch.cuda.is_available():
+                assert _moe(L, up, down, **ws) == qk.QK_ERR_NO_DEVICE
+        else:
+            assert _moe(L, up, down, **ws) == qk.QK_ERR_UNSUPPORTED and "gate_up" in qk.qk_last_error()
+        up, down = _init(L, rows=256, cols=I, stride=128)[1], _init(L, rows=I, cols=128, stride=stride)[1]
+        if good:
+            if not torch.cuda.is_available():
+                assert _moe(L, up, down, **ws) == qk.QK_ERR_NO_DEVICE
+        else:
+            assert _moe(L, up, down, **ws) == qk.QK_ERR_UNSUPPORTED and "down" in qk.qk_last_error()
+    big = 1 << 20
+    ws.update(x=1 << 36, y=1 << 37)
+    for H, I, rc in ((big, 2048, qk.QK_ERR_UNSUPPORTED), (2048, big, qk.QK_ERR_UNSUPPORTED), (big, 1024, qk.QK_ERR_NO_DEVICE)):
+        if rc == qk.QK_ERR_NO_DEVICE and torch.cuda.is_available():
+            continue
+        assert _moe_nf4(L, _nf4_state(L, 2 * I, H), _nf4_state(L, H, I, 32 * A), **ws) == rc, (H, I)
+
+
 def test_binding_refuses_host_tensors_and_wrong_shapes(L):
     z = torch.zeros
     codes, scales = z((4, 16), dtype=torch.uint8), z((4, 1), dtype=torch.float16)
