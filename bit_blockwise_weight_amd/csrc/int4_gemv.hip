@@ -90,7 +90,7 @@ constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 size_t x_lds(int M, int ng, int64_t K, bool resident) {
     return mi_for(M) == 1 ? w4_fix_bytes(4, M, ng, K, resident) : w4_x_bytes(4, M, K, resident);
 }
-size_t resident_lds(int M, int ng, int64_t K) { return w4_fixed_bytes(ng, kRt, mi_for(M), true) + x_lds(M, ng, K, true); }
+size_t resident_lds(int M, int ng, int64_t K) { return w4_fixed_bytes(kInt4Bf16, ng, kRt, mi_for(M), true) + x_lds(M, ng, K, true); }
 bool resident_for(int M, int ng, int64_t K) { return resident_lds(M, ng, K) <= kLdsBytes; }
 
 constexpr int32_t kNever = 0x7FFFFFFF;
@@ -189,7 +189,7 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             ++n;
         }
         const size_t lds = resident ? resident_lds(M, ng, kmax)
-                                    : w4_fixed_bytes(ng, kRt, mi_for(M), false) + x_lds(M, ng, kmax, false);
+                                    : w4_fixed_bytes(kInt4Bf16, ng, kRt, mi_for(M), false) + x_lds(M, ng, kmax, false);
         const int per_cu = lds > kLdsBytes / 2 ? 1 : 2;
         // the workgroups that the CUs hold at a time, dealt to the tasks by their work, at most one per item
         int64_t grid = 0;

@@ -31,16 +31,19 @@ constexpr int kMaxT = 16;
 constexpr int kMaxE = 256;
 constexpr int kMaxK = 16;
 constexpr int kMaxPairs = kMaxT * kMaxK;
-constexpr int kThreads = 512;
+template <int F>
+constexpr int kThreads = 64 * w4_waves((Form)F);
 
 // Routing result: the experts that have a token, in increasing order, and their tokens, in increasing
-// order, one after the other.
+// order, one after the other.  An expert with more tokens than the up kernel takes at once is listed again for
+// the rest of them, so that every listing is the same work (its weights are then read more than once, from cache
+// mostly).
 struct Routes {
-    int32_t nactive;
+    int32_t listed;
     int32_t pad[3];
     int32_t chosen[kMaxT];                // experts of each token (its positions 0, 1, ... are taken)
-    int32_t expert[kMaxE];
-    int32_t start[kMaxE + 4];             // first entry of each listed expert below; one more ends the last
+    int32_t expert[kMaxPairs];
+    int32_t start[kMaxPairs + 4];         // first entry of each listed expert below; one more ends the last
     float w[kMaxPairs];                   // weight of the entry
     uint8_t tok[kMaxPairs];               // its token
     uint8_t pair[kMaxPairs];              // its row of h: t * top_k + position
@@ -51,6 +54,7 @@ struct RouteArgs {
     const void* logits;
     int32_t dtype;
     int32_t T, E, top_k, renorm;
+    int32_t most;                         // tokens of a listing, at most
 };
 
 __device__ __forceinline__ float load_logit(const void* p, int32_t dtype, int i) {
@@ -69,7 +73,6 @@ struct RouteScratch {
     float den[kMaxT];
     uint32_t mask[kMaxE];                 // tokens of each expert
     int32_t first[kMaxE];                 // its first entry
-    uint32_t any[kMaxE / 32];             // experts with a token
     int32_t total[4];
 };
 
@@ -97,24 +100,24 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// Fills r (LDS) from the logits, by one workgroup of kThreads.  Every logit's rank among its token's is counted
+// Fills r (LDS) from the logits, by one workgroup of kThr threads.  Every logit's rank among its token's is counted
 // at once (how many are larger, or equal with a lower index): the rank is the position, so the choice takes no
 // rounds that wait for each other.  The loops stay rolled: the code runs once, and fetching it is much of its time.
+template <int kThr>
 __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Routes& r) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int padded = (a.E + 15) & ~15;
 #pragma unroll 1
-    for (int t = wave; t < a.T; t += 8)
+    for (int t = wave; t < a.T; t += kThr / 64)
 #pragma unroll 1
         for (int e = lane; e < padded; e += 64) s.logit[t][e] = e < a.E ? load_logit(a.logits, a.dtype, t * a.E + e) : -INFINITY;
     if (tid < kMaxE) {
         s.mask[tid] = 0;
         s.best[tid / kMaxK][tid % kMaxK] = -INFINITY;
     }
-    if (tid < kMaxE / 32) s.any[tid] = 0;
     __syncthreads();
 #pragma unroll 1
-    for (int i = tid; i < a.T * a.E; i += kThreads) {
+    for (int i = tid; i < a.T * a.E; i += kThr) {
         const int t = i / a.E, e = i - t * a.E;
         const float v = s.logit[t][e];
         int rank = 0;
@@ -130,7 +133,6 @@ __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Route
             s.best[t][rank] = v;
             s.who[t][rank] = e;
             atomicOr(&s.mask[e], 1u << t);
-            atomicOr(&s.any[e >> 5], 1u << (e & 31));
         }
     }
     __syncthreads();
@@ -139,7 +141,7 @@ __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Route
     float p = 0.0f, den = 1.0f;
     bool mine = false;
     uint32_t mk = 0;
-    int scan = 0;
+    int scan = 0;                                        // tokens of the experts up to here, and listings << 16
     if (tid < kMaxE) {
         const float v = s.best[t][k], top = s.best[t][0];
         mine = t < a.T && k < a.top_k && v != -INFINITY;
@@ -148,12 +150,12 @@ __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Route
         const int chosen = __popc((uint32_t)(__ballot(mine) >> (lane & 48)) & 0xFFFFu);
         if (k == 0 && t < a.T) r.chosen[t] = chosen;
         mk = s.mask[tid];
-        scan = wave_scan(__popc(mk));
+        scan = wave_scan(__popc(mk) + ((__popc(mk) + a.most - 1) / a.most << 16));
         if (lane == 63) s.total[wave] = scan;
     }
     if (!a.renorm) {                                     // the sum over every expert instead: a wave per token
 #pragma unroll 1
-        for (int tt = wave; tt < a.T; tt += 8) {
+        for (int tt = wave; tt < a.T; tt += kThr / 64) {
             const float top = s.best[tt][0];
             float sum = 0.0f;
 #pragma unroll 1
@@ -169,26 +171,23 @@ __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Route
     }
     __syncthreads();
     if (tid < kMaxE) {
-        int first = scan - __popc(mk), entries = 0, slot = 0, listed = 0;
+        const int tokens = __popc(mk), listings = (tokens + a.most - 1) / a.most;
+        int before = scan - tokens - (listings << 16), all = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            if (w < wave) first += s.total[w];
-            entries += s.total[w];
+            if (w < wave) before += s.total[w];
+            all += s.total[w];
         }
-#pragma unroll
-        for (int w = 0; w < kMaxE / 32; ++w) {
-            const uint32_t bits = s.any[w];
-            listed += __popc(bits);
-            slot += __popc(w < tid >> 5 ? bits : w == tid >> 5 ? bits & ((1u << (tid & 31)) - 1) : 0u);
-        }
+        const int first = before & 0xFFFF, slot = before >> 16;
         s.first[tid] = first;
-        if (mk) {
-            r.expert[slot] = tid;
-            r.start[slot] = first;
+#pragma unroll 1
+        for (int i = 0; i < listings; ++i) {
+            r.expert[slot + i] = tid;
+            r.start[slot + i] = first + i * a.most;
         }
         if (tid == 0) {
-            r.nactive = listed;
-            r.start[listed] = entries;
+            r.listed = all >> 16;
+            r.start[all >> 16] = all & 0xFFFF;
         }
     }
     __syncthreads();
@@ -241,7 +240,7 @@ size_t x_lds(int tokens, bool split, int64_t K, bool resident) {
 }
 template <int F, int NG, int RT, int MI>
 bool fits(int tokens, bool split, int64_t K) {
-    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes(NG, RT, MI, true) + x_lds<F, NG, MI>(tokens, split, K, true) <=
+    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes((Form)F, NG, RT, MI, true) + x_lds<F, NG, MI>(tokens, split, K, true) <=
            kLdsBytes;
 }
 // Tokens that a pass over an expert's rows takes; the down product needs two operand rows for one, but not in fixed
@@ -250,21 +249,21 @@ template <int F, int MI, bool kSplit>
 constexpr int kTokens = kSplit && (F == kLevels || MI > 1) ? 2 * MI : 4 * MI;
 
 template <int F, int NG, int MI, bool kResident>
-__global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertArgs<F> p, RouteArgs ra, Routes* keep) {
+__global__ __launch_bounds__(kThreads<F>, 4) void moe_up_kernel(ExpertArgs<F> p, RouteArgs ra, Routes* keep) {
     extern __shared__ __align__(16) uint8_t lds[];
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
     uint8_t* work = lds + (F == kLevels ? kTabBytes : 0) + sizeof(Routes);
     static_assert(sizeof(RouteScratch) <= Tiles::kFixedBytes);
     // Every workgroup routes for itself (a launch of its own would cost more); the first one keeps the result.
     Routes& routes = *reinterpret_cast<Routes*>(lds + (F == kLevels ? kTabBytes : 0));
-    route(ra, *reinterpret_cast<RouteScratch*>(work), routes);
+    route<kThreads<F>>(ra, *reinterpret_cast<RouteScratch*>(work), routes);
     if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < (int)(sizeof(Routes) / 4); i += kThreads)
+        for (int i = threadIdx.x; i < (int)(sizeof(Routes) / 4); i += kThreads<F>)
             reinterpret_cast<uint32_t*>(keep)[i] = reinterpret_cast<const uint32_t*>(&routes)[i];
-    if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads);
+    if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads<F>);
     // an item: per row group 16 rows of gate and the same of up of one listed expert; equal shares of the items
-    const int step = 128 >> p.kwl;
-    const uint32_t tiles = (uint32_t)(p.Ipad + step - 1) / step, all = tiles * (uint32_t)routes.nactive;
+    const int step = (16 * Tiles::W) >> p.kwl;
+    const uint32_t tiles = (uint32_t)(p.Ipad + step - 1) / step, all = tiles * (uint32_t)routes.listed;
     const uint32_t share = all / p.grid, more = all % p.grid, b = blockIdx.x;
     uint32_t lo = b * share + (b < more ? b : more);
     const uint32_t hi = lo + share + (b < more);
@@ -286,35 +285,31 @@ __global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_up_kernel(ExpertA
         r.x_rows = p.x_rows;
         r.x_aligned = p.x_aligned;
         r.kwl = p.kwl;
-        // 4 MI tokens at a time (an expert rarely has more)
-        for (int m0 = 0; m0 < count; m0 += 4 * MI) {
-            const int M = count - m0 < 4 * MI ? count - m0 : 4 * MI;
-            r.xrow = routes.tok + first + m0;
-            r.M = M;
-            Tiles::run(p.w, r, i0, i1, work, [&](int item, int q, const float* put) {
+        r.xrow = routes.tok + first;
+        r.M = count;
+        Tiles::run(p.w, r, i0, i1, work, [&](int item, int q, const float* put) {
 #pragma unroll
-                for (int s = threadIdx.x & 63; s < 64 * MI; s += 64) {
-                    const int m = Tiles::act_of(s);
-                    const int i = item * step + 16 * q + (s & 15);
-                    if (m < M && i < p.Ipad) {
-                        const float gate = Tiles::sum(put, p.kwl, q, 0, s), up = Tiles::sum(put, p.kwl, q, 1, s);
-                        const float v = gate / (1.0f + expf(-gate)) * up;
-                        p.out[(int64_t)routes.pair[first + m0 + m] * p.Ipad + i] = i < p.I ? v : 0.0f;
-                    }
+            for (int s = threadIdx.x & 63; s < 64 * MI; s += 64) {
+                const int m = Tiles::act_of(s);
+                const int i = item * step + 16 * q + (s & 15);
+                if (m < count && i < p.Ipad) {
+                    const float gate = Tiles::sum(put, p.kwl, q, 0, s), up = Tiles::sum(put, p.kwl, q, 1, s);
+                    const float v = gate / (1.0f + expf(-gate)) * up;
+                    p.out[(int64_t)routes.pair[first + m] * p.Ipad + i] = i < p.I ? v : 0.0f;
                 }
-            });
-        }
+            }
+        });
     }
 }
 
 template <int F, int NG, int RT, int MI, bool kResident>
-__global__ __launch_bounds__(kThreads, 2 * kPerCu<F>) void moe_down_kernel(ExpertArgs<F> p) {
+__global__ __launch_bounds__(kThreads<F>, 4) void moe_down_kernel(ExpertArgs<F> p) {
     extern __shared__ __align__(16) uint8_t lds[];
     typedef RowTiles<F, NG, RT, MI, kResident, true> Tiles;
     uint8_t* work = lds + (F == kLevels ? kTabBytes : 0);
-    if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads);
-    const int step = (16 * RT * 8) >> p.kwl;
-    const uint32_t tiles = (uint32_t)(p.H + step - 1) / step, all = tiles * (uint32_t)p.routes->nactive;
+    if constexpr (F == kLevels) build_table(lds, p.w.levels, threadIdx.x, kThreads<F>);
+    const int step = (16 * RT * Tiles::W) >> p.kwl;
+    const uint32_t tiles = (uint32_t)(p.H + step - 1) / step, all = tiles * (uint32_t)p.routes->listed;
     const uint32_t share = all / p.grid, more = all % p.grid, b = blockIdx.x;
     uint32_t lo = b * share + (b < more ? b : more);
     const uint32_t hi = lo + share + (b < more);
@@ -382,23 +377,27 @@ hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int
                        x_lds<F, NG, MI>(tokens, false, p.H, kResident);
     const hipError_t e = allow_lds<&moe_up_kernel<F, NG, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
-    const int64_t items = (int64_t)(p.Ipad + (128 >> p.kwl) - 1) / (128 >> p.kwl) * listed;
+    const int step = (16 * Tiles::W) >> p.kwl;
+    const int64_t items = (int64_t)(p.Ipad + step - 1) / step * listed;
     p.grid = (uint32_t)workgroups<F>(items, lds);
-    moe_up_kernel<F, NG, MI, kResident><<<dim3(p.grid), dim3(kThreads), lds, s>>>(p, ra, keep);
+    moe_up_kernel<F, NG, MI, kResident><<<dim3(p.grid), dim3(kThreads<F>), lds, s>>>(p, ra, keep);
     return hipGetLastError();
 }
 
 template <int F, int NG, int MI>
-hipError_t launch_up_mi(const ExpertArgs<F>& p, const RouteArgs& ra, Routes* keep, int32_t listed, hipStream_t s) {
+hipError_t launch_up_mi(const ExpertArgs<F>& p, RouteArgs ra, Routes* keep, int32_t* listed, hipStream_t s) {
     const int tokens = std::min(ra.T, kTokens<F, MI, false>);
-    if (fits<F, NG, 2, MI>(tokens, false, p.H)) return launch_up_one<F, NG, MI, true>(p, ra, keep, tokens, listed, s);
-    return launch_up_one<F, NG, MI, false>(p, ra, keep, tokens, listed, s);
+    ra.most = kTokens<F, MI, false>;
+    *listed = std::min(ra.E * ((ra.T + ra.most - 1) / ra.most), ra.T * ra.top_k);
+    if (fits<F, NG, 2, MI>(tokens, false, p.H)) return launch_up_one<F, NG, MI, true>(p, ra, keep, tokens, *listed, s);
+    return launch_up_one<F, NG, MI, false>(p, ra, keep, tokens, *listed, s);
 }
 
 // Tokens that a pass over an expert's rows takes (4 MI): by the number that it has on average.
+// listed: set to the most listings that there can be
 template <int F, int NG>
-hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int32_t listed, hipStream_t s) {
-    const RouteArgs ra{m.logits, m.logits_dtype, m.T, m.E, m.top_k, m.renorm};
+hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int32_t* listed, hipStream_t s) {
+    const RouteArgs ra{m.logits, m.logits_dtype, m.T, m.E, m.top_k, m.renorm, 0};
     const int pairs = m.T * m.top_k;
     if (m.T <= 4 || pairs <= 2 * m.E) return launch_up_mi<F, NG, 1>(p, ra, keep, listed, s);
     if (F == kLevels || m.T <= 8 || pairs <= 5 * m.E) return launch_up_mi<F, NG, 2>(p, ra, keep, listed, s);
@@ -412,9 +411,9 @@ hipError_t launch_down_one(ExpertArgs<F> p, int tokens, int32_t listed, hipStrea
     const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + x_lds<F, NG, MI>(tokens, true, p.I, kResident);
     const hipError_t e = allow_lds<&moe_down_kernel<F, NG, RT, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
-    const int64_t step = (16 * RT * 8) >> p.kwl, items = (p.H + step - 1) / step * listed;
+    const int64_t step = (16 * RT * Tiles::W) >> p.kwl, items = (p.H + step - 1) / step * listed;
     p.grid = (uint32_t)workgroups<F>(items, lds);
-    moe_down_kernel<F, NG, RT, MI, kResident><<<dim3(p.grid), dim3(kThreads), lds, s>>>(p);
+    moe_down_kernel<F, NG, RT, MI, kResident><<<dim3(p.grid), dim3(kThreads<F>), lds, s>>>(p);
     return hipGetLastError();
 }
 
@@ -485,7 +484,7 @@ ExpertArgs<F> expert_args(const MoeItem& m, const Buffers& b, bool up) {
 }
 
 template <int F>
-hipError_t launch_up_int4(const MoeItem& m, const Buffers& b, const qk_int4_state* w, int32_t listed, hipStream_t s) {
+hipError_t launch_up_int4(const MoeItem& m, const Buffers& b, const qk_int4_state* w, int32_t* listed, hipStream_t s) {
     ExpertArgs<F> p = expert_args<F>(m, b, true);
     p.w = int4_view(w);
     const int ng = int4_groups_per_chunk(w->group);
@@ -509,8 +508,8 @@ size_t moe_workspace_bytes(int32_t T, int32_t top_k, int64_t H, int64_t I) {
 hipError_t launch_moe_int4(const MoeItem& m, const qk_int4_state* gate_up, const qk_int4_state* down, void* workspace,
                            hipStream_t s) {
     const Buffers b = buffers(m, workspace);
-    const int32_t listed = std::min(m.E, m.T * m.top_k);
-    hipError_t e = m.f16 ? launch_up_int4<kInt4F16>(m, b, gate_up, listed, s) : launch_up_int4<kInt4Bf16>(m, b, gate_up, listed, s);
+    int32_t listed = 0;
+    hipError_t e = m.f16 ? launch_up_int4<kInt4F16>(m, b, gate_up, &listed, s) : launch_up_int4<kInt4Bf16>(m, b, gate_up, &listed, s);
     if (e != hipSuccess) return e;
     ExpertArgs<kInt4Bf16> p = expert_args<kInt4Bf16>(m, b, false);
     p.w = int4_view(down);
@@ -524,10 +523,10 @@ hipError_t launch_moe_int4(const MoeItem& m, const qk_int4_state* gate_up, const
 hipError_t launch_moe_levels(const MoeItem& m, const MatArgs& gate_up, const MatArgs& down, void* workspace,
                              hipStream_t s) {
     const Buffers b = buffers(m, workspace);
-    const int32_t listed = std::min(m.E, m.T * m.top_k);
+    int32_t listed = 0;
     ExpertArgs<kLevels> u = expert_args<kLevels>(m, b, true);
     u.w = levels_view(gate_up);
-    hipError_t e = launch_up<kLevels, 2>(u, m, b.routes, listed, s);
+    hipError_t e = launch_up<kLevels, 2>(u, m, b.routes, &listed, s);
     if (e != hipSuccess) return e;
     ExpertArgs<kLevels> d = expert_args<kLevels>(m, b, false);
     d.w = levels_view(down);

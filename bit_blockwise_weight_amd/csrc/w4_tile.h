@@ -33,6 +33,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "qk_device.h"
 #include "qk_internal.h"
@@ -194,15 +195,16 @@ struct LevelsView {
 };
 
 // Table of the 256 code bytes as (bf16 level of the high nibble, bf16 level of the low nibble),
-// 64 copies so that a lane reads its own bank: entry b of copy l at b * 256 + 4 l of LDS itself (the
-// kernels have no other LDS than the dynamic part, which starts at 0), so that a v_perm makes the address.
-constexpr int kTabBytes = 256 * 64 * 4;
+// 32 copies so that each lane of the 32 that are served at a time reads a bank of its own: entry b of copy l at
+// b * 256 + 4 l of LDS itself (the kernels have no other LDS than the dynamic part, which starts at 0), so that a
+// v_perm makes the address.  The other half of the 256 bytes holds rows of codes (RowTiles).
+constexpr int kTabBytes = 256 * 256;
 
 __device__ __forceinline__ void build_table(uint8_t* tab, const float* levels, int tid, int threads) {
-    for (int i = tid; i < 256 * 16; i += threads) {
-        const int b = i >> 4;
+    for (int i = tid; i < 256 * 8; i += threads) {
+        const int b = i >> 3;
         const uint32_t v = pack_bf16x2(levels[b >> 4], levels[b & 15]);
-        *reinterpret_cast<u32x4_t*>(tab + b * 256 + (i & 15) * 16) = (u32x4_t){v, v, v, v};
+        *reinterpret_cast<u32x4_t*>(tab + b * 256 + (i & 7) * 16) = (u32x4_t){v, v, v, v};
     }
 }
 
@@ -274,10 +276,13 @@ __device__ __forceinline__ constexpr int act_of_row(int row) { return MI * (row 
 constexpr int kLineK = 256;               // k of a 128-byte line of codes
 
 // bytes of LDS beside the activations: scales, codes, partial sums of a few items and their counters
-constexpr int w4_put_bytes(int RT, int MI) { return 8 * RT * 64 * MI * 4; }
-constexpr int w4_slots(bool resident) { return resident ? 2 : 3; }
-constexpr int w4_fixed_bytes(int NG, int RT, int MI, bool resident) {
-    return 8 * RT * 16 * ((2 * NG) | 1) * 8 + 8 * RT * 16 * 128 + w4_slots(resident) * (w4_put_bytes(RT, MI) + 32);
+constexpr int w4_waves(Form f) { return f == kLevels ? 16 : 8; }
+constexpr int w4_put_bytes(Form f, int RT, int MI) { return w4_waves(f) * RT * 64 * MI * 4; }
+constexpr int w4_slots(Form f, bool resident) { return resident || f == kLevels ? 2 : 3; }
+constexpr int w4_scale_bytes(Form f, int NG, int RT) { return w4_waves(f) * RT * 16 * ((2 * NG) | 1) * (f == kLevels ? 4 : 8); }
+constexpr int w4_code_bytes(int RT) { return 8 * RT * 16 * 128; }       // of 8 waves; 8 more have theirs beside the table
+constexpr int w4_fixed_bytes(Form f, int NG, int RT, int MI, bool resident) {
+    return w4_scale_bytes(f, NG, RT) + w4_code_bytes(RT) + w4_slots(f, resident) * (w4_put_bytes(f, RT, MI) + w4_waves(f) * 4);
 }
 constexpr size_t kLdsBytes = 160 * 1024;  // of a CU
 
@@ -315,26 +320,29 @@ inline int w4_kwl(int64_t K) {
 
 template <int F, int NG, int RT, int MI, bool kResident, bool kSplit>
 struct RowTiles {
-    static constexpr int W = 8;
+    static constexpr Form kForm = (Form)F;
+    static constexpr int W = w4_waves(kForm);
     static constexpr int kThreads = W * 64;
     static constexpr bool kFix = F != kLevels && MI == 1;       // up to four activations, in fixed point
     static constexpr int U = 2;                                 // chunks of a wave in a window
     static constexpr int kMfmas = 4 / NG;                       // MFMAs per scale group
     static constexpr int kEntries = U * NG;                     // scale groups of a wave's chunks in a window
     static constexpr int kSPitch = kEntries | 1;
-    static constexpr int kScaleBytes = W * RT * 16 * kSPitch * 8;
-    static constexpr int kCodeBytes = W * RT * 16 * 128;        // a window's codes changing layout
-    static constexpr int kPutBytes = w4_put_bytes(RT, MI);
-    static constexpr int kSlots = w4_slots(kResident);
+    static constexpr int kScaleBytes = w4_scale_bytes(kForm, NG, RT);
+    static constexpr int kCodeBytes = w4_code_bytes(RT);        // a window's codes changing layout
+    static constexpr int kCodePitch = F == kLevels ? 256 : 128; // from row to row there
+    static constexpr int kPutBytes = w4_put_bytes(kForm, RT, MI);
+    static constexpr int kSlots = w4_slots(kForm, kResident);
     // units of x per thread and batch; a window's fit one batch (kw <= 4)
-    static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : kSplit ? (MI + 1) / 2 : MI;
-    static constexpr int kFixedBytes = w4_fixed_bytes(NG, RT, MI, kResident);
-    static_assert(kFixedBytes == kScaleBytes + kCodeBytes + kSlots * (kPutBytes + 32));
+    static constexpr int kMaxM = kSplit && !kFix ? 2 * MI : 4 * MI;
+    static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : (kMaxM * 128 + kThreads - 1) / kThreads;
+    static constexpr int kFixedBytes = w4_fixed_bytes(kForm, NG, RT, MI, kResident);
 
     static_assert(RT == 2);
     // The scales of a window come by one load per kind, in lane 16 r + n for row n of tile r (a load instruction that
     // touches many lines costs as much as one that brings a kilobyte of codes): as dwords from an address rounded
     // down to 4 bytes, put right when they land.
+    typedef std::conditional_t<F == kLevels, float, floatx2_t> Scale;
     struct Fetched {
         u32x4_t c[RT][2];
         u32x4_t s;           // int4: 2 NG scales; levels: four block scales of a plain weight
@@ -351,8 +359,15 @@ struct RowTiles {
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int n = lane & 15, h = lane >> 4;
         const int kw = 1 << p.kwl, wk = wave & (kw - 1), wr = wave >> p.kwl;
-        floatx2_t* slds = reinterpret_cast<floatx2_t*>(lds) + wave * (RT * 16 * kSPitch);
+        Scale* slds = reinterpret_cast<Scale*>(lds) + wave * (RT * 16 * kSPitch);
+        // With a table the rows of codes are 256 bytes apart: eight waves' lie behind the table's entries (in front of
+        // lds, see there), those of eight more share a piece of their own, four and four.
         uint8_t* clds = lds + kScaleBytes + wave * (RT * 16 * 128);
+        if constexpr (F == kLevels) {
+            extern __shared__ __align__(16) uint8_t lds0[];
+            clds = wave < 8 ? lds0 + 128 + wave * (RT * 16 * 256)
+                            : lds + kScaleBytes + (wave & 3) * (RT * 16 * 256) + (wave >> 2 & 1) * 128;
+        }
         float* put = reinterpret_cast<float*>(lds + kScaleBytes + kCodeBytes);
         int* arrived = reinterpret_cast<int*>(lds + kScaleBytes + kCodeBytes + kSlots * kPutBytes);
         uint8_t* xlds = lds + kFixedBytes;
@@ -611,7 +626,7 @@ struct RowTiles {
             for (int r = 0; r < RT; ++r) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    *reinterpret_cast<u32x4_t*>(clds + (16 * r + 8 * q + (lane >> 3)) * 128 +
+                    *reinterpret_cast<u32x4_t*>(clds + (16 * r + 8 * q + (lane >> 3)) * kCodePitch +
                                                 16 * ((lane & 7) ^ (lane >> 3))) = f.c[r][q];
             }
             if (lane >= 32) return;
@@ -629,7 +644,7 @@ struct RowTiles {
                     } else {
                         v = as_float(o == 0 ? f.s[0] : o == 1 ? f.s[1] : o == 2 ? f.s[2] : f.s[3]);
                     }
-                    slds[lane * kSPitch + e] = (floatx2_t){e < left ? v : 0.0f, 0.0f};
+                    slds[lane * kSPitch + e] = e < left ? v : 0.0f;
                 }
             } else {
                 const uint32_t sh = 8 * ((2 * at + sfirst) & 2);
@@ -679,13 +694,13 @@ struct RowTiles {
             const int first = kResident ? c0 + wk * U : wk * U;  // the wave's first chunk in LDS
             const uint8_t* ax = xwin + arow + first * kChunk;
             const floatx2_t* xt = reinterpret_cast<const floatx2_t*>(xwin + xpair) + first * NG;
-            const floatx2_t* sp = slds + n * kSPitch;
+            const floatx2_t* sp = reinterpret_cast<const floatx2_t*>(slds) + n * kSPitch;
 #pragma unroll 1
             for (int u = 0; u < U; ++u) {
                 u32x4_t c[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
-                    c[r] = *reinterpret_cast<const u32x4_t*>(clds + (16 * r + n) * 128 + 16 * ((4 * u + h) ^ (n & 7)));
+                    c[r] = *reinterpret_cast<const u32x4_t*>(clds + (16 * r + n) * kCodePitch + 16 * ((4 * u + h) ^ (n & 7)));
                 u32x4_t a[2];
                 if constexpr (NG == 4) {                         // four products of 32 k, eight bytes a lane each
 #pragma unroll
@@ -728,13 +743,13 @@ struct RowTiles {
             }
             const int cw = c0 + wk * U;
             const uint8_t* ax = xwin + arow + 2 * (kResident ? cw * kChunk : wk * (U * kChunk));
-            const floatx2_t* sp = slds + n * kSPitch;
+            const Scale* sp = slds + n * kSPitch;
 #pragma unroll 1
             for (int u = 0; u < U; ++u) {
                 u32x4_t c[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
-                    c[r] = *reinterpret_cast<const u32x4_t*>(clds + (16 * r + n) * 128 + 16 * ((4 * u + h) ^ (n & 7)));
+                    c[r] = *reinterpret_cast<const u32x4_t*>(clds + (16 * r + n) * kCodePitch + 16 * ((4 * u + h) ^ (n & 7)));
                 u32x4_t a[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -751,7 +766,7 @@ struct RowTiles {
                         if constexpr (F == kLevels) {
 #pragma unroll
                             for (int r = 0; r < RT; ++r)
-                                acc[r] = mfma<F>(a[j], decode8_table(c[r][j], 4 * lane), acc[r]);
+                                acc[r] = mfma<F>(a[j], decode8_table(c[r][j], 4 * (lane & 31)), acc[r]);
                         } else {
                             xs = mfma<F>(a[j], ones<F>(), xs);
 #pragma unroll
@@ -760,11 +775,15 @@ struct RowTiles {
                     }
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const floatx2_t s = sp[16 * r * kSPitch + u * NG + q];
+                        const Scale s = sp[16 * r * kSPitch + u * NG + q];
 #pragma unroll
                         for (int i = 0; i < MI; ++i) {
-                            if constexpr (F != kLevels) y[r][i] = fmaf(-s[1], xs[i], y[r][i]);
-                            y[r][i] = fmaf(s[0], acc[r][i], y[r][i]);
+                            if constexpr (F == kLevels) {
+                                y[r][i] = fmaf(s, acc[r][i], y[r][i]);
+                            } else {
+                                y[r][i] = fmaf(-s[1], xs[i], y[r][i]);
+                                y[r][i] = fmaf(s[0], acc[r][i], y[r][i]);
+                            }
                         }
                     }
                 }
@@ -879,11 +898,12 @@ struct RowTiles {
     // order.  Its row in the tile is o % 16, its activation row act_of(o).
     static __device__ __forceinline__ float sum(const float* put, int kwl, int q, int r, int o) {
         const float* first = put + ((q << kwl) * RT + r) * (64 * MI) + o;
-        float p[W], v = 0.0f;                                    // all reads first, then the sum
+        constexpr int kMost = 8;                                 // waves that split a row
+        float p[kMost], v = 0.0f;                                // all reads first, then the sum
 #pragma unroll
-        for (int w = 0; w < W; ++w) p[w] = first[(w < (1 << kwl) ? w : 0) * (RT * 64 * MI)];
+        for (int w = 0; w < kMost; ++w) p[w] = first[(w < (1 << kwl) ? w : 0) * (RT * 64 * MI)];
 #pragma unroll
-        for (int w = 0; w < W; ++w) v += w < (1 << kwl) ? p[w] : 0.0f;
+        for (int w = 0; w < kMost; ++w) v += w < (1 << kwl) ? p[w] : 0.0f;
         return v;
     }
     static __device__ __forceinline__ int act_of(int o) { return MI * ((o & 63) >> 4) + (o >> 6); }
