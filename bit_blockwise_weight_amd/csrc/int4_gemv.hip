@@ -181,7 +181,7 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             t.N = st->rows;
             t.K = st->cols;
             t.x_aligned = st->cols % 8 == 0 && reinterpret_cast<uintptr_t>(items[i].x) % 4 == 0;
-            t.kwl = resident ? w4_kwl(st->cols) : 2;
+            t.kwl = w4_kwl(kInt4Bf16, st->cols, st->rows, 16 * kRt, resident ? 3 : 2);
             tiles[n] = (st->rows + 15) / 16;
             items_of[n] = (tiles[n] + ((kRt * 8) >> t.kwl) - 1) / ((kRt * 8) >> t.kwl);
             work += (double)tiles[n] * (double)st->cols;

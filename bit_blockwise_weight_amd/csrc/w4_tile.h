@@ -312,10 +312,14 @@ inline size_t w4_fix_bytes(int kw, int M, int NG, int64_t K, bool resident) {
     const size_t k = resident ? (size_t)((K + kLineK - 1) / kLineK) * kLineK : (size_t)kw * kLineK;
     return (size_t)M * (3 * (k + 16) + k / kChunk * NG * 8);
 }
-// log2 of the waves (of 8) that split a row of K: as many as it has lines
-inline int w4_kwl(int64_t K) {
-    const int64_t n = (K + kLineK - 1) / kLineK;
-    return n > 4 ? 3 : n > 2 ? 2 : n > 1 ? 1 : 0;
+// log2 of the waves that split a row of K: as many as it has lines, up to 8; more (some then have nothing to do) as
+// long as there are fewer items than CUs.  rows: of all items, in pieces of `piece` rows that a wave takes
+inline int w4_kwl(Form f, int64_t K, int64_t rows, int piece, int most) {
+    const int64_t n = (K + kLineK - 1) / kLineK, pieces = (rows + piece - 1) / piece;
+    int kwl = n > 4 ? 3 : n > 2 ? 2 : n > 1 ? 1 : 0;
+    if (kwl > most) kwl = most;
+    while (kwl < most && pieces * ((int64_t)1 << kwl) < (int64_t)w4_waves(f) * device_cu_count()) ++kwl;
+    return kwl;
 }
 
 template <int F, int NG, int RT, int MI, bool kResident, bool kSplit>
