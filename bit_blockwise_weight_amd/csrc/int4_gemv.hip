@@ -27,7 +27,7 @@ struct Int4Task {
     int64_t K;
     int32_t x_aligned;       // rows of x start at 16-byte boundaries
     int32_t kwl;             // log2 of the waves that split a row
-    int32_t share, more;     // tiles of 16 rows per workgroup; the first `more` workgroups take one tile more
+    int32_t share, more;     // items per workgroup; the first `more` workgroups take one more
 };
 
 // A launch of one weight has arguments of its own: finding a task in the longer list costs two
@@ -50,12 +50,13 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
     const Int4Task& t = g.t[ti];
     // this workgroup's rows
     const int b = (int)blockIdx.x - g.wg0[ti];
-    const int64_t row0 = 16 * ((int64_t)b * t.share + (b < t.more ? b : t.more));
-    const int64_t row1 = row0 + 16 * (t.share + (b < t.more));
     Rows<RT> p;
     p.kwl = t.kwl;
     p.group_step = 16 * RT;
     p.step = (16 * RT * 8) >> t.kwl;
+    const int64_t row0 = (int64_t)p.step * ((int64_t)b * t.share + (b < t.more ? b : t.more));
+    const int items = t.share + (b < t.more);
+    const int64_t row1 = row0 + (int64_t)p.step * items;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         p.base[r] = row0;
@@ -69,8 +70,7 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
     p.x_rows = g.M;
     p.x_aligned = t.x_aligned;
     p.M = g.M;
-    const int steps = 7 - t.kwl + (RT == 2);             // log2(step)
-    Tiles::run(t.w, p, 0, (p.count + p.step - 1) >> steps, lds, [&](int item, int q, const float* put) {
+    Tiles::run(t.w, p, 0, items, lds, [&](int item, int q, const float* put) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -83,21 +83,23 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
     });
 }
 
-constexpr int kRt = 2;                                   // tiles of 16 rows per item and row group
 constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
+// tiles of 16 rows per item and row group
+constexpr int rt_for(int mi) { return mi == 4 ? 1 : 2; }
 
-// The activations of a whole row stay in LDS where they fit.
-size_t x_lds(int M, int ng, int64_t K, bool resident) {
-    return mi_for(M) == 1 ? w4_fix_bytes(4, M, ng, K, resident) : w4_x_bytes(4, M, K, resident);
+size_t lds_bytes(int M, int ng, int64_t K, bool resident) {
+    const int mi = mi_for(M), rt = rt_for(mi), kw = 1 << kStreamKwl;
+    return w4_fixed_bytes(kInt4Bf16, ng, rt, mi, resident) +
+           (mi == 1 ? w4_fix_bytes(kw, M, ng, K, resident) : w4_x_bytes(kw, M, K, resident));
 }
-size_t resident_lds(int M, int ng, int64_t K) { return w4_fixed_bytes(kInt4Bf16, ng, kRt, mi_for(M), true) + x_lds(M, ng, K, true); }
-bool resident_for(int M, int ng, int64_t K) { return resident_lds(M, ng, K) <= kLdsBytes; }
+// The activations of a whole row stay in LDS where they fit.
+bool resident_for(int M, int ng, int64_t K) { return lds_bytes(M, ng, K, true) <= (rt_for(mi_for(M)) == 1 ? kLdsBytes / 2 : kLdsBytes); }
 
 constexpr int32_t kNever = 0x7FFFFFFF;
 
 template <int F, int NG, int MI, bool kResident, int kTasks>
 hipError_t launch_tasks(const Int4Group<kTasks>& g, int64_t grid, size_t lds, hipStream_t s) {
-    constexpr auto kernel = &int4_gemv_kernel<F, NG, kRt, MI, kResident, kTasks>;
+    constexpr auto kernel = &int4_gemv_kernel<F, NG, rt_for(MI), MI, kResident, kTasks>;
     const hipError_t e = allow_lds<kernel>(lds);
     if (e != hipSuccess) return e;
     kernel<<<dim3((unsigned)grid), dim3(kThreads), lds, s>>>(g);
@@ -106,9 +108,8 @@ hipError_t launch_tasks(const Int4Group<kTasks>& g, int64_t grid, size_t lds, hi
 
 template <int F, int NG, int MI, bool kResident>
 hipError_t launch_one(Int4Group<kMaxGemvTasks>& g, int64_t grid, int64_t kmax, hipStream_t s) {
-    typedef RowTiles<F, NG, kRt, MI, kResident, false> Tiles;
     g.pad = 0;
-    const size_t lds = Tiles::kFixedBytes + x_lds(g.M, NG, kmax, kResident);
+    const size_t lds = lds_bytes(g.M, NG, kmax, kResident);
     if (g.wg0[1] == kNever) {
         Int4Group<1> one;
         one.wg0[0] = 0;
@@ -159,6 +160,7 @@ Int4View int4_view(const qk_int4_state* st) {
 int int4_groups_per_chunk(int32_t group) { return group == 32 ? 4 : group == 64 ? 2 : 1; }
 
 hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t M, bool f16, hipStream_t s) {
+    const int rt = rt_for(mi_for(M));
     // One launch per run of up to kMaxGemvTasks weights of one scale granularity, in task order.
     bool done[256] = {false};
     for (int32_t first = 0; first < count; ++first) {
@@ -168,8 +170,7 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
         const bool resident = resident_for(M, ng, items[first].st->cols);
         Int4Group<kMaxGemvTasks> g;
         int32_t n = 0;
-        int64_t tiles[kMaxGemvTasks], items_of[kMaxGemvTasks], kmax = 0;
-        double work = 0;
+        int64_t items_of[kMaxGemvTasks], windows[kMaxGemvTasks], kmax = 0;
         for (int32_t i = first; i < count && n < kMaxGemvTasks; ++i) {
             const qk_int4_state* st = items[i].st;
             if (done[i] || int4_groups_per_chunk(st->group) != ng || resident_for(M, ng, st->cols) != resident) continue;
@@ -181,26 +182,45 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             t.N = st->rows;
             t.K = st->cols;
             t.x_aligned = st->cols % 8 == 0 && reinterpret_cast<uintptr_t>(items[i].x) % 4 == 0;
-            t.kwl = w4_kwl(kInt4Bf16, st->cols, st->rows, 16 * kRt, resident ? 3 : 2);
-            tiles[n] = (st->rows + 15) / 16;
-            items_of[n] = (tiles[n] + ((kRt * 8) >> t.kwl) - 1) / ((kRt * 8) >> t.kwl);
-            work += (double)tiles[n] * (double)st->cols;
+            t.kwl = w4_kwl(kInt4Bf16, st->cols, st->rows, 16 * rt, resident ? 3 : kStreamKwl);
+            while (t.kwl < kStreamKwl && ((16 * rt * 8) >> t.kwl) * st->code_stride > 1 << 30) ++t.kwl;
+            const int64_t step = (16 * rt * 8) >> t.kwl, window = (int64_t)kLineK << t.kwl;
+            items_of[n] = (st->rows + step - 1) / step;
+            windows[n] = (st->cols + window - 1) / window;
             kmax = std::max(kmax, st->cols);
             ++n;
         }
-        const size_t lds = resident ? resident_lds(M, ng, kmax)
-                                    : w4_fixed_bytes(kInt4Bf16, ng, kRt, mi_for(M), false) + x_lds(M, ng, kmax, false);
+        const size_t lds = lds_bytes(M, ng, kmax, resident);
         const int per_cu = lds > kLdsBytes / 2 ? 1 : 2;
-        // the workgroups that the CUs hold at a time, dealt to the tasks by their work, at most one per item
+        // The workgroups that the CUs hold at a time are dealt so that the longest one is as short as can be: with at
+        // most `most` windows each, a task needs ceil(items / floor(most / windows of an item)) of them.
+        const int64_t slots = (int64_t)per_cu * device_cu_count();
+        auto wgs_for = [&](int32_t i, int64_t most) {
+            const int64_t per = most / windows[i];
+            return (items_of[i] + per - 1) / per;
+        };
+        int64_t lo = 1, hi = 1;
+        for (int32_t i = 0; i < n; ++i) {
+            lo = std::max(lo, windows[i]);
+            hi = std::max(hi, windows[i] * items_of[i]);
+        }
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            int64_t need = 0;
+            for (int32_t i = 0; i < n; ++i) need += wgs_for(i, mid);
+            if (need <= slots) hi = mid;
+            else lo = mid + 1;
+        }
         int64_t grid = 0;
         for (int32_t i = 0; i < n; ++i) {
             Int4Task& t = g.t[i];
-            const double part = (double)per_cu * device_cu_count() * ((double)tiles[i] * (double)t.K / work);
-            int64_t wgs = std::max<int64_t>(1, std::min<int64_t>(items_of[i], (int64_t)(part + 0.5)));
-            // a workgroup's rows stay under 2 GB of codes (and of scales: at most two bytes for 16 of codes)
-            wgs = std::max(wgs, (int64_t)((double)(tiles[i] + 1) * 16 * (double)t.w.stride / (1 << 30)) + 1);
-            t.share = (int32_t)(tiles[i] / wgs);
-            t.more = (int32_t)(tiles[i] % wgs);
+            int64_t wgs = wgs_for(i, lo);
+            // A workgroup's rows stay under 2^29 bytes of codes and one item more, of 2^30 bytes at most: offsets of
+            // 32 bits reach them (and the scales: at most two bytes for 16 of codes).
+            const int64_t bytes = ((16 * rt * 8) >> t.kwl) * t.w.stride;
+            wgs = std::max(wgs, std::min(items_of[i], (int64_t)((double)items_of[i] * (double)bytes / (1 << 29)) + 1));
+            t.share = (int32_t)(items_of[i] / wgs);
+            t.more = (int32_t)(items_of[i] % wgs);
             g.wg0[i] = (int32_t)grid;
             grid += wgs;
         }

@@ -378,7 +378,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* parts, co
 template <int F, int NG, int MI, bool kResident>
 hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
-    p.kwl = w4_kwl((Form)F, p.H, (int64_t)p.Ipad * listed, 16, kResident ? 3 : 2);
+    p.kwl = w4_kwl((Form)F, p.H, (int64_t)p.Ipad * listed, 16, kResident ? 3 : kStreamKwl);
     const size_t lds = (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + Tiles::kFixedBytes +
                        x_lds<F, NG, MI>(tokens, false, p.H, kResident);
     const hipError_t e = allow_lds<&moe_up_kernel<F, NG, MI, kResident>>(lds);
@@ -413,7 +413,7 @@ hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int
 template <int F, int NG, int RT, int MI, bool kResident>
 hipError_t launch_down_one(ExpertArgs<F> p, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, RT, MI, kResident, true> Tiles;
-    p.kwl = w4_kwl((Form)F, p.I, (int64_t)p.H * listed, 16 * RT, kResident ? 3 : 2);
+    p.kwl = w4_kwl((Form)F, p.I, (int64_t)p.H * listed, 16 * RT, kResident ? 3 : kStreamKwl);
     const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + x_lds<F, NG, MI>(tokens, true, p.I, kResident);
     const hipError_t e = allow_lds<&moe_down_kernel<F, NG, RT, MI, kResident>>(lds);
     if (e != hipSuccess) return e;

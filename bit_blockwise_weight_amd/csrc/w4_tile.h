@@ -265,7 +265,7 @@ struct Rows {
     int32_t x_rows;          // rows of x
     int32_t x_aligned;       // rows of x start at multiples of 4 bytes and K % 8 == 0
     int32_t M;               // activations
-    int32_t kwl;             // log2(kw); at most 2 where x is not resident
+    int32_t kwl;             // log2(kw); at most kStreamKwl where x is not resident
 };
 
 // The product's row 4 h + i lands in register i of lane group h.  With few activation rows only the
@@ -278,11 +278,13 @@ constexpr int kLineK = 256;               // k of a 128-byte line of codes
 // bytes of LDS beside the activations: scales, codes, partial sums of a few items and their counters
 constexpr int w4_waves(Form f) { return f == kLevels ? 16 : 8; }
 constexpr int w4_put_bytes(Form f, int RT, int MI) { return w4_waves(f) * RT * 64 * MI * 4; }
-constexpr int w4_slots(Form f, bool resident) { return resident || f == kLevels ? 2 : 3; }
+constexpr int w4_slots(Form f, int RT, bool resident) { return resident || f == kLevels || RT == 1 ? 2 : 3; }
 constexpr int w4_scale_bytes(Form f, int NG, int RT) { return w4_waves(f) * RT * 16 * ((2 * NG) | 1) * (f == kLevels ? 4 : 8); }
+// log2 of the waves that split a row where the activations do not stay, at most: a window of theirs has to fit
+constexpr int kStreamKwl = 2;
 constexpr int w4_code_bytes(int RT) { return 8 * RT * 16 * 128; }       // of 8 waves; 8 more have theirs beside the table
 constexpr int w4_fixed_bytes(Form f, int NG, int RT, int MI, bool resident) {
-    return w4_scale_bytes(f, NG, RT) + w4_code_bytes(RT) + w4_slots(f, resident) * (w4_put_bytes(f, RT, MI) + w4_waves(f) * 4);
+    return w4_scale_bytes(f, NG, RT) + w4_code_bytes(RT) + w4_slots(f, RT, resident) * (w4_put_bytes(f, RT, MI) + w4_waves(f) * 4);
 }
 constexpr size_t kLdsBytes = 160 * 1024;  // of a CU
 
@@ -336,13 +338,13 @@ struct RowTiles {
     static constexpr int kCodeBytes = w4_code_bytes(RT);        // a window's codes changing layout
     static constexpr int kCodePitch = F == kLevels ? 256 : 128; // from row to row there
     static constexpr int kPutBytes = w4_put_bytes(kForm, RT, MI);
-    static constexpr int kSlots = w4_slots(kForm, kResident);
-    // units of x per thread and batch; a window's fit one batch (kw <= 4)
+    static constexpr int kSlots = w4_slots(kForm, RT, kResident);
+    // units of x per thread and batch; a window's fit one batch
     static constexpr int kMaxM = kSplit && !kFix ? 2 * MI : 4 * MI;
-    static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : (kMaxM * 128 + kThreads - 1) / kThreads;
+    static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : ((kMaxM * 32 << kStreamKwl) + kThreads - 1) / kThreads;
     static constexpr int kFixedBytes = w4_fixed_bytes(kForm, NG, RT, MI, kResident);
 
-    static_assert(RT == 2);
+    static_assert(RT == 1 || RT == 2);
     // The scales of a window come by one load per kind, in lane 16 r + n for row n of tile r (a load instruction that
     // touches many lines costs as much as one that brings a kilobyte of codes): as dwords from an address rounded
     // down to 4 bytes, put right when they land.
@@ -543,9 +545,9 @@ struct RowTiles {
         const int32_t stride = (int32_t)w.stride;
         const int32_t voff = (lane >> 3) * stride + 16 * (lane & 7);
         // scales: row of the lane relative to base[0]; lanes 32..63 and what is past the end read nothing
-        const int32_t apart = (int32_t)(p.base[1] - p.base[0]) + p.off[1];
+        const int32_t apart = (int32_t)(p.base[RT - 1] - p.base[0]) + p.off[RT - 1];
         const int32_t srow = n + (lane & 16 ? apart : p.off[0]);
-        const int64_t srows = p.base[1] - p.base[0] + p.count;
+        const int64_t srows = p.base[RT - 1] - p.base[0] + p.count;
         __amdgpu_buffer_rsrc_t sbuf, zbuf, dbuf;
         uint32_t sfirst = 0, zfirst = 0, dfirst = 0;             // of base[0], from the rounded-down address, in its unit
         if constexpr (F == kLevels) {
@@ -577,7 +579,7 @@ struct RowTiles {
         int left = 0;                                            // and the scale groups (runs of 64) from there to the row's end
         auto fetch = [&](Fetched& f, int j, int c0) {
             const int c = c0 + wk * U;
-            const bool in = j >= 0 && c < nchunk, lane_in = in && lane < 32;
+            const bool in = j >= 0 && c < nchunk, lane_in = in && lane < 16 * RT;
             at = scale_at(j, c);
             if constexpr (F == kLevels) left = (p.K >> 6) - 2 * c;
             else left = w.G - ((c * kChunk) >> w.gshift);
@@ -633,7 +635,7 @@ struct RowTiles {
                     *reinterpret_cast<u32x4_t*>(clds + (16 * r + 8 * q + (lane >> 3)) * kCodePitch +
                                                 16 * ((lane & 7) ^ (lane >> 3))) = f.c[r][q];
             }
-            if (lane >= 32) return;
+            if (lane >= 16 * RT) return;
             if constexpr (F == kLevels) {
                 // the four runs of 64: their blocks follow the first one's
                 const uint32_t blk = at >> w.bshift, run = at >> 6, shift = w.bshift - 6;
