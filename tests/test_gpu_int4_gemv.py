@@ -173,3 +173,86 @@ def test_a_row_of_infinite_scales_stays_in_its_outputs(M):
         keep = torch.arange(40, device="cuda") != 17
         assert torch.equal(y[:, keep], w.gemv(x)[:, keep])
         assert not bool(torch.isfinite(y[:, 17]).any())
+
+
+@pytest.mark.parametrize("M", [1, 16])
+def test_rows_of_codes_far_apart(M):
+    """300 rows, 16 MiB from one to the next: offsets that pass 32 bits, for one group per row and for several."""
+    buf = torch.empty((300, 1 << 24), dtype=torch.uint8, device="cuda")
+    for K, group in ((64, 0), (1000, 32)):
+        say(f"case: gemv_int4 rows 16 MiB apart M={M} K={K}")
+        w, x, ref, tol = _case(13, M, 300, K, group, True, torch.bfloat16, torch.float16)
+        buf[:, :w.codes.shape[1]] = w.codes
+        st = qk.qk_int4_state_init(300, K, group, buf, w.scales, w.zeros)
+        _check(qk.qk_gemv_int4(x, st), ref, tol, f"M={M} K={K}")
+
+
+def test_a_matrix_of_more_than_four_gib():
+    """The last rows of 9 GB of codes (2^21 rows of 8192 columns), against the same rows alone."""
+    N, K, tail = 1 << 21, 8192, 1000
+    for M in (1, 9):
+        say(f"case: gemv_int4 2^21 rows M={M}")
+        gen = torch.Generator(device="cuda").manual_seed(14)
+        q, s, z = make_int4(gen, tail, K, 128, True, torch.float16)
+        w = qk.Int4Weight(q, s, z, 128)
+        codes = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros((N, K // 128), dtype=torch.float16, device="cuda")
+        zeros = torch.zeros((N, K // 128), dtype=torch.uint8, device="cuda")
+        codes[-tail:], scales[-tail:], zeros[-tail:] = w.codes, s, z
+        x = torch.randn((M, K), generator=gen, device="cuda").to(torch.bfloat16)
+        y = qk.qk_gemv_int4(x, qk.qk_int4_state_init(N, K, 128, codes, scales, zeros))
+        assert bool((y[:, :-tail] == 0).all())
+        ref = x.double() @ int4_f64(q, s, z, 128).t()
+        assert float((y[:, -tail:].double() - ref).norm() / ref.norm()) < 2.0 ** -8
+        del codes, scales, zeros, y
+        torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("group", [32, 64, 256])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_values_of_very_different_size(group, dtype):
+    """Rows with one value far above its neighbours, very small rows, zeros.  Up to four rows are held in fixed point,
+    to 2^-22 of the largest value in each run of 128 inputs; 2^-121 below 2^-100."""
+    M, N, K = 4, 96, 1000
+    w, x, _, _ = _case(15, M, N, K, group, True, dtype, torch.bfloat16)
+    x[0, 77] = 1000.0
+    x[1, ::130] *= 500.0
+    x[2] *= 2.0 ** -12 if dtype is torch.float16 else 2.0 ** -60
+    x[3] = 0
+    x[3, 999] = 1.0
+    codes = torch.stack((w.codes >> 4, w.codes & 15), 2).view(N, -1)[:, :K]
+    w64 = int4_f64(codes, w.scales, w.zeros, group)
+    gi = torch.arange(K, device="cuda") // group
+    absw = w.scales.double().abs()[:, gi] * (143.0 + 128.0 + w.zeros.double()[:, gi])
+    ref = x.double() @ w64.t()
+    big = torch.nn.functional.pad(x.double().abs(), (0, 24)).view(M, 8, 128).amax(2).repeat_interleave(128, 1)[:, :K]
+    for m in range(1, M + 1):
+        say(f"case: gemv_int4 values of different size M={m} group={group} {dtype}")
+        tol = torch.finfo(dtype).eps / 2 * ref.abs() + 2.0 ** -24 * 150 * (x.double().abs() @ absw.t()) \
+            + 2.0 ** -22 * (big @ w64.abs().t()) + torch.finfo(dtype).smallest_normal
+        _check(w.gemv(x[:m].contiguous()), ref[:m], tol[:m], f"M={m}")
+    if dtype is torch.bfloat16:
+        say("case: gemv_int4 the largest and the smallest numbers")
+        x2 = torch.zeros((2, K), dtype=dtype, device="cuda")
+        x2[0] = 2.0 ** -120
+        x2[1, 5] = torch.finfo(dtype).max
+        y = w.gemv(x2)
+        assert bool((y[0].double().abs() < 2.0 ** -80).all())
+        want = (x2[1, 5].double() * w64[:, 5]).to(dtype)
+        same = y[1] == want                                  # infinities of one sign among them
+        assert bool((same | ((y[1].double() - want.double()).abs() <= 2.0 ** -7 * want.double().abs())).all())
+
+
+def test_refusals_on_the_device():
+    say("case: gemv_int4 refusals")
+    w, x, _, _ = _case(16, 4, 32, 64, 32, True, torch.bfloat16, torch.float16)
+    with pytest.raises(ValueError, match="contiguous"):
+        w.gemv(x.t().contiguous().t())
+    with pytest.raises(ValueError):
+        w.gemv(x, torch.empty((4, 31), dtype=x.dtype, device="cuda"))
+    with pytest.raises(ValueError):
+        w.gemv(x, torch.empty((4, 32), dtype=torch.float32, device="cuda"))
+    with pytest.raises(RuntimeError, match="1..16"):
+        w.gemv(torch.zeros((17, 64), dtype=x.dtype, device="cuda"))
+    with pytest.raises(RuntimeError, match="overlaps"):
+        qk.qk_gemv_int4_grouped([(x, w.state), (x, w.state)], [y := torch.empty((4, 32), dtype=x.dtype, device="cuda"), y])

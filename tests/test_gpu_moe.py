@@ -279,3 +279,80 @@ def test_a_row_of_infinite_block_scales_stays_in_its_outputs():
     y = qk.qk_moe_nf4(x, lg, 2, up.state, down.state)
     keep = torch.arange(H, device="cuda") != 17
     assert torch.equal(y[:, keep], want[:, keep]) and not bool(torch.isfinite(y[:, 17]).any())
+
+
+@pytest.mark.parametrize("E", [3, 4, 9])
+def test_every_token_at_the_same_expert(E):
+    """16 tokens of one expert: as many as a pass takes, or several passes; few and many experts beside it."""
+    T, H, I = 16, 200, 136
+    lg = torch.zeros((T, E), device="cuda")
+    lg[:, 1] = 3.0
+    lg[5:, 2] = 1.0
+    for k in (1, 2):
+        say(f"case: moe 16 tokens of one expert E={E} top_k={k}")
+        for group in (32, 128):
+            _run(60, T, E, k, H, I, lambda g: Int4Experts(g, E, 2 * I, H, group, True, torch.float16),
+                 lambda g: Int4Experts(g, E, H, I, group, True, torch.float16), torch.bfloat16, True, logits=lg)
+        _run(61, T, E, k, 192, 128, lambda g: Nf4Experts(g, E, 2 * 128, 192, 64, qk.NF4, True),
+             lambda g: Nf4Experts(g, E, 192, 128, 64, qk.NF4, True), torch.bfloat16, True, logits=lg)
+
+
+@pytest.mark.parametrize("H,I", [(12032, 64), (64, 12032)])
+@pytest.mark.parametrize("T,E", [(1, 2), (4, 3), (7, 2), (16, 2), (16, 9)])
+def test_long_rows(H, I, T, E):
+    """Rows whose activations do not stay on the chip, for each number of tokens that a pass takes."""
+    say(f"case: moe long rows H={H} I={I} T={T} E={E}")
+    for dtype in (torch.bfloat16, torch.float16):
+        _run(62, T, E, 2, H, I, lambda g: Int4Experts(g, E, 2 * I, H, 32, True, torch.bfloat16),
+             lambda g: Int4Experts(g, E, H, I, 64, True, torch.bfloat16), dtype, True)
+    _run(63, T, E, 2, H, I, lambda g: Nf4Experts(g, E, 2 * I, H, 64, qk.NF4, True),
+         lambda g: Nf4Experts(g, E, H, I, 128, qk.NF4, False), torch.bfloat16, True)
+
+
+def test_two_calls_at_once():
+    say("case: moe two streams, a workspace each")
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    up, down = _int4_small(gen)
+    xs = [torch.randn((16, 160), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    lg = torch.randn((16, 6), generator=gen, device="cuda")
+    want = [qk.qk_moe_int4(x, lg, 3, up.state, down.state) for x in xs]
+    n = qk.qk_moe_workspace_size(16, 3, 160, 96)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ys = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                qk.qk_moe_int4(xs[i], lg, 3, up.state, down.state, y=ys[i], workspace=ws[i])
+    torch.cuda.synchronize()
+    for y, w in zip(ys, want):
+        assert torch.equal(y, w)
+
+
+def test_experts_behind_four_gib():
+    """A stack of 8.6 GB of codes whose last expert alone is not zero."""
+    E, H, I = 64, 4096, 16384
+    say(f"case: moe_int4 E={E} H={H} I={I}")
+    gen = torch.Generator(device="cuda").manual_seed(12)
+
+    def last(rows, cols):
+        q, s, z = make_int4(gen, rows, cols, 128, True, torch.float16)
+        w = qk.Int4Weight(q, s, z, 128)
+        codes = torch.zeros((E * rows, cols // 2), dtype=torch.uint8, device="cuda")
+        scales = torch.zeros((E * rows, cols // 128), dtype=torch.float16, device="cuda")
+        zeros = torch.zeros((E * rows, cols // 128), dtype=torch.uint8, device="cuda")
+        codes[-rows:], scales[-rows:], zeros[-rows:] = w.codes, s, z
+        return w, (codes, scales, zeros), qk.qk_int4_state_init(E * rows, cols, 128, codes, scales, zeros)
+
+    u1, u_all, up = last(2 * I, H)
+    d1, d_all, down = last(H, I)
+    x = torch.randn((3, H), generator=gen, device="cuda").to(torch.bfloat16)
+    lg = torch.full((3, E), float("-inf"), device="cuda")
+    lg[:, E - 1] = 0.5
+    lg[1, 7] = 0.5                                           # a zero expert for half of token 1
+    y = qk.qk_moe_int4(x, lg, 2, up, down)
+    alone = qk.qk_moe_int4(x, torch.zeros((3, 1), device="cuda"), 1, u1.state, d1.state)
+    assert torch.equal(y[0], alone[0]) and torch.equal(y[2], alone[2])
+    assert float((2 * y[1].double() - alone[1].double()).norm() / alone[1].double().norm()) < 2.0 ** -7
+    assert bool((alone != 0).any())
