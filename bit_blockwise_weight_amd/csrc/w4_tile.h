@@ -463,33 +463,30 @@ struct RowTiles {
                 for (int q = 0; q < 8; ++q) big = max(big, as_uint(v[q]) & 0x7FFFFFFFu);
                 const uint32_t e = max(group_max_u32<16>(big) >> 23, 27u);      // below 2^-100: lost against 2^-121
                 const float up = as_float((148u + 127u - e) << 23);             // 2^(21 - (e - 127))
-                int32_t X[8], sum = 0;
+                // X + 0x8080 from the low bits of x 2^(21 - e) + 1.5 2^23; its bytes are b0, b1 + 128 and b2 + 128
+                uint32_t X[8];
+                int32_t sum = -8 * 0x8080;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    X[q] = (int32_t)rintf(v[q] * up);
-                    sum += X[q];
+                    float r = __builtin_fmaf(v[q], up, 12582912.0f);
+                    if constexpr (kSplit) r = fminf(r, 16777215.0f);            // fp32 may round up to 2^22: 1 less
+                    X[q] = as_uint(r) - (0x4B400000u - 0x8080u);
+                    sum += (int32_t)X[q];
                 }
                 // sums over a scale group (or a chunk): 4, 8 or 16 lanes
-#pragma unroll
-                for (int d = 1; d < 16 / NG; d <<= 1) sum += __shfl_xor(sum, d);
+                sum += __builtin_amdgcn_mov_dpp(sum, 0xB1, 0xF, 0xF, false);    // xor 1
+                sum += __builtin_amdgcn_mov_dpp(sum, 0x4E, 0xF, 0xF, false);    // xor 2
+                if constexpr (NG <= 2) sum += __builtin_amdgcn_mov_dpp(sum, 0x141, 0xF, 0xF, false);   // half mirror
+                if constexpr (NG == 1) sum += __builtin_amdgcn_mov_dpp(sum, 0x140, 0xF, 0xF, false);   // mirror
                 u32x2_t d0, d1, d2;
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {                    // the odd values, then the even ones
-                    const int32_t* q = X;
-                    uint32_t c[3][4];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int32_t x2 = q[2 * t + 1 - o], x1 = (x2 + 128) >> 8, x0 = (x1 + 128) >> 8;
-                        c[0][t] = (uint32_t)x0;
-                        c[1][t] = (uint32_t)x1;
-                        c[2][t] = (uint32_t)x2;
-                    }
-#pragma unroll
-                    for (int pl = 0; pl < 3; ++pl) {
-                        const uint32_t ab = __builtin_amdgcn_perm(c[pl][1], c[pl][0], 0x0C0C0400u);
-                        const uint32_t cd = __builtin_amdgcn_perm(c[pl][3], c[pl][2], 0x04000C0Cu);
-                        (pl == 0 ? d0 : pl == 1 ? d1 : d2)[o] = ab | cd;
-                    }
+                    const uint32_t *q = X + 1 - o;
+                    const uint32_t ab = __builtin_amdgcn_perm(q[2], q[0], 0x05010400u);     // b2 b2 b1 b1
+                    const uint32_t cd = __builtin_amdgcn_perm(q[6], q[4], 0x05010400u);
+                    d2[o] = __builtin_amdgcn_perm(cd, ab, 0x05040100u) ^ 0x80808080u;
+                    d1[o] = __builtin_amdgcn_perm(cd, ab, 0x07060302u) ^ 0x80808080u;
+                    d0[o] = __builtin_amdgcn_perm(q[2], q[0], 0x0C0C0602u) | __builtin_amdgcn_perm(q[6], q[4], 0x06020C0Cu);
                 }
                 const int at = in ? 3 * m * xpitch + 8 * u : xpitch - 16, row = in ? xpitch : 0;
                 *reinterpret_cast<u32x2_t*>(dst + at) = d0;
