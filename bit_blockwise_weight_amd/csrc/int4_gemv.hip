@@ -85,15 +85,16 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
 
 constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 // tiles of 16 rows per item and row group
-constexpr int rt_for(int mi) { return mi == 4 ? 1 : 2; }
+constexpr int rt_for(int mi) { return mi == 1 ? 2 : 1; }
 
 size_t lds_bytes(int M, int ng, int64_t K, bool resident) {
-    const int mi = mi_for(M), rt = rt_for(mi), kw = 1 << kStreamKwl;
+    const int mi = mi_for(M), rt = rt_for(mi), kw = 1 << w4_most_kwl(kInt4Bf16, mi);
     return w4_fixed_bytes(kInt4Bf16, ng, rt, mi, resident) +
            (mi == 1 ? w4_fix_bytes(kw, M, ng, K, resident) : w4_x_bytes(kw, M, K, resident));
 }
-// The activations of a whole row stay in LDS where they fit.
-bool resident_for(int M, int ng, int64_t K) { return lds_bytes(M, ng, K, true) <= (rt_for(mi_for(M)) == 1 ? kLdsBytes / 2 : kLdsBytes); }
+// The activations of a whole row stay in LDS where they fit (above four rows: where they leave room for a second
+// workgroup).
+bool resident_for(int M, int ng, int64_t K) { return lds_bytes(M, ng, K, true) <= (M > 4 ? kLdsBytes / 2 : kLdsBytes); }
 
 constexpr int32_t kNever = 0x7FFFFFFF;
 
@@ -160,20 +161,18 @@ Int4View int4_view(const qk_int4_state* st) {
 int int4_groups_per_chunk(int32_t group) { return group == 32 ? 4 : group == 64 ? 2 : 1; }
 
 hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t M, bool f16, hipStream_t s) {
-    const int rt = rt_for(mi_for(M));
+    const int rt = rt_for(mi_for(M)), most_kwl = w4_most_kwl(kInt4Bf16, mi_for(M));
     // One launch per run of up to kMaxGemvTasks weights of one scale granularity, in task order.
     bool done[256] = {false};
     for (int32_t first = 0; first < count; ++first) {
         if (done[first]) continue;
         const int ng = int4_groups_per_chunk(items[first].st->group);
-        // the weights of the launch: one scale granularity, activations that all fit, or all do not
-        const bool resident = resident_for(M, ng, items[first].st->cols);
         Int4Group<kMaxGemvTasks> g;
         int32_t n = 0;
         int64_t items_of[kMaxGemvTasks], windows[kMaxGemvTasks], kmax = 0;
         for (int32_t i = first; i < count && n < kMaxGemvTasks; ++i) {
             const qk_int4_state* st = items[i].st;
-            if (done[i] || int4_groups_per_chunk(st->group) != ng || resident_for(M, ng, st->cols) != resident) continue;
+            if (done[i] || int4_groups_per_chunk(st->group) != ng) continue;
             done[i] = true;
             Int4Task& t = g.t[n];
             t.x = static_cast<const uint16_t*>(items[i].x);
@@ -182,14 +181,16 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             t.N = st->rows;
             t.K = st->cols;
             t.x_aligned = st->cols % 8 == 0 && reinterpret_cast<uintptr_t>(items[i].x) % 4 == 0;
-            t.kwl = w4_kwl(kInt4Bf16, st->cols, st->rows, 16 * rt, resident ? 3 : kStreamKwl);
-            while (t.kwl < kStreamKwl && ((16 * rt * 8) >> t.kwl) * st->code_stride > 1 << 30) ++t.kwl;
+            t.kwl = w4_kwl(kInt4Bf16, st->cols, st->rows, 16 * rt, most_kwl);
+            while (t.kwl < most_kwl && ((16 * rt * 8) >> t.kwl) * st->code_stride > 1 << 30) ++t.kwl;
             const int64_t step = (16 * rt * 8) >> t.kwl, window = (int64_t)kLineK << t.kwl;
             items_of[n] = (st->rows + step - 1) / step;
             windows[n] = (st->cols + window - 1) / window;
             kmax = std::max(kmax, st->cols);
             ++n;
         }
+        // (an output's bits do not depend on whether the activations stay)
+        const bool resident = resident_for(M, ng, kmax);
         const size_t lds = lds_bytes(M, ng, kmax, resident);
         const int per_cu = lds > kLdsBytes / 2 ? 1 : 2;
         // The workgroups that the CUs hold at a time are dealt so that the longest one is as short as can be: with at

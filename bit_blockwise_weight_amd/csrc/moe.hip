@@ -235,8 +235,9 @@ int64_t workgroups(int64_t items, size_t lds) {
 // LDS of the activations; those of a whole row stay there where all of them fit.
 template <int F, int NG, int MI>
 size_t x_lds(int tokens, bool split, int64_t K, bool resident) {
-    return F != kLevels && MI == 1 ? w4_fix_bytes(4, tokens, NG, K, resident)
-                                   : w4_x_bytes(4, split ? 2 * tokens : tokens, K, resident);
+    constexpr int kw = 1 << w4_most_kwl((Form)F, MI);
+    return F != kLevels && MI == 1 ? w4_fix_bytes(kw, tokens, NG, K, resident)
+                                   : w4_x_bytes(kw, split ? 2 * tokens : tokens, K, resident);
 }
 template <int F, int NG, int RT, int MI>
 bool fits(int tokens, bool split, int64_t K) {
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* parts, co
 template <int F, int NG, int MI, bool kResident>
 hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
-    p.kwl = w4_kwl((Form)F, p.H, (int64_t)p.Ipad * listed, 16, kResident ? 3 : kStreamKwl);
+    p.kwl = w4_kwl((Form)F, p.H, (int64_t)p.Ipad * listed, 16, kResident ? 3 : w4_most_kwl((Form)F, MI));
     const size_t lds = (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + Tiles::kFixedBytes +
                        x_lds<F, NG, MI>(tokens, false, p.H, kResident);
     const hipError_t e = allow_lds<&moe_up_kernel<F, NG, MI, kResident>>(lds);
@@ -413,7 +414,7 @@ hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int
 template <int F, int NG, int RT, int MI, bool kResident>
 hipError_t launch_down_one(ExpertArgs<F> p, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, RT, MI, kResident, true> Tiles;
-    p.kwl = w4_kwl((Form)F, p.I, (int64_t)p.H * listed, 16 * RT, kResident ? 3 : kStreamKwl);
+    p.kwl = w4_kwl((Form)F, p.I, (int64_t)p.H * listed, 16 * RT, kResident ? 3 : w4_most_kwl((Form)F, MI));
     const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + x_lds<F, NG, MI>(tokens, true, p.I, kResident);
     const hipError_t e = allow_lds<&moe_down_kernel<F, NG, RT, MI, kResident>>(lds);
     if (e != hipSuccess) return e;

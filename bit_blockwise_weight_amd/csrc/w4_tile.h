@@ -265,7 +265,7 @@ struct Rows {
     int32_t x_rows;          // rows of x
     int32_t x_aligned;       // rows of x start at multiples of 4 bytes and K % 8 == 0
     int32_t M;               // activations
-    int32_t kwl;             // log2(kw); at most kStreamKwl where x is not resident
+    int32_t kwl;             // log2(kw); at most w4_most_kwl() where x is not resident
 };
 
 // The product's row 4 h + i lands in register i of lane group h.  With few activation rows only the
@@ -280,8 +280,8 @@ constexpr int w4_waves(Form f) { return f == kLevels ? 16 : 8; }
 constexpr int w4_put_bytes(Form f, int RT, int MI) { return w4_waves(f) * RT * 64 * MI * 4; }
 constexpr int w4_slots(Form f, int RT, bool resident) { return resident || f == kLevels || RT == 1 ? 2 : 3; }
 constexpr int w4_scale_bytes(Form f, int NG, int RT) { return w4_waves(f) * RT * 16 * ((2 * NG) | 1) * (f == kLevels ? 4 : 8); }
-// log2 of the waves that split a row where the activations do not stay, at most: a window of theirs has to fit
-constexpr int kStreamKwl = 2;
+// log2 of the waves that split a row, at most: a window of the activations has to fit where these do not stay
+constexpr int w4_most_kwl(Form f, int MI) { return f == kLevels || MI == 4 ? 2 : 3; }
 constexpr int w4_code_bytes(int RT) { return 8 * RT * 16 * 128; }       // of 8 waves; 8 more have theirs beside the table
 constexpr int w4_fixed_bytes(Form f, int NG, int RT, int MI, bool resident) {
     return w4_scale_bytes(f, NG, RT) + w4_code_bytes(RT) + w4_slots(f, RT, resident) * (w4_put_bytes(f, RT, MI) + w4_waves(f) * 4);
@@ -341,7 +341,7 @@ struct RowTiles {
     static constexpr int kSlots = w4_slots(kForm, RT, kResident);
     // units of x per thread and batch; a window's fit one batch
     static constexpr int kMaxM = kSplit && !kFix ? 2 * MI : 4 * MI;
-    static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : ((kMaxM * 32 << kStreamKwl) + kThreads - 1) / kThreads;
+    static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : ((kMaxM * 32 << w4_most_kwl(kForm, MI)) + kThreads - 1) / kThreads;
     static constexpr int kFixedBytes = w4_fixed_bytes(kForm, NG, RT, MI, kResident);
 
     static_assert(RT == 1 || RT == 2);
@@ -436,16 +436,18 @@ struct RowTiles {
         // are then exact int32 sums.  The rounding, at most 2^-22 of the chunk's largest value, is the size of
         // the rounding of an fp32 sum that holds that value.
         auto x_store_fix = [&](uint8_t* dst, int base, int k0) {
+            // (a rolled loop over the units of the batch, each moved to the front when its turn comes)
+            const int batch = min(total, base + kXUnits * kThreads);
 #pragma unroll 1
-            for (int b = 0; b < kXUnits; ++b) {
-                const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
+            for (; base < batch; base += kThreads) {
+                const int i = base + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
                 const bool in = i < total && u < units;
                 float v[8];
                 if constexpr (kSplit) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = as_float(xr[b][q >> 2][q & 3]);
+                    for (int q = 0; q < 8; ++q) v[q] = as_float(xr[0][q >> 2][q & 3]);
                 } else {
-                    const u32x4_t x8 = x_unit(b, m, k);
+                    const u32x4_t x8 = x_unit(0, m, k);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const uint32_t d = x8[q];
@@ -457,6 +459,12 @@ struct RowTiles {
                             v[2 * q + 1] = bf16_hi(d);
                         }
                     }
+                }
+#pragma unroll
+                for (int b = 0; b + 1 < kXUnits; ++b) {
+                    xr[b][0] = xr[b + 1][0];
+                    if constexpr (kSplit) xr[b][1] = xr[b + 1][1];
+                    else xe[b] = xe[b + 1];
                 }
                 uint32_t big = 0;
 #pragma unroll
