@@ -84,62 +84,66 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
 }
 
 constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
-// tiles of 16 rows per item and row group
-constexpr int rt_for(int mi) { return mi == 1 ? 2 : 1; }
 
-size_t lds_bytes(int M, int ng, int64_t K, bool resident) {
-    const int mi = mi_for(M), rt = rt_for(mi), kw = 1 << w4_most_kwl(kInt4Bf16, mi);
+size_t lds_bytes(int M, int ng, int rt, int64_t K, bool resident) {
+    const int mi = mi_for(M), kw = 1 << w4_most_kwl(kInt4Bf16, mi);
     return w4_fixed_bytes(kInt4Bf16, ng, rt, mi, resident) +
            (mi == 1 ? w4_fix_bytes(kw, M, ng, K, resident) : w4_x_bytes(kw, M, K, resident));
 }
 // The activations of a whole row stay in LDS where they fit (above four rows: where they leave room for a second
 // workgroup).
-bool resident_for(int M, int ng, int64_t K) { return lds_bytes(M, ng, K, true) <= (M > 4 ? kLdsBytes / 2 : kLdsBytes); }
+bool resident_for(int M, int ng, int rt, int64_t K) { return lds_bytes(M, ng, rt, K, true) <= (M > 4 ? kLdsBytes / 2 : kLdsBytes); }
 
 constexpr int32_t kNever = 0x7FFFFFFF;
 
-template <int F, int NG, int MI, bool kResident, int kTasks>
+template <int F, int NG, int RT, int MI, bool kResident, int kTasks>
 hipError_t launch_tasks(const Int4Group<kTasks>& g, int64_t grid, size_t lds, hipStream_t s) {
-    constexpr auto kernel = &int4_gemv_kernel<F, NG, rt_for(MI), MI, kResident, kTasks>;
+    constexpr auto kernel = &int4_gemv_kernel<F, NG, RT, MI, kResident, kTasks>;
     const hipError_t e = allow_lds<kernel>(lds);
     if (e != hipSuccess) return e;
     kernel<<<dim3((unsigned)grid), dim3(kThreads), lds, s>>>(g);
     return hipGetLastError();
 }
 
-template <int F, int NG, int MI, bool kResident>
-hipError_t launch_one(Int4Group<kMaxGemvTasks>& g, int64_t grid, int64_t kmax, hipStream_t s) {
+// How a launch is made.
+struct Launch {
+    int64_t grid;
+    size_t lds;
+    int ng, rt;
+    bool resident;
+};
+
+template <int F, int NG, int RT, int MI, bool kResident>
+hipError_t launch_one(Int4Group<kMaxGemvTasks>& g, const Launch& l, hipStream_t s) {
     g.pad = 0;
-    const size_t lds = lds_bytes(g.M, NG, kmax, kResident);
     if (g.wg0[1] == kNever) {
         Int4Group<1> one;
         one.wg0[0] = 0;
         one.M = g.M;
         one.pad = 0;
         one.t[0] = g.t[0];
-        return launch_tasks<F, NG, MI, kResident, 1>(one, grid, lds, s);
+        return launch_tasks<F, NG, RT, MI, kResident, 1>(one, l.grid, l.lds, s);
     }
-    return launch_tasks<F, NG, MI, kResident, kMaxGemvTasks>(g, grid, lds, s);
+    return launch_tasks<F, NG, RT, MI, kResident, kMaxGemvTasks>(g, l.grid, l.lds, s);
 }
 
-template <int F, int NG, int MI>
-hipError_t launch_shape(Int4Group<kMaxGemvTasks>& g, int64_t grid, bool resident, int64_t kmax, hipStream_t s) {
-    if (resident) return launch_one<F, NG, MI, true>(g, grid, kmax, s);
-    return launch_one<F, NG, MI, false>(g, grid, kmax, s);
+template <int F, int NG, int RT, int MI>
+hipError_t launch_shape(Int4Group<kMaxGemvTasks>& g, const Launch& l, hipStream_t s) {
+    return l.resident ? launch_one<F, NG, RT, MI, true>(g, l, s) : launch_one<F, NG, RT, MI, false>(g, l, s);
 }
 
 template <int F, int NG>
-hipError_t launch_mi(Int4Group<kMaxGemvTasks>& g, int64_t grid, bool resident, int64_t kmax, hipStream_t s) {
-    if (mi_for(g.M) == 1) return launch_shape<F, NG, 1>(g, grid, resident, kmax, s);
-    if (mi_for(g.M) == 2) return launch_shape<F, NG, 2>(g, grid, resident, kmax, s);
-    return launch_shape<F, NG, 4>(g, grid, resident, kmax, s);
+hipError_t launch_mi(Int4Group<kMaxGemvTasks>& g, const Launch& l, hipStream_t s) {
+    if (mi_for(g.M) == 4) return launch_shape<F, NG, 1, 4>(g, l, s);
+    if (mi_for(g.M) == 2) return launch_shape<F, NG, 1, 2>(g, l, s);
+    return l.rt == 1 ? launch_shape<F, NG, 1, 1>(g, l, s) : launch_shape<F, NG, 2, 1>(g, l, s);
 }
 
 template <int F>
-hipError_t launch_ng(Int4Group<kMaxGemvTasks>& g, int64_t grid, int ng, bool resident, int64_t kmax, hipStream_t s) {
-    if (ng == 4) return launch_mi<F, 4>(g, grid, resident, kmax, s);
-    if (ng == 2) return launch_mi<F, 2>(g, grid, resident, kmax, s);
-    return launch_mi<F, 1>(g, grid, resident, kmax, s);
+hipError_t launch_ng(Int4Group<kMaxGemvTasks>& g, const Launch& l, hipStream_t s) {
+    if (l.ng == 4) return launch_mi<F, 4>(g, l, s);
+    if (l.ng == 2) return launch_mi<F, 2>(g, l, s);
+    return launch_mi<F, 1>(g, l, s);
 }
 
 }  // namespace
@@ -161,18 +165,19 @@ Int4View int4_view(const qk_int4_state* st) {
 int int4_groups_per_chunk(int32_t group) { return group == 32 ? 4 : group == 64 ? 2 : 1; }
 
 hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t M, bool f16, hipStream_t s) {
-    const int rt = rt_for(mi_for(M)), most_kwl = w4_most_kwl(kInt4Bf16, mi_for(M));
+    const int most_kwl = w4_most_kwl(kInt4Bf16, mi_for(M));
     // One launch per run of up to kMaxGemvTasks weights of one scale granularity, in task order.
     bool done[256] = {false};
     for (int32_t first = 0; first < count; ++first) {
         if (done[first]) continue;
-        const int ng = int4_groups_per_chunk(items[first].st->group);
+        Launch l;
+        l.ng = int4_groups_per_chunk(items[first].st->group);
         Int4Group<kMaxGemvTasks> g;
         int32_t n = 0;
-        int64_t items_of[kMaxGemvTasks], windows[kMaxGemvTasks], kmax = 0;
+        int64_t items_of[kMaxGemvTasks], windows[kMaxGemvTasks], kmax = 0, pairs = 0;
         for (int32_t i = first; i < count && n < kMaxGemvTasks; ++i) {
             const qk_int4_state* st = items[i].st;
-            if (done[i] || int4_groups_per_chunk(st->group) != ng) continue;
+            if (done[i] || int4_groups_per_chunk(st->group) != l.ng) continue;
             done[i] = true;
             Int4Task& t = g.t[n];
             t.x = static_cast<const uint16_t*>(items[i].x);
@@ -181,18 +186,25 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             t.N = st->rows;
             t.K = st->cols;
             t.x_aligned = st->cols % 8 == 0 && reinterpret_cast<uintptr_t>(items[i].x) % 4 == 0;
-            t.kwl = w4_kwl(kInt4Bf16, st->cols, st->rows, 16 * rt, most_kwl);
-            while (t.kwl < most_kwl && ((16 * rt * 8) >> t.kwl) * st->code_stride > 1 << 30) ++t.kwl;
-            const int64_t step = (16 * rt * 8) >> t.kwl, window = (int64_t)kLineK << t.kwl;
-            items_of[n] = (st->rows + step - 1) / step;
+            // how many waves split a row decides the order of its sum: by the weight alone, not by its launch
+            t.kwl = w4_kwl(kInt4Bf16, st->cols, st->rows, 16, most_kwl);
+            while (t.kwl < most_kwl && (256 >> t.kwl) * st->code_stride > 1 << 30) ++t.kwl;
+            const int64_t window = (int64_t)kLineK << t.kwl;
             windows[n] = (st->cols + window - 1) / window;
+            pairs += (st->rows + (256 >> t.kwl) - 1) / (256 >> t.kwl);
             kmax = std::max(kmax, st->cols);
             ++n;
         }
+        const int per_cu_most = 2;
+        l.rt = mi_for(M) == 1 && pairs > (int64_t)per_cu_most * device_cu_count() ? 2 : 1;
         // (an output's bits do not depend on whether the activations stay)
-        const bool resident = resident_for(M, ng, kmax);
-        const size_t lds = lds_bytes(M, ng, kmax, resident);
-        const int per_cu = lds > kLdsBytes / 2 ? 1 : 2;
+        l.resident = resident_for(M, l.ng, l.rt, kmax);
+        l.lds = lds_bytes(M, l.ng, l.rt, kmax, l.resident);
+        const int per_cu = l.lds > kLdsBytes / 2 ? 1 : per_cu_most;
+        for (int32_t i = 0; i < n; ++i) {
+            const int64_t step = (128 * l.rt) >> g.t[i].kwl;
+            items_of[i] = (g.t[i].N + step - 1) / step;
+        }
         // The workgroups that the CUs hold at a time are dealt so that the longest one is as short as can be: with at
         // most `most` windows each, a task needs ceil(items / floor(most / windows of an item)) of them.
         const int64_t slots = (int64_t)per_cu * device_cu_count();
@@ -212,23 +224,22 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             if (need <= slots) hi = mid;
             else lo = mid + 1;
         }
-        int64_t grid = 0;
+        l.grid = 0;
         for (int32_t i = 0; i < n; ++i) {
             Int4Task& t = g.t[i];
             int64_t wgs = wgs_for(i, lo);
             // A workgroup's rows stay under 2^29 bytes of codes and one item more, of 2^30 bytes at most: offsets of
             // 32 bits reach them (and the scales: at most two bytes for 16 of codes).
-            const int64_t bytes = ((16 * rt * 8) >> t.kwl) * t.w.stride;
+            const int64_t bytes = ((128 * l.rt) >> t.kwl) * t.w.stride;
             wgs = std::max(wgs, std::min(items_of[i], (int64_t)((double)items_of[i] * (double)bytes / (1 << 29)) + 1));
             t.share = (int32_t)(items_of[i] / wgs);
             t.more = (int32_t)(items_of[i] % wgs);
-            g.wg0[i] = (int32_t)grid;
-            grid += wgs;
+            g.wg0[i] = (int32_t)l.grid;
+            l.grid += wgs;
         }
         for (int32_t i = n; i < kMaxGemvTasks; ++i) g.wg0[i] = kNever;
         g.M = M;
-        const hipError_t e = f16 ? launch_ng<kInt4F16>(g, grid, ng, resident, kmax, s)
-                                 : launch_ng<kInt4Bf16>(g, grid, ng, resident, kmax, s);
+        const hipError_t e = f16 ? launch_ng<kInt4F16>(g, l, s) : launch_ng<kInt4Bf16>(g, l, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

@@ -278,13 +278,15 @@ constexpr int kLineK = 256;               // k of a 128-byte line of codes
 // bytes of LDS beside the activations: scales, codes, partial sums of a few items and their counters
 constexpr int w4_waves(Form f) { return f == kLevels ? 16 : 8; }
 constexpr int w4_put_bytes(Form f, int RT, int MI) { return w4_waves(f) * RT * 64 * MI * 4; }
-constexpr int w4_slots(Form f, int RT, bool resident) { return resident || f == kLevels || RT == 1 ? 2 : 3; }
+constexpr int w4_slots(Form f, int RT, int MI, bool resident) {
+    return resident || f == kLevels ? 2 : RT == 2 ? 3 : MI == 4 ? 2 : 4;
+}
 constexpr int w4_scale_bytes(Form f, int NG, int RT) { return w4_waves(f) * RT * 16 * ((2 * NG) | 1) * (f == kLevels ? 4 : 8); }
 // log2 of the waves that split a row, at most: a window of the activations has to fit where these do not stay
 constexpr int w4_most_kwl(Form f, int MI) { return f == kLevels || MI == 4 ? 2 : 3; }
 constexpr int w4_code_bytes(int RT) { return 8 * RT * 16 * 128; }       // of 8 waves; 8 more have theirs beside the table
 constexpr int w4_fixed_bytes(Form f, int NG, int RT, int MI, bool resident) {
-    return w4_scale_bytes(f, NG, RT) + w4_code_bytes(RT) + w4_slots(f, RT, resident) * (w4_put_bytes(f, RT, MI) + w4_waves(f) * 4);
+    return w4_scale_bytes(f, NG, RT) + w4_code_bytes(RT) + w4_slots(f, RT, MI, resident) * (w4_put_bytes(f, RT, MI) + w4_waves(f) * 4);
 }
 constexpr size_t kLdsBytes = 160 * 1024;  // of a CU
 
@@ -338,7 +340,7 @@ struct RowTiles {
     static constexpr int kCodeBytes = w4_code_bytes(RT);        // a window's codes changing layout
     static constexpr int kCodePitch = F == kLevels ? 256 : 128; // from row to row there
     static constexpr int kPutBytes = w4_put_bytes(kForm, RT, MI);
-    static constexpr int kSlots = w4_slots(kForm, RT, kResident);
+    static constexpr int kSlots = w4_slots(kForm, RT, MI, kResident);
     // units of x per thread and batch; a window's fit one batch
     static constexpr int kMaxM = kSplit && !kFix ? 2 * MI : 4 * MI;
     static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : ((kMaxM * 32 << w4_most_kwl(kForm, MI)) + kThreads - 1) / kThreads;
