@@ -2,10 +2,14 @@
 //     y[m, n] = sum_k x[m, k] s[n, k / g] (q[n, k] - z[n, k / g]),   m < M <= 16
 // for one weight or for up to 16 of a grouped call in one launch.
 //
-// The host deals the workgroups (8 waves each, two per CU) to the weights of a launch by their
-// work; a workgroup owns a run of rows of one weight and walks it with RowTiles (w4_tile.h), the
+// The host deals the workgroups (8 waves each, two per CU) to the weights of a launch so that the longest
+// is as short as can be; a workgroup owns a run of rows of one weight and walks it with RowTiles (w4_tile.h), the
 // codes of the next rows being loaded while some are multiplied.
-// Bound by the bytes of the codes at every M (64 flops a byte at M = 16).
+//
+// Bound by the bytes of the codes, at 6 TB/s, where few rows of activations meet large weights: the seven weights of a
+// layer (4096 wide, 11008 inside, groups of 128, 106 MB) at M = 1 22.1 us, 4.8 TB/s; 28672 x 8192, M = 4, 28.1 us.  In
+// groups of 32 at M = 16 the layer takes 50 us, half of it instructions: scales and zero points, a product and a
+// sum of x per 32 k.  1024 x 1024 at M = 1 takes 4.4 us, a launch and two rounds of loads.
 #include <algorithm>
 
 #include "qk_device.h"
@@ -25,7 +29,7 @@ struct Int4Task {
     Int4View w;
     int64_t N;
     int64_t K;
-    int32_t x_aligned;       // rows of x start at 16-byte boundaries
+    int32_t x_aligned;       // rows of x start at 4-byte boundaries and K % 8 == 0
     int32_t kwl;             // log2 of the waves that split a row
     int32_t share, more;     // items per workgroup; the first `more` workgroups take one more
 };
@@ -83,6 +87,10 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
     });
 }
 
+// Registers of a product that carry activations: the least that hold M rows.  Up to four rows take the integer
+// product (w4_tile.h): the layer at M = 1 22 us, in bf16 28; at M = 4 27 and 35.  (4096 x 11008 alone at M = 4 would be
+// faster in bf16, 10 us against 15: every workgroup converts the rows anew.  But which product a weight takes may not
+// depend on its launch.)  Five to eight in the form of sixteen: 40 us instead of 34.
 constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
 size_t lds_bytes(int M, int ng, int rt, int64_t K, bool resident) {
@@ -90,9 +98,12 @@ size_t lds_bytes(int M, int ng, int rt, int64_t K, bool resident) {
     return w4_fixed_bytes(kInt4Bf16, ng, rt, mi, resident) +
            (mi == 1 ? w4_fix_bytes(kw, M, ng, K, resident) : w4_x_bytes(kw, M, K, resident));
 }
-// The activations of a whole row stay in LDS where they fit (above four rows: where they leave room for a second
-// workgroup).
-bool resident_for(int M, int ng, int rt, int64_t K) { return lds_bytes(M, ng, rt, K, true) <= (M > 4 ? kLdsBytes / 2 : kLdsBytes); }
+// The activations of a whole row stay in LDS where they fit; above four rows where they leave room for a second
+// workgroup on the CU (28672 x 8192 at M = 8: 32.5 us streaming with two, 33.1 resident with one; up to four, resident
+// at any size was faster, 25 us against 32 for the layer at M = 3).
+bool resident_for(int M, int ng, int rt, int64_t K) {
+    return lds_bytes(M, ng, rt, K, true) <= (M > 4 ? kLdsBytes / 2 : kLdsBytes);
+}
 
 constexpr int32_t kNever = 0x7FFFFFFF;
 
@@ -115,7 +126,6 @@ struct Launch {
 
 template <int F, int NG, int RT, int MI, bool kResident>
 hipError_t launch_one(Int4Group<kMaxGemvTasks>& g, const Launch& l, hipStream_t s) {
-    g.pad = 0;
     if (g.wg0[1] == kNever) {
         Int4Group<1> one;
         one.wg0[0] = 0;
@@ -196,6 +206,10 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
             ++n;
         }
         const int per_cu_most = 2;
+        // Tiles of 16 rows per item and row group: two, which bring more codes on their way at a time, where every
+        // workgroup has an item of two (M = 1: the layer 21.9 us, with one 24.2), one where not (4096 x 4096 5.3 us, with
+        // two 5.8) and above four rows, whose sums and scales leave no room for two workgroups on a CU (M = 16,
+        // groups of 32: the layer 50 us, with two 59; M = 8, groups of 128, 34 and 47).
         l.rt = mi_for(M) == 1 && pairs > (int64_t)per_cu_most * device_cu_count() ? 2 : 1;
         // (an output's bits do not depend on whether the activations stay)
         l.resident = resident_for(M, l.ng, l.rt, kmax);
@@ -239,6 +253,7 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
         }
         for (int32_t i = n; i < kMaxGemvTasks; ++i) g.wg0[i] = kNever;
         g.M = M;
+        g.pad = 0;
         const hipError_t e = f16 ? launch_ng<kInt4F16>(g, l, s) : launch_ng<kInt4Bf16>(g, l, s);
         if (e != hipSuccess) return e;
     }

@@ -6,16 +6,21 @@
 // with the weights of all experts stacked in two quantized tensors, gate and up rows of an
 // expert one after the other in the first.
 //
-//   moe_up_kernel       routes first: selects each token's experts and lists the experts
-//                       that have a token in increasing order, each with its tokens, their
-//                       weights and their pairs (token, position).  Then items of 16 rows of gate and the same 16 of up of a listed expert
-//                       (RowTiles, w4_tile.h), dealt in equal shares; only the expert's own
-//                       tokens are staged.  h is written in fp32.
-//   moe_down_kernel     items of rows of Wd of a listed expert times its tokens' h, which enters
-//                       the matrix cores as two bf16 values (hi + lo, 16 bits of mantissa), so the
-//                       product loses nothing against the 16-bit output; w h Wd^T goes to memory in fp32.
-//   moe_combine_kernel  adds each token's parts in the order of its choices: no atomics.
-// Every weight of a listed expert is read once per layer; that is the bound.
+//   moe_up_kernel       routes first: selects each token's experts and lists the experts that have a token in
+//                       increasing order, each with its tokens, their weights and their pairs (token, position).
+//                       Then items of 16 rows of gate and the same 16 of up of a listed expert (RowTiles,
+//                       w4_tile.h), dealt in equal shares; only the expert's own tokens are staged.  h is fp32.
+//   moe_down_kernel     items of rows of Wd of a listed expert times its tokens' h, which enters the matrix cores in
+//                       fixed point (22 bits below the largest of 128 values) or as two bf16 values (hi + lo, 16
+//                       bits of mantissa), so the product loses nothing against the 16-bit output; w h Wd^T goes
+//                       to memory in fp32.
+//   moe_combine_kernel  adds each token's parts in the order of its choices: no atomics.  Adding them in the down
+//                       kernel, by the wave that stores the last part, made that 82 us instead of 22 (16 tokens, top
+//                       8 of 64, 2048 x 1024): every wave then waits for its stores to reach memory.
+// Every weight of a listed expert is read once per listing; that is the bound.  At 6 TB/s, which a read of large
+// weights reaches, one token's top 2 of 8 experts of 4096 x 11008 take 24 us, measured 39; of 64 experts of
+// 2048 x 1024 with top 8 one token takes 4.4, measured 19 (three launches, the routing, one round of loads each),
+// sixteen tokens 31, measured 54 in int4 and 66 in NF4, whose table reads from LDS take as long as the loads.
 #include <algorithm>
 
 #include "qk_device.h"
@@ -400,15 +405,17 @@ hipError_t launch_up_mi(const ExpertArgs<F>& p, RouteArgs ra, Routes* keep, int3
     return launch_up_one<F, NG, MI, false>(p, ra, keep, tokens, *listed, s);
 }
 
-// Tokens that a pass over an expert's rows takes (4 MI): by the number that it has on average.
+// Tokens of a listing, four or eight, by how many an expert has on average.  Eight read the weights of crowded experts
+// less often; four take the integer product in int4, and less LDS.  16 tokens, four / eight: top 2 of 8 experts,
+// H = I = 4096 (4 an expert), int4 74 / 65 us, levels 86 / 78; top 8 of 64, 2048 x 1024 (2 an expert), int4 52 / 69,
+// levels 65 / 80; 12 tokens, top 2 of 8 (3 an expert), int4 61 / 63, levels 79 / 77.  Sixteen gained 2 % where every
+// expert has 16 and lost 10 % at 6.
 // listed: set to the most listings that there can be
 template <int F, int NG>
 hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int32_t* listed, hipStream_t s) {
     const RouteArgs ra{m.logits, m.logits_dtype, m.T, m.E, m.top_k, m.renorm, 0};
-    const int pairs = m.T * m.top_k;
-    if (m.T <= 4 || pairs <= 2 * m.E) return launch_up_mi<F, NG, 1>(p, ra, keep, listed, s);
-    if (F == kLevels || m.T <= 8 || pairs <= 5 * m.E) return launch_up_mi<F, NG, 2>(p, ra, keep, listed, s);
-    return launch_up_mi<F, NG, F == kLevels ? 2 : 4>(p, ra, keep, listed, s);
+    if (m.T <= 4 || m.T * m.top_k < (F == kLevels ? 3 : 4) * m.E) return launch_up_mi<F, NG, 1>(p, ra, keep, listed, s);
+    return launch_up_mi<F, NG, 2>(p, ra, keep, listed, s);
 }
 
 template <int F, int NG, int RT, int MI, bool kResident>
@@ -431,16 +438,15 @@ hipError_t launch_down_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hip
     return launch_down_one<F, NG, 2, MI, true>(p, tokens, listed, s);
 }
 
+// Tokens of a pass of the down product.  int4: four in fixed point, or eight as pairs of bf16 where experts are crowded
+// (the case of 16 tokens and 8 experts above: 71 / 65 us).  Levels, two or four: equal up to two tokens, with four
+// at a time top 8 of 64 experts take 40 us for 4 tokens instead of 48, and 65 for 16 instead of 79; one expert of two
+// tokens, 4096 x 4096, 44 us instead of 38.
 template <int F, int NG>
 hipError_t launch_down(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, hipStream_t s) {
-    const int pairs = m.T * m.top_k;
-    if constexpr (F == kLevels) {
-        if (m.T <= 2 || pairs <= m.E) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
-        return launch_down_mi<F, NG, 2>(p, m.T, listed, s);
-    } else {
-        if (m.T <= 4 || pairs <= 2 * m.E) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
-        return launch_down_mi<F, NG, 4>(p, m.T, listed, s);
-    }
+    const bool few = F == kLevels ? m.T <= 2 : m.T <= 4 || m.T * m.top_k < 4 * m.E;
+    if (few) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
+    return launch_down_mi<F, NG, F == kLevels ? 2 : 4>(p, m.T, listed, s);
 }
 
 LevelsView levels_view(const MatArgs& w) {

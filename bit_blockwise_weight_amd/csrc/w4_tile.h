@@ -2,31 +2,41 @@
 // weights straight from memory (int4 with group scales; NF4 and other 16-level tables
 // in the mixture-of-experts layer), for gfx950.
 //
-// One step of a wave is a "chunk": 16 weight rows x 128 k.  For its MFMAs (16x16x32) lane l
-// holds row n = l % 16 and, with h = l / 16, the 16 bytes of k = 128 c + 32 h + [0, 32).  Where
-// a scale group covers the whole chunk its four MFMAs take the four dwords as they are, in any k
-// order; for groups of 64 two lane swaps, for groups of 32 four, exchange dwords between the
-// lane groups, so that a pair of MFMAs, or every one, stays inside a group.
+// One step of a wave is a "chunk": 16 weight rows x 128 k.  For its matrix instructions lane l holds
+// row n = l % 16 and, with h = l / 16, the 16 bytes of k = 128 c + 32 h + [0, 32).  Where a scale
+// group covers the whole chunk the four dwords are taken as they are, in any k order; for groups of
+// 64 two lane swaps, for groups of 32 four, exchange dwords between the lane groups, so that a
+// product of 64 k, or of 32, stays inside a group.
 //
 // From memory the codes come in whole 128-byte lines, 8 rows x 128 bytes per load instruction,
 // and change to the layout above through a wave's own piece of LDS.  Loading them in that
 // layout directly (16 rows x 64 bytes an instruction) streams 105 MB in 23 us against 18 us.
 //
-//   A = activations (row m = l % 16, k = 8 (l / 16) + i), B = W^T (column n = l % 16, the
-//   same k), D: column n = l % 16, rows m = 4 (l / 16) + r.  A scale of row n is then one
-//   value per lane, applied to the fp32 partial product of its group.
+//   A = activations (row m = l % 16), B = W^T (column n = l % 16, the same k), D: column
+//   n = l % 16, rows m = 4 (l / 16) + r.  A scale of row n is then one value per lane, applied to
+//   the fp32 partial product of its group.
 //
-// int4 decoding, two weights an instruction pair: (dword >> 4 i) & 0x000F000F leaves two
-// codes in the low bits of the two halves; OR-ing an exponent whose last mantissa bits they
-// become gives 128 + q in bf16 (0x4300) or 1024 + q in fp16 (0x6400), both exact.  The halves
-// hold elements (1, 5), (0, 4), (3, 7), (2, 6) of the dword's eight (the first of a pair
-// sits in the high nibble), so the activations are stored in that order too.  The product
+// Up to four activations with int4 weights (a listing of four, for experts): integer products.  An
+// activation is held as three signed bytes, X = RN(x 2^(21 - e)), e the exponent of the largest |x| of
+// its 128 (RowTiles::run), in three of four rows of A; the codes enter as the bytes 0..15, masked
+// out of the dword and its shift, 3 instructions per 8 codes against 7 or 9 below.  The int32 sums
+// are exact, and with X's sum over the group
+//     sum x (q - z) = 2^(e - 21) (sum X q - z sum X)
+// in fp32.  M = 1, seven weights of a layer: 29 us with the bf16 products below, 22 with these.
+//
+// More activations, bf16 and fp16 products (16x16x32), two weights an instruction pair:
+// (dword >> 4 i) & 0x000F000F leaves two codes in the low bits of the two halves; OR-ing an exponent
+// whose last mantissa bits they become gives 128 + q in bf16 (0x4300) or 1024 + q in fp16 (0x6400),
+// both exact.  The halves hold elements (1, 5), (0, 4), (3, 7), (2, 6) of the dword's eight (the first
+// of a pair sits in the high nibble), so the activations are stored in that order too.  The product
 // with W is then
 //     sum x (q - z) = sum x (128 + q) - (128 + z) sum x,
 // where sum x comes from one more MFMA against a matrix of ones, in the layout of D.  fp16
 // subtracts 1032 from each pair first (exact: q - 8), which leaves (z - 8) sum x.  In bf16
 // the subtraction happens in fp32 after the sums: its rounding error is 2^-24 of terms up to
 // 143 |x|, about 2^-19 of the group's result, far under the 2^-9 of the rounded output.
+//
+// 16 levels: codes become bf16 levels by a table in LDS of all 256 bytes.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -227,16 +237,23 @@ __device__ __forceinline__ u32x4_t decode8_table(uint32_t w, uint32_t lane4) {
 // kw of the waves split k, W / kw groups of them take different rows.  A row is cut into windows
 // of kw * 256 k; a wave takes one line (128 bytes, 256 k) of each row per window, and the
 // partial outputs of the kw waves meet in LDS once per item, where the last wave to arrive adds
-// them in wave order (the same bits every time).  No wave waits for another except every
-// kSlots items, and per window of these where the activations do not stay.  While a wave works on one window the codes and scales of
-// the next one (of the same item or the next) are already on their way into registers.
+// them in wave order (the same bits every time).  No wave waits for another except every kSlots
+// items, and per window of these where the activations do not stay.  While a wave works on one
+// window the codes and scales of the next one (of the same item or the next) are already on their
+// way into registers: 16 waves of a CU have 64 KB of codes in flight with RT = 2, 32 KB with RT = 1.
 //
-// Activations (in the order of decoded int4, zero past K) live in LDS, 16 bytes more than a row
-// apart, so that a fragment read of 16 rows falls in different banks: all of K for the whole run
-// (kResident), or the current window, loaded one window ahead and used for kSlots items.  With kSplit they are fp32 and
-// become two bf16 rows, hi and lo (activation m: rows 2 m and 2 m + 1; 16 bits of mantissa).
-// Scales go to LDS as well, per row and group the pair (scale, scale * (zero point + bias)); a
-// wave writes and reads only its own, an odd number of pairs apart.
+// The code is kept small (5 to 8 KB a kernel; the loops over chunks stay rolled): a launch fetches it
+// anew, at 0.3 us a KB, and the smallest calls take 4 us.
+//
+// Activations live in LDS, zero past K, 16 bytes more than a row apart, so that a fragment read of 16
+// rows falls in different banks: all of K for the whole run (kResident), or the current window,
+// loaded one window ahead and used for kSlots items; sums are made in the same order either way.
+// They are held as three planes of bytes and a pair (unit, sum) per scale group (kFix), or as 16-bit
+// values in the order of decoded int4.  With kSplit they are fp32 and, where not kFix, become two
+// bf16 rows, hi and lo (activation m: rows 2 m and 2 m + 1; 16 bits of mantissa).
+// Scales go to LDS as well, per row and group the pair (scale, zero point) for kFix, (scale, scale *
+// (zero point + bias)) for 16-bit products, the scale alone for levels; a wave writes and reads only
+// its own, an odd number of entries apart.
 //
 // Codes are read by buffer loads whose range check returns 0 without a memory access: rows past
 // the last one and lines past K cost no traffic and no branch.
@@ -276,8 +293,13 @@ __device__ __forceinline__ constexpr int act_of_row(int row) { return MI * (row 
 constexpr int kLineK = 256;               // k of a 128-byte line of codes
 
 // bytes of LDS beside the activations: scales, codes, partial sums of a few items and their counters
+// With a table one workgroup of 16 waves fills a CU (two of 8 have no room for two tables): 16 tokens, top 8 of 64
+// experts of 2048 x 1024, 68 us against 98 with 8 waves; one token 24 against 23.
 constexpr int w4_waves(Form f) { return f == kLevels ? 16 : 8; }
 constexpr int w4_put_bytes(Form f, int RT, int MI) { return w4_waves(f) * RT * 64 * MI * 4; }
+// items that a window of activations serves, or (resident) whose sums wait for their last wave without a barrier.  One
+// tile a wave above four activations: four, 34 us for the seven weights of a layer at M = 8, with two 39; for more
+// than eight there is room for two.
 constexpr int w4_slots(Form f, int RT, int MI, bool resident) {
     return resident || f == kLevels ? 2 : RT == 2 ? 3 : MI == 4 ? 2 : 4;
 }
