@@ -7,6 +7,10 @@ so an absolute error of at most 2^-24 * depth * sum |x| |s| (143 + |z + 128|) ar
 number of roundings an addend passes.  Every MFMA adds 32 products to an accumulator (taken as 32 roundings), a
 chunk makes up to 4 of them, a wave takes ceil(K / 1024) chunks, and 8 waves are added: depth <=
 128 + 2 ceil(K / 1024) + 8 + 4.
+Up to M = 4 the sums over a chunk are exact integers instead, of activations rounded to 2^-22 of their chunk's
+largest: 4 * 2^-24 max |x| for each |s| |q - z|.  Of values that are all of one size (|x| on average a fifth of the
+largest, as in random normal rows) that is 20 of the roundings above, and the 128 of the accumulators do not occur.
+Rows that are not of one size have a test of their own, which counts the largest value.
 """
 
 import pytest
