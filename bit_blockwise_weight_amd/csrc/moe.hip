@@ -115,7 +115,8 @@ __device__ __forceinline__ void route(const RouteArgs& a, RouteScratch& s, Route
 #pragma unroll 1
     for (int t = wave; t < a.T; t += kThr / 64)
 #pragma unroll 1
-        for (int e = lane; e < padded; e += 64) s.logit[t][e] = e < a.E ? load_logit(a.logits, a.dtype, t * a.E + e) : -INFINITY;
+        for (int e = lane; e < padded; e += 64)
+            s.logit[t][e] = e < a.E ? load_logit(a.logits, a.dtype, t * a.E + e) : -INFINITY;
     if (tid < kMaxE) {
         s.mask[tid] = 0;
         s.best[tid / kMaxK][tid % kMaxK] = -INFINITY;
@@ -246,8 +247,8 @@ size_t x_lds(int tokens, bool split, int64_t K, bool resident) {
 }
 template <int F, int NG, int RT, int MI>
 bool fits(int tokens, bool split, int64_t K) {
-    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes((Form)F, NG, RT, MI, true) + x_lds<F, NG, MI>(tokens, split, K, true) <=
-           kLdsBytes;
+    return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes((Form)F, NG, RT, MI, true) +
+               x_lds<F, NG, MI>(tokens, split, K, true) <= kLdsBytes;
 }
 // Tokens that a pass over an expert's rows takes; the down product needs two operand rows for one, but not in fixed
 // point.
