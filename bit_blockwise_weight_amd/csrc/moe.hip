@@ -370,10 +370,11 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* parts, co
     const int chosen = routes->chosen[t];
     const float* src = parts + (int64_t)t * top_k * H + n;
     float v = 0.0f;
-    for (int k0 = 0; k0 < chosen; k0 += 8) {             // eight loads on their way at a time
+    // eight loads on their way at a time, beside that of `chosen` (what lies behind it is stale and not added)
+    for (int k0 = 0; k0 < top_k; k0 += 8) {
         float part[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) part[k] = src[(k0 + k < chosen ? k0 + k : k0) * H];
+        for (int k = 0; k < 8; ++k) part[k] = src[(k0 + k < top_k ? k0 + k : k0) * H];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k0 + k < chosen) v += part[k];
