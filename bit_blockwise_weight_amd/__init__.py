@@ -11,6 +11,7 @@ not at import.
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -915,6 +916,9 @@ def qk_moe_workspace_size(T: int, top_k: int, hidden: int, inner: int) -> int:
     return int(out.value)
 
 
+_moe_bytes = functools.lru_cache(maxsize=256)(qk_moe_workspace_size)
+
+
 def _moe(fn, dtype_arg, x, logits, top_k, gate_up, down, renormalize, y, workspace, dev):
     hidden, inner = gate_up.cols, down.cols
     if logits.dtype not in _DTYPE_CODE:
@@ -931,7 +935,7 @@ def _moe(fn, dtype_arg, x, logits, top_k, gate_up, down, renormalize, y, workspa
     else:
         _check_out(y, (T, hidden), x.dtype, "y")
     if workspace is None:
-        workspace = torch.empty(qk_moe_workspace_size(T, top_k, hidden, inner), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_moe_bytes(T, top_k, hidden, inner), dtype=torch.uint8, device=dev)
     _call(dev, fn, xp, *dtype_arg, T, lp, _DTYPE_CODE[logits.dtype], E, int(top_k), 1 if renormalize else 0, gate_up,
           down, _ready(y, dev, "y"), _ready(workspace, dev, "workspace"), workspace.nbytes)
     return y
