@@ -18,9 +18,9 @@
 //                       kernel, by the wave that stores the last part, made that 82 us instead of 22 (16 tokens, top
 //                       8 of 64, 2048 x 1024): every wave then waits for its stores to reach memory.
 // Every weight of a listed expert is read once per listing; that is the bound.  At 6 TB/s, which a read of large
-// weights reaches, one token's top 2 of 8 experts of 4096 x 11008 take 24 us, measured 39; of 64 experts of
-// 2048 x 1024 with top 8 one token takes 4.4, measured 19 (three launches, the routing, one round of loads each),
-// sixteen tokens 31, measured 54 in int4 and 66 in NF4, whose table reads from LDS take as long as the loads.
+// weights reaches, one token's top 2 of 8 experts of 4096 x 11008 take 24 us, measured 38; of 64 experts of
+// 2048 x 1024 with top 8 one token takes 4.4, measured 18.5 (three launches, one round of loads each), sixteen
+// tokens 31, measured 54 in int4 and 66 in NF4, whose table reads from LDS take as long as the loads.
 #include <algorithm>
 
 #include "qk_device.h"
