@@ -1,7 +1,8 @@
 """qk_moe_int4 and qk_moe_nf4 against the layer in 64 bits.
 
 Tolerance, derived before the first run.  y is rounded once: finfo.eps / 2 relative to the value.  h is kept as a
-bf16 pair: 2^-8 of the first rounding times 2^-8 of the second, 2^-16 relative.  The two products are fp32 sums:
+bf16 pair: 2^-8 of the first rounding times 2^-8 of the second, 2^-16 relative.  (int4 experts with few tokens
+hold x and h to 2^-22 of the largest of 128 values instead, which for values of one size is less than that.)  The two products are fp32 sums:
 their errors are 2^-24 * depth of the sums of their absolute terms, scaled for int4 by the excess of the stored codes
 (up to 271 + |z| instead of |q - z|; see the GEMV's tests), which here multiplies the absolute weights.  depth of a
 product over K: 128 + 2 ceil(K / 128) + 32.
@@ -356,3 +357,26 @@ def test_experts_behind_four_gib():
     assert torch.equal(y[0], alone[0]) and torch.equal(y[2], alone[2])
     assert float((2 * y[1].double() - alone[1].double()).norm() / alone[1].double().norm()) < 2.0 ** -7
     assert bool((alone != 0).any())
+
+
+def test_first_call_inside_a_capture():
+    """Sizes that nothing ran before, captured without an eager call: the library sets up its kernels on the way."""
+    say("case: moe and gemv captured first")
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    H, I, E, T = 7040, 320, 5, 15
+    up, down = (Int4Experts(gen, E, 2 * I, H, 64, False, torch.bfloat16), Int4Experts(gen, E, H, I, 64, False, torch.bfloat16))
+    x = torch.randn((T, H), generator=gen, device="cuda").to(torch.float16)
+    lg = torch.randn((T, E), generator=gen, device="cuda")
+    y, z = torch.empty_like(x), torch.empty((T, 2 * E * I), dtype=x.dtype, device="cuda")
+    ws = torch.empty(qk.qk_moe_workspace_size(T, 3, H, I), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qk.qk_moe_int4(x, lg, 3, up.state, down.state, y=y, workspace=ws)
+        qk.qk_gemv_int4(x, up.state, z)
+    for _ in range(3):
+        y.zero_()
+        z.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, qk.qk_moe_int4(x, lg, 3, up.state, down.state)) and torch.equal(z, up.w.gemv(x))
