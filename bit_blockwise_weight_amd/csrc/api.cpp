@@ -952,7 +952,7 @@ const char* qk_backend_info(void) {
         "; lora_merge: fp32 adapter sum in LDS, fused dequant; qlora_backward: dX 256x128 tiles mfma 32x32x16 bf16 with "
         "W^T dequantized into LDS, dA/dB row-slice reductions; quantize_8bit: LDS bin table built per workgroup; "
         "int8_matmul: mfma 32x32x32 i8 256x256 tiles 8 waves, fp16 outlier mfma in the epilogue; "
-        "gemv_int4: whole lines through wave-private LDS, mfma 16x16x64 i8 up to 4 rows, 16x16x32 bf16 / f16 above; "
+        "gemv_int4: whole lines through wave-private LDS, mfma 16x16x32 f16 of exact code - zero; "
         "moe: routing in the up kernel, up and down products of the listed experts, combine";
     return s.c_str();
 }

@@ -87,22 +87,18 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
     });
 }
 
-// Registers of a product that carry activations: the least that hold M rows.  Up to four rows take the integer
-// product (w4_tile.h): the layer at M = 1 22 us, in bf16 28; at M = 4 27 and 35.  (4096 x 11008 alone at M = 4 would be
-// faster in bf16, 10 us against 15: every workgroup converts the rows anew.  But which product a weight takes may not
-// depend on its launch.)  Five to eight in the form of sixteen: 40 us instead of 34.
+// Registers of a product that carry activations: the least that hold M rows.
 constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
-size_t lds_bytes(int M, int ng, int rt, int64_t K, bool resident) {
+size_t lds_bytes(int M, bool f16, int ng, int rt, int64_t K, bool resident) {
     const int mi = mi_for(M), kw = 1 << w4_most_kwl(kInt4Bf16, mi);
     return w4_fixed_bytes(kInt4Bf16, ng, rt, mi, resident) +
-           (mi == 1 ? w4_fix_bytes(kw, M, ng, K, resident) : w4_x_bytes(kw, M, K, resident));
+           w4_x_bytes(f16 ? kInt4F16 : kInt4Bf16, kw, M, mi, false, K, resident);
 }
 // The activations of a whole row stay in LDS where they fit; above four rows where they leave room for a second
-// workgroup on the CU (28672 x 8192 at M = 8: 32.5 us streaming with two, 33.1 resident with one; up to four, resident
-// at any size was faster, 25 us against 32 for the layer at M = 3).
-bool resident_for(int M, int ng, int rt, int64_t K) {
-    return lds_bytes(M, ng, rt, K, true) <= (M > 4 ? kLdsBytes / 2 : kLdsBytes);
+// workgroup on the CU.
+bool resident_for(int M, bool f16, int ng, int rt, int64_t K) {
+    return lds_bytes(M, f16, ng, rt, K, true) <= (M > 4 ? kLdsBytes / 2 : kLdsBytes);
 }
 
 constexpr int32_t kNever = 0x7FFFFFFF;
@@ -212,8 +208,8 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
         // groups of 32: the layer 50 us, with two 59; M = 8, groups of 128, 34 and 47).
         l.rt = mi_for(M) == 1 && pairs > (int64_t)per_cu_most * device_cu_count() ? 2 : 1;
         // (an output's bits do not depend on whether the activations stay)
-        l.resident = resident_for(M, l.ng, l.rt, kmax);
-        l.lds = lds_bytes(M, l.ng, l.rt, kmax, l.resident);
+        l.resident = resident_for(M, f16, l.ng, l.rt, kmax);
+        l.lds = lds_bytes(M, f16, l.ng, l.rt, kmax, l.resident);
         const int per_cu = l.lds > kLdsBytes / 2 ? 1 : per_cu_most;
         for (int32_t i = 0; i < n; ++i) {
             const int64_t step = (128 * l.rt) >> g.t[i].kwl;

@@ -10,10 +10,9 @@
 //                       increasing order, each with its tokens, their weights and their pairs (token, position).
 //                       Then items of 16 rows of gate and the same 16 of up of a listed expert (RowTiles,
 //                       w4_tile.h), dealt in equal shares; only the expert's own tokens are staged.  h is fp32.
-//   moe_down_kernel     items of rows of Wd of a listed expert times its tokens' h, which enters the matrix cores in
-//                       fixed point (22 bits below the largest of 128 values) or as two bf16 values (hi + lo, 16
-//                       bits of mantissa), so the product loses nothing against the 16-bit output; w h Wd^T goes
-//                       to memory in fp32.
+//   moe_down_kernel     items of rows of Wd of a listed expert times its tokens' h, which enters the matrix cores as two
+//                       values, hi + lo (w4_tile.h: int4 fp16, 24 bits of mantissa, levels bf16, 16 bits); w h Wd^T
+//                       goes to memory in fp32.
 //   moe_combine_kernel  adds each token's parts in the order of its choices: no atomics.  Adding them in the down
 //                       kernel, by the wave that stores the last part, made that 82 us instead of 22 (16 tokens, top
 //                       8 of 64, 2048 x 1024): every wave then waits for its stores to reach memory.
@@ -259,18 +258,16 @@ int64_t workgroups(int64_t items, size_t lds) {
 template <int F, int NG, int MI>
 size_t x_lds(int tokens, bool split, int64_t K, bool resident) {
     constexpr int kw = 1 << w4_most_kwl((Form)F, MI);
-    return F != kLevels && MI == 1 ? w4_fix_bytes(kw, tokens, NG, K, resident)
-                                   : w4_x_bytes(kw, split ? 2 * tokens : tokens, K, resident);
+    return w4_x_bytes((Form)F, kw, split ? 2 * tokens : tokens, MI, split, K, resident);
 }
 template <int F, int NG, int RT, int MI>
 bool fits(int tokens, bool split, int64_t K) {
     return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes((Form)F, NG, RT, MI, true) +
                x_lds<F, NG, MI>(tokens, split, K, true) <= kLdsBytes;
 }
-// Tokens that a pass over an expert's rows takes; the down product needs two operand rows for one, but not in fixed
-// point.
-template <int F, int MI, bool kSplit>
-constexpr int kTokens = kSplit && (F == kLevels || MI > 1) ? 2 * MI : 4 * MI;
+// Tokens that a pass over an expert's rows takes; the down product needs two operand rows for one.
+template <int MI, bool kSplit>
+constexpr int kTokens = kSplit ? 2 * MI : 4 * MI;
 
 template <int F, int NG, int MI, bool kResident>
 __global__ __launch_bounds__(kThreads<F>, 4) void moe_up_kernel(ExpertArgs<F> p, RouteArgs ra, Routes* keep) {
@@ -357,7 +354,7 @@ __global__ __launch_bounds__(kThreads<F>, 4) void moe_down_kernel(ExpertArgs<F> 
         r.x_rows = p.x_rows;
         r.x_aligned = 1;
         r.kwl = p.kwl;
-        constexpr int kTok = kTokens<F, MI, true>;
+        constexpr int kTok = kTokens<MI, true>;
         for (int m0 = 0; m0 < count; m0 += kTok) {
             const int M = count - m0 < kTok ? count - m0 : kTok;
             r.xrow = p.routes->pair + first + m0;
@@ -366,12 +363,9 @@ __global__ __launch_bounds__(kThreads<F>, 4) void moe_down_kernel(ExpertArgs<F> 
                 for (int o = threadIdx.x & 63; o < M * (16 * RT); o += 64) {
                     const int m = o / (16 * RT), row = o % (16 * RT), t = row / 16;
                     const int n = item * step + q * (16 * RT) + row;
-                    float v;
-                    if constexpr (Tiles::kFix)
-                        v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, m));
-                    else                                 // two operand rows a token
-                        v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m)) +
-                            Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m + 1));
+                    // two operand rows a token
+                    const float v = Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m)) +
+                                    Tiles::sum(put, p.kwl, q, t, Tiles::place_of(row & 15, 2 * m + 1));
                     if (n < p.H) p.out[(int64_t)p.routes->pair[first + m0 + m] * p.H + n] = v * p.routes->w[first + m0 + m];
                 }
             });
@@ -399,7 +393,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* parts, co
     y[t * H + n] = float_to_bits16(v, f16);
 }
 
-// rows: activation rows that a pass stages at most
+// tokens: that a pass stages at most; listed: the most listings that there can be
 template <int F, int NG, int MI, bool kResident>
 hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
@@ -417,8 +411,8 @@ hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int
 
 template <int F, int NG, int MI>
 hipError_t launch_up_mi(const ExpertArgs<F>& p, RouteArgs ra, Routes* keep, int32_t* listed, hipStream_t s) {
-    const int tokens = std::min(ra.T, kTokens<F, MI, false>);
-    ra.most = kTokens<F, MI, false>;
+    const int tokens = std::min(ra.T, kTokens<MI, false>);
+    ra.most = kTokens<MI, false>;
     *listed = std::min(ra.E * ((ra.T + ra.most - 1) / ra.most), ra.T * ra.top_k);
     if (fits<F, NG, 2, MI>(tokens, false, p.H)) return launch_up_one<F, NG, MI, true>(p, ra, keep, tokens, *listed, s);
     return launch_up_one<F, NG, MI, false>(p, ra, keep, tokens, *listed, s);
@@ -452,20 +446,20 @@ hipError_t launch_down_one(ExpertArgs<F> p, int tokens, int32_t listed, hipStrea
 
 template <int F, int NG, int MI>
 hipError_t launch_down_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hipStream_t s) {
-    const int tokens = std::min(T, kTokens<F, MI, true>);
+    const int tokens = std::min(T, kTokens<MI, true>);
     if (!fits<F, NG, 2, MI>(tokens, true, p.I)) return launch_down_one<F, NG, 2, MI, false>(p, tokens, listed, s);
     return launch_down_one<F, NG, 2, MI, true>(p, tokens, listed, s);
 }
 
-// Tokens of a pass of the down product.  int4: four in fixed point, or eight as pairs of bf16 where experts are crowded
-// (the case of 16 tokens and 8 experts above: 71 / 65 us).  Levels, two or four: equal up to two tokens, with four
-// at a time top 8 of 64 experts take 40 us for 4 tokens instead of 48, and 65 for 16 instead of 79; one expert of two
-// tokens, 4096 x 4096, 44 us instead of 38.
+// Tokens of a pass of the down product, two or four, in int4 eight where experts are crowded.  Levels: equal up to two
+// tokens, with four at a time top 8 of 64 experts take 40 us for 4 tokens instead of 48, and 65 for 16 instead of 79; one
+// expert of two tokens, 4096 x 4096, 44 us instead of 38.
 template <int F, int NG>
 hipError_t launch_down(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, hipStream_t s) {
-    const bool few = F == kLevels ? m.T <= 2 : m.T <= 4 || m.T * m.top_k < 4 * m.E;
-    if (few) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
-    return launch_down_mi<F, NG, F == kLevels ? 2 : 4>(p, m.T, listed, s);
+    if (m.T <= 2) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
+    if constexpr (F != kLevels)
+        if (m.T > 4 && m.T * m.top_k >= 4 * m.E) return launch_down_mi<F, NG, 4>(p, m.T, listed, s);
+    return launch_down_mi<F, NG, 2>(p, m.T, listed, s);
 }
 
 LevelsView levels_view(const MatArgs& w) {

@@ -16,27 +16,19 @@
 //   n = l % 16, rows m = 4 (l / 16) + r.  A scale of row n is then one value per lane, applied to
 //   the fp32 partial product of its group.
 //
-// Up to four activations with int4 weights (a listing of four, for experts): integer products.  An
-// activation is held as three signed bytes, X = RN(x 2^(21 - e)), e the exponent of the largest |x| of
-// its 128 (RowTiles::run), in three of four rows of A; the codes enter as the bytes 0..15, masked
-// out of the dword and its shift, 3 instructions per 8 codes against 7 or 9 below.  The int32 sums
-// are exact, and with X's sum over the group
-//     sum x (q - z) = 2^(e - 21) (sum X q - z sum X)
-// in fp32.  M = 1, seven weights of a layer: 29 us with the bf16 products below, 22 with these.
+// int4 products are fp16 (16x16x32), two weights an instruction pair: (dword >> 4 i) & 0x000F000F leaves two codes in
+// the low bits of the two halves; OR-ing 0x6400, an exponent whose last mantissa bits they become, gives 1024 + q, and
+// 1024 + z taken off in fp16 leaves q - z, all of it exact.  The halves hold elements (1, 5), (0, 4), (3, 7), (2, 6)
+// of the dword's eight (the first of a pair sits in the high nibble), so the activations are stored in that order
+// too.  The zero point goes before the product, not after the sum: a sum of x (128 + q) less (128 + z) times the sum of x, the
+// bf16 way, loses the neighbours of a large x whose q - z is 0.
 //
-// More activations, bf16 and fp16 products (16x16x32), two weights an instruction pair:
-// (dword >> 4 i) & 0x000F000F leaves two codes in the low bits of the two halves; OR-ing an exponent
-// whose last mantissa bits they become gives 128 + q in bf16 (0x4300) or 1024 + q in fp16 (0x6400),
-// both exact.  The halves hold elements (1, 5), (0, 4), (3, 7), (2, 6) of the dword's eight (the first
-// of a pair sits in the high nibble), so the activations are stored in that order too.  The product
-// with W is then
-//     sum x (q - z) = sum x (128 + q) - (128 + z) sum x,
-// where sum x comes from one more MFMA against a matrix of ones, in the layout of D.  fp16
-// subtracts 1032 from each pair first (exact: q - 8), which leaves (z - 8) sum x.  In bf16
-// the subtraction happens in fp32 after the sums: its rounding error is 2^-24 of terms up to
-// 143 |x|, about 2^-19 of the group's result, far under the 2^-9 of the rounded output.
+// Activations other than fp16 ones are scaled by a power of two for each run of 128 (a chunk), 2^(14 - e) with e the
+// exponent of the largest |x|, and become fp16 values: bf16 exactly down to 2^-31 of the largest, below to 2^-38 of it;
+// fp32 (h of the expert layer) as a pair hi + lo, to 2^-24 of themselves, or 2^-38 of the largest.  Each chunk's sums are
+// multiplied by 2^(e - 14) in fp32.
 //
-// 16 levels: codes become bf16 levels by a table in LDS of all 256 bytes.
+// 16 levels: bf16 products, codes become bf16 levels by a table in LDS of all 256 bytes.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -55,7 +47,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
-typedef int32_t intx4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x3_t __attribute__((ext_vector_type(3)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -106,33 +97,25 @@ __device__ __forceinline__ constexpr int chunk_k(int j, int h) {
 // which may read one scalar register and no literal).
 struct Magic {
     uint32_t m0, m4, e;          // masks of the low nibbles, of the next ones; exponent
-    __device__ __forceinline__ explicit Magic(bool f16) : m0(0x000F000Fu), m4(0x00F000F0u), e(f16 ? 0x64006400u : 0x43004300u) {
+    __device__ __forceinline__ Magic() : m0(0x000F000Fu), m4(0x00F000F0u), e(0x64006400u) {
         asm("" : "+s"(m0));
         asm("" : "+s"(m4));
         asm("" : "+v"(e));
     }
 };
 
-// Eight codes of a dword as an MFMA fragment (int4 forms): 7 instructions in bf16, 9 in fp16.
-template <int F>
-__device__ __forceinline__ u32x4_t decode8(uint32_t w, const Magic& k) {
-    static_assert(F == kInt4Bf16 || F == kInt4F16, "levels are decoded through their table");
+// Eight codes of a dword, less the zero point, as an MFMA fragment: 9 instructions.  zero: -(1024 + z) twice, zero4:
+// -(64 + z).
+__device__ __forceinline__ u32x4_t decode8(uint32_t w, f16x2_t zero, f16x2_t zero4, const Magic& k) {
+    // 1024 + q less 1024 + z, or (1024 + 16 q) / 16 less 64 + z
+    const uint32_t v = w >> 8;
+    const f16x2_t sc = {0.0625f, 0.0625f};
+    const uint32_t a0 = (w & k.m0) | k.e, a1 = (w & k.m4) | k.e, a2 = (v & k.m0) | k.e, a3 = (v & k.m4) | k.e;
     u32x4_t f;
-    if constexpr (F == kInt4Bf16) {
-        f[0] = (w & k.m0) | k.e;
-        f[1] = ((w >> 4) & k.m0) | k.e;
-        f[2] = ((w >> 8) & k.m0) | k.e;
-        f[3] = ((w >> 12) & k.m0) | k.e;
-    } else {
-        // 1024 + q less 1032, or (1024 + 16 q) / 16 less 72: q - 8 either way, exact
-        const uint32_t v = w >> 8;
-        const f16x2_t c1 = {-1032, -1032}, sc = {0.0625f, 0.0625f}, c2 = {-72, -72};
-        const uint32_t a0 = (w & k.m0) | k.e, a1 = (w & k.m4) | k.e, a2 = (v & k.m0) | k.e, a3 = (v & k.m4) | k.e;
-        f[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a0) + c1);
-        f[1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, a1), sc, c2));
-        f[2] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a2) + c1);
-        f[3] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, a3), sc, c2));
-    }
+    f[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a0) + zero);
+    f[1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, a1), sc, zero4));
+    f[2] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a2) + zero);
+    f[3] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, a3), sc, zero4));
     return f;
 }
 
@@ -147,36 +130,13 @@ __device__ __forceinline__ u32x4_t int4_order(u32x4_t v) {
 }
 template <int F>
 __device__ __forceinline__ floatx4_t mfma(u32x4_t a, u32x4_t b, floatx4_t c) {
-    if constexpr (F == kInt4F16)
+    if constexpr (F != kLevels)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
                                                       0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                        __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
-
-// Integer products of four dwords' 8 codes each, as bytes: 3 instructions a dword (the odd codes, then the even
-// ones; the activations' bytes are stored in that order).
-__device__ __forceinline__ intx4_t mfma_i8_64(u32x4_t a, uint32_t w0, uint32_t w1, intx4_t c) {
-    const u32x4_t b = {w0 & 0x0F0F0F0Fu, (w0 >> 4) & 0x0F0F0F0Fu, w1 & 0x0F0F0F0Fu, (w1 >> 4) & 0x0F0F0F0Fu};
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(intx4_t, a), __builtin_bit_cast(intx4_t, b), c, 0, 0,
-                                                 0);
-}
-__device__ __forceinline__ intx4_t mfma_i8_32(uint32_t a0, uint32_t a1, uint32_t w, intx4_t c) {
-    const uint64_t a = a0 | ((uint64_t)a1 << 32);
-    const uint64_t b = (w & 0x0F0F0F0Fu) | ((uint64_t)((w >> 4) & 0x0F0F0F0Fu) << 32);
-    return __builtin_amdgcn_mfma_i32_16x16x32_i8((long)a, (long)b, c, 0, 0, 0);
-}
-
-// A fragment of ones, and what the stored codes exceed q by.
-template <int F>
-__device__ __forceinline__ u32x4_t ones() {
-    constexpr uint32_t k = F == kInt4F16 ? 0x3C003C00u : 0x3F803F80u;
-    return (u32x4_t){k, k, k, k};
-}
-template <int F>
-constexpr float kCodeBias = F == kInt4Bf16 ? 128.0f : -8.0f;
-
 
 // One int4 weight as the kernels see it.
 struct Int4View {
@@ -248,17 +208,15 @@ __device__ __forceinline__ u32x4_t decode8_table(uint32_t w, uint32_t lane4) {
 // Activations live in LDS, zero past K, 16 bytes more than a row apart, so that a fragment read of 16
 // rows falls in different banks: all of K for the whole run (kResident), or the current window,
 // loaded one window ahead and used for kSlots items; sums are made in the same order either way.
-// They are held as three planes of bytes and a pair (unit, sum) per scale group (kFix), or as 16-bit
-// values in the order of decoded int4.  With kSplit they are fp32 and, where not kFix, become two
-// bf16 rows, hi and lo (activation m: rows 2 m and 2 m + 1; 16 bits of mantissa).
-// Scales go to LDS as well, per row and group the pair (scale, zero point) for kFix, (scale, scale *
-// (zero point + bias)) for 16-bit products, the scale alone for levels; a wave writes and reads only
-// its own, an odd number of entries apart.
+// They are 16-bit values, for int4 in the order of its decoded codes, with a factor for each chunk and row behind them
+// where they are scaled.  With kSplit they are fp32 and become two rows, hi and lo (activation m: rows 2 m and
+// 2 m + 1): fp16 for int4, bf16 (16 bits of mantissa) for levels.
+// Scales go to LDS as well, per row and group the pair (scale, -(1024 + zero point)) for int4, the scale alone for
+// levels; a wave writes and reads only its own, an odd number of entries apart.
 //
 // Codes are read by buffer loads whose range check returns 0 without a memory access: rows past
 // the last one and lines past K cost no traffic and no branch.
 // ---------------------------------------------------------------------------
-typedef __attribute__((ext_vector_type(2))) float floatx2_t;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
     const int32_t n = (int32_t)(bytes < 0x7FFF0000 ? bytes : 0x7FFF0000);
@@ -328,15 +286,13 @@ hipError_t allow_lds(size_t lds) {
     return e;
 }
 
-// bytes of LDS that the activations take: rows of 16-bit values (two an activation with kSplit), or M
-// activations in fixed point, three bytes a value and a pair per scale group (NG of them in a chunk)
-inline size_t w4_x_bytes(int kw, int rows, int64_t K, bool resident) {
+// Whether activations are scaled chunk by chunk: fp16 ones are what the product takes.
+constexpr bool w4_scaled(Form f, bool split) { return f != kLevels && (split || f != kInt4F16); }
+// bytes of LDS that the activations take: rows of 16-bit values (two an activation with kSplit), and the factors of the
+// chunks for the 4 mi rows of the operand
+inline size_t w4_x_bytes(Form f, int kw, int rows, int mi, bool split, int64_t K, bool resident) {
     const size_t k = resident ? (size_t)((K + kLineK - 1) / kLineK) * kLineK : (size_t)kw * kLineK;
-    return (size_t)rows * (k * 2 + 16);
-}
-inline size_t w4_fix_bytes(int kw, int M, int NG, int64_t K, bool resident) {
-    const size_t k = resident ? (size_t)((K + kLineK - 1) / kLineK) * kLineK : (size_t)kw * kLineK;
-    return (size_t)M * (3 * (k + 16) + k / kChunk * NG * 8);
+    return (size_t)rows * (k * 2 + 16) + (w4_scaled(f, split) ? k / kChunk * (size_t)(16 * mi) : 0);
 }
 // log2 of the waves that split a row of K: as many as it has lines, up to 8; more (some then have nothing to do) as
 // long as there are fewer items than CUs.  rows: of all items, in pieces of `piece` rows that a wave takes
@@ -353,7 +309,8 @@ struct RowTiles {
     static constexpr Form kForm = (Form)F;
     static constexpr int W = w4_waves(kForm);
     static constexpr int kThreads = W * 64;
-    static constexpr bool kFix = F != kLevels && MI == 1;       // up to four activations, in fixed point
+    static constexpr bool kScaled = w4_scaled(kForm, kSplit);
+    static constexpr int kOpRows = 4 * MI;                      // rows of the operand that carry activations, at most
     static constexpr int U = 2;                                 // chunks of a wave in a window
     static constexpr int kMfmas = 4 / NG;                       // MFMAs per scale group
     static constexpr int kEntries = U * NG;                     // scale groups of a wave's chunks in a window
@@ -364,15 +321,23 @@ struct RowTiles {
     static constexpr int kPutBytes = w4_put_bytes(kForm, RT, MI);
     static constexpr int kSlots = w4_slots(kForm, RT, MI, kResident);
     // units of x per thread and batch; a window's fit one batch
-    static constexpr int kMaxM = kSplit && !kFix ? 2 * MI : 4 * MI;
-    static constexpr int kXUnits = kResident ? (kFix ? 1 : 2) : ((kMaxM * 32 << w4_most_kwl(kForm, MI)) + kThreads - 1) / kThreads;
+    static constexpr int kMaxM = kSplit ? 2 * MI : 4 * MI;
+    static constexpr int kXUnits = kResident ? (MI == 1 && F != kLevels ? 1 : 2) : ((kMaxM * 32 << w4_most_kwl(kForm, MI)) + kThreads - 1) / kThreads;
     static constexpr int kFixedBytes = w4_fixed_bytes(kForm, NG, RT, MI, kResident);
 
     static_assert(RT == 1 || RT == 2);
     // The scales of a window come by one load per kind, in lane 16 r + n for row n of tile r (a load instruction that
     // touches many lines costs as much as one that brings a kilobyte of codes): as dwords from an address rounded
     // down to 4 bytes, put right when they land.
-    typedef std::conditional_t<F == kLevels, float, floatx2_t> Scale;
+    struct alignas(4 * MI) Factors {
+        float v[MI];
+        __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+    };
+    struct ScaleZero {
+        float s;
+        uint32_t zero;       // -(1024 + z) in fp16, twice
+    };
+    typedef std::conditional_t<F == kLevels, float, ScaleZero> Scale;
     struct Fetched {
         u32x4_t c[RT][2];
         u32x4_t s;           // int4: 2 NG scales; levels: four block scales of a plain weight
@@ -404,12 +369,13 @@ struct RowTiles {
         const int nchunk = (p.K + kChunk - 1) / kChunk;
         const int wchunks = kw * U;
         const int xchunks = kResident ? (nchunk + U - 1) / U * U : wchunks;   // chunks of x that LDS holds
-        const int xpitch = xchunks * (kFix ? kChunk : 2 * kChunk) + 16;
-        const int xrows = kFix ? 3 * p.M : kSplit ? 2 * p.M : p.M;
-        const Magic magic(F == kInt4F16);
-        float mean = 0.0f, zbias = 0.0f;
+        const int xpitch = xchunks * (2 * kChunk) + 16;
+        const int xrows = kSplit ? 2 * p.M : p.M;
+        const Magic magic;
+        float mean = 0.0f;
+        uint32_t zbase = 0;                                      // -1024 in fp16, and the zero point where there is no array
         if constexpr (F == kLevels) mean = w.nested ? *w.dq_mean : 0.0f;
-        else zbias = (kFix ? 0.0f : kCodeBias<F>) + (w.zeros ? 0.0f : 8.0f);
+        else zbase = 0xE400u + (w.zeros ? 0u : 8u);
         // Staging of activations, thread by thread, rows as if they had 2^ush units of 8 values.  A unit is read
         // as four dwords from an address rounded down to 4 bytes, and one dword more where rows may start
         // between dwords, and put right (and zero past K) when it is stored.
@@ -455,114 +421,69 @@ struct RowTiles {
         };
         // Every thread stores (what lies outside, to the 16 bytes behind row 0, which nobody reads): under a
         // condition the compiler would move the loads down to it, behind those of the codes.
-        // Fixed point: with e the exponent of the largest |x| of a chunk (16 lanes hold it), X = RN(x 2^(21 - e)) is
-        // an integer of 23 bits, kept as three signed bytes, X = b0 2^16 + b1 2^8 + b2; products with the codes
-        // are then exact int32 sums.  The rounding, at most 2^-22 of the chunk's largest value, is the size of
-        // the rounding of an fp32 sum that holds that value.
-        auto x_store_fix = [&](uint8_t* dst, int base, int k0) {
-            // (a rolled loop over the units of the batch, each moved to the front when its turn comes)
-            const int batch = min(total, base + kXUnits * kThreads);
-#pragma unroll 1
-            for (; base < batch; base += kThreads) {
-                const int i = base + tid, m = i >> ush, u = i & ((1 << ush) - 1), k = k0 + 8 * u;
-                const bool in = i < total && u < units;
+        // Stores unit b of a batch, the thread's i-th of all.
+        auto x_store_unit = [&](uint8_t* dst, int b, int i, int k0) {
+            const int m = i >> ush, u = i & ((1 << ush) - 1);
+            const bool in = i < total && u < units;
+            u32x4_t hi, lo;
+            if constexpr (!kSplit) hi = x_unit(b, m, k0 + 8 * u);
+            if constexpr (kScaled) {
                 float v[8];
+                uint32_t big;
                 if constexpr (kSplit) {
+                    big = 0;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = as_float(xr[0][q >> 2][q & 3]);
+                    for (int q = 0; q < 8; ++q) {
+                        v[q] = as_float(xr[b][q >> 2][q & 3]);
+                        big = max(big, as_uint(v[q]) & 0x7FFFFFFFu);
+                    }
                 } else {
-                    const u32x4_t x8 = x_unit(0, m, k);
+                    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+                    u16x2_t most = {0, 0};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t d = x8[q];
-                        if constexpr (F == kInt4F16) {
-                            v[2 * q] = f16_bits_to_float((uint16_t)d);
-                            v[2 * q + 1] = f16_bits_to_float((uint16_t)(d >> 16));
-                        } else {
-                            v[2 * q] = bf16_lo(d);
-                            v[2 * q + 1] = bf16_hi(d);
-                        }
+                        v[2 * q] = bf16_lo(hi[q]);
+                        v[2 * q + 1] = bf16_hi(hi[q]);
+                        most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, hi[q] & 0x7FFF7FFFu));
+                    }
+                    big = (uint32_t)max(most[0], most[1]) << 16;
+                }
+                // (16 lanes hold a chunk; below 2^-112, where 2^(e - 14) ends, by the factor of 2^-112; an infinity
+                // or a NaN stays one)
+                const uint32_t e = max(group_max_u32<16>(big) >> 23, 15u);
+                const float up = as_float((268u - e) << 23);                    // 2^(14 - (e - 127))
+                if (in && (lane & 15) == 0) {
+                    float* f = reinterpret_cast<float*>(dst + xrows * xpitch) + (u >> 4) * kOpRows + (kSplit ? 2 * m : m);
+                    f[0] = as_float((e - 14u) << 23);
+                    if constexpr (kSplit) f[1] = f[0];
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float a = v[2 * q] * up, c = v[2 * q + 1] * up;
+                    if constexpr (kSplit) {
+                        const _Float16 ah = (_Float16)a, ch = (_Float16)c;
+                        hi[q] = __builtin_bit_cast(uint32_t, (f16x2_t){ah, ch});
+                        lo[q] = __builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)(a - (float)ah), (_Float16)(c - (float)ch)});
+                    } else {
+                        hi[q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, c));
                     }
                 }
+            } else if constexpr (kSplit) {
 #pragma unroll
-                for (int b = 0; b + 1 < kXUnits; ++b) {
-                    xr[b][0] = xr[b + 1][0];
-                    if constexpr (kSplit) xr[b][1] = xr[b + 1][1];
-                    else xe[b] = xe[b + 1];
-                }
-                uint32_t big = 0;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) big = max(big, as_uint(v[q]) & 0x7FFFFFFFu);
-                const uint32_t e = max(group_max_u32<16>(big) >> 23, 27u);      // below 2^-100: lost against 2^-121
-                const float up = as_float((148u + 127u - e) << 23);             // 2^(21 - (e - 127))
-                // X + 0x8080 from the low bits of x 2^(21 - e) + 1.5 2^23; its bytes are b0, b1 + 128 and b2 + 128
-                uint32_t X[8];
-                int32_t sum = -8 * 0x8080;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float r = __builtin_fmaf(v[q], up, 12582912.0f);
-                    if constexpr (kSplit) r = fminf(r, 16777215.0f);            // fp32 may round up to 2^22: 1 less
-                    X[q] = as_uint(r) - (0x4B400000u - 0x8080u);
-                    sum += (int32_t)X[q];
-                }
-                // sums over a scale group (or a chunk): 4, 8 or 16 lanes
-                sum += __builtin_amdgcn_mov_dpp(sum, 0xB1, 0xF, 0xF, false);    // xor 1
-                sum += __builtin_amdgcn_mov_dpp(sum, 0x4E, 0xF, 0xF, false);    // xor 2
-                if constexpr (NG <= 2) sum += __builtin_amdgcn_mov_dpp(sum, 0x141, 0xF, 0xF, false);   // half mirror
-                if constexpr (NG == 1) sum += __builtin_amdgcn_mov_dpp(sum, 0x140, 0xF, 0xF, false);   // mirror
-                u32x2_t d0, d1, d2;
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {                    // the odd values, then the even ones
-                    const uint32_t *q = X + 1 - o;
-                    const uint32_t ab = __builtin_amdgcn_perm(q[2], q[0], 0x05010400u);     // b2 b2 b1 b1
-                    const uint32_t cd = __builtin_amdgcn_perm(q[6], q[4], 0x05010400u);
-                    d2[o] = __builtin_amdgcn_perm(cd, ab, 0x05040100u) ^ 0x80808080u;
-                    d1[o] = __builtin_amdgcn_perm(cd, ab, 0x07060302u) ^ 0x80808080u;
-                    d0[o] = __builtin_amdgcn_perm(q[2], q[0], 0x0C0C0602u) | __builtin_amdgcn_perm(q[6], q[4], 0x06020C0Cu);
-                }
-                const int at = in ? 3 * m * xpitch + 8 * u : xpitch - 16, row = in ? xpitch : 0;
-                *reinterpret_cast<u32x2_t*>(dst + at) = d0;
-                *reinterpret_cast<u32x2_t*>(dst + at + row) = d1;
-                *reinterpret_cast<u32x2_t*>(dst + at + 2 * row) = d2;
-                if (in && (lane & (16 / NG - 1)) == 0) {         // (2^(e - 21), sum); an infinity or a NaN makes its row NaN
-                    const float down = e == 255 ? __builtin_nanf("") : as_float((e + 127u - 148u) << 23);
-                    reinterpret_cast<floatx2_t*>(dst + 3 * p.M * xpitch)[m * (xchunks * NG) + (u * NG >> 4)] =
-                        (floatx2_t){down, (float)sum};
+                for (int q = 0; q < 4; ++q) {
+                    const float a = as_float(xr[b][q >> 1][2 * (q & 1)]), c = as_float(xr[b][q >> 1][2 * (q & 1) + 1]);
+                    const uint32_t pk = pack_bf16x2(a, c);
+                    hi[q] = pk;
+                    lo[q] = pack_bf16x2(a - bf16_lo(pk), c - bf16_hi(pk));
                 }
             }
+            const int at = in ? (kSplit ? 2 * m : m) * xpitch + 16 * u : xpitch - 16;
+            *reinterpret_cast<u32x4_t*>(dst + at) = F == kLevels ? hi : int4_order(hi);
+            if constexpr (kSplit) *reinterpret_cast<u32x4_t*>(dst + (in ? at + xpitch : at)) = F == kLevels ? lo : int4_order(lo);
         };
         auto x_store = [&](uint8_t* dst, int base, int k0) {
-            if constexpr (kFix) {
-                x_store_fix(dst, base, k0);
-                return;
-            }
 #pragma unroll
-            for (int b = 0; b < kXUnits; ++b) {
-                const int i = base + b * kThreads + tid, m = i >> ush, u = i & ((1 << ush) - 1);
-                const bool in = i < total && u < units;
-                if constexpr (kSplit) {
-                    u32x4_t hi, lo;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t w0 = xr[b][j >> 1][2 * (j & 1)], w1 = xr[b][j >> 1][2 * (j & 1) + 1];
-                        const float a = as_float(w0), c = as_float(w1);
-                        const uint32_t pk = pack_bf16x2(a, c);
-                        hi[j] = pk;
-                        lo[j] = pack_bf16x2(a - bf16_lo(pk), c - bf16_hi(pk));
-                    }
-                    if constexpr (F != kLevels) {
-                        hi = int4_order(hi);
-                        lo = int4_order(lo);
-                    }
-                    const int at = in ? 2 * m * xpitch + 16 * u : xpitch - 16;
-                    *reinterpret_cast<u32x4_t*>(dst + at) = hi;
-                    *reinterpret_cast<u32x4_t*>(dst + (in ? at + xpitch : at)) = lo;
-                } else {
-                    const int at = in ? m * xpitch + 16 * u : xpitch - 16;
-                    const u32x4_t v = x_unit(b, m, k0 + 8 * u);
-                    *reinterpret_cast<u32x4_t*>(dst + at) = F == kLevels ? v : int4_order(v);
-                }
-            }
+            for (int b = 0; b < kXUnits; ++b) x_store_unit(dst, b, base + b * kThreads + tid, k0);
         };
 
         // Codes and scales of the wave's line in the window that starts at chunk c0 of the item whose tile 0
@@ -705,79 +626,21 @@ struct RowTiles {
 #pragma unroll
                 for (int e = 0; e < kEntries; ++e) {
                     const uint16_t bits = (uint16_t)(sv[e >> 1] >> (16 * (e & 1)));
-                    floatx2_t v;
-                    v[0] = w.scale_f16 ? f16_bits_to_float(bits) : bf16_bits_to_float(bits);
-                    v[1] = (float)((zv[e >> 2] >> (8 * (e & 3))) & 255u) + zbias;
-                    if constexpr (!kFix) v[1] *= v[0];
-                    slds[lane * kSPitch + e] = v;
+                    const uint32_t z = ((zv[e >> 2] >> (8 * (e & 3))) & 255u) + zbase;
+                    slds[lane * kSPitch + e] = Scale{w.scale_f16 ? f16_bits_to_float(bits) : bf16_bits_to_float(bits), z | z << 16};
                 }
             }
         };
-        int arow;                                                // the lane's row of the activation operand
-        if constexpr (kFix) {                                    // row 4 m + i: byte i of activation m
-            const int m = (n >> 2) < p.M ? n >> 2 : p.M - 1, i = (n & 3) < 3 ? n & 3 : 2;
-            arow = (3 * m + i) * xpitch;
-        } else {
-            const int am = act_of_row<MI>(n);
-            arow = (am < xrows ? am : xrows - 1) * xpitch;
-        }
-        const int xpair = 3 * p.M * xpitch + (h < p.M ? h : p.M - 1) * (xchunks * NG * 8);
+        // the lane's row of the activation operand, and where the factors of its rows of the product start
+        const int am = act_of_row<MI>(n);
+        const int arow = (am < xrows ? am : xrows - 1) * xpitch;
+        const int xfac = xrows * xpitch + 4 * MI * h;
         float y[RT][MI];
         // The products of one window.  Rolled: a workgroup runs this code a few times at most, and fetching an
         // instruction for the first time costs more than looping.
-        auto compute_fix = [&](int c0, const uint8_t* xwin) {
-            const int first = kResident ? c0 + wk * U : wk * U;  // the wave's first chunk in LDS
-            const uint8_t* ax = xwin + arow + first * kChunk;
-            const floatx2_t* xt = reinterpret_cast<const floatx2_t*>(xwin + xpair) + first * NG;
-            const floatx2_t* sp = reinterpret_cast<const floatx2_t*>(slds) + n * kSPitch;
-#pragma unroll 1
-            for (int u = 0; u < U; ++u) {
-                u32x4_t c[RT];
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    c[r] = *reinterpret_cast<const u32x4_t*>(clds + (16 * r + n) * kCodePitch + 16 * ((4 * u + h) ^ (n & 7)));
-                u32x4_t a[2];
-                if constexpr (NG == 4) {                         // four products of 32 k, eight bytes a lane each
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const u32x2_t t = *reinterpret_cast<const u32x2_t*>(ax + u * kChunk + 32 * j + 8 * h);
-                        a[j >> 1][2 * (j & 1)] = t[0];
-                        a[j >> 1][2 * (j & 1) + 1] = t[1];
-                    }
-                } else {                                         // two of 64 k, sixteen bytes
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        a[j] = *reinterpret_cast<const u32x4_t*>(ax + u * kChunk + chunk_k<NG>(2 * j, h));
-                }
-#pragma unroll
-                for (int r = 0; r < RT; ++r) order_chunk<NG>(c[r]);
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const floatx2_t x = xt[u * NG + g];
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        intx4_t acc = {0, 0, 0, 0};
-                        if constexpr (NG == 4) {
-                            acc = mfma_i8_32(a[g >> 1][2 * (g & 1)], a[g >> 1][2 * (g & 1) + 1], c[r][g], acc);
-                        } else {
-#pragma unroll
-                            for (int j = 2 * g / NG; j < 2 * (g + 1) / NG; ++j)
-                                acc = mfma_i8_64(a[j], c[r][2 * j], c[r][2 * j + 1], acc);
-                        }
-                        const floatx2_t s = sp[16 * r * kSPitch + u * NG + g];
-                        const float v = fmaf((float)acc[0], 65536.0f, fmaf((float)acc[1], 256.0f, (float)acc[2]));
-                        y[r][0] = fmaf(s[0] * x[0], fmaf(-s[1], x[1], v), y[r][0]);
-                    }
-                }
-            }
-        };
         auto compute = [&](int c0, const uint8_t* xwin) {
-            if constexpr (kFix) {
-                compute_fix(c0, xwin);
-                return;
-            }
-            const int cw = c0 + wk * U;
-            const uint8_t* ax = xwin + arow + 2 * (kResident ? cw * kChunk : wk * (U * kChunk));
+            const int first = kResident ? c0 + wk * U : wk * U;  // the wave's first chunk in LDS
+            const uint8_t* ax = xwin + arow + first * (2 * kChunk);
             const Scale* sp = slds + n * kSPitch;
 #pragma unroll 1
             for (int u = 0; u < U; ++u) {
@@ -791,35 +654,46 @@ struct RowTiles {
                     a[j] = *reinterpret_cast<const u32x4_t*>(ax + 2 * (u * kChunk + chunk_k<NG>(j, h)));
 #pragma unroll
                 for (int r = 0; r < RT; ++r) order_chunk<NG>(c[r]);
+                // A chunk's sums, scale group by scale group; its factor at the end.
+                float t[RT][MI];
+                Factors x;
+                if constexpr (kScaled) x = *reinterpret_cast<const Factors*>(xwin + xfac + (first + u) * (4 * kOpRows));
 #pragma unroll
                 for (int q = 0; q < NG; ++q) {
-                    floatx4_t acc[RT], xs = {0, 0, 0, 0};
+                    Scale s[RT];
+                    floatx4_t acc[RT];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) acc[r] = (floatx4_t){0, 0, 0, 0};
+                    for (int r = 0; r < RT; ++r) {
+                        s[r] = sp[16 * r * kSPitch + u * NG + q];
+                        acc[r] = (floatx4_t){0, 0, 0, 0};
+                    }
 #pragma unroll
                     for (int j = q * kMfmas; j < (q + 1) * kMfmas; ++j) {
-                        if constexpr (F == kLevels) {
 #pragma unroll
-                            for (int r = 0; r < RT; ++r)
+                        for (int r = 0; r < RT; ++r) {
+                            if constexpr (F == kLevels) {
                                 acc[r] = mfma<F>(a[j], decode8_table(c[r][j], 4 * (lane & 31)), acc[r]);
-                        } else {
-                            xs = mfma<F>(a[j], ones<F>(), xs);
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) acc[r] = mfma<F>(a[j], decode8<F>(c[r][j], magic), acc[r]);
+                            } else {
+                                const f16x2_t zero = __builtin_bit_cast(f16x2_t, s[r].zero), zero4 = zero + (f16x2_t){960, 960};
+                                acc[r] = mfma<F>(a[j], decode8(c[r][j], zero, zero4, magic), acc[r]);
+                            }
                         }
                     }
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        const Scale s = sp[16 * r * kSPitch + u * NG + q];
 #pragma unroll
                         for (int i = 0; i < MI; ++i) {
-                            if constexpr (F == kLevels) {
-                                y[r][i] = fmaf(s, acc[r][i], y[r][i]);
-                            } else {
-                                y[r][i] = fmaf(-s[1], xs[i], y[r][i]);
-                                y[r][i] = fmaf(s[0], acc[r][i], y[r][i]);
-                            }
+                            if constexpr (F == kLevels) y[r][i] = fmaf(s[r], acc[r][i], y[r][i]);
+                            else if constexpr (!kScaled) y[r][i] = fmaf(s[r].s, acc[r][i], y[r][i]);
+                            else t[r][i] = q == 0 ? s[r].s * acc[r][i] : fmaf(s[r].s, acc[r][i], t[r][i]);
                         }
+                    }
+                }
+                if constexpr (kScaled) {
+#pragma unroll
+                    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) y[r][i] = fmaf(x[i], t[r][i], y[r][i]);
                     }
                 }
             }

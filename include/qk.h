@@ -622,11 +622,11 @@ qk_status qk_int4_state_init(qk_int4_state* st, int64_t rows, int64_t cols, int3
 /*
  * qk_gemv_int4 — device.  Decode-time product with an int4 weight,
  *     y[m, :] = x[m, :] · W^T,  m < M.
- *   The codes, less a constant, enter the products exactly; sums, scales and zero points
- *   are fp32 or wider, and y is rounded once.  Up to M = 4 the activations are held in fixed
- *   point, each run of 128 inputs of a row to 2^-22 of its largest magnitude (2^-121 where that is
- *   below 2^-100); a bf16 value above 2^-13 of the largest loses nothing.  The same inputs give
- *   the same bits on every call.  An infinity or a NaN in x spoils its own row of y only.
+ *   q - z and the activations enter the products exactly (a bf16 value more than 2^31 below the
+ *   largest of its run of 128 inputs to 2^-38 of that one): an input whose weight is 0 adds nothing,
+ *   and takes nothing from its neighbours, however large it is.  Sums and scales are fp32, y is
+ *   rounded once.  The same inputs give the same bits on every call.  An infinity or a NaN in x
+ *   spoils its own row of y only.
  *   x:  device, [M, K] of dtype (QK_BF16 or QK_F16) row-major, 2-byte aligned (4-byte
  *       alignment and K % 8 == 0 load fastest).
  *   M:  1..16.
@@ -672,8 +672,8 @@ qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t H, int64_t I, 
  *   A logit of -inf masks an expert for a token (a NaN counts as -inf): it is never chosen,
  *   and a token with nothing left to choose gets y_t = 0.  The weights are the int4 values,
  *   or, for qk_moe_nf4, the bf16 copies of the 16 levels times the fp32 block scale, as in
- *   qk_gemv_nf4.  Sums are fp32 or wider, qk_moe_int4 may hold x in fixed point as qk_gemv_int4 does,
- *   h is kept to 16 bits of mantissa or to 2^-22 of the largest of 128, y is rounded once.  Only
+ *   qk_gemv_nf4.  Sums are fp32, x enters qk_moe_int4 as it enters qk_gemv_int4, h is kept to 24 bits of
+ *   mantissa (or 2^-38 of the largest of 128), in qk_moe_nf4 to 16, y is rounded once.  Only
  *   the weights of chosen experts are read.  The same inputs give the same bits on every
  *   call, and a token's result does not depend on the other tokens' logits or values.
  *   x: device, [T, H] of dtype, 2-byte aligned (qk_moe_int4: QK_BF16 or QK_F16; qk_moe_nf4:
