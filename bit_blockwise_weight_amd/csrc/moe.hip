@@ -11,8 +11,7 @@
 //                       Then items of 16 rows of gate and the same 16 of up of a listed expert (RowTiles,
 //                       w4_tile.h), dealt in equal shares; only the expert's own tokens are staged.  h is fp32.
 //   moe_down_kernel     items of rows of Wd of a listed expert times its tokens' h, which enters the matrix cores as two
-//                       values, hi + lo (w4_tile.h: int4 fp16, 24 bits of mantissa, levels bf16, 16 bits); w h Wd^T
-//                       goes to memory in fp32.
+//                       values, hi + lo (w4_tile.h: 24 bits of mantissa); w h Wd^T goes to memory in fp32.
 //   moe_combine_kernel  adds each token's parts in the order of its choices: no atomics.  Adding them in the down
 //                       kernel, by the wave that stores the last part, made that 82 us instead of 22 (16 tokens, top
 //                       8 of 64, 2048 x 1024): every wave then waits for its stores to reach memory.
@@ -21,6 +20,8 @@
 // 2048 x 1024 with top 8 one token takes 4.4, measured 18.5 (three launches, one round of loads each), sixteen
 // tokens 31, measured 54 in int4 and 66 in NF4, whose table reads from LDS take as long as the loads.
 #include <algorithm>
+#include <cmath>
+#include <cstring>
 
 #include "qk_device.h"
 #include "qk_internal.h"
@@ -462,6 +463,15 @@ hipError_t launch_down(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed,
     return launch_down_mi<F, NG, 2>(p, m.T, listed, s);
 }
 
+// The bf16 copy of a level, as qk_gemv_nf4 reads it.
+float bf16_copy(float v) {
+    uint32_t u;
+    std::memcpy(&u, &v, 4);
+    u = (u + 0x7FFFu + (u >> 16 & 1)) & 0xFFFF0000u;
+    std::memcpy(&v, &u, 4);
+    return v;
+}
+
 LevelsView levels_view(const MatArgs& w) {
     LevelsView v;
     v.codes = w.w.codes;
@@ -472,7 +482,12 @@ LevelsView levels_view(const MatArgs& w) {
     v.stride = w.K / 2;
     v.bshift = w.w.blocksize_log2;
     v.nested = w.w.nested;
-    for (int i = 0; i < 16; ++i) v.levels[i] = w.w.levels[i];
+    float most = 0.0f;
+    for (int i = 0; i < 16; ++i) most = std::max(most, std::fabs(bf16_copy(w.w.levels[i])));
+    int k = 0;
+    if (most > 0.0f && std::isfinite(most)) k = 14 - std::ilogb(most);
+    for (int i = 0; i < 16; ++i) v.levels[i] = std::ldexp(bf16_copy(w.w.levels[i]), k);
+    v.unit = std::ldexp(1.0f, -k);
     return v;
 }
 

@@ -16,7 +16,7 @@
 //   n = l % 16, rows m = 4 (l / 16) + r.  A scale of row n is then one value per lane, applied to
 //   the fp32 partial product of its group.
 //
-// int4 products are fp16 (16x16x32), two weights an instruction pair: (dword >> 4 i) & 0x000F000F leaves two codes in
+// The products are fp16 (16x16x32).  int4, two weights an instruction pair: (dword >> 4 i) & 0x000F000F leaves two codes in
 // the low bits of the two halves; OR-ing 0x6400, an exponent whose last mantissa bits they become, gives 1024 + q, and
 // 1024 + z taken off in fp16 leaves q - z, all of it exact.  The halves hold elements (1, 5), (0, 4), (3, 7), (2, 6)
 // of the dword's eight (the first of a pair sits in the high nibble), so the activations are stored in that order
@@ -28,7 +28,8 @@
 // fp32 (h of the expert layer) as a pair hi + lo, to 2^-24 of themselves, or 2^-38 of the largest.  Each chunk's sums are
 // multiplied by 2^(e - 14) in fp32.
 //
-// 16 levels: bf16 products, codes become bf16 levels by a table in LDS of all 256 bytes.
+// 16 levels: codes become levels by a table in LDS of all 256 bytes.  A level is its bf16 copy times the power of two that
+// brings the largest of the table to 2^14, as fp16: exact down to 2^-31 of the largest.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -43,7 +44,6 @@
 namespace qk {
 namespace w4 {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
@@ -128,14 +128,8 @@ __device__ __forceinline__ u32x4_t int4_order(u32x4_t v) {
     r[3] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100);   // (2, 6)
     return r;
 }
-template <int F>
 __device__ __forceinline__ floatx4_t mfma(u32x4_t a, u32x4_t b, floatx4_t c) {
-    if constexpr (F != kLevels)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
-                                                      0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
 // One int4 weight as the kernels see it.
@@ -161,10 +155,11 @@ struct LevelsView {
     int64_t stride;           // K / 2
     int32_t bshift;           // log2(block size)
     int32_t nested;
-    float levels[16];
+    float levels[16];         // their bf16 copies times 2^k, the largest magnitude in [2^14, 2^15)
+    float unit;               // 2^-k
 };
 
-// Table of the 256 code bytes as (bf16 level of the high nibble, bf16 level of the low nibble),
+// Table of the 256 code bytes as (fp16 level of the high nibble, fp16 level of the low nibble),
 // 32 copies so that each lane of the 32 that are served at a time reads a bank of its own: entry b of copy l at
 // b * 256 + 4 l of LDS itself (the kernels have no other LDS than the dynamic part, which starts at 0), so that a
 // v_perm makes the address.  The other half of the 256 bytes holds rows of codes (RowTiles).
@@ -173,7 +168,7 @@ constexpr int kTabBytes = 256 * 256;
 __device__ __forceinline__ void build_table(uint8_t* tab, const float* levels, int tid, int threads) {
     for (int i = tid; i < 256 * 8; i += threads) {
         const int b = i >> 3;
-        const uint32_t v = pack_bf16x2(levels[b >> 4], levels[b & 15]);
+        const uint32_t v = __builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)levels[b >> 4], (_Float16)levels[b & 15]});
         *reinterpret_cast<u32x4_t*>(tab + b * 256 + (i & 7) * 16) = (u32x4_t){v, v, v, v};
     }
 }
@@ -210,7 +205,7 @@ __device__ __forceinline__ u32x4_t decode8_table(uint32_t w, uint32_t lane4) {
 // loaded one window ahead and used for kSlots items; sums are made in the same order either way.
 // They are 16-bit values, for int4 in the order of its decoded codes, with a factor for each chunk and row behind them
 // where they are scaled.  With kSplit they are fp32 and become two rows, hi and lo (activation m: rows 2 m and
-// 2 m + 1): fp16 for int4, bf16 (16 bits of mantissa) for levels.
+// 2 m + 1).
 // Scales go to LDS as well, per row and group the pair (scale, -(1024 + zero point)) for int4, the scale alone for
 // levels; a wave writes and reads only its own, an odd number of entries apart.
 //
@@ -287,7 +282,7 @@ hipError_t allow_lds(size_t lds) {
 }
 
 // Whether activations are scaled chunk by chunk: fp16 ones are what the product takes.
-constexpr bool w4_scaled(Form f, bool split) { return f != kLevels && (split || f != kInt4F16); }
+constexpr bool w4_scaled(Form f, bool split) { return split || f != kInt4F16; }
 // bytes of LDS that the activations take: rows of 16-bit values (two an activation with kSplit), and the factors of the
 // chunks for the 4 mi rows of the operand
 inline size_t w4_x_bytes(Form f, int kw, int rows, int mi, bool split, int64_t K, bool resident) {
@@ -468,14 +463,6 @@ struct RowTiles {
                         hi[q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, c));
                     }
                 }
-            } else if constexpr (kSplit) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float a = as_float(xr[b][q >> 1][2 * (q & 1)]), c = as_float(xr[b][q >> 1][2 * (q & 1) + 1]);
-                    const uint32_t pk = pack_bf16x2(a, c);
-                    hi[q] = pk;
-                    lo[q] = pack_bf16x2(a - bf16_lo(pk), c - bf16_hi(pk));
-                }
             }
             const int at = in ? (kSplit ? 2 * m : m) * xpitch + 16 * u : xpitch - 16;
             *reinterpret_cast<u32x4_t*>(dst + at) = F == kLevels ? hi : int4_order(hi);
@@ -600,7 +587,7 @@ struct RowTiles {
                     } else {
                         v = as_float(o == 0 ? f.s[0] : o == 1 ? f.s[1] : o == 2 ? f.s[2] : f.s[3]);
                     }
-                    slds[lane * kSPitch + e] = e < left ? v : 0.0f;
+                    slds[lane * kSPitch + e] = e < left ? v * w.unit : 0.0f;
                 }
             } else {
                 const uint32_t sh = 8 * ((2 * at + sfirst) & 2);
@@ -672,20 +659,22 @@ struct RowTiles {
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
                             if constexpr (F == kLevels) {
-                                acc[r] = mfma<F>(a[j], decode8_table(c[r][j], 4 * (lane & 31)), acc[r]);
+                                acc[r] = mfma(a[j], decode8_table(c[r][j], 4 * (lane & 31)), acc[r]);
                             } else {
                                 const f16x2_t zero = __builtin_bit_cast(f16x2_t, s[r].zero), zero4 = zero + (f16x2_t){960, 960};
-                                acc[r] = mfma<F>(a[j], decode8(c[r][j], zero, zero4, magic), acc[r]);
+                                acc[r] = mfma(a[j], decode8(c[r][j], zero, zero4, magic), acc[r]);
                             }
                         }
                     }
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
+                        float sr;
+                        if constexpr (F == kLevels) sr = s[r];
+                        else sr = s[r].s;
 #pragma unroll
                         for (int i = 0; i < MI; ++i) {
-                            if constexpr (F == kLevels) y[r][i] = fmaf(s[r], acc[r][i], y[r][i]);
-                            else if constexpr (!kScaled) y[r][i] = fmaf(s[r].s, acc[r][i], y[r][i]);
-                            else t[r][i] = q == 0 ? s[r].s * acc[r][i] : fmaf(s[r].s, acc[r][i], t[r][i]);
+                            if constexpr (!kScaled) y[r][i] = fmaf(sr, acc[r][i], y[r][i]);
+                            else t[r][i] = q == 0 ? sr * acc[r][i] : fmaf(sr, acc[r][i], t[r][i]);
                         }
                     }
                 }

@@ -672,9 +672,10 @@ qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t H, int64_t I, 
  *   A logit of -inf masks an expert for a token (a NaN counts as -inf): it is never chosen,
  *   and a token with nothing left to choose gets y_t = 0.  The weights are the int4 values,
  *   or, for qk_moe_nf4, the bf16 copies of the 16 levels times the fp32 block scale, as in
- *   qk_gemv_nf4.  Sums are fp32, x enters qk_moe_int4 as it enters qk_gemv_int4, h is kept to 24 bits of
- *   mantissa (or 2^-38 of the largest of 128), in qk_moe_nf4 to 16, y is rounded once.  Only
- *   the weights of chosen experts are read.  The same inputs give the same bits on every
+ *   qk_gemv_nf4 (a level more than 2^31 below the table's largest to 2^-38 of that one).  Sums are
+ *   fp32, x enters as it enters qk_gemv_int4, h is kept to 24 bits of mantissa (or 2^-38 of the
+ *   largest of 128), y is rounded once.  Only the weights of chosen experts are read.  The same
+ *   inputs give the same bits on every
  *   call, and a token's result does not depend on the other tokens' logits or values.
  *   x: device, [T, H] of dtype, 2-byte aligned (qk_moe_int4: QK_BF16 or QK_F16; qk_moe_nf4:
  *     bf16).   T: 1..16.

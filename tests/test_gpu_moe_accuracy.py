@@ -13,6 +13,7 @@ import torch
 
 import bit_blockwise_weight_amd as qk
 from tests.gpu_common import require_gpu, say
+from tests.gpu_int4 import moe_f64
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +84,61 @@ def test_int4_keeps_the_inner_values(H, I, E, large):
                 y = qk.qk_moe_int4(x, _logits(T, E), 1, w1.state, w2.state)
                 assert torch.equal(y.cpu().long(), (33 * sums).expand(T, H)), f"T={T} group={group}"
 
+
+@pytest.mark.parametrize("large", [False, True])
+@pytest.mark.parametrize("E", [2, 16])
+@pytest.mark.parametrize("H,I", [(256, 128), (256, 2048)])
+def test_levels_keep_the_inner_values(H, I, E, large):
+    """The same with a level table of its own, -8..7 (with +7 and 2^-3 in the place of two that are not used here)."""
+    gen = torch.Generator().manual_seed(2)
+    gu, down, scale, sums = _weights(gen, H, I, large)
+    (q1, s1), (q2, s2) = _stack(gu, scale, E), _stack(down, None, E)
+    levels = torch.arange(-8.0, 8.0)
+    levels[0], levels[1] = 2.0 ** -12, 1.0e4
+    keep = []
+
+    def state(q, s, block):
+        codes = ((q[:, 0::2] << 4) | q[:, 1::2]).view(-1)
+        absmax = s.expand(-1, q.shape[1] // block).reshape(-1).contiguous().float()
+        keep.append((codes, absmax))
+        return qk.qk_state_init(qk.CUSTOM, levels, q.shape[0], q.shape[1], block, codes, absmax)
+
+    for block in (64, 128):
+        up, dn = state(q1, s1, block), state(q2, s2, block)
+        for T in (1, 2, 3, 4, 8, 16):
+            say(f"case: moe_nf4 own levels, inner values T={T} E={E} H={H} I={I} block={block} large={large}")
+            x = _tokens(gen, T, H, torch.bfloat16)
+            y = qk.qk_moe_nf4(x, _logits(T, E), 1, up, dn)
+            assert torch.equal(y.cpu().long(), (33 * sums).expand(T, H)), f"T={T} block={block}"
+
+
+def test_levels_of_very_different_size():
+    """A table whose levels span 2^28, rows that read the small ones alone: each counts as its bf16 copy.  Tolerance: the
+    output's rounding, and fp32 sums over at most 4 matrix instructions of 32 products a chunk, a scale, a factor, 4 chunks
+    and 8 waves for each product (2^-23 a step, of the terms that it has), of which h itself is 2^-24."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    H, I, block, T = 256, 128, 64, 3
+    levels = torch.tensor([1.37 * 2.0 ** (-2 * i) * (-1) ** i for i in range(15)] + [0.0])
+    lv = levels.bfloat16().double().cuda()
+
+    def weight(rows, cols):
+        q = torch.randint(0, 4, (rows, cols), generator=gen, device="cuda", dtype=torch.uint8)
+        q[1::4] += 10                                        # 2^-20 to 2^-26 of the largest, and no other
+        q[2::4] = torch.randint(0, 16, (len(q[2::4]), cols), generator=gen, device="cuda", dtype=torch.uint8)
+        q[1::4, ::9] = 15
+        absmax = torch.rand(rows * cols // block, generator=gen, device="cuda") + 0.5
+        codes = ((q[:, 0::2] << 4) | q[:, 1::2]).contiguous().view(-1)
+        w = lv[q.long()] * absmax.double().view(rows, -1).repeat_interleave(block, 1)
+        return w, qk.qk_state_init(qk.CUSTOM, levels, rows, cols, block, codes, absmax)
+
+    up, up_state = weight(2 * I, H)
+    down, down_state = weight(H, I)
+    x = torch.randn((T, H), generator=gen, device="cuda").to(torch.bfloat16)
+    x[:, ::5] *= 8
+    y = qk.qk_moe_nf4(x, torch.zeros((T, 1), device="cuda"), 1, up_state, down_state)
+    say("case: moe_nf4 levels of very different size")
+    ref, bound = moe_f64(x, [[(0, 1.0)]] * T, lambda e: (up[:I], up[I:]), lambda e: down)
+    tol = torch.finfo(x.dtype).eps / 2 * ref.abs() + 2.0 ** -23 * (128 + 4 + 8 + 2) * bound + 2.0 ** -126
+    assert float(((y.double() - ref).abs() / tol).max()) <= 1.0
+    small = slice(1, H, 4)
+    assert float((y.double() - ref)[:, small].norm() / ref[:, small].norm()) <= torch.finfo(x.dtype).eps / 2
