@@ -809,6 +809,11 @@ def qk_qlora_backward(dY: torch.Tensor, state: QuantState, X=None, A=None, B=Non
     return dX, dA, dB
 
 
+def _by_row(t: torch.Tensor, rows: int, ngroups: int) -> bool:
+    """Whether t holds a value per row and group, row after row: [..., ngroups] or flat."""
+    return t.numel() == rows * ngroups and (ngroups == 1 or t.dim() == 1 or t.shape[-1] == ngroups)
+
+
 def qk_int4_state_init(rows: int, cols: int, group: int, codes: torch.Tensor, scales: torch.Tensor,
                        zeros=None) -> Int4State:
     """Descriptor of an int4 weight [rows, cols] with one scale (fp16 or bf16) and one zero point
@@ -818,9 +823,9 @@ def qk_int4_state_init(rows: int, cols: int, group: int, codes: torch.Tensor, sc
     ngroups = -(-cols // group) if group > 0 else 1
     if codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[0] != rows:
         raise ValueError(f"codes must be uint8 [{rows}, stride], got {codes.dtype} {tuple(codes.shape)}")
-    if scales.dtype not in (torch.float16, torch.bfloat16) or scales.numel() != rows * ngroups:
+    if scales.dtype not in (torch.float16, torch.bfloat16) or not _by_row(scales, rows, ngroups):
         raise ValueError(f"scales must be fp16 or bf16 [{rows}, {ngroups}], got {scales.dtype} {tuple(scales.shape)}")
-    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.numel() != rows * ngroups):
+    if zeros is not None and (zeros.dtype != torch.uint8 or not _by_row(zeros, rows, ngroups)):
         raise ValueError(f"zeros must be uint8 [{rows}, {ngroups}], got {zeros.dtype} {tuple(zeros.shape)}")
     dev = codes.device
     st = Int4State()
