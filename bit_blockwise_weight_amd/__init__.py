@@ -971,13 +971,28 @@ def qk_moe_nf4(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate_up: Quant
     return _moe(lib().qk_moe_nf4, (), x, logits, top_k, gate_up, down, renormalize, y, workspace, dev)
 
 
+def _check_range(t: torch.Tensor, most: int, name: str):
+    """Whole numbers 0..most (a NaN or an infinity is none)."""
+    if t.dtype in (torch.bool, torch.uint16, torch.uint32, torch.uint64):
+        t = t.to(torch.int64)
+    if t.numel() == 0:
+        return
+    lo, hi = torch.aminmax(t)
+    if not (0 <= lo.item() and hi.item() <= most) or (t.dtype.is_floating_point and bool((t != t.round()).any())):
+        raise ValueError(f"{name} must be whole numbers 0..{most}, got {lo.item()} to {hi.item()}")
+
+
 class Int4Weight:
     """A weight W[N, K] = scales * (codes - zeros) in int4 groups, packed on the device from unpacked
-    integer codes [N, K] (0..15), scales [N, G] (fp16 or bf16) and zero points [N, G] (None: 8)."""
+    integer codes [N, K] (0..15), scales [N, G] (fp16 or bf16) and zero points [N, G] (whole numbers 0..255; None: 8).
+    Codes and zero points are looked over, which waits for the device."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, zeros=None, group: int = 128):
-        if codes.dim() != 2 or codes.dtype.is_floating_point:
+        if codes.dim() != 2 or codes.dtype.is_floating_point or codes.dtype.is_complex:
             raise ValueError(f"codes must be integers [N, K], got {codes.dtype} {tuple(codes.shape)}")
+        _check_range(codes, 15, "codes")
+        if zeros is not None:
+            _check_range(zeros, 255, "zeros")
         rows, cols = codes.shape
         stride = (-(-cols // 2) + 15) // 16 * 16
         q = torch.zeros((rows, 2 * stride), dtype=torch.uint8, device=codes.device)

@@ -35,3 +35,30 @@ def test_one_group_per_row_in_any_shape():
     for shape in ((8, 1), (8,), (1, 8)):
         with pytest.raises(ValueError, match="HIP device"):
             qk.qk_int4_state_init(8, 64, 0, _codes(8, 64), torch.ones(shape, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.uint8, torch.int32, torch.int64])
+def test_codes_outside_four_bits_are_refused(dtype):
+    scales = torch.ones((2, 1), dtype=torch.float16)
+    for bad in ((16, -3, -1, 255) if dtype is not torch.int8 else (16, -3, -1, 127)):
+        if dtype is torch.uint8 and bad < 0:
+            continue
+        codes = torch.full((2, 32), 7, dtype=dtype)
+        codes[1, 5] = bad
+        with pytest.raises(ValueError, match="0..15"):
+            qk.Int4Weight(codes, scales, None, 32)
+    with pytest.raises(ValueError, match="HIP device"):
+        qk.Int4Weight(torch.arange(32).remainder(16).expand(2, 32).to(dtype), scales, None, 32)
+
+
+@pytest.mark.parametrize("dtype,bad", [(torch.float32, (7.6, -1.0, 256.0, float("nan"), float("inf"))),
+                                       (torch.float16, (8.5, -2.0, 300.0)), (torch.int32, (-1, 256)), (torch.int8, (-1,))])
+def test_zero_points_that_are_no_bytes_are_refused(dtype, bad):
+    codes, scales = torch.zeros((2, 64), dtype=torch.uint8), torch.ones((2, 2), dtype=torch.float16)
+    for v in bad:
+        zeros = torch.full((2, 2), 8, dtype=dtype)
+        zeros[0, 1] = v
+        with pytest.raises(ValueError, match="0..255"):
+            qk.Int4Weight(codes, scales, zeros, 32)
+    with pytest.raises(ValueError, match="HIP device"):
+        qk.Int4Weight(codes, scales, torch.full((2, 2), 8, dtype=dtype), 32)
