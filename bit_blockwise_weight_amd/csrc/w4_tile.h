@@ -562,6 +562,12 @@ struct RowTiles {
             }
         };
 
+        // The lanes of a wave exchange codes and scales through LDS.  Nothing waits (a wave's LDS accesses keep their
+        // order), but the compiler must not move one lane's reads across another's writes.
+        auto exchanged = [] {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
         // What was fetched goes to the wave's own LDS: codes from lines to fragments (16-byte unit u of row r
         // sits in unit u ^ (r % 8) of its row), scales converted.
         auto land = [&](const Fetched& f) {
@@ -734,7 +740,9 @@ struct RowTiles {
             __syncthreads();
             int item = item0, c0 = 0, slot = 0;
             while (true) {
+                exchanged();
                 land(f);
+                exchanged();
                 const bool last = c0 + wchunks >= nchunk;        // last window of the item
                 const bool end = last && item + 1 >= item1;
                 const int nc = last ? 0 : c0 + wchunks;
@@ -769,7 +777,9 @@ struct RowTiles {
                     __syncthreads();
 #pragma unroll 1
                     for (int slot = 0; slot < items; ++slot) {
+                        exchanged();
                         land(f);
+                        exchanged();
                         const bool turn = slot + 1 == items;     // on to the next window, or to the next items
                         const bool end = turn && last && first + items >= item1;
                         j = turn && !last ? j0 : j + p.step;
