@@ -428,7 +428,7 @@ hipError_t launch_up_mi(const ExpertArgs<F>& p, RouteArgs ra, Routes* keep, int3
 template <int F, int NG>
 hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int32_t* listed, hipStream_t s) {
     const RouteArgs ra{m.logits, m.logits_dtype, m.T, m.E, m.top_k, m.renorm, 0};
-    if (m.T <= 4 || m.T * m.top_k < (F == kLevels ? 3 : 4) * m.E) return launch_up_mi<F, NG, 1>(p, ra, keep, listed, s);
+    if (m.T <= 4 || m.T * m.top_k < 3 * m.E) return launch_up_mi<F, NG, 1>(p, ra, keep, listed, s);
     return launch_up_mi<F, NG, 2>(p, ra, keep, listed, s);
 }
 
@@ -448,8 +448,9 @@ hipError_t launch_down_one(ExpertArgs<F> p, int tokens, int32_t listed, hipStrea
 template <int F, int NG, int MI>
 hipError_t launch_down_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hipStream_t s) {
     const int tokens = std::min(T, kTokens<MI, true>);
-    if (!fits<F, NG, 2, MI>(tokens, true, p.I)) return launch_down_one<F, NG, 2, MI, false>(p, tokens, listed, s);
-    return launch_down_one<F, NG, 2, MI, true>(p, tokens, listed, s);
+    constexpr int RT = MI == 4 ? 1 : 2;                  // (eight tokens beside two tiles do not fit the registers)
+    if (!fits<F, NG, RT, MI>(tokens, true, p.I)) return launch_down_one<F, NG, RT, MI, false>(p, tokens, listed, s);
+    return launch_down_one<F, NG, RT, MI, true>(p, tokens, listed, s);
 }
 
 // Tokens of a pass of the down product, two or four, in int4 eight where experts are crowded.  Levels: equal up to two
@@ -459,7 +460,7 @@ template <int F, int NG>
 hipError_t launch_down(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, hipStream_t s) {
     if (m.T <= 2) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);
     if constexpr (F != kLevels)
-        if (m.T > 4 && m.T * m.top_k >= 4 * m.E) return launch_down_mi<F, NG, 4>(p, m.T, listed, s);
+        if (m.T > 4 && m.T * m.top_k >= 3 * m.E) return launch_down_mi<F, NG, 4>(p, m.T, listed, s);
     return launch_down_mi<F, NG, 2>(p, m.T, listed, s);
 }
 

@@ -119,7 +119,9 @@ __device__ __forceinline__ u32x4_t decode8(uint32_t w, f16x2_t zero, f16x2_t zer
     return f;
 }
 
-// Activations of eight consecutive k in the order decode8 gives the weights.
+// Activations of eight consecutive k in the order decode8 gives the weights: dword q holds int4_first(q) and the fourth
+// after it.
+__device__ __forceinline__ constexpr int int4_first(int q) { return q ^ 1; }
 __device__ __forceinline__ u32x4_t int4_order(u32x4_t v) {
     u32x4_t r;
     r[0] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302);   // (1, 5)
@@ -452,25 +454,42 @@ struct RowTiles {
                     f[0] = as_float((e - 14u) << 23);
                     if constexpr (kSplit) f[1] = f[0];
                 }
+                // in the order in which they are stored
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float a = v[2 * q] * up, c = v[2 * q + 1] * up;
-                    if constexpr (kSplit) {
-                        const _Float16 ah = (_Float16)a, ch = (_Float16)c;
-                        hi[q] = __builtin_bit_cast(uint32_t, (f16x2_t){ah, ch});
-                        lo[q] = __builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)(a - (float)ah), (_Float16)(c - (float)ch)});
-                    } else {
-                        hi[q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, c));
-                    }
+                    const int i0 = F == kLevels ? 2 * q : int4_first(q), i1 = F == kLevels ? 2 * q + 1 : int4_first(q) + 4;
+                    const float a = v[i0] * up, c = v[i1] * up;
+                    const f16x2_t near = {(_Float16)a, (_Float16)c};
+                    hi[q] = __builtin_bit_cast(uint32_t, near);
+                    if constexpr (kSplit)
+                        lo[q] = __builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)(a - (float)near[0]), (_Float16)(c - (float)near[1])});
                 }
+            } else {
+                hi = int4_order(hi);
             }
             const int at = in ? (kSplit ? 2 * m : m) * xpitch + 16 * u : xpitch - 16;
-            *reinterpret_cast<u32x4_t*>(dst + at) = F == kLevels ? hi : int4_order(hi);
-            if constexpr (kSplit) *reinterpret_cast<u32x4_t*>(dst + (in ? at + xpitch : at)) = F == kLevels ? lo : int4_order(lo);
+            *reinterpret_cast<u32x4_t*>(dst + at) = hi;
+            if constexpr (kSplit) *reinterpret_cast<u32x4_t*>(dst + (in ? at + xpitch : at)) = lo;
         };
         auto x_store = [&](uint8_t* dst, int base, int k0) {
+            // Two tiles beside the units in flight of more than one product register leave few registers: there the units
+            // come one after the other, each moved to the front.
+            if constexpr (!kResident && RT == 2 && MI > 1) {
+                const int batch = base + kXUnits * kThreads;
+#pragma unroll 1
+                for (; base < batch; base += kThreads) {
+                    x_store_unit(dst, 0, base + tid, k0);
 #pragma unroll
-            for (int b = 0; b < kXUnits; ++b) x_store_unit(dst, b, base + b * kThreads + tid, k0);
+                    for (int b = 0; b + 1 < kXUnits; ++b) {
+                        xr[b][0] = xr[b + 1][0];
+                        if constexpr (kSplit) xr[b][1] = xr[b + 1][1];
+                        else xe[b] = xe[b + 1];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < kXUnits; ++b) x_store_unit(dst, b, base + b * kThreads + tid, k0);
+            }
         };
 
         // Codes and scales of the wave's line in the window that starts at chunk c0 of the item whose tile 0
