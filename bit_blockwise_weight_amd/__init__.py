@@ -925,7 +925,7 @@ _moe_bytes = functools.lru_cache(maxsize=256)(qk_moe_workspace_size)
 
 
 def _moe(fn, dtype_arg, x, logits, top_k, gate_up, down, renormalize, y, workspace, dev):
-    hidden, inner = gate_up.cols, down.cols
+    hidden, inner, top_k = gate_up.cols, down.cols, int(top_k)
     if logits.dtype not in _DTYPE_CODE:
         raise ValueError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
     if x.dim() == 0 or x.shape[-1] != hidden:
@@ -941,7 +941,7 @@ def _moe(fn, dtype_arg, x, logits, top_k, gate_up, down, renormalize, y, workspa
         _check_out(y, (T, hidden), x.dtype, "y")
     if workspace is None:
         workspace = torch.empty(_moe_bytes(T, top_k, hidden, inner), dtype=torch.uint8, device=dev)
-    _call(dev, fn, xp, *dtype_arg, T, lp, _DTYPE_CODE[logits.dtype], E, int(top_k), 1 if renormalize else 0, gate_up,
+    _call(dev, fn, xp, *dtype_arg, T, lp, _DTYPE_CODE[logits.dtype], E, top_k, 1 if renormalize else 0, gate_up,
           down, _ready(y, dev, "y"), _ready(workspace, dev, "workspace"), workspace.nbytes)
     return y
 
