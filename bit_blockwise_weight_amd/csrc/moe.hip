@@ -256,7 +256,7 @@ int64_t workgroups(int64_t items, size_t lds) {
     return std::min<int64_t>(items, (lds > kLdsBytes / 2 ? 1 : kPerCu<F>) * device_cu_count());
 }
 // LDS of the activations; those of a whole row stay there where all of them fit.
-template <int F, int NG, int MI>
+template <int F, int MI>
 size_t x_lds(int tokens, bool split, int64_t K, bool resident) {
     constexpr int kw = 1 << w4_most_kwl((Form)F, MI);
     return w4_x_bytes((Form)F, kw, split ? 2 * tokens : tokens, MI, split, K, resident);
@@ -264,7 +264,7 @@ size_t x_lds(int tokens, bool split, int64_t K, bool resident) {
 template <int F, int NG, int RT, int MI>
 bool fits(int tokens, bool split, int64_t K) {
     return (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + w4_fixed_bytes((Form)F, NG, RT, MI, true) +
-               x_lds<F, NG, MI>(tokens, split, K, true) <= kLdsBytes;
+               x_lds<F, MI>(tokens, split, K, true) <= kLdsBytes;
 }
 // Tokens that a pass over an expert's rows takes; the down product needs two operand rows for one.
 template <int MI, bool kSplit>
@@ -400,7 +400,7 @@ hipError_t launch_up_one(ExpertArgs<F> p, const RouteArgs& ra, Routes* keep, int
     typedef RowTiles<F, NG, 2, MI, kResident, false> Tiles;
     p.kwl = w4_kwl((Form)F, p.H, (int64_t)p.Ipad * listed, 16, kResident ? 3 : w4_most_kwl((Form)F, MI));
     const size_t lds = (F == kLevels ? kTabBytes : 0) + sizeof(Routes) + Tiles::kFixedBytes +
-                       x_lds<F, NG, MI>(tokens, false, p.H, kResident);
+                       x_lds<F, MI>(tokens, false, p.H, kResident);
     const hipError_t e = allow_lds<&moe_up_kernel<F, NG, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
     const int step = (16 * Tiles::W) >> p.kwl;
@@ -436,7 +436,7 @@ template <int F, int NG, int RT, int MI, bool kResident>
 hipError_t launch_down_one(ExpertArgs<F> p, int tokens, int32_t listed, hipStream_t s) {
     typedef RowTiles<F, NG, RT, MI, kResident, true> Tiles;
     p.kwl = w4_kwl((Form)F, p.I, (int64_t)p.H * listed, 16 * RT, kResident ? 3 : w4_most_kwl((Form)F, MI));
-    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + x_lds<F, NG, MI>(tokens, true, p.I, kResident);
+    const size_t lds = (F == kLevels ? kTabBytes : 0) + Tiles::kFixedBytes + x_lds<F, MI>(tokens, true, p.I, kResident);
     const hipError_t e = allow_lds<&moe_down_kernel<F, NG, RT, MI, kResident>>(lds);
     if (e != hipSuccess) return e;
     const int64_t step = (16 * RT * Tiles::W) >> p.kwl, items = (p.H + step - 1) / step * listed;

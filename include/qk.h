@@ -606,7 +606,7 @@ typedef struct qk_int4_state {
                                 the high nibble of its byte t, code 2t+1 in the low nibble; what
                                 lies past the row's last code is ignored */
     const void* scales;      /* device, [rows, G] of scale_dtype, G = ceil(cols / group) (1 for
-                                group 0), 2-byte aligned; finite */
+                                group 0), 2-byte aligned; finite and under 2^96 in magnitude */
     const uint8_t* zeros;    /* device, [rows, G], values 0..255, or NULL: 8 for every group */
 } qk_int4_state;
 
@@ -683,7 +683,8 @@ qk_status qk_moe_workspace_size(int32_t T, int32_t top_k, int64_t H, int64_t I, 
  *     +inf is not supported (its tokens get NaN).   E: 1..256.   top_k: 1..min(E, 16).
  *   gate_up: host pointer to the descriptor of the stacked [E * 2 * I, H] weights: expert e's
  *     gate in rows [2 e I, 2 e I + I), its up projection in the next I rows.
- *   down: descriptor of the stacked [E * H, I] weights: expert e in rows [e H, e H + H).
+ *   down: descriptor of the stacked [E * H, I] weights: expert e in rows [e H, e H + H).  (qk_moe_nf4: a
+ *     block's scale times the largest level has to be under 2^96 in magnitude.)
  *   H and I follow from the descriptors (each at most 2^20).  One expert's gate, up or down matrix (qk_moe_nf4:
  *     gate and up together) must stay under about 2 GiB of codes (else QK_ERR_UNSUPPORTED); the stack may be as
  *     large as memory.  qk_moe_nf4 needs H and I to be multiples of 64 (else QK_ERR_UNSUPPORTED) and 16-byte
