@@ -7,9 +7,9 @@
 // codes of the next rows being loaded while some are multiplied.
 //
 // Bound by the bytes of the codes, at 6 TB/s, where few rows of activations meet large weights: the seven weights of a
-// layer (4096 wide, 11008 inside, groups of 128, 106 MB) at M = 1 22.1 us, 4.8 TB/s; 28672 x 8192, M = 4, 28.1 us.  In
-// groups of 32 at M = 16 the layer takes 50 us, half of it instructions: scales and zero points, a product and a
-// sum of x per 32 k.  1024 x 1024 at M = 1 takes 4.4 us, a launch and two rounds of loads.
+// layer (4096 wide, 11008 inside, groups of 128, 106 MB) at M = 1 23.9 us, 4.4 TB/s; 28672 x 8192, M = 4, 27.6 us.  In
+// groups of 32 at M = 16 the layer takes 53 us, more than half of it instructions: decoding, scales, and every
+// workgroup's turning of x into fp16.  1024 x 1024 at M = 1: a kernel of 4.2 us, a launch and two rounds of loads.
 #include <algorithm>
 
 #include "qk_device.h"
@@ -87,7 +87,8 @@ __global__ __launch_bounds__(kThreads, 4) void int4_gemv_kernel(Int4Group<kTasks
     });
 }
 
-// Registers of a product that carry activations: the least that hold M rows.
+// Registers of a product that carry activations: the least that hold M rows (weights from memory: the layer at M = 8 38 us,
+// in the form of sixteen 46).
 constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
 size_t lds_bytes(int M, bool f16, int ng, int rt, int64_t K, bool resident) {
@@ -96,7 +97,8 @@ size_t lds_bytes(int M, bool f16, int ng, int rt, int64_t K, bool resident) {
            w4_x_bytes(f16 ? kInt4F16 : kInt4Bf16, kw, M, mi, false, K, resident);
 }
 // The activations of a whole row stay in LDS where they fit; above four rows where they leave room for a second
-// workgroup on the CU.
+// workgroup on the CU (weights from memory, 28672 x 8192 at M = 8: 38.2 us streaming with two, 38.9 resident with one; at
+// M = 3 and 4, resident at any size is faster, 29.2 us against 30.8 for the layer at M = 3).
 bool resident_for(int M, bool f16, int ng, int rt, int64_t K) {
     return lds_bytes(M, f16, ng, rt, K, true) <= (M > 4 ? kLdsBytes / 2 : kLdsBytes);
 }
@@ -203,9 +205,9 @@ hipError_t launch_int4_gemv_group(const Int4Item* items, int32_t count, int32_t 
         }
         const int per_cu_most = 2;
         // Tiles of 16 rows per item and row group: two, which bring more codes on their way at a time, where every
-        // workgroup has an item of two (M = 1: the layer 21.9 us, with one 24.2), one where not (4096 x 4096 5.3 us, with
-        // two 5.8) and above four rows, whose sums and scales leave no room for two workgroups on a CU (M = 16,
-        // groups of 32: the layer 50 us, with two 59; M = 8, groups of 128, 34 and 47).
+        // workgroup has an item of two (weights from memory, M = 1: the layer 26.4 us, with one 28.8), one where not
+        // (4096 x 4096 5.4 us, with two 6.2) and above four rows, whose sums and scales leave no room for two workgroups on
+        // a CU (M = 16, groups of 32: the layer 56 us, with two 61; M = 8, groups of 128, 38 and 43).
         l.rt = mi_for(M) == 1 && pairs > (int64_t)per_cu_most * device_cu_count() ? 2 : 1;
         // (an output's bits do not depend on whether the activations stay)
         l.resident = resident_for(M, f16, l.ng, l.rt, kmax);

@@ -16,9 +16,9 @@
 //                       kernel, by the wave that stores the last part, made that 82 us instead of 22 (16 tokens, top
 //                       8 of 64, 2048 x 1024): every wave then waits for its stores to reach memory.
 // Every weight of a listed expert is read once per listing; that is the bound.  At 6 TB/s, which a read of large
-// weights reaches, one token's top 2 of 8 experts of 4096 x 11008 take 24 us, measured 38; of 64 experts of
-// 2048 x 1024 with top 8 one token takes 4.4, measured 18.5 (three launches, one round of loads each), sixteen
-// tokens 31, measured 54 in int4 and 66 in NF4, whose table reads from LDS take as long as the loads.
+// weights reaches, one token's top 2 of 8 experts of 4096 x 11008 take 24 us, measured 40; of 64 experts of
+// 2048 x 1024 with top 8 one token takes 4.4, measured 19.3 (three launches, one round of loads each), sixteen
+// tokens 31, measured 59 in int4 and 66 in NF4, whose table reads from LDS take as long as the loads.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -419,11 +419,11 @@ hipError_t launch_up_mi(const ExpertArgs<F>& p, RouteArgs ra, Routes* keep, int3
     return launch_up_one<F, NG, MI, false>(p, ra, keep, tokens, *listed, s);
 }
 
-// Tokens of a listing, four or eight, by how many an expert has on average.  Eight read the weights of crowded experts
-// less often; four take the integer product in int4, and less LDS.  16 tokens, four / eight: top 2 of 8 experts,
-// H = I = 4096 (4 an expert), int4 74 / 65 us, levels 86 / 78; top 8 of 64, 2048 x 1024 (2 an expert), int4 52 / 69,
-// levels 65 / 80; 12 tokens, top 2 of 8 (3 an expert), int4 61 / 63, levels 79 / 77.  Sixteen gained 2 % where every
-// expert has 16 and lost 10 % at 6.
+// Tokens of a listing, four or eight, by how many an expert has on average: eight read the weights of crowded experts
+// less often, four take less LDS and half the registers.  Weights from memory, four / eight (the down product likewise):
+// 16 tokens, top 2 of 8 experts, H = I = 4096 (4 an expert), int4 95 / 66 us, levels 110 / 84; 12 tokens (3 an expert),
+// int4 79 / 64, levels 100 / 82; top 8 of 64, 2048 x 1024 (2 an expert), int4 63 / 75, levels 69 / 85.  Sixteen gained 2 %
+// where every expert has 16 and lost 10 % at 6.
 // listed: set to the most listings that there can be
 template <int F, int NG>
 hipError_t launch_up(const ExpertArgs<F>& p, const MoeItem& m, Routes* keep, int32_t* listed, hipStream_t s) {
@@ -453,9 +453,9 @@ hipError_t launch_down_mi(const ExpertArgs<F>& p, int32_t T, int32_t listed, hip
     return launch_down_one<F, NG, RT, MI, true>(p, tokens, listed, s);
 }
 
-// Tokens of a pass of the down product, two or four, in int4 eight where experts are crowded.  Levels: equal up to two
-// tokens, with four at a time top 8 of 64 experts take 40 us for 4 tokens instead of 48, and 65 for 16 instead of 79; one
-// expert of two tokens, 4096 x 4096, 44 us instead of 38.
+// Tokens of a pass of the down product, two or four, in int4 eight where experts are crowded (see above).  Two at a time,
+// weights from memory: four tokens of top 8 of 64 experts int4 35.9 us instead of 35.0, levels 43.4 instead of 42.2; four
+// at a time, two tokens of one expert, 4096 x 4096: int4 equal, levels 37 us instead of 29.
 template <int F, int NG>
 hipError_t launch_down(const ExpertArgs<F>& p, const MoeItem& m, int32_t listed, hipStream_t s) {
     if (m.T <= 2) return launch_down_mi<F, NG, 1>(p, m.T, listed, s);

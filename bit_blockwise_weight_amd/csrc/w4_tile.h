@@ -20,7 +20,7 @@
 // the low bits of the two halves; OR-ing 0x6400, an exponent whose last mantissa bits they become, gives 1024 + q, and
 // 1024 + z taken off in fp16 leaves q - z, all of it exact.  The halves hold elements (1, 5), (0, 4), (3, 7), (2, 6)
 // of the dword's eight (the first of a pair sits in the high nibble), so the activations are stored in that order
-// too.  The zero point goes before the product, not after the sum: a sum of x (128 + q) less (128 + z) times the sum of x, the
+// too.  The zero point goes before the product, not after the sum: a sum of x (128 + q) less (128 + z) times that of x, the
 // bf16 way, loses the neighbours of a large x whose q - z is 0.
 //
 // Activations other than fp16 ones are scaled by a power of two for each run of 128 (a chunk), 2^(14 - e) with e the
@@ -249,11 +249,11 @@ constexpr int kLineK = 256;               // k of a 128-byte line of codes
 
 // bytes of LDS beside the activations: scales, codes, partial sums of a few items and their counters
 // With a table one workgroup of 16 waves fills a CU (two of 8 have no room for two tables): 16 tokens, top 8 of 64
-// experts of 2048 x 1024, 68 us against 98 with 8 waves; one token 24 against 23.
+// experts of 2048 x 1024, 66 us against 98 with 8 waves; one token 24 against 23.
 constexpr int w4_waves(Form f) { return f == kLevels ? 16 : 8; }
 constexpr int w4_put_bytes(Form f, int RT, int MI) { return w4_waves(f) * RT * 64 * MI * 4; }
 // items that a window of activations serves, or (resident) whose sums wait for their last wave without a barrier.  One
-// tile a wave above four activations: four, 34 us for the seven weights of a layer at M = 8, with two 39; for more
+// tile a wave above four activations: four, 38 us for the seven weights of a layer at M = 8, with two 45; for more
 // than eight there is room for two.
 constexpr int w4_slots(Form f, int RT, int MI, bool resident) {
     return resident || f == kLevels ? 2 : RT == 2 ? 3 : MI == 4 ? 2 : 4;
