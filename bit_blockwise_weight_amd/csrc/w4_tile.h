@@ -416,9 +416,8 @@ struct RowTiles {
             }
             return v;
         };
-        // Every thread stores (what lies outside, to the 16 bytes behind row 0, which nobody reads): under a
-        // condition the compiler would move the loads down to it, behind those of the codes.
-        // Stores unit b of a batch, the thread's i-th of all.
+        // Stores unit b of a batch, unit i of all.  Every thread stores (what lies outside, to the 16 bytes behind row 0,
+        // which nobody reads): under a condition the compiler would move the loads down to it, behind those of the codes.
         auto x_store_unit = [&](uint8_t* dst, int b, int i, int k0) {
             const int m = i >> ush, u = i & ((1 << ush) - 1);
             const bool in = i < total && u < units;
@@ -472,8 +471,8 @@ struct RowTiles {
             if constexpr (kSplit) *reinterpret_cast<u32x4_t*>(dst + (in ? at + xpitch : at)) = lo;
         };
         auto x_store = [&](uint8_t* dst, int base, int k0) {
-            // Two tiles beside the units in flight of more than one product register leave few registers: there the units
-            // come one after the other, each moved to the front.
+            // (with two tiles and two sums a lane the registers do not hold several units' intermediates: there the units
+            // come one after the other, each moved to the front)
             if constexpr (!kResident && RT == 2 && MI > 1) {
                 const int batch = base + kXUnits * kThreads;
 #pragma unroll 1
