@@ -135,6 +135,11 @@ def _randn(gen, shape, sigma=1.0):
     return torch.randn(shape, generator=gen, device="cuda", dtype=torch.float32) * sigma
 
 
+def _pow2(e):
+    """2^e in 64 bits for whole e, put together from its bits"""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _acts(gen, rows, cols):
     """activations: normal values, one column in a hundred twenty times larger"""
     gain = torch.where(torch.rand(cols, generator=gen, device="cuda") < 0.01, 20.0, 1.0)
@@ -171,7 +176,7 @@ def _mx4_plain(v):
     e = ((top.view(torch.int32) >> 23) - 2).clamp(min=0)               # the exponent bits are floor(log2) + 127
     # a / 2^(e - 127), in two factors that are both ordinary numbers
     half = 127 - e
-    t = a * torch.exp2((half // 2).float()).unsqueeze(-1) * torch.exp2((half - half // 2).float()).unsqueeze(-1)
+    t = a * _pow2(half // 2).float().unsqueeze(-1) * _pow2(half - half // 2).float().unsqueeze(-1)
     code = torch.zeros_like(t, dtype=torch.uint8)
     for mid, closed in ((0.25, False), (0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True),
                         (5.0, False)):
@@ -266,7 +271,7 @@ def _values(m, row0=0, rows=None):
     b = m["codes"][row0:row0 + rows, :groups * 16]
     q = torch.stack((b & 15, b >> 4), 2).view(rows, groups, 32)
     table = torch.tensor(_E2M1 + [-v for v in _E2M1], dtype=torch.float32, device=b.device)
-    s = torch.exp2(m["scales"][row0:row0 + rows, :groups].float() - 127.0)
+    s = _pow2(m["scales"][row0:row0 + rows, :groups].long() - 127).float()
     return (table[q.int()] * s.unsqueeze(2)).view(rows, groups * 32)[:, :cols]
 
 
@@ -278,7 +283,7 @@ def _plain_quant(state):
     v[:, :cols] = x
     e, q = _mx4_plain(v.view(rows, groups, 32))
     table = torch.tensor(_E2M1 + [-t for t in _E2M1], dtype=torch.float32, device=x.device)
-    y = table[q.int()] * torch.exp2(e.float() - 127.0).unsqueeze(2)
+    y = table[q.int()] * _pow2(e.long() - 127).float().unsqueeze(2)
     return [y.view(rows, -1)[:, :cols].to(x.dtype), e]
 
 
@@ -430,8 +435,8 @@ def _exact_values(m, r0=0, rows=None):
     sign = torch.where(q >= 8, -1.0, 1.0)
     q = q % 8
     ex, man = torch.floor(q / 2), q % 2
-    mag = torch.where(ex == 0, man * 0.5, (1 + man / 2) * 2.0 ** (ex - 1))
-    s = 2.0 ** (m["scales"][r0:r0 + rows].double() - 127)
+    mag = torch.where(ex == 0, man * 0.5, (1 + man / 2) * _pow2(ex - 1))
+    s = _pow2(m["scales"][r0:r0 + rows].long() - 127)
     return sign * mag * s.index_select(1, k // 32)
 
 
@@ -454,7 +459,7 @@ def _exact_quant(x):
             top = v.abs().amax(2)
             ex = torch.frexp(top)[1] - 1                               # top = f 2^(ex + 1), f in [1/2, 1)
             ex = torch.where(top > 0, (ex - 2).clamp(min=-127), torch.full_like(ex, -127))
-            unit = torch.ldexp(torch.ones_like(top), ex).unsqueeze(2)
+            unit = _pow2(ex).unsqueeze(2)
             t = v.abs() / unit
             hi = torch.bucketize(t.clamp(max=6.0), grid).clamp(max=7)  # the first value not under t
             lo = (hi - 1).clamp(min=0)
