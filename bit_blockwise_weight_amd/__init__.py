@@ -26,6 +26,9 @@ __all__ = [
     "qk_backend_info", "quantize",
     "Int4State", "Int4Weight", "qk_int4_state_init", "qk_gemv_int4", "qk_gemv_int4_grouped", "qk_moe_workspace_size",
     "qk_moe_int4", "qk_moe_nf4",
+    "Mx4State", "Mx4Weight", "MoePlan", "SOFTMAX", "SIGMOID", "qk_mx4_state_init", "qk_mx4_quantize", "qk_mx4_dequantize",
+    "qk_gemm_mx4", "qk_gemv_mx4", "qk_moe_route", "qk_moe_route_backward", "qk_moe_plan_size", "qk_moe_plan",
+    "qk_moe_up_mx4", "qk_moe_down_mx4_workspace_size", "qk_moe_down_mx4", "quantize_mx4", "moe_mx4",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +45,9 @@ QK_STATE_VERSION = 1
 QK_DQ_BLOCK = 256
 QK_INT4_MAGIC = 0x34494B51
 QK_INT4_VERSION = 1
+QK_MX4_MAGIC = 0x344D4B51
+QK_MX4_VERSION = 1
+SOFTMAX, SIGMOID = 0, 1
 
 _DTYPE_CODE = {torch.float32: QK_F32, torch.bfloat16: QK_BF16, torch.float16: QK_F16}
 
@@ -91,6 +97,22 @@ class Int4State(ctypes.Structure):
         ("codes", ctypes.c_void_p),
         ("scales", ctypes.c_void_p),
         ("zeros", ctypes.c_void_p),
+    ]
+
+
+class Mx4State(ctypes.Structure):
+    """Mirror of qk_mx4_state (include/qk.h)."""
+    _fields_ = [
+        ("magic", ctypes.c_uint32),
+        ("version", ctypes.c_uint32),
+        ("struct_bytes", ctypes.c_uint32),
+        ("reserved", ctypes.c_uint32),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("code_stride", ctypes.c_int64),
+        ("scale_stride", ctypes.c_int64),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
     ]
 
 
@@ -151,6 +173,8 @@ def lib():
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     st_p = ctypes.POINTER(QuantState)
     i4_p = ctypes.POINTER(Int4State)
+    mx_p = ctypes.POINTER(Mx4State)
+    size_p = ctypes.POINTER(ctypes.c_size_t)
     sigs = {
         "qk_make_codebook": [i32, ctypes.POINTER(ctypes.c_float)],
         "qk_quantize_blockwise": [vp, i32, i64, i32, ctypes.POINTER(ctypes.c_float), vp, vp, vp],
@@ -184,6 +208,18 @@ def lib():
         "qk_moe_workspace_size": [i32, i32, i64, i64, ctypes.POINTER(ctypes.c_size_t)],
         "qk_moe_int4": [vp, i32, i32, vp, i32, i32, i32, i32, i4_p, i4_p, vp, vp, ctypes.c_size_t, vp],
         "qk_moe_nf4": [vp, i32, vp, i32, i32, i32, i32, st_p, st_p, vp, vp, ctypes.c_size_t, vp],
+        "qk_mx4_state_init": [mx_p, i64, i64, vp, i64, vp, i64],
+        "qk_mx4_quantize": [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp],
+        "qk_mx4_dequantize": [mx_p, vp, i32, vp],
+        "qk_gemm_mx4": [mx_p, mx_p, vp, i32, vp],
+        "qk_gemv_mx4": [vp, i32, i32, mx_p, vp, vp],
+        "qk_moe_route": [vp, i32, i64, i32, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp],
+        "qk_moe_route_backward": [vp, i32, i64, i32, i32, i32, i32, f32, vp, vp, vp, vp],
+        "qk_moe_plan_size": [i64, i32, i32, size_p],
+        "qk_moe_plan": [vp, i64, i32, i32, vp, vp],
+        "qk_moe_up_mx4": [mx_p, mx_p, vp, i32, i32, vp, i32, vp],
+        "qk_moe_down_mx4_workspace_size": [i64, i32, i64, size_p],
+        "qk_moe_down_mx4": [mx_p, mx_p, vp, vp, i32, i32, vp, i32, vp, ctypes.c_size_t, vp],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -1008,6 +1044,291 @@ class Int4Weight:
 
     def gemv(self, x, y=None):
         return qk_gemv_int4(x, self.state, y)
+
+
+def _mx4_strides(cols: int):
+    """Bytes of a row of codes and of scales, padded as the descriptor asks."""
+    return (-(-cols // 2) + 15) // 16 * 16, (-(-cols // 32) + 3) // 4 * 4
+
+
+def _mx4_part(t: torch.Tensor, rows: int, least: int, multiple: int, name: str):
+    if t.dtype is not torch.uint8 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < least or t.shape[1] % multiple:
+        raise ValueError(f"{name} must be uint8 [{rows}, a multiple of {multiple}, at least {least}], got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def qk_mx4_state_init(rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor) -> Mx4State:
+    """Descriptor of a microscaled 4-bit matrix [rows, cols]: codes uint8 [rows, stride] (two a byte, the first in the low
+    nibble, stride a multiple of 16), scales uint8 [rows, stride] (one per 32 inputs, stride a multiple of 4)."""
+    rows, cols = int(rows), int(cols)
+    _mx4_part(codes, rows, -(-cols // 2), 16, "codes")
+    _mx4_part(scales, rows, -(-cols // 32), 4, "scales")
+    dev = codes.device
+    st = Mx4State()
+    _check(lib().qk_mx4_state_init(st, rows, cols, _ready(codes, dev, "codes"), codes.shape[1],
+                                   _ready(scales, dev, "scales"), scales.shape[1]))
+    # keep the device buffers alive as long as the descriptor
+    st._keep = (codes, scales)
+    st._device, st._shape = dev, (rows, cols)
+    return st
+
+
+def qk_mx4_quantize(x: torch.Tensor, codes=None, scales=None):
+    """(codes, scales) of the rows of x [..., cols] (bf16, fp16 or fp32) in the microscaled 4-bit form, padded as
+    qk_mx4_state_init takes them.  The rows of a 2-D x may lie apart (a slice of a wider matrix)."""
+    if x.dtype not in _DTYPE_CODE:
+        raise ValueError(f"unsupported input dtype {x.dtype}")
+    if x.dim() == 0:
+        raise ValueError("x needs at least one dimension")
+    if not x.is_cuda:
+        raise ValueError("tensors passed to libqk must be on a HIP device")
+    cols = x.shape[-1]
+    if x.dim() == 2 and not x.is_contiguous():
+        rows, pitch = x.shape[0], x.stride(0) if x.shape[0] > 1 else cols
+        if (cols > 1 and x.stride(1) != 1) or pitch < cols:
+            raise ValueError("tensors passed to libqk must be contiguous (the rows of a 2-D x may lie apart)")
+        xp = x.data_ptr()
+    else:
+        rows, pitch = x.numel() // max(1, cols), cols
+        xp = _ready(x, x.device, "x")
+    dev = x.device
+    cs, ss = _mx4_strides(cols)
+    if codes is None:
+        codes = torch.empty((rows, cs), dtype=torch.uint8, device=dev)
+    else:
+        _mx4_part(codes, rows, -(-cols // 2), 16, "codes")
+    if scales is None:
+        scales = torch.empty((rows, ss), dtype=torch.uint8, device=dev)
+    else:
+        _mx4_part(scales, rows, -(-cols // 32), 4, "scales")
+    _call(dev, lib().qk_mx4_quantize, xp, _DTYPE_CODE[x.dtype], rows, cols, pitch, _ready(codes, dev, "codes"),
+          codes.shape[1], _ready(scales, dev, "scales"), scales.shape[1])
+    return codes, scales
+
+
+def _mx4_out(t, shape, dtype, dev, name: str):
+    """(output allocated or checked, its address, its dtype's code)"""
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"{name} must be fp32, bf16 or fp16, got {dtype}")
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _check_out(t, shape, dtype, name)
+    return t, _ready(t, dev, name), _DTYPE_CODE[dtype]
+
+
+def _same_device(a: Mx4State, b: Mx4State, names: str):
+    if a._device != b._device:
+        raise ValueError(f"{names} must be on one device, got {a._device} and {b._device}")
+
+
+def qk_mx4_dequantize(state: Mx4State, dtype=torch.bfloat16, out=None) -> torch.Tensor:
+    """The values [rows, cols] of a microscaled matrix."""
+    dev = state._device
+    out, op, code = _mx4_out(out, state._shape, dtype, dev, "out")
+    _call(dev, lib().qk_mx4_dequantize, state, op, code)
+    return out
+
+
+def qk_gemm_mx4(x: Mx4State, w: Mx4State, dtype=torch.bfloat16, y=None) -> torch.Tensor:
+    """y [M, N] = x w^T of two microscaled matrices [M, K] and [N, K]."""
+    dev = w._device
+    _same_device(x, w, "x and w")
+    y, yp, code = _mx4_out(y, (x._shape[0], w._shape[0]), dtype, dev, "y")
+    _call(dev, lib().qk_gemm_mx4, x, w, yp, code)
+    return y
+
+
+def qk_gemv_mx4(x: torch.Tensor, state: Mx4State, y=None) -> torch.Tensor:
+    """y [M, N] = x W^T for x [M, K] (bf16 or fp16, M <= 16) and a microscaled weight, in x's dtype."""
+    dev = state._device
+    xp, M, y, yp = _int4_acts(x, state, y, dev, "")
+    _call(dev, lib().qk_gemv_mx4, xp, _DTYPE_CODE[x.dtype], M, state, yp)
+    return y
+
+
+def qk_moe_route(logits: torch.Tensor, top_k: int, bias=None, score: int = SOFTMAX, groups: int = 1, top_groups: int = 1,
+                 renormalize: bool = True, scale: float = 1.0, ids=None, weights=None):
+    """(ids int32 [T, top_k], weights fp32 [T, top_k]) of the router's logits [..., E]: the experts of each token by softmax
+    or sigmoid scores, ranked with a bias (fp32 [E]) where one is given, in the best top_groups of `groups` groups."""
+    if logits.dtype not in _DTYPE_CODE:
+        raise ValueError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
+    if logits.dim() == 0:
+        raise ValueError("logits need at least one dimension")
+    dev, E, top_k = logits.device, logits.shape[-1], int(top_k)
+    T = logits.numel() // max(1, E)
+    lp = _ready(logits, dev, "logits")
+    bp = None
+    if bias is not None:
+        if bias.dtype is not torch.float32 or bias.numel() != E:
+            raise ValueError(f"bias must be fp32 [{E}], got {bias.dtype} {tuple(bias.shape)}")
+        bp = _ready(bias, dev, "bias")
+    if top_k < 1:
+        raise ValueError(f"top_k must be at least 1, got {top_k}")
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    else:
+        _check_out(ids, (T, top_k), torch.int32, "ids")
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    else:
+        _check_out(weights, (T, top_k), torch.float32, "weights")
+    _call(dev, lib().qk_moe_route, lp, _DTYPE_CODE[logits.dtype], T, E, bp, int(score), int(groups), int(top_groups), top_k,
+          1 if renormalize else 0, float(scale), _ready(ids, dev, "ids"), _ready(weights, dev, "weights"))
+    return ids, weights
+
+
+def _slots(ids: torch.Tensor):
+    """(T, top_k) of ids [..., top_k]"""
+    if ids.dtype is not torch.int32:
+        raise ValueError(f"ids must be int32, got {ids.dtype}")
+    if ids.dim() < 1 or ids.numel() == 0:
+        raise ValueError(f"ids must be [T, top_k], got {tuple(ids.shape)}")
+    return ids.numel() // ids.shape[-1], ids.shape[-1]
+
+
+def qk_moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, score: int = SOFTMAX,
+                          renormalize: bool = True, scale: float = 1.0, dlogits=None) -> torch.Tensor:
+    """Gradient [..., E] with respect to the logits (in their dtype) of the weights that qk_moe_route gave for `ids`, from
+    their gradient dweights (fp32)."""
+    if logits.dtype not in _DTYPE_CODE:
+        raise ValueError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
+    T, top_k = _slots(ids)
+    dev, E = logits.device, logits.shape[-1] if logits.dim() else 0
+    if logits.numel() != T * E:
+        raise ValueError(f"logits {tuple(logits.shape)} do not hold one row per token ({T})")
+    if dweights.dtype is not torch.float32 or dweights.numel() != T * top_k or dweights.shape[-1] != top_k:
+        raise ValueError(f"dweights must be fp32 [{T}, {top_k}], got {dweights.dtype} {tuple(dweights.shape)}")
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    elif dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
+        raise ValueError(f"dlogits must be {logits.dtype} {tuple(logits.shape)}, got {dlogits.dtype} "
+                         f"{tuple(dlogits.shape)}")
+    _call(dev, lib().qk_moe_route_backward, _ready(logits, dev, "logits"), _DTYPE_CODE[logits.dtype], T, E, int(score),
+          top_k, 1 if renormalize else 0, float(scale), _ready(ids, dev, "ids"), _ready(dweights, dev, "dweights"),
+          _ready(dlogits, dev, "dlogits"))
+    return dlogits
+
+
+def qk_moe_plan_size(T: int, top_k: int, experts: int) -> int:
+    """Bytes of the plan of T tokens with top_k experts each."""
+    out = ctypes.c_size_t(0)
+    _check(lib().qk_moe_plan_size(int(T), int(top_k), int(experts), ctypes.byref(out)))
+    return int(out.value)
+
+
+class MoePlan:
+    """The slots (token, position) of a routing sorted by expert: `first` (int32 [experts + 1]) and `slots` (int32
+    [T * top_k]) are views of its one buffer."""
+
+    def __init__(self, data: torch.Tensor, T: int, top_k: int, experts: int):
+        self.data, self.T, self.top_k, self.experts = data, T, top_k, experts
+        self._device = data.device
+
+    @property
+    def first(self):
+        return self.data[:self.experts + 1]
+
+    @property
+    def slots(self):
+        at = (self.experts + 4) // 4 * 4
+        return self.data[at:at + self.T * self.top_k]
+
+
+def qk_moe_plan(ids: torch.Tensor, experts: int, plan=None) -> MoePlan:
+    """The plan of a routing: ids int32 [..., top_k], those outside 0..experts-1 having no expert.  plan: an int32 tensor
+    of at least qk_moe_plan_size() bytes to write it to."""
+    T, top_k = _slots(ids)
+    dev, experts = ids.device, int(experts)
+    words = qk_moe_plan_size(T, top_k, experts) // 4
+    if plan is None:
+        plan = torch.empty(words, dtype=torch.int32, device=dev)
+    elif plan.dtype is not torch.int32 or plan.numel() < words:
+        raise ValueError(f"plan must be int32 with at least {words} elements, got {plan.dtype} {tuple(plan.shape)}")
+    _call(dev, lib().qk_moe_plan, _ready(ids, dev, "ids"), T, top_k, experts, _ready(plan, dev, "plan"))
+    return MoePlan(plan, T, top_k, experts)
+
+
+def qk_moe_up_mx4(x: Mx4State, gate_up: Mx4State, plan: MoePlan, dtype=torch.bfloat16, h=None) -> torch.Tensor:
+    """h [T * top_k, I] = silu(x Wg^T) * (x Wu^T) of each slot's expert, for microscaled x [T, H] and gate_up [E * 2 * I, H]
+    (gate rows, then up rows, of each expert); zeros in slots without an expert."""
+    dev = gate_up._device
+    _same_device(x, gate_up, "x and gate_up")
+    if x._shape[0] != plan.T:
+        raise ValueError(f"x has {x._shape[0]} rows, the plan {plan.T} tokens")
+    h, hp, code = _mx4_out(h, (plan.T * plan.top_k, gate_up._shape[0] // (2 * plan.experts)), dtype, dev, "h")
+    _call(dev, lib().qk_moe_up_mx4, x, gate_up, _ready(plan.data, dev, "plan"), plan.top_k, plan.experts, hp, code)
+    return h
+
+
+def qk_moe_down_mx4_workspace_size(T: int, top_k: int, hidden: int) -> int:
+    """Workspace bytes of qk_moe_down_mx4 for T tokens of `hidden` outputs."""
+    out = ctypes.c_size_t(0)
+    _check(lib().qk_moe_down_mx4_workspace_size(int(T), int(top_k), int(hidden), ctypes.byref(out)))
+    return int(out.value)
+
+
+def qk_moe_down_mx4(h: Mx4State, down: Mx4State, plan: MoePlan, weights: torch.Tensor, dtype=torch.bfloat16, y=None,
+                    workspace=None) -> torch.Tensor:
+    """y [T, H] = the sum over a token's slots of weight * h Wd^T of the slot's expert, for microscaled h [T * top_k, I] and
+    down [E * H, I]."""
+    dev = down._device
+    _same_device(h, down, "h and down")
+    T, top_k = plan.T, plan.top_k
+    if h._shape[0] != T * top_k:
+        raise ValueError(f"h has {h._shape[0]} rows, the plan {T * top_k} slots")
+    if weights.dtype is not torch.float32 or weights.numel() != T * top_k or weights.shape[-1] != top_k:
+        raise ValueError(f"weights must be fp32 [{T}, {top_k}], got {weights.dtype} {tuple(weights.shape)}")
+    hidden = down._shape[0] // plan.experts
+    y, yp, code = _mx4_out(y, (T, hidden), dtype, dev, "y")
+    if workspace is None:
+        workspace = torch.empty(_moe_down_bytes(T, top_k, hidden), dtype=torch.uint8, device=dev)
+    _call(dev, lib().qk_moe_down_mx4, h, down, _ready(plan.data, dev, "plan"), _ready(weights, dev, "weights"), top_k,
+          plan.experts, yp, code, _ready(workspace, dev, "workspace"), workspace.nbytes)
+    return y
+
+
+_moe_down_bytes = functools.lru_cache(maxsize=256)(qk_moe_down_mx4_workspace_size)
+
+
+class Mx4Weight:
+    """A weight [N, K] in the microscaled 4-bit form: its buffers and its descriptor."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        self.codes, self.scales = codes, scales
+        self.state = qk_mx4_state_init(rows, cols, codes, scales)
+
+    @property
+    def shape(self):
+        return (self.state.rows, self.state.cols)
+
+    def dequantize(self, dtype=torch.bfloat16, out=None):
+        return qk_mx4_dequantize(self.state, dtype, out)
+
+    def gemv(self, x, y=None):
+        return qk_gemv_mx4(x, self.state, y)
+
+    def gemm(self, X, y=None):
+        """X W^T in X's dtype, X [M, K] being quantized to the microscaled form first."""
+        return qk_gemm_mx4(quantize_mx4(X).state, self.state, X.dtype, y)
+
+
+def quantize_mx4(w: torch.Tensor) -> Mx4Weight:
+    """qk_mx4_quantize of a 2-D matrix and the descriptor."""
+    if w.dim() != 2:
+        raise ValueError("quantize_mx4 expects a 2-D matrix [N, K]")
+    codes, scales = qk_mx4_quantize(w)
+    return Mx4Weight(codes, scales, w.shape[0], w.shape[1])
+
+
+def moe_mx4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: Mx4Weight, down: Mx4Weight) -> torch.Tensor:
+    """A mixture-of-experts layer of x [T, H] (bf16 or fp16) over microscaled experts and a routing of qk_moe_route: gate_up
+    [E * 2 * I, H], down [E * H, I].  x and the activations between the two products are quantized."""
+    if x.dim() != 2 or x.shape[1] < 1 or down.shape[0] % x.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} does not fit down {down.shape}")
+    plan = qk_moe_plan(ids, down.shape[0] // x.shape[1])
+    h = qk_moe_up_mx4(quantize_mx4(x).state, gate_up.state, plan, x.dtype)
+    return qk_moe_down_mx4(quantize_mx4(h).state, down.state, plan, weights, x.dtype)
 
 
 class QuantizedWeight:

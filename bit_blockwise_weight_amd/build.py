@@ -32,7 +32,7 @@ PROBE_SOURCE = "hbm_probe.hip"
 
 SOURCES = ["api.cpp", "codebook.cpp", "quantize.hip", "double_quant.hip", "dequantize.hip", "gemv.hip", "gemm.hip",
            "merge.hip", "backward.hip", "quantize8.hip", "int8mm.hip",
-           "int4_gemv.hip", "moe.hip"]
+           "int4_gemv.hip", "moe.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_gemv.hip", "route.hip"]
 
 COMMON_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

@@ -1,6 +1,7 @@
 // C ABI of libqk: argument and descriptor validation, error reporting, kernel
 // launch.  Every check runs on the host before anything is launched and no
 // device pointer is dereferenced here; a rejected call launches nothing.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -192,6 +193,78 @@ qk_status check_moe(const char* who, const qk::MoeItem& m, int64_t up_rows, int6
         return fail(QK_ERR_INVALID_ARG, "%s: the workspace overlaps x, logits or y", who);
     if (overlap(m.y, xb, m.x, xb) && m.y != m.x)
         return fail(QK_ERR_INVALID_ARG, "%s: y overlaps x without being x", who);
+    return QK_OK;
+}
+
+qk_status check_mx4_fields(const qk_mx4_state* st, qk_status bad, const char* who) {
+    if (st->rows < 1 || st->rows > ((int64_t)1 << 30) || st->cols < 1 || st->cols > ((int64_t)1 << 22))
+        return fail(bad, "%s: rows must be in 1..2^30 and cols in 1..2^22 (got %lld, %lld)", who, (long long)st->rows,
+                    (long long)st->cols);
+    if (st->code_stride % 16 != 0 || st->code_stride < cdiv(st->cols, 2) || st->code_stride > ((int64_t)1 << 22))
+        return fail(bad, "%s: code_stride %lld (a multiple of 16, at least %lld and at most 2^22)", who,
+                    (long long)st->code_stride, (long long)cdiv(st->cols, 2));
+    if (st->scale_stride % 4 != 0 || st->scale_stride < cdiv(st->cols, 32) || st->scale_stride > ((int64_t)1 << 22))
+        return fail(bad, "%s: scale_stride %lld (a multiple of 4, at least %lld and at most 2^22)", who,
+                    (long long)st->scale_stride, (long long)cdiv(st->cols, 32));
+    if (!st->codes || !st->scales) return fail(bad, "%s: codes or scales pointer is NULL", who);
+    if (!aligned(st->codes, 16) || !aligned(st->scales, 4))
+        return fail(bad, "%s: codes must be 16-byte aligned and scales 4-byte aligned", who);
+    return QK_OK;
+}
+
+qk_status validate_mx4(const qk_mx4_state* st) {
+    if (!st) return fail(QK_ERR_INVALID_ARG, "mx4 state pointer is NULL");
+    if (st->magic != QK_MX4_MAGIC)
+        return fail(QK_ERR_BAD_STATE, "mx4 state: bad magic 0x%08x (not a qk_mx4_state or corrupted)", st->magic);
+    if (st->version != QK_MX4_VERSION)
+        return fail(QK_ERR_BAD_STATE, "mx4 state: unknown version %u (this library reads %u)", st->version, QK_MX4_VERSION);
+    if (st->struct_bytes != sizeof(qk_mx4_state))
+        return fail(QK_ERR_BAD_STATE, "mx4 state: struct_bytes %u != %zu", st->struct_bytes, sizeof(qk_mx4_state));
+    if (st->reserved != 0) return fail(QK_ERR_BAD_STATE, "mx4 state: reserved field is not 0");
+    return check_mx4_fields(st, QK_ERR_BAD_STATE, "mx4 state");
+}
+
+bool known_dtype(int32_t d) { return d == QK_F32 || d == QK_BF16 || d == QK_F16; }
+size_t dtype_bytes(int32_t d) { return d == QK_F32 ? 4 : 2; }
+
+size_t mx4_code_bytes(const qk_mx4_state* st) { return (size_t)st->rows * (size_t)st->code_stride; }
+size_t mx4_scale_bytes(const qk_mx4_state* st) { return (size_t)st->rows * (size_t)st->scale_stride; }
+
+// An output of `bytes` at p beside a microscaled operand.
+bool overlaps_mx4(const void* p, size_t bytes, const qk_mx4_state* st) {
+    return overlap(p, bytes, st->codes, mx4_code_bytes(st)) || overlap(p, bytes, st->scales, mx4_scale_bytes(st));
+}
+
+// A typed output beside the operands of a product.
+qk_status check_mx4_out(const char* who, const char* name, const void* out, int32_t dtype, size_t elements,
+                        const qk_mx4_state* a, const qk_mx4_state* b) {
+    if (!out) return fail(QK_ERR_INVALID_ARG, "%s: NULL %s", who, name);
+    if (!known_dtype(dtype)) return fail(QK_ERR_INVALID_ARG, "%s: unknown dtype %d of %s", who, dtype, name);
+    if (!aligned(out, dtype_bytes(dtype)))
+        return fail(QK_ERR_INVALID_ARG, "%s: %s must be aligned to its elements", who, name);
+    const size_t bytes = elements * dtype_bytes(dtype);
+    if (overlaps_mx4(out, bytes, a) || overlaps_mx4(out, bytes, b))
+        return fail(QK_ERR_INVALID_ARG, "%s: %s overlaps an operand", who, name);
+    return QK_OK;
+}
+
+constexpr int32_t kMaxRouteExperts = 512, kMaxRouteTopK = 32;
+
+qk_status check_slots(const char* who, int64_t T, int32_t top_k, int32_t E) {
+    if (E < 1 || E > kMaxRouteExperts) return fail(QK_ERR_INVALID_ARG, "%s: E must be in 1..512 (got %d)", who, E);
+    if (top_k < 1 || top_k > kMaxRouteTopK)
+        return fail(QK_ERR_INVALID_ARG, "%s: top_k must be in 1..32 (got %d)", who, top_k);
+    if (T < 1 || T > ((int64_t)1 << 26) / top_k)
+        return fail(QK_ERR_INVALID_ARG, "%s: T must be at least 1 and T * top_k at most 2^26 (got %lld, %d)", who,
+                    (long long)T, top_k);
+    return QK_OK;
+}
+
+// Rows reached by 32-bit offsets, up to a line past the last one.
+qk_status check_gather(const char* who, const char* name, int64_t rows, int64_t code_stride, int64_t scale_stride) {
+    if (rows * std::max(code_stride, scale_stride) >= ((int64_t)1 << 32) - ((int64_t)1 << 24))
+        return fail(QK_ERR_UNSUPPORTED, "%s: %s passes 32-bit offsets (%lld rows of %lld bytes)", who, name,
+                    (long long)rows, (long long)std::max(code_stride, scale_stride));
     return QK_OK;
 }
 
@@ -938,6 +1011,253 @@ qk_status qk_moe_nf4(const void* x, int32_t T, const void* logits, int32_t logit
                                           qk::MatArgs{deq_args(down), down->rows, down->cols}, workspace,
                                           reinterpret_cast<hipStream_t>(stream)),
                     "qk_moe_nf4");
+}
+
+qk_status qk_mx4_state_init(qk_mx4_state* st, int64_t rows, int64_t cols, const uint8_t* codes, int64_t code_stride,
+                            const uint8_t* scales, int64_t scale_stride) {
+    if (!st) return fail(QK_ERR_INVALID_ARG, "qk_mx4_state_init: NULL state");
+    qk_mx4_state s;
+    std::memset(&s, 0, sizeof(s));
+    s.magic = QK_MX4_MAGIC;
+    s.version = QK_MX4_VERSION;
+    s.struct_bytes = sizeof(qk_mx4_state);
+    s.rows = rows;
+    s.cols = cols;
+    s.code_stride = code_stride;
+    s.scale_stride = scale_stride;
+    s.codes = codes;
+    s.scales = scales;
+    const qk_status v = check_mx4_fields(&s, QK_ERR_INVALID_ARG, "qk_mx4_state_init");
+    if (v != QK_OK) return v;
+    *st = s;
+    return ok();
+}
+
+qk_status qk_mx4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t x_stride, uint8_t* codes,
+                          int64_t code_stride, uint8_t* scales, int64_t scale_stride, void* stream) {
+    const char* who = "qk_mx4_quantize";
+    qk_mx4_state st;
+    std::memset(&st, 0, sizeof(st));
+    st.rows = rows;
+    st.cols = cols;
+    st.code_stride = code_stride;
+    st.scale_stride = scale_stride;
+    st.codes = codes;
+    st.scales = scales;
+    const qk_status v = check_mx4_fields(&st, QK_ERR_INVALID_ARG, who);
+    if (v != QK_OK) return v;
+    if (!x) return fail(QK_ERR_INVALID_ARG, "%s: NULL x", who);
+    if (!known_dtype(x_dtype)) return fail(QK_ERR_INVALID_ARG, "%s: unknown dtype %d of x", who, x_dtype);
+    if (!aligned(x, dtype_bytes(x_dtype))) return fail(QK_ERR_INVALID_ARG, "%s: x must be aligned to its elements", who);
+    if (x_stride < cols || x_stride > ((int64_t)1 << 40))
+        return fail(QK_ERR_INVALID_ARG, "%s: x_stride %lld (at least cols and at most 2^40)", who, (long long)x_stride);
+    int64_t span = 0;
+    if (__builtin_mul_overflow(rows - 1, x_stride, &span) || span > ((int64_t)1 << 58))
+        return fail(QK_ERR_INVALID_ARG, "%s: rows %lld of x_stride %lld pass the address space", who, (long long)rows,
+                    (long long)x_stride);
+    if (overlaps_mx4(x, (size_t)(span + cols) * dtype_bytes(x_dtype), &st) ||
+        overlap(codes, mx4_code_bytes(&st), scales, mx4_scale_bytes(&st)))
+        return fail(QK_ERR_INVALID_ARG, "%s: x, codes and scales overlap", who);
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_mx4_quantize(x, x_dtype, rows, cols, x_stride, codes, code_stride, scales, scale_stride,
+                                            reinterpret_cast<hipStream_t>(stream)),
+                    who);
+}
+
+qk_status qk_mx4_dequantize(const qk_mx4_state* st, void* out, int32_t out_dtype, void* stream) {
+    qk_status v = validate_mx4(st);
+    if (v == QK_OK)
+        v = check_mx4_out("qk_mx4_dequantize", "out", out, out_dtype, (size_t)st->rows * (size_t)st->cols, st, st);
+    if (v != QK_OK) return v;
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_mx4_dequantize(st, out, out_dtype, reinterpret_cast<hipStream_t>(stream)),
+                    "qk_mx4_dequantize");
+}
+
+qk_status qk_gemm_mx4(const qk_mx4_state* x, const qk_mx4_state* w, void* y, int32_t y_dtype, void* stream) {
+    qk_status v = validate_mx4(x);
+    if (v == QK_OK) v = validate_mx4(w);
+    if (v != QK_OK) return v;
+    if (x->cols != w->cols)
+        return fail(QK_ERR_INVALID_ARG, "qk_gemm_mx4: x has %lld columns, w %lld", (long long)x->cols, (long long)w->cols);
+    v = check_mx4_out("qk_gemm_mx4", "y", y, y_dtype, (size_t)x->rows * (size_t)w->rows, x, w);
+    if (v != QK_OK) return v;
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_mx4_gemm(x, w, y, y_dtype, reinterpret_cast<hipStream_t>(stream)), "qk_gemm_mx4");
+}
+
+qk_status qk_gemv_mx4(const void* x, int32_t dtype, int32_t M, const qk_mx4_state* st, void* y, void* stream) {
+    const char* who = "qk_gemv_mx4";
+    qk_status v = validate_mx4(st);
+    if (v != QK_OK) return v;
+    if (dtype != QK_BF16 && dtype != QK_F16)
+        return fail(QK_ERR_INVALID_ARG, "%s: dtype %d (expected QK_BF16 or QK_F16)", who, dtype);
+    if (M < 1 || M > 16) return fail(QK_ERR_INVALID_ARG, "%s: M must be in 1..16 (got %d)", who, M);
+    if (st->rows > ((int64_t)1 << 28))
+        return fail(QK_ERR_INVALID_ARG, "%s: N must be at most 2^28 (got %lld)", who, (long long)st->rows);
+    if (!x) return fail(QK_ERR_INVALID_ARG, "%s: NULL x", who);
+    if (!aligned(x, 2)) return fail(QK_ERR_INVALID_ARG, "%s: x must be 2-byte aligned", who);
+    v = check_mx4_out(who, "y", y, dtype, (size_t)M * (size_t)st->rows, st, st);
+    if (v != QK_OK) return v;
+    if (overlap(y, (size_t)M * (size_t)st->rows * 2, x, (size_t)M * (size_t)st->cols * 2))
+        return fail(QK_ERR_INVALID_ARG, "%s: y overlaps x", who);
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_mx4_gemv(x, M, st, y, dtype == QK_F16, reinterpret_cast<hipStream_t>(stream)), who);
+}
+
+qk_status qk_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t E, const float* bias, int32_t score,
+                       int32_t groups, int32_t top_groups, int32_t top_k, int32_t renormalize, float scale, int32_t* ids,
+                       float* weights, void* stream) {
+    const char* who = "qk_moe_route";
+    const qk_status v = check_slots(who, T, top_k, E);
+    if (v != QK_OK) return v;
+    if (!logits || !ids || !weights) return fail(QK_ERR_INVALID_ARG, "%s: NULL logits, ids or weights", who);
+    if (!known_dtype(dtype)) return fail(QK_ERR_INVALID_ARG, "%s: unknown dtype %d of the logits", who, dtype);
+    if (score != QK_SOFTMAX && score != QK_SIGMOID) return fail(QK_ERR_INVALID_ARG, "%s: unknown score %d", who, score);
+    if (groups < 1 || groups > 64 || E % groups != 0)
+        return fail(QK_ERR_INVALID_ARG, "%s: groups must be in 1..64 and divide E (got %d of %d experts)", who, groups, E);
+    if (top_groups < 1 || top_groups > groups)
+        return fail(QK_ERR_INVALID_ARG, "%s: top_groups must be in 1..groups (got %d of %d)", who, top_groups, groups);
+    if (top_k > E / groups * top_groups)
+        return fail(QK_ERR_INVALID_ARG, "%s: top_k %d of %d experts in %d groups", who, top_k, E / groups * top_groups,
+                    top_groups);
+    if (!std::isfinite(scale)) return fail(QK_ERR_INVALID_ARG, "%s: scale is not finite", who);
+    if (!aligned(logits, dtype_bytes(dtype)) || !aligned(ids, 4) || !aligned(weights, 4) || (bias && !aligned(bias, 4)))
+        return fail(QK_ERR_INVALID_ARG, "%s: buffers must be aligned to their elements", who);
+    const size_t lb = (size_t)T * (size_t)E * dtype_bytes(dtype), sb = (size_t)T * (size_t)top_k * 4;
+    if (overlap(ids, sb, logits, lb) || overlap(weights, sb, logits, lb) || overlap(ids, sb, weights, sb) ||
+        (bias && (overlap(ids, sb, bias, (size_t)E * 4) || overlap(weights, sb, bias, (size_t)E * 4))))
+        return fail(QK_ERR_INVALID_ARG, "%s: ids or weights overlap another buffer", who);
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    const qk::MoeRouteArgs a{logits, bias, ids, weights, T, dtype, E, score, groups, top_groups, top_k, renormalize != 0,
+                             scale};
+    return launched(qk::launch_moe_route(a, reinterpret_cast<hipStream_t>(stream)), who);
+}
+
+qk_status qk_moe_route_backward(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t score, int32_t top_k,
+                                int32_t renormalize, float scale, const int32_t* ids, const float* dweights,
+                                void* dlogits, void* stream) {
+    const char* who = "qk_moe_route_backward";
+    const qk_status v = check_slots(who, T, top_k, E);
+    if (v != QK_OK) return v;
+    if (!logits || !ids || !dweights || !dlogits)
+        return fail(QK_ERR_INVALID_ARG, "%s: NULL logits, ids, dweights or dlogits", who);
+    if (!known_dtype(dtype)) return fail(QK_ERR_INVALID_ARG, "%s: unknown dtype %d of the logits", who, dtype);
+    if (score != QK_SOFTMAX && score != QK_SIGMOID) return fail(QK_ERR_INVALID_ARG, "%s: unknown score %d", who, score);
+    if (!std::isfinite(scale)) return fail(QK_ERR_INVALID_ARG, "%s: scale is not finite", who);
+    if (!aligned(logits, dtype_bytes(dtype)) || !aligned(dlogits, dtype_bytes(dtype)) || !aligned(ids, 4) ||
+        !aligned(dweights, 4))
+        return fail(QK_ERR_INVALID_ARG, "%s: buffers must be aligned to their elements", who);
+    const size_t lb = (size_t)T * (size_t)E * dtype_bytes(dtype), sb = (size_t)T * (size_t)top_k * 4;
+    if ((dlogits != logits && overlap(dlogits, lb, logits, lb)) || overlap(dlogits, lb, ids, sb) ||
+        overlap(dlogits, lb, dweights, sb))
+        return fail(QK_ERR_INVALID_ARG, "%s: dlogits overlaps an input without being the logits", who);
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    const qk::MoeRouteBackwardArgs a{logits, ids, dweights, dlogits, T, dtype, E, score, top_k, renormalize != 0, scale};
+    return launched(qk::launch_moe_route_backward(a, reinterpret_cast<hipStream_t>(stream)), who);
+}
+
+qk_status qk_moe_plan_size(int64_t T, int32_t top_k, int32_t E, size_t* bytes) {
+    if (!bytes) return fail(QK_ERR_INVALID_ARG, "qk_moe_plan_size: bytes is NULL");
+    const qk_status v = check_slots("qk_moe_plan_size", T, top_k, E);
+    if (v != QK_OK) return v;
+    *bytes = (size_t)(qk::moe_plan_list(E) + T * top_k) * 4;
+    return ok();
+}
+
+qk_status qk_moe_plan(const int32_t* ids, int64_t T, int32_t top_k, int32_t E, int32_t* plan, void* stream) {
+    const char* who = "qk_moe_plan";
+    const qk_status v = check_slots(who, T, top_k, E);
+    if (v != QK_OK) return v;
+    if (!ids || !plan) return fail(QK_ERR_INVALID_ARG, "%s: NULL ids or plan", who);
+    if (!aligned(ids, 4) || !aligned(plan, 16))
+        return fail(QK_ERR_INVALID_ARG, "%s: ids must be 4-byte aligned and plan 16-byte aligned", who);
+    if (overlap(ids, (size_t)(T * top_k) * 4, plan, (size_t)(qk::moe_plan_list(E) + T * top_k) * 4))
+        return fail(QK_ERR_INVALID_ARG, "%s: plan overlaps ids", who);
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_moe_plan(ids, T * top_k, E, plan, reinterpret_cast<hipStream_t>(stream)), who);
+}
+
+qk_status qk_moe_up_mx4(const qk_mx4_state* x, const qk_mx4_state* gate_up, const int32_t* plan, int32_t top_k, int32_t E,
+                        void* h, int32_t h_dtype, void* stream) {
+    const char* who = "qk_moe_up_mx4";
+    qk_status v = validate_mx4(x);
+    if (v == QK_OK) v = validate_mx4(gate_up);
+    if (v == QK_OK) v = check_slots(who, x->rows, top_k, E);
+    if (v != QK_OK) return v;
+    if (x->cols != gate_up->cols || gate_up->rows % (2 * (int64_t)E) != 0)
+        return fail(QK_ERR_INVALID_ARG, "%s: x [%lld, %lld] and gate_up [%lld, %lld] are not [T, H] and [E*2*I, H] of %d experts",
+                    who, (long long)x->rows, (long long)x->cols, (long long)gate_up->rows, (long long)gate_up->cols, E);
+    const int64_t slots = x->rows * top_k, I = gate_up->rows / (2 * (int64_t)E);
+    const size_t pb = (size_t)(qk::moe_plan_list(E) + slots) * 4;
+    if (!plan || !aligned(plan, 16)) return fail(QK_ERR_INVALID_ARG, "%s: plan is NULL or not 16-byte aligned", who);
+    v = check_mx4_out(who, "h", h, h_dtype, (size_t)slots * (size_t)I, x, gate_up);
+    if (v == QK_OK) v = check_gather(who, "x", x->rows, x->code_stride, x->scale_stride);
+    if (v == QK_OK) v = check_gather(who, "an expert's gate_up", 2 * I, gate_up->code_stride, gate_up->scale_stride);
+    if (v != QK_OK) return v;
+    if (overlap(h, (size_t)slots * (size_t)I * dtype_bytes(h_dtype), plan, pb))
+        return fail(QK_ERR_INVALID_ARG, "%s: h overlaps the plan", who);
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_moe_up_mx4(x, gate_up, plan, top_k, E, h, h_dtype, reinterpret_cast<hipStream_t>(stream)),
+                    who);
+}
+
+qk_status qk_moe_down_mx4_workspace_size(int64_t T, int32_t top_k, int64_t hidden, size_t* bytes) {
+    if (!bytes) return fail(QK_ERR_INVALID_ARG, "qk_moe_down_mx4_workspace_size: bytes is NULL");
+    const qk_status v = check_slots("qk_moe_down_mx4_workspace_size", T, top_k, 1);
+    if (v != QK_OK) return v;
+    if (hidden < 1 || hidden > ((int64_t)1 << 30))
+        return fail(QK_ERR_INVALID_ARG, "qk_moe_down_mx4_workspace_size: hidden must be in 1..2^30 (got %lld)",
+                    (long long)hidden);
+    *bytes = qk::moe_down_mx4_workspace_bytes(T, top_k, hidden);
+    return ok();
+}
+
+qk_status qk_moe_down_mx4(const qk_mx4_state* h, const qk_mx4_state* down, const int32_t* plan, const float* weights,
+                          int32_t top_k, int32_t E, void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    const char* who = "qk_moe_down_mx4";
+    qk_status v = validate_mx4(h);
+    if (v == QK_OK) v = validate_mx4(down);
+    if (v != QK_OK) return v;
+    if (top_k < 1 || h->rows % top_k != 0)
+        return fail(QK_ERR_INVALID_ARG, "%s: h has %lld rows, no multiple of top_k %d", who, (long long)h->rows, top_k);
+    const int64_t T = h->rows / top_k;
+    v = check_slots(who, T, top_k, E);
+    if (v != QK_OK) return v;
+    if (h->cols != down->cols || down->rows % E != 0)
+        return fail(QK_ERR_INVALID_ARG, "%s: h [%lld, %lld] and down [%lld, %lld] are not [T*top_k, I] and [E*H, I] of %d experts",
+                    who, (long long)h->rows, (long long)h->cols, (long long)down->rows, (long long)down->cols, E);
+    const int64_t H = down->rows / E;
+    const size_t pb = (size_t)(qk::moe_plan_list(E) + h->rows) * 4, wb = (size_t)h->rows * 4;
+    if (!plan || !aligned(plan, 16)) return fail(QK_ERR_INVALID_ARG, "%s: plan is NULL or not 16-byte aligned", who);
+    if (!weights || !aligned(weights, 4)) return fail(QK_ERR_INVALID_ARG, "%s: weights is NULL or not 4-byte aligned", who);
+    v = check_mx4_out(who, "y", y, y_dtype, (size_t)T * (size_t)H, h, down);
+    if (v == QK_OK) v = check_gather(who, "h", h->rows, h->code_stride, h->scale_stride);
+    if (v != QK_OK) return v;
+    const size_t need = qk::moe_down_mx4_workspace_bytes(T, top_k, H), yb = (size_t)T * (size_t)H * dtype_bytes(y_dtype);
+    if (!workspace || workspace_bytes < need)
+        return fail(QK_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who, need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (!aligned(workspace, 16)) return fail(QK_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", who);
+    if (overlap(y, yb, plan, pb) || overlap(y, yb, weights, wb) || overlap(y, yb, workspace, need))
+        return fail(QK_ERR_INVALID_ARG, "%s: y overlaps the plan, the weights or the workspace", who);
+    if (overlap(workspace, need, plan, pb) || overlap(workspace, need, weights, wb) || overlaps_mx4(workspace, need, h) ||
+        overlaps_mx4(workspace, need, down))
+        return fail(QK_ERR_INVALID_ARG, "%s: the workspace overlaps another buffer", who);
+    const qk_status dev = ensure_device();
+    if (dev != QK_OK) return dev;
+    return launched(qk::launch_moe_down_mx4(h, down, plan, weights, top_k, E, y, y_dtype, workspace,
+                                            reinterpret_cast<hipStream_t>(stream)),
+                    who);
 }
 
 const char* qk_last_error(void) { return g_last_error.c_str(); }

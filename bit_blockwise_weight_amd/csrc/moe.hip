@@ -79,21 +79,6 @@ struct RouteScratch {
     int32_t total[4];
 };
 
-template <int kCtrl, int kRows>
-__device__ __forceinline__ int dpp_from(int v) {
-    return __builtin_amdgcn_update_dpp(0, v, kCtrl, kRows, 0xF, false);
-}
-// Inclusive prefix sum over the wave: shifts inside the rows of 16 lanes, then the last lane of row 0 and 2 added to
-// rows 1 and 3, and lane 31 to the upper half.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += dpp_from<0x111, 0xF>(v);
-    v += dpp_from<0x112, 0xF>(v);
-    v += dpp_from<0x114, 0xF>(v);
-    v += dpp_from<0x118, 0xF>(v);
-    v += dpp_from<0x142, 0xA>(v);
-    v += dpp_from<0x143, 0xC>(v);
-    return v;
-}
 // Sum over 16 lanes, in every one of them.
 __device__ __forceinline__ float row_sum(float v) {
     v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0xB1, 0xF, 0xF, false));    // xor 1

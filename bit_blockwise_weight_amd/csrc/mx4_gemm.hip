@@ -1,0 +1,660 @@
+// Products of microscaled 4-bit matrices on the scaled matrix cores of gfx950: Y = X W^T, and the gate / up and down
+// products of a mixture of experts over a routing.
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 takes, of each operand, a row's 32 codes (16 bytes) and their scale byte from every
+// lane: row l % 16, group l / 16 of the four.  Which four groups those are does not matter as long as both operands
+// agree.  A stage is 256 inputs, a 128-byte line of a row; its two instructions s = 0, 1 take group 2 (l / 16) + s, so
+// that a lane's two scale bytes are neighbours and the instruction picks one by its byte select.  W is the first operand: a
+// lane then ends up with 4 consecutive columns of one row of Y.
+//
+// Codes and scales go from memory straight to LDS.  A row of a stage keeps its 128 bytes, piece p of row r in slot
+// p ^ (r / 2 % 8): the 16 rows that 16 lanes read at a time then fall in all banks.
+//
+// What lies past the last input of a row (the row's padding, the next row, nothing) is in the last line too: before that
+// line is used its groups past the end get the scale 1 in both operands and its codes past the end become 0 in X.
+#include <algorithm>
+
+#include "mx4.h"
+
+namespace qk {
+namespace {
+
+using namespace mx4;
+
+typedef int v8i_t __attribute__((ext_vector_type(8)));
+typedef int v4i_t __attribute__((ext_vector_type(4)));
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr int kLineK = 256;                // inputs of a stage: 128 bytes of codes, 8 of scales
+constexpr int kXcds = 8;
+
+enum Mode { kDense, kUp, kDown };
+
+struct GemmArgs {
+    View x, w;
+    void* y;                   // dense: [M, N]; up: h [slots, I]; down: the weighted parts [slots, H], fp32
+    const int32_t* plan;
+    const float* weights;      // down: of the slots
+    int64_t M;                 // dense: rows of x
+    int64_t N;                 // outputs of a row: N, I or H
+    int64_t w_rows;            // rows of an expert's weights: 2 I or H
+    int32_t y_dtype;
+    int32_t top_k, E;
+    int32_t slots;
+};
+
+// The part of the product that a workgroup makes: rows of X by position 0..count-1, columns n0 on, of one expert.
+struct Tile {
+    int64_t m0;                // dense: first row of X and Y; otherwise the first place in the list of slots
+    int64_t n0;
+    int32_t count;
+    int32_t expert;            // E: slots without one
+};
+
+// Tile `bid` of a dense product.  Workgroup i runs on XCD i % 8: each XCD gets a run of tiles, 8 rows of them at a time
+// going through all columns, so that the tiles of an XCD share operands in its L2.
+template <int BM, int BN>
+__device__ __forceinline__ Tile dense_tile(const GemmArgs& a) {
+    const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + BN - 1) / BN), nt = tm * tn;
+    const uint32_t xcd = blockIdx.x % kXcds, q = nt / kXcds, rem = nt % kXcds;
+    const uint32_t lid = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
+    const uint32_t band = lid / (kXcds * tn), in = lid - band * (kXcds * tn);
+    const uint32_t rows = tm - band * kXcds < kXcds ? tm - band * kXcds : kXcds;
+    Tile t;
+    t.m0 = (int64_t)(band * kXcds + in % rows) * BM;
+    t.n0 = (int64_t)(in / rows) * BN;
+    t.count = (int32_t)(a.M - t.m0 < BM ? a.M - t.m0 : BM);
+    t.expert = 0;
+    return t;
+}
+
+// The same for the experts' products: the tiles of an expert one after the other, its rows fastest; count 0: none left.
+// Every wave finds its tile by itself, from a prefix sum over the experts' tiles (9 experts a lane at most).
+template <int BM, int BNo>
+__device__ __forceinline__ Tile expert_tile(const GemmArgs& a) {
+    const int lane = threadIdx.x & 63;
+    const uint32_t nb = (uint32_t)((a.N + BNo - 1) / BNo);
+    const int entries = a.E + 1, per = (entries + 63) / 64;          // the last entry: slots without an expert
+    auto start = [&](int e) { return e <= a.E ? a.plan[e] : a.slots; };
+    int tiles = 0;
+    for (int i = 0, p = start(min(lane * per, entries)); i < per; ++i) {
+        const int n = start(min(lane * per + i + 1, entries));
+        tiles += (n - p + BM - 1) / BM;
+        p = n;
+    }
+    const int incl = wave_scan(tiles);
+    const uint32_t nt = (uint32_t)__builtin_amdgcn_readlane(incl, 63) * nb;
+    Tile t;
+    t.count = 0;
+    t.m0 = t.n0 = 0;
+    t.expert = 0;
+    if (blockIdx.x >= nt) return t;
+    const uint32_t xcd = blockIdx.x % kXcds, q = nt / kXcds, rem = nt % kXcds;
+    const uint32_t lid = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
+    const int at = (int)(lid / nb);                                   // in [first tile of e, first tile of e + 1)
+    int first = incl - tiles, e = 0, p0 = 0, p1 = 0, tile0 = 0, mine = 0;
+    for (int i = 0, p = start(min(lane * per, entries)); i < per; ++i) {
+        const int n = start(min(lane * per + i + 1, entries));
+        const int k = (n - p + BM - 1) / BM;
+        if (at >= first && at < first + k) {
+            e = lane * per + i;
+            p0 = p;
+            p1 = n;
+            tile0 = first;
+            mine = k;
+        }
+        first += k;
+        p = n;
+    }
+    const int who = __builtin_ctzll(__ballot(mine > 0));
+    e = __builtin_amdgcn_readlane(e, who);
+    p0 = __builtin_amdgcn_readlane(p0, who);
+    p1 = __builtin_amdgcn_readlane(p1, who);
+    tile0 = __builtin_amdgcn_readlane(tile0, who);
+    mine = __builtin_amdgcn_readlane(mine, who);
+    const uint32_t in = lid - (uint32_t)tile0 * nb;
+    t.expert = e;
+    t.m0 = p0 + (int64_t)(in % (uint32_t)mine) * BM;
+    t.n0 = (int64_t)(in / (uint32_t)mine) * BNo;
+    t.count = p1 - (int)t.m0 < BM ? p1 - (int)t.m0 : BM;
+    return t;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, int64_t bytes) {
+    const uint32_t n = (uint32_t)(bytes < 0xFFFF0000ll ? bytes : 0xFFFF0000ll);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0, (int)n, 0x00020000);
+}
+
+// Where the rows of a tile's operands are.  Row i of X and of W (clamped to the last one there is) as a row of its buffer.
+template <Mode MODE>
+struct Operands {
+    __amdgpu_buffer_rsrc_t xc, xs, wc, ws;
+    const int32_t* list;       // slots of the tile
+    int32_t x_rows;            // of the tile
+    int32_t w_rows;            // of a kind, from n0 on
+    int32_t up;                // rows from a gate row to its up row
+    int32_t top_k;
+
+    __device__ __forceinline__ Operands(const GemmArgs& a, const Tile& t) {
+        x_rows = t.count;
+        top_k = a.top_k;
+        up = (int32_t)a.N;
+        const int64_t left = a.N - t.n0;
+        w_rows = (int32_t)(left < 1024 ? left : 1024);
+        const uint8_t *cx = a.x.codes, *sx = a.x.scales;
+        int64_t xr = a.x.rows;
+        if constexpr (MODE == kDense) {
+            cx += t.m0 * a.x.code_stride;
+            sx += t.m0 * a.x.scale_stride;
+            xr = t.count;
+        } else {
+            list = a.plan + moe_plan_list(a.E) + t.m0;
+        }
+        xc = buffer(cx, xr * a.x.code_stride);
+        xs = buffer(sx, xr * a.x.scale_stride);
+        const int64_t row0 = (MODE == kDense ? 0 : t.expert * a.w_rows) + t.n0;
+        const int64_t rows = MODE == kUp ? a.w_rows - t.n0 : w_rows;
+        wc = buffer(a.w.codes + row0 * a.w.code_stride, rows * a.w.code_stride);
+        ws = buffer(a.w.scales + row0 * a.w.scale_stride, rows * a.w.scale_stride);
+    }
+    __device__ __forceinline__ uint32_t x_row(int i) const {
+        i = min(i, x_rows - 1);
+        if constexpr (MODE == kDense) return (uint32_t)i;
+        if constexpr (MODE == kUp) return (uint32_t)list[i] / (uint32_t)top_k;
+        return (uint32_t)list[i];
+    }
+    // column c of the tile, of the gate or the up rows
+    __device__ __forceinline__ uint32_t w_row(int c, bool second) const {
+        c = min(c, w_rows - 1);
+        return (uint32_t)(MODE == kUp && second ? c + up : c);
+    }
+};
+
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)dst, 16, (int)voff, (int)soff, 0, 0);
+}
+__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t voff, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)dst, 4, (int)voff, (int)soff, 0, 0);
+}
+
+__device__ __forceinline__ int slot_of(int row, int piece) { return piece ^ ((row >> 1) & 7); }
+
+// The last line of a row, in LDS: groups past the end of scale 1, codes past the end 0 (X).  valid: inputs of the line.
+__device__ __forceinline__ void end_scales(uint8_t* s, int valid) {
+    const int groups = (valid + kGroup - 1) / kGroup;
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+        if (b >= groups) s[b] = 127;
+}
+__device__ __forceinline__ void end_codes(uint8_t* line, int row, int valid) {
+    for (int p = valid / kGroup; p < 8; ++p) {
+        v4i_t* at = reinterpret_cast<v4i_t*>(line + 16 * slot_of(row, p));
+        v4i_t v = *at;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int left = valid - kGroup * p - 8 * d;             // codes of this dword that count
+            v[d] = left >= 8 ? v[d] : left <= 0 ? 0 : (int)((uint32_t)v[d] & ((1u << (4 * left)) - 1u));
+        }
+        *at = v;
+    }
+}
+
+__device__ __forceinline__ v8i_t wide(v4i_t v) { return (v8i_t){v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+template <int S>
+__device__ __forceinline__ floatx4_t mfma(v4i_t w, int ws, v4i_t x, int xs, floatx4_t c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w), wide(x), c, 4, 4, S, ws, S, xs);
+}
+
+// Four consecutive outputs, those of them below `left`.
+__device__ __forceinline__ void store4(void* y, int32_t dtype, int64_t at, floatx4_t v, int64_t left) {
+    if (dtype == QK_F32) {
+        float* p = static_cast<float*>(y) + at;
+        if (left >= 4) {
+            __builtin_memcpy(p, &v, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) p[i] = v[i];
+        }
+    } else {
+        u32x2_t d;
+        typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+        if (dtype == QK_BF16) d = (u32x2_t){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        else d = (u32x2_t){__builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)v[0], (_Float16)v[1]}),
+                           __builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)v[2], (_Float16)v[3]})};
+        uint16_t* p = static_cast<uint16_t*>(y) + at;
+        if (left >= 4) {
+            __builtin_memcpy(p, &d, 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) p[i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
+        }
+    }
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+// Outputs of one wave: acc[i][j], rows 16 i + lane % 16 of the wave's rows m, columns 16 j + 4 (lane / 16) + q of its n
+// (up: the second half of the j are the up products of the first).
+template <Mode MODE, int MT, int RT>
+__device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, int m, int n, floatx4_t (&acc)[MT][RT]) {
+    const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+    constexpr int kCols = MODE == kUp ? RT / 2 : RT;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int pos = m + 16 * i + r;
+        if (pos >= t.count) continue;
+        int64_t row;
+        float wt = 1.0f;
+        if constexpr (MODE == kDense) {
+            row = t.m0 + pos;
+        } else {
+            row = a.plan[moe_plan_list(a.E) + t.m0 + pos];
+            if constexpr (MODE == kDown) wt = t.expert < a.E ? a.weights[row] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+            const int64_t col = t.n0 + n + 16 * j + 4 * h;
+            if (col >= a.N) continue;
+            floatx4_t v = acc[i][j];
+            if constexpr (MODE == kUp) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = silu(v[q]) * acc[i][j + RT / 2][q];
+            }
+            if constexpr (MODE == kDown) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] *= wt;
+            }
+            store4(a.y, MODE == kDown ? QK_F32 : a.y_dtype, row * a.N + col, v, a.N - col);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: tiles of BM x BN, waves of WM x WN, two stages of LDS.  Up: columns [0, WN / 2) of a wave are gate rows,
+// the others their up rows.
+// ---------------------------------------------------------------------------
+template <Mode MODE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(GemmArgs a) {
+    constexpr int kWaves = (BM / WM) * (BN / WN), kThreads = kWaves * 64;
+    constexpr int kLines = BM + BN;
+    constexpr int MT = WM / 16, RT = WN / 16;
+    constexpr int kLoads = kLines / 8 / kWaves, kXLoads = BM / 8 / kWaves;      // of codes, per wave
+    constexpr int kSLoads = (kLines / 32 + kWaves - 1) / kWaves;                // of scales
+    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && kLines % (32 * kWaves) == 0);
+    static_assert(BM % 32 == 0);
+    constexpr int kBNo = MODE == kUp ? BN / 2 : BN;
+    // rows of X, then rows of W, 128 bytes each; then their scales, 8 bytes each
+    __shared__ __align__(16) uint8_t lds0[kLines * 136];
+    __shared__ __align__(16) uint8_t lds1[kLines * 136];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / (BN / WN), wn = wave % (BN / WN);
+    const int r = lane & 15, h = lane >> 4;
+    const Tile t = MODE == kDense ? dense_tile<BM, BN>(a) : expert_tile<BM, kBNo>(a);
+    if (t.count <= 0) return;
+    floatx4_t acc[MT][RT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
+
+    if (MODE == kDense || t.expert < a.E) {
+        const Operands<MODE> op(a, t);
+        auto w_row = [&](int b) {                       // row b of the tile's W lines
+            const int q = b % WN;
+            return MODE == kUp ? op.w_row(b / WN * (WN / 2) + q % (WN / 2), q >= WN / 2) : op.w_row(b, false);
+        };
+        // what this lane copies: row l / 8 of 8, slot l % 8
+        uint32_t voff[kLoads], soff[kSLoads];
+#pragma unroll
+        for (int v = 0; v < kLoads; ++v) {
+            const int line = 8 * (wave + kWaves * v) + (lane >> 3), piece = slot_of(line, lane & 7);
+            voff[v] = v < kXLoads ? op.x_row(line) * (uint32_t)a.x.code_stride + 16 * piece
+                                  : w_row(line - BM) * (uint32_t)a.w.code_stride + 16 * piece;
+        }
+#pragma unroll
+        for (int v = 0; v < kSLoads; ++v) {
+            const int line = 32 * (wave + kWaves * v) + (lane >> 1);
+            soff[v] = 4 * (lane & 1) + (line < BM ? op.x_row(line) * (uint32_t)a.x.scale_stride
+                                                  : w_row(line - BM) * (uint32_t)a.w.scale_stride);
+        }
+        const int nst = (a.x.cols + kLineK - 1) / kLineK;
+        auto load = [&](uint8_t* dst, int st) {
+#pragma unroll
+            for (int v = 0; v < kLoads; ++v)
+                to_lds(v < kXLoads ? op.xc : op.wc, dst + (wave + kWaves * v) * 1024, voff[v], 128u * st);
+#pragma unroll
+            for (int v = 0; v < kSLoads; ++v) {
+                const bool x = 32 * (wave + kWaves * v) < BM;
+                to_lds4(x ? op.xs : op.ws, dst + kLines * 128 + (wave + kWaves * v) * 256, soff[v], 8u * st);
+            }
+        };
+        const int xline = (wm * WM + r) * 128, wline = (BM + wn * WN + r) * 128;
+        const int xsc = kLines * 128 + (wm * WM + r) * 8 + 2 * h, wsc = kLines * 128 + (BM + wn * WN + r) * 8 + 2 * h;
+        auto compute = [&](const uint8_t* src) {
+            int xs[MT], ws[RT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) xs[i] = *reinterpret_cast<const uint16_t*>(src + xsc + 128 * i);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) ws[j] = *reinterpret_cast<const uint16_t*>(src + wsc + 128 * j);
+            auto half = [&](auto S) {
+                constexpr int s = decltype(S)::value;
+                const int at = 16 * slot_of(r, 2 * h + s);
+                v4i_t x[MT], w[RT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) x[i] = *reinterpret_cast<const v4i_t*>(src + xline + at + 2048 * i);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) w[j] = *reinterpret_cast<const v4i_t*>(src + wline + at + 2048 * j);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) acc[i][j] = mfma<s>(w[j], ws[j], x[i], xs[i], acc[i][j]);
+            };
+            half(std::integral_constant<int, 0>{});
+            half(std::integral_constant<int, 1>{});
+        };
+        const int valid = a.x.cols - (nst - 1) * kLineK;              // inputs of the last line
+        // the stage that was loaded is in LDS, and every wave is done with the other one
+        auto landed = [&] {
+            __builtin_amdgcn_s_waitcnt(0);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        };
+        auto finish = [&](uint8_t* dst) {
+            for (int l = tid; l < kLines; l += kThreads) {
+                end_scales(dst + kLines * 128 + 8 * l, valid);
+                if (l < BM) end_codes(dst + 128 * l, l, valid);
+            }
+            __syncthreads();
+        };
+        load(lds0, 0);
+        landed();
+        int st = 0;
+        for (; st + 2 < nst; st += 2) {
+            load(lds1, st + 1);
+            compute(lds0);
+            landed();
+            load(lds0, st + 2);
+            compute(lds1);
+            landed();
+        }
+        if (st + 1 < nst) {
+            load(lds1, st + 1);
+            compute(lds0);
+            landed();
+            if (valid < kLineK) finish(lds1);
+            compute(lds1);
+        } else {
+            if (valid < kLineK) finish(lds0);
+            compute(lds0);
+        }
+    }
+    store_outputs<MODE>(a, t, wm * WM, MODE == kUp ? wn * (WN / 2) : wn * WN, acc);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: a workgroup makes 16 MT rows x 16 RT lines of W, its waves take every kWaves-th line of inputs and their sums
+// meet in LDS, added in wave order.  A wave has three stages of its own and waits for nobody in the loop.
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 4;
+
+template <Mode MODE, int MT, int RT>
+__global__ __launch_bounds__(kFewWaves * 64) void mx4_few_kernel(GemmArgs a) {
+    constexpr int kLines = 16 * (MT + RT);
+    constexpr int kStage = kLines * 128 + (kLines + 31) / 32 * 256;
+    constexpr int kLoads = 2 * (MT + RT), kSLoads = (kLines + 31) / 32;
+    constexpr int kBNo = MODE == kUp ? 8 * RT : 16 * RT;
+    constexpr int kSum = MT * RT * 1024;                // bytes of a wave's sums
+    static_assert(kSum <= kStage);
+    __shared__ __align__(16) uint8_t lds0[kFewWaves * kStage];
+    __shared__ __align__(16) uint8_t lds1[kFewWaves * kStage];
+    __shared__ __align__(16) uint8_t lds2[kFewWaves * kStage];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, h = lane >> 4;
+    const Tile t = MODE == kDense ? dense_tile<16 * MT, kBNo>(a) : expert_tile<16 * MT, kBNo>(a);
+    if (t.count <= 0) return;
+    floatx4_t acc[MT][RT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
+
+    if (MODE == kDense || t.expert < a.E) {
+        const Operands<MODE> op(a, t);
+        auto w_row = [&](int b) { return MODE == kUp ? op.w_row(b % (8 * RT), b >= 8 * RT) : op.w_row(b, false); };
+        uint32_t voff[kLoads], soff[kSLoads];
+#pragma unroll
+        for (int v = 0; v < kLoads; ++v) {
+            const int line = 8 * v + (lane >> 3), piece = slot_of(line, lane & 7);
+            voff[v] = v < 2 * MT ? op.x_row(line) * (uint32_t)a.x.code_stride + 16 * piece
+                                 : w_row(line - 16 * MT) * (uint32_t)a.w.code_stride + 16 * piece;
+        }
+        // scales: 32 lines an instruction, or two with half the lanes each where the first 16 are of X
+#pragma unroll
+        for (int v = 0; v < kSLoads; ++v) {
+            const int line = 32 * v + (lane >> 1);
+            soff[v] = 4 * (lane & 1) + (line < 16 * MT ? op.x_row(line) * (uint32_t)a.x.scale_stride
+                                                       : w_row(line - 16 * MT) * (uint32_t)a.w.scale_stride);
+        }
+        const int nst = (a.x.cols + kLineK - 1) / kLineK;
+        auto load = [&](uint8_t* ring, int st) {
+            uint8_t* dst = ring + wave * kStage;
+            // past the row every offset is outside its buffer, and nothing is read (loads under a condition would leave the
+            // waits below without a count)
+            const uint32_t out = st < nst ? 0u : 0xFFFF0000u, c = st < nst ? 128u * st : 0u, s = st < nst ? 8u * st : 0u;
+#pragma unroll
+            for (int v = 0; v < kLoads; ++v) to_lds(v < 2 * MT ? op.xc : op.wc, dst + v * 1024, voff[v] | out, c);
+#pragma unroll
+            for (int v = 0; v < kSLoads; ++v) {
+                const int first = 32 * v;                             // lines of X come first, 16 MT of them
+                uint8_t* to = dst + kLines * 128 + v * 256;
+                if (first + 32 <= 16 * MT) to_lds4(op.xs, to, soff[v] | out, s);
+                else if (first >= 16 * MT) to_lds4(op.ws, to, soff[v] | out, s);
+                else if (lane < 32) to_lds4(op.xs, to, soff[v] | out, s);
+                else to_lds4(op.ws, to, soff[v] | out, s);
+            }
+        };
+        auto compute = [&](const uint8_t* ring) {
+            const uint8_t* src = ring + wave * kStage;
+            int xs[MT], ws[RT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) xs[i] = *reinterpret_cast<const uint16_t*>(src + kLines * 128 + (16 * i + r) * 8 + 2 * h);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) ws[j] = *reinterpret_cast<const uint16_t*>(src + kLines * 128 + (16 * (MT + j) + r) * 8 + 2 * h);
+            auto half = [&](auto S) {
+                constexpr int s = decltype(S)::value;
+                const int at = r * 128 + 16 * slot_of(r, 2 * h + s);
+                v4i_t x[MT], w[RT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) x[i] = *reinterpret_cast<const v4i_t*>(src + at + 2048 * i);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) w[j] = *reinterpret_cast<const v4i_t*>(src + at + 2048 * (MT + j));
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) acc[i][j] = mfma<s>(w[j], ws[j], x[i], xs[i], acc[i][j]);
+            };
+            half(std::integral_constant<int, 0>{});
+            half(std::integral_constant<int, 1>{});
+        };
+        const int valid = a.x.cols - (nst - 1) * kLineK;
+        // the last line of a row, by the wave that has it
+        auto finish = [&](uint8_t* ring) {
+            uint8_t* dst = ring + wave * kStage;
+            for (int l = lane; l < kLines; l += 64) {
+                end_scales(dst + kLines * 128 + 8 * l, valid);
+                if (l < 16 * MT) end_codes(dst + 128 * l, l, valid);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+        load(lds0, wave);
+        load(lds1, wave + kFewWaves);
+        auto step = [&](uint8_t* cur, uint8_t* next, int st) {
+            load(next, st + 2 * kFewWaves);
+            constexpr int kInFlight = 2 * (kLoads + kSLoads + (MT & 1));   // stages st + 1, st + 2
+            __builtin_amdgcn_s_waitcnt((kInFlight & 15) | ((kInFlight >> 4) << 14) | 0x0F70);
+            asm volatile("" ::: "memory");
+            if (st == nst - 1 && valid < kLineK) finish(cur);
+            compute(cur);
+        };
+        int st = wave;
+        for (; st + 2 * kFewWaves < nst; st += 3 * kFewWaves) {
+            step(lds0, lds2, st);
+            step(lds1, lds0, st + kFewWaves);
+            step(lds2, lds1, st + 2 * kFewWaves);
+        }
+        if (st < nst) step(lds0, lds2, st);
+        if (st + kFewWaves < nst) step(lds1, lds0, st + kFewWaves);
+        __builtin_amdgcn_s_waitcnt(0);                                // nothing on its way to LDS any more
+        __syncthreads();
+        // wave w adds up and stores columns w, w + kFewWaves, ... of the 16 x 16 blocks
+        float* sums = reinterpret_cast<float*>(lds0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+                *reinterpret_cast<floatx4_t*>(sums + wave * (kSum / 4) + ((i * RT + j) * 64 + lane) * 4) = acc[i][j];
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+#pragma unroll
+                for (int o = 1; o < kFewWaves; ++o)
+                    acc[i][j] += *reinterpret_cast<const floatx4_t*>(sums + o * (kSum / 4) + ((i * RT + j) * 64 + lane) * 4);
+            }
+    }
+    if (wave > 0) return;
+    store_outputs<MODE>(a, t, 0, 0, acc);
+}
+
+// ---------------------------------------------------------------------------
+// The parts of each token's slots added in order.
+// ---------------------------------------------------------------------------
+constexpr int kCombineThreads = 256;
+
+__global__ __launch_bounds__(kCombineThreads) void moe_combine_mx4_kernel(const float* __restrict__ part, void* y, int32_t dtype,
+                                                                          int64_t T, int32_t top_k, int64_t H) {
+    const int64_t quads = (H + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
+    const int64_t tok = i / quads, col = (i - tok * quads) * 4;
+    if (tok >= T) return;
+    const int64_t left = H - col;
+    floatx4_t sum = {0, 0, 0, 0};
+    for (int32_t j = 0; j < top_k; ++j) {
+        const float* p = part + (tok * top_k + j) * H + col;
+        floatx4_t v = {0, 0, 0, 0};
+        if (left >= 4) {
+            __builtin_memcpy(&v, p, 16);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < left) v[q] = p[q];
+        }
+        sum += v;
+    }
+    store4(y, dtype, tok * H + col, sum, left);
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Workgroups of a launch of BM x BNo tiles.
+template <Mode MODE>
+int64_t grid_for(const GemmArgs& a, int64_t bm, int64_t bno) {
+    if (MODE == kDense) return cdiv(a.M, bm) * cdiv(a.N, bno);
+    // an expert's last tile may be partial
+    return (a.slots / bm + std::min<int64_t>(a.E + 1, a.slots)) * cdiv(a.N, bno);
+}
+
+template <Mode MODE, int BM, int BN, int WM, int WN>
+hipError_t launch_tile(const GemmArgs& a, hipStream_t s) {
+    const int64_t grid = grid_for<MODE>(a, BM, MODE == kUp ? BN / 2 : BN);
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    mx4_tile_kernel<MODE, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3((BM / WM) * (BN / WN) * 64), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <Mode MODE, int MT, int RT>
+hipError_t launch_few(const GemmArgs& a, hipStream_t s) {
+    const int64_t grid = grid_for<MODE>(a, 16 * MT, MODE == kUp ? 8 * RT : 16 * RT);
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    mx4_few_kernel<MODE, MT, RT><<<dim3((unsigned)grid), dim3(kFewWaves * 64), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <Mode MODE>
+hipError_t launch_any(const GemmArgs& a, hipStream_t s) {
+    // rows that meet a weight: of the product, or of an expert on average
+    const int64_t rows = MODE == kDense ? a.M : cdiv(a.slots, std::min<int64_t>(a.E, a.slots));
+    if (rows <= 16) return launch_few<MODE, 1, 2>(a, s);
+    if (rows <= 32) return launch_few<MODE, 2, 2>(a, s);
+    if (rows <= 64) return launch_few<MODE, 4, 2>(a, s);
+    if (grid_for<MODE>(a, 256, MODE == kUp ? 128 : 256) < device_cu_count()) return launch_tile<MODE, 128, 128, 64, 64>(a, s);
+    return launch_tile<MODE, 256, 256, 128, 128>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_gemm(const qk_mx4_state* x, const qk_mx4_state* w, void* y, int32_t y_dtype, hipStream_t s) {
+    GemmArgs a{};
+    a.x = view(x);
+    a.w = view(w);
+    a.y = y;
+    a.y_dtype = y_dtype;
+    a.M = x->rows;
+    a.N = w->rows;
+    a.w_rows = w->rows;
+    return launch_any<kDense>(a, s);
+}
+
+namespace {
+GemmArgs expert_args(const qk_mx4_state* x, const qk_mx4_state* w, const int32_t* plan, int32_t top_k, int32_t E) {
+    GemmArgs a{};
+    a.x = view(x);
+    a.w = view(w);
+    a.plan = plan;
+    a.top_k = top_k;
+    a.E = E;
+    a.w_rows = w->rows / E;
+    return a;
+}
+}  // namespace
+
+hipError_t launch_moe_up_mx4(const qk_mx4_state* x, const qk_mx4_state* gate_up, const int32_t* plan, int32_t top_k,
+                             int32_t E, void* h, int32_t h_dtype, hipStream_t s) {
+    GemmArgs a = expert_args(x, gate_up, plan, top_k, E);
+    a.slots = (int32_t)(x->rows * top_k);
+    a.y = h;
+    a.y_dtype = h_dtype;
+    a.N = a.w_rows / 2;
+    return launch_any<kUp>(a, s);
+}
+
+size_t moe_down_mx4_workspace_bytes(int64_t T, int32_t top_k, int64_t H) { return (size_t)(T * top_k) * (size_t)H * 4; }
+
+hipError_t launch_moe_down_mx4(const qk_mx4_state* h, const qk_mx4_state* down, const int32_t* plan, const float* weights,
+                               int32_t top_k, int32_t E, void* y, int32_t y_dtype, void* workspace, hipStream_t s) {
+    GemmArgs a = expert_args(h, down, plan, top_k, E);
+    a.slots = (int32_t)h->rows;
+    a.y = workspace;
+    a.weights = weights;
+    a.N = a.w_rows;
+    const hipError_t e = launch_any<kDown>(a, s);
+    if (e != hipSuccess) return e;
+    const int64_t T = h->rows / top_k, threads = T * ((a.N + 3) / 4), grid = cdiv(threads, kCombineThreads);
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    moe_combine_mx4_kernel<<<dim3((unsigned)grid), dim3(kCombineThreads), 0, s>>>(static_cast<const float*>(workspace), y,
+                                                                                y_dtype, T, top_k, a.N);
+    return hipGetLastError();
+}
+
+}  // namespace qk

@@ -1,0 +1,138 @@
+// Decode product of 16-bit activations with a microscaled 4-bit weight, for gfx950:
+//     y[m, n] = sum_k x[m, k] value(code[n, k]) 2^(e[n, k / 32] - 127),   m < M <= 16
+// A workgroup (8 waves, two per CU) owns a run of rows and walks it with RowTiles (w4_tile.h), the codes and scales of the
+// next rows being loaded while some are multiplied.  Bound by the bytes of the codes.
+#include <algorithm>
+
+#include "qk_device.h"
+#include "qk_internal.h"
+#include "w4_tile.h"
+
+namespace qk {
+namespace {
+
+using namespace w4;
+
+constexpr int kThreads = 512;
+
+struct GemvArgs {
+    const uint16_t* x;       // [M, K]
+    uint16_t* y;             // [M, N]
+    Mx4View w;
+    int64_t N;
+    int32_t K;
+    int32_t M;
+    int32_t x_aligned;       // rows of x start at 4-byte boundaries and K % 8 == 0
+    int32_t kwl;             // log2 of the waves that split a row
+    int32_t share, more;     // items per workgroup; the first `more` workgroups take one more
+};
+
+constexpr int groups_for(int f) { return f == kMx4F16 ? 4 : 1; }
+
+template <int F, int RT, int MI, bool kResident>
+__global__ __launch_bounds__(kThreads, 4) void mx4_gemv_kernel(GemvArgs a) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    typedef RowTiles<F, groups_for(F), RT, MI, kResident, false> Tiles;
+    const int b = (int)blockIdx.x;
+    Rows<RT> p;
+    p.kwl = a.kwl;
+    p.group_step = 16 * RT;
+    p.step = (16 * RT * 8) >> a.kwl;
+    const int64_t row0 = (int64_t)p.step * ((int64_t)b * a.share + (b < a.more ? b : a.more));
+    const int items = a.share + (b < a.more);
+    const int64_t row1 = row0 + (int64_t)p.step * items;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        p.base[r] = row0;
+        p.off[r] = 16 * r;
+    }
+    p.count = (int32_t)((row1 < a.N ? row1 : a.N) - row0);
+    p.x = a.x;
+    p.xrow = nullptr;
+    p.K = a.K;
+    p.x_pitch = a.K;
+    p.x_rows = a.M;
+    p.x_aligned = a.x_aligned;
+    p.M = a.M;
+    Tiles::run(a.w, p, 0, items, lds, [&](int item, int q, const float* put) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int o = 64 * i + (threadIdx.x & 63), m = Tiles::act_of(o);
+                const int j = item * p.step + q * (16 * RT) + 16 * r + (o & 15);
+                const float v = Tiles::sum(put, a.kwl, q, r, o);
+                if (m < a.M && j < p.count) a.y[m * a.N + row0 + j] = float_to_bits16(v, F == kMx4F16);
+            }
+    });
+}
+
+// Registers of a product that carry activations: the least that hold M rows.
+constexpr int mi_for(int M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
+
+size_t lds_bytes(Form f, int M, int rt, int64_t K, bool resident) {
+    const int mi = mi_for(M), kw = 1 << w4_most_kwl(f, mi);
+    return w4_fixed_bytes(f, groups_for(f), rt, mi, resident) + w4_x_bytes(f, kw, M, mi, false, K, resident);
+}
+
+template <int F, int RT, int MI, bool kResident>
+hipError_t launch(const GemvArgs& a, int64_t grid, size_t lds, hipStream_t s) {
+    constexpr auto kernel = &mx4_gemv_kernel<F, RT, MI, kResident>;
+    const hipError_t e = allow_lds<kernel>(lds);
+    if (e != hipSuccess) return e;
+    kernel<<<dim3((unsigned)grid), dim3(kThreads), lds, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int F, int RT, int MI>
+hipError_t launch(const GemvArgs& a, int64_t grid, size_t lds, bool resident, hipStream_t s) {
+    return resident ? launch<F, RT, MI, true>(a, grid, lds, s) : launch<F, RT, MI, false>(a, grid, lds, s);
+}
+
+template <int F>
+hipError_t launch_form(GemvArgs& a, hipStream_t s) {
+    const int mi = mi_for(a.M), most_kwl = w4_most_kwl((Form)F, mi);
+    // offsets of 32 bits: the bytes of a row's codes or scales, whichever are more
+    const int64_t pitch = std::max<int64_t>(a.w.stride, a.w.scale_stride);
+    a.kwl = w4_kwl((Form)F, a.K, a.N, 16, most_kwl);
+    while (a.kwl < most_kwl && (256 >> a.kwl) * pitch > 1 << 30) ++a.kwl;
+    const int64_t pairs = (a.N + (256 >> a.kwl) - 1) / (256 >> a.kwl);
+    // Two tiles of 16 rows per item, which bring more codes on their way at a time, where every workgroup has an item of
+    // two, and one where not and above four rows, as for int4.
+    const int rt = mi == 1 && pairs > 2 * (int64_t)device_cu_count() ? 2 : 1;
+    // the activations of a whole row stay in LDS where they fit, above four rows where they leave room for a second
+    // workgroup (an output's bits do not depend on it)
+    const bool resident = lds_bytes((Form)F, a.M, rt, a.K, true) <= (a.M > 4 ? kLdsBytes / 2 : kLdsBytes);
+    const size_t lds = lds_bytes((Form)F, a.M, rt, a.K, resident);
+    const int64_t slots = (lds > kLdsBytes / 2 ? 1 : 2) * (int64_t)device_cu_count();
+    const int64_t step = (128 * rt) >> a.kwl, items = (a.N + step - 1) / step;
+    const int64_t per = (items + slots - 1) / slots;
+    int64_t wgs = (items + per - 1) / per;
+    // a workgroup's rows stay under 2^29 bytes and one item more, of 2^30 at most
+    wgs = std::max(wgs, std::min(items, (int64_t)((double)items * (double)(step * pitch) / (1 << 29)) + 1));
+    a.share = (int32_t)(items / wgs);
+    a.more = (int32_t)(items % wgs);
+    if (mi == 4) return launch<F, 1, 4>(a, wgs, lds, resident, s);
+    if (mi == 2) return launch<F, 1, 2>(a, wgs, lds, resident, s);
+    return rt == 1 ? launch<F, 1, 1>(a, wgs, lds, resident, s) : launch<F, 2, 1>(a, wgs, lds, resident, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_gemv(const void* x, int32_t M, const qk_mx4_state* w, void* y, bool f16, hipStream_t s) {
+    GemvArgs a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.y = static_cast<uint16_t*>(y);
+    a.w.codes = w->codes;
+    a.w.scales = w->scales;
+    a.w.stride = w->code_stride;
+    a.w.scale_stride = (int32_t)w->scale_stride;
+    a.w.G = (int32_t)((w->cols + 31) / 32);
+    a.N = w->rows;
+    a.K = (int32_t)w->cols;
+    a.M = M;
+    a.x_aligned = w->cols % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 4 == 0;
+    return f16 ? launch_form<kMx4F16>(a, s) : launch_form<kMx4Bf16>(a, s);
+}
+
+}  // namespace qk

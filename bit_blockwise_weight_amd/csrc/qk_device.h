@@ -62,4 +62,20 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t v) {
     return v;
 }
 
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp_from(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, kCtrl, kRows, 0xF, false);
+}
+// Inclusive prefix sum over the wave: shifts inside the rows of 16 lanes, then the last lane of row 0 and 2 added to
+// rows 1 and 3, and lane 31 to the upper half.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp_from<0x111, 0xF>(v);
+    v += dpp_from<0x112, 0xF>(v);
+    v += dpp_from<0x114, 0xF>(v);
+    v += dpp_from<0x118, 0xF>(v);
+    v += dpp_from<0x142, 0xA>(v);
+    v += dpp_from<0x143, 0xC>(v);
+    return v;
+}
+
 }  // namespace qk

@@ -224,4 +224,42 @@ hipError_t launch_moe_int4(const MoeItem& m, const qk_int4_state* gate_up, const
 hipError_t launch_moe_levels(const MoeItem& m, const MatArgs& gate_up, const MatArgs& down, void* workspace,
                              hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// Microscaled 4-bit matrices, and the routing of a mixture-of-experts layer for any number of tokens
+// ---------------------------------------------------------------------------
+hipError_t launch_mx4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t pitch, uint8_t* codes,
+                               int64_t code_stride, uint8_t* scales, int64_t scale_stride, hipStream_t s);
+hipError_t launch_mx4_dequantize(const qk_mx4_state* st, void* out, int32_t out_dtype, hipStream_t s);
+hipError_t launch_mx4_gemm(const qk_mx4_state* x, const qk_mx4_state* w, void* y, int32_t y_dtype, hipStream_t s);
+hipError_t launch_mx4_gemv(const void* x, int32_t M, const qk_mx4_state* w, void* y, bool f16, hipStream_t s);
+
+struct MoeRouteArgs {
+    const void* logits;       // [T, E]
+    const float* bias;        // [E] or NULL
+    int32_t* ids;             // [T, top_k]
+    float* weights;
+    int64_t T;
+    int32_t dtype, E, score, groups, top_groups, top_k, renorm;
+    float scale;
+};
+hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s);
+struct MoeRouteBackwardArgs {
+    const void* logits;
+    const int32_t* ids;
+    const float* dweights;
+    void* dlogits;
+    int64_t T;
+    int32_t dtype, E, score, top_k, renorm;
+    float scale;
+};
+hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs& a, hipStream_t s);
+// Plan: E + 1 first places, padded to a multiple of 4, then the slots.
+constexpr int64_t moe_plan_list(int32_t E) { return (int64_t)(E + 4) / 4 * 4; }
+hipError_t launch_moe_plan(const int32_t* ids, int64_t slots, int32_t E, int32_t* plan, hipStream_t s);
+hipError_t launch_moe_up_mx4(const qk_mx4_state* x, const qk_mx4_state* gate_up, const int32_t* plan, int32_t top_k,
+                             int32_t E, void* h, int32_t h_dtype, hipStream_t s);
+size_t moe_down_mx4_workspace_bytes(int64_t T, int32_t top_k, int64_t H);
+hipError_t launch_moe_down_mx4(const qk_mx4_state* h, const qk_mx4_state* down, const int32_t* plan, const float* weights,
+                               int32_t top_k, int32_t E, void* y, int32_t y_dtype, void* workspace, hipStream_t s);
+
 }  // namespace qk

@@ -30,6 +30,11 @@
 //
 // 16 levels: codes become levels by a table in LDS of all 256 bytes.  A level is its bf16 copy times the power of two that
 // brings the largest of the table to 2^14, as fp16: exact down to 2^-31 of the largest.
+//
+// Microscaled e2m1 (mx4.h): times bf16, the scaled conversion makes a weight with its scale, exact in bf16, and nothing is
+// left to do after the product; activations are taken as they are, k in any order (a lane holds 32 k of one group).  Times
+// fp16, whose range does not hold the scales, the bare e2m1 values are converted and a group's sum is scaled, as for int4
+// in groups of 32.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -51,8 +56,11 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x3_t __attribute__((ext_vector_type(3)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// Weight forms of the kernels: int4 times bf16 or fp16 activations, 16 levels times bf16.
-enum Form { kInt4Bf16 = 0, kInt4F16 = 1, kLevels = 2 };
+// Weight forms of the kernels: int4 times bf16 or fp16 activations, 16 levels times bf16, microscaled e2m1 times bf16 or
+// fp16.
+enum Form { kInt4Bf16 = 0, kInt4F16 = 1, kLevels = 2, kMx4Bf16 = 3, kMx4F16 = 4 };
+constexpr bool is_int4(int f) { return f == kInt4Bf16 || f == kInt4F16; }
+constexpr bool is_mx4(int f) { return f == kMx4Bf16 || f == kMx4F16; }
 
 constexpr int kChunk = 128;               // k per step of a wave
 
@@ -134,6 +142,28 @@ __device__ __forceinline__ floatx4_t mfma(u32x4_t a, u32x4_t b, floatx4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ floatx4_t mfma_bf16(u32x4_t a, u32x4_t b, floatx4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+// Eight e2m1 codes of a dword in their order: times a scale as bf16, or by themselves as fp16.
+__device__ __forceinline__ u32x4_t decode8_mx4(uint32_t w, float scale) {
+    u32x4_t f;
+    f[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+    f[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+    f[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+    f[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+    return f;
+}
+__device__ __forceinline__ u32x4_t decode8_mx4(uint32_t w) {
+    u32x4_t f;
+    f[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
+    f[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
+    f[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
+    f[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
+    return f;
+}
+
 // One int4 weight as the kernels see it.
 struct Int4View {
     const uint8_t* codes;     // [rows, stride], 16-byte aligned
@@ -144,6 +174,15 @@ struct Int4View {
     int32_t gshift;           // log2 of the group size (>= 5); 30: one group
     int32_t scale_f16;        // 1: fp16 scales, 0: bf16
     int32_t pad;
+};
+
+// A microscaled weight as the kernels see it.
+struct Mx4View {
+    const uint8_t* codes;     // [rows, stride], 16-byte aligned
+    const uint8_t* scales;    // [rows, scale_stride], 4-byte aligned, scale_stride % 4 == 0
+    int64_t stride;
+    int32_t scale_stride;
+    int32_t G;                // groups of a row
 };
 
 // A 16-level weight (NF4 and the like) as the kernels see it: rows of K elements, K a multiple
@@ -258,7 +297,7 @@ constexpr int w4_put_bytes(Form f, int RT, int MI) { return w4_waves(f) * RT * 6
 constexpr int w4_slots(Form f, int RT, int MI, bool resident) {
     return resident || f == kLevels ? 2 : RT == 2 ? 3 : MI == 4 ? 2 : 4;
 }
-constexpr int w4_scale_bytes(Form f, int NG, int RT) { return w4_waves(f) * RT * 16 * ((2 * NG) | 1) * (f == kLevels ? 4 : 8); }
+constexpr int w4_scale_bytes(Form f, int NG, int RT) { return w4_waves(f) * RT * 16 * ((2 * NG) | 1) * (is_int4(f) ? 8 : 4); }
 // log2 of the waves that split a row, at most: a window of the activations has to fit where these do not stay
 constexpr int w4_most_kwl(Form f, int MI) { return f == kLevels || MI == 4 ? 2 : 3; }
 constexpr int w4_code_bytes(int RT) { return 8 * RT * 16 * 128; }       // of 8 waves; 8 more have theirs beside the table
@@ -283,8 +322,8 @@ hipError_t allow_lds(size_t lds) {
     return e;
 }
 
-// Whether activations are scaled chunk by chunk: fp16 ones are what the product takes.
-constexpr bool w4_scaled(Form f, bool split) { return split || f != kInt4F16; }
+// Whether activations are scaled chunk by chunk: not where they are what the product takes.
+constexpr bool w4_scaled(Form f, bool split) { return split || f == kInt4Bf16 || f == kLevels; }
 // bytes of LDS that the activations take: rows of 16-bit values (two an activation with kSplit), and the factors of the
 // chunks for the 4 mi rows of the operand
 inline size_t w4_x_bytes(Form f, int kw, int rows, int mi, bool split, int64_t K, bool resident) {
@@ -334,10 +373,11 @@ struct RowTiles {
         float s;
         uint32_t zero;       // -(1024 + z) in fp16, twice
     };
-    typedef std::conditional_t<F == kLevels, float, ScaleZero> Scale;
+    // (kMx4Bf16: the scale bytes of a chunk's four groups)
+    typedef std::conditional_t<is_int4(F), ScaleZero, std::conditional_t<F == kMx4Bf16, uint32_t, float>> Scale;
     struct Fetched {
         u32x4_t c[RT][2];
-        u32x4_t s;           // int4: 2 NG scales; levels: four block scales of a plain weight
+        u32x4_t s;           // int4: 2 NG scales; levels: four block scales of a plain weight; mx4: eight scales
         uint32_t s4;         // int4 with NG = 4: the fifth dword
         u32x3_t z;           // int4: 2 NG zero points; levels: q8 of four blocks
         u32x2_t d;           // levels: double-quantization scales of the first block and of the next 256
@@ -372,7 +412,7 @@ struct RowTiles {
         float mean = 0.0f;
         uint32_t zbase = 0;                                      // -1024 in fp16, and the zero point where there is no array
         if constexpr (F == kLevels) mean = w.nested ? *w.dq_mean : 0.0f;
-        else zbase = 0xE400u + (w.zeros ? 0u : 8u);
+        if constexpr (is_int4(F)) zbase = 0xE400u + (w.zeros ? 0u : 8u);
         // Staging of activations, thread by thread, rows as if they had 2^ush units of 8 values.  A unit is read
         // as four dwords from an address rounded down to 4 bytes, and one dword more where rows may start
         // between dwords, and put right (and zero past K) when it is stored.
@@ -463,7 +503,7 @@ struct RowTiles {
                     if constexpr (kSplit)
                         lo[q] = __builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)(a - (float)near[0]), (_Float16)(c - (float)near[1])});
                 }
-            } else {
+            } else if constexpr (is_int4(F)) {
                 hi = int4_order(hi);
             }
             const int at = in ? (kSplit ? 2 * m : m) * xpitch + 16 * u : xpitch - 16;
@@ -516,6 +556,8 @@ struct RowTiles {
             sfirst = (uint32_t)(e0 - (b0 << w.bshift));          // elements of the first block before base[0]
             zfirst = (uint32_t)(qa & 3);
             dfirst = (uint32_t)(b0 % QK_DQ_BLOCK);
+        } else if constexpr (is_mx4(F)) {
+            sbuf = buffer(w.scales + p.base[0] * w.scale_stride, srows * w.scale_stride);
         } else {
             const uint64_t sa = reinterpret_cast<uint64_t>(w.scales + p.base[0] * w.G);
             sbuf = buffer(reinterpret_cast<const void*>(sa & ~3ull), (srows * w.G * 2 + (int64_t)(sa & 3) + 3) / 4 * 4);
@@ -528,6 +570,7 @@ struct RowTiles {
         // block of the first 64 values, from the first block (and in `run` which 64 values of it).
         auto scale_at = [&](int j, int c) -> uint32_t {
             if constexpr (F == kLevels) return (uint32_t)(j + srow) * (uint32_t)p.K + (uint32_t)c * kChunk + sfirst;
+            else if constexpr (is_mx4(F)) return (uint32_t)(j + srow) * (uint32_t)w.scale_stride + (uint32_t)c * 4;
             else return (uint32_t)(j + srow) * (uint32_t)w.G + (uint32_t)((c * kChunk) >> w.gshift);
         };
         uint32_t at = 0;                                         // of the window in flight
@@ -537,6 +580,7 @@ struct RowTiles {
             const bool in = j >= 0 && c < nchunk, lane_in = in && lane < 16 * RT;
             at = scale_at(j, c);
             if constexpr (F == kLevels) left = (p.K >> 6) - 2 * c;
+            else if constexpr (is_mx4(F)) left = w.G - 4 * c;
             else left = w.G - ((c * kChunk) >> w.gshift);
             if constexpr (F == kLevels) {
                 const uint32_t blk = at >> w.bshift;
@@ -545,6 +589,10 @@ struct RowTiles {
                 f.z[0] = t[0];
                 f.z[1] = t[1];
                 f.d = __builtin_amdgcn_raw_buffer_load_b64(dbuf, lane_in ? (blk + dfirst) / QK_DQ_BLOCK * 4 : kOutside, 0, 0);
+            } else if constexpr (is_mx4(F)) {
+                const u32x2_t t = __builtin_amdgcn_raw_buffer_load_b64(sbuf, lane_in ? at : kOutside, 0, 0);
+                f.s[0] = t[0];
+                f.s[1] = t[1];
             } else {
                 const uint32_t so = lane_in ? (2 * at + sfirst) & ~3u : kOutside;
                 const uint32_t zo = lane_in ? (at + zfirst) & ~3u : kOutside;
@@ -612,6 +660,23 @@ struct RowTiles {
                         v = as_float(o == 0 ? f.s[0] : o == 1 ? f.s[1] : o == 2 ? f.s[2] : f.s[3]);
                     }
                     slds[lane * kSPitch + e] = e < left ? v * w.unit : 0.0f;
+                }
+            } else if constexpr (is_mx4(F)) {
+                // what lies behind the row's last scale meets activations of 0, but may be a NaN: 0, 2^-127, instead
+                uint32_t sv[2] = {f.s[0], f.s[1]};
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int n4 = left - 4 * u;
+                    sv[u] = n4 >= 4 ? sv[u] : n4 <= 0 ? 0u : sv[u] & ((1u << (8 * n4)) - 1u);
+                }
+#pragma unroll
+                for (int e = 0; e < kEntries; ++e) {
+                    if constexpr (F == kMx4Bf16) {
+                        slds[lane * kSPitch + e] = sv[e];
+                    } else {
+                        const uint32_t b = (sv[e >> 2] >> (8 * (e & 3))) & 255u;
+                        slds[lane * kSPitch + e] = as_float(b == 0 ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
+                    }
                 }
             } else {
                 const uint32_t sh = 8 * ((2 * at + sfirst) & 2);
@@ -682,7 +747,11 @@ struct RowTiles {
                     for (int j = q * kMfmas; j < (q + 1) * kMfmas; ++j) {
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
-                            if constexpr (F == kLevels) {
+                            if constexpr (F == kMx4Bf16) {
+                                acc[r] = mfma_bf16(a[j], decode8_mx4(c[r][j], as_float((s[r] >> (8 * h) & 255u) << 23)), acc[r]);
+                            } else if constexpr (F == kMx4F16) {
+                                acc[r] = mfma(a[j], decode8_mx4(c[r][j]), acc[r]);
+                            } else if constexpr (F == kLevels) {
                                 acc[r] = mfma(a[j], decode8_table(c[r][j], 4 * (lane & 31)), acc[r]);
                             } else {
                                 const f16x2_t zero = __builtin_bit_cast(f16x2_t, s[r].zero), zero4 = zero + (f16x2_t){960, 960};
@@ -692,12 +761,13 @@ struct RowTiles {
                     }
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
-                        float sr;
-                        if constexpr (F == kLevels) sr = s[r];
-                        else sr = s[r].s;
+                        float sr = 1.0f;
+                        if constexpr (is_int4(F)) sr = s[r].s;
+                        else if constexpr (F != kMx4Bf16) sr = s[r];
 #pragma unroll
                         for (int i = 0; i < MI; ++i) {
-                            if constexpr (!kScaled) y[r][i] = fmaf(sr, acc[r][i], y[r][i]);
+                            if constexpr (F == kMx4Bf16) y[r][i] += acc[r][i];
+                            else if constexpr (!kScaled) y[r][i] = fmaf(sr, acc[r][i], y[r][i]);
                             else t[r][i] = q == 0 ? sr * acc[r][i] : fmaf(sr, acc[r][i], t[r][i]);
                         }
                     }

@@ -703,6 +703,182 @@ qk_status qk_moe_nf4(const void* x, int32_t T, const void* logits, int32_t logit
                      int32_t renormalize, const qk_quant_state* gate_up, const qk_quant_state* down, void* y,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Descriptor of a microscaled 4-bit matrix [rows, cols]: e2m1 codes (sign, two bits of exponent, one of mantissa: 0, 1/2,
+ * 1, 3/2, 2, 3, 4, 6) and, per group of 32 consecutive inputs of a row (the last may be partial), one scale byte e,
+ *     X[r, k] = value(code[r, k]) * 2^(e[r, k / 32] - 127),
+ * e = 255 standing for NaN.  Groups never cross rows.  Weights and activations have this form alike.  Plain data, the
+ * pointers are device pointers owned by the caller.  Build it with qk_mx4_state_init(); a descriptor whose magic,
+ * version, size or fields do not fit is rejected with QK_ERR_BAD_STATE by every call that takes one.
+ */
+#define QK_MX4_MAGIC 0x344D4B51u     /* "QKM4" little-endian */
+#define QK_MX4_VERSION 1u
+
+typedef struct qk_mx4_state {
+    uint32_t magic;          /* QK_MX4_MAGIC */
+    uint32_t version;        /* QK_MX4_VERSION */
+    uint32_t struct_bytes;   /* sizeof(qk_mx4_state) */
+    uint32_t reserved;       /* 0 */
+    int64_t rows;            /* 1..2^30 */
+    int64_t cols;            /* 1..2^22 */
+    int64_t code_stride;     /* bytes from a row of codes to the next: a multiple of 16, >= ceil(cols / 2), at most 2^22 */
+    int64_t scale_stride;    /* bytes from a row of scales to the next: a multiple of 4, >= ceil(cols / 32), at most 2^22 */
+    const uint8_t* codes;    /* device, [rows, code_stride], 16-byte aligned: input 2t of a row in the low nibble of its
+                                byte t, input 2t+1 in the high nibble; what lies past the row's last code is ignored */
+    const uint8_t* scales;   /* device, [rows, scale_stride], 4-byte aligned; what lies past the row's last scale is
+                                ignored */
+} qk_mx4_state;
+
+/*
+ * qk_mx4_state_init — host.  Fills a descriptor.
+ *   Errors: QK_ERR_INVALID_ARG (null pointers, sizes or strides out of range, misaligned buffers).
+ */
+qk_status qk_mx4_state_init(qk_mx4_state* st, int64_t rows, int64_t cols, const uint8_t* codes, int64_t code_stride,
+                            const uint8_t* scales, int64_t scale_stride);
+
+/*
+ * qk_mx4_quantize — device.  Rows to the microscaled form.  Per group, with top = max |x|:
+ *     e    = max(floor(log2 top) - 2 + 127, 0)   (0 for a group of zeros)
+ *     code = the e2m1 value nearest to x / 2^(e - 127), ties to the even code, at most 6 in magnitude
+ *   exactly.  Signed zeros are kept.  A group that holds an infinity or a NaN gets e = 255 and codes 0.
+ *   x: device, [rows, cols] of x_dtype (QK_BF16, QK_F16 or QK_F32), aligned to its elements, row r at element
+ *     r * x_stride (x_stride >= cols, at most 2^40; 16-byte aligned rows load fastest).
+ *   codes, scales: device, as in qk_mx4_state; written: whole groups (zero past cols), scales up to the next multiple
+ *     of four bytes (zero past the last).  No overlap with x or each other.
+ *   Errors: QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_mx4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t x_stride, uint8_t* codes,
+                          int64_t code_stride, uint8_t* scales, int64_t scale_stride, void* stream);
+
+/*
+ * qk_mx4_dequantize — device.  The values of a microscaled matrix as fp32, bf16 or fp16 (round to nearest even: exact
+ *   in fp32 and, but for overflow and values under 2^-133, in bf16).
+ *   out: device, [rows, cols] of out_dtype, aligned to its elements, written.
+ *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_mx4_dequantize(const qk_mx4_state* st, void* out, int32_t out_dtype, void* stream);
+
+/*
+ * qk_gemm_mx4 — device.  Product of two microscaled matrices on the scaled matrix cores,
+ *     Y[m, n] = sum_k X[m, k] W[n, k],
+ *   X [M, K] and W [N, K] entering exactly, sums in fp32, Y rounded once.  The same inputs give the same bits on every
+ *   call.  A NaN scale spoils its own row of X, or of W, only.
+ *   x, w: host pointers to valid descriptors with the same cols; any M >= 1 and N >= 1.
+ *   y: device, [M, N] of y_dtype (QK_BF16, QK_F16 or QK_F32), aligned to its elements, written; no overlap with the
+ *     operands.
+ *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_gemm_mx4(const qk_mx4_state* x, const qk_mx4_state* w, void* y, int32_t y_dtype, void* stream);
+
+/*
+ * qk_gemv_mx4 — device.  Decode-time product of 16-bit activations with a microscaled weight,
+ *     y[m, :] = x[m, :] · W^T,  m < M.
+ *   Activations and weights enter the products exactly (but weights under 2^-126, which may count as zero), sums are
+ *   fp32, y is rounded once.  The same inputs give the same bits on every call.  An infinity or a NaN in x spoils its
+ *   own row of y only.
+ *   x:  device, [M, K] of dtype (QK_BF16 or QK_F16) row-major, 2-byte aligned (4-byte alignment and K % 8 == 0 load
+ *       fastest).   M: 1..16.
+ *   st: host pointer to a valid descriptor of W [N, K], N at most 2^28.
+ *   y:  device, [M, N] of dtype, written; must not overlap x.
+ *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_gemv_mx4(const void* x, int32_t dtype, int32_t M, const qk_mx4_state* st, void* y, void* stream);
+
+/* scores of qk_moe_route */
+enum { QK_SOFTMAX = 0, QK_SIGMOID = 1 };
+
+/*
+ * qk_moe_route — device.  The experts of each token and their weights, from the router's logits z = logits[t, :]:
+ *     s    = softmax(z), or 1 / (1 + exp(-z)) (QK_SIGMOID)
+ *     rank = s + bias as binary64 numbers; where bias is NULL, z (the same order)
+ *     G_t  = the top_groups of `groups` runs of E / groups experts whose two largest s + bias (or the only one) have the
+ *            largest sums (every expert where groups == 1)
+ *     ids  = the top_k experts of G_t by rank, largest first
+ *     w    = scale * s,  or with renormalize != 0  scale * s / (the sum of s over the token's ids)
+ *   Equal ranks, and groups of equal sums, go to the lower index.  Which of two is larger is decided in binary64: the
+ *   result does not depend on the rounding of s.  The bias only ranks.
+ *   A logit of -inf (a NaN counts as that, +inf as the largest finite value) masks an expert: it is never chosen and has no
+ *   part in the softmax; so does a bias of -inf or NaN but for the softmax.  A group without experts left is not taken.  Where
+ *   fewer than top_k experts are left, the remaining ids are -1, their weights 0.
+ *   logits: device, [T, E] of dtype (QK_F32, QK_BF16 or QK_F16), naturally aligned.  T: 1..2^26, E: 1..512.
+ *   bias: device, fp32 [E], or NULL.   groups: 1..64, divides E.   top_groups: 1..groups.
+ *   top_k: 1..32, at most E / groups * top_groups.   scale: finite.
+ *   ids: device, int32 [T, top_k], written.   weights: device, fp32 [T, top_k], written.
+ *   Errors: QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_moe_route(const void* logits, int32_t dtype, int64_t T, int32_t E, const float* bias, int32_t score,
+                       int32_t groups, int32_t top_groups, int32_t top_k, int32_t renormalize, float scale, int32_t* ids,
+                       float* weights, void* stream);
+
+/*
+ * qk_moe_route_backward — device.  Gradient of the weights of qk_moe_route with respect to the logits, the choice of
+ *   experts held fixed: with p the s of the chosen ones over their sum (renormalize) or s itself, and d = scale * dweights,
+ *     ds = (d - sum d p) / (sum of the chosen s)   (renormalize),   or d
+ *     dz = ds s (1 - s)  (QK_SIGMOID),   or   s (ds - sum ds s)   (QK_SOFTMAX),
+ *   0 for experts that are masked, and for those that have no part.  Sums in fp32, dlogits rounded once.
+ *   logits, dtype, T, E, score, renormalize, scale: as given to qk_moe_route.
+ *   ids: device, int32 [T, top_k], its result: the ids of a token are distinct; those outside 0..E-1 have no part.
+ *   top_k: 1..32.   dweights: device, fp32 [T, top_k]; not read where the id has no part.
+ *   dlogits: device, [T, E] of dtype, written; may be logits itself.
+ *   Errors: QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_moe_route_backward(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t score, int32_t top_k,
+                                int32_t renormalize, float scale, const int32_t* ids, const float* dweights,
+                                void* dlogits, void* stream);
+
+/*
+ * qk_moe_plan — device.  Sorts the pairs (token, position) of a routing, slot t * top_k + j, by expert, for the experts'
+ *   products: plan[0..E] are the first places of the experts in the list (plan[E]: the end of the last one), and the
+ *   list follows at plan[4 * ceil((E + 1) / 4)], the slots of one expert in increasing order, behind the last expert's
+ *   those whose id is outside 0..E-1.  An expert may occur more than once in a token.  Deterministic.
+ *   ids: device, int32 [T, top_k].   T: >= 1, T * top_k at most 2^26.   top_k: 1..32.   E: 1..512.
+ *   plan: device, 16-byte aligned, qk_moe_plan_size() bytes, written; no overlap with ids.
+ *   Errors: QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_moe_plan_size(int64_t T, int32_t top_k, int32_t E, size_t* bytes);
+qk_status qk_moe_plan(const int32_t* ids, int64_t T, int32_t top_k, int32_t E, int32_t* plan, void* stream);
+
+/*
+ * qk_moe_up_mx4 — device.  The gate and up products of the chosen experts and their SwiGLU, for any number of tokens:
+ *     h[t * top_k + j, :] = silu(x_t · Wg_e^T) * (x_t · Wu_e^T),   e = ids[t, j]
+ *   (zeros where the slot has no expert).  Operands enter exactly, sums and SwiGLU are fp32, h is rounded once.  A slot's
+ *   result does not depend on the other tokens' values.
+ *   x: host pointer to the descriptor of the tokens [T, H].
+ *   gate_up: descriptor of the stacked [E * 2 * I, H] weights, as for qk_moe_int4.
+ *   plan: device, of qk_moe_plan for the same T, top_k and E.
+ *   h: device, [T * top_k, I] of h_dtype (QK_BF16, QK_F16 or QK_F32), aligned to its elements, written; no overlap with
+ *     the operands.
+ *   T rows of x, and 2 * I rows of gate_up, must stay under 2^32 - 2^24 bytes of codes and of scales (else
+ *     QK_ERR_UNSUPPORTED); the stack may be as large as memory.
+ *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_UNSUPPORTED, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_moe_up_mx4(const qk_mx4_state* x, const qk_mx4_state* gate_up, const int32_t* plan, int32_t top_k, int32_t E,
+                        void* h, int32_t h_dtype, void* stream);
+
+/*
+ * qk_moe_down_mx4_workspace_size — host.  Bytes of device workspace of qk_moe_down_mx4 for T tokens of `hidden` outputs.
+ */
+qk_status qk_moe_down_mx4_workspace_size(int64_t T, int32_t top_k, int64_t hidden, size_t* bytes);
+
+/*
+ * qk_moe_down_mx4 — device.  The down products of the chosen experts, weighted and added per token:
+ *     y_t = sum over j with an expert e of weights[t, j] · h[t * top_k + j, :] · Wd_e^T
+ *   in fp32, in the order of j, rounded once; 0 for a token without experts.  What h and weights hold in slots without an
+ *   expert does not matter.  The same inputs give the same bits on every call.
+ *   h: descriptor of the slots' activations [T * top_k, I], quantized.
+ *   down: descriptor of the stacked [E * H, I] weights.   weights: device, fp32 [T, top_k].
+ *   plan: device, of qk_moe_plan for the same T, top_k and E.
+ *   y: device, [T, H] of y_dtype (QK_BF16, QK_F16 or QK_F32), aligned to its elements, written.
+ *   workspace: device, >= qk_moe_down_mx4_workspace_size(T, top_k, H) bytes, 16-byte aligned; contents on entry
+ *     ignored.  Neither y nor the workspace overlaps the operands or the other.  Calls that may run at the same time need
+ *     workspaces of their own.
+ *   The T * top_k rows of h must stay under 2^32 - 2^24 bytes of codes and of scales (else QK_ERR_UNSUPPORTED).
+ *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_UNSUPPORTED, QK_ERR_WORKSPACE, QK_ERR_NO_DEVICE, QK_ERR_HIP.
+ */
+qk_status qk_moe_down_mx4(const qk_mx4_state* h, const qk_mx4_state* down, const int32_t* plan, const float* weights,
+                          int32_t top_k, int32_t E, void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
 /* Message for the calling thread's last failed call ("" if none).  The
  * string stays valid until the thread's next qk_* call. */
 const char* qk_last_error(void);
