@@ -13,6 +13,8 @@
 // What lies past the last input of a row (the row's padding, the next row, nothing) is in the last line too: before that
 // line is used its groups past the end get the scale 1 in both operands and its codes past the end become 0 in X.
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "mx4.h"
 
@@ -179,6 +181,16 @@ __device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t r, uint8_t* dst, 
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)dst, 4, (int)voff, (int)soff, 0, 0);
 }
 
+// f(0), f(1), ... f(N - 1), each with its number as a constant (a loop this long is not unrolled).
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+    each_of(f, std::make_integer_sequence<int, N>{});
+}
+
 __device__ __forceinline__ int slot_of(int row, int piece) { return piece ^ ((row >> 1) & 7); }
 
 // The last line of a row, in LDS: groups past the end of scale 1, codes past the end 0 (X).  valid: inputs of the line.
@@ -206,6 +218,28 @@ __device__ __forceinline__ v8i_t wide(v4i_t v) { return (v8i_t){v[0], v[1], v[2]
 template <int S>
 __device__ __forceinline__ floatx4_t mfma(v4i_t w, int ws, v4i_t x, int xs, floatx4_t c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(w), wide(x), c, 4, 4, S, ws, S, xs);
+}
+
+// The same in place.  The compiler's own form may write its sum elsewhere, and with 256 of them there is no elsewhere: it
+// then moves sums about between the instructions.  What reads the sums has to wait for the last instruction by itself
+// (settle); operands come from LDS, whose waits the compiler sets for any reader.
+template <int S>
+__device__ __forceinline__ void mfma_in_place(floatx4_t& c, v4i_t w, int ws, v4i_t x, int xs) {
+    if constexpr (S == 0)
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs));
+    else
+        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                     : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs));
+}
+// 32 idle cycles, more than an instruction of 8 passes needs before its result may be read; the sums count as written behind them.
+template <int MT, int RT>
+__device__ __forceinline__ void settle(floatx4_t (&acc)[MT][RT]) {
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) asm volatile("" : "+a"(acc[i][j]));
 }
 
 // Four consecutive outputs, those of them below `left`.
@@ -277,16 +311,20 @@ __device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, 
 // ---------------------------------------------------------------------------
 // Many rows: tiles of BM x BN, waves of WM x WN, two stages of LDS.  Up: columns [0, WN / 2) of a wave are gate rows,
 // the others their up rows.
+//
+// A stage is two halves of WM / 16 x WN / 16 instructions.  While a half is multiplied, row of fragments by row, the X
+// fragments of the row after next and the W fragments of the next half are read from LDS, in the order written here (the
+// scheduling barriers keep it).  Two rows before a stage ends all waves meet: their reads of it are done, the next one has
+// landed; behind that the copies of the stage after next go where this one was, and have nearly a stage's time.
 // ---------------------------------------------------------------------------
 template <Mode MODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(GemmArgs a) {
     constexpr int kWaves = (BM / WM) * (BN / WN), kThreads = kWaves * 64;
     constexpr int kLines = BM + BN;
     constexpr int MT = WM / 16, RT = WN / 16;
-    constexpr int kLoads = kLines / 8 / kWaves, kXLoads = BM / 8 / kWaves;      // of codes, per wave
-    constexpr int kSLoads = (kLines / 32 + kWaves - 1) / kWaves;                // of scales
-    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && kLines % (32 * kWaves) == 0);
-    static_assert(BM % 32 == 0);
+    constexpr int kLoads = kLines / 8 / kWaves, kXLoads = BM / 8 / kWaves;      // copies of codes, per wave
+    constexpr int kSLoads = kLines / 32 / kWaves;                               // of scales
+    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && kLines % (32 * kWaves) == 0 && BM % 32 == 0);
     constexpr int kBNo = MODE == kUp ? BN / 2 : BN;
     // rows of X, then rows of W, 128 bytes each; then their scales, 8 bytes each
     __shared__ __align__(16) uint8_t lds0[kLines * 136];
@@ -324,76 +362,111 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
                                                   : w_row(line - BM) * (uint32_t)a.w.scale_stride);
         }
         const int nst = (a.x.cols + kLineK - 1) / kLineK;
-        auto load = [&](uint8_t* dst, int st) {
-#pragma unroll
-            for (int v = 0; v < kLoads; ++v)
-                to_lds(v < kXLoads ? op.xc : op.wc, dst + (wave + kWaves * v) * 1024, voff[v], 128u * st);
-#pragma unroll
-            for (int v = 0; v < kSLoads; ++v) {
-                const bool x = 32 * (wave + kWaves * v) < BM;
-                to_lds4(x ? op.xs : op.ws, dst + kLines * 128 + (wave + kWaves * v) * 256, soff[v], 8u * st);
+        // Copy v of stage st, which is line `line`; past the last stage every offset is outside its buffer, and nothing is
+        // read.
+        auto copy = [&](uint8_t* dst, int st, int line, int v) {
+            const uint32_t out = st < nst ? 0u : 0xFFFF0000u;
+            if (v < kLoads) {
+                to_lds(v < kXLoads ? op.xc : op.wc, dst + (wave + kWaves * v) * 1024, voff[v] | out, st < nst ? 128u * line : 0u);
+            } else {
+                const int u = v - kLoads;
+                const bool x = 32 * (wave + kWaves * u) < BM;
+                to_lds4(x ? op.xs : op.ws, dst + kLines * 128 + (wave + kWaves * u) * 256, soff[u] | out, st < nst ? 8u * line : 0u);
             }
         };
         const int xline = (wm * WM + r) * 128, wline = (BM + wn * WN + r) * 128;
         const int xsc = kLines * 128 + (wm * WM + r) * 8 + 2 * h, wsc = kLines * 128 + (BM + wn * WN + r) * 8 + 2 * h;
-        auto compute = [&](const uint8_t* src) {
-            int xs[MT], ws[RT];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) xs[i] = *reinterpret_cast<const uint16_t*>(src + xsc + 128 * i);
-#pragma unroll
-            for (int j = 0; j < RT; ++j) ws[j] = *reinterpret_cast<const uint16_t*>(src + wsc + 128 * j);
-            auto half = [&](auto S) {
-                constexpr int s = decltype(S)::value;
-                const int at = 16 * slot_of(r, 2 * h + s);
-                v4i_t x[MT], w[RT];
-#pragma unroll
-                for (int i = 0; i < MT; ++i) x[i] = *reinterpret_cast<const v4i_t*>(src + xline + at + 2048 * i);
-#pragma unroll
-                for (int j = 0; j < RT; ++j) w[j] = *reinterpret_cast<const v4i_t*>(src + wline + at + 2048 * j);
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < RT; ++j) acc[i][j] = mfma<s>(w[j], ws[j], x[i], xs[i], acc[i][j]);
-            };
-            half(std::integral_constant<int, 0>{});
-            half(std::integral_constant<int, 1>{});
+        const int at0 = 16 * slot_of(r, 2 * h), at1 = 16 * slot_of(r, 2 * h + 1);
+        // fragments of W by half; those of X, of which four are enough; scales by the parity of the stage
+        v4i_t wf[2][RT], xf[4];
+        int ws[2][RT], xs[2][MT];
+        auto read_x = [&](const uint8_t* src, int s, int i) {
+            xf[i % 4] = *reinterpret_cast<const v4i_t*>(src + xline + (s ? at1 : at0) + 2048 * i);
         };
-        const int valid = a.x.cols - (nst - 1) * kLineK;              // inputs of the last line
-        // the stage that was loaded is in LDS, and every wave is done with the other one
-        auto landed = [&] {
+        auto read_w = [&](const uint8_t* src, int s, int j) {
+            wf[s][j] = *reinterpret_cast<const v4i_t*>(src + wline + (s ? at1 : at0) + 2048 * j);
+        };
+        auto read_scale = [&](const uint8_t* src, int p, int n) {
+            if (n < RT) ws[p][n] = *reinterpret_cast<const uint16_t*>(src + wsc + 128 * n);
+            else xs[p][n - RT] = *reinterpret_cast<const uint16_t*>(src + xsc + 128 * (n - RT));
+        };
+        static_assert(MT % 4 == 0);
+        constexpr int kOps = MT * RT, kTail = 2 * RT;                 // instructions of a half; of it behind the meeting
+        constexpr int kCopies = kLoads + kSLoads, kEarly = kCopies / 2;
+        // Items 0..n-1 spread over instructions [from, to): those behind instruction o.
+        auto spread = [](auto O, auto From, auto To, auto N, auto&& item) {
+            constexpr int o = decltype(O)::value - decltype(From)::value, ops = decltype(To)::value - decltype(From)::value;
+            constexpr int n = decltype(N)::value;
+            if constexpr (o >= 0 && o < ops) {
+                constexpr int k0 = (o * n + ops - 1) / ops, k1 = ((o + 1) * n + ops - 1) / ops;
+                each<k1 - k0>([&](auto K) { item(k0 + decltype(K)::value); });
+            }
+        };
+        auto meet = [&] {
             __builtin_amdgcn_s_waitcnt(0);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
         };
-        auto finish = [&](uint8_t* dst) {
+        auto stage = [&](auto P, uint8_t* cur, uint8_t* next, int st) {
+            constexpr int p = decltype(P)::value;
+            each<2>([&](auto S) {
+                constexpr int s = decltype(S)::value;
+                each<kOps>([&](auto O) {
+                    constexpr int o = decltype(O)::value, i = o / RT, j = o % RT;
+                    if constexpr (s == 1 && o == kOps - kTail) meet();
+                    mfma_in_place<s>(acc[i][j], wf[s][j], ws[p][j], xf[i % 4], xs[p][i]);
+                    if constexpr (j == 0) {
+                        if constexpr (i + 2 < MT) read_x(cur, s, i + 2);
+                        else read_x(s == 0 ? cur : next, 1 - s, i + 2 - MT);
+                    }
+                    typedef std::integral_constant<int, 0> Begin;
+                    typedef std::integral_constant<int, kOps - kTail> Meeting;
+                    typedef std::integral_constant<int, kOps> End;
+                    if constexpr (s == 0) {
+                        spread(O, Begin{}, Meeting{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(cur, 1, k); });
+                        spread(O, Begin{}, std::integral_constant<int, kTail>{}, std::integral_constant<int, kCopies - kEarly>{},
+                               [&](int k) { copy(next, st + 1, st, kEarly + k); });
+                    } else {
+                        spread(O, Meeting{}, End{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(next, 0, k); });
+                        spread(O, Meeting{}, End{}, std::integral_constant<int, RT + MT>{}, [&](int k) { read_scale(next, 1 - p, k); });
+                        spread(O, Meeting{}, End{}, std::integral_constant<int, kEarly>{}, [&](int k) { copy(cur, st + 2, st + 1, k); });
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+            });
+        };
+        // the last line, which may end early, comes first
+        const int valid = a.x.cols - (nst - 1) * kLineK;              // inputs of it
+#pragma unroll
+        for (int v = 0; v < kCopies; ++v) copy(lds0, 0, nst - 1, v);
+        meet();
+#pragma unroll
+        for (int v = 0; v < kEarly; ++v) copy(lds1, 1, 0, v);
+        if (valid < kLineK) {
             for (int l = tid; l < kLines; l += kThreads) {
-                end_scales(dst + kLines * 128 + 8 * l, valid);
-                if (l < BM) end_codes(dst + 128 * l, l, valid);
+                end_scales(lds0 + kLines * 128 + 8 * l, valid);
+                if (l < BM) end_codes(lds0 + 128 * l, l, valid);
             }
-            __syncthreads();
-        };
-        load(lds0, 0);
-        landed();
-        int st = 0;
-        for (; st + 2 < nst; st += 2) {
-            load(lds1, st + 1);
-            compute(lds0);
-            landed();
-            load(lds0, st + 2);
-            compute(lds1);
-            landed();
+            __builtin_amdgcn_s_waitcnt(0xC07F);                       // LDS stores done, copies in flight left alone
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
         }
-        if (st + 1 < nst) {
-            load(lds1, st + 1);
-            compute(lds0);
-            landed();
-            if (valid < kLineK) finish(lds1);
-            compute(lds1);
-        } else {
-            if (valid < kLineK) finish(lds0);
-            compute(lds0);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) read_w(lds0, 0, j);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) read_x(lds0, 0, i);
+#pragma unroll
+        for (int k = 0; k < RT + MT; ++k) read_scale(lds0, 0, k);
+        // (an odd number of stages is one more of zeros: a way out between the two costs the compiler the registers)
+        for (int st = 0; st < nst; st += 2) {
+            stage(std::integral_constant<int, 0>{}, lds0, lds1, st);
+            stage(std::integral_constant<int, 1>{}, lds1, lds0, st + 1);
         }
+        __builtin_amdgcn_s_waitcnt(0);                                // nothing on its way to LDS any more
+        settle<MT, RT>(acc);
     }
     store_outputs<MODE>(a, t, wm * WM, MODE == kUp ? wn * (WN / 2) : wn * WN, acc);
 }
