@@ -1167,7 +1167,7 @@ qk_status qk_moe_plan_size(int64_t T, int32_t top_k, int32_t E, size_t* bytes) {
     if (!bytes) return fail(QK_ERR_INVALID_ARG, "qk_moe_plan_size: bytes is NULL");
     const qk_status v = check_slots("qk_moe_plan_size", T, top_k, E);
     if (v != QK_OK) return v;
-    *bytes = (size_t)(qk::moe_plan_list(E) + T * top_k) * 4;
+    *bytes = (size_t)qk::moe_plan_words(T * top_k, E) * 4;
     return ok();
 }
 
@@ -1178,7 +1178,7 @@ qk_status qk_moe_plan(const int32_t* ids, int64_t T, int32_t top_k, int32_t E, i
     if (!ids || !plan) return fail(QK_ERR_INVALID_ARG, "%s: NULL ids or plan", who);
     if (!aligned(ids, 4) || !aligned(plan, 16))
         return fail(QK_ERR_INVALID_ARG, "%s: ids must be 4-byte aligned and plan 16-byte aligned", who);
-    if (overlap(ids, (size_t)(T * top_k) * 4, plan, (size_t)(qk::moe_plan_list(E) + T * top_k) * 4))
+    if (overlap(ids, (size_t)(T * top_k) * 4, plan, (size_t)qk::moe_plan_words(T * top_k, E) * 4))
         return fail(QK_ERR_INVALID_ARG, "%s: plan overlaps ids", who);
     const qk_status dev = ensure_device();
     if (dev != QK_OK) return dev;
@@ -1196,7 +1196,7 @@ qk_status qk_moe_up_mx4(const qk_mx4_state* x, const qk_mx4_state* gate_up, cons
         return fail(QK_ERR_INVALID_ARG, "%s: x [%lld, %lld] and gate_up [%lld, %lld] are not [T, H] and [E*2*I, H] of %d experts",
                     who, (long long)x->rows, (long long)x->cols, (long long)gate_up->rows, (long long)gate_up->cols, E);
     const int64_t slots = x->rows * top_k, I = gate_up->rows / (2 * (int64_t)E);
-    const size_t pb = (size_t)(qk::moe_plan_list(E) + slots) * 4;
+    const size_t pb = (size_t)qk::moe_plan_words(slots, E) * 4;
     if (!plan || !aligned(plan, 16)) return fail(QK_ERR_INVALID_ARG, "%s: plan is NULL or not 16-byte aligned", who);
     v = check_mx4_out(who, "h", h, h_dtype, (size_t)slots * (size_t)I, x, gate_up);
     if (v == QK_OK) v = check_gather(who, "x", x->rows, x->code_stride, x->scale_stride);
@@ -1237,7 +1237,7 @@ qk_status qk_moe_down_mx4(const qk_mx4_state* h, const qk_mx4_state* down, const
         return fail(QK_ERR_INVALID_ARG, "%s: h [%lld, %lld] and down [%lld, %lld] are not [T*top_k, I] and [E*H, I] of %d experts",
                     who, (long long)h->rows, (long long)h->cols, (long long)down->rows, (long long)down->cols, E);
     const int64_t H = down->rows / E;
-    const size_t pb = (size_t)(qk::moe_plan_list(E) + h->rows) * 4, wb = (size_t)h->rows * 4;
+    const size_t pb = (size_t)qk::moe_plan_words(h->rows, E) * 4, wb = (size_t)h->rows * 4;
     if (!plan || !aligned(plan, 16)) return fail(QK_ERR_INVALID_ARG, "%s: plan is NULL or not 16-byte aligned", who);
     if (!weights || !aligned(weights, 4)) return fail(QK_ERR_INVALID_ARG, "%s: weights is NULL or not 4-byte aligned", who);
     v = check_mx4_out(who, "y", y, y_dtype, (size_t)T * (size_t)H, h, down);

@@ -7,8 +7,8 @@
 // that a lane's two scale bytes are neighbours and the instruction picks one by its byte select.  W is the first operand: a
 // lane then ends up with 4 consecutive columns of one row of Y.
 //
-// Codes and scales go from memory straight to LDS.  A row of a stage keeps its 128 bytes, piece p of row r in slot
-// p ^ (r / 2 % 8): the 16 rows that 16 lanes read at a time then fall in all banks.
+// Codes and scales go from memory straight to LDS.  A row of a stage keeps its 128 bytes, the pieces of 16 in an order
+// turned by the row: what lanes read at a time then falls in all banks (slot_of).
 //
 // What lies past the last input of a row (the row's padding, the next row, nothing) is in the last line too: before that
 // line is used its groups past the end get the scale 1 in both operands and its codes past the end become 0 in X.
@@ -27,6 +27,7 @@ typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef int v4i_t __attribute__((ext_vector_type(4)));
 typedef float floatx4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int kLineK = 256;                // inputs of a stage: 128 bytes of codes, 8 of scales
@@ -37,14 +38,16 @@ enum Mode { kDense, kUp, kDown };
 struct GemmArgs {
     View x, w;
     void* y;                   // dense: [M, N]; up: h [slots, I]; down: the weighted parts [slots, H], fp32
-    const int32_t* plan;
+    const int32_t* list;       // of the plan: the slots by expert
+    const int32_t* tiles;      // of the plan: how many tiles, and from the 4th number on each one's rows
     const float* weights;      // down: of the slots
     int64_t M;                 // dense: rows of x
     int64_t N;                 // outputs of a row: N, I or H
     int64_t w_rows;            // rows of an expert's weights: 2 I or H
     int32_t y_dtype;
-    int32_t top_k, E;
+    int32_t E;
     int32_t slots;
+    uint32_t per_token;        // ceil(2^32 / top_k): the token of a slot is the upper half of slot * per_token; 0: the slot
 };
 
 // The part of the product that a workgroup makes: rows of X by position 0..count-1, columns n0 on, of one expert.
@@ -55,72 +58,33 @@ struct Tile {
     int32_t expert;            // E: slots without one
 };
 
-// Tile `bid` of a dense product.  Workgroup i runs on XCD i % 8: each XCD gets a run of tiles, 8 rows of them at a time
-// going through all columns, so that the tiles of an XCD share operands in its L2.
-template <int BM, int BN>
-__device__ __forceinline__ Tile dense_tile(const GemmArgs& a) {
-    const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + BN - 1) / BN), nt = tm * tn;
-    const uint32_t xcd = blockIdx.x % kXcds, q = nt / kXcds, rem = nt % kXcds;
-    const uint32_t lid = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
-    const uint32_t band = lid / (kXcds * tn), in = lid - band * (kXcds * tn);
-    const uint32_t rows = tm - band * kXcds < kXcds ? tm - band * kXcds : kXcds;
-    Tile t;
-    t.m0 = (int64_t)(band * kXcds + in % rows) * BM;
-    t.n0 = (int64_t)(in / rows) * BN;
-    t.count = (int32_t)(a.M - t.m0 < BM ? a.M - t.m0 : BM);
-    t.expert = 0;
-    return t;
-}
-
-// The same for the experts' products: the tiles of an expert one after the other, its rows fastest; count 0: none left.
-// Every wave finds its tile by itself, from a prefix sum over the experts' tiles (9 experts a lane at most).
-template <int BM, int BNo>
-__device__ __forceinline__ Tile expert_tile(const GemmArgs& a) {
-    const int lane = threadIdx.x & 63;
-    const uint32_t nb = (uint32_t)((a.N + BNo - 1) / BNo);
-    const int entries = a.E + 1, per = (entries + 63) / 64;          // the last entry: slots without an expert
-    auto start = [&](int e) { return e <= a.E ? a.plan[e] : a.slots; };
-    int tiles = 0;
-    for (int i = 0, p = start(min(lane * per, entries)); i < per; ++i) {
-        const int n = start(min(lane * per + i + 1, entries));
-        tiles += (n - p + BM - 1) / BM;
-        p = n;
-    }
-    const int incl = wave_scan(tiles);
-    const uint32_t nt = (uint32_t)__builtin_amdgcn_readlane(incl, 63) * nb;
+// The tile of this workgroup; count 0: none.  Workgroup i runs on XCD i % 8: each XCD gets a run of tiles, 8 rows of them at a
+// time going through all columns, so that the tiles of an XCD share operands in its L2.  The experts' tiles have their rows
+// from the plan, one after the other in one list: those of an expert are neighbours.
+template <bool kExperts, int BM, int BN>
+__device__ __forceinline__ Tile find_tile(const GemmArgs& a) {
+    const uint32_t tm = kExperts ? (uint32_t)*a.tiles : (uint32_t)((a.M + BM - 1) / BM);
+    const uint32_t tn = (uint32_t)((a.N + BN - 1) / BN), nt = tm * tn;
     Tile t;
     t.count = 0;
     t.m0 = t.n0 = 0;
     t.expert = 0;
-    if (blockIdx.x >= nt) return t;
+    if (kExperts && blockIdx.x >= nt) return t;
     const uint32_t xcd = blockIdx.x % kXcds, q = nt / kXcds, rem = nt % kXcds;
     const uint32_t lid = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
-    const int at = (int)(lid / nb);                                   // in [first tile of e, first tile of e + 1)
-    int first = incl - tiles, e = 0, p0 = 0, p1 = 0, tile0 = 0, mine = 0;
-    for (int i = 0, p = start(min(lane * per, entries)); i < per; ++i) {
-        const int n = start(min(lane * per + i + 1, entries));
-        const int k = (n - p + BM - 1) / BM;
-        if (at >= first && at < first + k) {
-            e = lane * per + i;
-            p0 = p;
-            p1 = n;
-            tile0 = first;
-            mine = k;
-        }
-        first += k;
-        p = n;
+    const uint32_t band = lid / (kXcds * tn), in = lid - band * (kXcds * tn);
+    const uint32_t rows = tm - band * kXcds < kXcds ? tm - band * kXcds : kXcds;
+    const uint32_t m = band * kXcds + in % rows;
+    t.n0 = (int64_t)(in / rows) * BN;
+    if constexpr (kExperts) {
+        const MoeTile e = reinterpret_cast<const MoeTile*>(a.tiles + 4)[m];
+        t.m0 = e.first;
+        t.expert = e.expert_count & 0xFFFF;
+        t.count = e.expert_count >> 16;
+    } else {
+        t.m0 = (int64_t)m * BM;
+        t.count = (int32_t)(a.M - t.m0 < BM ? a.M - t.m0 : BM);
     }
-    const int who = __builtin_ctzll(__ballot(mine > 0));
-    e = __builtin_amdgcn_readlane(e, who);
-    p0 = __builtin_amdgcn_readlane(p0, who);
-    p1 = __builtin_amdgcn_readlane(p1, who);
-    tile0 = __builtin_amdgcn_readlane(tile0, who);
-    mine = __builtin_amdgcn_readlane(mine, who);
-    const uint32_t in = lid - (uint32_t)tile0 * nb;
-    t.expert = e;
-    t.m0 = p0 + (int64_t)(in % (uint32_t)mine) * BM;
-    t.n0 = (int64_t)(in / (uint32_t)mine) * BNo;
-    t.count = p1 - (int)t.m0 < BM ? p1 - (int)t.m0 : BM;
     return t;
 }
 
@@ -137,11 +101,11 @@ struct Operands {
     int32_t x_rows;            // of the tile
     int32_t w_rows;            // of a kind, from n0 on
     int32_t up;                // rows from a gate row to its up row
-    int32_t top_k;
+    uint32_t per_token;
 
     __device__ __forceinline__ Operands(const GemmArgs& a, const Tile& t) {
         x_rows = t.count;
-        top_k = a.top_k;
+        per_token = a.per_token;
         up = (int32_t)a.N;
         const int64_t left = a.N - t.n0;
         w_rows = (int32_t)(left < 1024 ? left : 1024);
@@ -152,7 +116,7 @@ struct Operands {
             sx += t.m0 * a.x.scale_stride;
             xr = t.count;
         } else {
-            list = a.plan + moe_plan_list(a.E) + t.m0;
+            list = a.list + t.m0;
         }
         xc = buffer(cx, xr * a.x.code_stride);
         xs = buffer(sx, xr * a.x.scale_stride);
@@ -164,7 +128,7 @@ struct Operands {
     __device__ __forceinline__ uint32_t x_row(int i) const {
         i = min(i, x_rows - 1);
         if constexpr (MODE == kDense) return (uint32_t)i;
-        if constexpr (MODE == kUp) return (uint32_t)list[i] / (uint32_t)top_k;
+        if constexpr (MODE == kUp) return per_token ? __umulhi((uint32_t)list[i], per_token) : (uint32_t)list[i];
         return (uint32_t)list[i];
     }
     // column c of the tile, of the gate or the up rows
@@ -191,7 +155,13 @@ __device__ __forceinline__ void each(F&& f) {
     each_of(f, std::make_integer_sequence<int, N>{});
 }
 
-__device__ __forceinline__ int slot_of(int row, int piece) { return piece ^ ((row >> 1) & 7); }
+// Slot of a 16-byte piece in its row of 128 bytes, and the piece in a slot.  The pieces of one instruction, 2 h + s, come to
+// lie in neighbouring slots, turned by the row: 4.1 cycles a 16-byte read of a wave; the pieces in their own order take 5.8.
+__device__ __forceinline__ int slot_of(int row, int piece) { return ((piece >> 1) | ((piece & 1) << 2)) ^ ((row >> 1) & 7); }
+__device__ __forceinline__ int piece_in(int row, int slot) {
+    const int t = slot ^ ((row >> 1) & 7);
+    return ((t & 3) << 1) | (t >> 2);
+}
 
 // The last line of a row, in LDS: groups past the end of scale 1, codes past the end 0 (X).  valid: inputs of the line.
 __device__ __forceinline__ void end_scales(uint8_t* s, int valid) {
@@ -242,70 +212,99 @@ __device__ __forceinline__ void settle(floatx4_t (&acc)[MT][RT]) {
         for (int j = 0; j < RT; ++j) asm volatile("" : "+a"(acc[i][j]));
 }
 
-// Four consecutive outputs, those of them below `left`.
-__device__ __forceinline__ void store4(void* y, int32_t dtype, int64_t at, floatx4_t v, int64_t left) {
-    if (dtype == QK_F32) {
+// N consecutive outputs (4 or 8), those of them below `left`.
+template <int DT, int N>
+__device__ __forceinline__ void store_row(void* y, int64_t at, const float (&v)[N], int64_t left) {
+    if constexpr (DT == QK_F32) {
         float* p = static_cast<float*>(y) + at;
-        if (left >= 4) {
-            __builtin_memcpy(p, &v, 16);
+        if (left >= N) {
+            __builtin_memcpy(p, v, 4 * N);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < N; ++i)
                 if (i < left) p[i] = v[i];
         }
     } else {
-        u32x2_t d;
         typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-        if (dtype == QK_BF16) d = (u32x2_t){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        else d = (u32x2_t){__builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)v[0], (_Float16)v[1]}),
-                           __builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)v[2], (_Float16)v[3]})};
+        uint32_t d[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i)
+            d[i] = DT == QK_BF16 ? pack_bf16x2(v[2 * i], v[2 * i + 1])
+                                 : __builtin_bit_cast(uint32_t, (f16x2_t){(_Float16)v[2 * i], (_Float16)v[2 * i + 1]});
         uint16_t* p = static_cast<uint16_t*>(y) + at;
-        if (left >= 4) {
-            __builtin_memcpy(p, &d, 8);
+        if (left >= N) {
+            __builtin_memcpy(p, d, 2 * N);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < N; ++i)
                 if (i < left) p[i] = (uint16_t)(d[i >> 1] >> (16 * (i & 1)));
         }
     }
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+// g / (1 + exp(-g)) to a few steps of fp32, by e = exp(-|g|) <= 1: the exponent of 2 in two parts, a reciprocal improved
+// once.  (The library's exponential and a full division take a third of a tile's time.)
+__device__ __forceinline__ float silu(float g) {
+    const float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
+    const float a = -fabsf(g), t = a * kLog2e;
+    const float low = fmaf(a, kLog2eLow, fmaf(a, kLog2e, -t));
+    const float p = __builtin_amdgcn_exp2f(t), e = fmaf(p, low * kLn2, p), d = 1.0f + e;
+    const float r = __builtin_amdgcn_rcpf(d), q = fmaf(fmaf(-d, r, 1.0f), r, r);
+    return g * (g >= 0.0f ? q : e * q);
+}
 
-// Outputs of one wave: acc[i][j], rows 16 i + lane % 16 of the wave's rows m, columns 16 j + 4 (lane / 16) + q of its n
-// (up: the second half of the j are the up products of the first).
-template <Mode MODE, int MT, int RT>
-__device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, int m, int n, floatx4_t (&acc)[MT][RT]) {
+// Which of a wave's columns line q of its W lines is.  Of every two neighbouring blocks of 16 the lines alternate by fours,
+// so that a lane's 4 outputs of the one and 4 of the other are neighbours: 8 of a row.
+__device__ __forceinline__ int column_of(int q) { return (q & ~31) | ((q >> 2 & 3) << 3) | ((q >> 4 & 1) << 2) | (q & 3); }
+
+// Outputs of one wave: acc[i][j], rows 16 i + lane % 16 of the wave's rows m, columns 4 (lane / 16) + q of block j of its n (up:
+// the second half of the blocks are the up products of the first).
+template <Mode MODE, int DT, bool kWhole, int MT, int RT>
+__device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, int m, int n, const floatx4_t (&acc)[MT][RT]) {
     const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
-    constexpr int kCols = MODE == kUp ? RT / 2 : RT;
+    constexpr int kCols = MODE == kUp ? RT / 2 : RT, kPair = kCols % 2 == 0 ? 2 : 1, kN = 4 * kPair;
+    const int64_t col0 = t.n0 + n + kN * h;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int pos = m + 16 * i + r;
-        if (pos >= t.count) continue;
+        if (!kWhole && pos >= t.count) continue;
         int64_t row;
         float wt = 1.0f;
         if constexpr (MODE == kDense) {
             row = t.m0 + pos;
         } else {
-            row = a.plan[moe_plan_list(a.E) + t.m0 + pos];
+            row = a.list[t.m0 + pos];
             if constexpr (MODE == kDown) wt = t.expert < a.E ? a.weights[row] : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-            const int64_t col = t.n0 + n + 16 * j + 4 * h;
-            if (col >= a.N) continue;
-            floatx4_t v = acc[i][j];
-            if constexpr (MODE == kUp) {
+        for (int j = 0; j < kCols; j += kPair) {
+            const int64_t col = col0 + 16 * j;
+            if (!kWhole && col >= a.N) continue;
+            float v[kN];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = silu(v[q]) * acc[i][j + RT / 2][q];
+            for (int q = 0; q < kN; ++q) {
+                const int b = j + q / 4;
+                v[q] = acc[i][b][q % 4];
+                if constexpr (MODE == kUp) v[q] = silu(v[q]) * acc[i][b + RT / 2][q % 4];
+                if constexpr (MODE == kDown) v[q] *= wt;
             }
-            if constexpr (MODE == kDown) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] *= wt;
-            }
-            store4(a.y, MODE == kDown ? QK_F32 : a.y_dtype, row * a.N + col, v, a.N - col);
+            store_row<DT, kN>(a.y, row * a.N + col, v, kWhole ? kN : a.N - col);
         }
     }
+}
+
+template <Mode MODE, bool kWhole, int MT, int RT>
+__device__ __forceinline__ void store_typed(const GemmArgs& a, const Tile& t, int m, int n, const floatx4_t (&acc)[MT][RT]) {
+    if (MODE == kDown || a.y_dtype == QK_F32) store_outputs<MODE, QK_F32, kWhole>(a, t, m, n, acc);
+    else if (a.y_dtype == QK_BF16) store_outputs<MODE, QK_BF16, kWhole>(a, t, m, n, acc);
+    else store_outputs<MODE, QK_F16, kWhole>(a, t, m, n, acc);
+}
+
+template <Mode MODE, int MT, int RT>
+__device__ __forceinline__ void store_wave(const GemmArgs& a, const Tile& t, int m, int n, const floatx4_t (&acc)[MT][RT]) {
+    const bool whole = m + 16 * MT <= t.count && t.n0 + n + 16 * (MODE == kUp ? RT / 2 : RT) <= a.N;
+    if (whole) store_typed<MODE, true>(a, t, m, n, acc);
+    else store_typed<MODE, false>(a, t, m, n, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -314,26 +313,28 @@ __device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, 
 //
 // A stage is two halves of WM / 16 x WN / 16 instructions.  While a half is multiplied, row of fragments by row, the X
 // fragments of the row after next and the W fragments of the next half are read from LDS, in the order written here (the
-// scheduling barriers keep it).  Two rows before a stage ends all waves meet: their reads of it are done, the next one has
-// landed; behind that the copies of the stage after next go where this one was, and have nearly a stage's time.
+// scheduling barriers keep it).  Between the halves, when the W lines of the stage have been read, all waves meet, and the W
+// lines of the stage after next start on their way to the same place; two rows before the stage ends they meet again: the
+// next stage has landed, and the X lines of the stage after next follow.
 // ---------------------------------------------------------------------------
 template <Mode MODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(GemmArgs a) {
     constexpr int kWaves = (BM / WM) * (BN / WN), kThreads = kWaves * 64;
-    constexpr int kLines = BM + BN;
     constexpr int MT = WM / 16, RT = WN / 16;
-    constexpr int kLoads = kLines / 8 / kWaves, kXLoads = BM / 8 / kWaves;      // copies of codes, per wave
-    constexpr int kSLoads = kLines / 32 / kWaves;                               // of scales
-    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && kLines % (32 * kWaves) == 0 && BM % 32 == 0);
+    static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && BM % 64 == 0 && BN % 64 == 0);
     constexpr int kBNo = MODE == kUp ? BN / 2 : BN;
-    // rows of X, then rows of W, 128 bytes each; then their scales, 8 bytes each
-    __shared__ __align__(16) uint8_t lds0[kLines * 136];
-    __shared__ __align__(16) uint8_t lds1[kLines * 136];
+    // codes of X and of W by the parity of the stage, 128 bytes a line (objects of their own: the compiler waits for copies on
+    // their way to the object that it reads from); scales of two stages, 16 bytes a line, by the parity of the pair
+    __shared__ __align__(16) uint8_t x0[BM * 128];
+    __shared__ __align__(16) uint8_t w0[BN * 128];
+    __shared__ __align__(16) uint8_t x1[BM * 128];
+    __shared__ __align__(16) uint8_t w1[BN * 128];
+    __shared__ __align__(16) uint8_t sc[2 * (BM + BN) * 16];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / (BN / WN), wn = wave % (BN / WN);
     const int r = lane & 15, h = lane >> 4;
-    const Tile t = MODE == kDense ? dense_tile<BM, BN>(a) : expert_tile<BM, kBNo>(a);
+    const Tile t = find_tile<MODE != kDense, BM, kBNo>(a);
     if (t.count <= 0) return;
     floatx4_t acc[MT][RT];
 #pragma unroll
@@ -344,38 +345,51 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
     if (MODE == kDense || t.expert < a.E) {
         const Operands<MODE> op(a, t);
         auto w_row = [&](int b) {                       // row b of the tile's W lines
-            const int q = b % WN;
-            return MODE == kUp ? op.w_row(b / WN * (WN / 2) + q % (WN / 2), q >= WN / 2) : op.w_row(b, false);
+            const int q = column_of(b % WN);
+            return MODE == kUp ? op.w_row(b / WN * (WN / 2) + q % (WN / 2), q >= WN / 2) : op.w_row(b / WN * WN + q, false);
         };
-        // what this lane copies: row l / 8 of 8, slot l % 8
-        uint32_t voff[kLoads], soff[kSLoads];
+        // what this lane copies: line l / 8 of 8, slot l % 8
+        constexpr int kXCopies = BM / 8 / kWaves, kWCopies = BN / 8 / kWaves, kSLoads = (BM + BN + kThreads - 1) / kThreads;
+        uint32_t xoff[kXCopies], woff[kWCopies], soff[kSLoads];
 #pragma unroll
-        for (int v = 0; v < kLoads; ++v) {
-            const int line = 8 * (wave + kWaves * v) + (lane >> 3), piece = slot_of(line, lane & 7);
-            voff[v] = v < kXLoads ? op.x_row(line) * (uint32_t)a.x.code_stride + 16 * piece
-                                  : w_row(line - BM) * (uint32_t)a.w.code_stride + 16 * piece;
+        for (int k = 0; k < kWCopies; ++k) {
+            const int line = 8 * (wave + kWaves * k) + (lane >> 3);
+            woff[k] = w_row(line) * (uint32_t)a.w.code_stride + 16 * piece_in(line, lane & 7);
         }
 #pragma unroll
-        for (int v = 0; v < kSLoads; ++v) {
-            const int line = 32 * (wave + kWaves * v) + (lane >> 1);
-            soff[v] = 4 * (lane & 1) + (line < BM ? op.x_row(line) * (uint32_t)a.x.scale_stride
-                                                  : w_row(line - BM) * (uint32_t)a.w.scale_stride);
+        for (int k = 0; k < kXCopies; ++k) {
+            const int line = 8 * (wave + kWaves * k) + (lane >> 3);
+            xoff[k] = op.x_row(line) * (uint32_t)a.x.code_stride + 16 * piece_in(line, lane & 7);
+        }
+        // and the lines whose scales it loads
+#pragma unroll
+        for (int k = 0; k < kSLoads; ++k) {
+            const int line = tid + kThreads * k;
+            soff[k] = line < BM ? op.x_row(line) * (uint32_t)a.x.scale_stride
+                                : w_row(min(line - BM, BN - 1)) * (uint32_t)a.w.scale_stride;
         }
         const int nst = (a.x.cols + kLineK - 1) / kLineK;
-        // Copy v of stage st, which is line `line`; past the last stage every offset is outside its buffer, and nothing is
-        // read.
-        auto copy = [&](uint8_t* dst, int st, int line, int v) {
-            const uint32_t out = st < nst ? 0u : 0xFFFF0000u;
-            if (v < kLoads) {
-                to_lds(v < kXLoads ? op.xc : op.wc, dst + (wave + kWaves * v) * 1024, voff[v] | out, st < nst ? 128u * line : 0u);
-            } else {
-                const int u = v - kLoads;
-                const bool x = 32 * (wave + kWaves * u) < BM;
-                to_lds4(x ? op.xs : op.ws, dst + kLines * 128 + (wave + kWaves * u) * 256, soff[u] | out, st < nst ? 8u * line : 0u);
-            }
+        // Copy k of stage st, which is line `line`; past the last stage every offset is outside its buffer, and zeros are
+        // written.
+        auto copy_x = [&](uint8_t* dst, int st, int line, int k) {
+            to_lds(op.xc, dst + (wave + kWaves * k) * 1024, xoff[k] | (st < nst ? 0u : 0xFFFF0000u), st < nst ? 128u * line : 0u);
         };
-        const int xline = (wm * WM + r) * 128, wline = (BM + wn * WN + r) * 128;
-        const int xsc = kLines * 128 + (wm * WM + r) * 8 + 2 * h, wsc = kLines * 128 + (BM + wn * WN + r) * 8 + 2 * h;
+        auto copy_w = [&](uint8_t* dst, int st, int line, int k) {
+            to_lds(op.wc, dst + (wave + kWaves * k) * 1024, woff[k] | (st < nst ? 0u : 0xFFFF0000u), st < nst ? 128u * line : 0u);
+        };
+        // Scales come 16 bytes a line at a time, those of two stages, through registers: a line of memory that is brought for
+        // 8 of its bytes costs as much as one of codes.
+        u32x4_t sv[kSLoads];
+        auto scale_load = [&](int k, uint32_t at) {
+            const bool x = 64 * wave + kThreads * k < BM;
+            return __builtin_amdgcn_raw_buffer_load_b128(x ? op.xs : op.ws, (int)soff[k], (int)at, 0);
+        };
+        auto scale_store = [&](int pair, int k) {
+            if (64 * wave + kThreads * k >= BM + BN) return;
+            *reinterpret_cast<u32x4_t*>(sc + (pair & 1) * ((BM + BN) * 16) + (tid + kThreads * k) * 16) = sv[k];
+        };
+        const int xline = (wm * WM + r) * 128, wline = (wn * WN + r) * 128;
+        const int xsc = (wm * WM + r) * 16 + 2 * h, wsc = (BM + wn * WN + r) * 16 + 2 * h;
         const int at0 = 16 * slot_of(r, 2 * h), at1 = 16 * slot_of(r, 2 * h + 1);
         // fragments of W by half; those of X, of which four are enough; scales by the parity of the stage
         v4i_t wf[2][RT], xf[4];
@@ -386,52 +400,70 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
         auto read_w = [&](const uint8_t* src, int s, int j) {
             wf[s][j] = *reinterpret_cast<const v4i_t*>(src + wline + (s ? at1 : at0) + 2048 * j);
         };
-        auto read_scale = [&](const uint8_t* src, int p, int n) {
-            if (n < RT) ws[p][n] = *reinterpret_cast<const uint16_t*>(src + wsc + 128 * n);
-            else xs[p][n - RT] = *reinterpret_cast<const uint16_t*>(src + xsc + 128 * (n - RT));
+        auto read_scale = [&](int st, int p, int n) {
+            const uint8_t* src = sc + (st >> 1 & 1) * ((BM + BN) * 16) + 8 * p;
+            if (n < RT) ws[p][n] = *reinterpret_cast<const uint16_t*>(src + wsc + 256 * n);
+            else xs[p][n - RT] = *reinterpret_cast<const uint16_t*>(src + xsc + 256 * (n - RT));
         };
         static_assert(MT % 4 == 0);
         constexpr int kOps = MT * RT, kTail = 2 * RT;                 // instructions of a half; of it behind the meeting
-        constexpr int kCopies = kLoads + kSLoads, kEarly = kCopies / 2;
         // Items 0..n-1 spread over instructions [from, to): those behind instruction o.
         auto spread = [](auto O, auto From, auto To, auto N, auto&& item) {
             constexpr int o = decltype(O)::value - decltype(From)::value, ops = decltype(To)::value - decltype(From)::value;
             constexpr int n = decltype(N)::value;
+            static_assert(ops > 0);
             if constexpr (o >= 0 && o < ops) {
                 constexpr int k0 = (o * n + ops - 1) / ops, k1 = ((o + 1) * n + ops - 1) / ops;
                 each<k1 - k0>([&](auto K) { item(k0 + decltype(K)::value); });
             }
         };
-        auto meet = [&] {
-            __builtin_amdgcn_s_waitcnt(0);
+        // Waves meet once all but the last `flying` copies of each have landed and its reads are done.
+        auto meet = [&](auto Flying) {
+            constexpr int n = decltype(Flying)::value;
+            __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x70);   // vmcnt(n) expcnt(7) lgkmcnt(0)
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
         };
-        auto stage = [&](auto P, uint8_t* cur, uint8_t* next, int st) {
+        constexpr int kXEarly = kXCopies / 4;                         // of the copies of X before the next stage begins
+        typedef std::integral_constant<int, kXEarly> XEarly;
+        typedef std::integral_constant<int, kWCopies> WCopies;
+        auto stage = [&](auto P, uint8_t* x, uint8_t* w, uint8_t* xnext, uint8_t* wnext, int st) {
             constexpr int p = decltype(P)::value;
             each<2>([&](auto S) {
                 constexpr int s = decltype(S)::value;
                 each<kOps>([&](auto O) {
                     constexpr int o = decltype(O)::value, i = o / RT, j = o % RT;
-                    if constexpr (s == 1 && o == kOps - kTail) meet();
+                    if constexpr (s == 1 && o == 0) meet(std::integral_constant<int, 63>{});
+                    if constexpr (s == 1 && o == kOps - kTail) meet(WCopies{});
                     mfma_in_place<s>(acc[i][j], wf[s][j], ws[p][j], xf[i % 4], xs[p][i]);
                     if constexpr (j == 0) {
-                        if constexpr (i + 2 < MT) read_x(cur, s, i + 2);
-                        else read_x(s == 0 ? cur : next, 1 - s, i + 2 - MT);
+                        if constexpr (i + 2 < MT) read_x(x, s, i + 2);
+                        else read_x(s == 0 ? x : xnext, 1 - s, i + 2 - MT);
                     }
                     typedef std::integral_constant<int, 0> Begin;
                     typedef std::integral_constant<int, kOps - kTail> Meeting;
                     typedef std::integral_constant<int, kOps> End;
                     if constexpr (s == 0) {
-                        spread(O, Begin{}, Meeting{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(cur, 1, k); });
-                        spread(O, Begin{}, std::integral_constant<int, kTail>{}, std::integral_constant<int, kCopies - kEarly>{},
-                               [&](int k) { copy(next, st + 1, st, kEarly + k); });
+                        spread(O, Begin{}, std::integral_constant<int, kOps / 2>{}, std::integral_constant<int, kXCopies - kXEarly>{},
+                               [&](int k) { copy_x(xnext, st + 1, st, kXEarly + k); });
+                        // (p == 0: scales of stages st + 2 and st + 3)
+                        if constexpr (p == 0)
+                            spread(O, std::integral_constant<int, kOps / 2>{}, End{}, std::integral_constant<int, kSLoads>{},
+                                   [&](int k) { sv[k] = scale_load(k, 8u * (st + 1)); });
+                        spread(O, Begin{}, Meeting{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(w, 1, k); });
                     } else {
-                        spread(O, Meeting{}, End{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(next, 0, k); });
-                        spread(O, Meeting{}, End{}, std::integral_constant<int, RT + MT>{}, [&](int k) { read_scale(next, 1 - p, k); });
-                        spread(O, Meeting{}, End{}, std::integral_constant<int, kEarly>{}, [&](int k) { copy(cur, st + 2, st + 1, k); });
+                        if constexpr (p == 1)
+                            spread(O, Begin{}, Meeting{}, std::integral_constant<int, kSLoads>{}, [&](int k) {
+                                // the second of the pair may be past the end: its codes are zeros, but not its scales
+                                if (st + 2 >= nst) sv[k][2] = sv[k][3] = 0;
+                                scale_store((st + 1) >> 1, k);
+                            });
+                        spread(O, Begin{}, Meeting{}, WCopies{}, [&](int k) { copy_w(w, st + 2, st + 1, k); });
+                        spread(O, Meeting{}, End{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(wnext, 0, k); });
+                        spread(O, Meeting{}, End{}, std::integral_constant<int, RT + MT>{}, [&](int k) { read_scale(st + 1, 1 - p, k); });
+                        spread(O, Meeting{}, End{}, XEarly{}, [&](int k) { copy_x(x, st + 2, st + 1, k); });
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 });
@@ -440,35 +472,47 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
         // the last line, which may end early, comes first
         const int valid = a.x.cols - (nst - 1) * kLineK;              // inputs of it
 #pragma unroll
-        for (int v = 0; v < kCopies; ++v) copy(lds0, 0, nst - 1, v);
-        meet();
+        for (int k = 0; k < kWCopies; ++k) copy_w(w0, 0, nst - 1, k);
 #pragma unroll
-        for (int v = 0; v < kEarly; ++v) copy(lds1, 1, 0, v);
-        if (valid < kLineK) {
-            for (int l = tid; l < kLines; l += kThreads) {
-                end_scales(lds0 + kLines * 128 + 8 * l, valid);
-                if (l < BM) end_codes(lds0 + 128 * l, l, valid);
+        for (int k = 0; k < kXCopies; ++k) copy_x(x0, 0, nst - 1, k);
+#pragma unroll
+        for (int k = 0; k < kWCopies; ++k) copy_w(w1, 1, 0, k);
+#pragma unroll
+        for (int k = 0; k < kXEarly; ++k) copy_x(x1, 1, 0, k);
+        // scales of the first pair: the last line's, 1 past the end, then those of line 0
+#pragma unroll
+        for (int k = 0; k < kSLoads; ++k) {
+            const u32x4_t last = scale_load(k, 8u * (nst - 1)), first = scale_load(k, 0);
+            const int groups = (valid + kGroup - 1) / kGroup;
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const int n = groups - 4 * d;
+                const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+                sv[k][d] = (last[d] & keep) | (0x7F7F7F7Fu & ~keep);
+                sv[k][2 + d] = nst > 1 ? first[d] : 0u;
             }
-            __builtin_amdgcn_s_waitcnt(0xC07F);                       // LDS stores done, copies in flight left alone
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
+            scale_store(0, k);
+        }
+        meet(std::integral_constant<int, 0>{});
+        if (valid < kLineK) {
+            for (int l = tid; l < BM; l += kThreads) end_codes(x0 + 128 * l, l, valid);
+            __syncthreads();
         }
 #pragma unroll
-        for (int j = 0; j < RT; ++j) read_w(lds0, 0, j);
+        for (int j = 0; j < RT; ++j) read_w(w0, 0, j);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) read_x(lds0, 0, i);
+        for (int i = 0; i < 2; ++i) read_x(x0, 0, i);
 #pragma unroll
-        for (int k = 0; k < RT + MT; ++k) read_scale(lds0, 0, k);
+        for (int k = 0; k < RT + MT; ++k) read_scale(0, 0, k);
         // (an odd number of stages is one more of zeros: a way out between the two costs the compiler the registers)
         for (int st = 0; st < nst; st += 2) {
-            stage(std::integral_constant<int, 0>{}, lds0, lds1, st);
-            stage(std::integral_constant<int, 1>{}, lds1, lds0, st + 1);
+            stage(std::integral_constant<int, 0>{}, x0, w0, x1, w1, st);
+            stage(std::integral_constant<int, 1>{}, x1, w1, x0, w0, st + 1);
         }
         __builtin_amdgcn_s_waitcnt(0);                                // nothing on its way to LDS any more
         settle<MT, RT>(acc);
     }
-    store_outputs<MODE>(a, t, wm * WM, MODE == kUp ? wn * (WN / 2) : wn * WN, acc);
+    store_wave<MODE>(a, t, wm * WM, MODE == kUp ? wn * (WN / 2) : wn * WN, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -491,7 +535,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_kernel(GemmArgs a) {
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, h = lane >> 4;
-    const Tile t = MODE == kDense ? dense_tile<16 * MT, kBNo>(a) : expert_tile<16 * MT, kBNo>(a);
+    const Tile t = find_tile<MODE != kDense, 16 * MT, kBNo>(a);
     if (t.count <= 0) return;
     floatx4_t acc[MT][RT];
 #pragma unroll
@@ -501,11 +545,15 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_kernel(GemmArgs a) {
 
     if (MODE == kDense || t.expert < a.E) {
         const Operands<MODE> op(a, t);
-        auto w_row = [&](int b) { return MODE == kUp ? op.w_row(b % (8 * RT), b >= 8 * RT) : op.w_row(b, false); };
+        auto w_row = [&](int b) {
+            if constexpr (MODE == kUp && RT == 2) return op.w_row(b % 16, b >= 16);
+            const int q = column_of(b);
+            return MODE == kUp ? op.w_row(q % (8 * RT), q >= 8 * RT) : op.w_row(q, false);
+        };
         uint32_t voff[kLoads], soff[kSLoads];
 #pragma unroll
         for (int v = 0; v < kLoads; ++v) {
-            const int line = 8 * v + (lane >> 3), piece = slot_of(line, lane & 7);
+            const int line = 8 * v + (lane >> 3), piece = piece_in(line, lane & 7);
             voff[v] = v < 2 * MT ? op.x_row(line) * (uint32_t)a.x.code_stride + 16 * piece
                                  : w_row(line - 16 * MT) * (uint32_t)a.w.code_stride + 16 * piece;
         }
@@ -607,7 +655,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_kernel(GemmArgs a) {
             }
     }
     if (wave > 0) return;
-    store_outputs<MODE>(a, t, 0, 0, acc);
+    store_wave<MODE>(a, t, 0, 0, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -635,7 +683,10 @@ __global__ __launch_bounds__(kCombineThreads) void moe_combine_mx4_kernel(const 
         }
         sum += v;
     }
-    store4(y, dtype, tok * H + col, sum, left);
+    const float out[4] = {sum[0], sum[1], sum[2], sum[3]};
+    if (dtype == QK_F32) store_row<QK_F32, 4>(y, tok * H + col, out, left);
+    else if (dtype == QK_BF16) store_row<QK_BF16, 4>(y, tok * H + col, out, left);
+    else store_row<QK_F16, 4>(y, tok * H + col, out, left);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -666,13 +717,14 @@ hipError_t launch_few(const GemmArgs& a, hipStream_t s) {
 
 template <Mode MODE>
 hipError_t launch_any(const GemmArgs& a, hipStream_t s) {
-    // rows that meet a weight: of the product, or of an expert on average
-    const int64_t rows = MODE == kDense ? a.M : cdiv(a.slots, std::min<int64_t>(a.E, a.slots));
+    // rows that meet a weight: of the product, or the rows of the plan's tiles
+    const int64_t rows = MODE == kDense ? a.M : moe_tile_rows(a.slots, a.E);
     if (rows <= 16) return launch_few<MODE, 1, 2>(a, s);
     if (rows <= 32) return launch_few<MODE, 2, 2>(a, s);
     if (rows <= 64) return launch_few<MODE, 4, 2>(a, s);
-    if (grid_for<MODE>(a, 256, MODE == kUp ? 128 : 256) < device_cu_count()) return launch_tile<MODE, 128, 128, 64, 64>(a, s);
-    return launch_tile<MODE, 256, 256, 128, 128>(a, s);
+    if constexpr (MODE == kDense)
+        if (grid_for<MODE>(a, 256, 256) >= device_cu_count()) return launch_tile<MODE, 256, 256, 128, 128>(a, s);
+    return launch_tile<MODE, 128, 128, 64, 64>(a, s);
 }
 
 }  // namespace
@@ -694,9 +746,9 @@ GemmArgs expert_args(const qk_mx4_state* x, const qk_mx4_state* w, const int32_t
     GemmArgs a{};
     a.x = view(x);
     a.w = view(w);
-    a.plan = plan;
-    a.top_k = top_k;
     a.E = E;
+    a.list = plan + moe_plan_list(E);
+    a.per_token = top_k == 1 ? 0 : (uint32_t)(((1ull << 32) + top_k - 1) / top_k);
     a.w_rows = w->rows / E;
     return a;
 }
@@ -706,6 +758,7 @@ hipError_t launch_moe_up_mx4(const qk_mx4_state* x, const qk_mx4_state* gate_up,
                              int32_t E, void* h, int32_t h_dtype, hipStream_t s) {
     GemmArgs a = expert_args(x, gate_up, plan, top_k, E);
     a.slots = (int32_t)(x->rows * top_k);
+    a.tiles = plan + moe_plan_tiles(E, a.slots);
     a.y = h;
     a.y_dtype = h_dtype;
     a.N = a.w_rows / 2;
@@ -718,6 +771,7 @@ hipError_t launch_moe_down_mx4(const qk_mx4_state* h, const qk_mx4_state* down, 
                                int32_t top_k, int32_t E, void* y, int32_t y_dtype, void* workspace, hipStream_t s) {
     GemmArgs a = expert_args(h, down, plan, top_k, E);
     a.slots = (int32_t)h->rows;
+    a.tiles = plan + moe_plan_tiles(E, a.slots);
     a.y = workspace;
     a.weights = weights;
     a.N = a.w_rows;

@@ -253,8 +253,26 @@ struct MoeRouteBackwardArgs {
     float scale;
 };
 hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs& a, hipStream_t s);
-// Plan: E + 1 first places, padded to a multiple of 4, then the slots.
+// Plan of a routing: E + 1 first places, padded to a multiple of 4 numbers; the slots, padded alike; how many tiles there are,
+// padded alike; the tiles: rows of the list of one expert (E: of none) that the products take together.
+struct MoeTile {
+    int32_t first;
+    int32_t expert_count;     // expert | count << 16
+};
 constexpr int64_t moe_plan_list(int32_t E) { return (int64_t)(E + 4) / 4 * 4; }
+constexpr int64_t moe_plan_tiles(int32_t E, int64_t slots) { return moe_plan_list(E) + (slots + 3) / 4 * 4; }
+// Rows of a tile, at most: the least of 16, 32, 64 and 128 that hold an expert's rows on average (more: half of the last
+// tile of an expert is idle; fewer: its weights are read again).
+constexpr int64_t moe_tile_rows(int64_t slots, int32_t E) {
+    const int64_t rows = (slots + (E < slots ? E : slots) - 1) / (E < slots ? E : slots);
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+constexpr int64_t moe_most_tiles(int64_t slots, int32_t E) {
+    return slots / moe_tile_rows(slots, E) + (E + 1 < slots ? E + 1 : slots);
+}
+constexpr int64_t moe_plan_words(int64_t slots, int32_t E) {
+    return moe_plan_tiles(E, slots) + 4 + 2 * moe_most_tiles(slots, E);
+}
 hipError_t launch_moe_plan(const int32_t* ids, int64_t slots, int32_t E, int32_t* plan, hipStream_t s);
 hipError_t launch_moe_up_mx4(const qk_mx4_state* x, const qk_mx4_state* gate_up, const int32_t* plan, int32_t top_k,
                              int32_t E, void* h, int32_t h_dtype, hipStream_t s);

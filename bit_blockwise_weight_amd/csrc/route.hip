@@ -236,46 +236,104 @@ __global__ __launch_bounds__(kThreads) void moe_route_backward_kernel(MoeRouteBa
 }
 
 // ---------------------------------------------------------------------------
-// Plan: workgroup e finds where expert e starts (how many slots go to lower experts) and lists its slots in order;
-// workgroup E those without an expert.  Nothing is shared between workgroups, so nothing depends on their order.
+// Plan: every workgroup counts the slots of all experts (whole numbers in LDS: their order does not matter) and finds from
+// the sums where each expert starts; workgroup e lists the slots of expert e in order and cuts them into tiles, workgroup E
+// those without an expert.  Nothing is shared between workgroups.  A thread takes kPer consecutive slots at a time.
 // ---------------------------------------------------------------------------
-template <int kBlock>
-__global__ __launch_bounds__(kBlock) void moe_plan_kernel(const int32_t* __restrict__ ids, int32_t slots, int32_t E,
+template <int kBlock, int kPer>
+__global__ __launch_bounds__(kBlock) void moe_plan_kernel(const int32_t* __restrict__ ids, int32_t slots, int32_t E, int32_t rows,
                                                           int32_t* __restrict__ plan) {
-    constexpr int kWaves = kBlock / 64;
-    __shared__ int32_t part[kWaves];
+    constexpr int kWaves = kBlock / 64, kBins = 576;               // of E + 1 <= 513, in whole waves
+    __shared__ int32_t bins[kBins];
+    __shared__ int32_t part[2][kBins / 64], part2[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int e = (int)blockIdx.x;
-    // expert of a slot, E for none
-    auto expert = [&](int i) {
-        const int v = ids[i];
-        return v < 0 || v >= E ? E : v;
-    };
-    int less = 0;
-    for (int i = tid; i < slots; i += kBlock) less += expert(i) < e;
-    less = wave_scan(less);
-    if (lane == 63) part[wave] = less;
+    for (int i = tid; i < kBins; i += kBlock) bins[i] = 0;
     __syncthreads();
-    int at = 0;
+    // the experts (E: none) of slots base .. base + kPer - 1; -1 past the end
+    auto load = [&](int64_t base, int (&v)[kPer]) {
+        if (base + kPer <= slots) {
+            __builtin_memcpy(v, ids + base, 4 * kPer);
+        } else {
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) at += part[w];
-    if (tid == 0) plan[e] = at;
+            for (int i = 0; i < kPer; ++i) v[i] = base + i < slots ? ids[base + i] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] = base + i >= slots ? -1 : v[i] < 0 || v[i] >= E ? E : v[i];
+    };
+    for (int64_t base = (int64_t)tid * kPer; base < slots; base += kBlock * kPer) {
+        int v[kPer];
+        load(base, v);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (v[i] >= 0) atomicAdd(&bins[v[i]], 1);
+    }
+    __syncthreads();
+    // sums of the slots and the tiles of the bins below one's own, 64 bins a wave
+    constexpr int kTurns = (kBins / 64 + kWaves - 1) / kWaves;
+    int n[kTurns], before[kTurns], tiles[kTurns];
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+        const int g = wave + kWaves * u;
+        n[u] = before[u] = tiles[u] = 0;
+        if (g >= kBins / 64) continue;
+        n[u] = bins[64 * g + lane];
+        before[u] = wave_scan(n[u]);
+        tiles[u] = wave_scan((n[u] + rows - 1) / rows);
+        if (lane == 63) {
+            part[0][g] = before[u];
+            part[1][g] = tiles[u];
+        }
+    }
+    __syncthreads();
+    int at = 0, tile0 = 0, mine = 0;
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+        const int g = wave + kWaves * u;
+        if (g >= kBins / 64) continue;
+        for (int w = 0; w < g; ++w) {
+            before[u] += part[0][w];
+            tiles[u] += part[1][w];
+        }
+        if (64 * g + lane == e) {                                   // hands its numbers to the workgroup
+            bins[0] = before[u] - n[u];
+            bins[1] = tiles[u] - (n[u] + rows - 1) / rows;
+            bins[2] = n[u];
+        }
+    }
+    __syncthreads();
+    at = bins[0];
+    tile0 = bins[1];
+    mine = bins[2];
+    int32_t* const tiles_at = plan + moe_plan_tiles(E, slots);
+    const int own_tiles = (mine + rows - 1) / rows;
+    if (tid == 0) {
+        plan[e] = at;
+        if (e == E) tiles_at[0] = tile0 + own_tiles;
+    }
+    MoeTile* const table = reinterpret_cast<MoeTile*>(tiles_at + 4);
+    for (int i = tid; i < own_tiles; i += kBlock)
+        table[tile0 + i] = MoeTile{at + i * rows, e | (mine - i * rows < rows ? mine - i * rows : rows) << 16};
     int32_t* list = plan + moe_plan_list(E);
-    for (int base = 0; base < slots; base += kBlock) {
-        const int i = base + tid;
-        const bool mine = i < slots && expert(i) == e;
-        const uint64_t b = __ballot(mine);
+    for (int64_t first = 0; first < slots; first += kBlock * kPer) {
+        const int64_t base = first + (int64_t)tid * kPer;
+        int v[kPer], count = 0;
+        load(base, v);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) count += v[i] == e;
+        const int incl = wave_scan(count);
         __syncthreads();
-        if (lane == 0) part[wave] = __builtin_popcountll(b);
+        if (lane == 63) part2[wave] = incl;
         __syncthreads();
-        int before = 0, all = 0;
+        int place = at + incl - count;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            before += w < wave ? part[w] : 0;
-            all += part[w];
+            place += w < wave ? part2[w] : 0;
+            at += part2[w];
         }
-        if (mine) list[at + before + __builtin_popcountll(b & ((1ull << lane) - 1))] = i;
-        at += all;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (v[i] == e) list[place++] = (int32_t)(base + i);
     }
 }
 
@@ -302,8 +360,10 @@ hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs& a, hipStream_t 
 }
 
 hipError_t launch_moe_plan(const int32_t* ids, int64_t slots, int32_t E, int32_t* plan, hipStream_t s) {
-    if (slots <= 2048) moe_plan_kernel<256><<<dim3((unsigned)E + 1), 256, 0, s>>>(ids, (int32_t)slots, E, plan);
-    else moe_plan_kernel<1024><<<dim3((unsigned)E + 1), 1024, 0, s>>>(ids, (int32_t)slots, E, plan);
+    const int32_t rows = (int32_t)moe_tile_rows(slots, E);
+    const dim3 grid((unsigned)E + 1);
+    if (slots <= 512) moe_plan_kernel<256, 2><<<grid, 256, 0, s>>>(ids, (int32_t)slots, E, rows, plan);
+    else moe_plan_kernel<1024, 16><<<grid, 1024, 0, s>>>(ids, (int32_t)slots, E, rows, plan);
     return hipGetLastError();
 }
 

@@ -830,7 +830,8 @@ qk_status qk_moe_route_backward(const void* logits, int32_t dtype, int64_t T, in
  * qk_moe_plan — device.  Sorts the pairs (token, position) of a routing, slot t * top_k + j, by expert, for the experts'
  *   products: plan[0..E] are the first places of the experts in the list (plan[E]: the end of the last one), and the
  *   list follows at plan[4 * ceil((E + 1) / 4)], the slots of one expert in increasing order, behind the last expert's
- *   those whose id is outside 0..E-1.  An expert may occur more than once in a token.  Deterministic.
+ *   those whose id is outside 0..E-1.  What follows the list is the library's own.  An expert may occur more than once in a
+ *   token.  Deterministic.
  *   ids: device, int32 [T, top_k].   T: >= 1, T * top_k at most 2^26.   top_k: 1..32.   E: 1..512.
  *   plan: device, 16-byte aligned, qk_moe_plan_size() bytes, written; no overlap with ids.
  *   Errors: QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
