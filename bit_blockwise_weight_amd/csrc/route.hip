@@ -5,7 +5,8 @@
 //   experts whose two largest s + bias sum highest;  w = scale s, or scale s / (sum of the chosen s)
 //
 // One wave per token, expert e in lane e % 64.  Which of two ranks is larger is decided in binary64, so that a choice does
-// not hang on the rounding of s.
+// not hang on the rounding of s: the choice is made in 32 bits, and where two ranks or two groups are closer than the error of
+// that, made again in 64.  (All in 64 bits 8192 tokens of 256 experts take 44 us.)
 #include <cmath>
 
 #include "qk_device.h"
@@ -35,15 +36,32 @@ template <class T>
 __device__ __forceinline__ T wave_xor(T v, int mask) {
     return __shfl_xor(v, mask, 64);
 }
+template <int kCtrl, int kRows = 0xF>
+__device__ __forceinline__ double dpp_move(double old, double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v), o = __builtin_bit_cast(uint64_t, old);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)u, kCtrl, kRows, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)(o >> 32), (int)(uint32_t)(u >> 32), kCtrl, kRows, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Over the wave, in every lane: inside the rows of 16, then rows 0 and 2 into 1 and 3, then the lower half into the upper.
+template <class Op>
+__device__ __forceinline__ double wave_reduce(double v, double none, Op&& op) {
+    v = op(v, dpp_move<0xB1>(none, v));
+    v = op(v, dpp_move<0x4E>(none, v));
+    v = op(v, dpp_move<0x141>(none, v));
+    v = op(v, dpp_move<0x140>(none, v));
+    v = op(v, dpp_move<0x142, 0xA>(none, v));
+    v = op(v, dpp_move<0x143, 0xC>(none, v));
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 __device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v = fmax(v, wave_xor(v, m));
-    return v;
+    return wave_reduce(v, -INFINITY, [](double a, double b) { return fmax(a, b); });
 }
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += wave_xor(v, m);
-    return v;
+    return wave_reduce(v, 0.0, [](double a, double b) { return a + b; });
 }
 
 // The place of the largest of v[i] at lane l, as 64 i + l, the lowest of equal ones; best: its value.
@@ -104,11 +122,22 @@ __device__ __forceinline__ double share_of(double z, bool sigmoid) {
     return total > 0.0 ? r / total : 0.0;
 }
 
+// What a token's choice leaves in lane j: its expert j, that one's logit and, where weights are not renormalized, its score.
+struct Choice {
+    int id;
+    float z;
+    double s;
+};
+
+__device__ __forceinline__ float load_bias(const float* bias, int e, int E) {
+    const float b = bias && e < E ? bias[e] : 0.0f;
+    return b == b ? fminf(b, 3.402823466e38f) : -INFINITY;
+}
+
+// The choice in binary64 throughout.
 template <int V>
-__global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteArgs a) {
+__device__ __forceinline__ Choice choose_exactly(const MoeRouteArgs& a, int64_t t) {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * kTokens + threadIdx.x / 64;
-    if (t >= a.T) return;
     double z[V], s[V], key[V], ranked[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -118,10 +147,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteArgs a) {
     scores<V>(z, a.score == QK_SIGMOID, s);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = 64 * i + lane;
-        float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
-        b = b == b ? fminf(b, 3.402823466e38f) : -INFINITY;
-        ranked[i] = z[i] == -INFINITY ? -INFINITY : s[i] + (double)b;
+        ranked[i] = z[i] == -INFINITY ? -INFINITY : s[i] + (double)load_bias(a.bias, 64 * i + lane, a.E);
         key[i] = a.bias ? ranked[i] : z[i];
     }
     if (a.groups > 1) {
@@ -158,25 +184,236 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(MoeRouteArgs a) {
             if (e < a.E && !(kept >> (e / per) & 1)) key[i] = -INFINITY;
         }
     }
-    int id = -1;
-    double zj = -INFINITY, sj = 0.0;
+    Choice c{-1, -INFINITY, 0.0};
     for (int j = 0; j < a.top_k; ++j) {
         double best;
         const int e = wave_argmax<V>(key, best);
         if (best == -INFINITY) break;
         const double ze = pick<V>(z, e), se = pick<V>(s, e);
-        if (lane == j) {
-            id = e;
-            zj = ze;
-            sj = se;
-        }
+        if (lane == j) c = Choice{e, (float)ze, se};
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (64 * i + lane == e) key[i] = -INFINITY;
     }
-    const double w = a.renorm ? share_of(zj, a.score == QK_SIGMOID) : sj;
+    return c;
+}
+
+// Whole numbers in the order of the floats (of equal zeros one), 0 below all of them but -NaN.
+__device__ __forceinline__ uint32_t order_of(float f) {
+    const uint32_t u = as_uint(f + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float float_of(uint32_t k) { return as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+constexpr uint32_t kNone = 0x007FFFFFu;                             // order_of(-inf)
+
+template <int kCtrl, int kRows = 0xF>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kCtrl, kRows, 0xF, false));
+}
+// Largest of the wave, as a scalar: inside the rows of 16 lanes, then across them.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = dpp_max<0xB1>(v);
+    v = dpp_max<0x4E>(v);
+    v = dpp_max<0x141>(v);
+    v = dpp_max<0x140>(v);
+    v = dpp_max<0x142, 0xA>(v);
+    v = dpp_max<0x143, 0xC>(v);
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += wave_xor(v, m);
+    return v;
+}
+
+// The largest key and the lowest place that has it (64 i + lane), which is taken out.
+template <int V>
+__device__ __forceinline__ int take_best(uint32_t (&key)[V], uint32_t& best) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) m = max(m, key[i]);
+    best = wave_max(m);
+    int at = 0;
+    uint64_t who = 0;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) {
+        const uint64_t b = __ballot(key[i] == best);
+        if (b) {
+            at = i;
+            who = b;
+        }
+    }
+    who &= -who;
+    const bool mine = (threadIdx.x & 63) == (uint32_t)__builtin_ctzll(who);
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = at == i && mine ? kNone : key[i];
+    return 64 * at + (int)__builtin_ctzll(who);
+}
+
+// The choice in 32 bits, for groups of 2^n experts; false where two ranks, or two groups, are too close for that.
+//   A score in 32 bits is off by less than 2^-20: its exponential by the rounding of the argument, 2^-24 |z - max| of itself, of
+// which x exp(-x) < 0.4 is left, and two steps; the sum of 512 of them by 2^-20 of itself, being made in a tree.  Added to a
+// bias it is rounded to 2^-24 of itself.
+__device__ __forceinline__ float slack(float rank) { return 4.0f * (9.5367431640625e-7f + 1.1920929e-7f * fabsf(rank)); }
+
+// The two largest of groups of lanes, joined across lanes that a DPP pattern pairs.
+__device__ __forceinline__ void join(uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
+    a2 = max(min(a1, b1), max(a2, b2));
+    a1 = max(a1, b1);
+}
+template <int kCtrl>
+__device__ __forceinline__ void join_dpp(uint32_t& a1, uint32_t& a2) {
+    join(a1, a2, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a1, kCtrl, 0xF, 0xF, true),
+         (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a2, kCtrl, 0xF, 0xF, true));
+}
+template <int V>
+__device__ __forceinline__ void join_groups(uint32_t (&m1)[V], uint32_t (&m2)[V], int per) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (per > 1) join_dpp<0xB1>(m1[i], m2[i]);
+        if (per > 2) join_dpp<0x4E>(m1[i], m2[i]);
+        if (per > 4) join_dpp<0x141>(m1[i], m2[i]);
+        if (per > 8) join_dpp<0x140>(m1[i], m2[i]);
+        if (per > 16) join(m1[i], m2[i], (uint32_t)wave_xor((int)m1[i], 16), (uint32_t)wave_xor((int)m2[i], 16));
+        if (per > 32) join(m1[i], m2[i], (uint32_t)wave_xor((int)m1[i], 32), (uint32_t)wave_xor((int)m2[i], 32));
+    }
+#pragma unroll
+    for (int d = 1; d < V; d <<= 1) {
+        if (64 * d >= per) break;
+        uint32_t b1[V], b2[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            b1[i] = m1[i ^ d];
+            b2[i] = m2[i ^ d];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) join(m1[i], m2[i], b1[i], b2[i]);
+    }
+}
+
+// v[e / 64] of lane e % 64, e a lane's own.
+template <int V>
+__device__ __forceinline__ float gather(const float (&v)[V], int e) {
+    float r = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float x = __shfl(v[i], e & 63, 64);
+        r = e >> 6 == i ? x : r;
+    }
+    return r;
+}
+
+template <int V>
+__device__ __forceinline__ bool choose_fast(const MoeRouteArgs& a, int64_t t, int group_shift, Choice& c) {
+    const int lane = threadIdx.x & 63;
+    const bool sigmoid = a.score == QK_SIGMOID;
+    float z[V];
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = 64 * i + lane;
+        z[i] = e < a.E ? load_logit(a.logits, a.dtype, t * a.E + e) : -INFINITY;
+        key[i] = order_of(z[i]);
+    }
+    float top = 0.0f, inv = 0.0f;                                   // of the softmax
+    if (a.bias || a.groups > 1 || !(a.renorm || sigmoid)) {
+        float s[V];
+        if (sigmoid) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float e = __expf(-fabsf(z[i])), r = __builtin_amdgcn_rcpf(1.0f + e);
+                s[i] = z[i] >= 0.0f ? r : e * r;
+            }
+        } else {
+            uint32_t m = key[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) m = max(m, key[i]);
+            top = float_of(wave_max(m));
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[i] = z[i] == -INFINITY ? 0.0f : __expf(z[i] - top);
+                sum += s[i];
+            }
+            inv = 1.0f / wave_sum(sum);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = s[i] > 0.0f ? s[i] * inv : 0.0f;
+        }
+        uint32_t ranked[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            ranked[i] = z[i] == -INFINITY ? kNone : order_of(a.bias ? s[i] + load_bias(a.bias, 64 * i + lane, a.E) : s[i]);
+            if (a.bias) key[i] = ranked[i];
+        }
+        if (a.groups > 1) {
+            uint32_t m1[V], m2[V];
+            float sum[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                m1[i] = ranked[i];
+                m2[i] = kNone;
+            }
+            join_groups<V>(m1, m2, 1 << group_shift);
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum[i] = float_of(m1[i]) + (m2[i] <= kNone ? 0.0f : float_of(m2[i]));
+            // group g in lane g; the best top_groups of them, and whether the next one is close to the last
+            uint32_t g = order_of(gather<V>(sum, lane << group_shift));
+            if (lane >= a.groups) g = 0;
+            uint64_t kept = 0;
+            uint32_t best = 0, last = 0;
+            for (int j = 0; j <= a.top_groups; ++j) {
+                best = wave_max(g);
+                if (best <= kNone) break;
+                if (j == a.top_groups) {
+                    const float v = float_of(best), w = float_of(last);
+                    if (!(w - v > 2.0f * (slack(v) + slack(w)))) return false;
+                    break;
+                }
+                last = best;
+                const int at = (int)__builtin_ctzll(__ballot(g == best));
+                kept |= 1ull << at;
+                g = lane == at ? 0u : g;
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (!(kept >> ((64 * i + lane) >> group_shift) & 1)) key[i] = kNone;
+        }
+    }
+    int id = -1;
+    uint32_t last = 0;
+    const int rounds = a.bias ? a.top_k + 1 : a.top_k;              // (the next one must not be close to the last one chosen)
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t best;
+        const int e = take_best<V>(key, best);
+        if (best <= kNone) break;
+        if (a.bias) {
+            const float v = float_of(best), w = float_of(last);
+            if (j > 0 && !(w - v > slack(v) + slack(w))) return false;
+            last = best;
+        }
+        if (lane == j && j < a.top_k) id = e;
+    }
+    c.id = id;
+    c.z = gather<V>(z, id < 0 ? 0 : id);
+    if (id < 0) c.z = -INFINITY;
+    c.s = a.renorm || sigmoid || id < 0 ? 0.0 : exp((double)c.z - (double)top) * (double)inv;
+    return true;
+}
+
+// (Sixteen waves a SIMD would need 32 registers; what the choice in 64 bits has beyond 64 goes to memory.)
+template <int V>
+__global__ __launch_bounds__(kThreads, V <= 4 ? 8 : 4) void moe_route_kernel(MoeRouteArgs a, int group_shift) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * kTokens + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    if (t >= a.T) return;
+    Choice c;
+    if (group_shift < 0 || !choose_fast<V>(a, t, group_shift, c)) c = choose_exactly<V>(a, t);
+    const bool sigmoid = a.score == QK_SIGMOID;
+    double w = c.s;
+    if (a.renorm) w = share_of((double)c.z, sigmoid);
+    else if (sigmoid) w = 1.0 / (1.0 + exp(-(double)c.z));
     if (lane < a.top_k) {
-        a.ids[t * a.top_k + lane] = id;
+        a.ids[t * a.top_k + lane] = c.id;
         a.weights[t * a.top_k + lane] = (float)(w * (double)a.scale);
     }
 }
@@ -343,10 +580,12 @@ unsigned token_grid(int64_t T) { return (unsigned)((T + kTokens - 1) / kTokens);
 
 hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s) {
     const dim3 grid(token_grid(a.T));
-    if (a.E <= 64) moe_route_kernel<1><<<grid, kThreads, 0, s>>>(a);
-    else if (a.E <= 128) moe_route_kernel<2><<<grid, kThreads, 0, s>>>(a);
-    else if (a.E <= 256) moe_route_kernel<4><<<grid, kThreads, 0, s>>>(a);
-    else moe_route_kernel<8><<<grid, kThreads, 0, s>>>(a);
+    // log2 of the experts of a group; groups of other sizes are chosen in 64 bits
+    const int per = a.E / a.groups, shift = a.groups == 1 ? 0 : (per & (per - 1)) == 0 ? __builtin_ctz((unsigned)per) : -1;
+    if (a.E <= 64) moe_route_kernel<1><<<grid, kThreads, 0, s>>>(a, shift);
+    else if (a.E <= 128) moe_route_kernel<2><<<grid, kThreads, 0, s>>>(a, shift);
+    else if (a.E <= 256) moe_route_kernel<4><<<grid, kThreads, 0, s>>>(a, shift);
+    else moe_route_kernel<8><<<grid, kThreads, 0, s>>>(a, shift);
     return hipGetLastError();
 }
 
