@@ -112,21 +112,100 @@ __device__ __forceinline__ void scores(const double (&z)[V], bool sigmoid, doubl
     for (int i = 0; i < V; ++i) s[i] = sum > 0.0 ? s[i] / sum : 0.0;
 }
 
+// Whole numbers in the order of the floats (of equal zeros one), 0 below all of them but -NaN.
+__device__ __forceinline__ uint32_t order_of(float f) {
+    const uint32_t u = as_uint(f + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float float_of(uint32_t k) { return as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
+constexpr uint32_t kNone = 0x007FFFFFu;                             // order_of(-inf)
+
+// Largest of the wave, as a scalar: inside the rows of 16 lanes, then of the four rows.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = group_max_u32<16>(v);
+    const uint32_t a = max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16));
+    const uint32_t b = max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48));
+    return max(a, b);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0xB1, 0xF, 0xF, false));
+    v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0x4E, 0xF, 0xF, false));
+    v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0x141, 0xF, 0xF, false));
+    v += as_float(__builtin_amdgcn_mov_dpp(as_uint(v), 0x140, 0xF, 0xF, false));
+    auto row = [&](int l) { return as_float((uint32_t)__builtin_amdgcn_readlane((int)as_uint(v), l)); };
+    return (row(0) + row(16)) + (row(32) + row(48));
+}
+
+__device__ __forceinline__ float sigmoid_of(float z) { return z >= 0.0f ? 1.0f / (1.0f + expf(-z)) : expf(z) / (1.0f + expf(z)); }
+
 // Shares of the chosen experts (one a lane; z = -inf: none): s_j / sum of s.  Relative to the largest, so that scores too
 // small for a number still have a ratio.
-__device__ __forceinline__ double share_of(double z, bool sigmoid) {
-    const double top = sigmoid ? fmin(wave_max(z), 0.0) : wave_max(z);
-    double r = 0.0;
-    if (z != -INFINITY) r = sigmoid && z >= 0.0 ? 1.0 / (1.0 + exp(-z)) : exp(z - top) / (sigmoid ? 1.0 + exp(z) : 1.0);
-    const double total = wave_sum(r);
-    return total > 0.0 ? r / total : 0.0;
+__device__ __forceinline__ float share_of(float z, bool sigmoid) {
+    const float most = float_of(wave_max(order_of(z))), top = sigmoid ? fminf(most, 0.0f) : most;
+    float r = 0.0f;
+    if (z != -INFINITY) r = sigmoid && z >= 0.0f ? 1.0f / (1.0f + expf(-z)) : expf(z - top) / (sigmoid ? 1.0f + expf(z) : 1.0f);
+    const float total = wave_sum(r);
+    return total > 0.0f ? r / total : 0.0f;
+}
+
+// The two largest of groups of 2^n experts, in every lane and register of the group: joined across the lanes that a DPP
+// pattern pairs, then across registers.
+template <class K>
+__device__ __forceinline__ void join(K& a1, K& a2, K b1, K b2) {
+    const K low = a1 < b1 ? a1 : b1, second = a2 < b2 ? b2 : a2;
+    a2 = low < second ? second : low;
+    a1 = a1 < b1 ? b1 : a1;
+}
+template <int kCtrl>
+__device__ __forceinline__ double dpp_pair(double v) {
+    return dpp_move<kCtrl>(v, v);
+}
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_pair(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true);
+}
+template <int V, class K>
+__device__ __forceinline__ void join_groups(K (&m1)[V], K (&m2)[V], int per) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (per > 1) join(m1[i], m2[i], dpp_pair<0xB1>(m1[i]), dpp_pair<0xB1>(m2[i]));       // lane ^ 1
+        if (per > 2) join(m1[i], m2[i], dpp_pair<0x4E>(m1[i]), dpp_pair<0x4E>(m2[i]));       // lane ^ 2
+        if (per > 4) join(m1[i], m2[i], dpp_pair<0x141>(m1[i]), dpp_pair<0x141>(m2[i]));     // 7 - lane of 8
+        if (per > 8) join(m1[i], m2[i], dpp_pair<0x140>(m1[i]), dpp_pair<0x140>(m2[i]));     // 15 - lane of 16
+        if (per > 16) join(m1[i], m2[i], wave_xor(m1[i], 16), wave_xor(m2[i], 16));
+        if (per > 32) join(m1[i], m2[i], wave_xor(m1[i], 32), wave_xor(m2[i], 32));
+    }
+#pragma unroll
+    for (int d = 1; d < V; d <<= 1) {
+        if (64 * d >= per) break;
+        K b1[V], b2[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            b1[i] = m1[i ^ d];
+            b2[i] = m2[i ^ d];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) join(m1[i], m2[i], b1[i], b2[i]);
+    }
+}
+
+// v[e / 64] of lane e % 64, e a lane's own.
+template <int V, class K>
+__device__ __forceinline__ K gather(const K (&v)[V], int e) {
+    K r = v[0];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const K x = __shfl(v[i], e & 63, 64);
+        r = e >> 6 == i ? x : r;
+    }
+    return r;
 }
 
 // What a token's choice leaves in lane j: its expert j, that one's logit and, where weights are not renormalized, its score.
 struct Choice {
     int id;
     float z;
-    double s;
+    float s;
 };
 
 __device__ __forceinline__ float load_bias(const float* bias, int e, int E) {
@@ -136,7 +215,7 @@ __device__ __forceinline__ float load_bias(const float* bias, int e, int E) {
 
 // The choice in binary64 throughout.
 template <int V>
-__device__ __forceinline__ Choice choose_exactly(const MoeRouteArgs& a, int64_t t) {
+__device__ __forceinline__ Choice choose_exactly(const MoeRouteArgs& a, int64_t t, int group_shift) {
     const int lane = threadIdx.x & 63;
     double z[V], s[V], key[V], ranked[V];
 #pragma unroll
@@ -152,31 +231,40 @@ __device__ __forceinline__ Choice choose_exactly(const MoeRouteArgs& a, int64_t 
     }
     if (a.groups > 1) {
         const int per = a.E / a.groups;
-        double mine = -INFINITY;                                    // lane g: the sum of group g's two largest
-        for (int g = 0; g < a.groups; ++g) {
-            double v[V], best;
+        double sum = -INFINITY;                                     // lane g: of group g's two largest
+        if (group_shift >= 0) {
+            double m1[V], m2[V], both[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = (64 * i + lane) / per == g ? ranked[i] : -INFINITY;
-            const int at = wave_argmax<V>(v, best);
-            double sum = best;
-            if (best != -INFINITY) {
+            for (int i = 0; i < V; ++i) {
+                m1[i] = ranked[i];
+                m2[i] = -INFINITY;
+            }
+            join_groups<V>(m1, m2, per);
+#pragma unroll
+            for (int i = 0; i < V; ++i) both[i] = m2[i] == -INFINITY ? m1[i] : m1[i] + m2[i];
+            const double v = gather<V>(both, lane << group_shift);
+            if (lane < a.groups) sum = v;
+        } else {
+            for (int g = 0; g < a.groups; ++g) {
+                double v[V], best, second;
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = (64 * i + lane) / per == g ? ranked[i] : -INFINITY;
+                const int at = wave_argmax<V>(v, best);
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (64 * i + lane == at) v[i] = -INFINITY;
-                double second;
                 wave_argmax<V>(v, second);
-                if (second != -INFINITY) sum += second;
+                if (lane == g) sum = second == -INFINITY ? best : best + second;
             }
-            if (lane == g) mine = sum;
         }
         uint64_t kept = 0;
         for (int j = 0; j < a.top_groups; ++j) {
-            const double m[1] = {mine};
+            const double m[1] = {sum};
             double best;
             const int g = wave_argmax<1>(m, best);
             if (best == -INFINITY) break;
             kept |= 1ull << g;
-            if (lane == g) mine = -INFINITY;
+            if (lane == g) sum = -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -184,46 +272,18 @@ __device__ __forceinline__ Choice choose_exactly(const MoeRouteArgs& a, int64_t 
             if (e < a.E && !(kept >> (e / per) & 1)) key[i] = -INFINITY;
         }
     }
-    Choice c{-1, -INFINITY, 0.0};
+    Choice c{-1, -INFINITY, 0.0f};
     for (int j = 0; j < a.top_k; ++j) {
         double best;
         const int e = wave_argmax<V>(key, best);
         if (best == -INFINITY) break;
         const double ze = pick<V>(z, e), se = pick<V>(s, e);
-        if (lane == j) c = Choice{e, (float)ze, se};
+        if (lane == j) c = Choice{e, (float)ze, (float)se};
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (64 * i + lane == e) key[i] = -INFINITY;
     }
     return c;
-}
-
-// Whole numbers in the order of the floats (of equal zeros one), 0 below all of them but -NaN.
-__device__ __forceinline__ uint32_t order_of(float f) {
-    const uint32_t u = as_uint(f + 0.0f);
-    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float float_of(uint32_t k) { return as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
-constexpr uint32_t kNone = 0x007FFFFFu;                             // order_of(-inf)
-
-template <int kCtrl, int kRows = 0xF>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-    return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, kCtrl, kRows, 0xF, false));
-}
-// Largest of the wave, as a scalar: inside the rows of 16 lanes, then across them.
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    v = dpp_max<0xB1>(v);
-    v = dpp_max<0x4E>(v);
-    v = dpp_max<0x141>(v);
-    v = dpp_max<0x140>(v);
-    v = dpp_max<0x142, 0xA>(v);
-    v = dpp_max<0x143, 0xC>(v);
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += wave_xor(v, m);
-    return v;
 }
 
 // The largest key and the lowest place that has it (64 i + lane), which is taken out.
@@ -250,57 +310,14 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[V], uint32_t& best) {
     return 64 * at + (int)__builtin_ctzll(who);
 }
 
-// The choice in 32 bits, for groups of 2^n experts; false where two ranks, or two groups, are too close for that.
-//   A score in 32 bits is off by less than 2^-20: its exponential by the rounding of the argument, 2^-24 |z - max| of itself, of
-// which x exp(-x) < 0.4 is left, and two steps; the sum of 512 of them by 2^-20 of itself, being made in a tree.  Added to a
-// bias it is rounded to 2^-24 of itself.
-__device__ __forceinline__ float slack(float rank) { return 4.0f * (9.5367431640625e-7f + 1.1920929e-7f * fabsf(rank)); }
-
-// The two largest of groups of lanes, joined across lanes that a DPP pattern pairs.
-__device__ __forceinline__ void join(uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
-    a2 = max(min(a1, b1), max(a2, b2));
-    a1 = max(a1, b1);
-}
-template <int kCtrl>
-__device__ __forceinline__ void join_dpp(uint32_t& a1, uint32_t& a2) {
-    join(a1, a2, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a1, kCtrl, 0xF, 0xF, true),
-         (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a2, kCtrl, 0xF, 0xF, true));
-}
-template <int V>
-__device__ __forceinline__ void join_groups(uint32_t (&m1)[V], uint32_t (&m2)[V], int per) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (per > 1) join_dpp<0xB1>(m1[i], m2[i]);
-        if (per > 2) join_dpp<0x4E>(m1[i], m2[i]);
-        if (per > 4) join_dpp<0x141>(m1[i], m2[i]);
-        if (per > 8) join_dpp<0x140>(m1[i], m2[i]);
-        if (per > 16) join(m1[i], m2[i], (uint32_t)wave_xor((int)m1[i], 16), (uint32_t)wave_xor((int)m2[i], 16));
-        if (per > 32) join(m1[i], m2[i], (uint32_t)wave_xor((int)m1[i], 32), (uint32_t)wave_xor((int)m2[i], 32));
-    }
-#pragma unroll
-    for (int d = 1; d < V; d <<= 1) {
-        if (64 * d >= per) break;
-        uint32_t b1[V], b2[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            b1[i] = m1[i ^ d];
-            b2[i] = m2[i ^ d];
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) join(m1[i], m2[i], b1[i], b2[i]);
-    }
-}
-
-// v[e / 64] of lane e % 64, e a lane's own.
-template <int V>
-__device__ __forceinline__ float gather(const float (&v)[V], int e) {
-    float r = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float x = __shfl(v[i], e & 63, 64);
-        r = e >> 6 == i ? x : r;
-    }
-    return r;
+// The choice with ranks in 32 bits, for groups of 2^n experts.  Where ranks in it are too close for that, the best ones up to
+// a clear gap behind the last one wanted are put in order by their ranks in 64 bits, one in each lane; false where that does
+// not do: a group too close to another, or more than 64 such ranks.
+//   A score in 32 bits is off by less than 2^-21 (sigmoid: its exponential by the rounding of the argument, 2^-24 |z| of itself,
+// of which x exp(-x) < 0.4 is left, and two steps, the reciprocal by one) or 2^-20 (softmax: the sum of 512, made in a tree, by
+// 2^-21 of itself more).  Added to a bias it is rounded to 2^-24 of itself.
+__device__ __forceinline__ float slack(float rank, bool sigmoid) {
+    return (sigmoid ? 4.76837158e-7f : 9.53674316e-7f) + 1.1920929e-7f * fabsf(rank);
 }
 
 template <int V>
@@ -366,7 +383,7 @@ __device__ __forceinline__ bool choose_fast(const MoeRouteArgs& a, int64_t t, in
                 if (best <= kNone) break;
                 if (j == a.top_groups) {
                     const float v = float_of(best), w = float_of(last);
-                    if (!(w - v > 2.0f * (slack(v) + slack(w)))) return false;
+                    if (!(w - v > 2.0f * (slack(v, sigmoid) + slack(w, sigmoid)))) return false;
                     break;
                 }
                 last = best;
@@ -379,24 +396,55 @@ __device__ __forceinline__ bool choose_fast(const MoeRouteArgs& a, int64_t t, in
                 if (!(kept >> ((64 * i + lane) >> group_shift) & 1)) key[i] = kNone;
         }
     }
-    int id = -1;
-    uint32_t last = 0;
-    const int rounds = a.bias ? a.top_k + 1 : a.top_k;              // (the next one must not be close to the last one chosen)
-    for (int j = 0; j < rounds; ++j) {
+    int id = -1, n = 0;                                             // candidate j in lane j
+    uint32_t mine = 0;
+    float wanted = 0.0f;                                            // rank of the last one wanted
+    while (true) {
         uint32_t best;
         const int e = take_best<V>(key, best);
         if (best <= kNone) break;
         if (a.bias) {
-            const float v = float_of(best), w = float_of(last);
-            if (j > 0 && !(w - v > slack(v) + slack(w))) return false;
-            last = best;
+            const float v = float_of(best);
+            if (n >= a.top_k && wanted - v > slack(wanted, sigmoid) + slack(v, sigmoid)) break;
+            if (n == 64) return false;
+            wanted = n == a.top_k - 1 ? v : wanted;
         }
-        if (lane == j && j < a.top_k) id = e;
+        if (lane == n) {
+            id = e;
+            mine = best;
+        }
+        if (++n == a.top_k && !a.bias) break;
+    }
+    if (a.bias) {
+        const float v = float_of(mine), next = __shfl_down(v, 1, 64);
+        const bool close = lane + 1 < n && !(v - next > slack(v, sigmoid) + slack(next, sigmoid));
+        if (__ballot(close)) {
+            const int e = id < 0 ? 0 : id;
+            const double ze = (double)gather<V>(z, e);
+            double s;
+            if (sigmoid) {
+                s = 1.0 / (1.0 + exp(-ze));
+            } else {
+                double sum = 0.0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum += z[i] == -INFINITY ? 0.0 : exp((double)z[i] - (double)top);
+                s = exp(ze - (double)top) / wave_sum(sum);
+            }
+            const double r = s + (double)load_bias(a.bias, e, a.E);
+            int place = 0;
+            for (int i = 0; i < n; ++i) {
+                const double ri = __shfl(r, i, 64);
+                const int ei = __shfl(id, i, 64);
+                place += ri > r || (ri == r && ei < id);
+            }
+            id = __builtin_amdgcn_ds_permute(4 * (lane < n ? place : lane), id);
+        }
+        if (lane >= a.top_k) id = -1;
     }
     c.id = id;
     c.z = gather<V>(z, id < 0 ? 0 : id);
     if (id < 0) c.z = -INFINITY;
-    c.s = a.renorm || sigmoid || id < 0 ? 0.0 : exp((double)c.z - (double)top) * (double)inv;
+    c.s = a.renorm || sigmoid || id < 0 ? 0.0f : expf(c.z - top) * inv;
     return true;
 }
 
@@ -407,14 +455,12 @@ __global__ __launch_bounds__(kThreads, V <= 4 ? 8 : 4) void moe_route_kernel(Moe
     const int64_t t = (int64_t)blockIdx.x * kTokens + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     if (t >= a.T) return;
     Choice c;
-    if (group_shift < 0 || !choose_fast<V>(a, t, group_shift, c)) c = choose_exactly<V>(a, t);
+    if (group_shift < 0 || !choose_fast<V>(a, t, group_shift, c)) c = choose_exactly<V>(a, t, group_shift);
     const bool sigmoid = a.score == QK_SIGMOID;
-    double w = c.s;
-    if (a.renorm) w = share_of((double)c.z, sigmoid);
-    else if (sigmoid) w = 1.0 / (1.0 + exp(-(double)c.z));
+    const float w = a.renorm ? share_of(c.z, sigmoid) : sigmoid ? sigmoid_of(c.z) : c.s;
     if (lane < a.top_k) {
         a.ids[t * a.top_k + lane] = c.id;
-        a.weights[t * a.top_k + lane] = (float)(w * (double)a.scale);
+        a.weights[t * a.top_k + lane] = w * a.scale;
     }
 }
 
@@ -428,47 +474,52 @@ __global__ __launch_bounds__(kThreads) void moe_route_backward_kernel(MoeRouteBa
     const bool sigmoid = a.score == QK_SIGMOID;
     int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
     if (id >= a.E) id = -1;
-    const double z = id >= 0 ? (double)load_logit(a.logits, a.dtype, t * a.E + id) : -INFINITY;
-    const double d = id >= 0 ? (double)a.scale * (double)a.dweights[t * a.top_k + lane] : 0.0;
-    double all = 0.0, own;                                          // dz = own at the chosen, all * s at every expert
-    double s[V];
+    const float z = id >= 0 ? load_logit(a.logits, a.dtype, t * a.E + id) : -INFINITY;
+    const float d = id >= 0 ? a.scale * a.dweights[t * a.top_k + lane] : 0.0f;
+    float all = 0.0f, own;                                          // dz = own at the chosen, all * s at every expert
+    float s[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = 0.0;
+    for (int i = 0; i < V; ++i) s[i] = 0.0f;
     if (a.renorm) {
-        const double p = share_of(z, sigmoid), mean = wave_sum(d * p);
+        const float p = share_of(z, sigmoid), mean = wave_sum(d * p);
         // softmax: p (d - mean); sigmoid: (d - mean) / total * s (1 - s) = (d - mean) p (1 - s)
-        own = (d - mean) * p * (sigmoid ? 1.0 / (1.0 + exp(z)) : 1.0);
+        own = (d - mean) * p * (sigmoid ? sigmoid_of(-z) : 1.0f);
     } else if (sigmoid) {
-        own = z == -INFINITY ? 0.0 : d / (1.0 + exp(-z)) / (1.0 + exp(z));
+        own = z == -INFINITY ? 0.0f : d * sigmoid_of(z) * sigmoid_of(-z);
     } else {
-        double zz[V];
+        float zz[V];
+        uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = 64 * i + lane;
-            zz[i] = e < a.E ? (double)load_logit(a.logits, a.dtype, t * a.E + e) : -INFINITY;
+            zz[i] = e < a.E ? load_logit(a.logits, a.dtype, t * a.E + e) : -INFINITY;
+            m = max(m, order_of(zz[i]));
         }
-        scores<V>(zz, false, s);
-        double se = 0.0;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int e = __shfl(id, j, 64);
-            if (e < 0) continue;
-            const double v = pick<V>(s, e);
-            if (lane == j) se = v;
+        const float top = float_of(wave_max(m));
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[i] = zz[i] == -INFINITY ? 0.0f : expf(zz[i] - top);
+            sum += s[i];
         }
-        own = d * se;
+        sum = wave_sum(sum);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] *= inv;
+        own = z == -INFINITY ? 0.0f : d * expf(z - top) * inv;
         all = -wave_sum(own);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) dz[64 * i + lane] = 0.0f;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (id >= 0 && z != -INFINITY) dz[id] = (float)own;
+    if (id >= 0 && z != -INFINITY) dz[id] = own;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = 64 * i + lane;
-        if (e < a.E) store_logit(a.dlogits, a.dtype, t * a.E + e, (float)((double)dz[e] + all * s[i]));
+        if (e < a.E) store_logit(a.dlogits, a.dtype, t * a.E + e, fmaf(all, s[i], dz[e]));
     }
 }
 
