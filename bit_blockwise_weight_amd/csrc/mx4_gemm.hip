@@ -255,7 +255,12 @@ __device__ __forceinline__ float silu(float g) {
 
 // Which of a wave's columns line q of its W lines is.  Of every two neighbouring blocks of 16 the lines alternate by fours,
 // so that a lane's 4 outputs of the one and 4 of the other are neighbours: 8 of a row.
-__device__ __forceinline__ int column_of(int q) { return (q & ~31) | ((q >> 2 & 3) << 3) | ((q >> 4 & 1) << 2) | (q & 3); }
+// (A wave with one block of gate and one of up rows keeps them apart.)
+template <Mode MODE, int RT>
+__device__ __forceinline__ int column_of(int q) {
+    if constexpr (MODE == kUp && RT == 2) return q;
+    return (q & ~31) | ((q >> 2 & 3) << 3) | ((q >> 4 & 1) << 2) | (q & 3);
+}
 
 // Outputs of one wave: acc[i][j], rows 16 i + lane % 16 of the wave's rows m, columns 4 (lane / 16) + q of block j of its n (up:
 // the second half of the blocks are the up products of the first).
@@ -345,7 +350,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
     if (MODE == kDense || t.expert < a.E) {
         const Operands<MODE> op(a, t);
         auto w_row = [&](int b) {                       // row b of the tile's W lines
-            const int q = column_of(b % WN);
+            const int q = column_of<MODE, RT>(b % WN);
             return MODE == kUp ? op.w_row(b / WN * (WN / 2) + q % (WN / 2), q >= WN / 2) : op.w_row(b / WN * WN + q, false);
         };
         // what this lane copies: line l / 8 of 8, slot l % 8
@@ -546,8 +551,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_kernel(GemmArgs a) {
     if (MODE == kDense || t.expert < a.E) {
         const Operands<MODE> op(a, t);
         auto w_row = [&](int b) {
-            if constexpr (MODE == kUp && RT == 2) return op.w_row(b % 16, b >= 16);
-            const int q = column_of(b);
+            const int q = column_of<MODE, RT>(b);
             return MODE == kUp ? op.w_row(q % (8 * RT), q >= 8 * RT) : op.w_row(q, false);
         };
         uint32_t voff[kLoads], soff[kSLoads];
@@ -696,7 +700,7 @@ template <Mode MODE>
 int64_t grid_for(const GemmArgs& a, int64_t bm, int64_t bno) {
     if (MODE == kDense) return cdiv(a.M, bm) * cdiv(a.N, bno);
     // an expert's last tile may be partial
-    return (a.slots / bm + std::min<int64_t>(a.E + 1, a.slots)) * cdiv(a.N, bno);
+    return moe_most_tiles(a.slots, a.E) * cdiv(a.N, bno);
 }
 
 template <Mode MODE, int BM, int BN, int WM, int WN>
@@ -715,16 +719,37 @@ hipError_t launch_few(const GemmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Which tiles.  Times in us, weights in cache where they fit.
+hipError_t launch_dense(const GemmArgs& a, hipStream_t s) {
+    const int64_t cus = device_cu_count();
+    // Workgroups that split the inputs among their waves where tiles would leave half of the CUs without one, and up to 16
+    // rows always: 16 x 4096 x 11008 6.6, tiles of 64 x 64 16; 64 x 4096 x 4096 7.5 and 8.7; 64 x 11008 x 4096 12.5 and 9.0.
+    if (a.M <= 16) return launch_few<kDense, 1, 2>(a, s);
+    if (a.M <= 128 && grid_for<kDense>(a, 64, 64) <= cus / 2)
+        return a.M <= 32 ? launch_few<kDense, 2, 2>(a, s) : launch_few<kDense, 4, 2>(a, s);
+    // The largest tiles of which there is one for every CU: 4096 x 4096 x 4096 41, in tiles of 128 51; 2048 x 4096 x 4096 40 and
+    // 25; 1000 x 4096 x 4096 in tiles of 128 15.4, of 64 x 128 17.2; 512 x 4096 x 4096 13.5 and 11.5; 200 x 4096 x 4096 in
+    // tiles of 64 x 128 10.5, of 64 9.6.
+    if (grid_for<kDense>(a, 256, 256) >= cus) return launch_tile<kDense, 256, 256, 128, 128>(a, s);
+    if (grid_for<kDense>(a, 128, 128) >= cus) return launch_tile<kDense, 128, 128, 64, 64>(a, s);
+    if (grid_for<kDense>(a, 64, 128) >= cus * 5 / 8) return launch_tile<kDense, 64, 128, 64, 32>(a, s);
+    return launch_tile<kDense, 64, 64, 64, 32>(a, s);
+}
+
 template <Mode MODE>
-hipError_t launch_any(const GemmArgs& a, hipStream_t s) {
-    // rows that meet a weight: of the product, or the rows of the plan's tiles
-    const int64_t rows = MODE == kDense ? a.M : moe_tile_rows(a.slots, a.E);
-    if (rows <= 16) return launch_few<MODE, 1, 2>(a, s);
-    if (rows <= 32) return launch_few<MODE, 2, 2>(a, s);
-    if (rows <= 64) return launch_few<MODE, 4, 2>(a, s);
-    if constexpr (MODE == kDense)
-        if (grid_for<MODE>(a, 256, 256) >= device_cu_count()) return launch_tile<MODE, 256, 256, 128, 128>(a, s);
-    return launch_tile<MODE, 128, 128, 64, 64>(a, s);
+hipError_t launch_experts(const GemmArgs& a, hipStream_t s) {
+    const int64_t cus = device_cu_count(), half = MODE == kUp ? 2 : 1;
+    if (moe_tile_rows(a.slots, a.E) == 128) {
+        // Rows of an expert on average.  512 tokens of 8 experts of 4096 x 11008, top 2 (down, 128 rows): 61, in tiles of
+        // 128 x 128 76; 4096 tokens of 64 experts, top 8 (up, 512 rows): 128 and 121.
+        const int64_t rows = a.slots / std::min<int64_t>(a.E, a.slots);
+        return rows <= 256 ? launch_tile<MODE, 128, 256, 64, 64>(a, s) : launch_tile<MODE, 128, 128, 64, 64>(a, s);
+    }
+    // A few slots of few outputs: the inputs split among the waves of a workgroup (one token's top 2 of 8 experts of
+    // 4096 x 11008, down: 12.8, in tiles of 64 x 64 23).  Otherwise the larger tiles where they fill the CUs twice.
+    if (a.slots <= 16 && grid_for<MODE>(a, 64, 64 / half) <= cus) return launch_few<MODE, 1, 2>(a, s);
+    if (grid_for<MODE>(a, 64, 128 / half) >= 2 * cus) return launch_tile<MODE, 64, 128, 64, 32>(a, s);
+    return launch_tile<MODE, 64, 64, 64, 32>(a, s);
 }
 
 }  // namespace
@@ -738,7 +763,7 @@ hipError_t launch_mx4_gemm(const qk_mx4_state* x, const qk_mx4_state* w, void* y
     a.M = x->rows;
     a.N = w->rows;
     a.w_rows = w->rows;
-    return launch_any<kDense>(a, s);
+    return launch_dense(a, s);
 }
 
 namespace {
@@ -762,7 +787,7 @@ hipError_t launch_moe_up_mx4(const qk_mx4_state* x, const qk_mx4_state* gate_up,
     a.y = h;
     a.y_dtype = h_dtype;
     a.N = a.w_rows / 2;
-    return launch_any<kUp>(a, s);
+    return launch_experts<kUp>(a, s);
 }
 
 size_t moe_down_mx4_workspace_bytes(int64_t T, int32_t top_k, int64_t H) { return (size_t)(T * top_k) * (size_t)H * 4; }
@@ -775,7 +800,7 @@ hipError_t launch_moe_down_mx4(const qk_mx4_state* h, const qk_mx4_state* down, 
     a.y = workspace;
     a.weights = weights;
     a.N = a.w_rows;
-    const hipError_t e = launch_any<kDown>(a, s);
+    const hipError_t e = launch_experts<kDown>(a, s);
     if (e != hipSuccess) return e;
     const int64_t T = h->rows / top_k, threads = T * ((a.N + 3) / 4), grid = cdiv(threads, kCombineThreads);
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
