@@ -192,15 +192,20 @@ __device__ __forceinline__ floatx4_t mfma(v4i_t w, int ws, v4i_t x, int xs, floa
 
 // The same in place.  The compiler's own form may write its sum elsewhere, and with 256 of them there is no elsewhere: it
 // then moves sums about between the instructions.  What reads the sums has to wait for the last instruction by itself
-// (settle); operands come from LDS, whose waits the compiler sets for any reader.
+// (settle).  A vector instruction that writes an operand has to be two instructions away, which the compiler does not see to
+// here: operands are whole dwords as they come from LDS, whose waits the compiler sets for any reader (of a 16-bit read it
+// clears the upper half first; two idle cycles before every product would cost 5%).
 template <int S>
 __device__ __forceinline__ void mfma_in_place(floatx4_t& c, v4i_t w, int ws, v4i_t x, int xs) {
-    if constexpr (S == 0)
-        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-                     : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs));
-    else
-        asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
-                     : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs));
+#define QK_MFMA(SEL, SEL_HI)                                                                                                 \
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:" SEL " op_sel_hi:" SEL_HI          \
+                 " cbsz:4 blgp:4"                                                                                            \
+                 : "+a"(c) : "v"(w), "v"(x), "v"(ws), "v"(xs))
+    if constexpr (S == 0) QK_MFMA("[0,0,0]", "[0,0,0]");
+    else if constexpr (S == 1) QK_MFMA("[1,1,0]", "[0,0,0]");
+    else if constexpr (S == 2) QK_MFMA("[0,0,0]", "[1,1,0]");
+    else QK_MFMA("[1,1,0]", "[1,1,0]");
+#undef QK_MFMA
 }
 // 32 idle cycles, more than an instruction of 8 passes needs before its result may be read; the sums count as written behind them.
 template <int MT, int RT>
@@ -391,10 +396,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
         };
         auto scale_store = [&](int pair, int k) {
             if (64 * wave + kThreads * k >= BM + BN) return;
-            *reinterpret_cast<u32x4_t*>(sc + (pair & 1) * ((BM + BN) * 16) + (tid + kThreads * k) * 16) = sv[k];
+            const u32x4_t v = sv[k];
+            *reinterpret_cast<u32x4_t*>(sc + (pair & 1) * ((BM + BN) * 16) + (tid + kThreads * k) * 16) =
+                (u32x4_t){__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
+                          __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
         };
         const int xline = (wm * WM + r) * 128, wline = (wn * WN + r) * 128;
-        const int xsc = (wm * WM + r) * 16 + 2 * h, wsc = (BM + wn * WN + r) * 16 + 2 * h;
+        const int xsc = (wm * WM + r) * 16 + 4 * h, wsc = (BM + wn * WN + r) * 16 + 4 * h;
         const int at0 = 16 * slot_of(r, 2 * h), at1 = 16 * slot_of(r, 2 * h + 1);
         // fragments of W by half; those of X, of which four are enough; scales by the parity of the stage
         v4i_t wf[2][RT], xf[4];
@@ -406,9 +414,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
             wf[s][j] = *reinterpret_cast<const v4i_t*>(src + wline + (s ? at1 : at0) + 2048 * j);
         };
         auto read_scale = [&](int st, int p, int n) {
-            const uint8_t* src = sc + (st >> 1 & 1) * ((BM + BN) * 16) + 8 * p;
-            if (n < RT) ws[p][n] = *reinterpret_cast<const uint16_t*>(src + wsc + 256 * n);
-            else xs[p][n - RT] = *reinterpret_cast<const uint16_t*>(src + xsc + 256 * (n - RT));
+            const uint8_t* src = sc + (st >> 1 & 1) * ((BM + BN) * 16);
+            if (n < RT) ws[p][n] = *reinterpret_cast<const int*>(src + wsc + 256 * n);
+            else xs[p][n - RT] = *reinterpret_cast<const int*>(src + xsc + 256 * (n - RT));
         };
         static_assert(MT % 4 == 0);
         constexpr int kOps = MT * RT, kTail = 2 * RT;                 // instructions of a half; of it behind the meeting
@@ -442,7 +450,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
                     constexpr int o = decltype(O)::value, i = o / RT, j = o % RT;
                     if constexpr (s == 1 && o == 0) meet(std::integral_constant<int, 63>{});
                     if constexpr (s == 1 && o == kOps - kTail) meet(WCopies{});
-                    mfma_in_place<s>(acc[i][j], wf[s][j], ws[p][j], xf[i % 4], xs[p][i]);
+                    mfma_in_place<2 * p + s>(acc[i][j], wf[s][j], ws[p][j], xf[i % 4], xs[p][i]);
                     if constexpr (j == 0) {
                         if constexpr (i + 2 < MT) read_x(x, s, i + 2);
                         else read_x(s == 0 ? x : xnext, 1 - s, i + 2 - MT);
