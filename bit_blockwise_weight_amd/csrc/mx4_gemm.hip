@@ -58,53 +58,67 @@ struct Tile {
     int32_t expert;            // E: slots without one
 };
 
-// The tile of this workgroup; count 0: none.  Workgroup i runs on XCD i % 8: each XCD gets a run of tiles, 8 rows of them at a
-// time going through all columns, so that the tiles of an XCD share operands in its L2.  The experts' tiles have their rows
-// from the plan, one after the other in one list: those of an expert are neighbours.
-template <bool kExperts, int BM, int BN>
-__device__ __forceinline__ Tile find_tile(const GemmArgs& a) {
-    const uint32_t tm = kExperts ? (uint32_t)*a.tiles : (uint32_t)((a.M + BM - 1) / BM);
-    const uint32_t tn = (uint32_t)((a.N + BN - 1) / BN), nt = tm * tn;
-    Tile t;
-    t.count = 0;
-    t.m0 = t.n0 = 0;
-    t.expert = 0;
-    if (kExperts && blockIdx.x >= nt) return t;
-    const uint32_t xcd = blockIdx.x % kXcds, q = nt / kXcds, rem = nt % kXcds;
-    const uint32_t lid = xcd * q + (xcd < rem ? xcd : rem) + blockIdx.x / kXcds;
-    const uint32_t band = lid / (kXcds * tn), in = lid - band * (kXcds * tn);
-    const uint32_t rows = tm - band * kXcds < kXcds ? tm - band * kXcds : kXcds;
-    const uint32_t m = band * kXcds + in % rows;
-    t.n0 = (int64_t)(in / rows) * BN;
-    if constexpr (kExperts) {
-        const MoeTile e = reinterpret_cast<const MoeTile*>(a.tiles + 4)[m];
-        t.m0 = e.first;
-        t.expert = e.expert_count & 0xFFFF;
-        t.count = e.expert_count >> 16;
-    } else {
-        t.m0 = (int64_t)m * BM;
-        t.count = (int32_t)(a.M - t.m0 < BM ? a.M - t.m0 : BM);
-    }
-    return t;
+// Numbers of the plan, which no kernel here writes: through the scalar cache.
+__device__ __forceinline__ int32_t plan_number(const int32_t* p) {
+    return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
 }
+
+// Rows and number of the tiles of a launch.
+template <bool kExperts, int BM, int BN>
+struct Tiling {
+    uint32_t rows, cols;
+    __device__ __forceinline__ explicit Tiling(const GemmArgs& a) {
+        rows = kExperts ? (uint32_t)plan_number(a.tiles) : (uint32_t)((a.M + BM - 1) / BM);
+        cols = (uint32_t)((a.N + BN - 1) / BN);
+    }
+    __device__ __forceinline__ uint32_t count() const { return rows * cols; }
+
+    // Tile `id`, made on XCD id % 8: each XCD gets a run of tiles, 8 rows of them at a time going through all columns, so that
+    // the tiles of an XCD share operands in its L2.  The experts' tiles have their rows from the plan, one after the other in
+    // one list: those of an expert are neighbours.
+    __device__ __forceinline__ Tile at(const GemmArgs& a, uint32_t id) const {
+        const uint32_t nt = count(), xcd = id % kXcds, q = nt / kXcds, rem = nt % kXcds;
+        const uint32_t lid = xcd * q + (xcd < rem ? xcd : rem) + id / kXcds;
+        const uint32_t band = lid / (kXcds * cols), in = lid - band * (kXcds * cols);
+        const uint32_t high = rows - band * kXcds < kXcds ? rows - band * kXcds : kXcds;
+        const uint32_t m = band * kXcds + in % high;
+        Tile t;
+        t.n0 = (int64_t)(in / high) * BN;
+        if constexpr (kExperts) {
+            const int32_t expert_count = plan_number(a.tiles + 4 + 2 * m + 1);
+            t.m0 = plan_number(a.tiles + 4 + 2 * m);
+            t.expert = expert_count & 0xFFFF;
+            t.count = expert_count >> 16;
+        } else {
+            t.m0 = (int64_t)m * BM;
+            t.expert = 0;
+            t.count = (int32_t)(a.M - t.m0 < BM ? a.M - t.m0 : BM);
+        }
+        return t;
+    }
+};
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const uint8_t* p, int64_t bytes) {
     const uint32_t n = (uint32_t)(bytes < 0xFFFF0000ll ? bytes : 0xFFFF0000ll);
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), (short)0, (int)n, 0x00020000);
 }
 
-// Where the rows of a tile's operands are.  Row i of X and of W (clamped to the last one there is) as a row of its buffer.
+// Row i of a tile (clamped to its last one): its slot (dense: itself).
+template <Mode MODE>
+__device__ __forceinline__ uint32_t slot_at(const GemmArgs& a, const Tile& t, int i) {
+    i = min(i, t.count - 1);
+    return MODE == kDense ? (uint32_t)i : (uint32_t)a.list[t.m0 + i];
+}
+
+// Where the rows of a tile's operands are.  Rows of X and of W (clamped to the last one there is) as rows of their buffers.
 template <Mode MODE>
 struct Operands {
     __amdgpu_buffer_rsrc_t xc, xs, wc, ws;
-    const int32_t* list;       // slots of the tile
-    int32_t x_rows;            // of the tile
     int32_t w_rows;            // of a kind, from n0 on
     int32_t up;                // rows from a gate row to its up row
     uint32_t per_token;
 
     __device__ __forceinline__ Operands(const GemmArgs& a, const Tile& t) {
-        x_rows = t.count;
         per_token = a.per_token;
         up = (int32_t)a.N;
         const int64_t left = a.N - t.n0;
@@ -115,8 +129,6 @@ struct Operands {
             cx += t.m0 * a.x.code_stride;
             sx += t.m0 * a.x.scale_stride;
             xr = t.count;
-        } else {
-            list = a.list + t.m0;
         }
         xc = buffer(cx, xr * a.x.code_stride);
         xs = buffer(sx, xr * a.x.scale_stride);
@@ -125,11 +137,9 @@ struct Operands {
         wc = buffer(a.w.codes + row0 * a.w.code_stride, rows * a.w.code_stride);
         ws = buffer(a.w.scales + row0 * a.w.scale_stride, rows * a.w.scale_stride);
     }
-    __device__ __forceinline__ uint32_t x_row(int i) const {
-        i = min(i, x_rows - 1);
-        if constexpr (MODE == kDense) return (uint32_t)i;
-        if constexpr (MODE == kUp) return per_token ? __umulhi((uint32_t)list[i], per_token) : (uint32_t)list[i];
-        return (uint32_t)list[i];
+    // the row of X of a slot
+    __device__ __forceinline__ uint32_t row_of(uint32_t slot) const {
+        return MODE == kUp && per_token ? __umulhi(slot, per_token) : slot;
     }
     // column c of the tile, of the gate or the up rows
     __device__ __forceinline__ uint32_t w_row(int c, bool second) const {
@@ -247,13 +257,16 @@ __device__ __forceinline__ void store_row(void* y, int64_t at, const float (&v)[
     }
 }
 
-// g / (1 + exp(-g)) to a few steps of fp32, by e = exp(-|g|) <= 1: the exponent of 2 in two parts, a reciprocal improved
-// once.  (The library's exponential and a full division take a third of a tile's time.)
+// g / (1 + exp(-g)) by e = exp(-|g|) <= 1.  For outputs of 16 bits: e to |g| 2^-24 of itself, the rounding of its exponent, 2^-17
+// where it matters.  For fp32 to a few of its steps: the exponent of 2 in two parts, a reciprocal improved once.  (The
+// library's exponential and a full division took a third of a tile's time.)
+template <int DT>
 __device__ __forceinline__ float silu(float g) {
     const float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
-    const float a = -fabsf(g), t = a * kLog2e;
+    const float a = -fabsf(g), t = a * kLog2e, p = __builtin_amdgcn_exp2f(t);
+    if constexpr (DT != QK_F32) return g * (g >= 0.0f ? 1.0f : p) * __builtin_amdgcn_rcpf(1.0f + p);
     const float low = fmaf(a, kLog2eLow, fmaf(a, kLog2e, -t));
-    const float p = __builtin_amdgcn_exp2f(t), e = fmaf(p, low * kLn2, p), d = 1.0f + e;
+    const float e = fmaf(p, low * kLn2, p), d = 1.0f + e;
     const float r = __builtin_amdgcn_rcpf(d), q = fmaf(fmaf(-d, r, 1.0f), r, r);
     return g * (g >= 0.0f ? q : e * q);
 }
@@ -268,9 +281,10 @@ __device__ __forceinline__ int column_of(int q) {
 }
 
 // Outputs of one wave: acc[i][j], rows 16 i + lane % 16 of the wave's rows m, columns 4 (lane / 16) + q of block j of its n (up:
-// the second half of the blocks are the up products of the first).
+// the second half of the blocks are the up products of the first).  slots, weights: of the tile's rows.
 template <Mode MODE, int DT, bool kWhole, int MT, int RT>
-__device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, int m, int n, const floatx4_t (&acc)[MT][RT]) {
+__device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, const int32_t* slots, const float* weights, int m,
+                                              int n, const floatx4_t (&acc)[MT][RT]) {
     const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
     constexpr int kCols = MODE == kUp ? RT / 2 : RT, kPair = kCols % 2 == 0 ? 2 : 1, kN = 4 * kPair;
     const int64_t col0 = t.n0 + n + kN * h;
@@ -283,8 +297,8 @@ __device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, 
         if constexpr (MODE == kDense) {
             row = t.m0 + pos;
         } else {
-            row = a.list[t.m0 + pos];
-            if constexpr (MODE == kDown) wt = t.expert < a.E ? a.weights[row] : 0.0f;
+            row = slots[pos];
+            if constexpr (MODE == kDown) wt = weights[pos];
         }
 #pragma unroll
         for (int j = 0; j < kCols; j += kPair) {
@@ -295,7 +309,7 @@ __device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, 
             for (int q = 0; q < kN; ++q) {
                 const int b = j + q / 4;
                 v[q] = acc[i][b][q % 4];
-                if constexpr (MODE == kUp) v[q] = silu(v[q]) * acc[i][b + RT / 2][q % 4];
+                if constexpr (MODE == kUp) v[q] = silu<DT>(v[q]) * acc[i][b + RT / 2][q % 4];
                 if constexpr (MODE == kDown) v[q] *= wt;
             }
             store_row<DT, kN>(a.y, row * a.N + col, v, kWhole ? kN : a.N - col);
@@ -303,18 +317,18 @@ __device__ __forceinline__ void store_outputs(const GemmArgs& a, const Tile& t, 
     }
 }
 
-template <Mode MODE, bool kWhole, int MT, int RT>
-__device__ __forceinline__ void store_typed(const GemmArgs& a, const Tile& t, int m, int n, const floatx4_t (&acc)[MT][RT]) {
-    if (MODE == kDown || a.y_dtype == QK_F32) store_outputs<MODE, QK_F32, kWhole>(a, t, m, n, acc);
-    else if (a.y_dtype == QK_BF16) store_outputs<MODE, QK_BF16, kWhole>(a, t, m, n, acc);
-    else store_outputs<MODE, QK_F16, kWhole>(a, t, m, n, acc);
-}
-
 template <Mode MODE, int MT, int RT>
-__device__ __forceinline__ void store_wave(const GemmArgs& a, const Tile& t, int m, int n, const floatx4_t (&acc)[MT][RT]) {
+__device__ __forceinline__ void store_wave(const GemmArgs& a, const Tile& t, const int32_t* slots, const float* weights, int m, int n,
+                                           const floatx4_t (&acc)[MT][RT]) {
     const bool whole = m + 16 * MT <= t.count && t.n0 + n + 16 * (MODE == kUp ? RT / 2 : RT) <= a.N;
-    if (whole) store_typed<MODE, true>(a, t, m, n, acc);
-    else store_typed<MODE, false>(a, t, m, n, acc);
+    auto typed = [&](auto Whole) {
+        constexpr bool w = decltype(Whole)::value;
+        if (MODE == kDown || a.y_dtype == QK_F32) store_outputs<MODE, QK_F32, w>(a, t, slots, weights, m, n, acc);
+        else if (a.y_dtype == QK_BF16) store_outputs<MODE, QK_BF16, w>(a, t, slots, weights, m, n, acc);
+        else store_outputs<MODE, QK_F16, w>(a, t, slots, weights, m, n, acc);
+    };
+    if (whole) typed(std::true_type{});
+    else typed(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
@@ -326,13 +340,21 @@ __device__ __forceinline__ void store_wave(const GemmArgs& a, const Tile& t, int
 // scheduling barriers keep it).  Between the halves, when the W lines of the stage have been read, all waves meet, and the W
 // lines of the stage after next start on their way to the same place; two rows before the stage ends they meet again: the
 // next stage has landed, and the X lines of the stage after next follow.
+//
+// A workgroup makes one tile after the other (kTurns; a launch has as many as are on the CUs at a time): while a tile is
+// multiplied the slots of the next one's rows come from the plan, and its first copies are on their way while outputs are
+// stored.  4096 tokens of 64 experts, up: 117 us where every tile has a workgroup of its own, 107 so.  Not in the largest tiles, whose
+// sums leave no registers for it.
 // ---------------------------------------------------------------------------
+constexpr bool takes_turns(int BM, int BN) { return BM * BN < 256 * 256; }
+
 template <Mode MODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(GemmArgs a) {
     constexpr int kWaves = (BM / WM) * (BN / WN), kThreads = kWaves * 64;
     constexpr int MT = WM / 16, RT = WN / 16;
     static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && BM % 64 == 0 && BN % 64 == 0);
     constexpr int kBNo = MODE == kUp ? BN / 2 : BN;
+    constexpr bool kTurns = takes_turns(BM, BN);
     // codes of X and of W by the parity of the stage, 128 bytes a line (objects of their own: the compiler waits for copies on
     // their way to the object that it reads from); scales of two stages, 16 bytes a line, by the parity of the pair
     __shared__ __align__(16) uint8_t x0[BM * 128];
@@ -340,27 +362,110 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
     __shared__ __align__(16) uint8_t x1[BM * 128];
     __shared__ __align__(16) uint8_t w1[BN * 128];
     __shared__ __align__(16) uint8_t sc[2 * (BM + BN) * 16];
+    // slots of the tile's rows and their weights, by the parity of the tile
+    __shared__ int32_t slots[MODE == kDense ? 1 : 2 * BM];
+    __shared__ float weights[MODE == kDown ? 2 * BM : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / (BN / WN), wn = wave % (BN / WN);
     const int r = lane & 15, h = lane >> 4;
-    const Tile t = find_tile<MODE != kDense, BM, kBNo>(a);
-    if (t.count <= 0) return;
-    floatx4_t acc[MT][RT];
+    const Tiling<MODE != kDense, BM, kBNo> tiling(a);
+    uint32_t id = blockIdx.x;
+    if (id >= tiling.count()) return;
+    Tile t = tiling.at(a, id);
+    const int nst = (a.x.cols + kLineK - 1) / kLineK;
+    const int valid = a.x.cols - (nst - 1) * kLineK;                  // inputs of the last line
+    Operands<MODE> op(a, t);
+    auto w_row = [&](int b) {                           // row b of the tile's W lines
+        const int q = column_of<MODE, RT>(b % WN);
+        return MODE == kUp ? op.w_row(b / WN * (WN / 2) + q % (WN / 2), q >= WN / 2) : op.w_row(b / WN * WN + q, false);
+    };
+    // what this lane copies: line l / 8 of 8, slot l % 8; and the lines whose scales it loads
+    constexpr int kXCopies = BM / 8 / kWaves, kWCopies = BN / 8 / kWaves, kSLoads = (BM + BN + kThreads - 1) / kThreads;
+    uint32_t xslot[kXCopies], sslot[kSLoads], xoff[kXCopies], woff[kWCopies], soff[kSLoads];
+    auto look_up = [&](const Tile& u) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+        for (int k = 0; k < kXCopies; ++k) xslot[k] = slot_at<MODE>(a, u, 8 * (wave + kWaves * k) + (lane >> 3));
 #pragma unroll
-        for (int j = 0; j < RT; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
-
-    if (MODE == kDense || t.expert < a.E) {
-        const Operands<MODE> op(a, t);
-        auto w_row = [&](int b) {                       // row b of the tile's W lines
-            const int q = column_of<MODE, RT>(b % WN);
-            return MODE == kUp ? op.w_row(b / WN * (WN / 2) + q % (WN / 2), q >= WN / 2) : op.w_row(b / WN * WN + q, false);
-        };
-        // what this lane copies: line l / 8 of 8, slot l % 8
-        constexpr int kXCopies = BM / 8 / kWaves, kWCopies = BN / 8 / kWaves, kSLoads = (BM + BN + kThreads - 1) / kThreads;
-        uint32_t xoff[kXCopies], woff[kWCopies], soff[kSLoads];
+        for (int k = 0; k < kSLoads; ++k)
+            if (64 * wave + kThreads * k < BM) sslot[k] = slot_at<MODE>(a, u, tid + kThreads * k);
+    };
+    // Copy k of stage st, which is line `line`; past the last stage every offset is outside its buffer, and zeros are written.
+    auto copy_x = [&](uint8_t* dst, int st, int line, int k) {
+        to_lds(op.xc, dst + (wave + kWaves * k) * 1024, xoff[k] | (st < nst ? 0u : 0xFFFF0000u), st < nst ? 128u * line : 0u);
+    };
+    auto copy_w = [&](uint8_t* dst, int st, int line, int k) {
+        to_lds(op.wc, dst + (wave + kWaves * k) * 1024, woff[k] | (st < nst ? 0u : 0xFFFF0000u), st < nst ? 128u * line : 0u);
+    };
+    // Scales come 16 bytes a line at a time, those of two stages, through registers: a line of memory that is brought for
+    // 8 of its bytes costs as much as one of codes.  In LDS dword h of a line holds groups 2 h and 2 h + 1 of the first stage,
+    // then of the second: what a lane needs.
+    u32x4_t sv[kSLoads], sl[kSLoads];
+    auto scale_load = [&](int k, uint32_t at) {
+        const bool x = 64 * wave + kThreads * k < BM;
+        return __builtin_amdgcn_raw_buffer_load_b128(x ? op.xs : op.ws, (int)soff[k], (int)at, 0);
+    };
+    auto scale_store = [&](int pair, int k) {
+        if (64 * wave + kThreads * k >= BM + BN) return;
+        const u32x4_t v = sv[k];
+        *reinterpret_cast<u32x4_t*>(sc + (pair & 1) * ((BM + BN) * 16) + (tid + kThreads * k) * 16) =
+            (u32x4_t){__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
+                      __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
+    };
+    const int xline = (wm * WM + r) * 128, wline = (wn * WN + r) * 128;
+    const int xsc = (wm * WM + r) * 16 + 4 * h, wsc = (BM + wn * WN + r) * 16 + 4 * h;
+    const int at0 = 16 * slot_of(r, 2 * h), at1 = 16 * slot_of(r, 2 * h + 1);
+    // fragments of W by half; those of X, of which four are enough; scales by the parity of the stage
+    v4i_t wf[2][RT], xf[4];
+    int ws[2][RT], xs[2][MT];
+    auto read_x = [&](const uint8_t* src, int s, int i) {
+        xf[i % 4] = *reinterpret_cast<const v4i_t*>(src + xline + (s ? at1 : at0) + 2048 * i);
+    };
+    auto read_w = [&](const uint8_t* src, int s, int j) {
+        wf[s][j] = *reinterpret_cast<const v4i_t*>(src + wline + (s ? at1 : at0) + 2048 * j);
+    };
+    auto read_scale = [&](int st, int p, int n) {
+        const uint8_t* src = sc + (st >> 1 & 1) * ((BM + BN) * 16);
+        if (n < RT) ws[p][n] = *reinterpret_cast<const int*>(src + wsc + 256 * n);
+        else xs[p][n - RT] = *reinterpret_cast<const int*>(src + xsc + 256 * (n - RT));
+    };
+    static_assert(MT % 4 == 0);
+    constexpr int kOps = MT * RT, kTail = 2 * RT;                 // instructions of a half; of it behind the meeting
+    // Items 0..n-1 spread over instructions [from, to): those behind instruction o.
+    auto spread = [](auto O, auto From, auto To, auto N, auto&& item) {
+        constexpr int o = decltype(O)::value - decltype(From)::value, ops = decltype(To)::value - decltype(From)::value;
+        constexpr int n = decltype(N)::value;
+        static_assert(ops > 0);
+        if constexpr (o >= 0 && o < ops) {
+            constexpr int k0 = (o * n + ops - 1) / ops, k1 = ((o + 1) * n + ops - 1) / ops;
+            each<k1 - k0>([&](auto K) { item(k0 + decltype(K)::value); });
+        }
+    };
+    // Waves meet once all but the last `flying` copies of each have landed and its reads are done.
+    auto meet = [&](auto Flying) {
+        constexpr int n = decltype(Flying)::value;
+        __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x70);   // vmcnt(n) expcnt(7) lgkmcnt(0)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int kXEarly = kXCopies / 4;                             // of the copies of X before the next stage begins
+    typedef std::integral_constant<int, kXEarly> XEarly;
+    typedef std::integral_constant<int, kWCopies> WCopies;
+    // Sends the first copies of tile u on their way (the last line, which may end early, comes first), from what look_up found.
+    auto begin = [&](const Tile& u, int parity) {
+        if constexpr (MODE != kDense) {
+#pragma unroll
+            for (int k = 0; k < kSLoads; ++k) {
+                const int line = tid + kThreads * k;
+                if (64 * wave + kThreads * k >= BM) continue;
+                slots[parity * BM + line] = (int32_t)sslot[k];
+                if constexpr (MODE == kDown) weights[parity * BM + line] = u.expert < a.E ? a.weights[sslot[k]] : 0.0f;
+            }
+            if (u.expert >= a.E) return;
+        }
+        op = Operands<MODE>(a, u);
 #pragma unroll
         for (int k = 0; k < kWCopies; ++k) {
             const int line = 8 * (wave + kWaves * k) + (lane >> 3);
@@ -369,163 +474,121 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
 #pragma unroll
         for (int k = 0; k < kXCopies; ++k) {
             const int line = 8 * (wave + kWaves * k) + (lane >> 3);
-            xoff[k] = op.x_row(line) * (uint32_t)a.x.code_stride + 16 * piece_in(line, lane & 7);
+            xoff[k] = op.row_of(xslot[k]) * (uint32_t)a.x.code_stride + 16 * piece_in(line, lane & 7);
         }
-        // and the lines whose scales it loads
 #pragma unroll
-        for (int k = 0; k < kSLoads; ++k) {
-            const int line = tid + kThreads * k;
-            soff[k] = line < BM ? op.x_row(line) * (uint32_t)a.x.scale_stride
-                                : w_row(min(line - BM, BN - 1)) * (uint32_t)a.w.scale_stride;
-        }
-        const int nst = (a.x.cols + kLineK - 1) / kLineK;
-        // Copy k of stage st, which is line `line`; past the last stage every offset is outside its buffer, and zeros are
-        // written.
-        auto copy_x = [&](uint8_t* dst, int st, int line, int k) {
-            to_lds(op.xc, dst + (wave + kWaves * k) * 1024, xoff[k] | (st < nst ? 0u : 0xFFFF0000u), st < nst ? 128u * line : 0u);
-        };
-        auto copy_w = [&](uint8_t* dst, int st, int line, int k) {
-            to_lds(op.wc, dst + (wave + kWaves * k) * 1024, woff[k] | (st < nst ? 0u : 0xFFFF0000u), st < nst ? 128u * line : 0u);
-        };
-        // Scales come 16 bytes a line at a time, those of two stages, through registers: a line of memory that is brought for
-        // 8 of its bytes costs as much as one of codes.
-        u32x4_t sv[kSLoads];
-        auto scale_load = [&](int k, uint32_t at) {
-            const bool x = 64 * wave + kThreads * k < BM;
-            return __builtin_amdgcn_raw_buffer_load_b128(x ? op.xs : op.ws, (int)soff[k], (int)at, 0);
-        };
-        auto scale_store = [&](int pair, int k) {
-            if (64 * wave + kThreads * k >= BM + BN) return;
-            const u32x4_t v = sv[k];
-            *reinterpret_cast<u32x4_t*>(sc + (pair & 1) * ((BM + BN) * 16) + (tid + kThreads * k) * 16) =
-                (u32x4_t){__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-                          __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
-        };
-        const int xline = (wm * WM + r) * 128, wline = (wn * WN + r) * 128;
-        const int xsc = (wm * WM + r) * 16 + 4 * h, wsc = (BM + wn * WN + r) * 16 + 4 * h;
-        const int at0 = 16 * slot_of(r, 2 * h), at1 = 16 * slot_of(r, 2 * h + 1);
-        // fragments of W by half; those of X, of which four are enough; scales by the parity of the stage
-        v4i_t wf[2][RT], xf[4];
-        int ws[2][RT], xs[2][MT];
-        auto read_x = [&](const uint8_t* src, int s, int i) {
-            xf[i % 4] = *reinterpret_cast<const v4i_t*>(src + xline + (s ? at1 : at0) + 2048 * i);
-        };
-        auto read_w = [&](const uint8_t* src, int s, int j) {
-            wf[s][j] = *reinterpret_cast<const v4i_t*>(src + wline + (s ? at1 : at0) + 2048 * j);
-        };
-        auto read_scale = [&](int st, int p, int n) {
-            const uint8_t* src = sc + (st >> 1 & 1) * ((BM + BN) * 16);
-            if (n < RT) ws[p][n] = *reinterpret_cast<const int*>(src + wsc + 256 * n);
-            else xs[p][n - RT] = *reinterpret_cast<const int*>(src + xsc + 256 * (n - RT));
-        };
-        static_assert(MT % 4 == 0);
-        constexpr int kOps = MT * RT, kTail = 2 * RT;                 // instructions of a half; of it behind the meeting
-        // Items 0..n-1 spread over instructions [from, to): those behind instruction o.
-        auto spread = [](auto O, auto From, auto To, auto N, auto&& item) {
-            constexpr int o = decltype(O)::value - decltype(From)::value, ops = decltype(To)::value - decltype(From)::value;
-            constexpr int n = decltype(N)::value;
-            static_assert(ops > 0);
-            if constexpr (o >= 0 && o < ops) {
-                constexpr int k0 = (o * n + ops - 1) / ops, k1 = ((o + 1) * n + ops - 1) / ops;
-                each<k1 - k0>([&](auto K) { item(k0 + decltype(K)::value); });
-            }
-        };
-        // Waves meet once all but the last `flying` copies of each have landed and its reads are done.
-        auto meet = [&](auto Flying) {
-            constexpr int n = decltype(Flying)::value;
-            __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x70);   // vmcnt(n) expcnt(7) lgkmcnt(0)
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        constexpr int kXEarly = kXCopies / 4;                         // of the copies of X before the next stage begins
-        typedef std::integral_constant<int, kXEarly> XEarly;
-        typedef std::integral_constant<int, kWCopies> WCopies;
-        auto stage = [&](auto P, uint8_t* x, uint8_t* w, uint8_t* xnext, uint8_t* wnext, int st) {
-            constexpr int p = decltype(P)::value;
-            each<2>([&](auto S) {
-                constexpr int s = decltype(S)::value;
-                each<kOps>([&](auto O) {
-                    constexpr int o = decltype(O)::value, i = o / RT, j = o % RT;
-                    if constexpr (s == 1 && o == 0) meet(std::integral_constant<int, 63>{});
-                    if constexpr (s == 1 && o == kOps - kTail) meet(WCopies{});
-                    mfma_in_place<2 * p + s>(acc[i][j], wf[s][j], ws[p][j], xf[i % 4], xs[p][i]);
-                    if constexpr (j == 0) {
-                        if constexpr (i + 2 < MT) read_x(x, s, i + 2);
-                        else read_x(s == 0 ? x : xnext, 1 - s, i + 2 - MT);
-                    }
-                    typedef std::integral_constant<int, 0> Begin;
-                    typedef std::integral_constant<int, kOps - kTail> Meeting;
-                    typedef std::integral_constant<int, kOps> End;
-                    if constexpr (s == 0) {
-                        spread(O, Begin{}, std::integral_constant<int, kOps / 2>{}, std::integral_constant<int, kXCopies - kXEarly>{},
-                               [&](int k) { copy_x(xnext, st + 1, st, kXEarly + k); });
-                        // (p == 0: scales of stages st + 2 and st + 3)
-                        if constexpr (p == 0)
-                            spread(O, std::integral_constant<int, kOps / 2>{}, End{}, std::integral_constant<int, kSLoads>{},
-                                   [&](int k) { sv[k] = scale_load(k, 8u * (st + 1)); });
-                        spread(O, Begin{}, Meeting{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(w, 1, k); });
-                    } else {
-                        if constexpr (p == 1)
-                            spread(O, Begin{}, Meeting{}, std::integral_constant<int, kSLoads>{}, [&](int k) {
-                                // the second of the pair may be past the end: its codes are zeros, but not its scales
-                                if (st + 2 >= nst) sv[k][2] = sv[k][3] = 0;
-                                scale_store((st + 1) >> 1, k);
-                            });
-                        spread(O, Begin{}, Meeting{}, WCopies{}, [&](int k) { copy_w(w, st + 2, st + 1, k); });
-                        spread(O, Meeting{}, End{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(wnext, 0, k); });
-                        spread(O, Meeting{}, End{}, std::integral_constant<int, RT + MT>{}, [&](int k) { read_scale(st + 1, 1 - p, k); });
-                        spread(O, Meeting{}, End{}, XEarly{}, [&](int k) { copy_x(x, st + 2, st + 1, k); });
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                });
-            });
-        };
-        // the last line, which may end early, comes first
-        const int valid = a.x.cols - (nst - 1) * kLineK;              // inputs of it
+        for (int k = 0; k < kSLoads; ++k)
+            soff[k] = 64 * wave + kThreads * k < BM ? op.row_of(sslot[k]) * (uint32_t)a.x.scale_stride
+                                                    : w_row(min(tid + kThreads * k - BM, BN - 1)) * (uint32_t)a.w.scale_stride;
 #pragma unroll
         for (int k = 0; k < kWCopies; ++k) copy_w(w0, 0, nst - 1, k);
 #pragma unroll
         for (int k = 0; k < kXCopies; ++k) copy_x(x0, 0, nst - 1, k);
 #pragma unroll
+        for (int k = 0; k < kSLoads; ++k) {
+            sl[k] = scale_load(k, 8u * (nst - 1));
+            sv[k] = scale_load(k, 0);
+        }
+#pragma unroll
         for (int k = 0; k < kWCopies; ++k) copy_w(w1, 1, 0, k);
 #pragma unroll
         for (int k = 0; k < kXEarly; ++k) copy_x(x1, 1, 0, k);
-        // scales of the first pair: the last line's, 1 past the end, then those of line 0
+    };
+    look_up(t);
+    begin(t, 0);
+    for (int parity = 0;; parity ^= 1) {
+        const bool live = MODE == kDense || t.expert < a.E, more = kTurns && id + gridDim.x < tiling.count();
+        Tile next = t;
+        if (more) next = tiling.at(a, id + gridDim.x);
+        floatx4_t acc[MT][RT];
 #pragma unroll
-        for (int k = 0; k < kSLoads; ++k) {
-            const u32x4_t last = scale_load(k, 8u * (nst - 1)), first = scale_load(k, 0);
-            const int groups = (valid + kGroup - 1) / kGroup;
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                const int n = groups - 4 * d;
-                const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
-                sv[k][d] = (last[d] & keep) | (0x7F7F7F7Fu & ~keep);
-                sv[k][2 + d] = nst > 1 ? first[d] : 0u;
+            for (int j = 0; j < RT; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
+        if (live) {
+            auto stage = [&](auto P, uint8_t* x, uint8_t* w, uint8_t* xnext, uint8_t* wnext, int st) {
+                constexpr int p = decltype(P)::value;
+                each<2>([&](auto S) {
+                    constexpr int s = decltype(S)::value;
+                    each<kOps>([&](auto O) {
+                        constexpr int o = decltype(O)::value, i = o / RT, j = o % RT;
+                        if constexpr (s == 1 && o == 0) meet(std::integral_constant<int, 63>{});
+                        if constexpr (s == 1 && o == kOps - kTail) meet(WCopies{});
+                        mfma_in_place<2 * p + s>(acc[i][j], wf[s][j], ws[p][j], xf[i % 4], xs[p][i]);
+                        if constexpr (j == 0) {
+                            if constexpr (i + 2 < MT) read_x(x, s, i + 2);
+                            else read_x(s == 0 ? x : xnext, 1 - s, i + 2 - MT);
+                        }
+                        typedef std::integral_constant<int, 0> Begin;
+                        typedef std::integral_constant<int, kOps - kTail> Meeting;
+                        typedef std::integral_constant<int, kOps> End;
+                        if constexpr (s == 0) {
+                            spread(O, Begin{}, std::integral_constant<int, kOps / 2>{}, std::integral_constant<int, kXCopies - kXEarly>{},
+                                   [&](int k) { copy_x(xnext, st + 1, st, kXEarly + k); });
+                            // (p == 0: scales of stages st + 2 and st + 3)
+                            if constexpr (p == 0)
+                                spread(O, std::integral_constant<int, kOps / 2>{}, End{}, std::integral_constant<int, kSLoads>{},
+                                       [&](int k) { sv[k] = scale_load(k, 8u * (st + 1)); });
+                            spread(O, Begin{}, Meeting{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(w, 1, k); });
+                        } else {
+                            if constexpr (p == 1)
+                                spread(O, Begin{}, Meeting{}, std::integral_constant<int, kSLoads>{}, [&](int k) {
+                                    // the second of the pair may be past the end: its codes are zeros, but not its scales
+                                    if (st + 2 >= nst) sv[k][2] = sv[k][3] = 0;
+                                    scale_store((st + 1) >> 1, k);
+                                });
+                            spread(O, Begin{}, Meeting{}, WCopies{}, [&](int k) { copy_w(w, st + 2, st + 1, k); });
+                            spread(O, Meeting{}, End{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(wnext, 0, k); });
+                            spread(O, Meeting{}, End{}, std::integral_constant<int, RT + MT>{}, [&](int k) { read_scale(st + 1, 1 - p, k); });
+                            spread(O, Meeting{}, End{}, XEarly{}, [&](int k) { copy_x(x, st + 2, st + 1, k); });
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                });
+            };
+            // scales of the first pair: the last line's, 1 past the end, then those of line 0
+#pragma unroll
+            for (int k = 0; k < kSLoads; ++k) {
+                const int groups = (valid + kGroup - 1) / kGroup;
+                const u32x4_t first = sv[k];
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    const int n = groups - 4 * d;
+                    const uint32_t keep = n >= 4 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+                    sv[k][d] = (sl[k][d] & keep) | (0x7F7F7F7Fu & ~keep);
+                    sv[k][2 + d] = nst > 1 ? first[d] : 0u;
+                }
+                scale_store(0, k);
             }
-            scale_store(0, k);
-        }
-        meet(std::integral_constant<int, 0>{});
-        if (valid < kLineK) {
-            for (int l = tid; l < BM; l += kThreads) end_codes(x0 + 128 * l, l, valid);
-            __syncthreads();
-        }
+            meet(std::integral_constant<int, 0>{});
+            if (more) look_up(next);
+            if (valid < kLineK) {
+                for (int l = tid; l < BM; l += kThreads) end_codes(x0 + 128 * l, l, valid);
+                __syncthreads();
+            }
 #pragma unroll
-        for (int j = 0; j < RT; ++j) read_w(w0, 0, j);
+            for (int j = 0; j < RT; ++j) read_w(w0, 0, j);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) read_x(x0, 0, i);
+            for (int i = 0; i < 2; ++i) read_x(x0, 0, i);
 #pragma unroll
-        for (int k = 0; k < RT + MT; ++k) read_scale(0, 0, k);
-        // (an odd number of stages is one more of zeros: a way out between the two costs the compiler the registers)
-        for (int st = 0; st < nst; st += 2) {
-            stage(std::integral_constant<int, 0>{}, x0, w0, x1, w1, st);
-            stage(std::integral_constant<int, 1>{}, x1, w1, x0, w0, st + 1);
+            for (int k = 0; k < RT + MT; ++k) read_scale(0, 0, k);
+            // (an odd number of stages is one more of zeros: a way out between the two costs the compiler the registers)
+            for (int st = 0; st < nst; st += 2) {
+                stage(std::integral_constant<int, 0>{}, x0, w0, x1, w1, st);
+                stage(std::integral_constant<int, 1>{}, x1, w1, x0, w0, st + 1);
+            }
+            __builtin_amdgcn_s_waitcnt(0);                            // nothing on its way to LDS any more
+            settle<MT, RT>(acc);
+        } else if (more) {
+            look_up(next);
         }
-        __builtin_amdgcn_s_waitcnt(0);                                // nothing on its way to LDS any more
-        settle<MT, RT>(acc);
+        if (more || !live) __syncthreads();                           // every wave is done with LDS; slots are there
+        if (more) begin(next, parity ^ 1);
+        store_wave<MODE>(a, t, slots + parity * BM, weights + parity * BM, wm * WM, MODE == kUp ? wn * (WN / 2) : wn * WN, acc);
+        if (!more) return;
+        t = next;
+        id += gridDim.x;
     }
-    store_wave<MODE>(a, t, wm * WM, MODE == kUp ? wn * (WN / 2) : wn * WN, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -545,11 +608,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_kernel(GemmArgs a) {
     __shared__ __align__(16) uint8_t lds0[kFewWaves * kStage];
     __shared__ __align__(16) uint8_t lds1[kFewWaves * kStage];
     __shared__ __align__(16) uint8_t lds2[kFewWaves * kStage];
+    __shared__ int32_t slots[MODE == kDense ? 1 : 16 * MT];
+    __shared__ float weights[MODE == kDown ? 16 * MT : 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, h = lane >> 4;
-    const Tile t = find_tile<MODE != kDense, 16 * MT, kBNo>(a);
-    if (t.count <= 0) return;
+    const Tiling<MODE != kDense, 16 * MT, kBNo> tiling(a);
+    if (blockIdx.x >= tiling.count()) return;
+    const Tile t = tiling.at(a, blockIdx.x);
     floatx4_t acc[MT][RT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -566,14 +632,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_kernel(GemmArgs a) {
 #pragma unroll
         for (int v = 0; v < kLoads; ++v) {
             const int line = 8 * v + (lane >> 3), piece = piece_in(line, lane & 7);
-            voff[v] = v < 2 * MT ? op.x_row(line) * (uint32_t)a.x.code_stride + 16 * piece
+            voff[v] = v < 2 * MT ? op.row_of(slot_at<MODE>(a, t, line)) * (uint32_t)a.x.code_stride + 16 * piece
                                  : w_row(line - 16 * MT) * (uint32_t)a.w.code_stride + 16 * piece;
         }
         // scales: 32 lines an instruction, or two with half the lanes each where the first 16 are of X
 #pragma unroll
         for (int v = 0; v < kSLoads; ++v) {
             const int line = 32 * v + (lane >> 1);
-            soff[v] = 4 * (lane & 1) + (line < 16 * MT ? op.x_row(line) * (uint32_t)a.x.scale_stride
+            soff[v] = 4 * (lane & 1) + (line < 16 * MT ? op.row_of(slot_at<MODE>(a, t, line)) * (uint32_t)a.x.scale_stride
                                                        : w_row(line - 16 * MT) * (uint32_t)a.w.scale_stride);
         }
         const int nst = (a.x.cols + kLineK - 1) / kLineK;
@@ -667,7 +733,16 @@ __global__ __launch_bounds__(kFewWaves * 64) void mx4_few_kernel(GemmArgs a) {
             }
     }
     if (wave > 0) return;
-    store_wave<MODE>(a, t, 0, 0, acc);
+    if constexpr (MODE != kDense) {
+        if (lane < 16 * MT) {
+            const uint32_t slot = slot_at<MODE>(a, t, lane);
+            slots[lane] = (int32_t)slot;
+            if constexpr (MODE == kDown) weights[lane] = t.expert < a.E ? a.weights[slot] : 0.0f;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    store_wave<MODE>(a, t, slots, weights, 0, 0, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -713,8 +788,11 @@ int64_t grid_for(const GemmArgs& a, int64_t bm, int64_t bno) {
 
 template <Mode MODE, int BM, int BN, int WM, int WN>
 hipError_t launch_tile(const GemmArgs& a, hipStream_t s) {
-    const int64_t grid = grid_for<MODE>(a, BM, MODE == kUp ? BN / 2 : BN);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const int64_t tiles = grid_for<MODE>(a, BM, MODE == kUp ? BN / 2 : BN);
+    if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
+    // workgroups that the LDS of the CUs holds
+    constexpr int64_t kLds = (BM + BN) * 288 + (MODE == kDense ? 0 : MODE == kUp ? 8 : 16) * BM;
+    const int64_t grid = std::min<int64_t>(tiles, takes_turns(BM, BN) ? device_cu_count() / kXcds * kXcds * (160 * 1024 / kLds) : tiles);
     mx4_tile_kernel<MODE, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3((BM / WM) * (BN / WN) * 64), 0, s>>>(a);
     return hipGetLastError();
 }
