@@ -341,6 +341,9 @@ __device__ __forceinline__ void store_wave(const GemmArgs& a, const Tile& t, con
 // lines of the stage after next start on their way to the same place; two rows before the stage ends they meet again: the
 // next stage has landed, and the X lines of the stage after next follow.
 //
+// A stage's copies set out two stages before it (W: one and a half of them, X: one), or one stage earlier yet where LDS
+// holds a ring of three (kRing).
+//
 // A workgroup makes one tile after the other (kTurns; a launch has as many as are on the CUs at a time): while a tile is
 // multiplied the slots of the next one's rows come from the plan, and its first copies are on their way while outputs are
 // stored.  4096 tokens of 64 experts, up: 117 us where every tile has a workgroup of its own, 107 so.  Not in the largest tiles, whose
@@ -348,7 +351,7 @@ __device__ __forceinline__ void store_wave(const GemmArgs& a, const Tile& t, con
 // ---------------------------------------------------------------------------
 constexpr bool takes_turns(int BM, int BN) { return BM * BN < 256 * 256; }
 
-template <Mode MODE, int BM, int BN, int WM, int WN>
+template <Mode MODE, int BM, int BN, int WM, int WN, int kRing>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(GemmArgs a) {
     constexpr int kWaves = (BM / WM) * (BN / WN), kThreads = kWaves * 64;
     constexpr int MT = WM / 16, RT = WN / 16;
@@ -361,6 +364,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
     __shared__ __align__(16) uint8_t w0[BN * 128];
     __shared__ __align__(16) uint8_t x1[BM * 128];
     __shared__ __align__(16) uint8_t w1[BN * 128];
+    __shared__ __align__(16) uint8_t x2[kRing > 2 ? BM * 128 : 16];
+    __shared__ __align__(16) uint8_t w2[kRing > 2 ? BN * 128 : 16];
     __shared__ __align__(16) uint8_t sc[2 * (BM + BN) * 16];
     // slots of the tile's rows and their weights, by the parity of the tile
     __shared__ int32_t slots[MODE == kDense ? 1 : 2 * BM];
@@ -453,6 +458,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
     constexpr int kXEarly = kXCopies / 4;                             // of the copies of X before the next stage begins
     typedef std::integral_constant<int, kXEarly> XEarly;
     typedef std::integral_constant<int, kWCopies> WCopies;
+    // copies that are sent off later than those of the next stage: W's of the last one to come, in a ring of three all of the one before
+    typedef std::integral_constant<int, kWCopies + (kRing - 2) * (kWCopies + kXCopies)> Flying;
     // Sends the first copies of tile u on their way (the last line, which may end early, comes first), from what look_up found.
     auto begin = [&](const Tile& u, int parity) {
         if constexpr (MODE != kDense) {
@@ -491,8 +498,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
         }
 #pragma unroll
         for (int k = 0; k < kWCopies; ++k) copy_w(w1, 1, 0, k);
+        if constexpr (kRing > 2) {
 #pragma unroll
-        for (int k = 0; k < kXEarly; ++k) copy_x(x1, 1, 0, k);
+            for (int k = 0; k < kXCopies; ++k) copy_x(x1, 1, 0, k);
+#pragma unroll
+            for (int k = 0; k < kWCopies; ++k) copy_w(w2, 2, 1, k);
+        }
+#pragma unroll
+        for (int k = 0; k < kXEarly; ++k) copy_x(kRing > 2 ? x2 : x1, kRing - 1, kRing - 2, k);
     };
     look_up(t);
     begin(t, 0);
@@ -506,14 +519,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
 #pragma unroll
             for (int j = 0; j < RT; ++j) acc[i][j] = (floatx4_t){0, 0, 0, 0};
         if (live) {
-            auto stage = [&](auto P, uint8_t* x, uint8_t* w, uint8_t* xnext, uint8_t* wnext, int st) {
+            auto stage = [&](auto P, uint8_t* x, uint8_t* w, uint8_t* xnext, uint8_t* wnext, uint8_t* xlast, int st) {
                 constexpr int p = decltype(P)::value;
                 each<2>([&](auto S) {
                     constexpr int s = decltype(S)::value;
                     each<kOps>([&](auto O) {
                         constexpr int o = decltype(O)::value, i = o / RT, j = o % RT;
                         if constexpr (s == 1 && o == 0) meet(std::integral_constant<int, 63>{});
-                        if constexpr (s == 1 && o == kOps - kTail) meet(WCopies{});
+                        if constexpr (s == 1 && o == kOps - kTail) meet(Flying{});
                         mfma_in_place<2 * p + s>(acc[i][j], wf[s][j], ws[p][j], xf[i % 4], xs[p][i]);
                         if constexpr (j == 0) {
                             if constexpr (i + 2 < MT) read_x(x, s, i + 2);
@@ -524,7 +537,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
                         typedef std::integral_constant<int, kOps> End;
                         if constexpr (s == 0) {
                             spread(O, Begin{}, std::integral_constant<int, kOps / 2>{}, std::integral_constant<int, kXCopies - kXEarly>{},
-                                   [&](int k) { copy_x(xnext, st + 1, st, kXEarly + k); });
+                                   [&](int k) { copy_x(xlast, st + kRing - 1, st + kRing - 2, kXEarly + k); });
                             // (p == 0: scales of stages st + 2 and st + 3)
                             if constexpr (p == 0)
                                 spread(O, std::integral_constant<int, kOps / 2>{}, End{}, std::integral_constant<int, kSLoads>{},
@@ -537,10 +550,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
                                     if (st + 2 >= nst) sv[k][2] = sv[k][3] = 0;
                                     scale_store((st + 1) >> 1, k);
                                 });
-                            spread(O, Begin{}, Meeting{}, WCopies{}, [&](int k) { copy_w(w, st + 2, st + 1, k); });
+                            spread(O, Begin{}, Meeting{}, WCopies{}, [&](int k) { copy_w(w, st + kRing, st + kRing - 1, k); });
                             spread(O, Meeting{}, End{}, std::integral_constant<int, RT>{}, [&](int k) { read_w(wnext, 0, k); });
                             spread(O, Meeting{}, End{}, std::integral_constant<int, RT + MT>{}, [&](int k) { read_scale(st + 1, 1 - p, k); });
-                            spread(O, Meeting{}, End{}, XEarly{}, [&](int k) { copy_x(x, st + 2, st + 1, k); });
+                            spread(O, Meeting{}, End{}, XEarly{}, [&](int k) { copy_x(x, st + kRing, st + kRing - 1, k); });
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     });
@@ -560,7 +573,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
                 }
                 scale_store(0, k);
             }
-            meet(std::integral_constant<int, 0>{});
+            meet(std::integral_constant<int, kWCopies + kXEarly + (kRing - 2) * (kWCopies + kXCopies)>{});
             if (more) look_up(next);
             if (valid < kLineK) {
                 for (int l = tid; l < BM; l += kThreads) end_codes(x0 + 128 * l, l, valid);
@@ -573,9 +586,26 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
 #pragma unroll
             for (int k = 0; k < RT + MT; ++k) read_scale(0, 0, k);
             // (an odd number of stages is one more of zeros: a way out between the two costs the compiler the registers)
-            for (int st = 0; st < nst; st += 2) {
-                stage(std::integral_constant<int, 0>{}, x0, w0, x1, w1, st);
-                stage(std::integral_constant<int, 1>{}, x1, w1, x0, w0, st + 1);
+            const std::integral_constant<int, 0> even;
+            const std::integral_constant<int, 1> odd;
+            if constexpr (kRing == 2) {
+                for (int st = 0; st < nst; st += 2) {
+                    stage(even, x0, w0, x1, w1, x1, st);
+                    stage(odd, x1, w1, x0, w0, x0, st + 1);
+                }
+            } else {
+                for (int st = 0; st < nst; st += 6) {
+                    stage(even, x0, w0, x1, w1, x2, st);
+                    stage(odd, x1, w1, x2, w2, x0, st + 1);
+                    if (st + 2 < nst) {
+                        stage(even, x2, w2, x0, w0, x1, st + 2);
+                        stage(odd, x0, w0, x1, w1, x2, st + 3);
+                    }
+                    if (st + 4 < nst) {
+                        stage(even, x1, w1, x2, w2, x0, st + 4);
+                        stage(odd, x2, w2, x0, w0, x1, st + 5);
+                    }
+                }
             }
             __builtin_amdgcn_s_waitcnt(0);                            // nothing on its way to LDS any more
             settle<MT, RT>(acc);
@@ -786,14 +816,14 @@ int64_t grid_for(const GemmArgs& a, int64_t bm, int64_t bno) {
     return moe_most_tiles(a.slots, a.E) * cdiv(a.N, bno);
 }
 
-template <Mode MODE, int BM, int BN, int WM, int WN>
+template <Mode MODE, int BM, int BN, int WM, int WN, int kRing>
 hipError_t launch_tile(const GemmArgs& a, hipStream_t s) {
     const int64_t tiles = grid_for<MODE>(a, BM, MODE == kUp ? BN / 2 : BN);
     if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
     // workgroups that the LDS of the CUs holds
-    constexpr int64_t kLds = (BM + BN) * 288 + (MODE == kDense ? 0 : MODE == kUp ? 8 : 16) * BM;
+    constexpr int64_t kLds = (BM + BN) * (128 * kRing + 32) + (MODE == kDense ? 0 : MODE == kUp ? 8 : 16) * BM;
     const int64_t grid = std::min<int64_t>(tiles, takes_turns(BM, BN) ? device_cu_count() / kXcds * kXcds * (160 * 1024 / kLds) : tiles);
-    mx4_tile_kernel<MODE, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3((BM / WM) * (BN / WN) * 64), 0, s>>>(a);
+    mx4_tile_kernel<MODE, BM, BN, WM, WN, kRing><<<dim3((unsigned)grid), dim3((BM / WM) * (BN / WN) * 64), 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -816,26 +846,27 @@ hipError_t launch_dense(const GemmArgs& a, hipStream_t s) {
     // The largest tiles of which there is one for every CU: 4096 x 4096 x 4096 41, in tiles of 128 51; 2048 x 4096 x 4096 40 and
     // 25; 1000 x 4096 x 4096 in tiles of 128 15.4, of 64 x 128 17.2; 512 x 4096 x 4096 13.5 and 11.5; 200 x 4096 x 4096 in
     // tiles of 64 x 128 10.5, of 64 9.6.
-    if (grid_for<kDense>(a, 256, 256) >= cus) return launch_tile<kDense, 256, 256, 128, 128>(a, s);
-    if (grid_for<kDense>(a, 128, 128) >= cus) return launch_tile<kDense, 128, 128, 64, 64>(a, s);
-    if (grid_for<kDense>(a, 64, 128) >= cus * 5 / 8) return launch_tile<kDense, 64, 128, 64, 32>(a, s);
-    return launch_tile<kDense, 64, 64, 64, 32>(a, s);
+    if (grid_for<kDense>(a, 256, 256) >= cus) return launch_tile<kDense, 256, 256, 128, 128, 2>(a, s);
+    // A ring of three stages where it costs no second workgroup on a CU: 1000 x 4096 x 4096 14.6, of two 15.8 (weights from
+    // memory: 16.2 and 17.2); 200 x 4096 x 4096 8.7 and 9.3 (10.4 and 12.3).
+    const int64_t tiles = grid_for<kDense>(a, 128, 128);
+    if (tiles >= 2 * cus) return launch_tile<kDense, 128, 128, 64, 64, 2>(a, s);
+    if (tiles >= cus) return launch_tile<kDense, 128, 128, 64, 64, 3>(a, s);
+    if (grid_for<kDense>(a, 64, 128) >= cus * 5 / 8) return launch_tile<kDense, 64, 128, 64, 32, 3>(a, s);
+    return launch_tile<kDense, 64, 64, 64, 32, 3>(a, s);
 }
 
 template <Mode MODE>
 hipError_t launch_experts(const GemmArgs& a, hipStream_t s) {
     const int64_t cus = device_cu_count(), half = MODE == kUp ? 2 : 1;
-    if (moe_tile_rows(a.slots, a.E) == 128) {
-        // Rows of an expert on average.  512 tokens of 8 experts of 4096 x 11008, top 2 (down, 128 rows): 61, in tiles of
-        // 128 x 128 76; 4096 tokens of 64 experts, top 8 (up, 512 rows): 128 and 121.
-        const int64_t rows = a.slots / std::min<int64_t>(a.E, a.slots);
-        return rows <= 256 ? launch_tile<MODE, 128, 256, 64, 64>(a, s) : launch_tile<MODE, 128, 128, 64, 64>(a, s);
-    }
+    // (4096 tokens of 64 experts, top 8, up: 110 us, in tiles of 128 x 128 in a ring of two stages the same, with the weights from
+    // memory 122 and 127; 512 tokens of 8 experts of 4096 x 11008, top 2, down: 60 and 76)
+    if (moe_tile_rows(a.slots, a.E) == 128) return launch_tile<MODE, 128, 256, 64, 64, 3>(a, s);
     // A few slots of few outputs: the inputs split among the waves of a workgroup (one token's top 2 of 8 experts of
     // 4096 x 11008, down: 12.8, in tiles of 64 x 64 23).  Otherwise the larger tiles where they fill the CUs twice.
     if (a.slots <= 16 && grid_for<MODE>(a, 64, 64 / half) <= cus) return launch_few<MODE, 1, 2>(a, s);
-    if (grid_for<MODE>(a, 64, 128 / half) >= 2 * cus) return launch_tile<MODE, 64, 128, 64, 32>(a, s);
-    return launch_tile<MODE, 64, 64, 64, 32>(a, s);
+    if (grid_for<MODE>(a, 64, 128 / half) >= 2 * cus) return launch_tile<MODE, 64, 128, 64, 32, 2>(a, s);
+    return launch_tile<MODE, 64, 64, 64, 32, 2>(a, s);
 }
 
 }  // namespace
