@@ -844,24 +844,33 @@ hipError_t launch_dense(const GemmArgs& a, hipStream_t s) {
     if (a.M <= 128 && grid_for<kDense>(a, 64, 64) <= cus / 2)
         return a.M <= 32 ? launch_few<kDense, 2, 2>(a, s) : launch_few<kDense, 4, 2>(a, s);
     // The largest tiles of which there is one for every CU: 4096 x 4096 x 4096 41, in tiles of 128 51; 2048 x 4096 x 4096 40 and
-    // 25; 1000 x 4096 x 4096 in tiles of 128 15.4, of 64 x 128 17.2; 512 x 4096 x 4096 13.5 and 11.5; 200 x 4096 x 4096 in
-    // tiles of 64 x 128 10.5, of 64 9.6.
+    // 25.  Two workgroups a CU of tiles of 128 where there is more than one for each (1100 x 4096 x 4096 22.5, one workgroup and
+    // a ring of three stages 26), one and a ring of three up to that, where tiles of 64 x 128 would be more than the CUs
+    // (800 x 4096 x 4096 14.0, of 64 x 128 17.4; 600 x 3500 x 4096 12.9 and 16.1).  Below, those of 64 x 128 (512 x 4096 x 4096
+    // 11.5, of 128 12.5, of 64 13.5) down to 5 / 8 of the CUs (200 x 4096 x 4096 10.5, of 64 9.6), a ring of three always: 200
+    // x 4096 x 4096 in tiles of 64 with weights from memory 10.4, of two 12.3.
     if (grid_for<kDense>(a, 256, 256) >= cus) return launch_tile<kDense, 256, 256, 128, 128, 2>(a, s);
-    // A ring of three stages where it costs no second workgroup on a CU: 1000 x 4096 x 4096 14.6, of two 15.8 (weights from
-    // memory: 16.2 and 17.2); 200 x 4096 x 4096 8.7 and 9.3 (10.4 and 12.3).
-    const int64_t tiles = grid_for<kDense>(a, 128, 128);
-    if (tiles >= 2 * cus) return launch_tile<kDense, 128, 128, 64, 64, 2>(a, s);
-    if (tiles >= cus) return launch_tile<kDense, 128, 128, 64, 64, 3>(a, s);
-    if (grid_for<kDense>(a, 64, 128) >= cus * 5 / 8) return launch_tile<kDense, 64, 128, 64, 32, 3>(a, s);
+    if (grid_for<kDense>(a, 128, 128) > cus) return launch_tile<kDense, 128, 128, 64, 64, 2>(a, s);
+    const int64_t tiles = grid_for<kDense>(a, 64, 128);
+    if (tiles > cus) return launch_tile<kDense, 128, 128, 64, 64, 3>(a, s);
+    if (tiles >= cus * 5 / 8) return launch_tile<kDense, 64, 128, 64, 32, 3>(a, s);
     return launch_tile<kDense, 64, 64, 64, 32, 3>(a, s);
 }
 
 template <Mode MODE>
 hipError_t launch_experts(const GemmArgs& a, hipStream_t s) {
     const int64_t cus = device_cu_count(), half = MODE == kUp ? 2 : 1;
-    // (4096 tokens of 64 experts, top 8, up: 110 us, in tiles of 128 x 128 in a ring of two stages the same, with the weights from
-    // memory 122 and 127; 512 tokens of 8 experts of 4096 x 11008, top 2, down: 60 and 76)
-    if (moe_tile_rows(a.slots, a.E) == 128) return launch_tile<MODE, 128, 256, 64, 64, 3>(a, s);
+    if (moe_tile_rows(a.slots, a.E) == 128) {
+        // Tiles of 128 x 256, a ring of three stages and one workgroup a CU, where there is about one for each CU (half of
+        // an expert's last tile counted): 512 tokens of 8 experts of 4096 x 11008, top 2, down 60 us, in tiles of 128 x 128 76;
+        // 600 of 8 experts of 8192 inputs and 2048 outputs (107 tiles) 43 and 35; 1000 of the first (314 tiles) 107 and 100; 2048
+        // of 8 experts, up, of 4096 inputs and 2000 outputs (576 tiles) 61 and 55.  And where there are so many that the last turn
+        // does not matter: 4096 tokens of 64 experts, top 8, up (2320 tiles), weights from memory 123 and 126.
+        const int64_t experts = std::min<int64_t>(a.E, a.slots);
+        const int64_t tiles = (a.slots / 128 + (experts + 1) / 2) * cdiv(a.N, 256 / half);
+        if ((tiles > cus / 2 && tiles <= cus) || tiles > 8 * cus) return launch_tile<MODE, 128, 256, 64, 64, 3>(a, s);
+        return launch_tile<MODE, 128, 128, 64, 64, 2>(a, s);
+    }
     // A few slots of few outputs: the inputs split among the waves of a workgroup (one token's top 2 of 8 experts of
     // 4096 x 11008, down: 12.8, in tiles of 64 x 64 23).  Otherwise the larger tiles where they fill the CUs twice.
     if (a.slots <= 16 && grid_for<MODE>(a, 64, 64 / half) <= cus) return launch_few<MODE, 1, 2>(a, s);

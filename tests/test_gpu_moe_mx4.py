@@ -102,6 +102,30 @@ def test_experts(T, top_k, E, H, I):
     check(y, *_down_f64(c, T, top_k, E, H, I), torch.float32, "down")
 
 
+@pytest.mark.parametrize("T,top_k,E,H,I", [(1500, 2, 4, 300, 1500), (1500, 2, 4, 3001, 130), (400, 8, 64, 300, 500),
+                                           (400, 8, 64, 1100, 90), (2600, 1, 3, 700, 1290)])
+def test_more_tiles_than_workgroups(T, top_k, E, H, I):
+    """A workgroup makes several tiles, some of them of slots without an expert."""
+    c = _case(T, top_k, E, H, I, T + E + H)
+    h, y = _run(c, T, top_k, E, H, I, torch.float32)
+    flat = c["ids"].view(-1)
+    assert float(h[(flat < 0) | (flat >= E)].abs().sum()) == 0.0
+    check(h, *_up_f64(c, T, top_k, E, H, I), torch.float32, "up")
+    check(y, *_down_f64(c, T, top_k, E, H, I), torch.float32, "down")
+
+
+@pytest.mark.parametrize("K", [1, 32, 255, 256, 257, 512, 513, 770, 1030, 1290, 1536, 1540, 1800, 2049, 3100])
+@pytest.mark.parametrize("T", [60, 300])
+def test_experts_lengths(T, K):
+    E, top_k = 2, 2
+    c = _case(T, top_k, E, K, 72, T + K)
+    h, _ = _run(c, T, top_k, E, K, 72, torch.float32)
+    check(h, *_up_f64(c, T, top_k, E, K, 72), torch.float32, "up")
+    c = _case(T, top_k, E, 72, K, T + K + 1)
+    _, y = _run(c, T, top_k, E, 72, K, torch.float32)
+    check(y, *_down_f64(c, T, top_k, E, 72, K), torch.float32, "down")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("T", [1, 9, 90, 600])
 def test_experts_in_16_bits(dtype, T):

@@ -170,6 +170,12 @@ def test_gemm_large(dtype, M, N, K):
     _product(M, N, K, DT[dtype], M + N + K, 118, 126)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(2304, 4096, 300), (2250, 4001, 530), (1100, 4096, 1300), (1090, 4030, 2049)])
+def test_gemm_more_tiles_than_workgroups(dtype, M, N, K):
+    _product(M, N, K, DT[dtype], M + N + K, 118, 126)
+
+
 @pytest.mark.parametrize("M", [5, 30, 300])
 def test_gemm_wide_scales(M):
     """Groups of very different size, the least and the largest scales among them."""
