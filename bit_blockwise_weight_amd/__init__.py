@@ -1082,27 +1082,32 @@ def qk_mx4_quantize(x: torch.Tensor, codes=None, scales=None):
         raise ValueError("x needs at least one dimension")
     if not x.is_cuda:
         raise ValueError("tensors passed to libqk must be on a HIP device")
-    cols = x.shape[-1]
-    if x.dim() == 2 and not x.is_contiguous():
-        rows, pitch = x.shape[0], x.stride(0) if x.shape[0] > 1 else cols
+    shape = x.shape
+    cols = shape[-1]
+    if x.is_contiguous():
+        rows, pitch = x.numel() // max(1, cols), cols
+    else:
+        if len(shape) != 2:
+            raise ValueError("tensors passed to libqk must be contiguous")
+        rows = shape[0]
+        pitch = x.stride(0) if rows > 1 else cols
         if (cols > 1 and x.stride(1) != 1) or pitch < cols:
             raise ValueError("tensors passed to libqk must be contiguous (the rows of a 2-D x may lie apart)")
-        xp = x.data_ptr()
-    else:
-        rows, pitch = x.numel() // max(1, cols), cols
-        xp = _ready(x, x.device, "x")
     dev = x.device
     cs, ss = _mx4_strides(cols)
     if codes is None:
         codes = torch.empty((rows, cs), dtype=torch.uint8, device=dev)
+        cp = codes.data_ptr()
     else:
         _mx4_part(codes, rows, -(-cols // 2), 16, "codes")
+        cs, cp = codes.shape[1], _ready(codes, dev, "codes")
     if scales is None:
         scales = torch.empty((rows, ss), dtype=torch.uint8, device=dev)
+        sp = scales.data_ptr()
     else:
         _mx4_part(scales, rows, -(-cols // 32), 4, "scales")
-    _call(dev, lib().qk_mx4_quantize, xp, _DTYPE_CODE[x.dtype], rows, cols, pitch, _ready(codes, dev, "codes"),
-          codes.shape[1], _ready(scales, dev, "scales"), scales.shape[1])
+        ss, sp = scales.shape[1], _ready(scales, dev, "scales")
+    _call(dev, lib().qk_mx4_quantize, x.data_ptr(), _DTYPE_CODE[x.dtype], rows, cols, pitch, cp, cs, sp, ss)
     return codes, scales
 
 
@@ -1110,11 +1115,12 @@ def _mx4_out(t, shape, dtype, dev, name: str):
     """(output allocated or checked, its address, its dtype's code)"""
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"{name} must be fp32, bf16 or fp16, got {dtype}")
+    code = _DTYPE_CODE[dtype]
     if t is None:
         t = torch.empty(shape, dtype=dtype, device=dev)
-    else:
-        _check_out(t, shape, dtype, name)
-    return t, _ready(t, dev, name), _DTYPE_CODE[dtype]
+        return t, t.data_ptr(), code
+    _check_out(t, shape, dtype, name)
+    return t, _ready(t, dev, name), code
 
 
 def _same_device(a: Mx4State, b: Mx4State, names: str):
@@ -1167,14 +1173,18 @@ def qk_moe_route(logits: torch.Tensor, top_k: int, bias=None, score: int = SOFTM
         raise ValueError(f"top_k must be at least 1, got {top_k}")
     if ids is None:
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        ip = ids.data_ptr()
     else:
         _check_out(ids, (T, top_k), torch.int32, "ids")
+        ip = _ready(ids, dev, "ids")
     if weights is None:
         weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        wp = weights.data_ptr()
     else:
         _check_out(weights, (T, top_k), torch.float32, "weights")
+        wp = _ready(weights, dev, "weights")
     _call(dev, lib().qk_moe_route, lp, _DTYPE_CODE[logits.dtype], T, E, bp, int(score), int(groups), int(top_groups), top_k,
-          1 if renormalize else 0, float(scale), _ready(ids, dev, "ids"), _ready(weights, dev, "weights"))
+          1 if renormalize else 0, float(scale), ip, wp)
     return ids, weights
 
 
@@ -1217,6 +1227,9 @@ def qk_moe_plan_size(T: int, top_k: int, experts: int) -> int:
     return int(out.value)
 
 
+_moe_plan_bytes = functools.lru_cache(maxsize=256)(qk_moe_plan_size)
+
+
 class MoePlan:
     """The slots (token, position) of a routing sorted by expert: `first` (int32 [experts + 1]) and `slots` (int32
     [T * top_k]) are views of its one buffer."""
@@ -1240,7 +1253,7 @@ def qk_moe_plan(ids: torch.Tensor, experts: int, plan=None) -> MoePlan:
     of at least qk_moe_plan_size() bytes to write it to."""
     T, top_k = _slots(ids)
     dev, experts = ids.device, int(experts)
-    words = qk_moe_plan_size(T, top_k, experts) // 4
+    words = _moe_plan_bytes(T, top_k, experts) // 4
     if plan is None:
         plan = torch.empty(words, dtype=torch.int32, device=dev)
     elif plan.dtype is not torch.int32 or plan.numel() < words:
