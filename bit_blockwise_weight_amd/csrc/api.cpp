@@ -1273,7 +1273,9 @@ const char* qk_backend_info(void) {
         "W^T dequantized into LDS, dA/dB row-slice reductions; quantize_8bit: LDS bin table built per workgroup; "
         "int8_matmul: mfma 32x32x32 i8 256x256 tiles 8 waves, fp16 outlier mfma in the epilogue; "
         "gemv_int4: whole lines through wave-private LDS, mfma 16x16x32 f16 of exact code - zero; "
-        "moe: routing in the up kernel, up and down products of the listed experts, combine";
+        "moe: routing in the up kernel, up and down products of the listed experts, combine; "
+        "mx4: scaled mfma 16x16x128 of e2m1 codes through LDS rings, tiles to 256x256, scaled conversions in the decode product; "
+        "route: wave per token, choices in fp32 and fp64 where they are close; plan: counting sort by expert";
     return s.c_str();
 }
 

@@ -341,8 +341,8 @@ __device__ __forceinline__ void store_wave(const GemmArgs& a, const Tile& t, con
 // lines of the stage after next start on their way to the same place; two rows before the stage ends they meet again: the
 // next stage has landed, and the X lines of the stage after next follow.
 //
-// A stage's copies set out two stages before it (W: one and a half of them, X: one), or one stage earlier yet where LDS
-// holds a ring of three (kRing).
+// Copies of W set out a stage and a half before they are read, those of X one stage, in a ring of three stages (kRing) one
+// stage earlier.
 //
 // A workgroup makes one tile after the other (kTurns; a launch has as many as are on the CUs at a time): while a tile is
 // multiplied the slots of the next one's rows come from the plan, and its first copies are on their way while outputs are
