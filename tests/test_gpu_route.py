@@ -195,6 +195,18 @@ def test_backward_over_the_logits_themselves_and_wrong_ids():
     assert torch.equal(qk.qk_moe_route_backward(z, bad, dw, renormalize=False), qk.qk_moe_route_backward(z, a, b, renormalize=False))
 
 
+@pytest.mark.parametrize("T", [511, 512, 513, 1023, 1025, 4096, 4097, 8191, 8192, 8193, 16385, 32768, 32769, 49153, 100001])
+def test_plan_lengths(T):
+    """Slots of a workgroup's runs, whole and with one more or less."""
+    g = _gen(T)
+    ids = torch.randint(-1, 8, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    p = qk.qk_moe_plan(ids, 7)
+    flat = torch.where(ids.view(-1) < 0, torch.full_like(ids.view(-1), 7), ids.view(-1)).long()
+    n = torch.bincount(flat, minlength=8)
+    assert torch.equal(p.slots.long(), torch.sort(flat, stable=True)[1])
+    assert torch.equal(p.first.long(), torch.cumsum(n, 0) - n)
+
+
 @pytest.mark.parametrize("T,top_k,E", [(1, 1, 1), (1, 8, 64), (3, 2, 5), (40, 4, 512), (700, 3, 17), (5000, 8, 64), (2049, 1, 3)])
 def test_plan(T, top_k, E):
     g = _gen(T)
