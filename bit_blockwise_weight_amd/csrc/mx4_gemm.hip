@@ -840,7 +840,8 @@ hipError_t launch_dense(const GemmArgs& a, hipStream_t s) {
     const int64_t cus = device_cu_count();
     // Workgroups that split the inputs among their waves where tiles would leave half of the CUs without one, and up to 16
     // rows always: 16 x 4096 x 11008 6.6, tiles of 64 x 64 16; 64 x 4096 x 4096 7.5 and 8.7; 64 x 11008 x 4096 12.5 and 9.0.
-    if (a.M <= 16) return launch_few<kDense, 1, 2>(a, s);
+    // (A launch has fewer than 2^32 threads; tiles are made by as many workgroups as there is room for.)
+    if (a.M <= 16 && a.N <= (int64_t)1 << 28) return launch_few<kDense, 1, 2>(a, s);
     if (a.M <= 128 && grid_for<kDense>(a, 64, 64) <= cus / 2)
         return a.M <= 32 ? launch_few<kDense, 2, 2>(a, s) : launch_few<kDense, 4, 2>(a, s);
     // The largest tiles of which there is one for every CU: 4096 x 4096 x 4096 41, in tiles of 128 51; 2048 x 4096 x 4096 40 and
@@ -928,11 +929,17 @@ hipError_t launch_moe_down_mx4(const qk_mx4_state* h, const qk_mx4_state* down, 
     a.N = a.w_rows;
     const hipError_t e = launch_experts<kDown>(a, s);
     if (e != hipSuccess) return e;
-    const int64_t T = h->rows / top_k, threads = T * ((a.N + 3) / 4), grid = cdiv(threads, kCombineThreads);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    moe_combine_mx4_kernel<<<dim3((unsigned)grid), dim3(kCombineThreads), 0, s>>>(static_cast<const float*>(workspace), y,
-                                                                                y_dtype, T, top_k, a.N);
-    return hipGetLastError();
+    // pieces of fewer than 2^32 threads
+    const int64_t T = h->rows / top_k, quads = (a.N + 3) / 4, most = std::max<int64_t>(1, ((int64_t)1 << 30) / quads);
+    for (int64_t t = 0; t < T; t += most) {
+        const int64_t n = std::min(most, T - t);
+        moe_combine_mx4_kernel<<<dim3((unsigned)cdiv(n * quads, kCombineThreads)), dim3(kCombineThreads), 0, s>>>(
+            static_cast<const float*>(workspace) + t * top_k * a.N, static_cast<uint8_t*>(y) + t * a.N * (y_dtype == QK_F32 ? 4 : 2),
+            y_dtype, n, top_k, a.N);
+        const hipError_t c = hipGetLastError();
+        if (c != hipSuccess) return c;
+    }
+    return hipSuccess;
 }
 
 }  // namespace qk

@@ -223,10 +223,10 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(DequantArgs a)
     }
 }
 
-// Launches over rows in pieces of fewer than 2^31 runs: launch(first row, rows).
+// Launches over rows in pieces of at most 2^28 runs (a launch has fewer than 2^32 threads): launch(first row, rows).
 template <class Launch>
 hipError_t by_rows(int64_t rows, int64_t per_row, Launch&& launch) {
-    const int64_t most = std::max<int64_t>(1, ((int64_t)1 << 30) / per_row);
+    const int64_t most = std::max<int64_t>(1, ((int64_t)1 << 28) / per_row);
     for (int64_t r = 0; r < rows; r += most) {
         launch(r, std::min(most, rows - r));
         const hipError_t e = hipGetLastError();

@@ -241,6 +241,12 @@ struct MoeRouteArgs {
     int64_t T;
     int32_t dtype, E, score, groups, top_groups, top_k, renorm;
     float scale;
+
+    void move(int64_t t) {    // the tokens from t on
+        logits = static_cast<const uint8_t*>(logits) + t * E * (dtype == QK_F32 ? 4 : 2);
+        ids += t * top_k;
+        weights += t * top_k;
+    }
 };
 hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s);
 struct MoeRouteBackwardArgs {
@@ -251,6 +257,14 @@ struct MoeRouteBackwardArgs {
     int64_t T;
     int32_t dtype, E, score, top_k, renorm;
     float scale;
+
+    void move(int64_t t) {
+        const int64_t at = t * E * (dtype == QK_F32 ? 4 : 2);
+        logits = static_cast<const uint8_t*>(logits) + at;
+        dlogits = static_cast<uint8_t*>(dlogits) + at;
+        ids += t * top_k;
+        dweights += t * top_k;
+    }
 };
 hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs& a, hipStream_t s);
 // Plan of a routing: E + 1 first places, padded to a multiple of 4 numbers; the slots, padded alike; how many tiles there are,

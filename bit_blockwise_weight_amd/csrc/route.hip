@@ -646,26 +646,44 @@ __global__ __launch_bounds__(kBlock) void moe_plan_kernel(const int32_t* __restr
 
 unsigned token_grid(int64_t T) { return (unsigned)((T + kTokens - 1) / kTokens); }
 
-}  // namespace
-
-hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s) {
-    const dim3 grid(token_grid(a.T));
-    // log2 of the experts of a group; groups of other sizes are chosen in 64 bits
-    const int per = a.E / a.groups, shift = a.groups == 1 ? 0 : (per & (per - 1)) == 0 ? __builtin_ctz((unsigned)per) : -1;
-    if (a.E <= 64) moe_route_kernel<1><<<grid, kThreads, 0, s>>>(a, shift);
-    else if (a.E <= 128) moe_route_kernel<2><<<grid, kThreads, 0, s>>>(a, shift);
-    else if (a.E <= 256) moe_route_kernel<4><<<grid, kThreads, 0, s>>>(a, shift);
-    else moe_route_kernel<8><<<grid, kThreads, 0, s>>>(a, shift);
-    return hipGetLastError();
+// Launches over tokens in pieces (a launch has fewer than 2^32 threads): launch(arguments of the piece).
+template <class Args, class Launch>
+hipError_t by_tokens(const Args& a, Launch&& launch) {
+    constexpr int64_t kMost = (int64_t)1 << 24;
+    for (int64_t t = 0; t < a.T; t += kMost) {
+        Args p = a;
+        p.T = a.T - t < kMost ? a.T - t : kMost;
+        p.move(t);
+        launch(p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
-hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs& a, hipStream_t s) {
-    const dim3 grid(token_grid(a.T));
-    if (a.E <= 64) moe_route_backward_kernel<1><<<grid, kThreads, 0, s>>>(a);
-    else if (a.E <= 128) moe_route_backward_kernel<2><<<grid, kThreads, 0, s>>>(a);
-    else if (a.E <= 256) moe_route_backward_kernel<4><<<grid, kThreads, 0, s>>>(a);
-    else moe_route_backward_kernel<8><<<grid, kThreads, 0, s>>>(a);
-    return hipGetLastError();
+}  // namespace
+
+hipError_t launch_moe_route(const MoeRouteArgs& all, hipStream_t s) {
+    // log2 of the experts of a group; groups of other sizes are chosen in 64 bits
+    const int per = all.E / all.groups;
+    const int shift = all.groups == 1 ? 0 : (per & (per - 1)) == 0 ? __builtin_ctz((unsigned)per) : -1;
+    return by_tokens(all, [&](const MoeRouteArgs& a) {
+        const dim3 grid(token_grid(a.T));
+        if (a.E <= 64) moe_route_kernel<1><<<grid, kThreads, 0, s>>>(a, shift);
+        else if (a.E <= 128) moe_route_kernel<2><<<grid, kThreads, 0, s>>>(a, shift);
+        else if (a.E <= 256) moe_route_kernel<4><<<grid, kThreads, 0, s>>>(a, shift);
+        else moe_route_kernel<8><<<grid, kThreads, 0, s>>>(a, shift);
+    });
+}
+
+hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs& all, hipStream_t s) {
+    return by_tokens(all, [&](const MoeRouteBackwardArgs& a) {
+        const dim3 grid(token_grid(a.T));
+        if (a.E <= 64) moe_route_backward_kernel<1><<<grid, kThreads, 0, s>>>(a);
+        else if (a.E <= 128) moe_route_backward_kernel<2><<<grid, kThreads, 0, s>>>(a);
+        else if (a.E <= 256) moe_route_backward_kernel<4><<<grid, kThreads, 0, s>>>(a);
+        else moe_route_backward_kernel<8><<<grid, kThreads, 0, s>>>(a);
+    });
 }
 
 hipError_t launch_moe_plan(const int32_t* ids, int64_t slots, int32_t E, int32_t* plan, hipStream_t s) {

@@ -244,3 +244,15 @@ def test_stack_past_32_bits():
         assert float(h[0].abs().max()) == 0.0
         c = {"ids": torch.zeros((1, 1), dtype=torch.int32, device="cuda"), "x": (x[0][1:2], x[1][1:2]), "up": (tc, ts)}
         check(h[1:2], *_up_f64(c, 1, 1, 1, H, I), torch.bfloat16)
+
+
+def test_more_outputs_than_a_launch_has_threads_for():
+    T, I, H = (1 << 18) + 1, 32, 1 << 16
+    g = _gen(53)
+    h, down = make_mx4(g, T, I, 118, 126), make_mx4(g, H, I, 112, 120)
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    w = torch.rand((T, 1), generator=g, device="cuda")
+    y = qk.qk_moe_down_mx4(qk.qk_mx4_state_init(T, I, *h), qk.qk_mx4_state_init(H, I, *down), qk.qk_moe_plan(ids, 1), w)
+    for r in (slice(0, 3), slice((1 << 16) - 2, (1 << 16) + 2), slice(T - 2, T)):
+        c = {"ids": ids[r], "h": (h[0][r], h[1][r]), "down": down, "w": w[r]}
+        check(y[r], *_down_f64(c, r.stop - r.start, 1, 1, H, I), torch.bfloat16)

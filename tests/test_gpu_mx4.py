@@ -346,3 +346,22 @@ def test_offsets_past_32_bits():
     del got
     tail = qk.qk_mx4_dequantize(qk.qk_mx4_state_init(N, K, codes, scales))[-40:]
     assert torch.equal(tail, wv.bfloat16())
+
+
+def test_more_short_rows_than_a_launch_has_threads_for():
+    rows = (1 << 29) + 7
+    x = torch.ones((rows, 1), dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, (1 << 28) - 1, 1 << 28, 1 << 29, rows - 1]
+    for i, r in enumerate(at):
+        x[r] = -2.0 ** i
+    codes, scales = qk.qk_mx4_quantize(x)
+    st = qk.qk_mx4_state_init(rows, 1, codes, scales)
+    y = qk.qk_mx4_dequantize(st)
+    assert torch.equal(y, x)
+    del y
+    one = qk.quantize_mx4(torch.ones((1, 1), dtype=torch.bfloat16, device="cuda"))
+    got = qk.qk_gemm_mx4(one.state, st, torch.bfloat16)             # so many outputs of one row
+    assert torch.equal(got.view(-1), x.view(-1))
+    del got
+    got = qk.qk_gemm_mx4(st, one.state, torch.bfloat16)             # and so many rows
+    assert torch.equal(got.view(-1), x.view(-1))

@@ -261,3 +261,16 @@ def test_many_tokens():
     assert torch.equal(ids.long(), want[:, :2])
     ref = torch.softmax(top[:, :2].double(), 1)
     assert bool(((w.double() - ref).abs() <= ref * 2.0 ** -24 * 64).all())
+
+
+def test_most_tokens():
+    """2^26 tokens of one expert: more threads than a launch may have."""
+    T = 1 << 26
+    z = torch.zeros((T, 1), device="cuda")
+    z[-1], z[1 << 24], z[(1 << 24) - 1] = float("-inf"), 2.0, -3.0
+    ids, w = qk.qk_moe_route(z, 1, score=qk.SIGMOID, renormalize=False)
+    want = torch.sigmoid(z.double())
+    assert int(ids[-1]) == -1 and int(ids.sum()) == -1
+    assert bool(((w.double() - want).abs() <= 4 * 2.0 ** -24).all())
+    dz = qk.qk_moe_route_backward(z, ids, torch.ones_like(w), score=qk.SIGMOID, renormalize=False)
+    assert bool(((dz.double() - want * (1 - want)).abs() <= 4 * 2.0 ** -24).all())
