@@ -365,32 +365,31 @@ __device__ __forceinline__ bool choose_fast(const MoeRouteArgs& a, int64_t t, in
         }
         if (a.groups > 1) {
             uint32_t m1[V], m2[V];
-            float sum[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 m1[i] = ranked[i];
                 m2[i] = kNone;
             }
             join_groups<V>(m1, m2, 1 << group_shift);
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = float_of(m1[i]) + (m2[i] <= kNone ? 0.0f : float_of(m2[i]));
-            // group g in lane g; the best top_groups of them, and whether the next one is close to the last
-            uint32_t g = order_of(gather<V>(sum, lane << group_shift));
-            if (lane >= a.groups) g = 0;
-            uint64_t kept = 0;
-            uint32_t best = 0, last = 0;
-            for (int j = 0; j <= a.top_groups; ++j) {
-                best = wave_max(g);
-                if (best <= kNone) break;
-                if (j == a.top_groups) {
-                    const float v = float_of(best), w = float_of(last);
-                    if (!(w - v > 2.0f * (slack(v, sigmoid) + slack(w, sigmoid)))) return false;
-                    break;
-                }
-                last = best;
+            // Group g in lane g: its sum, and what 32 bits may have that off by.  The two ranks may cancel, their errors do not.
+            const uint32_t k1 = gather<V>(m1, lane << group_shift), k2 = gather<V>(m2, lane << group_shift);
+            const bool one = k2 <= kNone;
+            const float v1 = float_of(k1), v2 = one ? 0.0f : float_of(k2), sum = v1 + v2;
+            const float off = slack(v1, sigmoid) + (one ? 0.0f : slack(v2, sigmoid)) + 1.1920929e-7f * fabsf(sum);
+            uint32_t g = lane < a.groups && k1 > kNone ? order_of(sum) : 0u;
+            uint64_t kept = 0;                                      // the best top_groups
+            for (int j = 0; j < a.top_groups; ++j) {
+                const uint32_t best = wave_max(g);
+                if (best == 0) break;
                 const int at = (int)__builtin_ctzll(__ballot(g == best));
                 kept |= 1ull << at;
                 g = lane == at ? 0u : g;
+            }
+            // a clear gap between the least that one of them may be and the most that one of the others may be
+            const uint32_t most = wave_max(g ? order_of(sum + off) : 0u);
+            if (most) {
+                const float low = fmaxf(sum - off, -INFINITY);      // (of infinities: -inf)
+                if (!(~wave_max(kept >> lane & 1 ? ~order_of(low) : 0u) > most)) return false;
             }
 #pragma unroll
             for (int i = 0; i < V; ++i)

@@ -274,3 +274,21 @@ def test_most_tokens():
     assert bool(((w.double() - want).abs() <= 4 * 2.0 ** -24).all())
     dz = qk.qk_moe_route_backward(z, ids, torch.ones_like(w), score=qk.SIGMOID, renormalize=False)
     assert bool(((dz.double() - want * (1 - want)).abs() <= 4 * 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("score", [qk.SOFTMAX, qk.SIGMOID])
+@pytest.mark.parametrize("size", [32.0, 100.0, 1000.0, 1e30])
+@pytest.mark.parametrize("E,groups,top_groups", [(4, 2, 1), (16, 4, 2), (128, 8, 3)])
+def test_groups_of_biases_of_opposite_sign(score, size, E, groups, top_groups):
+    """The two best ranks of a group cancel: their sum is small, what 32 bits take from each of them is not.  Sums of groups a
+    few 2^-18 apart."""
+    g = _gen(int(size) % 1009 + E)
+    per = E // groups
+    z = torch.randn((1500, 1, per), generator=g, device="cuda") * 0.5
+    z = (z + torch.randn((1500, groups, per), generator=g, device="cuda") * 2.0 ** -18).reshape(1500, E)
+    b = torch.full((E,), -2.0 * size, device="cuda")
+    b[::per], b[1::per] = size, -size
+    _check(z, 2, score=score, bias=b, groups=groups, top_groups=top_groups)
+    if (E, size) == (4, 100.0) and score == qk.SIGMOID:           # sums 1.00000610 and 1.00000457
+        ids, _ = qk.qk_moe_route(torch.tensor([[1.22e-5, 1.22e-5, 1.83e-5, 0.0]], device="cuda"), 1, b, score, groups=2)
+        assert ids.tolist() == [[0]]
