@@ -372,9 +372,12 @@ __device__ __forceinline__ bool choose_fast(const MoeRouteArgs& a, int64_t t, in
             }
             join_groups<V>(m1, m2, 1 << group_shift);
             // Group g in lane g: its sum, and what 32 bits may have that off by.  The two ranks may cancel, their errors do not.
+            // A sum past the largest numbers counts as one of them, from which its error reaches to an infinity: two such are
+            // never clear of each other.
             const uint32_t k1 = gather<V>(m1, lane << group_shift), k2 = gather<V>(m2, lane << group_shift);
             const bool one = k2 <= kNone;
-            const float v1 = float_of(k1), v2 = one ? 0.0f : float_of(k2), sum = v1 + v2;
+            const float v1 = float_of(k1), v2 = one ? 0.0f : float_of(k2);
+            const float sum = fminf(fmaxf(v1 + v2, -3.402823466e38f), 3.402823466e38f);
             const float off = slack(v1, sigmoid) + (one ? 0.0f : slack(v2, sigmoid)) + 1.1920929e-7f * fabsf(sum);
             uint32_t g = lane < a.groups && k1 > kNone ? order_of(sum) : 0u;
             uint64_t kept = 0;                                      // the best top_groups
@@ -388,8 +391,7 @@ __device__ __forceinline__ bool choose_fast(const MoeRouteArgs& a, int64_t t, in
             // a clear gap between the least that one of them may be and the most that one of the others may be
             const uint32_t most = wave_max(g ? order_of(sum + off) : 0u);
             if (most) {
-                const float low = fmaxf(sum - off, -INFINITY);      // (of infinities: -inf)
-                if (!(~wave_max(kept >> lane & 1 ? ~order_of(low) : 0u) > most)) return false;
+                if (~wave_max(kept >> lane & 1 ? ~order_of(sum - off) : 0u) <= most) return false;
             }
 #pragma unroll
             for (int i = 0; i < V; ++i)

@@ -292,3 +292,23 @@ def test_groups_of_biases_of_opposite_sign(score, size, E, groups, top_groups):
     if (E, size) == (4, 100.0) and score == qk.SIGMOID:           # sums 1.00000610 and 1.00000457
         ids, _ = qk.qk_moe_route(torch.tensor([[1.22e-5, 1.22e-5, 1.83e-5, 0.0]], device="cuda"), 1, b, score, groups=2)
         assert ids.tolist() == [[0]]
+
+
+@pytest.mark.parametrize("score", [qk.SOFTMAX, qk.SIGMOID])
+@pytest.mark.parametrize("E,groups,top_groups,top_k", [(8, 2, 2, 8), (8, 4, 2, 4), (64, 8, 3, 20), (12, 4, 3, 9), (16, 16, 5, 5)])
+def test_biases_of_the_largest_size(score, E, groups, top_groups, top_k):
+    """A bias of the lowest finite value masks nothing: its experts, and groups of them whose sums pass fp32, come last.  The
+    largest value ranks first."""
+    g = _gen(E + groups)
+    z = torch.randn((40, E), generator=g, device="cuda")
+    z[5, E // 2:] = float("-inf")
+    per, lowest = E // groups, torch.finfo(torch.float32).min
+    one = torch.randn(E, generator=g, device="cuda") * 0.1
+    one[per:] = lowest                                           # all groups but the first
+    every = torch.full((E,), lowest, device="cuda")
+    last = torch.randn(E, generator=g, device="cuda") * 0.1
+    last[-per:] = -lowest
+    mixed = one.clone()
+    mixed[::per], mixed[-per:] = -lowest, float("-inf")
+    for b in (one, every, -every, last, mixed):
+        _check(z, top_k, score=score, bias=b, groups=groups, top_groups=top_groups)
