@@ -258,12 +258,13 @@ __device__ __forceinline__ void store_row(void* y, int64_t at, const float (&v)[
 }
 
 // g / (1 + exp(-g)) by e = exp(-|g|) <= 1.  For outputs of 16 bits: e to |g| 2^-24 of itself, the rounding of its exponent, 2^-17
-// where it matters.  For fp32 to a few of its steps: the exponent of 2 in two parts, a reciprocal improved once.  (The
-// library's exponential and a full division took a third of a tile's time.)
+// where it matters.  For fp32 to a few of its steps: the exponent of 2 in two parts, a reciprocal improved once; e is 0 from
+// |g| = 104 on, and the parts of a larger one would pass the largest number.  (The library's exponential and a full division
+// took a third of a tile's time.)
 template <int DT>
 __device__ __forceinline__ float silu(float g) {
     const float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
-    const float a = -fabsf(g), t = a * kLog2e, p = __builtin_amdgcn_exp2f(t);
+    const float a = DT == QK_F32 ? fmaxf(-fabsf(g), -256.0f) : -fabsf(g), t = a * kLog2e, p = __builtin_amdgcn_exp2f(t);
     if constexpr (DT != QK_F32) return g * (g >= 0.0f ? 1.0f : p) * __builtin_amdgcn_rcpf(1.0f + p);
     const float low = fmaf(a, kLog2eLow, fmaf(a, kLog2e, -t));
     const float e = fmaf(p, low * kLn2, p), d = 1.0f + e;

@@ -256,3 +256,35 @@ def test_more_outputs_than_a_launch_has_threads_for():
     for r in (slice(0, 3), slice((1 << 16) - 2, (1 << 16) + 2), slice(T - 2, T)):
         c = {"ids": ids[r], "h": (h[0][r], h[1][r]), "down": down, "w": w[r]}
         check(y[r], *_down_f64(c, r.stop - r.start, 1, 1, H, I), torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 3, 60, 300])
+def test_gates_of_every_size(dtype, T):
+    """SwiGLU of gates to the largest numbers and past them: each gate is one weight times 1."""
+    I, H = 32, 32
+    scales = [253, 252, 251, 254, 250, 134, 131, 129, 128, 127, 124, 100, 20, 1]
+    codes = [5, 7, 7, 7, 4, 7, 7, 5, 7, 2, 1, 3, 6, 2]               # 2.55e38 twice, 1.28e38, infinite, 2.1e37, 768, 96, 12, ...
+    up = torch.zeros((2 * I, 16), dtype=torch.uint8, device="cuda")
+    us = torch.full((2 * I, 4), 127, dtype=torch.uint8, device="cuda")
+    for i in range(I):
+        up[i, 0] = codes[i // 2 % 14] | 8 * (i % 2)
+        us[i, 0] = scales[i // 2 % 14]
+        up[I + i, 0], us[I + i, 0] = 2, 124                         # the up product: 1/8
+    x = torch.zeros((T, 16), dtype=torch.uint8, device="cuda")
+    x[:, 0] = 2
+    xs = torch.full((T, 4), 127, dtype=torch.uint8, device="cuda")
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    h = qk.qk_moe_up_mx4(qk.qk_mx4_state_init(T, H, x, xs), qk.qk_mx4_state_init(2 * I, H, up, us), qk.qk_moe_plan(ids, 1), DT[dtype])
+    gate = values(up[:I], us[:I], H)[:, 0]
+    gate = torch.where(gate.abs() >= 2.0 ** 128, gate.sign() * float("inf"), gate)
+    # x / (1 + exp(-x)) but for -inf, which has no value in fp32
+    want = torch.nn.functional.silu(gate) * 0.125
+    there = gate != float("-inf")
+    got, want = h[:, there].double(), want[there].expand(T, -1)
+    assert torch.equal(torch.isinf(got), torch.isinf(want)) and not bool(torch.isnan(got).any())
+    fin = torch.isfinite(want)
+    # silu in fp32: the exponential to 2 steps (none below 2^-126), a sum, a quotient, a product; in 16 bits the exponential's
+    # rounded exponent, |g| of it
+    size = want.abs() * (8 + (0 if dtype == "f32" else 2 * 96)) * 2.0 ** -24 + 96 * 0.125 * 2.0 ** -126
+    check(h[:, there][fin], want[fin], size[fin], DT[dtype])
