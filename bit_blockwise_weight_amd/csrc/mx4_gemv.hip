@@ -30,24 +30,77 @@ struct GemvArgs {
 
 constexpr int groups_for(int f) { return f == kMx4F16 ? 4 : 1; }
 
+// First row of workgroup b and the row behind its last one.
+template <int RT>
+__device__ __forceinline__ int step_of(const GemvArgs& a) { return (16 * RT * 8) >> a.kwl; }
+template <int RT>
+__device__ __forceinline__ void rows_of(const GemvArgs& a, int b, int64_t& row0, int64_t& row1) {
+    row0 = (int64_t)step_of<RT>(a) * ((int64_t)b * a.share + (b < a.more ? b : a.more));
+    row1 = row0 + (int64_t)step_of<RT>(a) * (a.share + (b < a.more));
+    row1 = row1 < a.N ? row1 : a.N;
+}
+
+// Weights of the two largest scales may pass bf16, though their products with small activations are numbers: an infinity among
+// them, or a NaN where it meets a 0, stays in the sum.  The outputs of row group q of an item for which that may be so, no
+// numbers and with such a scale in their row, are made again, each group's scale applied to its sum: one after the other, the
+// lanes taking groups.  (Quantization gives no scale over 252.  Looking for them in the loop costs every call 1 to 3 %; so would
+// the registers of arguments kept until here, they are read anew.)
+template <int RT, int MI, class Tiles>
+__device__ __forceinline__ void make_again(int item, int q, const float* put) {
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    auto args = (const __attribute__((address_space(4))) GemvArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(args));
+    const GemvArgs& a = *(const GemvArgs*)args;
+    const int lane = threadIdx.x & 63;
+    int64_t row0, row1;
+    rows_of<RT>(a, (int)blockIdx.x, row0, row1);
+#pragma unroll 1
+    for (int t = 0; t < RT * MI; ++t) {
+        const int r = t / MI, o = 64 * (t % MI) + lane;
+        const int64_t first = row0 + item * step_of<RT>(a) + q * (16 * RT) + 16 * r;
+        uint64_t bad = __ballot(!(fabsf(Tiles::sum(put, a.kwl, q, r, o)) < INFINITY));
+        for (; bad; bad &= bad - 1) {
+            const int l = (int)__builtin_ctzll(bad), m = Tiles::act_of(o - lane + l);
+            const int64_t row = first + (l & 15);
+            if (m >= a.M || row >= row1) continue;
+            const uint8_t* scales = a.w.scales + row * a.w.scale_stride;
+            bool large = false;
+            for (int g = lane; g < a.w.G; g += 64) large |= (uint32_t)scales[g] - 253u < 2u;
+            if (!__ballot(large)) continue;
+            float sum = 0.0f;
+            for (int g = lane; g < a.w.G; g += 64) {
+                const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.w.codes + row * a.w.stride) + 4 * g;
+                float part = 0.0f;
+                for (int k = 0; k < 32 && 32 * g + k < a.K; ++k) {
+                    const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[k / 8] >> (4 * (k % 8)), 1.0f, 0);
+                    part = fmaf(bf16_bits_to_float(a.x[(int64_t)m * a.K + 32 * g + k]), v[0], part);
+                }
+                const uint32_t e = scales[g];
+                sum = fmaf(part, as_float(e == 0 ? 0x00400000u : e == 255u ? 0x7FC00000u : e << 23), sum);
+            }
+#pragma unroll 1
+            for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+            if (lane == 0) a.y[m * a.N + row] = float_to_bits16(sum, false);
+        }
+    }
+}
+
 template <int F, int RT, int MI, bool kResident>
 __global__ __launch_bounds__(kThreads, 4) void mx4_gemv_kernel(GemvArgs a) {
     extern __shared__ __align__(16) uint8_t lds[];
     typedef RowTiles<F, groups_for(F), RT, MI, kResident, false> Tiles;
-    const int b = (int)blockIdx.x;
     Rows<RT> p;
     p.kwl = a.kwl;
     p.group_step = 16 * RT;
-    p.step = (16 * RT * 8) >> a.kwl;
-    const int64_t row0 = (int64_t)p.step * ((int64_t)b * a.share + (b < a.more ? b : a.more));
-    const int items = a.share + (b < a.more);
-    const int64_t row1 = row0 + (int64_t)p.step * items;
+    p.step = step_of<RT>(a);
+    int64_t row0, row1;
+    rows_of<RT>(a, (int)blockIdx.x, row0, row1);
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         p.base[r] = row0;
         p.off[r] = 16 * r;
     }
-    p.count = (int32_t)((row1 < a.N ? row1 : a.N) - row0);
+    p.count = (int32_t)(row1 - row0);
     p.x = a.x;
     p.xrow = nullptr;
     p.K = a.K;
@@ -55,7 +108,9 @@ __global__ __launch_bounds__(kThreads, 4) void mx4_gemv_kernel(GemvArgs a) {
     p.x_rows = a.M;
     p.x_aligned = a.x_aligned;
     p.M = a.M;
+    const int items = a.share + ((int)blockIdx.x < a.more);
     Tiles::run(a.w, p, 0, items, lds, [&](int item, int q, const float* put) {
+        bool all = true;                                            // numbers
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -63,8 +118,12 @@ __global__ __launch_bounds__(kThreads, 4) void mx4_gemv_kernel(GemvArgs a) {
                 const int o = 64 * i + (threadIdx.x & 63), m = Tiles::act_of(o);
                 const int j = item * p.step + q * (16 * RT) + 16 * r + (o & 15);
                 const float v = Tiles::sum(put, a.kwl, q, r, o);
+                all &= fabsf(v) < INFINITY;
                 if (m < a.M && j < p.count) a.y[m * a.N + row0 + j] = float_to_bits16(v, F == kMx4F16);
             }
+        if constexpr (F == kMx4Bf16) {
+            if (__builtin_expect(__ballot(!all) != 0, 0)) make_again<RT, MI, Tiles>(item, q, put);
+        }
     });
 }
 

@@ -752,7 +752,7 @@ qk_status qk_mx4_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t 
 
 /*
  * qk_mx4_dequantize — device.  The values of a microscaled matrix as fp32, bf16 or fp16 (round to nearest even: exact
- *   in fp32 and, but for overflow and values under 2^-133, in bf16).
+ *   but for overflow in fp32 and, but for that and values under 2^-133, in bf16).
  *   out: device, [rows, cols] of out_dtype, aligned to its elements, written.
  *   Errors: QK_ERR_BAD_STATE, QK_ERR_INVALID_ARG, QK_ERR_NO_DEVICE, QK_ERR_HIP.
  */
@@ -775,7 +775,8 @@ qk_status qk_gemm_mx4(const qk_mx4_state* x, const qk_mx4_state* w, void* y, int
  *     y[m, :] = x[m, :] · W^T,  m < M.
  *   Activations and weights enter the products exactly (but weights under 2^-126, which may count as zero), sums are
  *   fp32, y is rounded once.  The same inputs give the same bits on every call.  An infinity or a NaN in x spoils its
- *   own row of y only.
+ *   own row of y only.  (bf16: outputs that meet weights of scale bytes 253 and 254, which qk_mx4_quantize does not give, may
+ *   take much longer.)
  *   x:  device, [M, K] of dtype (QK_BF16 or QK_F16) row-major, 2-byte aligned (4-byte alignment and K % 8 == 0 load
  *       fastest).   M: 1..16.
  *   st: host pointer to a valid descriptor of W [N, K], N at most 2^28.

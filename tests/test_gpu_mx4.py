@@ -365,3 +365,38 @@ def test_more_short_rows_than_a_launch_has_threads_for():
     del got
     got = qk.qk_gemm_mx4(st, one.state, torch.bfloat16)             # and so many rows
     assert torch.equal(got.view(-1), x.view(-1))
+
+
+@pytest.mark.parametrize("M", [1, 3, 6, 16])
+@pytest.mark.parametrize("N,K", [(64, 512), (33, 100), (300, 1001), (48, 16384), (70000, 300)])
+def test_gemv_largest_scales(M, N, K):
+    """Weights of the two largest scales pass bf16 (and fp32) by themselves; their products with small activations do not.
+    What lies past a row's end, and weights of 0, meet them too."""
+    dt = torch.bfloat16
+    g = _gen(M + N + K)
+    wc, ws = make_mx4(g, N, K, 115, 130)
+    groups = -(-K // 32)
+    big = torch.rand((N, groups), generator=g, device="cuda") < 0.2
+    ws[:, :groups] = torch.where(big, torch.randint(252, 255, (N, groups), generator=g, device="cuda", dtype=torch.uint8), ws[:, :groups])
+    ws[::3, groups - 1] = 254                                    # the last group, partial in most
+    ws[4], wc[5, :16], ws[5, 0] = 254, 0, 253                    # (row 5: weights of 0)
+    ws[5, 1:groups] = 120
+    x = (torch.randn((M, K), generator=g, device="cuda") * 2.0 ** -20).to(dt)
+    x[:, ::7] = 0
+    if M > 1:
+        x[1] = 0
+    got = qk.qk_gemv_mx4(x, qk.qk_mx4_state_init(N, K, wc, ws))
+    wv = values(wc, ws, K)
+    bound = product_bound(x.double(), wv, K)
+    check(got, x.double() @ wv.t(), bound, dt)
+    if M > 1:
+        assert float(got[1].abs().max()) == 0.0
+    if M > 1:                                                    # a row's bits do not depend on the others
+        other = x.clone()
+        other[0] = float("nan")
+        assert torch.equal(qk.qk_gemv_mx4(other, qk.qk_mx4_state_init(N, K, wc, ws))[1:], got[1:])
+    ws[7, 0] = 255                                               # beside a NaN scale, too
+    got = qk.qk_gemv_mx4(x, qk.qk_mx4_state_init(N, K, wc, ws))
+    keep = torch.arange(N, device="cuda") != 7
+    assert bool(torch.isnan(got[:, 7]).all())
+    check(got[:, keep], (x.double() @ wv.t())[:, keep], bound[:, keep], dt)
