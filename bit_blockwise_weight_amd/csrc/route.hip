@@ -483,9 +483,12 @@ __global__ __launch_bounds__(kThreads) void moe_route_backward_kernel(MoeRouteBa
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = 0.0f;
     if (a.renorm) {
-        const float p = share_of(z, sigmoid), mean = wave_sum(d * p);
-        // softmax: p (d - mean); sigmoid: (d - mean) / total * s (1 - s) = (d - mean) p (1 - s)
-        own = (d - mean) * p * (sigmoid ? sigmoid_of(-z) : 1.0f);
+        // softmax: p (d - mean); sigmoid: (d - mean) / total * s (1 - s) = (d - mean) p (1 - s).  Both relative to the d of the
+        // largest p: of one near 1 only what the others have is left, and d - mean would be the rounding of d.
+        const float p = share_of(z, sigmoid);
+        const int most = (int)__builtin_ctzll(__ballot(order_of(z) == wave_max(order_of(z))));
+        const float rel = d - as_float((uint32_t)__builtin_amdgcn_readlane((int)as_uint(d), most));
+        own = (rel - wave_sum(rel * p)) * p * (sigmoid ? sigmoid_of(-z) : 1.0f);
     } else if (sigmoid) {
         own = z == -INFINITY ? 0.0f : d * sigmoid_of(z) * sigmoid_of(-z);
     } else {
@@ -508,8 +511,23 @@ __global__ __launch_bounds__(kThreads) void moe_route_backward_kernel(MoeRouteBa
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) s[i] *= inv;
-        own = z == -INFINITY ? 0.0f : d * expf(z - top) * inv;
+        const float p = z == -INFINITY ? 0.0f : expf(z - top) * inv;
+        own = d * p;
         all = -wave_sum(own);
+        // p (d - sum d p) of one near 1 would be the rounding of d, too: p (d (1 - p) - the others' sum), 1 - p from their s
+        const uint64_t near_one = __ballot(p > 0.5f);
+        if (near_one) {
+            const int at = (int)__builtin_ctzll(near_one), e = __builtin_amdgcn_readlane(id, at);
+            float rest = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[i] = 64 * i + lane == e ? 0.0f : s[i];
+                rest += s[i];
+            }
+            rest = wave_sum(rest);
+            const float others = wave_sum(lane == at ? 0.0f : own);
+            own = lane == at ? p * (d * rest - others) : own;
+        }
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) dz[64 * i + lane] = 0.0f;

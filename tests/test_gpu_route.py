@@ -312,3 +312,48 @@ def test_biases_of_the_largest_size(score, E, groups, top_groups, top_k):
     mixed[::per], mixed[-per:] = -lowest, float("-inf")
     for b in (one, every, -every, last, mixed):
         _check(z, top_k, score=score, bias=b, groups=groups, top_groups=top_groups)
+
+
+@pytest.mark.parametrize("score", [qk.SOFTMAX, qk.SIGMOID])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("E,top_k", [(5, 5), (64, 8), (300, 8)])
+@pytest.mark.parametrize("gap", [4.0, 12.0, 30.0])
+def test_backward_where_one_expert_has_nearly_all(score, renormalize, E, top_k, gap):
+    """The largest expert's gradient is what the others' small shares leave of its own: it keeps its digits."""
+    g = _gen(E + int(gap))
+    T = 40
+    z = -gap + torch.randint(0, 4, (T, E), generator=g, device="cuda").float() * 0.25
+    top = torch.randint(0, E, (T, 1), generator=g, device="cuda")
+    z.scatter_(1, top, gap)
+    ids, _ = qk.qk_moe_route(z, top_k, score=score, renormalize=renormalize)
+    assert torch.equal(ids[:, :1].long(), top)
+    # nothing cancels but the largest one's share against the whole: the others' d are on the other side of its own
+    dw = -1.0 - torch.rand((T, top_k), generator=g, device="cuda")
+    dw[:, 0] = 1.0
+    zz = z.double().cpu().requires_grad_(True)
+    _weights_f64(zz, ids.cpu(), score == qk.SIGMOID, renormalize, 1.0).backward(dw.double().cpu())
+    got = qk.qk_moe_route_backward(z, ids, dw, score, renormalize).double().cpu()
+    want = zz.grad
+    if not renormalize and score == qk.SOFTMAX:
+        # in 64 bits, too, 1 - s cancels: from the others' shares instead
+        s = torch.softmax(z.double().cpu(), 1)
+        d = torch.zeros_like(s).scatter(1, ids.cpu().long(), dw.double().cpu())
+        t = top.cpu()
+        others = s.scatter(1, t, 0.0)
+        want = s * (d - (s * d).sum(1, keepdim=True))
+        want.scatter_(1, t, s.gather(1, t) * (others.sum(1, keepdim=True) - (others * d).sum(1, keepdim=True)))
+    elif not renormalize:
+        i = ids.cpu().long()
+        z8 = z.double().cpu().gather(1, i)
+        want = torch.zeros_like(want).scatter(1, i, dw.double().cpu() * torch.sigmoid(z8) * torch.sigmoid(-z8))
+    else:
+        s = torch.sigmoid(z.double().cpu()) if score == qk.SIGMOID else torch.softmax(z.double().cpu(), 1)
+        i = ids.cpu().long()
+        c = s.gather(1, i)
+        p, d = c / c.sum(1, keepdim=True), dw.double().cpu() - 1.0
+        own = p * (d - (p * d).sum(1, keepdim=True)) * (torch.sigmoid(-z.double().cpu()).gather(1, i) if score == qk.SIGMOID else 1.0)
+        want = torch.zeros_like(s).scatter(1, i, own)
+    # half steps of fp32: an exponential 4, sums of shares 9 + 6, the quotient and the products 6, sums of the chosen 6, the
+    # others' sum 9, the last difference 1
+    tol = want.abs() * 41 * 2.0 ** -24
+    assert bool(((got - want).abs() <= tol).all()), float(((got - want).abs() / want.abs().clamp(min=1e-300)).max() * 2 ** 24)
