@@ -204,7 +204,8 @@ __device__ __forceinline__ floatx4_t mfma(v4i_t w, int ws, v4i_t x, int xs, floa
 // then moves sums about between the instructions.  What reads the sums has to wait for the last instruction by itself
 // (settle).  A vector instruction that writes an operand has to be two instructions away, which the compiler does not see to
 // here: operands are whole dwords as they come from LDS, whose waits the compiler sets for any reader (of a 16-bit read it
-// clears the upper half first; two idle cycles before every product would cost 5%).
+// clears the upper half first; two idle cycles before every product would cost 5%).  That nothing stands too close in the code
+// that comes of it is checked in the built library (tests/test_mfma_operands.py).
 template <int S>
 __device__ __forceinline__ void mfma_in_place(floatx4_t& c, v4i_t w, int ws, v4i_t x, int xs) {
 #define QK_MFMA(SEL, SEL_HI)                                                                                                 \
@@ -586,16 +587,18 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
             for (int i = 0; i < 2; ++i) read_x(x0, 0, i);
 #pragma unroll
             for (int k = 0; k < RT + MT; ++k) read_scale(0, 0, k);
-            // (an odd number of stages is one more of zeros: a way out between the two costs the compiler the registers)
+            // (an odd number of stages is one more of zeros: a way out between the two costs the compiler the registers.  A way
+            // past the loop would have it move sums to where the zeros of that way are, before they have settled.)
             const std::integral_constant<int, 0> even;
             const std::integral_constant<int, 1> odd;
+            int st = 0;
             if constexpr (kRing == 2) {
-                for (int st = 0; st < nst; st += 2) {
+                do {
                     stage(even, x0, w0, x1, w1, x1, st);
                     stage(odd, x1, w1, x0, w0, x0, st + 1);
-                }
+                } while ((st += 2) < nst);
             } else {
-                for (int st = 0; st < nst; st += 6) {
+                do {
                     stage(even, x0, w0, x1, w1, x2, st);
                     stage(odd, x1, w1, x2, w2, x0, st + 1);
                     if (st + 2 < nst) {
@@ -606,7 +609,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tile_kernel(Ge
                         stage(even, x1, w1, x2, w2, x0, st + 4);
                         stage(odd, x2, w2, x0, w0, x1, st + 5);
                     }
-                }
+                } while ((st += 6) < nst);
             }
             __builtin_amdgcn_s_waitcnt(0);                            // nothing on its way to LDS any more
             settle<MT, RT>(acc);
