@@ -1156,7 +1156,8 @@ def qk_gemv_mx4(x: torch.Tensor, state: Mx4State, y=None) -> torch.Tensor:
 def qk_moe_route(logits: torch.Tensor, top_k: int, bias=None, score: int = SOFTMAX, groups: int = 1, top_groups: int = 1,
                  renormalize: bool = True, scale: float = 1.0, ids=None, weights=None):
     """(ids int32 [T, top_k], weights fp32 [T, top_k]) of the router's logits [..., E]: the experts of each token by softmax
-    or sigmoid scores, ranked with a bias (fp32 [E]) where one is given, in the best top_groups of `groups` groups."""
+    or sigmoid scores, ranked with a bias (fp32 [E]) where one is given, in the best top_groups of `groups` groups.  Like
+    every call here it records nothing for autograd: the logits' gradient is qk_moe_route_backward of the weights'."""
     if logits.dtype not in _DTYPE_CODE:
         raise ValueError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
     if logits.dim() == 0:
@@ -1232,11 +1233,20 @@ _moe_plan_bytes = functools.lru_cache(maxsize=256)(qk_moe_plan_size)
 
 class MoePlan:
     """The slots (token, position) of a routing sorted by expert: `first` (int32 [experts + 1]) and `slots` (int32
-    [T * top_k]) are views of its one buffer."""
+    [T * top_k]) are views of its one buffer, which qk_moe_plan has written for the same T, top_k and experts.  Writing
+    another plan to the buffer ends this one."""
 
     def __init__(self, data: torch.Tensor, T: int, top_k: int, experts: int):
+        T, top_k, experts = int(T), int(top_k), int(experts)
+        words = _moe_plan_bytes(T, top_k, experts) // 4
+        if data.dtype is not torch.int32 or data.numel() < words:
+            raise ValueError(f"plan must be int32 with at least {words} elements, got {data.dtype} {tuple(data.shape)}")
+        self._set(data, T, top_k, experts)
+
+    def _set(self, data, T, top_k, experts):
         self.data, self.T, self.top_k, self.experts = data, T, top_k, experts
         self._device = data.device
+        return self
 
     @property
     def first(self):
@@ -1253,13 +1263,13 @@ def qk_moe_plan(ids: torch.Tensor, experts: int, plan=None) -> MoePlan:
     of at least qk_moe_plan_size() bytes to write it to."""
     T, top_k = _slots(ids)
     dev, experts = ids.device, int(experts)
-    words = _moe_plan_bytes(T, top_k, experts) // 4
     if plan is None:
-        plan = torch.empty(words, dtype=torch.int32, device=dev)
-    elif plan.dtype is not torch.int32 or plan.numel() < words:
-        raise ValueError(f"plan must be int32 with at least {words} elements, got {plan.dtype} {tuple(plan.shape)}")
+        plan = torch.empty(_moe_plan_bytes(T, top_k, experts) // 4, dtype=torch.int32, device=dev)
+        out = MoePlan.__new__(MoePlan)._set(plan, T, top_k, experts)
+    else:
+        out = MoePlan(plan, T, top_k, experts)
     _call(dev, lib().qk_moe_plan, _ready(ids, dev, "ids"), T, top_k, experts, _ready(plan, dev, "plan"))
-    return MoePlan(plan, T, top_k, experts)
+    return out
 
 
 def qk_moe_up_mx4(x: Mx4State, gate_up: Mx4State, plan: MoePlan, dtype=torch.bfloat16, h=None) -> torch.Tensor:

@@ -232,3 +232,14 @@ def test_wrappers_check_shapes_and_devices():
     assert qk.qk_moe_plan_size(5, 8, 64) >= 4 * (68 + 40)
     with pytest.raises(qk.QKError):
         qk.qk_moe_plan_size(5, 8, 513)
+
+
+def test_a_plan_has_a_buffer_that_holds_it():
+    words = qk.qk_moe_plan_size(5, 8, 64) // 4
+    p = qk.MoePlan(torch.zeros(words, dtype=torch.int32), 5, 8, 64)
+    assert p.first.shape == (65,) and p.slots.shape == (40,)
+    for bad in (torch.zeros(words - 1, dtype=torch.int32), torch.zeros(words, dtype=torch.int64), torch.zeros(words)):
+        with pytest.raises(ValueError, match="plan must be int32"):
+            qk.MoePlan(bad, 5, 8, 64)
+    with pytest.raises(qk.QKError):
+        qk.MoePlan(torch.zeros(words, dtype=torch.int32), 5, 33, 64)
