@@ -26,7 +26,6 @@ struct View {
     int32_t cols;
     int32_t code_stride;
     int32_t scale_stride;
-    int32_t groups;           // of a row
 };
 
 inline View view(const qk_mx4_state* st) {
@@ -37,7 +36,6 @@ inline View view(const qk_mx4_state* st) {
     v.cols = (int32_t)st->cols;
     v.code_stride = (int32_t)st->code_stride;
     v.scale_stride = (int32_t)st->scale_stride;
-    v.groups = (int32_t)((st->cols + kGroup - 1) / kGroup);
     return v;
 }
 
