@@ -797,7 +797,7 @@ enum { QK_SOFTMAX = 0, QK_SIGMOID = 1 };
  *     ids  = the top_k experts of G_t by rank, largest first
  *     w    = scale * s,  or with renormalize != 0  scale * s / (the sum of s over the token's ids)
  *   Equal ranks, and groups of equal sums, go to the lower index.  Which of two is larger is decided in binary64: the
- *   result does not depend on the rounding of s.  The bias only ranks.
+ *   result does not depend on the rounding of s.  The bias only ranks.  Weights are made in fp32, a few of its steps off.
  *   A logit of -inf (a NaN counts as that, +inf as the largest finite value) masks an expert: it is never chosen and has no
  *   part in the softmax; so does a bias of -inf or NaN but for the softmax.  A group without experts left is not taken.  Where
  *   fewer than top_k experts are left, the remaining ids are -1, their weights 0.

@@ -288,3 +288,18 @@ def test_gates_of_every_size(dtype, T):
     # rounded exponent, |g| of it
     size = want.abs() * (8 + (0 if dtype == "f32" else 2 * 96)) * 2.0 ** -24 + 96 * 0.125 * 2.0 ** -126
     check(h[:, there][fin], want[fin], size[fin], DT[dtype])
+
+
+@pytest.mark.parametrize("T,top_k,E,H,I", [(1, 2, 3, 40, 4099), (20, 2, 4, 130, 3000), (500, 2, 2, 200, 1000), (900, 4, 8, 300, 2050),
+                                           (4000, 1, 2, 2100, 600)])
+def test_down_of_whole_numbers_is_exact(T, top_k, E, H, I):
+    """Sums below 2^24 units: nothing may be lost, however small beside the rest."""
+    g = _gen(T + I)
+    c = {"ids": _ids(g, T, top_k, E, True), "h": make_mx4(g, T * top_k, I, 127, 128), "down": make_mx4(g, E * H, I, 126, 127)}
+    c["w"] = torch.randint(1, 5, (T, top_k), generator=g, device="cuda").float()
+    y = qk.qk_moe_down_mx4(qk.qk_mx4_state_init(T * top_k, I, *c["h"]), qk.qk_mx4_state_init(E * H, I, *c["down"]),
+                           qk.qk_moe_plan(c["ids"], E), c["w"], torch.float32)
+    want, bound = _down_f64(c, T, top_k, E, H, I)
+    # multiples of 1/8; the bound holds the sums of absolute values, 2 I 2^-24 of them and more
+    assert float(bound.max()) * 2 ** 24 / (2 * I) * 8 < 2 ** 24
+    assert torch.equal(y.double(), want)

@@ -400,3 +400,45 @@ def test_gemv_largest_scales(M, N, K):
     keep = torch.arange(N, device="cuda") != 7
     assert bool(torch.isnan(got[:, 7]).all())
     check(got[:, keep], (x.double() @ wv.t())[:, keep], bound[:, keep], dt)
+
+
+@pytest.mark.parametrize("M", [5, 30, 100, 300])
+def test_gemm_largest_scales(M):
+    """The two largest scales against small ones: no product of a value and a scale is made by itself."""
+    g = _gen(M)
+    N, K = 150, 700
+    xc, xs = make_mx4(g, M, K, 60, 100)
+    wc, ws = make_mx4(g, N, K, 115, 130)
+    ws[::3, 4], ws[1::3, 21], ws[2::5, 0] = 254, 253, 252
+    got = qk.qk_gemm_mx4(qk.qk_mx4_state_init(M, K, xc, xs), qk.qk_mx4_state_init(N, K, wc, ws), torch.float32)
+    xv, wv = values(xc, xs, K), values(wc, ws, K)
+    check(got, xv @ wv.t(), product_bound(xv, wv, K), torch.float32)
+
+
+@pytest.mark.parametrize("M", [1, 16, 30, 100, 130, 700, 2100])
+@pytest.mark.parametrize("N,K", [(40, 4099), (300, 1000), (2100, 8192)])
+def test_gemm_of_whole_numbers_is_exact(M, N, K):
+    """Sums below 2^24 units: nothing may be lost, however small beside the rest."""
+    g = _gen(M + N + K)
+    xc, xs = make_mx4(g, M, K, 127, 128)
+    wc, ws = make_mx4(g, N, K, 126, 127)
+    got = qk.qk_gemm_mx4(qk.qk_mx4_state_init(M, K, xc, xs), qk.qk_mx4_state_init(N, K, wc, ws), torch.float32)
+    xv, wv = values(xc, xs, K), values(wc, ws, K)
+    # values are multiples of 1/2 and 1/4, at most 12 and 6: sums of multiples of 1/8
+    assert float((xv.abs() @ wv.abs().t()).max()) * 8 < 2 ** 24
+    assert torch.equal(got.double(), xv @ wv.t())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 4, 7, 16])
+@pytest.mark.parametrize("N,K", [(40, 4099), (300, 1000), (70000, 300), (48, 16384)])
+def test_gemv_of_whole_numbers_is_exact(dtype, M, N, K):
+    g = _gen(M + N + K)
+    wc, ws = make_mx4(g, N, K, 126, 128)
+    x = torch.randint(-8, 9, (M, K), generator=g, device="cuda").to(DT[dtype])
+    x[:, ::3] = 0.5
+    wv = values(wc, ws, K)
+    # multiples of 1/8; sums of absolute values below 2^24 of them
+    assert float((x.double().abs() @ wv.abs().t()).max()) * 8 < 2 ** 24
+    got = qk.qk_gemv_mx4(x, qk.qk_mx4_state_init(N, K, wc, ws))
+    assert torch.equal(got, (x.double() @ wv.t()).float().to(DT[dtype]))
