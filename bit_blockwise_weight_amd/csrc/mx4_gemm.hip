@@ -348,7 +348,7 @@ __device__ __forceinline__ void store_wave(const GemmArgs& a, const Tile& t, con
 //
 // A workgroup makes one tile after the other (kTurns; a launch has as many as are on the CUs at a time): while a tile is
 // multiplied the slots of the next one's rows come from the plan, and its first copies are on their way while outputs are
-// stored.  4096 tokens of 64 experts, up: 117 us where every tile has a workgroup of its own, 107 so.  Not in the largest tiles, whose
+// stored.  4096 tokens of 64 experts, up: 126 us where every tile has a workgroup of its own, 111 so.  Not in the largest tiles, whose
 // sums leave no registers for it.
 // ---------------------------------------------------------------------------
 constexpr bool takes_turns(int BM, int BN) { return BM * BN < 256 * 256; }
@@ -843,17 +843,17 @@ hipError_t launch_few(const GemmArgs& a, hipStream_t s) {
 hipError_t launch_dense(const GemmArgs& a, hipStream_t s) {
     const int64_t cus = device_cu_count();
     // Workgroups that split the inputs among their waves where tiles would leave half of the CUs without one, and up to 16
-    // rows always: 16 x 4096 x 11008 6.6, tiles of 64 x 64 16; 64 x 4096 x 4096 7.5 and 8.7; 64 x 11008 x 4096 12.5 and 9.0.
+    // rows always: 16 x 4096 x 11008 6.4, tiles of 64 x 64 16; 64 x 4096 x 4096 6.6 and 8.1; 64 x 11008 x 4096 12.1 and 8.6.
     // (A launch has fewer than 2^32 threads; tiles are made by as many workgroups as there is room for.)
     if (a.M <= 16 && a.N <= (int64_t)1 << 28) return launch_few<kDense, 1, 2>(a, s);
     if (a.M <= 128 && grid_for<kDense>(a, 64, 64) <= cus / 2)
         return a.M <= 32 ? launch_few<kDense, 2, 2>(a, s) : launch_few<kDense, 4, 2>(a, s);
-    // The largest tiles of which there is one for every CU: 4096 x 4096 x 4096 41, in tiles of 128 51; 2048 x 4096 x 4096 40 and
-    // 25.  Two workgroups a CU of tiles of 128 where there is more than one for each (1100 x 4096 x 4096 22.5, one workgroup and
-    // a ring of three stages 26), one and a ring of three up to that, where tiles of 64 x 128 would be more than the CUs
-    // (800 x 4096 x 4096 14.0, of 64 x 128 17.4; 600 x 3500 x 4096 12.9 and 16.1).  Below, those of 64 x 128 (512 x 4096 x 4096
-    // 11.5, of 128 12.5, of 64 13.5) down to 5 / 8 of the CUs (200 x 4096 x 4096 10.5, of 64 9.6), a ring of three always: 200
-    // x 4096 x 4096 in tiles of 64 with weights from memory 10.4, of two 12.3.
+    // The largest tiles where there is one for every CU: 4096 x 4096 x 4096 39.9, in tiles of 128 43.9; 2048 x 4096 x 4096 31.3 and
+    // 24.0 (a bound of 3 / 4 of the CUs would do as well or better: 3000 x 4096 x 4096 33.8 and 34.4, 3800 37.8 and 42.6).  Two workgroups
+    // a CU of tiles of 128 where there is more than one for each (1100 x 4096 x 4096 22.1, one workgroup and a ring of three stages
+    // 25.2), one and a ring of three up to that (1000 13.7, of two 14.3), where tiles of 64 x 128 would be more than the CUs
+    // (800 x 4096 x 4096 12.5, of 64 x 128 16.0; 560 11.6 and 17.8).  Below, those of 64 x 128 (512 x 4096 x 4096 10.6, of 128
+    // 11.6, of 64 11.3) down to 5 / 8 of the CUs (300 x 4096 x 4096 9.4, of 64 10.6; 200 9.3 and 8.5), with a ring of three.
     if (grid_for<kDense>(a, 256, 256) >= cus) return launch_tile<kDense, 256, 256, 128, 128, 2>(a, s);
     if (grid_for<kDense>(a, 128, 128) > cus) return launch_tile<kDense, 128, 128, 64, 64, 2>(a, s);
     const int64_t tiles = grid_for<kDense>(a, 64, 128);
@@ -867,17 +867,21 @@ hipError_t launch_experts(const GemmArgs& a, hipStream_t s) {
     const int64_t cus = device_cu_count(), half = MODE == kUp ? 2 : 1;
     if (moe_tile_rows(a.slots, a.E) == 128) {
         // Tiles of 128 x 256, a ring of three stages and one workgroup a CU, where there is about one for each CU (half of
-        // an expert's last tile counted): 512 tokens of 8 experts of 4096 x 11008, top 2, down 60 us, in tiles of 128 x 128 76;
-        // 600 of 8 experts of 8192 inputs and 2048 outputs (107 tiles) 43 and 35; 1000 of the first (314 tiles) 107 and 100; 2048
-        // of 8 experts, up, of 4096 inputs and 2000 outputs (576 tiles) 61 and 55.  And where there are so many that the last turn
-        // does not matter: 4096 tokens of 64 experts, top 8, up (2320 tiles), weights from memory 123 and 126.
+        // an expert's last tile counted): top 2 of 8 experts of 4096 x 11008, down, 400 tokens (160 tiles) 58 us, in tiles of 128 x
+        // 128 72; 512 (192) 60 and 69; 700 (224) 62 and 65; 800 (256, by then more than one) 106 and 100; 1000 (304) 105 and 97; 600
+        // of 8 experts of 8192 inputs and 2048 outputs (104) 43 and 33.  And where there are so many that the last turn does not matter:
+        // 8192 tokens down (2112) 594 and 616; 1400 up (2150) 208 and 239; 4096 tokens of 64 experts, up (2304), weights from memory 118
+        // and 121, 8192 (4352) 214 and 220.  From 2 to 8 for each CU either is better, by what the last turn has left: 2600 down (704)
+        // 204 and 223, 4096 down (1088) 317 and 307, 5000 (1312) 360 and 387; 2048 tokens of 64 experts, up (1280) 68 and 63.
         const int64_t experts = std::min<int64_t>(a.E, a.slots);
         const int64_t tiles = (a.slots / 128 + (experts + 1) / 2) * cdiv(a.N, 256 / half);
         if ((tiles > cus / 2 && tiles <= cus) || tiles > 8 * cus) return launch_tile<MODE, 128, 256, 64, 64, 3>(a, s);
         return launch_tile<MODE, 128, 128, 64, 64, 2>(a, s);
     }
     // A few slots of few outputs: the inputs split among the waves of a workgroup (one token's top 2 of 8 experts of
-    // 4096 x 11008, down: 12.8, in tiles of 64 x 64 23).  Otherwise the larger tiles where they fill the CUs twice.
+    // 4096 x 11008, down: 12.6, in tiles of 64 x 64 24, its up products, of more tiles than CUs, 22 and 17; two tokens' top 8 of
+    // 64 of 2048 x 1024, down, 10.8 and 9.7).  Otherwise the larger tiles where they fill the CUs twice (200 tokens of the first,
+    // up, 92, of 64 x 64 109; of the second, weights from memory, 38 and 40; 100 tokens of the first, down, once: 39 both).
     if (a.slots <= 16 && grid_for<MODE>(a, 64, 64 / half) <= cus) return launch_few<MODE, 1, 2>(a, s);
     if (grid_for<MODE>(a, 64, 128 / half) >= 2 * cus) return launch_tile<MODE, 64, 128, 64, 32, 2>(a, s);
     return launch_tile<MODE, 64, 64, 64, 32, 2>(a, s);

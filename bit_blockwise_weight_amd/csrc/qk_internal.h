@@ -277,9 +277,9 @@ constexpr int64_t moe_plan_list(int32_t E) { return (int64_t)(E + 4) / 4 * 4; }
 constexpr int64_t moe_plan_tiles(int32_t E, int64_t slots) { return moe_plan_list(E) + (slots + 3) / 4 * 4; }
 // Rows of a tile, at most, by the rows of an expert on average: half of an expert's last tile is idle, and where there are
 // more tiles than experts a weight is read more than once, which costs most where few experts have large weights.  Times of the
-// products in us, weights from memory, tiles of 64 and of 128 rows.  64 experts of 2048 x 1024, up, 64 rows 41 and 44,
-// 96 rows 52 and 46; 32 of 2048 x 2048, 64 rows 42 and 45; 16 of 4096 x 2048, 64 rows 44 and 40; 8 of 4096 x 4096, 32 rows
-// 32 and 35, 64 rows 43 and 35; 8 of 4096 x 11008, down, 32 rows 53 and 52, 64 rows 72 and 57.
+// products in us, weights from memory, tiles of 64 and of 128 rows.  64 experts of 2048 x 1024, up, 64 rows 42 and 44,
+// 96 rows 50 and 44; 32 of 2048 x 2048, 64 rows 43 and 39, 96 rows 55 and 45; 16 of 4096 x 2048, 33 rows 31 and 33, 64 rows 47 and
+// 34; 8 of 4096 x 4096, 32 rows 31 and 34, 40 rows 42 and 33; 8 of 4096 x 11008, down, 32 rows 52 and 50, 64 rows 73 and 52.
 constexpr int64_t moe_tile_rows(int64_t slots, int32_t E) {
     const int64_t experts = E < slots ? E : slots;
     return (slots + experts - 1) / experts <= (experts <= 16 ? 32 : 64) ? 64 : 128;
