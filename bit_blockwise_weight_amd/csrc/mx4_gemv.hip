@@ -41,12 +41,12 @@ __device__ __forceinline__ void rows_of(const GemvArgs& a, int b, int64_t& row0,
 }
 
 // Weights of the two largest scales may pass bf16, though their products with small activations are numbers: an infinity among
-// them, or a NaN where it meets a 0, stays in the sum.  The outputs of row group q of an item for which that may be so, no
+// them, or a NaN where it meets a 0, stays in the sum.  The outputs of row group q of an item for which that may be so, stored as no
 // numbers and with such a scale in their row, are made again, each group's scale applied to its sum: one after the other, the
-// lanes taking groups.  (Quantization gives no scale over 252.  Looking for them in the loop costs every call 1 to 3 %; so would
-// the registers of arguments kept until here, they are read anew.)
+// lanes taking groups.  (Quantization gives no scale over 252.  Looking for them where scales land costs every call 1 to 3 %.  This
+// code stands behind the kernel's end, and reads its arguments anew: between the loops, or with registers kept for it, it costs as much.)
 template <int RT, int MI, class Tiles>
-__device__ __forceinline__ void make_again(int item, int q, const float* put) {
+__device__ __forceinline__ void make_again(int item, int q) {
     typedef float f32x2_t __attribute__((ext_vector_type(2)));
     auto args = (const __attribute__((address_space(4))) GemvArgs*)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(args));
@@ -58,22 +58,51 @@ __device__ __forceinline__ void make_again(int item, int q, const float* put) {
     for (int t = 0; t < RT * MI; ++t) {
         const int r = t / MI, o = 64 * (t % MI) + lane;
         const int64_t first = row0 + item * step_of<RT>(a) + q * (16 * RT) + 16 * r;
-        uint64_t bad = __ballot(!(fabsf(Tiles::sum(put, a.kwl, q, r, o)) < INFINITY));
+        // the rows with such a scale, lane l looking through a quarter of row l % 16's
+        bool large = false;
+        if (first + (lane & 15) < row1) {
+            const uint32_t* scales = reinterpret_cast<const uint32_t*>(a.w.scales + (first + (lane & 15)) * a.w.scale_stride);
+#pragma unroll 4
+            for (int d = lane >> 4; 4 * d < a.w.G; d += 4) {        // (bytes behind the last scale may be anything, and 255 is)
+                const uint32_t v = scales[d];
+                large |= (((v & 0x7F7F7F7Fu) + 0x03030303u) & v & 0x80808080u) != 0;
+            }
+        }
+        uint64_t rows = __ballot(large);
+        rows |= rows >> 32 | rows << 32;
+        rows |= rows >> 16 | rows << 48;
+        const bool mine = Tiles::act_of(o) < a.M && first + (lane & 15) < row1;
+        const uint16_t y = mine ? a.y[Tiles::act_of(o) * a.N + first + (lane & 15)] : 0;
+        uint64_t bad = rows & __ballot((y & 0x7F80) == 0x7F80);
         for (; bad; bad &= bad - 1) {
             const int l = (int)__builtin_ctzll(bad), m = Tiles::act_of(o - lane + l);
             const int64_t row = first + (l & 15);
-            if (m >= a.M || row >= row1) continue;
             const uint8_t* scales = a.w.scales + row * a.w.scale_stride;
-            bool large = false;
-            for (int g = lane; g < a.w.G; g += 64) large |= (uint32_t)scales[g] - 253u < 2u;
-            if (!__ballot(large)) continue;
             float sum = 0.0f;
             for (int g = lane; g < a.w.G; g += 64) {
-                const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.w.codes + row * a.w.stride) + 4 * g;
+                // a group of 32: its codes, padded, and its activations, or what there are of them
+                const uint8_t* codes = a.w.codes + row * a.w.stride + 16 * g;
+                const uint16_t* x = a.x + (int64_t)m * a.K + 32 * g;
+                uint32_t c[4];
+                __builtin_memcpy(c, codes, 16);
                 float part = 0.0f;
-                for (int k = 0; k < 32 && 32 * g + k < a.K; ++k) {
-                    const f32x2_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[k / 8] >> (4 * (k % 8)), 1.0f, 0);
-                    part = fmaf(bf16_bits_to_float(a.x[(int64_t)m * a.K + 32 * g + k]), v[0], part);
+#pragma unroll 1
+                for (int d = 0; d < 4; ++d) {
+                    uint16_t v[8];
+                    if (32 * g + 8 * d + 8 <= a.K) {
+                        __builtin_memcpy(v, x + 8 * d, 16);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = 32 * g + 8 * d + i < a.K ? x[8 * d + i] : 0;
+                    }
+                    const uint32_t w = d == 0 ? c[0] : d == 1 ? c[1] : d == 2 ? c[2] : c[3];
+                    f32x2_t f[4];
+                    f[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+                    f[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+                    f[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+                    f[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) part = fmaf(bf16_bits_to_float(v[i]), f[i / 2][i % 2], part);
                 }
                 const uint32_t e = scales[g];
                 sum = fmaf(part, as_float(e == 0 ? 0x00400000u : e == 255u ? 0x7FC00000u : e << 23), sum);
@@ -109,6 +138,7 @@ __global__ __launch_bounds__(kThreads, 4) void mx4_gemv_kernel(GemvArgs a) {
     p.x_aligned = a.x_aligned;
     p.M = a.M;
     const int items = a.share + ((int)blockIdx.x < a.more);
+    uint64_t again = 0;                                             // the items (modulo 64) of this wave with outputs that are no numbers
     Tiles::run(a.w, p, 0, items, lds, [&](int item, int q, const float* put) {
         bool all = true;                                            // numbers
 #pragma unroll
@@ -121,10 +151,16 @@ __global__ __launch_bounds__(kThreads, 4) void mx4_gemv_kernel(GemvArgs a) {
                 all &= fabsf(v) < INFINITY;
                 if (m < a.M && j < p.count) a.y[m * a.N + row0 + j] = float_to_bits16(v, F == kMx4F16);
             }
-        if constexpr (F == kMx4Bf16) {
-            if (__builtin_expect(__ballot(!all) != 0, 0)) make_again<RT, MI, Tiles>(item, q, put);
-        }
+        if (F == kMx4Bf16 && __ballot(!all)) again |= 1ull << (item & 63);
     });
+    if constexpr (F == kMx4Bf16) {
+        if (__builtin_expect(again != 0, 0)) {
+            const int q = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >> p.kwl;   // the row group that this wave sums
+#pragma unroll 1
+            for (int item = 0; item < items; ++item)
+                if (again >> (item & 63) & 1) make_again<RT, MI, Tiles>(item, q);
+        }
+    }
 }
 
 // Registers of a product that carry activations: the least that hold M rows.
