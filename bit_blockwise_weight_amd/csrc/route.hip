@@ -6,8 +6,8 @@
 //
 // One wave per token, expert e in lane e % 64.  Which of two ranks is larger is decided in binary64, so that a choice does
 // not hang on the rounding of s: the choice is made in 32 bits, and where two ranks or two groups are closer than the error of
-// that, made again in 64.  (8192 tokens of 256 experts in 8 groups, top 8: 17.1 us in a captured graph, 18.0 under the
-// profiler, instructions, VALU busy 71 %; all in 64 bits 44.)
+// that, made again in 64.  (8192 tokens of 256 experts in 8 groups, top 8: 17.1 us in a captured graph, 18.7 under the
+// profiler, instructions, VALU busy 72 %; all in 64 bits 44.)
 #include <cmath>
 
 #include "qk_device.h"
